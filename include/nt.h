@@ -341,6 +341,135 @@ nt_status nt_rmsnorm(const float* x, const float* gamma, int B, int D, float eps
                      void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Verifying a drafted token tree ("The 0.6B model does not get to decide": the large model
+ * scores every drafted position in one batched pass and keeps the longest prefix on which the
+ * draft agrees with it; here the drafts form a tree, so several continuations are scored at
+ * once). The pages describe neither a tree nor these operations; formulas and readings are
+ * stated per call. A tree has 1 <= B <= 256 nodes; node 0 is its root (the last emitted token),
+ * parent[b] < b is the node that b follows (-1: none). One pass is: nt_tree_layout; per layer
+ * the projections, nt_qk_norm_rope_append and nt_tree_attention; the output projection,
+ * nt_logits_adjust, nt_tree_accept, nt_tree_commit and nt_token_counts. B = 1 with a mask of
+ * one set bit is plain decoding. The kernels of these calls are programmatic dependent launches:
+ * they start while the previous kernel of the stream finishes and touch memory after it.
+ */
+typedef enum nt_dtype { NT_F32 = 0, NT_BF16 = 1 } nt_dtype; /* fp32; bf16 bit patterns */
+enum nt_rope_layout { NT_ROPE_HALF = 0,          /* pair i of the rotated r dimensions: (i, i + r / 2) */
+                      NT_ROPE_INTERLEAVED = 1 }; /* (2i, 2i + 1) */
+enum nt_rope_scaling {
+  NT_ROPE_PLAIN = 0,     /* f_i = base^(-2i / r) */
+  NT_ROPE_LINEAR = 1,    /* f_i / factor: positions interpolated */
+  NT_ROPE_WAVELENGTH = 2 /* f_i * (w + (1 - w) / factor), w = clamp((n_i - slow) / (fast - slow), 0, 1),
+                            n_i = trained_len * f_i / (2 pi) the turns of pair i over the trained
+                            length: short wavelengths stay, long ones are interpolated */
+};
+
+/* Angles per position of each rotated pair, in double: inv_freq [rotary_dim / 2] (device, output).
+ * Run once per model. rotary_dim: a multiple of 8, 8..256; base > 1; factor > 0 and, for
+ * NT_ROPE_WAVELENGTH, trained_len >= 1 and 0 <= slow < fast (otherwise ignored). */
+nt_status nt_rope_frequencies(int rotary_dim, double base, int scaling, double factor, int trained_len,
+                              double slow, double fast, double* inv_freq, void* stream);
+
+/* Norms of queries and keys per head, rotary embedding and cache append of B tokens in one pass.
+ * Per query or key head x: y = x * r * gamma, r = 1 / sqrt(mean(x^2) + eps) (gamma NULL: y = x);
+ * then each pair (a, b) of the first rotary_dim dimensions becomes (a c - b s, b c + a s), (c, s) =
+ * amplitude * (cos, sin)(p_b * inv_freq[i]); the other dimensions pass through. All in fp32,
+ * rounded once; the angles are reduced modulo one turn in 64-bit integers, so a position of any
+ * int size costs no precision. Values are copied.
+ *   q [B][Hq][D], k and v [B][Hkv][D] of type dtype (nt_dtype), tokens q_stride, k_stride and
+ *     v_stride elements apart (multiples of 4), so they may be columns of one fused projection
+ *   q_gamma_opt, k_gamma_opt [D] fp32 or NULL      eps >= 0
+ *   D a multiple of 8 up to 256; rotary_dim a multiple of 8 in 0..D (0: no rotation)
+ *   inv_freq [rotary_dim / 2] double (nt_rope_frequencies, or the caller's own; any finite value)
+ *   pos_opt [B] int32 device positions, or NULL: token b has position pos0 + b
+ *   rows_opt [B] int32 device cache rows (distinct), or NULL: token b has row row0 + b
+ *   q_out [B][Hq][D] of type dtype (may be q when q_stride = Hq * D)
+ *   k_cache, v_cache [Hkv][t_stride][D] bf16: row b's key and value, round to nearest even
+ *   n_bad_opt: device uint32 counter or NULL; the call ADDS the number of rows outside
+ *     [0, t_stride), which are not written
+ * Alignment: q, k, v 16 bytes (bf16: 8), gammas, q_out and caches 16, inv_freq 8, int32 4. */
+nt_status nt_qk_norm_rope_append(const void* q, const void* k, const void* v, int dtype, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const float* q_gamma_opt,
+                                 const float* k_gamma_opt, float eps, int B, int Hq, int Hkv, int D,
+                                 const double* inv_freq, int rotary_dim, int layout, float amplitude,
+                                 const int32_t* pos_opt, int pos0, const int32_t* rows_opt, int row0,
+                                 void* q_out, uint16_t* k_cache, uint16_t* v_cache, int t_stride,
+                                 uint32_t* n_bad_opt, void* stream);
+
+/* Ancestor bits and positions of a tree. mask [B][mask_words] (output, mask_words >= ceil(B / 32)):
+ * bit j % 32 of word j / 32 of row b is set when node j is b or an ancestor of b; further bits and
+ * words are 0. pos_opt [B] or NULL (output): pos0 + the node's depth. A parent that is not below
+ * its node counts as none and adds 1 to the device counter n_bad_opt (may be NULL). */
+nt_status nt_tree_layout(const int32_t* parent, int B, int pos0, uint32_t* mask, int mask_words,
+                         int32_t* pos_opt, uint32_t* n_bad_opt, void* stream);
+
+/* Attention of B nodes over a cache: node b sees the sequence's rows 0 .. prefix - 1 and, of the
+ * tree's rows tree_row0 .. tree_row0 + B - 1 (row tree_row0 + j is node j's), those whose bit is
+ * set in mask row b (nt_tree_layout, or any other bits; only bits below B count).
+ * out[b][h] = sum_t softmax_t(q[b][h] . k[g][t] / sqrt(D)) v[g][t], g = h / (Hq / Hkv); a node
+ * that sees no row gets 0. What a node does not see has no part in its result, whatever it
+ * holds: masked rows and the rows between prefix and tree_row0 may be NaN or infinite.
+ *   q, out [B][Hq][D] of type dtype (nt_dtype; out may be q); k_cache, v_cache [Hkv][t_stride][D]
+ *   bf16; D 64 or 128; Hq a multiple of Hkv; B * Hq <= 1048576; 0 <= prefix <= tree_row0,
+ *   tree_row0 + B <= t_stride. q, out and caches 16-byte aligned.
+ *   ws: nt_tree_attention_workspace_size bytes (16-byte aligned, zero-filled before its first use;
+ *   calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
+ */
+nt_status nt_tree_attention_workspace_size(int B, int Hq, int Hkv, int D, int prefix, size_t* bytes);
+nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, const uint16_t* v_cache,
+                            int B, int Hq, int Hkv, int D, int prefix, int tree_row0, int t_stride,
+                            const uint32_t* mask, int mask_words, void* out, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Counts of the tokens a sequence has used: counts[tokens[i]] += 1 for i < m, or
+ * counts[tokens[index_opt[i]]] += 1 with an index, m = n or, with n_opt (device), min(n, *n_opt).
+ * With nt_tree_accept's path and n_emit as index_opt and n_opt it counts the tokens of the
+ * committed nodes. Tokens outside [0, V) and indexes outside [0, n) add 1 to n_bad_opt (device
+ * uint32 or NULL) instead. counts [V] int32 (zero-filled at the start of a sequence). */
+nt_status nt_token_counts(const int32_t* tokens, const int32_t* index_opt, int n, const int32_t* n_opt,
+                          int V, int32_t* counts, uint32_t* n_bad_opt, void* stream);
+
+/* Adjusted logits of B rows and their greedy choice. With c = the times row b has used token v --
+ * counts[v], plus, for a tree, the nodes j with tokens[j] == v whose bit is set in the row's
+ * tree mask (the row's own path) -- and x = logits[b][v]:
+ *   c > 0:  x <- x / repetition if x > 0, else x * repetition; x <- (x - frequency * c) - presence
+ *   bias:   x <- x + bias[v]
+ *   grammar: x <- -inf unless bit v % 32 of word v / 32 of the row's allowed words is set
+ * each step one fp32 rounding. argmax[b] = the lowest index of the largest value above -inf
+ * (NaN is never chosen), -1 if there is none (a row with nothing allowed).
+ *   logits [B][V] fp32; counts_opt, bias_opt, allowed_opt: rows of V int32, V fp32, ceil(V / 32)
+ *   words, their strides in elements (words) per row, 0 = one row for all; NULL: left out
+ *   tree_mask_opt [B][mask_words] with tokens_opt [B] (both or neither; then B <= 256)
+ *   repetition > 0 (1: none); frequency, presence finite (0: none)
+ *   out_opt [B][V] (may be logits) and argmax_opt [B] int32, at least one of them
+ *   ws: nt_logits_adjust_workspace_size bytes (16-byte aligned, zero-filled before its first use,
+ *   left zero; calls sharing it must not overlap); may be NULL without argmax_opt. */
+nt_status nt_logits_adjust_workspace_size(int V, int B, size_t* bytes);
+nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* counts_opt,
+                           int64_t counts_stride, const uint32_t* tree_mask_opt, int mask_words,
+                           const int32_t* tokens_opt, float repetition, float frequency, float presence,
+                           const float* bias_opt, int64_t bias_stride, const uint32_t* allowed_opt,
+                           int64_t allowed_stride, float* out_opt, int32_t* argmax_opt, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Acceptance of the longest drafted path that agrees with the model (nt_verify_accept for a
+ * tree): from the root, a node is followed by its lowest child whose token is argmax[node].
+ * path [B]: the accepted nodes, root first, then -1; emit [B]: argmax of each (the accepted drafts,
+ * then the model's own next token), then -1; *n_emit: their number, at least 1. Nodes whose
+ * parent is not below them follow no one. parent, token, argmax [B] int32; all device. */
+nt_status nt_tree_accept(const int32_t* parent, const int32_t* token, const int32_t* argmax, int B,
+                         int32_t* emit, int32_t* path, int32_t* n_emit, void* stream);
+
+/* Move of the accepted nodes' cache rows behind the sequence's, in every layer: for i < *n_emit,
+ * row dst_row0 + i <- row src_row0 + path[i] of every head of every cache. k_caches, v_caches:
+ * host arrays of n_layers device pointers to [Hkv][t_stride][D] bf16 (16-byte aligned); D a
+ * multiple of 8 up to 256; Hkv <= 65535; dst_row0 <= src_row0, src_row0 + B <= t_stride; the ranges
+ * may be the same. path and n_emit: device, from nt_tree_accept (path rises strictly from
+ * path[0] >= 0; an entry that is outside i .. B - 1 moves nothing). */
+nt_status nt_tree_commit(uint16_t* const* k_caches, uint16_t* const* v_caches, int n_layers, int Hkv, int D,
+                         int t_stride, const int32_t* path, const int32_t* n_emit, int B, int src_row0,
+                         int dst_row0, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Decode step: every projection of every layer, then optionally the output projection, in
  * one submission ("A 104 microsecond floor ...": on the instrumented A100 step, roughly
  * 590 of 694 microseconds were spent across about 120 kernel boundaries rather than in

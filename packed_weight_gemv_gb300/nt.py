@@ -34,6 +34,13 @@ NT_STEP_CHAINED = 2
 NT_LAUNCH_PERSISTENT = 0
 NT_LAUNCH_GRAPH = 1
 NT_LAUNCH_STREAM = 2
+NT_F32 = 0
+NT_BF16 = 1
+NT_ROPE_HALF = 0
+NT_ROPE_INTERLEAVED = 1
+NT_ROPE_PLAIN = 0
+NT_ROPE_LINEAR = 1
+NT_ROPE_WAVELENGTH = 2
 
 # Every symbol include/nt.h declares.
 EXPORTS = (
@@ -44,6 +51,9 @@ EXPORTS = (
     "nt_ternary_gemm_multi", "nt_int8_logits_workspace_size", "nt_int8_logits_argmax",
     "nt_int8_logits_argmax_noalloc", "nt_embed_rows", "nt_verify_accept",
     "nt_attention_workspace_size", "nt_attention_decode", "nt_rope_append", "nt_rmsnorm",
+    "nt_rope_frequencies", "nt_qk_norm_rope_append", "nt_tree_layout", "nt_tree_attention_workspace_size",
+    "nt_tree_attention", "nt_token_counts", "nt_logits_adjust_workspace_size", "nt_logits_adjust",
+    "nt_tree_accept", "nt_tree_commit",
     "nt_decode_plan_create", "nt_decode_step", "nt_decode_step_status", "nt_decode_plan_reset",
     "nt_decode_plan_set_position",
     "nt_decode_plan_trace_layout", "nt_decode_plan_set_trace", "nt_decode_plan_capture_size",
@@ -100,6 +110,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(path)
         i, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+        i64, f, d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
         sig = {
             "nt_abi_version": ([], i),
             "nt_status_string": ([i], ctypes.c_char_p),
@@ -126,6 +137,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "nt_attention_decode": ([vp, vp, vp, i, i, i, i, i, i, vp, vp, sz, vp], i),
             "nt_rope_append": ([vp, vp, vp, i, i, i, i, i, ctypes.c_float, vp, vp, vp, i, vp], i),
             "nt_rmsnorm": ([vp, vp, i, i, ctypes.c_float, vp, vp], i),
+            "nt_rope_frequencies": ([i, d, i, d, i, d, d, vp, vp], i),
+            "nt_qk_norm_rope_append": ([vp, vp, vp, i, i64, i64, i64, vp, vp, f, i, i, i, i, vp, i, i, f, vp, i, vp, i,
+                                        vp, vp, vp, i, vp, vp], i),
+            "nt_tree_layout": ([vp, i, i, vp, i, vp, vp, vp], i),
+            "nt_tree_attention_workspace_size": ([i, i, i, i, i, ctypes.POINTER(sz)], i),
+            "nt_tree_attention": ([vp, i, vp, vp, i, i, i, i, i, i, i, vp, i, vp, vp, sz, vp], i),
+            "nt_token_counts": ([vp, vp, i, vp, i, vp, vp, vp], i),
+            "nt_logits_adjust_workspace_size": ([i, i, ctypes.POINTER(sz)], i),
+            "nt_logits_adjust": ([vp, i, i, vp, i64, vp, i, vp, f, f, f, vp, i64, vp, i64, vp, vp, vp, sz, vp], i),
+            "nt_tree_accept": ([vp, vp, vp, i, vp, vp, vp, vp], i),
+            "nt_tree_commit": ([vp, vp, i, i, i, i, vp, vp, i, i, i, vp], i),
             "nt_decode_plan_create": ([ctypes.POINTER(nt_decode_desc), ctypes.POINTER(vp)], i),
             "nt_decode_step": ([vp, vp], i),
             "nt_decode_step_status": ([vp, ctypes.POINTER(i)], i),
@@ -138,9 +160,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "nt_decode_plan_destroy": ([vp], None),
         }
         for name, (args, res) in sig.items():
-            f = getattr(lib, name)
-            f.argtypes = args
-            f.restype = res
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = res
         _lib = lib
         return lib
 
@@ -322,6 +344,178 @@ def nt_rope_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, B:
 def nt_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, B: int, D: int, eps: float, y: torch.Tensor,
                stream=None):
     _check(load_library().nt_rmsnorm(_ptr(x), _ptr(gamma), B, D, eps, _ptr(y), _stream(stream)), "nt_rmsnorm")
+
+
+# ---- verifying a drafted token tree --------------------------------------------------------
+# Shapes and strides are read from the tensors; what the C ABI cannot see (another type, other
+# shapes, elements that are not contiguous) is refused here, with the same exception.
+_DTYPES = {torch.float32: NT_F32, torch.bfloat16: NT_BF16}
+
+
+def _refuse(call: str, what: str):
+    raise NtError(NT_ERR_INVALID_ARG, call, what)
+
+
+def _flat(call: str, name: str, t: Optional[torch.Tensor], dtype, shape=None):
+    """Address of a contiguous tensor of this type (and shape); None stays None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(call, f"{name} must be a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape else ""))
+    return t.data_ptr()
+
+
+def _rows(call: str, name: str, t: torch.Tensor, dtype, shape):
+    """Address and row stride of a 3-D tensor whose rows' elements are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        _refuse(call, f"{name} must be {dtype} {tuple(shape)} with contiguous heads")
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1] * shape[2])
+
+
+def _shared(call: str, name: str, t: Optional[torch.Tensor], dtype, B: int, n: int):
+    """Address and row stride of a [n] tensor for all rows or a [B, n] tensor (0: one row for all)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape[-1] != n or t.stride(-1) != 1 or not (
+            t.dim() == 1 or (t.dim() == 2 and t.shape[0] in (1, B))):
+        _refuse(call, f"{name} must be {dtype} [{n}] or [{B}, {n}] with contiguous rows")
+    return t.data_ptr(), (0 if t.dim() == 1 or t.shape[0] == 1 else t.stride(0))
+
+
+def nt_rope_frequencies(rotary_dim: int, base: float, inv_freq: torch.Tensor, scaling: int = NT_ROPE_PLAIN,
+                        factor: float = 1.0, trained_len: int = 0, slow: float = 1.0, fast: float = 32.0, stream=None):
+    ptr = _flat("nt_rope_frequencies", "inv_freq", inv_freq, torch.float64, (rotary_dim // 2,))
+    _check(load_library().nt_rope_frequencies(rotary_dim, base, scaling, factor, trained_len, slow, fast, ptr,
+                                              _stream(stream)), "nt_rope_frequencies")
+
+
+def nt_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_gamma: Optional[torch.Tensor],
+                           k_gamma: Optional[torch.Tensor], eps: float, inv_freq: Optional[torch.Tensor], layout: int,
+                           amplitude: float, q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           pos: Optional[torch.Tensor] = None, pos0: int = 0, rows: Optional[torch.Tensor] = None,
+                           row0: int = 0, n_bad: Optional[torch.Tensor] = None, stream=None):
+    """q [B, Hq, D], k and v [B, Hkv, D] (tokens any stride apart), caches [Hkv, t_stride, D] bf16."""
+    call = "nt_qk_norm_rope_append"
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 3 or q.dtype not in _DTYPES:
+        _refuse(call, "q, k and the caches must have three dimensions, q of fp32 or bf16")
+    B, Hq, D = q.shape
+    Hkv, ts = k.shape[1], k_cache.shape[1]
+    (qp, qs), (kp, ks) = _rows(call, "q", q, q.dtype, (B, Hq, D)), _rows(call, "k", k, q.dtype, (B, Hkv, D))
+    vp, vs = _rows(call, "v", v, q.dtype, (B, Hkv, D))
+    _check(load_library().nt_qk_norm_rope_append(
+        qp, kp, vp, _DTYPES[q.dtype], qs, ks, vs, _flat(call, "q_gamma", q_gamma, torch.float32, (D,)),
+        _flat(call, "k_gamma", k_gamma, torch.float32, (D,)), eps, B, Hq, Hkv, D,
+        _flat(call, "inv_freq", inv_freq, torch.float64), 0 if inv_freq is None else 2 * inv_freq.numel(), layout,
+        amplitude, _flat(call, "pos", pos, torch.int32, (B,)), pos0, _flat(call, "rows", rows, torch.int32, (B,)), row0,
+        _flat(call, "q_out", q_out, q.dtype, (B, Hq, D)), _flat(call, "k_cache", k_cache, torch.bfloat16, (Hkv, ts, D)),
+        _flat(call, "v_cache", v_cache, torch.bfloat16, (Hkv, ts, D)), ts, _ptr(n_bad), _stream(stream)), call)
+
+
+def nt_tree_layout(parent: torch.Tensor, mask: torch.Tensor, pos: Optional[torch.Tensor] = None, pos0: int = 0,
+                   n_bad: Optional[torch.Tensor] = None, stream=None):
+    """parent [B] int32 -> ancestor bits mask [B, words] int32 and positions pos [B] int32."""
+    call = "nt_tree_layout"
+    B = parent.numel()
+    if mask.dim() != 2 or mask.shape[0] != B:
+        _refuse(call, "mask must be [B, words]")
+    _check(load_library().nt_tree_layout(
+        _flat(call, "parent", parent, torch.int32), B, pos0, _flat(call, "mask", mask, torch.int32), mask.shape[1],
+        _flat(call, "pos", pos, torch.int32, (B,)), _ptr(n_bad), _stream(stream)), call)
+
+
+def nt_tree_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int, prefix: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().nt_tree_attention_workspace_size(B, Hq, Hkv, D, prefix, ctypes.byref(n)),
+           "nt_tree_attention_workspace_size")
+    return n.value
+
+
+def nt_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, prefix: int, tree_row0: int,
+                      mask: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None):
+    """q and out [B, Hq, D] fp32 or bf16, caches [Hkv, t_stride, D] bf16, mask [B, words] int32."""
+    call = "nt_tree_attention"
+    if q.dim() != 3 or k_cache.dim() != 3 or mask.dim() != 2 or mask.shape[0] != q.shape[0] or q.dtype not in _DTYPES:
+        _refuse(call, "q [B, Hq, D] fp32 or bf16, caches [Hkv, t_stride, D] and mask [B, words] are needed")
+    B, Hq, D = q.shape
+    Hkv, ts = k_cache.shape[0], k_cache.shape[1]
+    _check(load_library().nt_tree_attention(
+        _flat(call, "q", q, q.dtype), _DTYPES[q.dtype], _flat(call, "k_cache", k_cache, torch.bfloat16, (Hkv, ts, D)),
+        _flat(call, "v_cache", v_cache, torch.bfloat16, (Hkv, ts, D)), B, Hq, Hkv, D, prefix, tree_row0, ts,
+        _flat(call, "mask", mask, torch.int32), mask.shape[1], _flat(call, "out", out, q.dtype, (B, Hq, D)),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)), call)
+
+
+def nt_token_counts(tokens: torch.Tensor, counts: torch.Tensor, index: Optional[torch.Tensor] = None,
+                    n: Optional[torch.Tensor] = None, n_bad: Optional[torch.Tensor] = None, stream=None):
+    """counts [V] int32 += the tokens (int32), or those an index names; n: a device int32 bound on their number."""
+    call = "nt_token_counts"
+    _check(load_library().nt_token_counts(
+        _flat(call, "tokens", tokens, torch.int32), _flat(call, "index", index, torch.int32, tokens.shape),
+        tokens.numel(), _flat(call, "n", n, torch.int32), counts.numel(), _flat(call, "counts", counts, torch.int32),
+        _ptr(n_bad), _stream(stream)), call)
+
+
+def nt_logits_adjust_workspace_size(V: int, B: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().nt_logits_adjust_workspace_size(V, B, ctypes.byref(n)), "nt_logits_adjust_workspace_size")
+    return n.value
+
+
+def nt_logits_adjust(logits: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                     tree_mask: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                     repetition: float = 1.0, frequency: float = 0.0, presence: float = 0.0,
+                     bias: Optional[torch.Tensor] = None, allowed: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, argmax: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None, stream=None):
+    """logits [B, V] fp32; counts int32, bias fp32 [V] or [B, V]; allowed int32 words [W] or [B, W], W = ceil(V / 32)."""
+    call = "nt_logits_adjust"
+    if logits.dim() != 2 or (tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != logits.shape[0])):
+        _refuse(call, "logits [B, V] and tree_mask [B, words] are needed")
+    B, V = logits.shape
+    cp, cs = _shared(call, "counts", counts, torch.int32, B, V)
+    bp, bs = _shared(call, "bias", bias, torch.float32, B, V)
+    ap, as_ = _shared(call, "allowed", allowed, torch.int32, B, (V + 31) // 32)
+    _check(load_library().nt_logits_adjust(
+        _flat(call, "logits", logits, torch.float32), B, V, cp, cs, _flat(call, "tree_mask", tree_mask, torch.int32),
+        0 if tree_mask is None else tree_mask.shape[1], _flat(call, "tokens", tokens, torch.int32, (B,)), repetition,
+        frequency, presence, bp, bs, ap, as_, _flat(call, "out", out, torch.float32, (B, V)),
+        _flat(call, "argmax", argmax, torch.int32, (B,)), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), call)
+
+
+def nt_tree_accept(parent: torch.Tensor, token: torch.Tensor, argmax: torch.Tensor, emit: torch.Tensor,
+                   path: torch.Tensor, n_emit: torch.Tensor, stream=None):
+    call = "nt_tree_accept"
+    B = parent.numel()
+    p = [_flat(call, n, t, torch.int32, (B,)) for n, t in
+         (("parent", parent), ("token", token), ("argmax", argmax), ("emit", emit), ("path", path))]
+    _check(load_library().nt_tree_accept(p[0], p[1], p[2], B, p[3], p[4], _flat(call, "n_emit", n_emit, torch.int32),
+                                         _stream(stream)), call)
+
+
+class pointer_array:
+    """The addresses of a model's caches, layer by layer, for nt_tree_commit: made once and kept
+    with the caches (it keeps them alive). Each is a contiguous bf16 [Hkv, t_stride, D] tensor."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        self._keep = list(tensors)
+        for t in self._keep:
+            _flat("pointer_array", "a cache", t, torch.bfloat16, self._keep[0].shape)
+        self.array = (ctypes.c_void_p * len(self._keep))(*[t.data_ptr() for t in self._keep])
+
+    def __len__(self):
+        return len(self._keep)
+
+
+def nt_tree_commit(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, path: torch.Tensor,
+                   n_emit: torch.Tensor, src_row0: int, dst_row0: int, stream=None):
+    call = "nt_tree_commit"
+    if len(k_caches) != len(v_caches) or not len(k_caches) or any(
+            c._keep[0].shape != (Hkv, t_stride, D) for c in (k_caches, v_caches)):
+        _refuse(call, "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
+    _check(load_library().nt_tree_commit(
+        k_caches.array, v_caches.array, len(k_caches), Hkv, D, t_stride, _flat(call, "path", path, torch.int32),
+        _flat(call, "n_emit", n_emit, torch.int32), path.numel(), src_row0, dst_row0, _stream(stream)), call)
 
 
 class DecodePlan:
