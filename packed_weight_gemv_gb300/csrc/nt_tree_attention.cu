@@ -1,79 +1,688 @@
 // nt_tree_attention.cu -- attention of a drafted token tree over a bf16 key-value cache: every
 // node sees the sequence's cached rows and the tree rows its mask names.
+//
+//   out[b][h] = sum_t p_t v_t / sum_t p_t,   p_t = 2^(q . k_t log2(e) / sqrt(D) - m)
+//
+// The R = B * Hq / Hkv query rows that share a key-value head read the cache once: they are the
+// M side of tcgen05.mma (128 rows to a tile), 64 keys at a time the N side of the scores, and the
+// weights, written back to tensor memory, the A operand of the weighted values.
+//
+// Products are exact: queries enter as bf16 terms (three for fp32 queries, which hold every bit of
+// a value; one for bf16 queries), keys and values are bf16, and the weights are three bf16 terms
+// cut from the fp32 weight without loss (fp32 queries) or two rounded ones (bf16 queries: 2^-17,
+// small next to the output's 2^-9). Scores, weights, sums and the output accumulate in fp32.
+//
+// CTA (192 threads): one tile of rows, one key-value head, a range of 64-key tiles.
+//   warp 4 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
+//   warp 5 lane 0  -- MMA issuer: scores of tile j + 2 and weighted values of tile j, while
+//   warps 0-3      -- (thread = row = tensor-memory lane) turn the scores of tile j + 1 into weights
+//                     over the same columns. The reference maximum m of a row is raised only when
+//                     a score exceeds it by 2^8, and the accumulator rescaled only then.
+// Few rows are spread over the lanes: with R <= 32 (64) each row stands in four (two) lanes, each
+// of which weighs a quarter (half) of every tile's keys with a maximum and sum of its own and
+// leaves zeros elsewhere; their accumulators are joined at the end. So the instructions of the
+// softmax, which would otherwise be one warp's, are shared by four.
+// The keys of one head are split over CTAs so that the GPU is filled once; the parts' results
+// (weighted sum, m, sum) meet in the workspace and a second kernel joins them.
+//
+// What a node does not see has no part in its result: the rows past the sequence and past the
+// tree are beyond the extent of their tensor maps (zeros), masked scores are replaced, and a tree
+// value that is not finite is taken out of shared memory before the product and added to the
+// nodes that see it at the end.
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
+#include <string>
 
 #include "nt_kernels.cuh"
 
 namespace nt {
 namespace {
 
-struct TreeAttnArgs {
-  const void* q;  // [B][Hq][D]
-  const uint16_t *kc, *vc;  // [Hkv][ts][D] bf16
-  const uint32_t* mask;     // [B][words]
-  void* out;                // [B][Hq][D]
-  int B, Hq, Hkv, prefix, row0, ts, words;
+constexpr int kTaKeys = 64;             // keys per tile
+constexpr int kTaStages = 12;           // ring slots, each one tile's keys or values
+constexpr int kTaSoftmax = 128;         // threads = tensor-memory lanes
+constexpr int kTaProducer = 4, kTaMma = 5;
+constexpr int kTaThreads = 192;
+constexpr int kTaTmemCols = 512;
+constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
+constexpr float kTaLazy = 8.0f;         // a maximum is raised once a score exceeds it by 2^8
+constexpr uint64_t kTaTimeoutNs = 2000000000ull;
+constexpr unsigned int kTaErrWait = 18;  // status code of a wait that ran out
+
+template <typename T, int D>
+struct TaShape {
+  static constexpr int kTermsQ = sizeof(T) == 4 ? 3 : 1;
+  static constexpr int kTermsP = sizeof(T) == 4 ? 3 : 2;
+  static constexpr int kSlot = kTaKeys * D * 2;            // bytes
+  static constexpr int kBuf = kTermsP == 3 ? 96 : 64;      // columns of a score / weight buffer
+  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQ * D / 2;
+  static constexpr int kPitch = D + 4;                     // floats: staged output rows
+  static constexpr int kSmem = kTaStages * kSlot + 1024;   // and alignment
+  static_assert(kColS + 2 * kBuf <= kTaTmemCols, "tensor-memory columns");
+  static_assert(128 * kPitch * 4 <= kTaStages * kSlot, "the output is staged in the ring");
 };
 
-__device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+struct TaArgs {
+  const void* q;            // [B][Hq][D]
+  void* out;                // [B][Hq][D]
+  const uint32_t* mask;     // [B][words]
+  const uint16_t* vtree;    // the tree's first value row of head 0
+  int64_t head_stride;      // elements between heads of a cache
+  float* part;              // [units][rows][D] weighted sums of a split
+  float2* ml;               // [units][rows] (m, sum)
+  unsigned int* err;        // the workspace's status header [code, CTA]
+  uint64_t timeout_ns;
+  int fault;
+  int B, Hq, G, R, words;   // R = B * G rows per key-value head
+  int prefix, pre_tiles, tiles;  // 64-key tiles of the sequence, and with the tree's
+  int nsplit, mtiles;
+  float scale_log2;         // log2(e) / sqrt(D)
+};
+struct TaMaps {
+  CUtensorMap kp, vp, kt, vt;  // sequence and tree rows of keys and values
+};
 
-// CTA of 4 warps per (head, node): each warp walks keys w, w + 4, ... with a running maximum.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) tree_attn_kernel(const TreeAttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  dependent_launch_wait();
-  const int h = blockIdx.x, b = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = h / (a.Hq / a.Hkv);
-  auto elem = [](const T* p, int e) { return sizeof(T) == 4 ? (float)p[e] : bf16_f((uint16_t)p[e]); };
-  const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + h) * D + lane * E;
-  float x[E], o[E];
-  for (int e = 0; e < E; ++e) {
-    x[e] = elem(q, e);
-    o[e] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const float scale = 1.0f / sqrtf((float)D);
-  const uint16_t* kh = a.kc + (int64_t)g * a.ts * D + lane * E;
-  const uint16_t* vh = a.vc + (int64_t)g * a.ts * D + lane * E;
-  for (int t = w; t < a.prefix + a.B; t += 4) {
-    const int j = t - a.prefix;
-    if (j >= 0 && !(a.mask[(int64_t)b * a.words + (j >> 5)] >> (j & 31) & 1u)) continue;
-    const int64_t row = (int64_t)(j >= 0 ? a.row0 + j : t) * D;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], bf16_f(kh[row + e]), s);
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    s *= scale;
-    const float mn = fmaxf(m, s), c = m == -INFINITY ? 0.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(s - mn);
-    l = l * c + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * bf16_f(vh[row + e]);
-    m = mn;
-  }
-  if (lane == 0) {
-    sm[w] = m;
-    sl[w] = l;
-  }
-  for (int e = 0; e < E; ++e) so[w][lane * E + e] = o[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY, L = 0.0f, O = 0.0f;
-    for (int k = 0; k < 4; ++k) M = fmaxf(M, sm[k]);
-    for (int k = 0; k < 4; ++k) {
-      const float c = sm[k] == -INFINITY ? 0.0f : expf(sm[k] - M);
-      L += sl[k] * c;
-      O += so[k][threadIdx.x] * c;
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait; false after the timeout or once another role of the CTA has given up.
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
+  const uint64_t deadline = globaltimer_ns() + timeout_ns;
+  for (uint32_t it = 1;; ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 63u) == 0u && (*fail || globaltimer_ns() > deadline)) {
+      *fail = 1;
+      return false;
     }
-    const float y = L > 0.0f ? O / L : L == 0.0f ? 0.0f : NAN;
-    const int64_t at = ((int64_t)b * a.Hq + h) * D + threadIdx.x;
-    if (sizeof(T) == 4) static_cast<float*>(a.out)[at] = y;
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+  }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity, fail, timeout_ns);
+}
+// The same for a whole warp: every lane gets one answer, so the warp stays together.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, fail, timeout_ns));
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Shared-memory operand with the 128-byte swizzle, as the TMA boxes of 64 elements x 64 rows
+// write it: 8-row groups 1,024 bytes apart. K-major for the keys (rows = keys, 64 dimensions of
+// the reduction in a row); for the values rows are the reduction and the second 64 dimensions
+// stand `lead` bytes on.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lead >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;  // descriptor version (sm_100)
+  d |= (uint64_t)2 << 61;  // 128-byte swizzle
+  return d;
+}
+// kind::f16, A = B = bf16, D = fp32, M = 128, N = n; B K-major, or with the reduction along rows.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_rows) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+// Waits for this thread's tensor-memory loads; the values may be used only after it.
+template <int N>
+__device__ __forceinline__ void tm_ld_wait(float (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
+                 "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]), "+f"(r[i + 10]), "+f"(r[i + 11]),
+                 "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]), "+f"(r[i + 15])::"memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x (2^-inf = +0)
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Two values as pairs of bf16 terms, term t of both in w[t]: with three terms the leading 8, next
+// 8 and last 8 bits of the significand, cut off one after the other, so nothing is lost (a value
+// below 2^-110 aside); otherwise each term is the rest so far, rounded.
+template <int N>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&w)[N]) {
+  if constexpr (N == 3) {
+    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
+    w[0] = prmt(ux, uy, 0x7632u);
+    const float rx = x - high_f(ux), ry = y - high_f(uy);
+    w[1] = prmt(__float_as_uint(rx), __float_as_uint(ry), 0x7632u);
+    const float sx = rx - high_f(__float_as_uint(rx)), sy = ry - high_f(__float_as_uint(ry));
+    w[2] = prmt(__float_as_uint(sx), __float_as_uint(sy), 0x7632u);
+  } else {
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      w[t] = pack_rn(x, y);
+      x -= low_f(w[t]);
+      y -= high_f(w[t]);
+    }
+  }
+}
+// Whether a word holds a bf16 that is not finite.
+__device__ __forceinline__ bool word_bad(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+__device__ __forceinline__ int ring_key(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int ring_val(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+
+template <typename T, int D, int DUP>
+__global__ void __launch_bounds__(kTaThreads, 1)
+    tree_attn_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
+  using S = TaShape<T, D>;
+  constexpr int kRows = 128 / DUP;       // rows of a tile
+  constexpr int kCols = kTaKeys / DUP;   // keys of a tile that one lane weighs
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bars[2 * kTaStages + 7];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_fail, s_bad;
+  __shared__ float2 s_ml[128];
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kTaStages, sfull0 = empty0 + 8 * kTaStages;
+  const uint32_t pfull0 = sfull0 + 16, pvdone = pfull0 + 16, qfull = pvdone + 8, drain = qfull + 8;
+  volatile int* fail = &s_fail;
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+
+  const int unit = blockIdx.x;
+  const int mt = unit % a.mtiles, sp = unit / a.mtiles % a.nsplit, g = unit / a.mtiles / a.nsplit;
+  const int t0 = (int)((int64_t)a.tiles * sp / a.nsplit), n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
+  const int rows = min(kRows, a.R - mt * kRows);
+
+  if (i == 0) {
+    for (int s = 0; s < kTaStages; ++s) {
+      bar_init(full0 + 8 * s, 1);
+      bar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(sfull0 + 8 * b, 1);
+      bar_init(pfull0 + 8 * b, kTaSoftmax);
+    }
+    bar_init(pvdone, 1);
+    bar_init(qfull, kTaSoftmax);
+    bar_init(drain, 1);
+    s_fail = 0;
+    s_bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTaMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kTaTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // The set-up above overlaps the previous kernel; nothing below reads an input before its end.
+  dependent_launch_wait();
+
+  float m = -INFINITY, l = 0.0f;  // this lane's reference maximum (log2 units) and weight sum
+  const int part = (i & 127) / kRows;     // which keys of a tile this lane weighs (the same in a warp)
+  const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+
+  if (warp == kTaProducer) {
+    if (lane == 0) {
+      int k = 0;
+      for (; k < 2 * n && !a.fault; ++k) {
+        const int s = k % kTaStages;
+        if (k >= kTaStages && !bar_wait(empty0 + 8 * s, ((k / kTaStages) - 1) & 1, fail, a.timeout_ns)) break;
+        const bool val = k == 2 * n - 1 || (k > 0 && !(k & 1));
+        const int t = t0 + (k == 2 * n - 1 ? n - 1 : k == 0 ? 0 : (k & 1) ? (k + 1) / 2 : k / 2 - 1);
+        const bool tree = t >= a.pre_tiles;
+        const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
+        const int y = (tree ? t - a.pre_tiles : t) * kTaKeys;
+        const uint32_t dst = smem_u32(ring + s * S::kSlot);
+        bar_expect_tx(full0 + 8 * s, S::kSlot);
+#pragma unroll
+        for (int x = 0; x < D; x += 64) tma_3d(dst + x * kTaKeys * 2, map, x, y, g, full0 + 8 * s);
+      }
+      // every copy must land before the CTA may exit
+      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+      for (int j = max(0, k - kTaStages); j < k; ++j)
+        while (!bar_try(full0 + 8 * (j % kTaStages), (j / kTaStages) & 1))
+          if (globaltimer_ns() > deadline) break;
+    }
+  } else if (warp == kTaMma) {
+    if (lane == 0) {
+      auto scores = [&](int j) {
+        const int k = ring_key(j), s = k % kTaStages;
+        if (!bar_wait(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns)) return false;
+        tm_fence_after();
+        const uint32_t d = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
+#pragma unroll
+        for (int t = 0; t < S::kTermsQ; ++t)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, sdesc(b + (kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32, 16),
+                       idesc_bf16(kTaKeys, false), (t | kk) != 0);
+        mma_commit(empty0 + 8 * s);
+        mma_commit(sfull0 + 8 * (j & 1));
+        return true;
+      };
+      auto values = [&](int j) {
+        const int k = ring_val(j, n), s = k % kTaStages;
+        if (!bar_wait(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns) ||
+            !bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns))
+          return false;
+        tm_fence_after();
+        const uint32_t p = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
+#pragma unroll
+        for (int t = 0; t < S::kTermsP; ++t)
+#pragma unroll
+          for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
+            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, sdesc(b + kk * 2048, kTaKeys * 128),
+                       idesc_bf16(D, true), (j | t | kk) != 0);
+        mma_commit(empty0 + 8 * s);
+        mma_commit(pvdone);
+        return true;
+      };
+      bool ok = bar_wait(qfull, 0, fail, a.timeout_ns) && scores(0) && (n < 2 || scores(1));
+      for (int j = 0; ok && j < n; ++j) {
+        ok = values(j);
+        // the weights of tile j must have been read before the scores of tile j + 2 replace them
+        if (ok && j + 2 < n) ok = bar_wait(pvdone, j & 1, fail, a.timeout_ns) && scores(j + 2);
+      }
+      mma_commit(drain);  // every MMA of this CTA done, before the memory is freed
+      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+      while (!bar_try(drain, 0))
+        if (globaltimer_ns() > deadline) break;
+    }
+  } else {
+    const int r = i % kRows, rr = mt * kRows + r;  // row of the tile; node rr / G, head rr % G of the group
+    const int b = rr / a.G;
+    const bool live = r < rows;
+    {  // the row's query terms into tensor memory
+      const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + rr % a.G) * D;
+#pragma unroll 2
+      for (int c = 0; c < D; c += 16) {
+        uint32_t w[S::kTermsQ][8];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = live ? reinterpret_cast<const float4*>(q + c)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t x[3], y[3];
+            split(v.x, v.y, x);
+            split(v.z, v.w, y);
+#pragma unroll
+            for (int t = 0; t < S::kTermsQ; ++t) {
+              w[t][2 * e] = x[t];
+              w[t][2 * e + 1] = y[t];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint4 v = live ? reinterpret_cast<const uint4*>(q + c)[e] : make_uint4(0u, 0u, 0u, 0u);
+            w[0][4 * e] = v.x; w[0][4 * e + 1] = v.y; w[0][4 * e + 2] = v.z; w[0][4 * e + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + c / 2, w[t]);
+      }
+      tm_st_wait();
+      tm_fence_before();
+      bar_arrive(qfull);
+    }
+    // a warp of rows past the last one only keeps the barriers going (its lanes' weights are
+    // whatever the columns hold, and reach no row that is read)
+    const bool idle = r - lane >= rows;
+    const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    for (int j = 0; j < n; ++j) {
+      const uint32_t buf = tl + S::kColS + (j & 1) * S::kBuf;
+      const int t = t0 + j;
+      const bool tree = t >= a.pre_tiles;
+      if (tree) {  // take tree values that are not finite out of the product
+        const int k = ring_val(j, n), s = k % kTaStages;
+        if (!bar_wait_warp(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns)) break;
+        bool bad = false;
+        for (int e = i; e < S::kSlot / 16; e += kTaSoftmax) {
+          uint4* p = reinterpret_cast<uint4*>(ring + s * S::kSlot) + e;
+          const uint4 v = *p;
+          if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
+            uint16_t* h = reinterpret_cast<uint16_t*>(p);
+            for (int x = 0; x < 8; ++x)
+              if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
+            bad = true;
+          }
+        }
+        if (bad) s_bad = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      if (!bar_wait_warp(sfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns)) break;
+      tm_fence_after();
+      if (!idle) {
+        float s[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) tm_ld16(buf + part * kCols + c, s + c);
+        tm_ld_wait(s);
+        const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
+        if (tree || left < kTaKeys) {
+          uint64_t seen = ~0ull;
+          if (tree) {
+            const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
+            seen = w[0];
+            if (left > 32) seen |= (uint64_t)w[1] << 32;
+          }
+          if (left < kTaKeys) seen &= (1ull << left) - 1;
+          if (!live) seen = 0;
+          seen >>= part * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            if (!(seen >> c & 1)) s[c] = -INFINITY;
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int c = 1; c < kCols; ++c) mx = fmaxf(mx, s[c]);
+        mx *= a.scale_log2;
+        if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+          const float mn = fmaxf(m, mx), corr = mn == m ? 1.0f : ex2(m - mn);
+          if (j > 0) {
+            if (!bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns)) break;
+            tm_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tm_ld16(tl + S::kColO + c, o);
+              tm_ld16(tl + S::kColO + c + 16, o + 16);
+              tm_ld_wait(o);
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * corr);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) tm_st8(tl + S::kColO + c + e, w + e);
+            }
+          }
+          l *= corr;
+          m = mn;
+        }
+        const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c8 = 0; c8 < kCols / 16; ++c8) {
+          uint32_t w[S::kTermsP][8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = 16 * c8 + 2 * e;
+            const float p0 = ex2(fmaf(s[c], a.scale_log2, -mu)), p1 = ex2(fmaf(s[c + 1], a.scale_log2, -mu));
+            ls[e & 3] += p0 + p1;
+            uint32_t x[S::kTermsP];
+            split(p0, p1, x);
+#pragma unroll
+            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][e] = x[tt];
+          }
+#pragma unroll
+          for (int tt = 0; tt < S::kTermsP; ++tt)
+            tm_st8(buf + tt * (kTaKeys / 2) + part * (kCols / 2) + 8 * c8, w[tt]);
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if constexpr (DUP > 1) {  // the keys that other lanes weigh
+#pragma unroll
+          for (int tt = 0; tt < S::kTermsP; ++tt)
+#pragma unroll
+            for (int c = 0; c < kTaKeys / 2; c += 8)
+              if (c / (kCols / 2) != part) tm_st8(buf + tt * (kTaKeys / 2) + c, zero);
+        }
+        tm_st_wait();
+      }
+      tm_fence_before();
+      bar_arrive(pfull0 + 8 * (j & 1));
+    }
+    // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
+    const bool ok = bar_wait_warp(drain, 0, fail, a.timeout_ns);
+    tm_fence_after();
+    if (ok) {
+      float* st = reinterpret_cast<float*>(ring) + i * S::kPitch;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tm_ld16(tl + S::kColO + c, o);
+        tm_ld16(tl + S::kColO + c + 16, o + 16);
+        tm_ld_wait(o);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      s_ml[i] = make_float2(m, l);
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (warp == kTaMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
+  if (*fail) {
+    if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
+    return;
+  }
+  // join the lanes of each row; a split's sum goes to the workspace, a whole one to the output
+  const float* st = reinterpret_cast<const float*>(ring);
+  for (int e = i; e < rows * (D / 4); e += kTaThreads) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    float M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DUP; ++d) M = fmaxf(M, s_ml[r + d * kRows].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int d = 0; d < DUP; ++d) {
+      const float2 ml = s_ml[r + d * kRows];
+      const float4 x = *reinterpret_cast<const float4*>(st + (r + d * kRows) * S::kPitch + c);
+      const float w = DUP == 1 || ml.x == M ? 1.0f : ex2(ml.x - M);
+      L = fmaf(ml.y, w, L);
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
+    }
+    const int rr = mt * kRows + r, b = rr / a.G;
+    if (s_bad) {  // tree values that are not finite, for the nodes that see them
+      for (int k = max(t0 - a.pre_tiles, 0) * kTaKeys; k < min(a.B, (t0 + n - a.pre_tiles) * kTaKeys); ++k) {
+        if (!(a.mask[(int64_t)b * a.words + (k >> 5)] >> (k & 31) & 1u)) continue;
+        const uint2 v = *reinterpret_cast<const uint2*>(a.vtree + (int64_t)g * a.head_stride + (int64_t)k * D + c);
+        if (!isfinite(low_f(v.x))) o.x += low_f(v.x);
+        if (!isfinite(high_f(v.x))) o.y += high_f(v.x);
+        if (!isfinite(low_f(v.y))) o.z += low_f(v.y);
+        if (!isfinite(high_f(v.y))) o.w += high_f(v.y);
+      }
+    }
+    if (a.nsplit > 1) {
+      const int64_t at = (int64_t)unit * kRows + r;
+      *reinterpret_cast<float4*>(a.part + at * D + c) = o;
+      if (c == 0) a.ml[at] = make_float2(M, L);
+    } else {
+      const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
+      const int64_t at = ((int64_t)b * a.Hq + g * a.G + rr % a.G) * D + c;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
+    }
   }
 }
 
-size_t tree_attn_ws_bytes(int, int, int, int, int) { return sizeof(WsHeader); }
+// Joins the splits of a row: one warp per row, a lane D / 32 of its dimensions.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int rows_per_tile) {
+  constexpr int E = D / 32;
+  dependent_launch_wait();
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // b * Hq + h
+  if (row >= (int64_t)a.B * a.Hq) return;
+  const int lane = threadIdx.x & 31, b = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / a.G;
+  const int rr = b * a.G + h % a.G, mt = rr / rows_per_tile, r = rr % rows_per_tile;
+  const int64_t first = ((int64_t)g * a.nsplit * a.mtiles + mt) * rows_per_tile + r;
+  const int64_t step = (int64_t)a.mtiles * rows_per_tile;
+  float M = -INFINITY;
+  for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, a.ml[first + s * step].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.0f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < a.nsplit; ++s) {
+    const int64_t at = first + s * step;
+    const float2 ml = a.ml[at];
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 v = reinterpret_cast<const float4*>(a.part + at * D)[lane];
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = reinterpret_cast<const float2*>(a.part + at * D)[lane];
+      x[0] = v.x; x[1] = v.y;
+    }
+    const float w = ml.x == M ? 1.0f : ex2(ml.x - M);  // M = -inf: nothing seen, all sums 0
+    L = fmaf(ml.y, w, L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], w, acc[e]);
+  }
+  const float s = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] *= s;
+  const int64_t at = row * D + lane * E;
+  if constexpr (sizeof(T) == 4) {
+    float* y = static_cast<float*>(a.out) + at;
+    if constexpr (E == 4) *reinterpret_cast<float4*>(y) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    else *reinterpret_cast<float2*>(y) = make_float2(acc[0], acc[1]);
+  } else {
+    uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) y[e / 2] = pack_rn(acc[e], acc[e + 1]);
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------------
+struct TaPlan {
+  int dup, rows, mtiles, nsplit, tiles, pre_tiles;
+  int64_t units;  // CTAs
+};
+TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
+  TaPlan p;
+  const int R = B * (Hq / Hkv);
+  p.dup = R <= 32 ? 4 : R <= 64 ? 2 : 1;
+  p.rows = 128 / p.dup;
+  p.mtiles = (R + p.rows - 1) / p.rows;
+  p.pre_tiles = (int)(((int64_t)prefix + kTaKeys - 1) / kTaKeys);
+  p.tiles = p.pre_tiles + (B + kTaKeys - 1) / kTaKeys;
+  const int64_t groups = (int64_t)Hkv * p.mtiles;
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, kTaFill / groups));
+  p.units = groups * p.nsplit;
+  return p;
+}
+size_t ta_part_bytes(const TaPlan& p, int D) { return p.nsplit == 1 ? 0 : (size_t)p.units * p.rows * D * 4; }
+size_t tree_attn_ws_bytes(int B, int Hq, int Hkv, int D, int prefix) {
+  const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
+  return kWsHeaderBytes + ta_part_bytes(p, D) + (p.nsplit == 1 ? 0 : (size_t)p.units * p.rows * sizeof(float2));
+}
+
+std::mutex g_ta_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_ta_encode = nullptr;
+
+nt_status ta_setup() {
+  std::lock_guard<std::mutex> lock(g_ta_mu);
+  if (!g_ta_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    NT_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q));
+    if (q != cudaDriverEntryPointSuccess || !fn) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled not available");
+    g_ta_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  return NT_OK;
+}
+
+// Rows [0, rows) of every head from `base` on, boxes of 64 dimensions x 64 rows; further rows read as 0.
+nt_status ta_map(CUtensorMap* map, const uint16_t* base, int D, int rows, int Hkv, int ts) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ts * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kTaKeys, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_ta_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box,
+                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
+  return NT_OK;
+}
+
+template <typename T, int D, int DUP>
+nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p, cudaStream_t st) {
+  static std::atomic<int> attr_set[64];  // per device: the ring's dynamic shared memory allowed
+  int dev = 0;
+  NT_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return set_error(NT_ERR_CUDA, "device index out of range");
+  constexpr int smem = TaShape<T, D>::kSmem;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    NT_CUDA_TRY(cudaFuncSetAttribute(tree_attn_kernel<T, D, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    attr_set[dev].store(1, std::memory_order_release);
+  }
+  NT_CUDA_TRY(launch_kernel(tree_attn_kernel<T, D, DUP>, dim3((unsigned)p.units), dim3(kTaThreads), smem, st, true, maps, a));
+  NT_TRY(check_launch("tree_attn_kernel"));
+  if (p.nsplit > 1) {
+    const int64_t rows = (int64_t)a.B * a.Hq;
+    NT_CUDA_TRY(launch_kernel(tree_attn_join_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, true, a, p.rows));
+    NT_TRY(check_launch("tree_attn_join_kernel"));
+  }
+  return NT_OK;
+}
+template <typename T, int D>
+nt_status launch_tree_attn_dup(const TaMaps& maps, const TaArgs& a, const TaPlan& p, cudaStream_t st) {
+  return p.dup == 4 ? launch_tree_attn<T, D, 4>(maps, a, p, st)
+         : p.dup == 2 ? launch_tree_attn<T, D, 2>(maps, a, p, st) : launch_tree_attn<T, D, 1>(maps, a, p, st);
+}
 
 }  // namespace
 }  // namespace nt
@@ -109,11 +718,39 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   if (!ws || !aligned(ws, 16) || ws_bytes < tree_attn_ws_bytes(B, Hq, Hkv, D, prefix))
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_tree_attention_workspace_size");
   NT_TRY(check_device());
-  const TreeAttnArgs a{q, k_cache, v_cache, mask, out, B, Hq, Hkv, prefix, tree_row0, t_stride, mask_words};
-  auto kern = dtype == NT_F32 ? (D == 64 ? tree_attn_kernel<float, 64> : tree_attn_kernel<float, 128>)
-                              : (D == 64 ? tree_attn_kernel<uint16_t, 64> : tree_attn_kernel<uint16_t, 128>);
-  NT_CUDA_TRY(launch_kernel(kern, dim3(Hq, B), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), true, a));
-  return check_launch("tree_attn_kernel");
+  NT_TRY(ta_setup());
+  const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
+  TaArgs a{};
+  a.q = q;
+  a.out = out;
+  a.mask = mask;
+  a.vtree = v_cache + (int64_t)tree_row0 * D;
+  a.head_stride = (int64_t)t_stride * D;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+  a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes + ta_part_bytes(p, D));
+  a.err = static_cast<unsigned int*>(ws);
+  a.timeout_ns = test_fault_timeout_ns(kTaTimeoutNs);
+  a.fault = test_fault() == kFaultTree;
+  a.B = B;
+  a.Hq = Hq;
+  a.G = Hq / Hkv;
+  a.R = B * a.G;
+  a.words = mask_words;
+  a.prefix = prefix;
+  a.pre_tiles = p.pre_tiles;
+  a.tiles = p.tiles;
+  a.nsplit = p.nsplit;
+  a.mtiles = p.mtiles;
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
+  TaMaps maps;
+  // without a sequence its maps are not used; they still have to be valid
+  NT_TRY(ta_map(&maps.kp, k_cache, D, std::max(prefix, 1), Hkv, t_stride));
+  NT_TRY(ta_map(&maps.vp, v_cache, D, std::max(prefix, 1), Hkv, t_stride));
+  NT_TRY(ta_map(&maps.kt, k_cache + (int64_t)tree_row0 * D, D, B, Hkv, t_stride));
+  NT_TRY(ta_map(&maps.vt, a.vtree, D, B, Hkv, t_stride));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == NT_F32) return D == 64 ? launch_tree_attn_dup<float, 64>(maps, a, p, st) : launch_tree_attn_dup<float, 128>(maps, a, p, st);
+  return D == 64 ? launch_tree_attn_dup<uint16_t, 64>(maps, a, p, st) : launch_tree_attn_dup<uint16_t, 128>(maps, a, p, st);
 }
 
 }  // extern "C"

@@ -474,6 +474,25 @@ def test_attention_bits_past_the_tree_do_not_count():
     assert torch.equal(a, run_attend(q, k, v, 40, 40, wide, words=3))
 
 
+def test_attention_timeout_is_reported_until_cleared():
+    q, k, v = attn_inputs(9, 8, 2, 128, 400, 0, "f32")
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(6), 9))
+    want = run_attend(q, k, v, 400, 400, sees)
+    ws = torch.zeros(nt.nt_tree_attention_workspace_size(9, 8, 2, 128, 400), dtype=torch.uint8, device=DEV)
+    mask, out = dev(_tree.pack(sees)), torch.empty_like(q)
+    try:
+        nt.nt_set_test_fault(5, 20.0)
+        nt.nt_tree_attention(q, k, v, 400, 400, mask, out, ws)
+        torch.cuda.synchronize()
+    finally:
+        nt.nt_set_test_fault(0)
+    assert nt.nt_workspace_status(ws) == nt.NT_ERR_TIMEOUT
+    ws.zero_()
+    nt.nt_tree_attention(q, k, v, 400, 400, mask, out, ws)
+    torch.cuda.synchronize()
+    assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
+
+
 # ---- streams and graphs --------------------------------------------------------------------------
 def test_a_whole_pass_on_another_stream_and_in_a_graph():
     rs = np.random.RandomState(5)
