@@ -12,12 +12,12 @@
 // cut from the fp32 weight without loss (fp32 queries) or two rounded ones (bf16 queries: 2^-17,
 // small next to the output's 2^-9). Scores, weights, sums and the output accumulate in fp32.
 //
-// CTA (192 threads): one tile of rows, one key-value head, a range of 64-key tiles.
-//   warp 4 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
-//   warp 5 lane 0  -- MMA issuer: scores of tile j + 2 and weighted values of tile j, while
-//   warps 0-3      -- (thread = row = tensor-memory lane) turn the scores of tile j + 1 into weights
-//                     over the same columns. The reference maximum m of a row is raised only when
-//                     a score exceeds it by 2^8, and the accumulator rescaled only then.
+// CTA (320 threads): one tile of rows, one key-value head, a range of 64-key tiles.
+//   warp 8 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
+//   warp 9 lane 0  -- MMA issuer: scores of tile j + 2 and weighted values of tile j, while
+//   warps 0-7      -- (two threads per row = tensor-memory lane) turn the scores of tile j + 1 into
+//                     weights over the same columns. The reference maximum m of a row is raised only
+//                     when a score exceeds it by 2^8, and the accumulator rescaled only then.
 // Few rows are spread over the lanes: with R <= 32 (64) each row stands in four (two) lanes, each
 // of which weighs a quarter (half) of every tile's keys with a maximum and sum of its own and
 // leaves zeros elsewhere; their accumulators are joined at the end. So the instructions of the
@@ -45,10 +45,9 @@ namespace nt {
 namespace {
 
 constexpr int kTaKeys = 64;             // keys per tile
-constexpr int kTaStages = 12;           // ring slots, each one tile's keys or values
-constexpr int kTaSoftmax = 128;         // threads = tensor-memory lanes
-constexpr int kTaProducer = 4, kTaMma = 5;
-constexpr int kTaThreads = 192;
+constexpr int kTaSoftmax = 256;         // two threads per tensor-memory lane
+constexpr int kTaProducer = 8, kTaMma = 9;
+constexpr int kTaThreads = 320;
 constexpr int kTaTmemCols = 512;
 constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
 constexpr float kTaLazy = 8.0f;         // a maximum is raised once a score exceeds it by 2^8
@@ -59,13 +58,20 @@ template <typename T, int D>
 struct TaShape {
   static constexpr int kTermsQ = sizeof(T) == 4 ? 3 : 1;
   static constexpr int kTermsP = sizeof(T) == 4 ? 3 : 2;
-  static constexpr int kSlot = kTaKeys * D * 2;            // bytes
+  static constexpr int kSlot = kTaKeys * D * 2;            // bytes of a ring slot: one tile's keys or values
+  // The whole ring is 192 KB for either D: a second CTA on an SM would only wait for the first one's
+  // tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
+  static constexpr int kStages = 192 * 1024 / kSlot;
   static constexpr int kBuf = kTermsP == 3 ? 96 : 64;      // columns of a score / weight buffer
   static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQ * D / 2;
+  // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
+  // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
+  // started afresh every kFlush tiles; next to a bf16 output the loss does not count.
+  static constexpr int kFlush = sizeof(T) == 4 ? 4 : 0;
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
-  static constexpr int kSmem = kTaStages * kSlot + 1024;   // and alignment
+  static constexpr int kSmem = kStages * kSlot + 1024;   // and alignment
   static_assert(kColS + 2 * kBuf <= kTaTmemCols, "tensor-memory columns");
-  static_assert(128 * kPitch * 4 <= kTaStages * kSlot, "the output is staged in the ring");
+  static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
 
 struct TaArgs {
@@ -160,6 +166,12 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ void tm_ld8(uint32_t addr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -168,19 +180,30 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-// Waits for this thread's tensor-memory loads; the values may be used only after it.
+// N columns (a multiple of 8) of this lane; the values may be used only after the wait in it.
 template <int N>
-__device__ __forceinline__ void tm_ld_wait(float (&r)[N]) {
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
+  if constexpr (N % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) tm_ld8(addr + i, r + i);
+  }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < N; i += 16)
+  for (int i = 0; i < N; i += 8)
     asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
-                 "+f"(r[i + 6]), "+f"(r[i + 7]), "+f"(r[i + 8]), "+f"(r[i + 9]), "+f"(r[i + 10]), "+f"(r[i + 11]),
-                 "+f"(r[i + 12]), "+f"(r[i + 13]), "+f"(r[i + 14]), "+f"(r[i + 15])::"memory");
+                 "+f"(r[i + 6]), "+f"(r[i + 7])::"memory");
 }
 __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tm_st4(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
                : "memory");
 }
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -196,6 +219,18 @@ __device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
 }
 __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// Barrier of the two warps that share a quarter of the lanes, and whether any lane of either says so.
+__device__ __forceinline__ void pair_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
+__device__ __forceinline__ bool pair_any(int quarter, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.aligned.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(1 + quarter), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 
 // Two values as pairs of bf16 terms, term t of both in w[t]: with three terms the leading 8, next
 // 8 and last 8 bits of the significand, cut off one after the other, so nothing is lost (a value
@@ -230,15 +265,15 @@ template <typename T, int D, int DUP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
   using S = TaShape<T, D>;
-  constexpr int kRows = 128 / DUP;       // rows of a tile
-  constexpr int kCols = kTaKeys / DUP;   // keys of a tile that one lane weighs
+  constexpr int kRows = 128 / DUP;           // rows of a tile
+  constexpr int kCols = kTaKeys / DUP / 2;   // keys of a tile that one thread weighs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * kTaStages + 7];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 7];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
-  __shared__ float2 s_ml[128];
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kTaStages, sfull0 = empty0 + 8 * kTaStages;
+  __shared__ float s_m[128], s_l[2][128], s_mx[2][128];
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
   const uint32_t pfull0 = sfull0 + 16, pvdone = pfull0 + 16, qfull = pvdone + 8, drain = qfull + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
@@ -249,7 +284,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const int rows = min(kRows, a.R - mt * kRows);
 
   if (i == 0) {
-    for (int s = 0; s < kTaStages; ++s) {
+    for (int s = 0; s < S::kStages; ++s) {
       bar_init(full0 + 8 * s, 1);
       bar_init(empty0 + 8 * s, 1);
     }
@@ -277,16 +312,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   // The set-up above overlaps the previous kernel; nothing below reads an input before its end.
   dependent_launch_wait();
 
-  float m = -INFINITY, l = 0.0f;  // this lane's reference maximum (log2 units) and weight sum
-  const int part = (i & 127) / kRows;     // which keys of a tile this lane weighs (the same in a warp)
-  const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-
   if (warp == kTaProducer) {
     if (lane == 0) {
       int k = 0;
       for (; k < 2 * n && !a.fault; ++k) {
-        const int s = k % kTaStages;
-        if (k >= kTaStages && !bar_wait(empty0 + 8 * s, ((k / kTaStages) - 1) & 1, fail, a.timeout_ns)) break;
+        const int s = k % S::kStages;
+        if (k >= S::kStages && !bar_wait(empty0 + 8 * s, ((k / S::kStages) - 1) & 1, fail, a.timeout_ns)) break;
         const bool val = k == 2 * n - 1 || (k > 0 && !(k & 1));
         const int t = t0 + (k == 2 * n - 1 ? n - 1 : k == 0 ? 0 : (k & 1) ? (k + 1) / 2 : k / 2 - 1);
         const bool tree = t >= a.pre_tiles;
@@ -299,40 +330,44 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
       // every copy must land before the CTA may exit
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-      for (int j = max(0, k - kTaStages); j < k; ++j)
-        while (!bar_try(full0 + 8 * (j % kTaStages), (j / kTaStages) & 1))
+      for (int j = max(0, k - S::kStages); j < k; ++j)
+        while (!bar_try(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1))
           if (globaltimer_ns() > deadline) break;
     }
   } else if (warp == kTaMma) {
     if (lane == 0) {
       auto scores = [&](int j) {
-        const int k = ring_key(j), s = k % kTaStages;
-        if (!bar_wait(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns)) return false;
+        const int k = ring_key(j), s = k % S::kStages;
+        if (!bar_wait(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns)) return false;
         tm_fence_after();
         const uint32_t d = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
+        const uint64_t bd = sdesc(b, 16);
+        // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t)
+        for (int t = S::kTermsQ - 1; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, sdesc(b + (kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32, 16),
-                       idesc_bf16(kTaKeys, false), (t | kk) != 0);
+            mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16,
+                       idesc_bf16(kTaKeys, false), t < S::kTermsQ - 1 || kk > 0);
         mma_commit(empty0 + 8 * s);
         mma_commit(sfull0 + 8 * (j & 1));
         return true;
       };
       auto values = [&](int j) {
-        const int k = ring_val(j, n), s = k % kTaStages;
-        if (!bar_wait(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns) ||
+        const int k = ring_val(j, n), s = k % S::kStages;
+        if (!bar_wait(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns) ||
             !bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns))
           return false;
         tm_fence_after();
         const uint32_t p = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
+        const uint64_t bd = sdesc(b, kTaKeys * 128);
+        const bool fresh = S::kFlush ? j % S::kFlush == 0 : j == 0;
 #pragma unroll
-        for (int t = 0; t < S::kTermsP; ++t)
+        for (int t = S::kTermsP - 1; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, sdesc(b + kk * 2048, kTaKeys * 128),
-                       idesc_bf16(D, true), (j | t | kk) != 0);
+            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
+                       t < S::kTermsP - 1 || kk > 0 || !fresh);
         mma_commit(empty0 + 8 * s);
         mma_commit(pvdone);
         return true;
@@ -349,13 +384,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (globaltimer_ns() > deadline) break;
     }
   } else {
-    const int r = i % kRows, rr = mt * kRows + r;  // row of the tile; node rr / G, head rr % G of the group
-    const int b = rr / a.G;
+    const int quarter = warp & 3, half = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
+    const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
+    const int rr = mt * kRows + r, b = rr / a.G;  // node b, head rr % G of the group
     const bool live = r < rows;
-    {  // the row's query terms into tensor memory
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    {  // the row's query terms into tensor memory, half of the dimensions each
       const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + rr % a.G) * D;
 #pragma unroll 2
-      for (int c = 0; c < D; c += 16) {
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         uint32_t w[S::kTermsQ][8];
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -384,19 +421,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tm_fence_before();
       bar_arrive(qfull);
     }
-    // a warp of rows past the last one only keeps the barriers going (its lanes' weights are
+    // warps of rows past the last one only keep the barriers going (their lanes' weights are
     // whatever the columns hold, and reach no row that is read)
     const bool idle = r - lane >= rows;
+    const int c0 = part * (kTaKeys / DUP) + half * kCols;  // this thread's first key of a tile
+    const uint32_t ocol = tl + S::kColO + half * (D / 2);  // and its half of the accumulator
     const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units), this thread's weight sum
+    float acc[S::kFlush ? D / 2 : 1];
+    if constexpr (S::kFlush > 0) {
+#pragma unroll
+      for (int e = 0; e < D / 2; ++e) acc[e] = 0.0f;
+    }
+    // After a wait that ran out a warp keeps walking the tiles, as the barrier with its other half
+    // needs it, and leaves the rest out.
+    bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t buf = tl + S::kColS + (j & 1) * S::kBuf;
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
-      if (tree) {  // take tree values that are not finite out of the product
-        const int k = ring_val(j, n), s = k % kTaStages;
-        if (!bar_wait_warp(full0 + 8 * s, (k / kTaStages) & 1, fail, a.timeout_ns)) break;
+      if (tree && ok) {  // take tree values that are not finite out of the product
+        const int k = ring_val(j, n), s = k % S::kStages;
+        ok = bar_wait_warp(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns);
         bool bad = false;
-        for (int e = i; e < S::kSlot / 16; e += kTaSoftmax) {
+        for (int e = i; ok && e < S::kSlot / 16; e += kTaSoftmax) {
           uint4* p = reinterpret_cast<uint4*>(ring + s * S::kSlot) + e;
           const uint4 v = *p;
           if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
@@ -409,13 +457,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (bad) s_bad = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      if (!bar_wait_warp(sfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns)) break;
+      ok = ok && bar_wait_warp(sfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
       tm_fence_after();
       if (!idle) {
         float s[kCols];
+        if (ok) tm_load(buf + c0, s);
+        else {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) tm_ld16(buf + part * kCols + c, s + c);
-        tm_ld_wait(s);
+          for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
+        }
         const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
         if (tree || left < kTaKeys) {
           uint64_t seen = ~0ull;
@@ -426,83 +476,109 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
           if (left < kTaKeys) seen &= (1ull << left) - 1;
           if (!live) seen = 0;
-          seen >>= part * kCols;
+          seen >>= c0;
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             if (!(seen >> c & 1)) s[c] = -INFINITY;
         }
-        float mx = s[0];
+        float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 1; c < kCols; ++c) mx = fmaxf(mx, s[c]);
-        mx *= a.scale_log2;
-        if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
-          const float mn = fmaxf(m, mx), corr = mn == m ? 1.0f : ex2(m - mn);
-          if (j > 0) {
-            if (!bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns)) break;
+        for (int c = 4; c < kCols; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+        float pend = 1.0f;  // rescaling of what the next flush adds
+        const bool flush = S::kFlush > 0 && j > 0 && j % (S::kFlush > 0 ? S::kFlush : 1) == 0;
+        // the barrier also stands between the loads of the scores and the weights that replace them
+        if (pair_any(quarter, mx > m + kTaLazy)) {
+          s_mx[half][ln] = mx;
+          pair_sync(quarter);
+          const float mn = fmaxf(m, fmaxf(mx, s_mx[half ^ 1][ln])), corr = mn == m ? 1.0f : ex2(m - mn);
+          if (flush) pend = corr;
+          else if (j > 0 && ok && (ok = bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns))) {
             tm_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tm_ld16(tl + S::kColO + c, o);
-              tm_ld16(tl + S::kColO + c + 16, o + 16);
-              tm_ld_wait(o);
-              uint32_t w[32];
+            for (int c = 0; c < D / 2; c += 16) {
+              float o[16];
+              tm_load(ocol + c, o);
+              uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * corr);
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) tm_st8(tl + S::kColO + c + e, w + e);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
+              tm_st8(ocol + c, w);
+              tm_st8(ocol + c + 8, w + 8);
             }
+          }
+          if constexpr (S::kFlush > 0) {
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) acc[e] *= corr;
           }
           l *= corr;
           m = mn;
         }
-        const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (ok) {
+          const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+          float ls[2] = {0.0f, 0.0f};
+          uint32_t w[S::kTermsP][kCols / 2];
 #pragma unroll
-        for (int c8 = 0; c8 < kCols / 16; ++c8) {
-          uint32_t w[S::kTermsP][8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = 16 * c8 + 2 * e;
+          for (int c = 0; c < kCols; c += 2) {
             const float p0 = ex2(fmaf(s[c], a.scale_log2, -mu)), p1 = ex2(fmaf(s[c + 1], a.scale_log2, -mu));
-            ls[e & 3] += p0 + p1;
+            ls[0] += p0;
+            ls[1] += p1;
             uint32_t x[S::kTermsP];
             split(p0, p1, x);
 #pragma unroll
-            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][e] = x[tt];
+            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = x[tt];
           }
+          l += ls[0] + ls[1];
 #pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt)
-            tm_st8(buf + tt * (kTaKeys / 2) + part * (kCols / 2) + 8 * c8, w[tt]);
+          for (int tt = 0; tt < S::kTermsP; ++tt) {
+            const uint32_t at = buf + tt * (kTaKeys / 2);
+            if constexpr (kCols >= 16) {
+#pragma unroll
+              for (int c = 0; c < kCols / 2; c += 8) tm_st8(at + c0 / 2 + c, w[tt] + c);
+            } else {
+              tm_st4(at + c0 / 2, w[tt]);
+            }
+            if constexpr (DUP > 1) {  // the keys that other lanes weigh
+#pragma unroll
+              for (int c = 0; c < kTaKeys / 2; c += 8)
+                if (c / (kTaKeys / 2 / DUP) != part && (c / 8 & 1) == half) tm_st8(at + c, zero);
+            }
+          }
+          if constexpr (S::kFlush > 0) {
+            if (flush && (ok = bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns))) {
+              tm_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 2; c += 16) {
+                float o[16];
+                tm_load(ocol + c, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], pend, acc[c + e]);
+              }
+            }
+          }
+          tm_st_wait();
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-        if constexpr (DUP > 1) {  // the keys that other lanes weigh
-#pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt)
-#pragma unroll
-            for (int c = 0; c < kTaKeys / 2; c += 8)
-              if (c / (kCols / 2) != part) tm_st8(buf + tt * (kTaKeys / 2) + c, zero);
-        }
-        tm_st_wait();
       }
       tm_fence_before();
-      bar_arrive(pfull0 + 8 * (j & 1));
+      if (ok) bar_arrive(pfull0 + 8 * (j & 1));
     }
     // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
-    const bool ok = bar_wait_warp(drain, 0, fail, a.timeout_ns);
+    ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
     tm_fence_after();
     if (ok) {
-      float* st = reinterpret_cast<float*>(ring) + i * S::kPitch;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        tm_ld16(tl + S::kColO + c, o);
-        tm_ld16(tl + S::kColO + c + 16, o + 16);
-        tm_ld_wait(o);
+      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + half * (D / 2);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      for (int c = 0; c < D / 2; c += 16) {
+        float o[16];
+        tm_load(ocol + c, o);
+        if constexpr (S::kFlush > 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] += acc[c + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      s_ml[i] = make_float2(m, l);
+      if (half == 0) s_m[ln] = m;
+      s_l[half][ln] = l;
     }
   }
   tm_fence_before();
@@ -519,14 +595,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int r = e / (D / 4), c = e % (D / 4) * 4;
     float M = -INFINITY, L = 0.0f;
 #pragma unroll
-    for (int d = 0; d < DUP; ++d) M = fmaxf(M, s_ml[r + d * kRows].x);
+    for (int d = 0; d < DUP; ++d) M = fmaxf(M, s_m[r + d * kRows]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int d = 0; d < DUP; ++d) {
-      const float2 ml = s_ml[r + d * kRows];
-      const float4 x = *reinterpret_cast<const float4*>(st + (r + d * kRows) * S::kPitch + c);
-      const float w = DUP == 1 || ml.x == M ? 1.0f : ex2(ml.x - M);
-      L = fmaf(ml.y, w, L);
+      const int ln = r + d * kRows;
+      const float4 x = *reinterpret_cast<const float4*>(st + ln * S::kPitch + c);
+      const float w = DUP == 1 || s_m[ln] == M ? 1.0f : ex2(s_m[ln] - M);
+      L = fmaf(s_l[0][ln] + s_l[1][ln], w, L);
       o.x = fmaf(x.x, w, o.x);
       o.y = fmaf(x.y, w, o.y);
       o.z = fmaf(x.z, w, o.z);
