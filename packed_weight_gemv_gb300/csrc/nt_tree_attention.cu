@@ -38,6 +38,7 @@
 #include <atomic>
 #include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "nt_kernels.cuh"
 
@@ -62,15 +63,25 @@ struct TaShape {
   // The whole ring is 192 KB for either D: a second CTA on an SM would only wait for the first one's
   // tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
   static constexpr int kStages = 192 * 1024 / kSlot;
-  static constexpr int kBuf = kTermsP == 3 ? 96 : 64;      // columns of a score / weight buffer
-  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQ * D / 2;
+  // Tensor-memory columns: the accumulator, the query terms, two score buffers and the weights.
+  // Where two buffers of all weight terms do not fit beside them (fp32 queries, D = 128), the
+  // smallest term goes over the scores it came from and one buffer holds the others.
+  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQ * D / 2, kColP = kColS + 2 * kTaKeys;
+  static constexpr bool kLowOverS = kColP + 2 * kTermsP * (kTaKeys / 2) > kTaTmemCols;
+  static constexpr int kPBufs = kLowOverS ? 1 : 2;
+  static constexpr int kPCols = (kTermsP - (kLowOverS ? 1 : 0)) * (kTaKeys / 2);
+  // The queries pass through the end of the ring on their way to tensor memory: per warp 32 rows of
+  // half the dimensions, 16 bytes apart from a multiple of 128 so that a column of rows has no
+  // bank conflicts.
+  static constexpr int kQRow = D / 2 * (int)sizeof(T), kQPitch = kQRow + 16;
+  static constexpr int kQSlot = kStages - (kTaSoftmax * kQPitch + kSlot - 1) / kSlot;  // first ring slot they use
   // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
   // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
   // started afresh every kFlush tiles; next to a bf16 output the loss does not count.
   static constexpr int kFlush = sizeof(T) == 4 ? 4 : 0;
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
   static constexpr int kSmem = kStages * kSlot + 1024;   // and alignment
-  static_assert(kColS + 2 * kBuf <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kColP + kPBufs * kPCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
 
@@ -89,6 +100,7 @@ struct TaArgs {
   int prefix, pre_tiles, tiles;  // 64-key tiles of the sequence, and with the tree's
   int nsplit, mtiles;
   float scale_log2;         // log2(e) / sqrt(D)
+  float inv_g;              // 1 / G
 };
 struct TaMaps {
   CUtensorMap kp, vp, kt, vt;  // sequence and tree rows of keys and values
@@ -127,6 +139,11 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
   return bar_try(bar, parity) || bar_wait_slow(bar, parity, fail, timeout_ns);
 }
+// One arrival for a warp (32 separate ones, times eight warps, held a tile up by 350 cycles).
+__device__ __forceinline__ void bar_arrive_warp(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) bar_arrive(bar);
+}
 // The same for a whole warp: every lane gets one answer, so the warp stays together.
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, fail, timeout_ns));
@@ -159,6 +176,14 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdes
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp, the same one every time: code under it stays uniform for the
+// compiler, which feeds the MMAs from uniform registers (measured: 29 cycles to issue a 128 x 64 x 16
+// MMA instead of 45 under `lane == 0`; its execution takes 32).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -232,6 +257,23 @@ __device__ __forceinline__ bool pair_any(int quarter, bool x) {
   return r != 0;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
 // Two values as pairs of bf16 terms, term t of both in w[t]: with three terms the leading 8, next
 // 8 and last 8 bits of the significand, cut off one after the other, so nothing is lost (a value
 // below 2^-110 aside); otherwise each term is the rest so far, rounded.
@@ -240,10 +282,12 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[N]) {
   if constexpr (N == 3) {
     const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
     w[0] = prmt(ux, uy, 0x7632u);
-    const float rx = x - high_f(ux), ry = y - high_f(uy);
-    w[1] = prmt(__float_as_uint(rx), __float_as_uint(ry), 0x7632u);
-    const float sx = rx - high_f(__float_as_uint(rx)), sy = ry - high_f(__float_as_uint(ry));
-    w[2] = prmt(__float_as_uint(sx), __float_as_uint(sy), 0x7632u);
+    // differences as x - h = fma(h, -1, x)
+    const float2 neg = make_float2(-1.0f, -1.0f);
+    const float2 r = fma2(make_float2(high_f(ux), high_f(uy)), neg, make_float2(x, y));
+    w[1] = prmt(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632u);
+    const float2 q = fma2(make_float2(high_f(__float_as_uint(r.x)), high_f(__float_as_uint(r.y))), neg, r);
+    w[2] = prmt(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632u);
   } else {
 #pragma unroll
     for (int t = 0; t < N; ++t) {
@@ -258,6 +302,9 @@ __device__ __forceinline__ bool word_bad(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// Node of a row, row / G: exact for rows up to 2^20 (half a row is more than the product's error).
+__device__ __forceinline__ int node_of(int row, float inv_g) { return (int)(((float)row + 0.5f) * inv_g); }
+
 __device__ __forceinline__ int ring_key(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int ring_val(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
 
@@ -269,12 +316,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   constexpr int kCols = kTaKeys / DUP / 2;   // keys of a tile that one thread weighs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 7];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
   __shared__ float s_m[128], s_l[2][128], s_mx[2][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
-  const uint32_t pfull0 = sfull0 + 16, pvdone = pfull0 + 16, qfull = pvdone + 8, drain = qfull + 8;
+  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, lowdone = pvdone0 + 16, qfull = lowdone + 8, drain = qfull + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
@@ -290,10 +337,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(sfull0 + 8 * b, 1);
-      bar_init(pfull0 + 8 * b, kTaSoftmax);
+      bar_init(pfull0 + 8 * b, kTaSoftmax / 32);
+      bar_init(pvdone0 + 8 * b, 1);
     }
-    bar_init(pvdone, 1);
-    bar_init(qfull, kTaSoftmax);
+    bar_init(lowdone, 1);
+    bar_init(qfull, kTaSoftmax / 32);
     bar_init(drain, 1);
     s_fail = 0;
     s_bad = 0;
@@ -318,6 +366,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (; k < 2 * n && !a.fault; ++k) {
         const int s = k % S::kStages;
         if (k >= S::kStages && !bar_wait(empty0 + 8 * s, ((k / S::kStages) - 1) & 1, fail, a.timeout_ns)) break;
+        if (k == S::kQSlot && !bar_wait(qfull, 0, fail, a.timeout_ns)) break;  // the queries have left the ring
         const bool val = k == 2 * n - 1 || (k > 0 && !(k & 1));
         const int t = t0 + (k == 2 * n - 1 ? n - 1 : k == 0 ? 0 : (k & 1) ? (k + 1) / 2 : k / 2 - 1);
         const bool tree = t >= a.pre_tiles;
@@ -335,13 +384,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (globaltimer_ns() > deadline) break;
     }
   } else if (warp == kTaMma) {
-    if (lane == 0) {
+    if (elect_one()) {
       auto scores = [&](int j) {
         const int k = ring_key(j), s = k % S::kStages;
-        if (!bar_wait(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns)) return false;
-        tm_fence_after();
-        const uint32_t d = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
-        const uint64_t bd = sdesc(b, 16);
+        const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
+        const uint64_t bd = sdesc(smem_u32(ring + s * S::kSlot), 16);
         // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
         for (int t = S::kTermsQ - 1; t >= 0; --t)
@@ -349,58 +396,85 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int kk = 0; kk < D / 16; ++kk)
             mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16,
                        idesc_bf16(kTaKeys, false), t < S::kTermsQ - 1 || kk > 0);
-        mma_commit(empty0 + 8 * s);
         mma_commit(sfull0 + 8 * (j & 1));
-        return true;
+        mma_commit(empty0 + 8 * s);
       };
       auto values = [&](int j) {
         const int k = ring_val(j, n), s = k % S::kStages;
-        if (!bar_wait(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns) ||
-            !bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns))
-          return false;
-        tm_fence_after();
-        const uint32_t p = tmem + S::kColS + (j & 1) * S::kBuf, b = smem_u32(ring + s * S::kSlot);
-        const uint64_t bd = sdesc(b, kTaKeys * 128);
+        const uint32_t p = tmem + S::kColP + (j % S::kPBufs) * S::kPCols;
+        const uint64_t bd = sdesc(smem_u32(ring + s * S::kSlot), kTaKeys * 128);
         const bool fresh = S::kFlush ? j % S::kFlush == 0 : j == 0;
 #pragma unroll
-        for (int t = S::kTermsP - 1; t >= 0; --t)
+        for (int t = S::kTermsP - 1; t >= 0; --t) {
+          const bool low = S::kLowOverS && t == S::kTermsP - 1;
+          const uint32_t pt = low ? tmem + S::kColS + (j & 1) * kTaKeys : p + t * (kTaKeys / 2);
 #pragma unroll
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
+            mma_tmem_a(tmem + S::kColO, pt + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
                        t < S::kTermsP - 1 || kk > 0 || !fresh);
+          if (low) mma_commit(lowdone);
+        }
+        mma_commit(pvdone0 + 8 * (j & 1));
         mma_commit(empty0 + 8 * s);
-        mma_commit(pvdone);
-        return true;
       };
-      bool ok = bar_wait(qfull, 0, fail, a.timeout_ns) && scores(0) && (n < 2 || scores(1));
+      auto loaded = [&](int k) { return bar_wait(full0 + 8 * (k % S::kStages), (k / S::kStages) & 1, fail, a.timeout_ns); };
+      bool ok = bar_wait(qfull, 0, fail, a.timeout_ns);
+      tm_fence_after();
+      for (int j = 0; ok && j < min(n, 2); ++j)
+        if ((ok = loaded(ring_key(j)))) scores(j);
       for (int j = 0; ok && j < n; ++j) {
-        ok = values(j);
-        // the weights of tile j must have been read before the scores of tile j + 2 replace them
-        if (ok && j + 2 < n) ok = bar_wait(pvdone, j & 1, fail, a.timeout_ns) && scores(j + 2);
+        ok = loaded(ring_val(j, n)) && bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+        if (!ok) break;
+        tm_fence_after();
+        values(j);
+        if (j + 2 < n) {
+          // the scores of tile j have been taken (its weights are here); what replaces them has to wait
+          // only for the weight term that stands over them, read first
+          ok = loaded(ring_key(j + 2)) && (!S::kLowOverS || bar_wait(lowdone, j & 1, fail, a.timeout_ns));
+          if (ok) {
+            tm_fence_after();
+            scores(j + 2);
+          }
+        }
       }
       mma_commit(drain);  // every MMA of this CTA done, before the memory is freed
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
       while (!bar_try(drain, 0))
         if (globaltimer_ns() > deadline) break;
     }
+    __syncwarp();
   } else {
     const int quarter = warp & 3, half = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
     const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
-    const int rr = mt * kRows + r, b = rr / a.G;  // node b, head rr % G of the group
+    const int b = node_of(mt * kRows + r, a.inv_g);
     const bool live = r < rows;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     {  // the row's query terms into tensor memory, half of the dimensions each
-      const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + rr % a.G) * D;
-#pragma unroll 2
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+      constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a half row; half rows per load
+      uint8_t* stage = ring + S::kQSlot * S::kSlot + warp * 32 * S::kQPitch;
+      uint4 v[kVecs];
+#pragma unroll
+      for (int e = 0; e < kVecs; ++e) {  // whole rows at a time: 32 lanes read 512 contiguous bytes or a few pieces
+        const int ri = (quarter * 32 + e * kAtOnce + lane / kVecs) % kRows, ra = mt * kRows + ri;
+        const int rb = node_of(ra, a.inv_g);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + half * (D / 2);
+        v[e] = ri < rows ? reinterpret_cast<const uint4*>(q)[lane % kVecs] : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int e = 0; e < kVecs; ++e)
+        *reinterpret_cast<uint4*>(stage + (e * kAtOnce + lane / kVecs) * S::kQPitch + lane % kVecs * 16) = v[e];
+      __syncwarp();
+      const uint4* own = reinterpret_cast<const uint4*>(stage + lane * S::kQPitch);
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 16) {
         uint32_t w[S::kTermsQ][8];
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 v = live ? reinterpret_cast<const float4*>(q + c)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint4 u = own[c / 4 + e];
             uint32_t x[3], y[3];
-            split(v.x, v.y, x);
-            split(v.z, v.w, y);
+            split(__uint_as_float(u.x), __uint_as_float(u.y), x);
+            split(__uint_as_float(u.z), __uint_as_float(u.w), y);
 #pragma unroll
             for (int t = 0; t < S::kTermsQ; ++t) {
               w[t][2 * e] = x[t];
@@ -410,16 +484,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint4 v = live ? reinterpret_cast<const uint4*>(q + c)[e] : make_uint4(0u, 0u, 0u, 0u);
-            w[0][4 * e] = v.x; w[0][4 * e + 1] = v.y; w[0][4 * e + 2] = v.z; w[0][4 * e + 3] = v.w;
+            const uint4 u = own[c / 8 + e];
+            w[0][4 * e] = u.x; w[0][4 * e + 1] = u.y; w[0][4 * e + 2] = u.z; w[0][4 * e + 3] = u.w;
           }
         }
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + c / 2, w[t]);
+        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (half * (D / 2) + c) / 2, w[t]);
       }
       tm_st_wait();
       tm_fence_before();
-      bar_arrive(qfull);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies into the staging slots come after
+      bar_arrive_warp(qfull, lane);
     }
     // warps of rows past the last one only keep the barriers going (their lanes' weights are
     // whatever the columns hold, and reach no row that is read)
@@ -437,7 +512,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // needs it, and leaves the rest out.
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const uint32_t buf = tl + S::kColS + (j & 1) * S::kBuf;
+      const uint32_t buf = tl + S::kColS + (j & 1) * kTaKeys;
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
       if (tree && ok) {  // take tree values that are not finite out of the product
@@ -493,7 +568,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           pair_sync(quarter);
           const float mn = fmaxf(m, fmaxf(mx, s_mx[half ^ 1][ln])), corr = mn == m ? 1.0f : ex2(m - mn);
           if (flush) pend = corr;
-          else if (j > 0 && ok && (ok = bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns))) {
+          else if (j > 0 && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
             tm_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
@@ -515,22 +590,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         if (ok) {
           const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
-          float ls[2] = {0.0f, 0.0f};
+          float2 ls = make_float2(0.0f, 0.0f);
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
           uint32_t w[S::kTermsP][kCols / 2];
 #pragma unroll
           for (int c = 0; c < kCols; c += 2) {
-            const float p0 = ex2(fmaf(s[c], a.scale_log2, -mu)), p1 = ex2(fmaf(s[c + 1], a.scale_log2, -mu));
-            ls[0] += p0;
-            ls[1] += p1;
-            uint32_t x[S::kTermsP];
-            split(p0, p1, x);
+            const float2 x = fma2(make_float2(s[c], s[c + 1]), sc, mm);
+            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+            ls = add2(ls, pp);
+            uint32_t term[S::kTermsP];
+            split(pp.x, pp.y, term);
 #pragma unroll
-            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = x[tt];
+            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
-          l += ls[0] + ls[1];
+          l += ls.x + ls.y;
+          // the buffer's last weights must have been read
+          if (j >= S::kPBufs)
+            ok = bar_wait_warp(pvdone0 + 8 * ((j - S::kPBufs) & 1), ((j - S::kPBufs) >> 1) & 1, fail, a.timeout_ns);
+          tm_fence_after();
 #pragma unroll
           for (int tt = 0; tt < S::kTermsP; ++tt) {
-            const uint32_t at = buf + tt * (kTaKeys / 2);
+            const uint32_t at = S::kLowOverS && tt == S::kTermsP - 1 ? buf
+                                                                     : tl + S::kColP + (j % S::kPBufs) * S::kPCols + tt * (kTaKeys / 2);
             if constexpr (kCols >= 16) {
 #pragma unroll
               for (int c = 0; c < kCols / 2; c += 8) tm_st8(at + c0 / 2 + c, w[tt] + c);
@@ -544,7 +625,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
           }
           if constexpr (S::kFlush > 0) {
-            if (flush && (ok = bar_wait_warp(pvdone, (j - 1) & 1, fail, a.timeout_ns))) {
+            if (flush && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
               tm_fence_after();
 #pragma unroll
               for (int c = 0; c < D / 2; c += 16) {
@@ -559,7 +640,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
       tm_fence_before();
-      if (ok) bar_arrive(pfull0 + 8 * (j & 1));
+      if (ok) bar_arrive_warp(pfull0 + 8 * (j & 1), lane);
     }
     // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
     ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
@@ -608,7 +689,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       o.z = fmaf(x.z, w, o.z);
       o.w = fmaf(x.w, w, o.w);
     }
-    const int rr = mt * kRows + r, b = rr / a.G;
+    const int rr = mt * kRows + r, b = node_of(rr, a.inv_g);
     if (s_bad) {  // tree values that are not finite, for the nodes that see them
       for (int k = max(t0 - a.pre_tiles, 0) * kTaKeys; k < min(a.B, (t0 + n - a.pre_tiles) * kTaKeys); ++k) {
         if (!(a.mask[(int64_t)b * a.words + (k >> 5)] >> (k & 31) & 1u)) continue;
@@ -625,7 +706,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if (c == 0) a.ml[at] = make_float2(M, L);
     } else {
       const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
-      const int64_t at = ((int64_t)b * a.Hq + g * a.G + rr % a.G) * D + c;
+      const int64_t at = ((int64_t)b * a.Hq + g * a.G + (rr - b * a.G)) * D + c;
       if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
       else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
     }
@@ -643,29 +724,38 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
   const int rr = b * a.G + h % a.G, mt = rr / rows_per_tile, r = rr % rows_per_tile;
   const int64_t first = ((int64_t)g * a.nsplit * a.mtiles + mt) * rows_per_tile + r;
   const int64_t step = (int64_t)a.mtiles * rows_per_tile;
-  float M = -INFINITY;
-  for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, a.ml[first + s * step].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.0f, acc[E];
+  using V = typename std::conditional<E == 4, float4, float2>::type;
+  float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < a.nsplit; ++s) {
-    const int64_t at = first + s * step;
-    const float2 ml = a.ml[at];
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 v = reinterpret_cast<const float4*>(a.part + at * D)[lane];
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = reinterpret_cast<const float2*>(a.part + at * D)[lane];
-      x[0] = v.x; x[1] = v.y;
-    }
-    const float w = ml.x == M ? 1.0f : ex2(ml.x - M);  // M = -inf: nothing seen, all sums 0
-    L = fmaf(ml.y, w, L);
+  for (int s0 = 0; s0 < a.nsplit; s0 += 32) {  // 32 splits: a lane has the maximum and sum of one
+    const int cnt = min(32, a.nsplit - s0);
+    const float2 ml = lane < cnt ? __ldcg(a.ml + first + (s0 + lane) * step) : make_float2(-INFINITY, 0.0f);
+    float mn = ml.x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], w, acc[e]);
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(M, mn);
+    const float corr = M == mn ? 1.0f : ex2(M - mn);  // M = -inf: nothing seen so far, all sums 0
+    const float wl = ml.x == mn ? 1.0f : ex2(ml.x - mn);
+    M = mn;
+    L *= corr;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= corr;
+    for (int k0 = 0; k0 < cnt; k0 += 8) {
+      V x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = __ldcg(reinterpret_cast<const V*>(a.part + (first + (s0 + min(k0 + k, cnt - 1)) * step) * D) + lane);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k0 + k >= cnt) break;  // the same in every lane
+        const float w = __shfl_sync(0xffffffffu, wl, k0 + k);
+        L = fmaf(__shfl_sync(0xffffffffu, ml.y, k0 + k), w, L);
+        const float* xe = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(xe[e], w, acc[e]);
+      }
+    }
   }
   const float s = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
@@ -817,6 +907,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
   a.mtiles = p.mtiles;
+  a.inv_g = 1.0f / (float)a.G;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   TaMaps maps;
   // without a sequence its maps are not used; they still have to be valid
