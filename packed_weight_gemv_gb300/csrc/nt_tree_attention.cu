@@ -51,6 +51,7 @@ constexpr int kTaProducer = 8, kTaMma = 9;
 constexpr int kTaThreads = 320;
 constexpr int kTaTmemCols = 512;
 constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
+constexpr int kTaFirst = 3;             // ring slots filled before the queries have arrived
 constexpr float kTaLazy = 8.0f;         // a maximum is raised once a score exceeds it by 2^8
 constexpr uint64_t kTaTimeoutNs = 2000000000ull;
 constexpr unsigned int kTaErrWait = 18;  // status code of a wait that ran out
@@ -81,6 +82,7 @@ struct TaShape {
   static constexpr int kFlush = sizeof(T) == 4 ? 4 : 0;
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
   static constexpr int kSmem = kStages * kSlot + 1024;   // and alignment
+  static_assert(kQSlot >= kTaFirst, "the queries' staging slots are filled after them");
   static_assert(kColP + kPBufs * kPCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
@@ -125,12 +127,16 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait; false after the timeout or once another role of the CTA has given up.
+// Bounded wait; false after the timeout or once another role of the CTA has given up. The clock
+// is first read after 256 polls: reading it before the first one cost every short wait 300 cycles.
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
-  const uint64_t deadline = globaltimer_ns() + timeout_ns;
+  uint64_t deadline = 0;
   for (uint32_t it = 1;; ++it) {
     if (bar_try(bar, parity)) return true;
-    if ((it & 63u) == 0u && (*fail || globaltimer_ns() > deadline)) {
+    if ((it & 255u) != 0u) continue;
+    const uint64_t now = globaltimer_ns();
+    if (deadline == 0) deadline = now + timeout_ns;
+    if (*fail || now > deadline) {
       *fail = 1;
       return false;
     }
@@ -205,9 +211,9 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-// N columns (a multiple of 8) of this lane; the values may be used only after the wait in it.
+// N columns (a multiple of 8) of this lane: the loads, and the wait before the values may be used.
 template <int N>
-__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
+__device__ __forceinline__ void tm_load_begin(uint32_t addr, float (&r)[N]) {
   if constexpr (N % 16 == 0) {
 #pragma unroll
     for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
@@ -215,11 +221,19 @@ __device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 8) tm_ld8(addr + i, r + i);
   }
+}
+template <int N>
+__device__ __forceinline__ void tm_load_end(float (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i += 8)
     asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
                  "+f"(r[i + 6]), "+f"(r[i + 7])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
+  tm_load_begin(addr, r);
+  tm_load_end(r);
 }
 __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
@@ -366,7 +380,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (; k < 2 * n && !a.fault; ++k) {
         const int s = k % S::kStages;
         if (k >= S::kStages && !bar_wait(empty0 + 8 * s, ((k / S::kStages) - 1) & 1, fail, a.timeout_ns)) break;
-        if (k == S::kQSlot && !bar_wait(qfull, 0, fail, a.timeout_ns)) break;  // the queries have left the ring
+        // The first tiles' keys and values, then the queries (which pass through the ring's end), then
+        // the rest: with the whole ring asked for at once the queries arrived 4 us later.
+        if (k == kTaFirst && !bar_wait(qfull, 0, fail, a.timeout_ns)) break;
         const bool val = k == 2 * n - 1 || (k > 0 && !(k & 1));
         const int t = t0 + (k == 2 * n - 1 ? n - 1 : k == 0 ? 0 : (k & 1) ? (k + 1) / 2 : k / 2 - 1);
         const bool tree = t >= a.pre_tiles;
@@ -713,14 +729,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   }
 }
 
-// Joins the splits of a row: one warp per row, a lane D / 32 of its dimensions.
-template <typename T, int D>
+// Joins the splits of a row: W warps of a CTA share a row (warp w takes splits w, w + W, ...), a
+// lane D / 32 of its dimensions. A warp's first 8 splits are asked for together with their maxima, so
+// up to 8 W splits take one round trip to L2.
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int rows_per_tile) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kBatch = 8;
+  __shared__ float s_m[4], s_l[4], s_o[W > 1 ? 4 : 1][D];
   dependent_launch_wait();
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // b * Hq + h
-  if (row >= (int64_t)a.B * a.Hq) return;
-  const int lane = threadIdx.x & 31, b = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / a.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+  const int64_t row = min((int64_t)blockIdx.x * (4 / W) + warp / W, (int64_t)a.B * a.Hq - 1);  // b * Hq + h
+  const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / a.G;
   const int rr = b * a.G + h % a.G, mt = rr / rows_per_tile, r = rr % rows_per_tile;
   const int64_t first = ((int64_t)g * a.nsplit * a.mtiles + mt) * rows_per_tile + r;
   const int64_t step = (int64_t)a.mtiles * rows_per_tile;
@@ -728,33 +747,56 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
   float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int s0 = 0; s0 < a.nsplit; s0 += 32) {  // 32 splits: a lane has the maximum and sum of one
-    const int cnt = min(32, a.nsplit - s0);
-    const float2 ml = lane < cnt ? __ldcg(a.ml + first + (s0 + lane) * step) : make_float2(-INFINITY, 0.0f);
-    float mn = ml.x;
+  for (int s0 = w; s0 < a.nsplit; s0 += kBatch * W) {
+    V x[kBatch];
+    float2 ml[kBatch];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mn = fmaxf(M, mn);
+    for (int k = 0; k < kBatch; ++k) {
+      const int s = s0 + k * W;
+      const int64_t at = first + min(s, a.nsplit - 1) * step;
+      x[k] = __ldcg(reinterpret_cast<const V*>(a.part + at * D) + lane);
+      ml[k] = __ldcg(a.ml + at);
+      if (s >= a.nsplit) ml[k] = make_float2(-INFINITY, 0.0f);
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
     const float corr = M == mn ? 1.0f : ex2(M - mn);  // M = -inf: nothing seen so far, all sums 0
-    const float wl = ml.x == mn ? 1.0f : ex2(ml.x - mn);
-    M = mn;
     L *= corr;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= corr;
-    for (int k0 = 0; k0 < cnt; k0 += 8) {
-      V x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        x[k] = __ldcg(reinterpret_cast<const V*>(a.part + (first + (s0 + min(k0 + k, cnt - 1)) * step) * D) + lane);
+    for (int k = 0; k < kBatch; ++k) {
+      if (s0 + k * W >= a.nsplit) break;
+      const float wt = ml[k].x == mn ? 1.0f : ex2(ml[k].x - mn);
+      L = fmaf(ml[k].y, wt, L);
+      const float* xe = reinterpret_cast<const float*>(&x[k]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k0 + k >= cnt) break;  // the same in every lane
-        const float w = __shfl_sync(0xffffffffu, wl, k0 + k);
-        L = fmaf(__shfl_sync(0xffffffffu, ml.y, k0 + k), w, L);
-        const float* xe = reinterpret_cast<const float*>(&x[k]);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(xe[e], wt, acc[e]);
+    }
+    M = mn;
+  }
+  if constexpr (W > 1) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(xe[e], w, acc[e]);
-      }
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (w != 0) return;
+    float mn = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < W; ++k) mn = fmaxf(mn, s_m[warp + k]);
+    L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float wt = s_m[warp + k] == mn ? 1.0f : ex2(s_m[warp + k] - mn);
+      L = fmaf(s_l[warp + k], wt, L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(s_o[warp + k][lane * E + e], wt, acc[e]);
     }
   }
   const float s = L == 0.0f ? 0.0f : 1.0f / L;
@@ -839,7 +881,9 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
   NT_TRY(check_launch("tree_attn_kernel"));
   if (p.nsplit > 1) {
     const int64_t rows = (int64_t)a.B * a.Hq;
-    NT_CUDA_TRY(launch_kernel(tree_attn_join_kernel<T, D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, true, a, p.rows));
+    const int w = p.nsplit > 8 ? 4 : 1;  // warps per row
+    auto join = w == 4 ? tree_attn_join_kernel<T, D, 4> : tree_attn_join_kernel<T, D, 1>;
+    NT_CUDA_TRY(launch_kernel(join, dim3((unsigned)((rows * w + 3) / 4)), dim3(128), 0, st, true, a, p.rows));
     NT_TRY(check_launch("tree_attn_join_kernel"));
   }
   return NT_OK;
