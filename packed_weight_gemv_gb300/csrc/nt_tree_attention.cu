@@ -14,10 +14,10 @@
 //
 // CTA (320 threads): one tile of rows, one key-value head, a range of 64-key tiles.
 //   warp 8 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
-//   warp 9 lane 0  -- MMA issuer: scores of tile j + 2 and weighted values of tile j, while
+//   warp 9         -- MMA issuer (one lane): weighted values of tile j, then scores of tile j + 2, while
 //   warps 0-7      -- (two threads per row = tensor-memory lane) turn the scores of tile j + 1 into
-//                     weights over the same columns. The reference maximum m of a row is raised only
-//                     when a score exceeds it by 2^8, and the accumulator rescaled only then.
+//                     weights. The reference maximum m of a row is raised only when a score exceeds
+//                     it by 2^8, and the accumulator rescaled only then.
 // Few rows are spread over the lanes: with R <= 32 (64) each row stands in four (two) lanes, each
 // of which weighs a quarter (half) of every tile's keys with a maximum and sum of its own and
 // leaves zeros elsewhere; their accumulators are joined at the end. So the instructions of the
@@ -46,9 +46,10 @@ namespace nt {
 namespace {
 
 constexpr int kTaKeys = 64;             // keys per tile
-constexpr int kTaSoftmax = 256;         // two threads per tensor-memory lane
-constexpr int kTaProducer = 8, kTaMma = 9;
-constexpr int kTaThreads = 320;
+constexpr int kTaSub = 2;               // threads per tensor-memory lane (row)
+constexpr int kTaSoftmax = 128 * kTaSub;
+constexpr int kTaProducer = kTaSoftmax / 32, kTaMma = kTaProducer + 1;
+constexpr int kTaThreads = kTaSoftmax + 64;
 constexpr int kTaTmemCols = 512;
 constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
 constexpr int kTaFirst = 3;             // ring slots filled before the queries have arrived
@@ -74,7 +75,7 @@ struct TaShape {
   // The queries pass through the end of the ring on their way to tensor memory: per warp 32 rows of
   // half the dimensions, 16 bytes apart from a multiple of 128 so that a column of rows has no
   // bank conflicts.
-  static constexpr int kQRow = D / 2 * (int)sizeof(T), kQPitch = kQRow + 16;
+  static constexpr int kQRow = D / kTaSub * (int)sizeof(T), kQPitch = kQRow + 16;
   static constexpr int kQSlot = kStages - (kTaSoftmax * kQPitch + kSlot - 1) / kSlot;  // first ring slot they use
   // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
   // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
@@ -150,6 +151,21 @@ __device__ __forceinline__ void bar_arrive_warp(uint32_t bar, int lane) {
   __syncwarp();
   if (lane == 0) bar_arrive(bar);
 }
+// Two barriers tested together: a test takes 110 cycles, of which the two share most.
+__device__ __forceinline__ bool bar_try2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, volatile int* fail,
+                                          uint64_t timeout_ns) {
+  return bar_try2(b0, p0, b1, p1) || (bar_wait_slow(b0, p0, fail, timeout_ns) && bar_wait_slow(b1, p1, fail, timeout_ns));
+}
 // The same for a whole warp: every lane gets one answer, so the warp stays together.
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, fail, timeout_ns));
@@ -211,39 +227,37 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-// N columns (a multiple of 8) of this lane: the loads, and the wait before the values may be used.
+// N columns (8, 16 or 32) of this lane; the values may be used only after the wait in it.
 template <int N>
-__device__ __forceinline__ void tm_load_begin(uint32_t addr, float (&r)[N]) {
-  if constexpr (N % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
+  if constexpr (N == 8) {
+    tm_ld8(addr, r);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 8) tm_ld8(addr + i, r + i);
+    for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
   }
-}
-template <int N>
-__device__ __forceinline__ void tm_load_end(float (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i += 8)
     asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
                  "+f"(r[i + 6]), "+f"(r[i + 7])::"memory");
 }
-template <int N>
-__device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
-  tm_load_begin(addr, r);
-  tm_load_end(r);
-}
 __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tm_st4(uint32_t addr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3])
-               : "memory");
+template <int N>
+__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t (&r)[N]) {
+  if constexpr (N >= 8) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) tm_st8(addr + i, r + i);
+  } else {
+    static_assert(N == 4, "columns");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+  }
 }
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -259,14 +273,16 @@ __device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
 __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// Barrier of the two warps that share a quarter of the lanes, and whether any lane of either says so.
-__device__ __forceinline__ void pair_sync(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
-__device__ __forceinline__ bool pair_any(int quarter, bool x) {
+// Barrier of the warps that share a quarter of the lanes, and whether any lane of theirs says so.
+__device__ __forceinline__ void quarter_sync(int quarter) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kTaSub) : "memory");
+}
+__device__ __forceinline__ bool quarter_any(int quarter, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.aligned.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.aligned.pred q, %1, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(1 + quarter), "r"((uint32_t)x)
+      : "r"(1 + quarter), "r"((uint32_t)x), "n"(32 * kTaSub)
       : "memory");
   return r != 0;
 }
@@ -326,14 +342,15 @@ template <typename T, int D, int DUP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
   using S = TaShape<T, D>;
-  constexpr int kRows = 128 / DUP;           // rows of a tile
-  constexpr int kCols = kTaKeys / DUP / 2;   // keys of a tile that one thread weighs
+  constexpr int kRows = 128 / DUP;               // rows of a tile
+  constexpr int kCols = kTaKeys / DUP / kTaSub;  // keys of a tile that one thread weighs
+  constexpr int kDims = D / kTaSub;              // and the part of a row's accumulator it looks after
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bars[2 * S::kStages + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
-  __shared__ float s_m[128], s_l[2][128], s_mx[2][128];
+  __shared__ float s_m[128], s_l[kTaSub][128], s_mx[kTaSub][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
   const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, lowdone = pvdone0 + 16, qfull = lowdone + 8, drain = qfull + 8;
   volatile int* fail = &s_fail;
@@ -433,25 +450,33 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         mma_commit(pvdone0 + 8 * (j & 1));
         mma_commit(empty0 + 8 * s);
       };
-      auto loaded = [&](int k) { return bar_wait(full0 + 8 * (k % S::kStages), (k / S::kStages) & 1, fail, a.timeout_ns); };
+      auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
+      auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
+      // a tile's values and the keys that follow them, asked for ahead of the weights
+      auto loaded = [&](int j) {
+        const int v = ring_val(j, n), k = ring_key(min(j + 2, n - 1));
+        return bar_wait2(full(v), turn(v), full(k), turn(k), fail, a.timeout_ns);
+      };
       bool ok = bar_wait(qfull, 0, fail, a.timeout_ns);
       tm_fence_after();
       for (int j = 0; ok && j < min(n, 2); ++j)
-        if ((ok = loaded(ring_key(j)))) scores(j);
+        if ((ok = bar_wait(full(ring_key(j)), 0, fail, a.timeout_ns))) scores(j);
+      ok = ok && loaded(0);
       for (int j = 0; ok && j < n; ++j) {
-        ok = loaded(ring_val(j, n)) && bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+        ok = bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
         if (!ok) break;
         tm_fence_after();
         values(j);
         if (j + 2 < n) {
           // the scores of tile j have been taken (its weights are here); what replaces them has to wait
           // only for the weight term that stands over them, read first
-          ok = loaded(ring_key(j + 2)) && (!S::kLowOverS || bar_wait(lowdone, j & 1, fail, a.timeout_ns));
-          if (ok) {
+          if (S::kLowOverS) {
+            ok = bar_wait(lowdone, j & 1, fail, a.timeout_ns);
             tm_fence_after();
-            scores(j + 2);
           }
+          if (ok) scores(j + 2);
         }
+        if (j + 1 < n) ok = ok && loaded(j + 1);
       }
       mma_commit(drain);  // every MMA of this CTA done, before the memory is freed
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
@@ -460,20 +485,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, half = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
+    const int quarter = warp & 3, sub = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
     const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
     const int b = node_of(mt * kRows + r, a.inv_g);
     const bool live = r < rows;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    {  // the row's query terms into tensor memory, half of the dimensions each
-      constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a half row; half rows per load
+    {  // the row's query terms into tensor memory, kDims dimensions each
+      constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a part of a row; parts per load
       uint8_t* stage = ring + S::kQSlot * S::kSlot + warp * 32 * S::kQPitch;
       uint4 v[kVecs];
 #pragma unroll
-      for (int e = 0; e < kVecs; ++e) {  // whole rows at a time: 32 lanes read 512 contiguous bytes or a few pieces
+      for (int e = 0; e < kVecs; ++e) {
         const int ri = (quarter * 32 + e * kAtOnce + lane / kVecs) % kRows, ra = mt * kRows + ri;
         const int rb = node_of(ra, a.inv_g);
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + half * (D / 2);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + sub * kDims;
         v[e] = ri < rows ? reinterpret_cast<const uint4*>(q)[lane % kVecs] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
@@ -482,7 +507,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       __syncwarp();
       const uint4* own = reinterpret_cast<const uint4*>(stage + lane * S::kQPitch);
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 16) {
+      for (int c = 0; c < kDims; c += 16) {
         uint32_t w[S::kTermsQ][8];
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
         }
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (half * (D / 2) + c) / 2, w[t]);
+        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (sub * kDims + c) / 2, w[t]);
       }
       tm_st_wait();
       tm_fence_before();
@@ -515,17 +540,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // warps of rows past the last one only keep the barriers going (their lanes' weights are
     // whatever the columns hold, and reach no row that is read)
     const bool idle = r - lane >= rows;
-    const int c0 = part * (kTaKeys / DUP) + half * kCols;  // this thread's first key of a tile
-    const uint32_t ocol = tl + S::kColO + half * (D / 2);  // and its half of the accumulator
+    const int c0 = part * (kTaKeys / DUP) + sub * kCols;  // this thread's first key of a tile
+    const uint32_t ocol = tl + S::kColO + sub * kDims;
     const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
     float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units), this thread's weight sum
-    float acc[S::kFlush ? D / 2 : 1];
+    float acc[S::kFlush ? kDims : 1];
     if constexpr (S::kFlush > 0) {
 #pragma unroll
-      for (int e = 0; e < D / 2; ++e) acc[e] = 0.0f;
+      for (int e = 0; e < kDims; ++e) acc[e] = 0.0f;
     }
-    // After a wait that ran out a warp keeps walking the tiles, as the barrier with its other half
-    // needs it, and leaves the rest out.
+    // After a wait that ran out a warp keeps walking the tiles, as the barrier with the others of
+    // its quarter needs it, and leaves the rest out.
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint32_t buf = tl + S::kColS + (j & 1) * kTaKeys;
@@ -548,7 +573,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (bad) s_bad = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      ok = ok && bar_wait_warp(sfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+      if (ok) {
+        // the scores; and, with two buffers of weights, that this tile's has been read
+        const uint32_t sb = sfull0 + 8 * (j & 1), sp = (j >> 1) & 1;
+        ok = __all_sync(0xffffffffu, S::kPBufs == 2 && j >= 2 ? bar_wait2(sb, sp, pvdone0 + 8 * (j & 1), sp ^ 1u, fail, a.timeout_ns)
+                                                              : bar_wait(sb, sp, fail, a.timeout_ns));
+      }
       tm_fence_after();
       if (!idle) {
         float s[kCols];
@@ -579,15 +609,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         float pend = 1.0f;  // rescaling of what the next flush adds
         const bool flush = S::kFlush > 0 && j > 0 && j % (S::kFlush > 0 ? S::kFlush : 1) == 0;
         // the barrier also stands between the loads of the scores and the weights that replace them
-        if (pair_any(quarter, mx > m + kTaLazy)) {
-          s_mx[half][ln] = mx;
-          pair_sync(quarter);
-          const float mn = fmaxf(m, fmaxf(mx, s_mx[half ^ 1][ln])), corr = mn == m ? 1.0f : ex2(m - mn);
+        if (quarter_any(quarter, mx > m + kTaLazy)) {
+          s_mx[sub][ln] = mx;
+          quarter_sync(quarter);
+          float mn = m;
+#pragma unroll
+          for (int k = 0; k < kTaSub; ++k) mn = fmaxf(mn, s_mx[k][ln]);
+          const float corr = mn == m ? 1.0f : ex2(m - mn);
           if (flush) pend = corr;
           else if (j > 0 && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
             tm_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
+            for (int c = 0; c < kDims; c += 16) {
               float o[16];
               tm_load(ocol + c, o);
               uint32_t w[16];
@@ -599,7 +632,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
           if constexpr (S::kFlush > 0) {
 #pragma unroll
-            for (int e = 0; e < D / 2; ++e) acc[e] *= corr;
+            for (int e = 0; e < kDims; ++e) acc[e] *= corr;
           }
           l *= corr;
           m = mn;
@@ -620,31 +653,26 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
           l += ls.x + ls.y;
-          // the buffer's last weights must have been read
-          if (j >= S::kPBufs)
-            ok = bar_wait_warp(pvdone0 + 8 * ((j - S::kPBufs) & 1), ((j - S::kPBufs) >> 1) & 1, fail, a.timeout_ns);
-          tm_fence_after();
+          if (S::kPBufs == 1 && j >= 1) {  // the one buffer's last weights must have been read
+            ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns);
+            tm_fence_after();
+          }
 #pragma unroll
           for (int tt = 0; tt < S::kTermsP; ++tt) {
             const uint32_t at = S::kLowOverS && tt == S::kTermsP - 1 ? buf
                                                                      : tl + S::kColP + (j % S::kPBufs) * S::kPCols + tt * (kTaKeys / 2);
-            if constexpr (kCols >= 16) {
-#pragma unroll
-              for (int c = 0; c < kCols / 2; c += 8) tm_st8(at + c0 / 2 + c, w[tt] + c);
-            } else {
-              tm_st4(at + c0 / 2, w[tt]);
-            }
+            tm_store(at + c0 / 2, w[tt]);
             if constexpr (DUP > 1) {  // the keys that other lanes weigh
 #pragma unroll
               for (int c = 0; c < kTaKeys / 2; c += 8)
-                if (c / (kTaKeys / 2 / DUP) != part && (c / 8 & 1) == half) tm_st8(at + c, zero);
+                if (c / (kTaKeys / 2 / DUP) != part && (c / 8) % kTaSub == sub) tm_st8(at + c, zero);
             }
           }
           if constexpr (S::kFlush > 0) {
             if (flush && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
               tm_fence_after();
 #pragma unroll
-              for (int c = 0; c < D / 2; c += 16) {
+              for (int c = 0; c < kDims; c += 16) {
                 float o[16];
                 tm_load(ocol + c, o);
 #pragma unroll
@@ -662,9 +690,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
     tm_fence_after();
     if (ok) {
-      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + half * (D / 2);
+      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + sub * kDims;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 16) {
+      for (int c = 0; c < kDims; c += 16) {
         float o[16];
         tm_load(ocol + c, o);
         if constexpr (S::kFlush > 0) {
@@ -674,8 +702,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      if (half == 0) s_m[ln] = m;
-      s_l[half][ln] = l;
+      if (sub == 0) s_m[ln] = m;
+      s_l[sub][ln] = l;
     }
   }
   tm_fence_before();
