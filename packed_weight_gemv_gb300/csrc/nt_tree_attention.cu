@@ -14,10 +14,12 @@
 //
 // CTA (320 threads): one tile of rows, one key-value head, a range of 64-key tiles.
 //   warp 8 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
-//   warp 9         -- MMA issuer (one lane): weighted values of tile j, then scores of tile j + 2, while
-//   warps 0-7      -- (two threads per row = tensor-memory lane) turn the scores of tile j + 1 into
-//                     weights. The reference maximum m of a row is raised only when a score exceeds
-//                     it by 2^8, and the accumulator rescaled only then.
+//   warp 9         -- MMA issuer (one lane): scores of tile j + 2 and weighted values of tile j;
+//   warps 0-3, 4-7 -- two groups (thread = row = tensor-memory lane) that turn the scores of every
+//                     other tile into weights, one in its arithmetic while the other waits for a
+//                     tile. The reference maximum m of a row is raised only when a score exceeds it
+//                     by 2^8, and the accumulator rescaled only then; both groups add to one
+//                     accumulator, so they decide on m tile after tile, in turns.
 // Few rows are spread over the lanes: with R <= 32 (64) each row stands in four (two) lanes, each
 // of which weighs a quarter (half) of every tile's keys with a maximum and sum of its own and
 // leaves zeros elsewhere; their accumulators are joined at the end. So the instructions of the
@@ -46,8 +48,7 @@ namespace nt {
 namespace {
 
 constexpr int kTaKeys = 64;             // keys per tile
-constexpr int kTaSub = 2;               // threads per tensor-memory lane (row)
-constexpr int kTaSoftmax = 128 * kTaSub;
+constexpr int kTaSoftmax = 256;         // two groups of 128 threads = tensor-memory lanes (rows)
 constexpr int kTaProducer = kTaSoftmax / 32, kTaMma = kTaProducer + 1;
 constexpr int kTaThreads = kTaSoftmax + 64;
 constexpr int kTaTmemCols = 512;
@@ -75,7 +76,7 @@ struct TaShape {
   // The queries pass through the end of the ring on their way to tensor memory: per warp 32 rows of
   // half the dimensions, 16 bytes apart from a multiple of 128 so that a column of rows has no
   // bank conflicts.
-  static constexpr int kQRow = D / kTaSub * (int)sizeof(T), kQPitch = kQRow + 16;
+  static constexpr int kQRow = D / 2 * (int)sizeof(T), kQPitch = kQRow + 16;
   static constexpr int kQSlot = kStages - (kTaSoftmax * kQPitch + kSlot - 1) / kSlot;  // first ring slot they use
   // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
   // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
@@ -213,12 +214,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tm_ld8(uint32_t addr, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -227,15 +222,11 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
       : "r"(addr)
       : "memory");
 }
-// N columns (8, 16 or 32) of this lane; the values may be used only after the wait in it.
+// N columns (a multiple of 16) of this lane; the values may be used only after the wait in it.
 template <int N>
 __device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
-  if constexpr (N == 8) {
-    tm_ld8(addr, r);
-  } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
-  }
+  for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i += 8)
@@ -249,15 +240,8 @@ __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
 }
 template <int N>
 __device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t (&r)[N]) {
-  if constexpr (N >= 8) {
 #pragma unroll
-    for (int i = 0; i < N; i += 8) tm_st8(addr + i, r + i);
-  } else {
-    static_assert(N == 4, "columns");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3])
-                 : "memory");
-  }
+  for (int i = 0; i < N; i += 8) tm_st8(addr + i, r + i);
 }
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -273,18 +257,13 @@ __device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
 __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// Barrier of the warps that share a quarter of the lanes, and whether any lane of theirs says so.
-__device__ __forceinline__ void quarter_sync(int quarter) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + quarter), "n"(32 * kTaSub) : "memory");
+// Tiles are decided on in order, quarter of the lanes by quarter: the group that has decided on a
+// tile lets the other one, which has the next tile, go on.
+__device__ __forceinline__ void turn_wait(int quarter, int group) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + 2 * quarter + group) : "memory");
 }
-__device__ __forceinline__ bool quarter_any(int quarter, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.aligned.pred q, %1, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(1 + quarter), "r"((uint32_t)x), "n"(32 * kTaSub)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ void turn_pass(int quarter, int group) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(1 + 2 * quarter + (group ^ 1)) : "memory");
 }
 
 // Two fp32 operations in one instruction.
@@ -335,24 +314,26 @@ __device__ __forceinline__ bool word_bad(uint32_t w) {
 // Node of a row, row / G: exact for rows up to 2^20 (half a row is more than the product's error).
 __device__ __forceinline__ int node_of(int row, float inv_g) { return (int)(((float)row + 0.5f) * inv_g); }
 
-__device__ __forceinline__ int ring_key(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int ring_val(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+// Ring order of a CTA's n tiles: keys of tiles 0 and 1, then keys j + 2 and values j in turn.
+__device__ __forceinline__ int ring_key(int j) { return j < 2 ? j : 2 * j - 2; }
+__device__ __forceinline__ int ring_val(int j, int n) { return min(2 * j + 3, n + j); }
 
 template <typename T, int D, int DUP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
   using S = TaShape<T, D>;
-  constexpr int kRows = 128 / DUP;               // rows of a tile
-  constexpr int kCols = kTaKeys / DUP / kTaSub;  // keys of a tile that one thread weighs
-  constexpr int kDims = D / kTaSub;              // and the part of a row's accumulator it looks after
+  constexpr int kRows = 128 / DUP;      // rows of a tile
+  constexpr int kCols = kTaKeys / DUP;  // keys of a tile that one thread weighs
+  constexpr int kDims = D / 2;          // dimensions of a row that one thread looks after outside the tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 9];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 12];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
-  __shared__ float s_m[128], s_l[kTaSub][128], s_mx[kTaSub][128];
+  __shared__ float s_m[128], s_l[2][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
-  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, lowdone = pvdone0 + 16, qfull = lowdone + 8, drain = qfull + 8;
+  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16, lowdone = sfree0 + 16;
+  const uint32_t qfull = lowdone + 8, flushed = qfull + 8, drain = flushed + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
@@ -368,16 +349,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(sfull0 + 8 * b, 1);
-      bar_init(pfull0 + 8 * b, kTaSoftmax / 32);
+      bar_init(pfull0 + 8 * b, 4);  // the warps of the tile's group
+      bar_init(sfree0 + 8 * b, 4);
       bar_init(pvdone0 + 8 * b, 1);
     }
     bar_init(lowdone, 1);
     bar_init(qfull, kTaSoftmax / 32);
+    bar_init(flushed, 4);
     bar_init(drain, 1);
     s_fail = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (i < 128) s_m[i] = -INFINITY;
   if (warp == kTaMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                  "r"(kTaTmemCols)
@@ -400,8 +384,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         // The first tiles' keys and values, then the queries (which pass through the ring's end), then
         // the rest: with the whole ring asked for at once the queries arrived 4 us later.
         if (k == kTaFirst && !bar_wait(qfull, 0, fail, a.timeout_ns)) break;
-        const bool val = k == 2 * n - 1 || (k > 0 && !(k & 1));
-        const int t = t0 + (k == 2 * n - 1 ? n - 1 : k == 0 ? 0 : (k & 1) ? (k + 1) / 2 : k / 2 - 1);
+        const bool val = k >= min(2, n) && ((k & 1) || k > 2 * n - 4);
+        const int t = t0 + (!val ? (k < 2 ? k : k / 2 + 1) : k >= 2 * n - 3 ? k - n : (k - 3) / 2);
         const bool tree = t >= a.pre_tiles;
         const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
         const int y = (tree ? t - a.pre_tiles : t) * kTaKeys;
@@ -436,7 +420,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int k = ring_val(j, n), s = k % S::kStages;
         const uint32_t p = tmem + S::kColP + (j % S::kPBufs) * S::kPCols;
         const uint64_t bd = sdesc(smem_u32(ring + s * S::kSlot), kTaKeys * 128);
-        const bool fresh = S::kFlush ? j % S::kFlush == 0 : j == 0;
+        const bool fresh = S::kFlush ? j % (S::kFlush ? S::kFlush : 1) == 0 : j == 0;
 #pragma unroll
         for (int t = S::kTermsP - 1; t >= 0; --t) {
           const bool low = S::kLowOverS && t == S::kTermsP - 1;
@@ -452,31 +436,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       };
       auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
       auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
-      // a tile's values and the keys that follow them, asked for ahead of the weights
-      auto loaded = [&](int j) {
-        const int v = ring_val(j, n), k = ring_key(min(j + 2, n - 1));
-        return bar_wait2(full(v), turn(v), full(k), turn(k), fail, a.timeout_ns);
-      };
       bool ok = bar_wait(qfull, 0, fail, a.timeout_ns);
       tm_fence_after();
       for (int j = 0; ok && j < min(n, 2); ++j)
         if ((ok = bar_wait(full(ring_key(j)), 0, fail, a.timeout_ns))) scores(j);
-      ok = ok && loaded(0);
       for (int j = 0; ok && j < n; ++j) {
-        ok = bar_wait(pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+        const int v = ring_val(j, n), k = ring_key(j + 2);
+        if (!S::kLowOverS && j + 2 < n) {  // tile j's scores have been taken: the next ones of its group
+          ok = bar_wait2(full(k), turn(k), sfree0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+          if (!ok) break;
+          tm_fence_after();
+          scores(j + 2);
+        }
+        ok = bar_wait2(full(v), turn(v), pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+        if (S::kFlush && j > 0 && j % (S::kFlush ? S::kFlush : 1) == 0)  // the other group's part of the sum so far has been taken
+          ok = ok && bar_wait(flushed, (j / (S::kFlush ? S::kFlush : 1) - 1) & 1, fail, a.timeout_ns);
         if (!ok) break;
         tm_fence_after();
         values(j);
-        if (j + 2 < n) {
-          // the scores of tile j have been taken (its weights are here); what replaces them has to wait
-          // only for the weight term that stands over them, read first
-          if (S::kLowOverS) {
-            ok = bar_wait(lowdone, j & 1, fail, a.timeout_ns);
-            tm_fence_after();
-          }
-          if (ok) scores(j + 2);
+        if (S::kLowOverS && j + 2 < n) {  // the weight term that stands over tile j's scores, read first, is through
+          ok = bar_wait2(full(k), turn(k), lowdone, j & 1, fail, a.timeout_ns);
+          if (!ok) break;
+          tm_fence_after();
+          scores(j + 2);
         }
-        if (j + 1 < n) ok = ok && loaded(j + 1);
       }
       mma_commit(drain);  // every MMA of this CTA done, before the memory is freed
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
@@ -485,7 +468,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, sub = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
+    const int quarter = warp & 3, group = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
     const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
     const int b = node_of(mt * kRows + r, a.inv_g);
     const bool live = r < rows;
@@ -498,7 +481,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int e = 0; e < kVecs; ++e) {
         const int ri = (quarter * 32 + e * kAtOnce + lane / kVecs) % kRows, ra = mt * kRows + ri;
         const int rb = node_of(ra, a.inv_g);
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + sub * kDims;
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + group * kDims;
         v[e] = ri < rows ? reinterpret_cast<const uint4*>(q)[lane % kVecs] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
@@ -530,7 +513,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
         }
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (sub * kDims + c) / 2, w[t]);
+        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
       }
       tm_st_wait();
       tm_fence_before();
@@ -540,28 +523,78 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // warps of rows past the last one only keep the barriers going (their lanes' weights are
     // whatever the columns hold, and reach no row that is read)
     const bool idle = r - lane >= rows;
-    const int c0 = part * (kTaKeys / DUP) + sub * kCols;  // this thread's first key of a tile
-    const uint32_t ocol = tl + S::kColO + sub * kDims;
+    const int c0 = part * kCols;  // this thread's first key of a tile
+    const uint32_t ocol = tl + S::kColO + group * kDims;  // its half of the accumulator
     const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units), this thread's weight sum
+    float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units) as this group knows it, its weight sum
+    constexpr int kF = S::kFlush ? S::kFlush : 1;
     float acc[S::kFlush ? kDims : 1];
     if constexpr (S::kFlush > 0) {
 #pragma unroll
       for (int e = 0; e < kDims; ++e) acc[e] = 0.0f;
     }
-    // After a wait that ran out a warp keeps walking the tiles, as the barrier with the others of
-    // its quarter needs it, and leaves the rest out.
+    // After a wait that ran out a warp keeps walking the tiles, as the other group's turns need it,
+    // and leaves the rest out.
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t buf = tl + S::kColS + (j & 1) * kTaKeys;
+    auto done = [&](int j) {  // tile j's products have been added
+      ok = ok && bar_wait_warp(pvdone0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+      tm_fence_after();
+    };
+    auto rescale = [&](float to) {  // what this thread holds, to another reference
+      const float corr = m == to ? 1.0f : ex2(m - to);
+      l *= corr;
+      if constexpr (S::kFlush > 0) {
+#pragma unroll
+        for (int e = 0; e < kDims; ++e) acc[e] *= corr;
+      }
+      m = to;
+      return corr;
+    };
+    auto flush = [&](int j, float corr) {  // the accumulator before tile j, times corr, into registers
+      done(j - 1);
+      if (ok && !idle) {
+        if constexpr (S::kFlush > 0) {
+#pragma unroll
+          for (int c = 0; c < kDims; c += 16) {
+            float o[16];
+            tm_load(ocol + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], corr, acc[c + e]);
+          }
+        }
+      }
+    };
+    auto weights = [&](int j, int term) {  // columns of a term of tile j's weights
+      return S::kLowOverS && term == S::kTermsP - 1 ? tl + S::kColS + (j & 1) * kTaKeys
+                                                    : tl + S::kColP + (j % S::kPBufs) * S::kPCols + term * (kTaKeys / 2);
+    };
+    for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
-      if (tree && ok) {  // take tree values that are not finite out of the product
-        const int k = ring_val(j, n), s = k % S::kStages;
-        ok = bar_wait_warp(full0 + 8 * s, (k / S::kStages) & 1, fail, a.timeout_ns);
+      if (ok) {
+        // the scores; and, with two buffers of weights, that this group's last ones have been read
+        const uint32_t sb = sfull0 + 8 * group, sp = (j >> 1) & 1;
+        ok = __all_sync(0xffffffffu, S::kPBufs == 2 && j >= 2 ? bar_wait2(sb, sp, pvdone0 + 8 * group, sp ^ 1u, fail, a.timeout_ns)
+                                                              : bar_wait(sb, sp, fail, a.timeout_ns));
+      }
+      tm_fence_after();
+      float s[kCols];
+      if (ok && !idle) {
+        tm_load(tl + S::kColS + group * kTaKeys + c0, s);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
+      }
+      if (!S::kLowOverS) {
+        tm_fence_before();
+        if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
+      }
+      if (tree) {  // take tree values that are not finite out of the product
+        const int k = ring_val(j, n), slot = k % S::kStages;
+        ok = ok && bar_wait_warp(full0 + 8 * slot, (k / S::kStages) & 1, fail, a.timeout_ns);
         bool bad = false;
-        for (int e = i; ok && e < S::kSlot / 16; e += kTaSoftmax) {
-          uint4* p = reinterpret_cast<uint4*>(ring + s * S::kSlot) + e;
+        for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
+          uint4* p = reinterpret_cast<uint4*>(ring + slot * S::kSlot) + e;
           const uint4 v = *p;
           if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
             uint16_t* h = reinterpret_cast<uint16_t*>(p);
@@ -573,78 +606,67 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (bad) s_bad = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      if (ok) {
-        // the scores; and, with two buffers of weights, that this tile's has been read
-        const uint32_t sb = sfull0 + 8 * (j & 1), sp = (j >> 1) & 1;
-        ok = __all_sync(0xffffffffu, S::kPBufs == 2 && j >= 2 ? bar_wait2(sb, sp, pvdone0 + 8 * (j & 1), sp ^ 1u, fail, a.timeout_ns)
-                                                              : bar_wait(sb, sp, fail, a.timeout_ns));
+      const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
+      if (tree || left < kTaKeys) {
+        uint64_t seen = ~0ull;
+        if (tree) {
+          const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
+          seen = w[0];
+          if (left > 32) seen |= (uint64_t)w[1] << 32;
+        }
+        if (left < kTaKeys) seen &= (1ull << left) - 1;
+        if (!live) seen = 0;
+        seen >>= c0;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (!(seen >> c & 1)) s[c] = -INFINITY;
       }
-      tm_fence_after();
+      float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kCols; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+      if (S::kFlush > 0 && group == 1 && j > 1 && (j - 1) % kF == 0) {  // the other group's tile starts afresh
+        flush(j - 1, 1.0f);
+        tm_fence_before();
+        if (ok) bar_arrive_warp(flushed, lane);
+      }
+      // this tile's reference, after the one of the tile before it
+      const bool restart = S::kFlush > 0 && group == 0 && j > 0 && j % kF == 0;
+      float pend = 1.0f;  // rescaling of what this group's flush adds
+      if (j > 0) turn_wait(quarter, group);
       if (!idle) {
-        float s[kCols];
-        if (ok) tm_load(buf + c0, s);
-        else {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
-        }
-        const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
-        if (tree || left < kTaKeys) {
-          uint64_t seen = ~0ull;
-          if (tree) {
-            const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
-            seen = w[0];
-            if (left > 32) seen |= (uint64_t)w[1] << 32;
-          }
-          if (left < kTaKeys) seen &= (1ull << left) - 1;
-          if (!live) seen = 0;
-          seen >>= c0;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (!(seen >> c & 1)) s[c] = -INFINITY;
-        }
-        float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < kCols; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-        float pend = 1.0f;  // rescaling of what the next flush adds
-        const bool flush = S::kFlush > 0 && j > 0 && j % (S::kFlush > 0 ? S::kFlush : 1) == 0;
-        // the barrier also stands between the loads of the scores and the weights that replace them
-        if (quarter_any(quarter, mx > m + kTaLazy)) {
-          s_mx[sub][ln] = mx;
-          quarter_sync(quarter);
-          float mn = m;
-#pragma unroll
-          for (int k = 0; k < kTaSub; ++k) mn = fmaxf(mn, s_mx[k][ln]);
-          const float corr = mn == m ? 1.0f : ex2(m - mn);
-          if (flush) pend = corr;
-          else if (j > 0 && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
-            tm_fence_after();
+        const float known = s_m[ln];
+        if (__any_sync(0xffffffffu, known != m)) rescale(known);
+        if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+          const float corr = rescale(fmaxf(m, mx));
+          s_m[ln] = m;
+          if (restart) {
+            pend = corr;
+          } else if (j > 0) {
+            done(j - 1);
 #pragma unroll 1
-            for (int c = 0; c < kDims; c += 16) {
+            for (int c = 0; ok && c < D; c += 16) {
               float o[16];
-              tm_load(ocol + c, o);
+              tm_load(tl + S::kColO + c, o);
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
-              tm_st8(ocol + c, w);
-              tm_st8(ocol + c + 8, w + 8);
+              tm_store(tl + S::kColO + c, w);
             }
           }
-          if constexpr (S::kFlush > 0) {
-#pragma unroll
-            for (int e = 0; e < kDims; ++e) acc[e] *= corr;
-          }
-          l *= corr;
-          m = mn;
         }
-        if (ok) {
-          const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
-          float2 ls = make_float2(0.0f, 0.0f);
-          const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
-          uint32_t w[S::kTermsP][kCols / 2];
+      }
+      if (j + 1 < n) turn_pass(quarter, group);
+      if (!idle && ok) {
+        const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+        float2 ls = make_float2(0.0f, 0.0f);
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            const float2 x = fma2(make_float2(s[c], s[c + 1]), sc, mm);
+        for (int ch = 0; ch < kCols; ch += 16) {  // 16 keys at a time, for the registers' sake
+          uint32_t w[S::kTermsP][8];
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float2 x = fma2(make_float2(s[ch + c], s[ch + c + 1]), sc, mm);
             const float2 pp = make_float2(ex2(x.x), ex2(x.y));
             ls = add2(ls, pp);
             uint32_t term[S::kTermsP];
@@ -652,45 +674,36 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
             for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
-          l += ls.x + ls.y;
-          if (S::kPBufs == 1 && j >= 1) {  // the one buffer's last weights must have been read
-            ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns);
-            tm_fence_after();
-          }
+          if (S::kPBufs == 1 && ch == 0 && j > 0) done(j - 1);  // the one buffer's last weights must have been read
 #pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt) {
-            const uint32_t at = S::kLowOverS && tt == S::kTermsP - 1 ? buf
-                                                                     : tl + S::kColP + (j % S::kPBufs) * S::kPCols + tt * (kTaKeys / 2);
-            tm_store(at + c0 / 2, w[tt]);
-            if constexpr (DUP > 1) {  // the keys that other lanes weigh
+          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(weights(j, tt) + (c0 + ch) / 2, w[tt]);
+        }
+        l += ls.x + ls.y;
+        if constexpr (DUP > 1) {  // the keys that other lanes weigh
 #pragma unroll
-              for (int c = 0; c < kTaKeys / 2; c += 8)
-                if (c / (kTaKeys / 2 / DUP) != part && (c / 8) % kTaSub == sub) tm_st8(at + c, zero);
-            }
-          }
-          if constexpr (S::kFlush > 0) {
-            if (flush && ok && (ok = bar_wait_warp(pvdone0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns))) {
-              tm_fence_after();
+          for (int tt = 0; tt < S::kTermsP; ++tt)
 #pragma unroll
-              for (int c = 0; c < kDims; c += 16) {
-                float o[16];
-                tm_load(ocol + c, o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], pend, acc[c + e]);
-              }
-            }
-          }
-          tm_st_wait();
+            for (int c = 0; c < kTaKeys / 2; c += 8)
+              if (c / (kCols / 2) != part) tm_store(weights(j, tt) + c, zero);
         }
       }
+      if (restart) flush(j, pend);
+      tm_st_wait();
       tm_fence_before();
-      if (ok) bar_arrive_warp(pfull0 + 8 * (j & 1), lane);
+      if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
+    }
+    if (S::kFlush > 0 && group == 1 && n > 1 && (n - 1) % kF == 0) {  // the last tile is the other group's, and starts afresh
+      flush(n - 1, 1.0f);
+      tm_fence_before();
+      if (ok) bar_arrive_warp(flushed, lane);
     }
     // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
     ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
     tm_fence_after();
+    asm volatile("bar.sync 9, 256;" ::: "memory");  // both groups' last word on the references
     if (ok) {
-      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + sub * kDims;
+      rescale(s_m[ln]);
+      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + group * kDims;
 #pragma unroll
       for (int c = 0; c < kDims; c += 16) {
         float o[16];
@@ -702,8 +715,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      if (sub == 0) s_m[ln] = m;
-      s_l[sub][ln] = l;
+      s_l[group][ln] = l;
     }
   }
   tm_fence_before();
