@@ -12,10 +12,11 @@
 // cut from the fp32 weight without loss (fp32 queries) or two rounded ones (bf16 queries: 2^-17,
 // small next to the output's 2^-9). Scores, weights, sums and the output accumulate in fp32.
 //
-// CTA (320 threads): one tile of rows, one key-value head, a range of 64-key tiles.
-//   warp 8 lane 0  -- producer: 64-row TMA boxes of keys and values (128-byte swizzle) into a ring;
-//   warp 9         -- MMA issuer (one lane): scores of tile j + 2 and weighted values of tile j;
-//   warps 0-3, 4-7 -- two groups (thread = row = tensor-memory lane) that turn the scores of every
+// CTA (384 threads): one tile of rows, one key-value head, a range of 64-key tiles.
+//   warps 0, 3     -- (one lane each) 64-row TMA boxes of keys, of values (128-byte swizzle) into a ring;
+//   warps 1, 2     -- (one lane each) the scores' MMAs, the weighted values'. One issuer for both spent
+//                     its time in waits of 100 to 300 cycles, one behind the other;
+//   warps 4-7, 8-11 - two groups (thread = row = tensor-memory lane) that turn the scores of every
 //                     other tile into weights, one in its arithmetic while the other waits for a
 //                     tile. The reference maximum m of a row is raised only when a score exceeds it
 //                     by 2^8, and the accumulator rescaled only then; both groups add to one
@@ -48,9 +49,10 @@ namespace nt {
 namespace {
 
 constexpr int kTaKeys = 64;             // keys per tile
+// Warps: the issuers come first, as the scheduler prefers older warps and each of them holds up all others.
+constexpr int kTaKeyLoad = 0, kTaScore = 1, kTaValue = 2, kTaValueLoad = 3, kTaFirstSoftmax = 4;
 constexpr int kTaSoftmax = 256;         // two groups of 128 threads = tensor-memory lanes (rows)
-constexpr int kTaProducer = kTaSoftmax / 32, kTaMma = kTaProducer + 1;
-constexpr int kTaThreads = kTaSoftmax + 64;
+constexpr int kTaThreads = 32 * kTaFirstSoftmax + kTaSoftmax;
 constexpr int kTaTmemCols = 512;
 constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
 constexpr int kTaFirst = 3;             // ring slots filled before the queries have arrived
@@ -151,21 +153,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ void bar_arrive_warp(uint32_t bar, int lane) {
   __syncwarp();
   if (lane == 0) bar_arrive(bar);
-}
-// Two barriers tested together: a test takes 110 cycles, of which the two share most.
-__device__ __forceinline__ bool bar_try2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool bar_wait2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, volatile int* fail,
-                                          uint64_t timeout_ns) {
-  return bar_try2(b0, p0, b1, p1) || (bar_wait_slow(b0, p0, fail, timeout_ns) && bar_wait_slow(b1, p1, fail, timeout_ns));
 }
 // The same for a whole warp: every lane gets one answer, so the warp stays together.
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
@@ -327,13 +314,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   constexpr int kDims = D / 2;          // dimensions of a row that one thread looks after outside the tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 12];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 13];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
   __shared__ float s_m[128], s_l[2][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
-  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16, lowdone = sfree0 + 16;
-  const uint32_t qfull = lowdone + 8, flushed = qfull + 8, drain = flushed + 8;
+  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16, lowdone0 = sfree0 + 16;
+  const uint32_t qfull = lowdone0 + 16, flushed = qfull + 8, drain = flushed + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
@@ -351,18 +338,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       bar_init(sfull0 + 8 * b, 1);
       bar_init(pfull0 + 8 * b, 4);  // the warps of the tile's group
       bar_init(sfree0 + 8 * b, 4);
+      bar_init(lowdone0 + 8 * b, 1);
       bar_init(pvdone0 + 8 * b, 1);
     }
-    bar_init(lowdone, 1);
     bar_init(qfull, kTaSoftmax / 32);
     bar_init(flushed, 4);
-    bar_init(drain, 1);
+    bar_init(drain, 2);
     s_fail = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (i < 128) s_m[i] = -INFINITY;
-  if (warp == kTaMma) {
+  if (warp == kTaScore) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                  "r"(kTaTmemCols)
                  : "memory");
@@ -375,37 +362,53 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   // The set-up above overlaps the previous kernel; nothing below reads an input before its end.
   dependent_launch_wait();
 
-  if (warp == kTaProducer) {
-    if (lane == 0) {
-      int k = 0;
-      for (; k < 2 * n && !a.fault; ++k) {
-        const int s = k % S::kStages;
-        if (k >= S::kStages && !bar_wait(empty0 + 8 * s, ((k / S::kStages) - 1) & 1, fail, a.timeout_ns)) break;
+  auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
+  auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
+  auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
+  auto slot = [&](int k) { return smem_u32(ring + (k % S::kStages) * S::kSlot); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+
+  if (warp == kTaKeyLoad || warp == kTaValueLoad) {
+    if (elect_one()) {
+      const bool val = warp == kTaValueLoad;
+      int j = 0;
+      for (; j < n && !a.fault; ++j) {
+        const int k = val ? ring_val(j, n) : ring_key(j);
+        if (k >= S::kStages && !wait(empty(k), turn(k) ^ 1u)) break;
         // The first tiles' keys and values, then the queries (which pass through the ring's end), then
         // the rest: with the whole ring asked for at once the queries arrived 4 us later.
-        if (k == kTaFirst && !bar_wait(qfull, 0, fail, a.timeout_ns)) break;
-        const bool val = k >= min(2, n) && ((k & 1) || k > 2 * n - 4);
-        const int t = t0 + (!val ? (k < 2 ? k : k / 2 + 1) : k >= 2 * n - 3 ? k - n : (k - 3) / 2);
+        if (k >= kTaFirst && !wait(qfull, 0)) break;
+        const int t = t0 + j;
         const bool tree = t >= a.pre_tiles;
         const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
         const int y = (tree ? t - a.pre_tiles : t) * kTaKeys;
-        const uint32_t dst = smem_u32(ring + s * S::kSlot);
-        bar_expect_tx(full0 + 8 * s, S::kSlot);
+        bar_expect_tx(full(k), S::kSlot);
 #pragma unroll
-        for (int x = 0; x < D; x += 64) tma_3d(dst + x * kTaKeys * 2, map, x, y, g, full0 + 8 * s);
+        for (int x = 0; x < D; x += 64) tma_3d(slot(k) + x * kTaKeys * 2, map, x, y, g, full(k));
       }
       // every copy must land before the CTA may exit
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-      for (int j = max(0, k - S::kStages); j < k; ++j)
-        while (!bar_try(full0 + 8 * (j % S::kStages), (j / S::kStages) & 1))
+      for (int d = max(0, j - S::kStages); d < j; ++d) {
+        const int k = val ? ring_val(d, n) : ring_key(d);
+        if (k + S::kStages < 2 * n && *fail == 0) continue;  // its slot has been filled again since
+        while (!bar_try(full(k), turn(k)))
           if (globaltimer_ns() > deadline) break;
+      }
     }
-  } else if (warp == kTaMma) {
+    __syncwarp();
+  } else if (warp == kTaScore) {
     if (elect_one()) {
-      auto scores = [&](int j) {
-        const int k = ring_key(j), s = k % S::kStages;
+      bool ok = wait(qfull, 0);
+      tm_fence_after();
+      for (int j = 0; ok && j < n; ++j) {
+        const int k = ring_key(j);
+        ok = wait(full(k), turn(k));
+        if (ok && j >= 2)  // the scores of this group's last tile have been taken, and no weight term stands over them
+          ok = wait((S::kLowOverS ? lowdone0 : sfree0) + 8 * (j & 1), ((j >> 1) - 1) & 1);
+        if (!ok) break;
+        tm_fence_after();
         const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
-        const uint64_t bd = sdesc(smem_u32(ring + s * S::kSlot), 16);
+        const uint64_t bd = sdesc(slot(k), 16);
         // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
         for (int t = S::kTermsQ - 1; t >= 0; --t)
@@ -414,13 +417,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16,
                        idesc_bf16(kTaKeys, false), t < S::kTermsQ - 1 || kk > 0);
         mma_commit(sfull0 + 8 * (j & 1));
-        mma_commit(empty0 + 8 * s);
-      };
-      auto values = [&](int j) {
-        const int k = ring_val(j, n), s = k % S::kStages;
+        mma_commit(empty(k));
+      }
+      mma_commit(drain);
+    }
+    __syncwarp();
+  } else if (warp == kTaValue) {
+    if (elect_one()) {
+      for (int j = 0; j < n; ++j) {
+        const int k = ring_val(j, n);
+        constexpr int kF = S::kFlush ? S::kFlush : 1;
+        const bool fresh = S::kFlush ? j % kF == 0 : j == 0;
+        bool ok = wait(full(k), turn(k));
+        if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
+        if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
+        tm_fence_after();
         const uint32_t p = tmem + S::kColP + (j % S::kPBufs) * S::kPCols;
-        const uint64_t bd = sdesc(smem_u32(ring + s * S::kSlot), kTaKeys * 128);
-        const bool fresh = S::kFlush ? j % (S::kFlush ? S::kFlush : 1) == 0 : j == 0;
+        const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
 #pragma unroll
         for (int t = S::kTermsP - 1; t >= 0; --t) {
           const bool low = S::kLowOverS && t == S::kTermsP - 1;
@@ -429,53 +442,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
             mma_tmem_a(tmem + S::kColO, pt + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
                        t < S::kTermsP - 1 || kk > 0 || !fresh);
-          if (low) mma_commit(lowdone);
+          if (low) mma_commit(lowdone0 + 8 * (j & 1));
         }
         mma_commit(pvdone0 + 8 * (j & 1));
-        mma_commit(empty0 + 8 * s);
-      };
-      auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
-      auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
-      bool ok = bar_wait(qfull, 0, fail, a.timeout_ns);
-      tm_fence_after();
-      for (int j = 0; ok && j < min(n, 2); ++j)
-        if ((ok = bar_wait(full(ring_key(j)), 0, fail, a.timeout_ns))) scores(j);
-      for (int j = 0; ok && j < n; ++j) {
-        const int v = ring_val(j, n), k = ring_key(j + 2);
-        if (!S::kLowOverS && j + 2 < n) {  // tile j's scores have been taken: the next ones of its group
-          ok = bar_wait2(full(k), turn(k), sfree0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
-          if (!ok) break;
-          tm_fence_after();
-          scores(j + 2);
-        }
-        ok = bar_wait2(full(v), turn(v), pfull0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
-        if (S::kFlush && j > 0 && j % (S::kFlush ? S::kFlush : 1) == 0)  // the other group's part of the sum so far has been taken
-          ok = ok && bar_wait(flushed, (j / (S::kFlush ? S::kFlush : 1) - 1) & 1, fail, a.timeout_ns);
-        if (!ok) break;
-        tm_fence_after();
-        values(j);
-        if (S::kLowOverS && j + 2 < n) {  // the weight term that stands over tile j's scores, read first, is through
-          ok = bar_wait2(full(k), turn(k), lowdone, j & 1, fail, a.timeout_ns);
-          if (!ok) break;
-          tm_fence_after();
-          scores(j + 2);
-        }
+        mma_commit(empty(k));
       }
-      mma_commit(drain);  // every MMA of this CTA done, before the memory is freed
-      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-      while (!bar_try(drain, 0))
-        if (globaltimer_ns() > deadline) break;
+      mma_commit(drain);
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, group = warp >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
+    const int quarter = warp & 3, group = (warp - kTaFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
     const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
     const int b = node_of(mt * kRows + r, a.inv_g);
     const bool live = r < rows;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     {  // the row's query terms into tensor memory, kDims dimensions each
       constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a part of a row; parts per load
-      uint8_t* stage = ring + S::kQSlot * S::kSlot + warp * 32 * S::kQPitch;
+      uint8_t* stage = ring + S::kQSlot * S::kSlot + (warp - kTaFirstSoftmax) * 32 * S::kQPitch;
       uint4 v[kVecs];
 #pragma unroll
       for (int e = 0; e < kVecs; ++e) {
@@ -571,12 +554,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
-      if (ok) {
-        // the scores; and, with two buffers of weights, that this group's last ones have been read
-        const uint32_t sb = sfull0 + 8 * group, sp = (j >> 1) & 1;
-        ok = __all_sync(0xffffffffu, S::kPBufs == 2 && j >= 2 ? bar_wait2(sb, sp, pvdone0 + 8 * group, sp ^ 1u, fail, a.timeout_ns)
-                                                              : bar_wait(sb, sp, fail, a.timeout_ns));
-      }
+      if (S::kPBufs == 2 && j >= 2) done(j - 2);  // this group's last weights have been read
+      ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
       tm_fence_after();
       float s[kCols];
       if (ok && !idle) {
@@ -590,11 +569,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
       }
       if (tree) {  // take tree values that are not finite out of the product
-        const int k = ring_val(j, n), slot = k % S::kStages;
-        ok = ok && bar_wait_warp(full0 + 8 * slot, (k / S::kStages) & 1, fail, a.timeout_ns);
+        const int k = ring_val(j, n);
+        ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
         bool bad = false;
         for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
-          uint4* p = reinterpret_cast<uint4*>(ring + slot * S::kSlot) + e;
+          uint4* p = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
           const uint4 v = *p;
           if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
             uint16_t* h = reinterpret_cast<uint16_t*>(p);
@@ -720,7 +699,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   }
   tm_fence_before();
   __syncthreads();
-  if (warp == kTaMma)
+  if (warp == kTaScore)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
   if (*fail) {
     if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
