@@ -554,7 +554,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
-      if (S::kPBufs == 2 && j >= 2) done(j - 2);  // this group's last weights have been read
       ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
       tm_fence_after();
       float s[kCols];
@@ -653,7 +652,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
             for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
-          if (S::kPBufs == 1 && ch == 0 && j > 0) done(j - 1);  // the one buffer's last weights must have been read
+          if (ch == 0 && j >= S::kPBufs) done(j - S::kPBufs);  // the buffer's last weights must have been read
 #pragma unroll
           for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(weights(j, tt) + (c0 + ch) / 2, w[tt]);
         }
