@@ -65,16 +65,20 @@ struct TaShape {
   static constexpr int kTermsQ = sizeof(T) == 4 ? 3 : 1;
   static constexpr int kTermsP = sizeof(T) == 4 ? 3 : 2;
   static constexpr int kSlot = kTaKeys * D * 2;            // bytes of a ring slot: one tile's keys or values
-  // The whole ring is 192 KB for either D: a second CTA on an SM would only wait for the first one's
-  // tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
-  static constexpr int kStages = 192 * 1024 / kSlot;
-  // Tensor-memory columns: the accumulator, the query terms, two score buffers and the weights.
-  // Where two buffers of all weight terms do not fit beside them (fp32 queries, D = 128), the
-  // smallest term goes over the scores it came from and one buffer holds the others.
-  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQ * D / 2, kColP = kColS + 2 * kTaKeys;
-  static constexpr bool kLowOverS = kColP + 2 * kTermsP * (kTaKeys / 2) > kTaTmemCols;
-  static constexpr int kPBufs = kLowOverS ? 1 : 2;
-  static constexpr int kPCols = (kTermsP - (kLowOverS ? 1 : 0)) * (kTaKeys / 2);
+  // Tensor-memory columns: the accumulator, query terms, a buffer of scores per group and the weights.
+  // Where the weights would not fit beside all query terms (fp32 queries, D = 128), the smallest
+  // query term is a shared-memory operand (51 cycles per MMA instead of 32) and the groups share one
+  // buffer of weights.
+  static constexpr bool kLowInSmem = D + kTermsQ * D / 2 + 2 * kTaKeys + kTermsP * (kTaKeys / 2) > kTaTmemCols;
+  static constexpr int kTermsQT = kTermsQ - (kLowInSmem ? 1 : 0);  // query terms in tensor memory
+  static constexpr int kPCols = kTermsP * (kTaKeys / 2);
+  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + 2 * kTaKeys;
+  static constexpr int kPBufs = kColP + 2 * kPCols <= kTaTmemCols ? 2 : 1;
+  static constexpr int kLowBytes = kLowInSmem ? 128 * D * 2 : 0;
+  // Ring and query term take 192 KB for either D: a second CTA on an SM would only wait for the first
+  // one's tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
+  static constexpr int kStages = (192 * 1024 - kLowBytes) / kSlot;
+  static_assert(kStages % 2 == 0, "keys keep to even slots, values to odd ones but for the ends");
   // The queries pass through the end of the ring on their way to tensor memory: per warp 32 rows of
   // half the dimensions, 16 bytes apart from a multiple of 128 so that a column of rows has no
   // bank conflicts.
@@ -83,9 +87,9 @@ struct TaShape {
   // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
   // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
   // started afresh every kFlush tiles; next to a bf16 output the loss does not count.
-  static constexpr int kFlush = sizeof(T) == 4 ? 4 : 0;
+  static constexpr int kFlush = sizeof(T) == 4 ? 8 : 0;
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
-  static constexpr int kSmem = kStages * kSlot + 1024;   // and alignment
+  static constexpr int kSmem = kStages * kSlot + kLowBytes + 1024;  // and alignment
   static_assert(kQSlot >= kTaFirst, "the queries' staging slots are filled after them");
   static_assert(kColP + kPBufs * kPCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
@@ -195,30 +199,49 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
 }
+__device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+// Columns of this lane. The wait stands in the same statement as the load: registers of a load on
+// its way must not be moved or spilled.
 __device__ __forceinline__ void tm_ld16(uint32_t addr, float* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16]; tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(addr)
       : "memory");
 }
-// N columns (a multiple of 16) of this lane; the values may be used only after the wait in it.
+__device__ __forceinline__ void tm_ld32(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32]; tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
 template <int N>
 __device__ __forceinline__ void tm_load(uint32_t addr, float (&r)[N]) {
+  if constexpr (N == 16) {
+    tm_ld16(addr, r);
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; i += 16) tm_ld16(addr + i, r + i);
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    asm volatile("" : "+f"(r[i]), "+f"(r[i + 1]), "+f"(r[i + 2]), "+f"(r[i + 3]), "+f"(r[i + 4]), "+f"(r[i + 5]),
-                 "+f"(r[i + 6]), "+f"(r[i + 7])::"memory");
+    for (int i = 0; i < N; i += 32) tm_ld32(addr + i, r + i);
+  }
 }
 __device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
@@ -314,13 +337,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   constexpr int kDims = D / 2;          // dimensions of a row that one thread looks after outside the tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 13];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 11];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
   __shared__ float s_m[128], s_l[2][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
-  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16, lowdone0 = sfree0 + 16;
-  const uint32_t qfull = lowdone0 + 16, flushed = qfull + 8, drain = flushed + 8;
+  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16;
+  const uint32_t qfull = sfree0 + 16, flushed = qfull + 8, drain = flushed + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
@@ -338,7 +361,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       bar_init(sfull0 + 8 * b, 1);
       bar_init(pfull0 + 8 * b, 4);  // the warps of the tile's group
       bar_init(sfree0 + 8 * b, 4);
-      bar_init(lowdone0 + 8 * b, 1);
       bar_init(pvdone0 + 8 * b, 1);
     }
     bar_init(qfull, kTaSoftmax / 32);
@@ -403,8 +425,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const int k = ring_key(j);
         ok = wait(full(k), turn(k));
-        if (ok && j >= 2)  // the scores of this group's last tile have been taken, and no weight term stands over them
-          ok = wait((S::kLowOverS ? lowdone0 : sfree0) + 8 * (j & 1), ((j >> 1) - 1) & 1);
+        if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
         if (!ok) break;
         tm_fence_after();
         const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
@@ -413,9 +434,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
         for (int t = S::kTermsQ - 1; t >= 0; --t)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16,
-                       idesc_bf16(kTaKeys, false), t < S::kTermsQ - 1 || kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b = bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16;
+            const uint32_t more = t < S::kTermsQ - 1 || kk > 0;
+            if (t < S::kTermsQT)
+              mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, b, idesc_bf16(kTaKeys, false), more);
+            else
+              mma_smem_a(d, sdesc(smem_u32(ring + S::kStages * S::kSlot), 16) + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, b,
+                         idesc_bf16(kTaKeys, false), more);
+          }
         mma_commit(sfull0 + 8 * (j & 1));
         mma_commit(empty(k));
       }
@@ -435,15 +462,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const uint32_t p = tmem + S::kColP + (j % S::kPBufs) * S::kPCols;
         const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
 #pragma unroll
-        for (int t = S::kTermsP - 1; t >= 0; --t) {
-          const bool low = S::kLowOverS && t == S::kTermsP - 1;
-          const uint32_t pt = low ? tmem + S::kColS + (j & 1) * kTaKeys : p + t * (kTaKeys / 2);
+        for (int t = S::kTermsP - 1; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, pt + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
+            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
                        t < S::kTermsP - 1 || kk > 0 || !fresh);
-          if (low) mma_commit(lowdone0 + 8 * (j & 1));
-        }
         mma_commit(pvdone0 + 8 * (j & 1));
         mma_commit(empty(k));
       }
@@ -496,11 +519,18 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
         }
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
+        for (int t = 0; t < S::kTermsQT; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
+        if constexpr (S::kLowInSmem) {  // rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
+          uint8_t* low = ring + S::kStages * S::kSlot + group * (128 * 128) + ln * 128;
+          const uint32_t* x = w[S::kTermsQ - 1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint4*>(low + (((c / 8 + e) ^ (ln & 7)) * 16)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        }
       }
       tm_st_wait();
       tm_fence_before();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies into the staging slots come after
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before MMAs that read it, copies over the staging slots
       bar_arrive_warp(qfull, lane);
     }
     // warps of rows past the last one only keep the barriers going (their lanes' weights are
@@ -548,8 +578,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
     };
     auto weights = [&](int j, int term) {  // columns of a term of tile j's weights
-      return S::kLowOverS && term == S::kTermsP - 1 ? tl + S::kColS + (j & 1) * kTaKeys
-                                                    : tl + S::kColP + (j % S::kPBufs) * S::kPCols + term * (kTaKeys / 2);
+      return tl + S::kColP + (j % S::kPBufs) * S::kPCols + term * (kTaKeys / 2);
     };
     for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
@@ -563,10 +592,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
         for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
       }
-      if (!S::kLowOverS) {
-        tm_fence_before();
-        if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
-      }
+      tm_fence_before();
+      if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
       if (tree) {  // take tree values that are not finite out of the product
         const int k = ring_val(j, n);
         ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
@@ -614,22 +641,24 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if (j > 0) turn_wait(quarter, group);
       if (!idle) {
         const float known = s_m[ln];
-        if (__any_sync(0xffffffffu, known != m)) rescale(known);
-        if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
-          const float corr = rescale(fmaxf(m, mx));
-          s_m[ln] = m;
-          if (restart) {
-            pend = corr;
-          } else if (j > 0) {
-            done(j - 1);
+        if (__any_sync(0xffffffffu, known != m || mx > m + kTaLazy)) {
+          rescale(known);
+          if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+            const float corr = rescale(fmaxf(m, mx));
+            s_m[ln] = m;
+            if (restart) {
+              pend = corr;
+            } else if (j > 0) {
+              done(j - 1);
 #pragma unroll 1
-            for (int c = 0; ok && c < D; c += 16) {
-              float o[16];
-              tm_load(tl + S::kColO + c, o);
-              uint32_t w[16];
+              for (int c = 0; ok && c < D; c += 16) {
+                float o[16];
+                tm_load(tl + S::kColO + c, o);
+                uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
-              tm_store(tl + S::kColO + c, w);
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
+                tm_store(tl + S::kColO + c, w);
+              }
             }
           }
         }
@@ -665,6 +694,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               if (c / (kCols / 2) != part) tm_store(weights(j, tt) + c, zero);
         }
       }
+      // An idle warp also waits for its group's last products: its arrival below must not count for them.
+      if (idle && j >= S::kPBufs) done(j - S::kPBufs);
       if (restart) flush(j, pend);
       tm_st_wait();
       tm_fence_before();
