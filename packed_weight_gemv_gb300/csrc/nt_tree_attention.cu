@@ -65,16 +65,17 @@ struct TaShape {
   static constexpr int kTermsQ = sizeof(T) == 4 ? 3 : 1;
   static constexpr int kTermsP = sizeof(T) == 4 ? 3 : 2;
   static constexpr int kSlot = kTaKeys * D * 2;            // bytes of a ring slot: one tile's keys or values
-  // Tensor-memory columns: the accumulator, query terms, a buffer of scores per group and the weights.
-  // Where the weights would not fit beside all query terms (fp32 queries, D = 128), the smallest
-  // query term is a shared-memory operand (51 cycles per MMA instead of 32) and the groups share one
-  // buffer of weights.
-  static constexpr bool kLowInSmem = D + kTermsQ * D / 2 + 2 * kTaKeys + kTermsP * (kTaKeys / 2) > kTaTmemCols;
-  static constexpr int kTermsQT = kTermsQ - (kLowInSmem ? 1 : 0);  // query terms in tensor memory
+  // Tensor-memory columns: the accumulator, the query terms, a buffer of scores and one of weights for
+  // each group. Where they do not fit (fp32 queries, D = 128) the smallest query term is a
+  // shared-memory operand (51 cycles per MMA instead of 32) and the groups share the scores' buffer,
+  // which is in use for half of a tile's time; sharing the weights' buffer instead made every tile
+  // wait for the products of the one before (39.5 us at 25 nodes over 26K).
   static constexpr int kPCols = kTermsP * (kTaKeys / 2);
-  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + 2 * kTaKeys;
-  static constexpr int kPBufs = kColP + 2 * kPCols <= kTaTmemCols ? 2 : 1;
-  static constexpr int kLowBytes = kLowInSmem ? 128 * D * 2 : 0;
+  static constexpr bool kTight = D + kTermsQ * D / 2 + 2 * kTaKeys + 2 * kPCols > kTaTmemCols;
+  static constexpr int kTermsQT = kTermsQ - (kTight ? 1 : 0);  // query terms in tensor memory
+  static constexpr int kSBufs = kTight ? 1 : 2;
+  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + kSBufs * kTaKeys;
+  static constexpr int kLowBytes = kTight ? 128 * D * 2 : 0;
   // Ring and query term take 192 KB for either D: a second CTA on an SM would only wait for the first
   // one's tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
   static constexpr int kStages = (192 * 1024 - kLowBytes) / kSlot;
@@ -91,7 +92,7 @@ struct TaShape {
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
   static constexpr int kSmem = kStages * kSlot + kLowBytes + 1024;  // and alignment
   static_assert(kQSlot >= kTaFirst, "the queries' staging slots are filled after them");
-  static_assert(kColP + kPBufs * kPCols <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kColP + 2 * kPCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
 
@@ -425,10 +426,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const int k = ring_key(j);
         ok = wait(full(k), turn(k));
-        if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
+        const int last = j - S::kSBufs;
+        if (ok && last >= 0) ok = wait(sfree0 + 8 * (last & 1), (last >> 1) & 1);  // the buffer's last scores have been taken
         if (!ok) break;
         tm_fence_after();
-        const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
+        const uint32_t d = tmem + S::kColS + (j % S::kSBufs) * kTaKeys;
         const uint64_t bd = sdesc(slot(k), 16);
         // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
         if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
         tm_fence_after();
-        const uint32_t p = tmem + S::kColP + (j % S::kPBufs) * S::kPCols;
+        const uint32_t p = tmem + S::kColP + (j & 1) * S::kPCols;
         const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
 #pragma unroll
         for (int t = S::kTermsP - 1; t >= 0; --t)
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
 #pragma unroll
         for (int t = 0; t < S::kTermsQT; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
-        if constexpr (S::kLowInSmem) {  // rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
+        if constexpr (S::kTight) {  // rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
           uint8_t* low = ring + S::kStages * S::kSlot + group * (128 * 128) + ln * 128;
           const uint32_t* x = w[S::kTermsQ - 1];
 #pragma unroll
@@ -577,9 +579,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
     };
-    auto weights = [&](int j, int term) {  // columns of a term of tile j's weights
-      return tl + S::kColP + (j % S::kPBufs) * S::kPCols + term * (kTaKeys / 2);
-    };
+    const uint32_t pcol = tl + S::kColP + group * S::kPCols;
     for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tm_fence_after();
       float s[kCols];
       if (ok && !idle) {
-        tm_load(tl + S::kColS + group * kTaKeys + c0, s);
+        tm_load(tl + S::kColS + (j % S::kSBufs) * kTaKeys + c0, s);
       } else {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
@@ -681,9 +681,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
             for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
-          if (ch == 0 && j >= S::kPBufs) done(j - S::kPBufs);  // the buffer's last weights must have been read
+          if (ch == 0 && j >= 2) done(j - 2);  // the group's last weights must have been read
 #pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(weights(j, tt) + (c0 + ch) / 2, w[tt]);
+          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(pcol + tt * (kTaKeys / 2) + (c0 + ch) / 2, w[tt]);
         }
         l += ls.x + ls.y;
         if constexpr (DUP > 1) {  // the keys that other lanes weigh
@@ -691,11 +691,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int tt = 0; tt < S::kTermsP; ++tt)
 #pragma unroll
             for (int c = 0; c < kTaKeys / 2; c += 8)
-              if (c / (kCols / 2) != part) tm_store(weights(j, tt) + c, zero);
+              if (c / (kCols / 2) != part) tm_store(pcol + tt * (kTaKeys / 2) + c, zero);
         }
       }
       // An idle warp also waits for its group's last products: its arrival below must not count for them.
-      if (idle && j >= S::kPBufs) done(j - S::kPBufs);
+      if (idle && j >= 2) done(j - 2);
       if (restart) flush(j, pend);
       tm_st_wait();
       tm_fence_before();
