@@ -779,11 +779,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // Joins the splits of a row: W warps of a CTA share a row (warp w takes splits w, w + W, ...), a
-// lane D / 32 of its dimensions. A warp's first 8 splits are asked for together with their maxima, so
-// up to 8 W splits take one round trip to L2.
-template <typename T, int D, int W>
+// lane D / 32 of its dimensions. A warp asks for kBatch splits together with their maxima, so up to
+// kBatch * W splits take one round trip to L2. As a programmatic dependent launch this kernel adds
+// 3 us to a call of 25 nodes over 26K; joining in the kernel above behind a barrier of the splits
+// added 6, and its cooperative launch took away the overlap with the kernel before (2.5 us).
+template <typename T, int D, int W, int kBatch>
 __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int rows_per_tile) {
-  constexpr int E = D / 32, kBatch = 8;
+  constexpr int E = D / 32;
   __shared__ float s_m[4], s_l[4], s_o[W > 1 ? 4 : 1][D];
   dependent_launch_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
@@ -930,8 +932,11 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
   NT_TRY(check_launch("tree_attn_kernel"));
   if (p.nsplit > 1) {
     const int64_t rows = (int64_t)a.B * a.Hq;
-    const int w = p.nsplit > 8 ? 4 : 1;  // warps per row
-    auto join = w == 4 ? tree_attn_join_kernel<T, D, 4> : tree_attn_join_kernel<T, D, 1>;
+    // Warps per row and splits at a time: one round trip for up to 32 splits, and no load twice for few.
+    const int w = p.nsplit > 4 ? 4 : 1;
+    auto join = p.nsplit > 16 ? tree_attn_join_kernel<T, D, 4, 8> : p.nsplit > 8 ? tree_attn_join_kernel<T, D, 4, 4>
+                : p.nsplit > 4 ? tree_attn_join_kernel<T, D, 4, 2> : p.nsplit > 2 ? tree_attn_join_kernel<T, D, 1, 4>
+                : tree_attn_join_kernel<T, D, 1, 2>;
     NT_CUDA_TRY(launch_kernel(join, dim3((unsigned)((rows * w + 3) / 4)), dim3(128), 0, st, true, a, p.rows));
     NT_TRY(check_launch("tree_attn_join_kernel"));
   }
