@@ -1,4 +1,5 @@
-"""Builds ``libnt.so`` (the C ABI library of include/nt.h) in-tree with nvcc for sm_103a.
+"""Builds ``libnt.so`` (the C ABI library of include/nt.h) in-tree with nvcc for sm_103a, and
+``_ntbind.so``, the native part of its Python binding, with g++.
 
 Each ``csrc/*.cu`` translation unit is compiled in its own nvcc process (in parallel), then
 linked into ``packed_weight_gemv_gb300/_lib/libnt.so``. Re-running is incremental: a unit is
@@ -7,10 +8,12 @@ rebuilt when it or any header is newer than its object.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libnt.so")
+BIND = os.path.join(OUT_DIR, "_ntbind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,6 +36,26 @@ def nvcc() -> str:
 def _flags(extra=()):
     return [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
             "-I", CSRC, "--expt-relaxed-constexpr", *extra]
+
+
+def build_binding() -> str:
+    """csrc/nt_binding.cpp against this machine's torch and Python headers."""
+    src = os.path.join(CSRC, "nt_binding.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "nt.h")))
+    if os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+        return BIND
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BIND + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", INCLUDE, src, "-o", tmp, "-L", os.path.join(torch_dir, "lib"),
+           "-Wl,-rpath," + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on nt_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -53,7 +77,9 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(build_binding)
         results = list(ex.map(compile_one, sources))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_info:
         for _, log in results:

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of the C ABI in include/nt.h (libnt.so), with the same call names.
+"""Thin binding of the C ABI in include/nt.h (libnt.so), with the same call names: ctypes, and for the
+calls of a token-tree pass a native module (csrc/nt_binding.cpp).
 
 Argument marshalling only: every call passes device pointers of torch tensors (and the
 current torch CUDA stream unless one is given) to the library, and raises :class:`NtError`
@@ -8,6 +9,8 @@ when the library returns a non-zero status. There is no fallback of any kind: if
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional, Sequence
@@ -16,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libnt.so")
+BIND_PATH = os.path.join(_HERE, "_lib", "_ntbind.so")
 
 NT_OK = 0
 NT_ERR_INVALID_ARG = 1
@@ -97,17 +101,23 @@ class nt_decode_desc(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_bind = None  # the native binding of the tree-verify calls
+
+# What the native binding calls, in the order of its init().
+_BOUND = ("nt_last_error_string", "nt_qk_norm_rope_append", "nt_tree_layout", "nt_tree_attention", "nt_token_counts",
+          "nt_logits_adjust", "nt_tree_accept", "nt_tree_commit")
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Loads libnt.so (once). Raises if it is missing: there is no other implementation."""
-    global _lib
+    """Loads libnt.so and its native binding (once). Raises if one is missing: there is no other implementation."""
+    global _lib, _bind
     with _lock:
         if _lib is not None:
             return _lib
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        for p in (path, BIND_PATH):
+            if not os.path.exists(p):
+                raise RuntimeError(f"{p} is missing: build it with "
+                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(path)
         i, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
         i64, f, d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
@@ -163,6 +173,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        loader = importlib.machinery.ExtensionFileLoader("_ntbind", BIND_PATH)
+        bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ntbind", loader))
+        loader.exec_module(bind)
+        bind.init(NtError, *[ctypes.cast(getattr(lib, name), vp).value for name in _BOUND])
+        _bind = bind
         _lib = lib
         return lib
 
@@ -347,46 +362,22 @@ def nt_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, B: int, D: int, eps: float,
 
 
 # ---- verifying a drafted token tree --------------------------------------------------------
-# Shapes and strides are read from the tensors; what the C ABI cannot see (another type, other
-# shapes, elements that are not contiguous) is refused here, with the same exception.
-_DTYPES = {torch.float32: NT_F32, torch.bfloat16: NT_BF16}
-
-
-def _refuse(call: str, what: str):
-    raise NtError(NT_ERR_INVALID_ARG, call, what)
-
-
-def _flat(call: str, name: str, t: Optional[torch.Tensor], dtype, shape=None):
-    """Address of a contiguous tensor of this type (and shape); None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        _refuse(call, f"{name} must be a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape else ""))
-    return t.data_ptr()
-
-
-def _rows(call: str, name: str, t: torch.Tensor, dtype, shape):
-    """Address and row stride of a 3-D tensor whose rows' elements are contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
-        _refuse(call, f"{name} must be {dtype} {tuple(shape)} with contiguous heads")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1] * shape[2])
-
-
-def _shared(call: str, name: str, t: Optional[torch.Tensor], dtype, B: int, n: int):
-    """Address and row stride of a [n] tensor for all rows or a [B, n] tensor (0: one row for all)."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype or t.shape[-1] != n or t.stride(-1) != 1 or not (
-            t.dim() == 1 or (t.dim() == 2 and t.shape[0] in (1, B))):
-        _refuse(call, f"{name} must be {dtype} [{n}] or [{B}, {n}] with contiguous rows")
-    return t.data_ptr(), (0 if t.dim() == 1 or t.shape[0] == 1 else t.stride(0))
+# These calls go through the native binding (csrc/nt_binding.cpp), which reads shapes and strides from
+# the tensors and refuses what the C ABI cannot see (another type, other shapes, elements that are
+# not contiguous) with the same exception.
+def _native():
+    if _bind is None:
+        load_library()
+    return _bind
 
 
 def nt_rope_frequencies(rotary_dim: int, base: float, inv_freq: torch.Tensor, scaling: int = NT_ROPE_PLAIN,
                         factor: float = 1.0, trained_len: int = 0, slow: float = 1.0, fast: float = 32.0, stream=None):
-    ptr = _flat("nt_rope_frequencies", "inv_freq", inv_freq, torch.float64, (rotary_dim // 2,))
-    _check(load_library().nt_rope_frequencies(rotary_dim, base, scaling, factor, trained_len, slow, fast, ptr,
-                                              _stream(stream)), "nt_rope_frequencies")
+    """Angles per position of each rotated pair into inv_freq [rotary_dim / 2] float64."""
+    if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous() or 2 * inv_freq.numel() != rotary_dim:
+        raise NtError(NT_ERR_INVALID_ARG, "nt_rope_frequencies", "inv_freq must be contiguous float64 [rotary_dim / 2]")
+    _check(load_library().nt_rope_frequencies(rotary_dim, base, scaling, factor, trained_len, slow, fast,
+                                              inv_freq.data_ptr(), _stream(stream)), "nt_rope_frequencies")
 
 
 def nt_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_gamma: Optional[torch.Tensor],
@@ -395,32 +386,14 @@ def nt_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_
                            pos: Optional[torch.Tensor] = None, pos0: int = 0, rows: Optional[torch.Tensor] = None,
                            row0: int = 0, n_bad: Optional[torch.Tensor] = None, stream=None):
     """q [B, Hq, D], k and v [B, Hkv, D] (tokens any stride apart), caches [Hkv, t_stride, D] bf16."""
-    call = "nt_qk_norm_rope_append"
-    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 3 or q.dtype not in _DTYPES:
-        _refuse(call, "q, k and the caches must have three dimensions, q of fp32 or bf16")
-    B, Hq, D = q.shape
-    Hkv, ts = k.shape[1], k_cache.shape[1]
-    (qp, qs), (kp, ks) = _rows(call, "q", q, q.dtype, (B, Hq, D)), _rows(call, "k", k, q.dtype, (B, Hkv, D))
-    vp, vs = _rows(call, "v", v, q.dtype, (B, Hkv, D))
-    _check(load_library().nt_qk_norm_rope_append(
-        qp, kp, vp, _DTYPES[q.dtype], qs, ks, vs, _flat(call, "q_gamma", q_gamma, torch.float32, (D,)),
-        _flat(call, "k_gamma", k_gamma, torch.float32, (D,)), eps, B, Hq, Hkv, D,
-        _flat(call, "inv_freq", inv_freq, torch.float64), 0 if inv_freq is None else 2 * inv_freq.numel(), layout,
-        amplitude, _flat(call, "pos", pos, torch.int32, (B,)), pos0, _flat(call, "rows", rows, torch.int32, (B,)), row0,
-        _flat(call, "q_out", q_out, q.dtype, (B, Hq, D)), _flat(call, "k_cache", k_cache, torch.bfloat16, (Hkv, ts, D)),
-        _flat(call, "v_cache", v_cache, torch.bfloat16, (Hkv, ts, D)), ts, _ptr(n_bad), _stream(stream)), call)
+    _native().append(q, k, v, q_gamma, k_gamma, eps, inv_freq, layout, amplitude, q_out, k_cache, v_cache, pos, pos0,
+                     rows, row0, n_bad, stream)
 
 
 def nt_tree_layout(parent: torch.Tensor, mask: torch.Tensor, pos: Optional[torch.Tensor] = None, pos0: int = 0,
                    n_bad: Optional[torch.Tensor] = None, stream=None):
     """parent [B] int32 -> ancestor bits mask [B, words] int32 and positions pos [B] int32."""
-    call = "nt_tree_layout"
-    B = parent.numel()
-    if mask.dim() != 2 or mask.shape[0] != B:
-        _refuse(call, "mask must be [B, words]")
-    _check(load_library().nt_tree_layout(
-        _flat(call, "parent", parent, torch.int32), B, pos0, _flat(call, "mask", mask, torch.int32), mask.shape[1],
-        _flat(call, "pos", pos, torch.int32, (B,)), _ptr(n_bad), _stream(stream)), call)
+    _native().layout(parent, mask, pos, pos0, n_bad, stream)
 
 
 def nt_tree_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int, prefix: int) -> int:
@@ -433,26 +406,13 @@ def nt_tree_attention_workspace_size(B: int, Hq: int, Hkv: int, D: int, prefix: 
 def nt_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, prefix: int, tree_row0: int,
                       mask: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None):
     """q and out [B, Hq, D] fp32 or bf16, caches [Hkv, t_stride, D] bf16, mask [B, words] int32."""
-    call = "nt_tree_attention"
-    if q.dim() != 3 or k_cache.dim() != 3 or mask.dim() != 2 or mask.shape[0] != q.shape[0] or q.dtype not in _DTYPES:
-        _refuse(call, "q [B, Hq, D] fp32 or bf16, caches [Hkv, t_stride, D] and mask [B, words] are needed")
-    B, Hq, D = q.shape
-    Hkv, ts = k_cache.shape[0], k_cache.shape[1]
-    _check(load_library().nt_tree_attention(
-        _flat(call, "q", q, q.dtype), _DTYPES[q.dtype], _flat(call, "k_cache", k_cache, torch.bfloat16, (Hkv, ts, D)),
-        _flat(call, "v_cache", v_cache, torch.bfloat16, (Hkv, ts, D)), B, Hq, Hkv, D, prefix, tree_row0, ts,
-        _flat(call, "mask", mask, torch.int32), mask.shape[1], _flat(call, "out", out, q.dtype, (B, Hq, D)),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)), call)
+    _native().attention(q, k_cache, v_cache, prefix, tree_row0, mask, out, ws, stream)
 
 
 def nt_token_counts(tokens: torch.Tensor, counts: torch.Tensor, index: Optional[torch.Tensor] = None,
                     n: Optional[torch.Tensor] = None, n_bad: Optional[torch.Tensor] = None, stream=None):
     """counts [V] int32 += the tokens (int32), or those an index names; n: a device int32 bound on their number."""
-    call = "nt_token_counts"
-    _check(load_library().nt_token_counts(
-        _flat(call, "tokens", tokens, torch.int32), _flat(call, "index", index, torch.int32, tokens.shape),
-        tokens.numel(), _flat(call, "n", n, torch.int32), counts.numel(), _flat(call, "counts", counts, torch.int32),
-        _ptr(n_bad), _stream(stream)), call)
+    _native().counts(tokens, index, n, counts, n_bad, stream)
 
 
 def nt_logits_adjust_workspace_size(V: int, B: int) -> int:
@@ -468,29 +428,14 @@ def nt_logits_adjust(logits: torch.Tensor, counts: Optional[torch.Tensor] = None
                      out: Optional[torch.Tensor] = None, argmax: Optional[torch.Tensor] = None,
                      ws: Optional[torch.Tensor] = None, stream=None):
     """logits [B, V] fp32; counts int32, bias fp32 [V] or [B, V]; allowed int32 words [W] or [B, W], W = ceil(V / 32)."""
-    call = "nt_logits_adjust"
-    if logits.dim() != 2 or (tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != logits.shape[0])):
-        _refuse(call, "logits [B, V] and tree_mask [B, words] are needed")
-    B, V = logits.shape
-    cp, cs = _shared(call, "counts", counts, torch.int32, B, V)
-    bp, bs = _shared(call, "bias", bias, torch.float32, B, V)
-    ap, as_ = _shared(call, "allowed", allowed, torch.int32, B, (V + 31) // 32)
-    _check(load_library().nt_logits_adjust(
-        _flat(call, "logits", logits, torch.float32), B, V, cp, cs, _flat(call, "tree_mask", tree_mask, torch.int32),
-        0 if tree_mask is None else tree_mask.shape[1], _flat(call, "tokens", tokens, torch.int32, (B,)), repetition,
-        frequency, presence, bp, bs, ap, as_, _flat(call, "out", out, torch.float32, (B, V)),
-        _flat(call, "argmax", argmax, torch.int32, (B,)), None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), call)
+    _native().adjust(logits, counts, tree_mask, tokens, repetition, frequency, presence, bias, allowed, out, argmax, ws,
+                     stream)
 
 
 def nt_tree_accept(parent: torch.Tensor, token: torch.Tensor, argmax: torch.Tensor, emit: torch.Tensor,
                    path: torch.Tensor, n_emit: torch.Tensor, stream=None):
-    call = "nt_tree_accept"
-    B = parent.numel()
-    p = [_flat(call, n, t, torch.int32, (B,)) for n, t in
-         (("parent", parent), ("token", token), ("argmax", argmax), ("emit", emit), ("path", path))]
-    _check(load_library().nt_tree_accept(p[0], p[1], p[2], B, p[3], p[4], _flat(call, "n_emit", n_emit, torch.int32),
-                                         _stream(stream)), call)
+    """parent, token, argmax [B] int32 -> emit, path [B] and n_emit [1] int32."""
+    _native().accept(parent, token, argmax, emit, path, n_emit, stream)
 
 
 class pointer_array:
@@ -499,9 +444,12 @@ class pointer_array:
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         self._keep = list(tensors)
+        self.shape = tuple(self._keep[0].shape) if self._keep else ()
         for t in self._keep:
-            _flat("pointer_array", "a cache", t, torch.bfloat16, self._keep[0].shape)
+            if t.dtype is not torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != self.shape or t.dim() != 3:
+                raise NtError(NT_ERR_INVALID_ARG, "pointer_array", "caches must be contiguous bf16 [Hkv, t_stride, D], all alike")
         self.array = (ctypes.c_void_p * len(self._keep))(*[t.data_ptr() for t in self._keep])
+        self.address = ctypes.addressof(self.array)
 
     def __len__(self):
         return len(self._keep)
@@ -509,13 +457,11 @@ class pointer_array:
 
 def nt_tree_commit(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, path: torch.Tensor,
                    n_emit: torch.Tensor, src_row0: int, dst_row0: int, stream=None):
-    call = "nt_tree_commit"
-    if len(k_caches) != len(v_caches) or not len(k_caches) or any(
-            c._keep[0].shape != (Hkv, t_stride, D) for c in (k_caches, v_caches)):
-        _refuse(call, "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
-    _check(load_library().nt_tree_commit(
-        k_caches.array, v_caches.array, len(k_caches), Hkv, D, t_stride, _flat(call, "path", path, torch.int32),
-        _flat(call, "n_emit", n_emit, torch.int32), path.numel(), src_row0, dst_row0, _stream(stream)), call)
+    """Moves the accepted nodes' rows in every layer's caches (pointer_array); path [B], n_emit [1] int32."""
+    n = len(k_caches)
+    if n == 0 or len(v_caches) != n or k_caches.shape != (Hkv, t_stride, D) or v_caches.shape != k_caches.shape:
+        raise NtError(NT_ERR_INVALID_ARG, "nt_tree_commit", "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
+    _native().commit(k_caches.address, v_caches.address, n, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream)
 
 
 class DecodePlan:
