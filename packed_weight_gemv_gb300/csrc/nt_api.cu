@@ -5,7 +5,7 @@
 #include <mutex>
 #include <string>
 
-#include "nt_kernels.cuh"
+#include "nt_tree.cuh"
 
 namespace nt {
 

@@ -23,7 +23,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 // Test hook of the per-call timeout paths (nt_set_test_fault): the fault that is set (0 =
 // none) and the bound on the per-call kernels' waits while it is set (`dflt` otherwise).
-enum : int { kFaultNone = 0, kFaultHeadStream = 1, kFaultTc8 = 2, kFaultPrefill = 3, kFaultTree = 5 };
+enum : int { kFaultNone = 0, kFaultHeadStream = 1, kFaultTc8 = 2, kFaultPrefill = 3 };
 int test_fault();
 uint64_t test_fault_timeout_ns(uint64_t dflt);
 

@@ -88,9 +88,6 @@ struct HeadWs {
 // Bytes in front of the data of the GEMM workspaces (the status header, padded so the data
 // keeps the alignment its tensor maps need).
 constexpr size_t kWsHeaderBytes = 256;
-// Drafted token trees (nt_tree.cu, nt_tree_attention.cu, nt_logits_adjust.cu).
-constexpr int kTreeMaxNodes = 256;
-constexpr int64_t kTreeMaxRows = 1 << 20;  // nodes x query heads of one attention call
 inline size_t head_ws_bytes(int B) { return 16 + sizeof(HeadPartial) * (size_t)kHeadMaxCtas * B; }
 
 // Launchers (asynchronous on `st`; they return launch-configuration errors only).

@@ -10,7 +10,7 @@
 
 #include <algorithm>
 
-#include "nt_kernels.cuh"
+#include "nt_tree.cuh"
 
 namespace nt {
 namespace {

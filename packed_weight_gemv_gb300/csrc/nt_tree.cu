@@ -5,7 +5,7 @@
 // All three are small; their time is the launch and a few dependent steps.
 #include <algorithm>
 
-#include "nt_kernels.cuh"
+#include "nt_tree.cuh"
 
 namespace nt {
 namespace {

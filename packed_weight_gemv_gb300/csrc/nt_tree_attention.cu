@@ -43,7 +43,7 @@
 #include <string>
 #include <type_traits>
 
-#include "nt_kernels.cuh"
+#include "nt_tree.cuh"
 
 namespace nt {
 namespace {
