@@ -3,9 +3,15 @@
 // token counts that the penalties go by.
 //
 // Per value: x -> x / r or x * r by its sign, - f * count, - p where the token was used; + bias;
-// -inf where it is not allowed. Every step is one fp32 rounding, in this order. A value is read
-// once and written once; counts and bias rows are shared by the batch and come out of L2, so
-// the kernel is bound by memory.
+// -inf where it is not allowed. Every step is one fp32 rounding, in this order.
+//
+// A value is read once and written once, so the kernel is bound by memory if enough reads are on
+// their way and the instructions per value are few. A CTA holds a chunk of 1,024 tokens -- their
+// counts and biases, when the batch shares them, in registers -- and walks a group of rows over it;
+// the rows' values come through shared memory by asynchronous copies, up to eight rows ahead.
+// The penalties are straight-line code for every value: with a branch around them nearly every warp
+// took it for each of a lane's four tokens (a chunk has a few used tokens, a text's first chunks
+// hundreds), and a row cost 240 instructions per 128 values, twice the memory's time.
 #include <math.h>
 
 #include <algorithm>
@@ -16,10 +22,13 @@ namespace nt {
 namespace {
 
 constexpr int kAdjThreads = 256;
+constexpr int kAdjChunk = 4 * kAdjThreads;  // tokens of a CTA, four per thread
+constexpr int kAdjRows = 16;                // rows of a group at most
+constexpr int kAdjAhead = 8;                // rows of the ring in shared memory
 static_assert(kTreeMaxNodes <= kAdjThreads, "one thread per node");
 
-// Workspace: the 16-byte status header, then per row the best (value, index) key and the
-// counter of CTAs done with the row; both are zero between calls.
+// Workspace: the 16-byte status header, then per row the best (value, index) key and, in the first row
+// of a group, the counter of CTAs done with the group; all zero between calls.
 struct AdjWs {
   WsHeader head;
   struct Row {
@@ -37,6 +46,7 @@ struct AdjArgs {
   int mask_words;
   const int32_t* tokens;  // [B] the nodes' tokens
   float rep, freq, pres;
+  float rep_inv;  // 1 / rep rounded, 0 where quotient() does not apply
   const float* bias;
   int64_t bias_stride;
   const uint32_t* allowed;  // rows allowed_stride words apart
@@ -44,104 +54,240 @@ struct AdjArgs {
   float* out;       // [B][V] or null
   int32_t* argmax;  // [B] or null
   AdjWs* ws;
-  int per;  // values per CTA, a multiple of 4 * kAdjThreads
+  int group;  // rows of a CTA, at most kAdjRows
 };
 
-__device__ __forceinline__ float penalise(float x, int count, const AdjArgs& a) {
-  if (count <= 0) return x;
-  float y = x > 0.0f ? __fdiv_rn(x, a.rep) : __fmul_rn(x, a.rep);
-  y = __fsub_rn(y, __fmul_rn(a.freq, __int2float_rn(count)));
-  return __fsub_rn(y, a.pres);
+// x / rep rounded to nearest, by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / rep
+// rounded, one step q + (x - rep q) y brings q = x y within an ulp, and a second one, whose remainder
+// is exact, to the rounded quotient. It holds while nothing leaves the normal range: `plain`.
+__device__ __forceinline__ float quotient(float x, float rep, float rep_inv) {
+  float q = __fmul_rn(x, rep_inv);
+  q = __fmaf_rn(__fmaf_rn(-rep, q, x), rep_inv, q);
+  return __fmaf_rn(__fmaf_rn(-rep, q, x), rep_inv, q);
+}
+// Whether |x| is outside [2^-100, 2^100), as an unsigned number above kAdjRange.
+constexpr uint32_t kAdjSmall = (127u - 100u) << 23, kAdjRange = (200u << 23) - 1u;
+__device__ __forceinline__ uint32_t size_code(float x) { return (__float_as_uint(x) & 0x7fffffffu) - kAdjSmall; }
+// The quotients of values outside that range, out of the way of the others.
+__device__ __noinline__ float4 divide_all(float4 x, float rep) {
+  return make_float4(__fdiv_rn(x.x, rep), __fdiv_rn(x.y, rep), __fdiv_rn(x.z, rep), __fdiv_rn(x.w, rep));
 }
 
-// A key that orders values above -inf by (value, lower index first); 0 for the others.
-__device__ __forceinline__ unsigned long long choice_key(float y, int v) {
-  if (!(y > -INFINITY)) return 0ull;  // -inf and NaN are never chosen
+// Orders values above -inf as unsigned numbers; 0 for the others (-inf and NaN are never chosen).
+__device__ __forceinline__ uint32_t choice_key(float y) {
+  if (!(y > -INFINITY)) return 0u;
   const uint32_t u = __float_as_uint(y + 0.0f);  // -0 as +0
-  const uint32_t o = (u >> 31) ? ~u : u | 0x80000000u;
-  return ((unsigned long long)o << 32) | (uint32_t)~v;
+  return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// CTA: values [blockIdx.x * per, + per) of row blockIdx.y.
-template <int VEC>
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+// CTA: chunk blockIdx.x of the tokens, rows group * blockIdx.y ... . With VEC = 4 a thread has four
+// neighbouring tokens (16-byte accesses), with VEC = 1 four that are 256 apart (rows of any alignment).
+template <int VEC, bool kPenalties, bool kChoice>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
-  __shared__ int path_tok[kTreeMaxNodes];  // tokens of the row's path inside this CTA's range
-  __shared__ int n_path;
-  __shared__ unsigned long long warp_best[kAdjThreads / 32];
+  __shared__ __align__(16) float ring[kAdjAhead][kAdjChunk];         // rows on their way
+  __shared__ int path_node[kTreeMaxNodes], path_tok[kTreeMaxNodes];  // the tree's tokens inside the chunk
+  __shared__ uint32_t path_rows[kTreeMaxNodes];                      // bit r: on the path of the group's row r
+  __shared__ int n_path, s_last;
+  __shared__ unsigned long long row_best[kAdjRows][kAdjThreads / 32];
   dependent_launch_wait();
-  const int b = blockIdx.y, i = threadIdx.x;
-  const int v0 = blockIdx.x * a.per, v1 = min(a.V, v0 + a.per);
-  if (i == 0) n_path = 0;
-  __syncthreads();
-  if (a.tree_mask && i < a.B) {  // thread = node: a tree has at most kAdjThreads
-    const uint32_t w = a.tree_mask[(int64_t)b * a.mask_words + (i >> 5)];
-    const int t = a.tokens[i];
-    if ((w >> (i & 31) & 1u) && t >= v0 && t < v1) path_tok[atomicAdd(&n_path, 1)] = t;
+  const int i = threadIdx.x, lane = i & 31, v0 = blockIdx.x * kAdjChunk, first = v0 + (VEC == 4 ? 4 * i : i);
+  const int b0 = blockIdx.y * a.group, nb = min(a.group, a.B - b0);
+  constexpr int kStep = VEC == 4 ? 1 : kAdjThreads;  // between a thread's tokens
+  auto on = [&](int e) { return first + e * kStep < a.V; };  // with VEC = 4, V is a multiple of 4
+  const int words = (a.V + 31) / 32;
+  // A thread copies its own tokens and reads no other's, so the ring needs no barrier.
+  const float* next_x = a.x + (int64_t)b0 * a.V + first;
+  auto fetch = [&](int r) {
+    if (r < nb) {
+      float* st = ring[r % kAdjAhead];
+      if constexpr (VEC == 4) {
+        if (on(0)) copy_async<16>(st + 4 * i, next_x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (on(e)) copy_async<4>(st + i + e * kStep, next_x + e * kStep);
+      }
+      next_x += a.V;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");  // one group per row, an empty one past the last
+  };
+#pragma unroll
+  for (int r = 0; r < kAdjAhead; ++r) fetch(r);
+  // A warp's 128 tokens take four words of a row's allowed bits: with VEC = 4 a lane loads its own, with
+  // VEC = 1 lane e the one of all lanes' token e. Loaded a row ahead.
+  const int word = VEC == 4 ? first >> 5 : (first >> 5) + (lane & 3) * (kStep / 32);
+  const bool has_word = a.allowed && word < words;
+  const uint32_t* next_word = has_word ? a.allowed + b0 * a.allowed_stride + word : nullptr;
+  auto load_allowed = [&](int r) -> uint32_t {
+    if (!has_word || r >= nb) return ~0u;
+    const uint32_t w = __ldg(next_word);
+    next_word += a.allowed_stride;
+    return w;
+  };
+  uint32_t next_allowed = load_allowed(0);
+  float* out = a.out ? a.out + (int64_t)b0 * a.V + first : nullptr;
+
+  int np = 0;
+  if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
+    if (i == 0) n_path = 0;
+    __syncthreads();
+    const int t = i < a.B ? a.tokens[i] : -1;
+    if (t >= v0 && t < v0 + kAdjChunk && t < a.V) {
+      const int at = atomicAdd(&n_path, 1);
+      path_node[at] = i;
+      path_tok[at] = t;
+      path_rows[at] = 0u;
+    }
+    __syncthreads();
+    np = n_path;
+    for (int x = i; x < np * nb; x += kAdjThreads) {
+      const int p = x / nb, r = x - p * nb, node = path_node[p];
+      if (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (node >> 5)) >> (node & 31) & 1u) atomicOr(&path_rows[p], 1u << r);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int np = n_path;
-  const float* x = a.x + (int64_t)b * a.V;
-  const int32_t* cnt = a.counts ? a.counts + b * a.counts_stride : nullptr;
-  const float* bias = a.bias ? a.bias + b * a.bias_stride : nullptr;
-  const uint32_t* allowed = a.allowed ? a.allowed + b * a.allowed_stride : nullptr;
-  float* out = a.out ? a.out + (int64_t)b * a.V : nullptr;
-  unsigned long long best = 0;
-  for (int v = v0 + i * VEC; v < v1; v += kAdjThreads * VEC) {
-    float y[VEC], bi[VEC];
-    int c[VEC];
+  auto load_counts = [&](int b, int (&c)[4]) {
+    const int32_t* p = a.counts + b * a.counts_stride + first;
     if constexpr (VEC == 4) {
-      const float4 t = __ldcs(reinterpret_cast<const float4*>(x + v));
-      y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
-      const int4 ct = cnt ? __ldg(reinterpret_cast<const int4*>(cnt + v)) : make_int4(0, 0, 0, 0);
-      c[0] = ct.x; c[1] = ct.y; c[2] = ct.z; c[3] = ct.w;
-      const float4 bt = bias ? __ldg(reinterpret_cast<const float4*>(bias + v)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      bi[0] = bt.x; bi[1] = bt.y; bi[2] = bt.z; bi[3] = bt.w;
+      const int4 t = on(0) ? __ldg(reinterpret_cast<const int4*>(p)) : make_int4(0, 0, 0, 0);
+      c[0] = t.x; c[1] = t.y; c[2] = t.z; c[3] = t.w;
     } else {
-      y[0] = __ldcs(x + v);
-      c[0] = cnt ? __ldg(cnt + v) : 0;
-      bi[0] = bias ? __ldg(bias + v) : 0.0f;
-    }
-    const uint32_t w = allowed ? __ldg(allowed + (v >> 5)) >> (v & 31) : ~0u;
-    for (int k = 0; k < np; ++k) {
-      const int t = path_tok[k];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] += t == v + e;
+      for (int e = 0; e < 4; ++e) c[e] = on(e) ? __ldg(p + e * kStep) : 0;
+    }
+  };
+  auto load_bias = [&](int b, float (&x)[4]) {
+    const float* p = a.bias + b * a.bias_stride + first;
+    if constexpr (VEC == 4) {
+      const float4 t = on(0) ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = on(e) ? __ldg(p + e * kStep) : 0.0f;
+    }
+  };
+  int c[4] = {0, 0, 0, 0};
+  float bias[4] = {-0.f, -0.f, -0.f, -0.f};  // x + -0 is x, whatever x is
+  if (a.counts && a.counts_stride == 0) load_counts(0, c);
+  if (a.bias && a.bias_stride == 0) load_bias(0, bias);
+  uint32_t path = 0;  // bit e: token e is on some path of the group
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    for (int p = 0; p < np; ++p) path |= (uint32_t)(path_tok[p] == first + e * kStep) << e;
+  const bool warp_path = __any_sync(0xffffffffu, path != 0);
+  const bool row_counts = a.counts && a.counts_stride != 0, row_bias = a.bias && a.bias_stride != 0;
+  float less[4];  // frequency * count
+#pragma unroll
+  for (int e = 0; e < 4; ++e) less[e] = __fmul_rn(a.freq, __int2float_rn(c[e]));
+
+  for (int r = 0; r < nb; ++r) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAdjAhead - 1) : "memory");  // this row is here
+    const float* st = ring[r % kAdjAhead];
+    float y[4];
+    if constexpr (VEC == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(st + 4 * i);
+      y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = st[i + e * kStep];
+    }
+    uint32_t allow = next_allowed;
+    next_allowed = load_allowed(r + 1);
+    fetch(r + kAdjAhead);
+    if constexpr (VEC == 4) {
+      allow >>= first & 31;
+    } else {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bits |= (__shfl_sync(0xffffffffu, allow, e) >> (first & 31) & 1u) << e;
+      allow = bits;
+    }
+    if (row_bias) load_bias(b0 + r, bias);
+    if constexpr (kPenalties) {
+      int n[4] = {c[0], c[1], c[2], c[3]};
+      if (row_counts || warp_path) {
+        if (row_counts) load_counts(b0 + r, n);
+        for (int p = 0; warp_path && p < np; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[e] += path_tok[p] == first + e * kStep ? (int)(path_rows[p] >> r & 1u) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) less[e] = __fmul_rn(a.freq, __int2float_rn(n[e]));
+      }
+      float q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = quotient(y[e], a.rep, a.rep_inv);
+      const uint32_t code = max(max(size_code(y[0]), size_code(y[1])), max(size_code(y[2]), size_code(y[3])));
+      if (code > kAdjRange || a.rep_inv == 0.0f) {  // rare
+        const float4 t = divide_all(make_float4(y[0], y[1], y[2], y[3]), a.rep);
+        q[0] = t.x; q[1] = t.y; q[2] = t.z; q[3] = t.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = __fsub_rn(__fsub_rn(y[e] > 0.0f ? q[e] : __fmul_rn(y[e], a.rep), less[e]), a.pres);
+        y[e] = n[e] > 0 ? v : y[e];
+      }
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      y[e] = penalise(y[e], c[e], a);
-      if (bias) y[e] = __fadd_rn(y[e], bi[e]);
-      if (!(w >> e & 1u)) y[e] = -INFINITY;
-      const unsigned long long key = choice_key(y[e], v + e);
-      best = key > best ? key : best;
+    for (int e = 0; e < 4; ++e) {
+      y[e] = __fadd_rn(y[e], bias[e]);
+      y[e] = allow >> e & 1u ? y[e] : -INFINITY;
     }
     if (out) {
-      if constexpr (VEC == 4) __stcs(reinterpret_cast<float4*>(out + v), make_float4(y[0], y[1], y[2], y[3]));
-      else __stcs(out + v, y[0]);
+      if constexpr (VEC == 4) {
+        if (on(0)) __stcs(reinterpret_cast<float4*>(out), make_float4(y[0], y[1], y[2], y[3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (on(e)) __stcs(out + e * kStep, y[e]);
+      }
+      out += a.V;
+    }
+    if constexpr (kChoice) {
+      if (VEC == 1 || !on(3)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!on(e)) y[e] = -INFINITY;
+      }
+      const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));  // NaN is left out
+      const uint32_t key = choice_key(top), most = __reduce_max_sync(0xffffffffu, key);
+      // the lowest token with that value: with VEC = 4 it is the lowest lane's
+      const uint32_t with = __ballot_sync(0xffffffffu, key == most);
+      const bool mine = VEC == 1 ? key == most : lane == __ffs(with) - 1;
+      uint32_t at = ~0u;
+      if (mine) at = first + (y[0] == top ? 0 : y[1] == top ? kStep : y[2] == top ? 2 * kStep : 3 * kStep);
+      if (VEC == 1) at = __reduce_min_sync(0xffffffffu, at);
+      if (VEC == 1 ? lane == 0 : mine) row_best[r][i >> 5] = most ? ((unsigned long long)most << 32) | (uint32_t)~at : 0ull;
     }
   }
-  if (!a.argmax) return;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-    best = other > best ? other : best;
-  }
-  if ((i & 31) == 0) warp_best[i >> 5] = best;
+  if constexpr (!kChoice) return;
   __syncthreads();
-  if (i == 0) {
+  unsigned long long best = 0;
+  AdjWs::Row* row = a.ws->row + b0;
+  if (i < nb) {  // thread = row of the group
 #pragma unroll
-    for (int k = 1; k < kAdjThreads / 32; ++k) best = warp_best[k] > best ? warp_best[k] : best;
-    AdjWs::Row& r = a.ws->row[b];
+    for (int k = 0; k < kAdjThreads / 32; ++k) best = row_best[i][k] > best ? row_best[i][k] : best;
     if (gridDim.x > 1) {
-      atomicMax(&r.best, best);
+      if (best) atomicMax(&row[i].best, best);
       __threadfence();
-      if (atomicAdd(&r.done, 1u) != gridDim.x - 1) return;
-      __threadfence();
-      best = atomicExch(&r.best, 0ull);  // the row's last CTA; back to zero for the next call
-      r.done = 0u;
     }
-    a.argmax[b] = best ? (int32_t)~(uint32_t)best : -1;
   }
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (i == 0) s_last = atomicAdd(&row[0].done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (i < nb) best = atomicExch(&row[i].best, 0ull);  // the group's last CTA; back to zero for the next call
+    if (i == 0) row[0].done = 0u;
+  }
+  if (i < nb) a.argmax[b0 + i] = best ? (int32_t)~(uint32_t)best : -1;
 }
 
 __global__ void __launch_bounds__(kAdjThreads) count_kernel(const int32_t* __restrict__ tokens,
@@ -215,13 +361,21 @@ nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* cou
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_logits_adjust_workspace_size");
   NT_TRY(check_device());
   AdjArgs a{logits, B, V, counts_opt, counts_stride, tree_mask_opt, mask_words, tokens_opt, repetition, frequency,
-            presence, bias_opt, bias_stride, allowed_opt, allowed_stride, out_opt, argmax_opt, static_cast<AdjWs*>(ws),
-            4 * kAdjThreads};
+            presence, 0.0f, bias_opt, bias_stride, allowed_opt, allowed_stride, out_opt, argmax_opt, static_cast<AdjWs*>(ws),
+            1};
+  if (repetition > 1e-9f && repetition < 1e9f) a.rep_inv = 1.0f / repetition;
   const bool vec = V % 4 == 0 && aligned(logits, 16) && (!out_opt || aligned(out_opt, 16)) &&
                    (!counts_opt || (aligned(counts_opt, 16) && counts_stride % 4 == 0)) &&
                    (!bias_opt || (aligned(bias_opt, 16) && bias_stride % 4 == 0));
-  auto kern = vec ? adjust_kernel<4> : adjust_kernel<1>;
-  const dim3 grid((V + a.per - 1) / a.per, B);
+  const bool pen = counts_opt || tree_mask_opt;
+  auto kern = vec ? (pen ? (argmax_opt ? adjust_kernel<4, true, true> : adjust_kernel<4, true, false>)
+                         : (argmax_opt ? adjust_kernel<4, false, true> : adjust_kernel<4, false, false>))
+                  : (pen ? (argmax_opt ? adjust_kernel<1, true, true> : adjust_kernel<1, true, false>)
+                         : (argmax_opt ? adjust_kernel<1, false, true> : adjust_kernel<1, false, false>));
+  // Rows per CTA: as many as leave every SM its four CTAs.
+  const int chunks = (V + kAdjChunk - 1) / kAdjChunk;
+  a.group = (int)std::min<int64_t>(kAdjRows, std::max<int64_t>(1, (int64_t)chunks * B / (4 * device_sm_count())));
+  const dim3 grid(chunks, (B + a.group - 1) / a.group);
   NT_CUDA_TRY(launch_kernel(kern, grid, dim3(kAdjThreads), 0, reinterpret_cast<cudaStream_t>(stream), true, a));
   return check_launch("adjust_kernel");
 }

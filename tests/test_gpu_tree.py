@@ -297,6 +297,21 @@ def test_adjust_ties_nans_and_infinities(V):
     assert np.array_equal(y[:6], x[:6], equal_nan=True) and y[6, 5] == -np.inf
 
 
+@pytest.mark.parametrize("rep", [1.1, 1.0, 1.25, 3.0, 0.7, 1.9999999, 1e-5, 7e4, 1e-30, 1e30])
+def test_adjust_quotients_are_rounded(rep):
+    """Every significand of one binade, and values of any size, divided as IEEE division does."""
+    sig = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(127 << 23)).view(np.float32)
+    rs = np.random.RandomState(1)
+    odd = rs.randint(0, 0x7f800000, 1 << 16).astype(np.uint32).view(np.float32)
+    x = np.concatenate([sig, odd, -odd, np.float32([0.0, -0.0, np.inf, -np.inf, 1e-45])])
+    out = torch.empty(1, x.size, device=DEV)
+    nt.nt_logits_adjust(dev(x[None]), counts=torch.ones(x.size, dtype=torch.int32, device=DEV), repetition=rep, out=out)
+    with np.errstate(over="ignore", under="ignore"):
+        r = np.float32(rep)
+        want = np.where(x > 0, x / r, x * r)
+    assert np.array_equal(host(out)[0], want)
+
+
 def test_token_counts():
     rs = np.random.RandomState(0)
     for n in (0, 1, 255, 70000):
