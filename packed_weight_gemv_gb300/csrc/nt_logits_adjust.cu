@@ -6,13 +6,14 @@
 // -inf where it is not allowed. Every step is one fp32 rounding, in this order.
 //
 // A value is read once and written once, so the kernel is bound by memory if enough reads are on
-// their way and the instructions per value are few. A CTA holds a chunk of 1,024 tokens -- their
+// their way and the instructions per value are few. A CTA holds a chunk of 2,048 tokens -- their
 // counts and biases, when the batch shares them, in registers -- and walks a group of rows over it;
-// the rows' values come through shared memory by asynchronous copies, up to eight rows ahead.
-// The penalties are straight-line code for every value: with a branch around them nearly every warp
-// took it for each of a lane's four tokens (a chunk has a few used tokens, a text's first chunks
-// hundreds), and a row cost 240 instructions per 128 values, twice the memory's time.
+// the rows' values come through shared memory by asynchronous copies, up to four rows ahead.
+// The penalties are straight-line code for every value, two values to an instruction: with a branch
+// around them nearly every warp took it for each of a lane's tokens (a chunk has a few used tokens, a
+// text's first chunks hundreds), and a row cost 240 instructions per 128 values.
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -22,9 +23,10 @@ namespace nt {
 namespace {
 
 constexpr int kAdjThreads = 256;
-constexpr int kAdjChunk = 4 * kAdjThreads;  // tokens of a CTA, four per thread
+constexpr int kAdjPer = 8;                  // tokens per thread
+constexpr int kAdjChunk = kAdjPer * kAdjThreads;
 constexpr int kAdjRows = 16;                // rows of a group at most
-constexpr int kAdjAhead = 8;                // rows of the ring in shared memory
+constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
 static_assert(kTreeMaxNodes <= kAdjThreads, "one thread per node");
 
 // Workspace: the 16-byte status header, then per row the best (value, index) key and, in the first row
@@ -60,18 +62,42 @@ struct AdjArgs {
 // x / rep rounded to nearest, by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / rep
 // rounded, one step q + (x - rep q) y brings q = x y within an ulp, and a second one, whose remainder
 // is exact, to the rounded quotient. It holds while nothing leaves the normal range: `plain`.
-__device__ __forceinline__ float quotient(float x, float rep, float rep_inv) {
-  float q = __fmul_rn(x, rep_inv);
-  q = __fmaf_rn(__fmaf_rn(-rep, q, x), rep_inv, q);
-  return __fmaf_rn(__fmaf_rn(-rep, q, x), rep_inv, q);
+struct Pair {  // two fp32 values that one instruction works on
+  float x, y;
+};
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ Pair both(float v) { return Pair{v, v}; }
+__device__ __forceinline__ Pair quotient(Pair x, Pair minus_rep, Pair rep_inv) {
+  Pair q = mul2(x, rep_inv);
+  q = fma2(fma2(minus_rep, q, x), rep_inv, q);
+  return fma2(fma2(minus_rep, q, x), rep_inv, q);
 }
 // Whether |x| is outside [2^-100, 2^100), as an unsigned number above kAdjRange.
 constexpr uint32_t kAdjSmall = (127u - 100u) << 23, kAdjRange = (200u << 23) - 1u;
 __device__ __forceinline__ uint32_t size_code(float x) { return (__float_as_uint(x) & 0x7fffffffu) - kAdjSmall; }
 // The quotients of values outside that range, out of the way of the others.
-__device__ __noinline__ float4 divide_all(float4 x, float rep) {
-  return make_float4(__fdiv_rn(x.x, rep), __fdiv_rn(x.y, rep), __fdiv_rn(x.z, rep), __fdiv_rn(x.w, rep));
-}
+__device__ __noinline__ float divide_one(float x, float rep) { return __fdiv_rn(x, rep); }
 
 // Orders values above -inf as unsigned numbers; 0 for the others (-inf and NaN are never chosen).
 __device__ __forceinline__ uint32_t choice_key(float y) {
@@ -87,62 +113,63 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
 }
 
-// CTA: chunk blockIdx.x of the tokens, rows group * blockIdx.y ... . With VEC = 4 a thread has four
-// neighbouring tokens (16-byte accesses), with VEC = 1 four that are 256 apart (rows of any alignment).
+// CTA: chunk blockIdx.x of the tokens, rows group * blockIdx.y ... . With VEC = 4 a thread has two times
+// four neighbouring tokens (16-byte accesses), with VEC = 1 eight that are 256 apart (rows of any alignment).
 template <int VEC, bool kPenalties, bool kChoice>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
+  constexpr int N = kAdjPer;
   __shared__ __align__(16) float ring[kAdjAhead][kAdjChunk];         // rows on their way
   __shared__ int path_node[kTreeMaxNodes], path_tok[kTreeMaxNodes];  // the tree's tokens inside the chunk
   __shared__ uint32_t path_rows[kTreeMaxNodes];                      // bit r: on the path of the group's row r
   __shared__ int n_path, s_last;
   __shared__ unsigned long long row_best[kAdjRows][kAdjThreads / 32];
   dependent_launch_wait();
-  const int i = threadIdx.x, lane = i & 31, v0 = blockIdx.x * kAdjChunk, first = v0 + (VEC == 4 ? 4 * i : i);
+  const int i = threadIdx.x, lane = i & 31, v0 = blockIdx.x * kAdjChunk;
   const int b0 = blockIdx.y * a.group, nb = min(a.group, a.B - b0);
-  constexpr int kStep = VEC == 4 ? 1 : kAdjThreads;  // between a thread's tokens
-  auto on = [&](int e) { return first + e * kStep < a.V; };  // with VEC = 4, V is a multiple of 4
-  const int words = (a.V + 31) / 32;
+  // place of the thread's token e in the chunk
+  auto place = [&](int e) { return VEC == 4 ? e / 4 * (4 * kAdjThreads) + 4 * i + e % 4 : e * kAdjThreads + i; };
+  const int inside = a.V - v0;
+  auto on = [&](int e) { return place(VEC == 4 ? e & ~3 : e) < inside; };  // with VEC = 4, V is a multiple of 4
+  const bool whole = inside >= kAdjChunk;  // every token of the chunk exists
   // A thread copies its own tokens and reads no other's, so the ring needs no barrier.
-  const float* next_x = a.x + (int64_t)b0 * a.V + first;
+  const float* next_x = a.x + (int64_t)b0 * a.V + v0;
   auto fetch = [&](int r) {
     if (r < nb) {
       float* st = ring[r % kAdjAhead];
-      if constexpr (VEC == 4) {
-        if (on(0)) copy_async<16>(st + 4 * i, next_x);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (on(e)) copy_async<4>(st + i + e * kStep, next_x + e * kStep);
-      }
+      for (int e = 0; e < N; e += VEC)
+        if (whole || on(e)) copy_async<4 * VEC>(st + place(e), next_x + place(e));
       next_x += a.V;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");  // one group per row, an empty one past the last
   };
 #pragma unroll
   for (int r = 0; r < kAdjAhead; ++r) fetch(r);
-  // A warp's 128 tokens take four words of a row's allowed bits: with VEC = 4 a lane loads its own, with
-  // VEC = 1 lane e the one of all lanes' token e. Loaded a row ahead.
-  const int word = VEC == 4 ? first >> 5 : (first >> 5) + (lane & 3) * (kStep / 32);
-  const bool has_word = a.allowed && word < words;
-  const uint32_t* next_word = has_word ? a.allowed + b0 * a.allowed_stride + word : nullptr;
-  auto load_allowed = [&](int r) -> uint32_t {
-    if (!has_word || r >= nb) return ~0u;
-    const uint32_t w = __ldg(next_word);
-    next_word += a.allowed_stride;
-    return w;
+  // A row's allowed bits of this thread: with VEC = 4 of its own two words, with VEC = 1 lane e loads the
+  // one of all lanes' token e. Loaded a row ahead.
+  const int words = (a.V + 31) / 32 - (v0 >> 5);  // from the chunk's first on
+  const int w0 = VEC == 4 ? place(0) >> 5 : (i >> 5) + (lane & 7) * (kAdjThreads / 32), w1 = VEC == 4 ? place(4) >> 5 : 0;
+  const uint32_t* next_word = a.allowed ? a.allowed + b0 * a.allowed_stride + (v0 >> 5) : nullptr;
+  uint32_t next_allowed[2] = {~0u, ~0u};
+  auto load_allowed = [&](int r) {
+    if (next_word && r < nb) {
+      if (w0 < words) next_allowed[0] = __ldg(next_word + w0);
+      if (VEC == 4 && w1 < words) next_allowed[1] = __ldg(next_word + w1);
+      next_word += a.allowed_stride;
+    }
   };
-  uint32_t next_allowed = load_allowed(0);
-  float* out = a.out ? a.out + (int64_t)b0 * a.V + first : nullptr;
+  load_allowed(0);
+  float* out = a.out ? a.out + (int64_t)b0 * a.V + v0 : nullptr;
 
   int np = 0;
   if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
     if (i == 0) n_path = 0;
     __syncthreads();
     const int t = i < a.B ? a.tokens[i] : -1;
-    if (t >= v0 && t < v0 + kAdjChunk && t < a.V) {
+    if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
       const int at = atomicAdd(&n_path, 1);
       path_node[at] = i;
-      path_tok[at] = t;
+      path_tok[at] = t - v0;
       path_rows[at] = 0u;
     }
     __syncthreads();
@@ -153,117 +180,124 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
     }
     __syncthreads();
   }
-  auto load_counts = [&](int b, int (&c)[4]) {
-    const int32_t* p = a.counts + b * a.counts_stride + first;
-    if constexpr (VEC == 4) {
-      const int4 t = on(0) ? __ldg(reinterpret_cast<const int4*>(p)) : make_int4(0, 0, 0, 0);
-      c[0] = t.x; c[1] = t.y; c[2] = t.z; c[3] = t.w;
-    } else {
+  auto load = [&](const auto* row, auto(&x)[N], auto none) {  // this thread's part of a row of counts or biases
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = on(e) ? __ldg(p + e * kStep) : 0;
+    for (int e = 0; e < N; e += VEC) {
+      if constexpr (VEC == 4) {
+        const uint4 t = on(e) ? __ldg(reinterpret_cast<const uint4*>(row + place(e))) : make_uint4(0u, 0u, 0u, 0u);
+        memcpy(&x[e], &t, 16);
+        if (!on(e)) x[e] = x[e + 1] = x[e + 2] = x[e + 3] = none;
+      } else {
+        x[e] = on(e) ? __ldg(row + place(e)) : none;
+      }
     }
   };
-  auto load_bias = [&](int b, float (&x)[4]) {
-    const float* p = a.bias + b * a.bias_stride + first;
-    if constexpr (VEC == 4) {
-      const float4 t = on(0) ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-    } else {
+  int c[N] = {};
+  float bias[N];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = on(e) ? __ldg(p + e * kStep) : 0.0f;
-    }
-  };
-  int c[4] = {0, 0, 0, 0};
-  float bias[4] = {-0.f, -0.f, -0.f, -0.f};  // x + -0 is x, whatever x is
-  if (a.counts && a.counts_stride == 0) load_counts(0, c);
-  if (a.bias && a.bias_stride == 0) load_bias(0, bias);
-  uint32_t path = 0;  // bit e: token e is on some path of the group
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    for (int p = 0; p < np; ++p) path |= (uint32_t)(path_tok[p] == first + e * kStep) << e;
-  const bool warp_path = __any_sync(0xffffffffu, path != 0);
+  for (int e = 0; e < N; ++e) bias[e] = -0.0f;  // x + -0 is x, whatever x is
   const bool row_counts = a.counts && a.counts_stride != 0, row_bias = a.bias && a.bias_stride != 0;
-  float less[4];  // frequency * count
+  if (a.counts && !row_counts) load(a.counts + v0, c, 0);
+  if (a.bias && !row_bias) load(a.bias + v0, bias, -0.0f);
+  bool on_path = false;  // a token is on some path of the group
+  for (int p = 0; p < np; ++p)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) less[e] = __fmul_rn(a.freq, __int2float_rn(c[e]));
+    for (int e = 0; e < N; ++e) on_path |= path_tok[p] == place(e);
+  const bool warp_path = __any_sync(0xffffffffu, on_path);
+  float less[N];      // - frequency * count
+  uint32_t used = 0;  // bit e: token e has been used
+  auto count = [&](const int(&n)[N]) {
+    used = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      less[e] = -__fmul_rn(a.freq, __int2float_rn(n[e]));
+      used |= (uint32_t)(n[e] > 0) << e;
+    }
+  };
+  count(c);
 
   for (int r = 0; r < nb; ++r) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdjAhead - 1) : "memory");  // this row is here
     const float* st = ring[r % kAdjAhead];
-    float y[4];
+    float y[N];
+#pragma unroll
+    for (int e = 0; e < N; e += VEC) {
+      if constexpr (VEC == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(st + place(e));
+        y[e] = t.x; y[e + 1] = t.y; y[e + 2] = t.z; y[e + 3] = t.w;
+      } else {
+        y[e] = st[place(e)];
+      }
+    }
+    uint32_t allow = 0;  // bit e: token e
     if constexpr (VEC == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(st + 4 * i);
-      y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
+      allow = (next_allowed[0] >> (4 * i & 31) & 15u) | (next_allowed[1] >> (4 * i & 31) & 15u) << 4;
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = st[i + e * kStep];
+      for (int e = 0; e < N; ++e) allow |= (__shfl_sync(0xffffffffu, next_allowed[0], e) >> (i & 31) & 1u) << e;
     }
-    uint32_t allow = next_allowed;
-    next_allowed = load_allowed(r + 1);
+    load_allowed(r + 1);
     fetch(r + kAdjAhead);
-    if constexpr (VEC == 4) {
-      allow >>= first & 31;
-    } else {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bits |= (__shfl_sync(0xffffffffu, allow, e) >> (first & 31) & 1u) << e;
-      allow = bits;
-    }
-    if (row_bias) load_bias(b0 + r, bias);
+    if (row_bias) load(a.bias + (b0 + r) * a.bias_stride + v0, bias, -0.0f);
     if constexpr (kPenalties) {
-      int n[4] = {c[0], c[1], c[2], c[3]};
       if (row_counts || warp_path) {
-        if (row_counts) load_counts(b0 + r, n);
+        int n[N];
+        if (row_counts) load(a.counts + (b0 + r) * a.counts_stride + v0, n, 0);
+#pragma unroll
+        for (int e = 0; e < N; ++e) n[e] = row_counts ? n[e] : c[e];
         for (int p = 0; warp_path && p < np; ++p)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) n[e] += path_tok[p] == first + e * kStep ? (int)(path_rows[p] >> r & 1u) : 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) less[e] = __fmul_rn(a.freq, __int2float_rn(n[e]));
+          for (int e = 0; e < N; ++e) n[e] += path_tok[p] == place(e) ? (int)(path_rows[p] >> r & 1u) : 0;
+        count(n);
       }
-      float q[4];
+      uint32_t code = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = quotient(y[e], a.rep, a.rep_inv);
-      const uint32_t code = max(max(size_code(y[0]), size_code(y[1])), max(size_code(y[2]), size_code(y[3])));
-      if (code > kAdjRange || a.rep_inv == 0.0f) {  // rare
-        const float4 t = divide_all(make_float4(y[0], y[1], y[2], y[3]), a.rep);
-        q[0] = t.x; q[1] = t.y; q[2] = t.z; q[3] = t.w;
-      }
+      for (int e = 0; e < N; ++e) code = max(code, size_code(y[e]));
+      const bool rare = code > kAdjRange || a.rep_inv == 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = __fsub_rn(__fsub_rn(y[e] > 0.0f ? q[e] : __fmul_rn(y[e], a.rep), less[e]), a.pres);
-        y[e] = n[e] > 0 ? v : y[e];
+      for (int e = 0; e < N; e += 2) {
+        const Pair x{y[e], y[e + 1]}, low = mul2(x, both(a.rep));
+        Pair q = quotient(x, both(-a.rep), both(a.rep_inv));
+        if (rare) q = Pair{divide_one(x.x, a.rep), divide_one(x.y, a.rep)};
+        Pair v{x.x > 0.0f ? q.x : low.x, x.y > 0.0f ? q.y : low.y};
+        v = add2(add2(v, Pair{less[e], less[e + 1]}), both(-a.pres));  // a - b as a + (-b): the same rounding
+        y[e] = used >> e & 1u ? v.x : x.x;
+        y[e + 1] = used >> (e + 1) & 1u ? v.y : x.y;
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[e] = __fadd_rn(y[e], bias[e]);
-      y[e] = allow >> e & 1u ? y[e] : -INFINITY;
+    for (int e = 0; e < N; e += 2) {
+      const Pair v = add2(Pair{y[e], y[e + 1]}, Pair{bias[e], bias[e + 1]});
+      y[e] = allow >> e & 1u ? v.x : -INFINITY;
+      y[e + 1] = allow >> (e + 1) & 1u ? v.y : -INFINITY;
     }
     if (out) {
-      if constexpr (VEC == 4) {
-        if (on(0)) __stcs(reinterpret_cast<float4*>(out), make_float4(y[0], y[1], y[2], y[3]));
-      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (on(e)) __stcs(out + e * kStep, y[e]);
-      }
+      for (int e = 0; e < N; e += VEC)
+        if (whole || on(e)) {
+          if constexpr (VEC == 4) __stcs(reinterpret_cast<float4*>(out + place(e)), make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]));
+          else __stcs(out + place(e), y[e]);
+        }
       out += a.V;
     }
     if constexpr (kChoice) {
-      if (VEC == 1 || !on(3)) {
+      if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < N; ++e)
           if (!on(e)) y[e] = -INFINITY;
       }
-      const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));  // NaN is left out
+      float top = y[0];
+#pragma unroll
+      for (int e = 1; e < N; ++e) top = fmaxf(top, y[e]);  // NaN is left out
       const uint32_t key = choice_key(top), most = __reduce_max_sync(0xffffffffu, key);
-      // the lowest token with that value: with VEC = 4 it is the lowest lane's
-      const uint32_t with = __ballot_sync(0xffffffffu, key == most);
-      const bool mine = VEC == 1 ? key == most : lane == __ffs(with) - 1;
-      uint32_t at = ~0u;
-      if (mine) at = first + (y[0] == top ? 0 : y[1] == top ? kStep : y[2] == top ? 2 * kStep : 3 * kStep);
-      if (VEC == 1) at = __reduce_min_sync(0xffffffffu, at);
-      if (VEC == 1 ? lane == 0 : mine) row_best[r][i >> 5] = most ? ((unsigned long long)most << 32) | (uint32_t)~at : 0ull;
+      uint32_t at = ~0u;  // the lowest token with that value
+      if (key == most) {
+#pragma unroll
+        for (int e = N - 1; e >= 0; --e)
+          if (y[e] == top) at = v0 + place(e);
+      }
+      at = __reduce_min_sync(0xffffffffu, at);
+      if (lane == 0) row_best[r][i >> 5] = most ? ((unsigned long long)most << 32) | (uint32_t)~at : 0ull;
     }
   }
   if constexpr (!kChoice) return;
@@ -372,9 +406,11 @@ nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* cou
                          : (argmax_opt ? adjust_kernel<4, false, true> : adjust_kernel<4, false, false>))
                   : (pen ? (argmax_opt ? adjust_kernel<1, true, true> : adjust_kernel<1, true, false>)
                          : (argmax_opt ? adjust_kernel<1, false, true> : adjust_kernel<1, false, false>));
-  // Rows per CTA: as many as leave every SM its four CTAs.
+  // Rows per CTA: as many as leave every SM its three CTAs, alike in all groups.
   const int chunks = (V + kAdjChunk - 1) / kAdjChunk;
-  a.group = (int)std::min<int64_t>(kAdjRows, std::max<int64_t>(1, (int64_t)chunks * B / (4 * device_sm_count())));
+  const int64_t most = std::min<int64_t>(kAdjRows, std::max<int64_t>(1, (int64_t)chunks * B / (3 * device_sm_count())));
+  const int groups = (int)((B + most - 1) / most);
+  a.group = (B + groups - 1) / groups;
   const dim3 grid(chunks, (B + a.group - 1) / a.group);
   NT_CUDA_TRY(launch_kernel(kern, grid, dim3(kAdjThreads), 0, reinterpret_cast<cudaStream_t>(stream), true, a));
   return check_launch("adjust_kernel");
