@@ -67,14 +67,20 @@ struct TaShape {
   static constexpr int kSlot = kTaKeys * D * 2;            // bytes of a ring slot: one tile's keys or values
   // Tensor-memory columns: the accumulator, the query terms, a buffer of scores and one of weights for
   // each group. Where they do not fit (fp32 queries, D = 128) the smallest query term is a
-  // shared-memory operand (51 cycles per MMA instead of 32) and the groups share the scores' buffer,
-  // which is in use for half of a tile's time; sharing the weights' buffer instead made every tile
-  // wait for the products of the one before (39.5 us at 25 nodes over 26K).
-  static constexpr int kPCols = kTermsP * (kTaKeys / 2);
-  static constexpr bool kTight = D + kTermsQ * D / 2 + 2 * kTaKeys + 2 * kPCols > kTaTmemCols;
+  // shared-memory operand (51 cycles per MMA instead of 32), and the weights' terms, which the MMAs read
+  // smallest first, take turns in four places of one term each: tile j + 1's go where tile j's have
+  // been read, down to the largest. (One buffer of scores and two of weights took 38.4 us at 25
+  // nodes over 26K, one of weights and two of scores 39.5.)
+  static constexpr int kTermCols = kTaKeys / 2;
+  static constexpr bool kTight = D + kTermsQ * D / 2 + 2 * kTaKeys + 2 * kTermsP * kTermCols > kTaTmemCols;
   static constexpr int kTermsQT = kTermsQ - (kTight ? 1 : 0);  // query terms in tensor memory
-  static constexpr int kSBufs = kTight ? 1 : 2;
-  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + kSBufs * kTaKeys;
+  static constexpr int kPlaces = kTight ? 4 : 2 * kTermsP;     // of weight terms
+  static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + 2 * kTaKeys;
+  static_assert(!kTight || kTermsP == 3, "the turns of the places");
+  // Columns of term t (0 the largest) of tile j's weights.
+  __device__ static __forceinline__ int weights(int j, int t) {
+    return kColP + kTermCols * (kTight ? (3 * j + 2 - t) & 3 : (j & 1) * kTermsP + t);
+  }
   static constexpr int kLowBytes = kTight ? 128 * D * 2 : 0;
   // Ring and query term take 192 KB for either D: a second CTA on an SM would only wait for the first
   // one's tensor memory (with 96 KB at D = 64 a call behind another took 368 us instead of 220).
@@ -92,7 +98,7 @@ struct TaShape {
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
   static constexpr int kSmem = kStages * kSlot + kLowBytes + 1024;  // and alignment
   static_assert(kQSlot >= kTaFirst, "the queries' staging slots are filled after them");
-  static_assert(kColP + 2 * kPCols <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kColP + kPlaces * kTermCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
 
@@ -338,13 +344,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   constexpr int kDims = D / 2;          // dimensions of a row that one thread looks after outside the tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 11];
+  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 13];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
   __shared__ float s_m[128], s_l[2][128];
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
   const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16;
-  const uint32_t qfull = sfree0 + 16, flushed = qfull + 8, drain = flushed + 8;
+  const uint32_t readmost0 = sfree0 + 16, qfull = readmost0 + 16, flushed = qfull + 8, drain = flushed + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
@@ -362,6 +368,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       bar_init(sfull0 + 8 * b, 1);
       bar_init(pfull0 + 8 * b, 4);  // the warps of the tile's group
       bar_init(sfree0 + 8 * b, 4);
+      bar_init(readmost0 + 8 * b, 1);
       bar_init(pvdone0 + 8 * b, 1);
     }
     bar_init(qfull, kTaSoftmax / 32);
@@ -426,11 +433,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const int k = ring_key(j);
         ok = wait(full(k), turn(k));
-        const int last = j - S::kSBufs;
-        if (ok && last >= 0) ok = wait(sfree0 + 8 * (last & 1), (last >> 1) & 1);  // the buffer's last scores have been taken
+        if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
         if (!ok) break;
         tm_fence_after();
-        const uint32_t d = tmem + S::kColS + (j % S::kSBufs) * kTaKeys;
+        const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
         const uint64_t bd = sdesc(slot(k), 16);
         // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
@@ -461,14 +467,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
         if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
         tm_fence_after();
-        const uint32_t p = tmem + S::kColP + (j & 1) * S::kPCols;
         const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
 #pragma unroll
-        for (int t = S::kTermsP - 1; t >= 0; --t)
+        for (int t = S::kTermsP - 1; t >= 0; --t) {
+          const uint32_t p = tmem + S::weights(j, t);
 #pragma unroll
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, p + t * (kTaKeys / 2) + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
+            mma_tmem_a(tmem + S::kColO, p + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
                        t < S::kTermsP - 1 || kk > 0 || !fresh);
+          if (S::kTight && t == 1) mma_commit(readmost0 + 8 * (j & 1));
+        }
         mma_commit(pvdone0 + 8 * (j & 1));
         mma_commit(empty(k));
       }
@@ -579,7 +587,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
     };
-    const uint32_t pcol = tl + S::kColP + group * S::kPCols;
+    auto room = [&](int j) {  // for tile j's weights: what stood in their places has been read
+      if (!S::kTight) {
+        if (j >= 2) done(j - 2);
+      } else if (j >= 1) {  // all but the largest term of the tile before, and so everything before that
+        ok = ok && bar_wait_warp(readmost0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns);
+        tm_fence_after();
+      }
+    };
     for (int j = group; j < n; j += 2) {
       const int t = t0 + j;
       const bool tree = t >= a.pre_tiles;
@@ -587,7 +602,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       tm_fence_after();
       float s[kCols];
       if (ok && !idle) {
-        tm_load(tl + S::kColS + (j % S::kSBufs) * kTaKeys + c0, s);
+        tm_load(tl + S::kColS + group * kTaKeys + c0, s);
       } else {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
@@ -681,9 +696,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
             for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
           }
-          if (ch == 0 && j >= 2) done(j - 2);  // the group's last weights must have been read
+          if (ch == 0) room(j);
 #pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(pcol + tt * (kTaKeys / 2) + (c0 + ch) / 2, w[tt]);
+          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(tl + S::weights(j, tt) + (c0 + ch) / 2, w[tt]);
         }
         l += ls.x + ls.y;
         if constexpr (DUP > 1) {  // the keys that other lanes weigh
@@ -691,11 +706,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int tt = 0; tt < S::kTermsP; ++tt)
 #pragma unroll
             for (int c = 0; c < kTaKeys / 2; c += 8)
-              if (c / (kCols / 2) != part) tm_store(pcol + tt * (kTaKeys / 2) + c, zero);
+              if (c / (kCols / 2) != part) tm_store(tl + S::weights(j, tt) + c, zero);
         }
       }
       // An idle warp also waits for its group's last products: its arrival below must not count for them.
-      if (idle && j >= 2) done(j - 2);
+      if (idle) room(j);
       if (restart) flush(j, pend);
       tm_st_wait();
       tm_fence_before();
