@@ -187,9 +187,9 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lead) {
   d |= (uint64_t)2 << 61;  // 128-byte swizzle
   return d;
 }
-// kind::f16, A = B = bf16, D = fp32, M = 128, N = n; B K-major, or with the reduction along rows.
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_rows) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// kind::f16, A = B = bf16, D = fp32, M = 128, N = n; B K-major, or with the reduction along rows; A's sign turned.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_rows, bool minus_a = false) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (minus_a ? 1u << 13 : 0u) | (b_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -300,27 +300,36 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
 }
-// Two values as pairs of bf16 terms, term t of both in w[t]: with three terms the leading 8, next
-// 8 and last 8 bits of the significand, cut off one after the other, so nothing is lost (a value
-// below 2^-110 aside); otherwise each term is the rest so far, rounded.
+// The bf16 pair in w less two values: w.lo - x, w.hi - y, each one rounding (here exact).
+__device__ __forceinline__ float2 less2(uint32_t w, float x, float y) {
+  float2 r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n sub.f32.bf16 %0, l, %3;\n sub.f32.bf16 %1, h, %4;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(w), "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two values as pairs of bf16 terms, term t of both in w[t], the second one with its sign turned: with
+// three terms the leading 8, next 8 and last 8 bits of the significand, cut off one after the other, so
+// nothing is lost (a value below 2^-110 aside); with two, each the rest so far, rounded. (With masks and
+// fp32 differences in place of less2, the half-rate logic operations bound the softmax.)
 template <int N>
 __device__ __forceinline__ void split(float x, float y, uint32_t (&w)[N]) {
   if constexpr (N == 3) {
-    const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
-    w[0] = prmt(ux, uy, 0x7632u);
-    // differences as x - h = fma(h, -1, x)
-    const float2 neg = make_float2(-1.0f, -1.0f);
-    const float2 r = fma2(make_float2(high_f(ux), high_f(uy)), neg, make_float2(x, y));
+    w[0] = prmt(__float_as_uint(x), __float_as_uint(y), 0x7632u);
+    const float2 r = less2(w[0], x, y);  // - the rest
     w[1] = prmt(__float_as_uint(r.x), __float_as_uint(r.y), 0x7632u);
-    const float2 q = fma2(make_float2(high_f(__float_as_uint(r.x)), high_f(__float_as_uint(r.y))), neg, r);
+    const float2 q = less2(w[1], r.x, r.y);  // the rest's rest
     w[2] = prmt(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632u);
   } else {
-#pragma unroll
-    for (int t = 0; t < N; ++t) {
-      w[t] = pack_rn(x, y);
-      x -= low_f(w[t]);
-      y -= high_f(w[t]);
-    }
+    static_assert(N == 2, "terms");
+    w[0] = pack_rn(x, y);
+    const float2 r = less2(w[0], x, y);
+    w[1] = pack_rn(r.x, r.y);
   }
 }
 // Whether a word holds a bf16 that is not finite.
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const uint32_t p = tmem + S::weights(j, t);
 #pragma unroll
           for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, p + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true),
+            mma_tmem_a(tmem + S::kColO, p + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true, t == 1),
                        t < S::kTermsP - 1 || kk > 0 || !fresh);
           if (S::kTight && t == 1) mma_commit(readmost0 + 8 * (j & 1));
         }
@@ -517,8 +526,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             split(__uint_as_float(u.z), __uint_as_float(u.w), y);
 #pragma unroll
             for (int t = 0; t < S::kTermsQ; ++t) {
-              w[t][2 * e] = x[t];
-              w[t][2 * e + 1] = y[t];
+              const uint32_t sign = t == 1 ? 0x80008000u : 0u;
+              w[t][2 * e] = x[t] ^ sign;
+              w[t][2 * e + 1] = y[t] ^ sign;
             }
           }
         } else {
@@ -641,10 +651,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         for (int c = 0; c < kCols; ++c)
           if (!(seen >> c & 1)) s[c] = -INFINITY;
       }
-      float mx4[4] = {s[0], s[1], s[2], s[3]};
+      float mx2[2] = {s[0], s[1]};
 #pragma unroll
-      for (int c = 4; c < kCols; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
+      for (int c = 2; c + 1 < kCols; c += 2) mx2[c >> 1 & 1] = max3(mx2[c >> 1 & 1], s[c], s[c + 1]);
+      const float mx = fmaxf(mx2[0], mx2[1]) * a.scale_log2;
       if (S::kFlush > 0 && group == 1 && j > 1 && (j - 1) % kF == 0) {  // the other group's tile starts afresh
         flush(j - 1, 1.0f);
         tm_fence_before();
