@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         *reinterpret_cast<uint4*>(stage + (e * kAtOnce + lane / kVecs) * S::kQPitch + lane % kVecs * 16) = v[e];
       __syncwarp();
       const uint4* own = reinterpret_cast<const uint4*>(stage + lane * S::kQPitch);
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < kDims; c += 16) {
         uint32_t w[S::kTermsQ][8];
         if constexpr (sizeof(T) == 4) {
@@ -569,7 +569,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // After a wait that ran out a warp keeps walking the tiles, as the other group's turns need it,
     // and leaves the rest out.
     bool ok = true;
-    auto done = [&](int j) {  // tile j's products have been added
+    // Tile j's products have been added. A parity tells a phase from the next one only, so a caller
+    // knows of tile j - 2 before it asks for j: room(j) leaves tile j - 2's known.
+    auto done = [&](int j) {
       ok = ok && bar_wait_warp(pvdone0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
       tm_fence_after();
     };
@@ -674,6 +676,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (restart) {
               pend = corr;
             } else if (j > 0) {
+              if (j > 1) done(j - 2);  // room(j - 2) told of j - 4
               done(j - 1);
 #pragma unroll 1
               for (int c = 0; ok && c < D; c += 16) {

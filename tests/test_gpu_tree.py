@@ -399,6 +399,36 @@ def test_attention_many_heads():
     check_attend(3, 320, 2, 128, 70, 0, "f32")     # 160 query heads share one
 
 
+def attend_64(q, k, v, prefix, row0, sees):
+    """_tree.attend for many heads at a time."""
+    (B, Hq, D), Hkv = q.shape, k.shape[0]
+    rows = torch.cat([torch.arange(prefix, device=DEV), torch.arange(row0, row0 + B, device=DEV)])
+    seen = torch.cat([torch.ones(B, prefix, dtype=torch.bool, device=DEV), dev(sees)], dim=1)
+    qd = q.double().view(B, Hkv, Hq // Hkv, D)
+    s = torch.einsum("bhgd,htd->hgbt", qd, k[:, rows].double()) / D ** 0.5
+    w = s.masked_fill(~seen, float("-inf")).softmax(-1)
+    return f64(torch.einsum("hgbt,htd->bhgd", w, v[:, rows].double()).reshape(B, Hq, D))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B", [2, 40, 70, 133])
+@pytest.mark.parametrize("kind", ["random", "rise"])
+def test_attention_many_tiles_to_a_block(B, D, kind):
+    """A head to a block (more heads than SMs), so that one block walks every tile count about the
+    points where the accumulator is taken to registers; also with a maximum that keeps rising."""
+    Hkv = 160
+    for tiles in (1, 2, 3, 7, 8, 9, 10, 15, 16, 17, 18, 24, 25):
+        prefix = max(0, 64 * tiles - 64 * ((B + 63) // 64) - (tiles % 3) * 9)
+        q, k, v = attn_inputs(B, Hkv, Hkv, D, prefix, 0, "f32", seed=tiles)
+        if kind == "rise":
+            ramp = torch.linspace(0, 10, k.shape[1], device=DEV)
+            k = (k * 0.1 + ramp[None, :, None] * q.mean(0)[:, None] / q.mean(0).norm(dim=-1)[:, None, None]).bfloat16()
+        sees = _tree.ancestors(_tree.parents(np.random.RandomState(tiles), B))
+        out = run_attend(q, k, v, prefix, prefix, sees, runs=2)
+        want = attend_64(q, k, v, prefix, prefix, sees)
+        within(f64(out), want, attn_bound(q, k, v, prefix, sees, "f32", want), (kind, tiles))
+
+
 def test_attention_chain_matches_the_chain_call():
     q, k, v = attn_inputs(6, 32, 8, 128, 700, 0, "f32", tail=0)
     sees = np.tril(np.ones((6, 6), bool))
