@@ -6,7 +6,9 @@
 // (c, s) = amplitude * (cos, sin)(p * inv_freq[i]); the other dimensions pass through.
 //
 // Every value is read once and written once (queries to q_out, keys and values rounded to bf16
-// into the cache), so the kernel is bound by memory for many tokens and by the launch for few.
+// into the cache), so the kernel is bound by memory for many tokens and by the launch for few:
+// 8,191 tokens of 32 + 8 heads of 128 (fp32, 369 MB) take 64.6 us = 5.7 TB/s, 84 % of the measured
+// copy rate; one such token 2.1 us and 64 of them in bf16 2.5 us in a replayed graph.
 #include <cuda_bf16.h>
 
 #include <algorithm>

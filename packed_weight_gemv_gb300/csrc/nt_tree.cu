@@ -2,7 +2,9 @@
 // nodes' parents, acceptance of the longest drafted path that agrees with the model ("The
 // Neutrino Engine", § "The 0.6B model does not get to decide", with a tree of drafts in place
 // of one chain), and the move of the accepted rows behind the sequence's in every layer's cache.
-// All three are small; their time is the launch and a few dependent steps.
+// All three are small; their time is the launch and a few dependent steps: in a replayed graph
+// acceptance takes 1.5 us for a chain of 8 and 1.9 for 256 nodes, the move of 5 rows in 36 layers 2.0
+// and of 20 rows 3.3 (5.9 MB read and written).
 #include <algorithm>
 
 #include "nt_tree.cuh"
