@@ -1,0 +1,494 @@
+// nt_tree_few.cu -- attention of a drafted token tree with few query rows: single tokens and small
+// trees, up to 32 rows B * Hq / Hkv per key-value head (the formula and the rules on what a node sees
+// are the same as for more rows).
+//
+// With the query rows on the M side of tcgen05.mma, 128 of them to a tile, few rows cost the tensor
+// pipe as much as 128 do: 0.88 us per 64 keys for fp32 queries, above the 0.7 us that a CTA's share of
+// the memory rate takes. So the products are turned: keys are the M side of the scores, 128 to a
+// tile, dimensions the M side of the weighted values, and the rows the N side -- all terms of all
+// rows together, so the three terms of an fp32 query or weight are columns of one product, summed in
+// registers, instead of three products.
+//
+//   S[key][term, row] = K q      O[dim][term, row] = V^T p      (A and B from shared memory)
+//
+// A thread is a key of the scores and a dimension of the sums. Its weights go to shared memory, 8
+// rows of a term to a 16-byte store, and each tile's sums come back to registers, where they are
+// rounded to nearest: the tensor core, which cuts its sums off, adds 128 keys at most.
+//
+// CTA (384 threads): a key-value head, a range of 64-key tiles taken in pairs.
+//   warps 0, 3     -- TMA copies of keys and of values, a ring each;
+//   warps 1, 2     -- the scores' MMAs, the sums';
+//   warps 4-7, 8-11 - two groups, each with every other pair of tiles, a maximum, sum and accumulator of
+//                     its own, so they meet only at the end. The maxima are raised when a score of any row
+//                     exceeds its maximum by 2^8.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "nt_tree_attn.cuh"
+
+namespace nt {
+namespace {
+
+constexpr int kTfKeys = 2 * kTaKeys;    // keys of a pair of tiles
+constexpr float kTfLowest = -3.0e38f;   // reference of a row that has seen nothing (its weights are 0)
+
+constexpr int up16(int n) { return (n + 15) / 16 * 16; }
+
+template <typename T, int D, int RP>
+struct TfShape {
+  static constexpr int kTermsQ = sizeof(T) == 4 ? 3 : 1;
+  static constexpr int kTermsP = sizeof(T) == 4 ? 3 : 2;
+  static constexpr int kNQ = up16(kTermsQ * RP), kNP = up16(kTermsP * RP);  // columns: term * RP + row
+  static constexpr int kSlot = kTfKeys * D * 2;                   // a pair's keys or values
+  static constexpr int kBlock = kTfKeys * 128;                    // bytes of 64 columns of weights, or 64 dimensions
+  static constexpr int kP = (kNP + 63) / 64 * kBlock, kQ = kNQ * D * 2;
+  static constexpr int kSlots = (222 * 1024 - 2 * kP - kQ) / kSlot;
+  static constexpr int kKeySlots = (kSlots + 1) / 2, kValSlots = kSlots / 2;
+  static constexpr int kAtV = kKeySlots * kSlot, kAtP = kSlots * kSlot, kAtQ = kAtP + 2 * kP;
+  static constexpr int kSmem = kAtQ + kQ + 1024;                  // and alignment
+  static constexpr int kColS = 0, kColO = 2 * kNQ;                // tensor-memory columns, one of each per group
+  static_assert(kValSlots >= 2 && 2 * (kNQ + kNP) <= kTaTmemCols, "ring and tensor memory");
+  static_assert(2 * RP * D * 4 <= kSlots * kSlot, "the sums are staged in the ring");
+};
+
+__host__ __device__ constexpr uint32_t idesc_few(int n, bool rows) {  // both operands K-major, or both with the reduction along rows
+  return (1u << 4) | (1u << 7) | (1u << 10) | (rows ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tm_ld8(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8]; tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(addr)
+      : "memory");
+}
+// The terms' columns of 8 rows, summed from the smallest on; the second term's sign is turned.
+template <int TERMS, int RP>
+__device__ __forceinline__ void tm_terms8(uint32_t addr, float (&x)[8]) {
+  float hi[8];
+  if constexpr (TERMS == 1) {
+    tm_ld8(addr, x);
+  } else {
+    float mid[8];
+    tm_ld8(addr + RP, mid);
+    if constexpr (TERMS == 3) {
+      tm_ld8(addr + 2 * RP, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] -= mid[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = -mid[e];
+    }
+    tm_ld8(addr, hi);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += hi[e];
+  }
+}
+__device__ __forceinline__ float warp_max(float x) {  // NaN left out
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Whether any thread of a group says so.
+__device__ __forceinline__ bool group_any(int group, bool x) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(1 + group)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int group) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+
+template <typename T, int D, int RP>
+__global__ void __launch_bounds__(kTaThreads, 1)
+    tree_few_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
+  using S = TfShape<T, D, RP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bars[2 * S::kSlots + 10];
+  __shared__ uint32_t tmem_slot, s_mask[RP];
+  __shared__ int s_fail, s_bad;
+  __shared__ __align__(16) float s_nm[2][RP];  // minus a group's reference maxima (log2 units)
+  __shared__ float s_w[2][4][RP];  // a warp's largest scores; at the end its sums
+  const uint32_t keyfull = smem_u32(bars), keyempty = keyfull + 8 * S::kKeySlots;
+  const uint32_t valfull = keyempty + 8 * S::kKeySlots, valempty = valfull + 8 * S::kValSlots;
+  const uint32_t sfull0 = valempty + 8 * S::kValSlots, sfree0 = sfull0 + 16, pfull0 = sfree0 + 16, pvdone0 = pfull0 + 16;
+  const uint32_t qfull = pvdone0 + 16, drain = qfull + 8;
+  volatile int* fail = &s_fail;
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+
+  const int unit = blockIdx.x, g = unit / a.nsplit, sp = unit % a.nsplit;
+  const int t0 = (int)((int64_t)a.tiles * sp / a.nsplit), n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
+  const int pairs = (n + 1) / 2;
+
+  if (i == 0) {
+    for (int s = 0; s < 2 * S::kSlots; ++s) bar_init(smem_u32(bars) + 8 * s, 1);
+    for (int b = 0; b < 2; ++b) {
+      bar_init(sfull0 + 8 * b, 1);
+      bar_init(sfree0 + 8 * b, 4);  // the warps of the group
+      bar_init(pfull0 + 8 * b, 4);
+      bar_init(pvdone0 + 8 * b, 1);
+    }
+    bar_init(qfull, kTaSoftmax / 32);
+    bar_init(drain, 2);
+    s_fail = 0;
+    s_bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (i < 2 * RP) s_nm[i / RP][i % RP] = -kTfLowest;
+  if (warp == kTaScore) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(kTaTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // The set-up above overlaps the previous kernel; nothing below reads an input before its end.
+  dependent_launch_wait();
+
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+
+  if (warp == kTaKeyLoad || warp == kTaValueLoad) {
+    if (elect_one()) {
+      const bool val = warp == kTaValueLoad;
+      const int slots = val ? S::kValSlots : S::kKeySlots;
+      const uint32_t full = val ? valfull : keyfull, empty = val ? valempty : keyempty;
+      const uint32_t at = smem_u32(ring) + (val ? S::kAtV : 0);
+      int j = 0;
+      for (; j < pairs && !a.fault; ++j) {
+        const int k = j % slots;
+        if (j >= slots && !wait(empty + 8 * k, (j / slots - 1) & 1)) break;
+        if (j >= 1 && !wait(qfull, 0)) break;  // the queries before all but the first copies
+        bar_expect_tx(full + 8 * k, S::kSlot);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = t0 + 2 * j + u;
+          const bool tree = t >= a.pre_tiles;
+          const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
+          // past the CTA's last tile: rows beyond the tree's, which read as zeros
+          const int y = 2 * j + u < n ? (tree ? t - a.pre_tiles : t) * kTaKeys : tree ? 4 * kTreeMaxNodes : a.prefix;
+#pragma unroll
+          for (int x = 0; x < D; x += 64) tma_3d(at + k * S::kSlot + x / 64 * S::kBlock + u * (kTaKeys * 128), map, x, y, g, full + 8 * k);
+        }
+      }
+      // every copy must land before the CTA may exit
+      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+      for (int d = max(0, j - slots); d < j; ++d)
+        while (!bar_try(full + 8 * (d % slots), (d / slots) & 1))
+          if (globaltimer_ns() > deadline) break;
+    }
+    __syncwarp();
+  } else if (warp == kTaScore) {
+    if (elect_one()) {
+      bool ok = wait(qfull, 0);
+      tm_fence_after();
+      for (int j = 0; ok && j < pairs; ++j) {
+        const int k = j % S::kKeySlots;
+        ok = wait(keyfull + 8 * k, (j / S::kKeySlots) & 1);
+        if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
+        if (!ok) break;
+        tm_fence_after();
+        const uint64_t ad = sdesc(smem_u32(ring) + k * S::kSlot, 16), bd = sdesc(smem_u32(ring) + S::kAtQ, 16);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_smem_a(tmem + S::kColS + (j & 1) * S::kNQ, ad + ((kk >> 2) * S::kBlock + (kk & 3) * 32) / 16,
+                     bd + ((kk >> 2) * (S::kNQ * 128) + (kk & 3) * 32) / 16, idesc_few(S::kNQ, false), kk > 0);
+        mma_commit(sfull0 + 8 * (j & 1));
+        mma_commit(keyempty + 8 * k);
+      }
+      mma_commit(drain);
+    }
+    __syncwarp();
+  } else if (warp == kTaValue) {
+    if (elect_one()) {
+      for (int j = 0; j < pairs; ++j) {
+        const int k = j % S::kValSlots;
+        if (!wait(valfull + 8 * k, (j / S::kValSlots) & 1) || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
+        tm_fence_after();
+        // with 64 dimensions the second half of the M side reads them again
+        const uint64_t ad = sdesc(smem_u32(ring) + S::kAtV + k * S::kSlot, D == 128 ? S::kBlock : 0);
+        const uint64_t bd = sdesc(smem_u32(ring) + S::kAtP + (j & 1) * S::kP, S::kBlock);
+#pragma unroll
+        for (int kk = 0; kk < kTfKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each block
+          mma_smem_a(tmem + S::kColO + (j & 1) * S::kNP, ad + kk * 2048 / 16, bd + kk * 2048 / 16, idesc_few(S::kNP, true), kk > 0);
+        mma_commit(pvdone0 + 8 * (j & 1));
+        mma_commit(valempty + 8 * k);
+      }
+      mma_commit(drain);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, group = (warp - kTaFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // key, dimension
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    {  // the query terms: rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
+      const int idx = i - 32 * kTaFirstSoftmax;
+      if (idx < RP) s_mask[idx] = idx < a.R ? a.mask[(int64_t)node_of(idx, a.inv_g) * a.words] : 0u;
+      uint8_t* qs = ring + S::kAtQ;
+#pragma unroll
+      for (int e = idx; e < RP * (D / 8); e += kTaSoftmax) {
+        const int r = e / (D / 8), c = e % (D / 8), b = node_of(r, a.inv_g);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c * 8;
+        uint32_t w[S::kTermsQ][4];
+        if constexpr (sizeof(T) == 4) {
+          float4 v[2] = {};
+          if (r < a.R) {
+            v[0] = reinterpret_cast<const float4*>(q)[0];
+            v[1] = reinterpret_cast<const float4*>(q)[1];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[3], y[3];
+            split(v[h].x, v[h].y, x);
+            split(v[h].z, v[h].w, y);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              w[t][2 * h] = x[t];
+              w[t][2 * h + 1] = y[t];
+            }
+          }
+        } else {
+          const uint4 v = r < a.R ? *reinterpret_cast<const uint4*>(q) : make_uint4(0u, 0u, 0u, 0u);
+          w[0][0] = v.x; w[0][1] = v.y; w[0][2] = v.z; w[0][3] = v.w;
+        }
+#pragma unroll
+        for (int t = 0; t < S::kTermsQ; ++t) {
+          const int nr = t * RP + r;
+          *reinterpret_cast<uint4*>(qs + (c >> 3) * (S::kNQ * 128) + nr * 128 + (((c & 7) ^ (nr & 7)) * 16)) =
+              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive_warp(qfull, lane);
+      asm volatile("bar.sync 3, 256;" ::: "memory");  // s_mask
+    }
+    float acc[RP];  // dimension ln of the rows' weighted sums
+    float2 l[RP / 2];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) acc[r] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < RP / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
+    uint8_t* prow = ring + S::kAtP + group * S::kP + ln * 128;  // this key's weights
+    const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+    // After a wait that ran out a warp keeps walking the tiles, as its group's barriers need it.
+    bool ok = true;
+    auto take = [&](int j) {  // pair j's sums to registers
+      ok = ok && bar_wait_warp(pvdone0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
+      tm_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < RP; c += 8) {
+          float o[8];
+          tm_terms8<S::kTermsP, RP>(tl + S::kColO + group * S::kNP + c, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[c + e] += o[e];
+        }
+      }
+    };
+    for (int j = group; j < pairs; j += 2) {
+      ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
+      tm_fence_after();
+      float s[RP];
+#pragma unroll
+      for (int c = 0; c < RP; c += 8) {
+        float x[8] = {};
+        if (ok) tm_terms8<S::kTermsQ, RP>(tl + S::kColS + group * S::kNQ + c, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[c + e] = x[e];
+      }
+      tm_fence_before();
+      if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
+      {  // what the rows see of this key
+        const int t = t0 + 2 * j + (ln >> 6), key = ln & 63;
+        uint32_t seen = 0u;
+        if (t - t0 < n) {
+          if (t < a.pre_tiles) {
+            if (key < a.prefix - t * kTaKeys) seen = ~0u;
+          } else if (key < a.B) {  // all of the tree is one tile
+#pragma unroll
+            for (int r = 0; r < RP; ++r) seen |= (s_mask[r] >> key & 1u) << r;
+          }
+        }
+        if (seen != ~0u) {
+#pragma unroll
+          for (int r = 0; r < RP; ++r)
+            if (!(seen >> r & 1u)) s[r] = -INFINITY;
+        }
+      }
+      const int tree = a.pre_tiles - t0 - 2 * j;  // which half is the tree's
+      if (tree < 2 && tree >= 0 && a.pre_tiles < t0 + n) {  // take its values that are not finite out of the product
+        const int k = j % S::kValSlots;
+        ok = ok && bar_wait_warp(valfull + 8 * k, (j / S::kValSlots) & 1, fail, a.timeout_ns);
+        bool bad = false;
+        for (int e = ln; ok && e < a.B * (D / 8); e += 128) {
+          const int row = e / (D / 8), c = e % (D / 8);
+          uint4* p = reinterpret_cast<uint4*>(ring + S::kAtV + k * S::kSlot + (c >> 3) * S::kBlock + (tree * kTaKeys + row) * 128 + (c & 7) * 16);
+          const uint4 v = *p;
+          if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
+            uint16_t* h = reinterpret_cast<uint16_t*>(p);
+            for (int x = 0; x < 8; ++x)
+              if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
+            bad = true;
+          }
+        }
+        if (bad) s_bad = 1;
+      }
+      if (j >= 2) take(j - 2);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < RP; r += 2) {
+        const float2 x = fma2(make_float2(s[r], s[r + 1]), sc, *reinterpret_cast<const float2*>(&s_nm[group][r]));
+        mx = max3(mx, x.x, x.y);
+      }
+      if (group_any(group, mx > kTaLazy)) {
+        float mine = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float w = warp_max(s[r]);
+          if (lane == r) mine = w;
+        }
+        if (lane < RP) s_w[group][quarter][lane] = mine;
+        group_sync(group);
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float top = fmaxf(fmaxf(s_w[group][0][r], s_w[group][1][r]), fmaxf(s_w[group][2][r], s_w[group][3][r]));
+          const float old = -s_nm[group][r], to = fmaxf(old, top * a.scale_log2);
+          const float corr = old == to ? 1.0f : ex2(old - to);
+          acc[r] *= corr;
+          if (r & 1) l[r / 2].y *= corr;
+          else l[r / 2].x *= corr;
+          if (ln == r) mine = to;
+        }
+        group_sync(group);
+        if (ln < RP) s_nm[group][ln] = -mine;
+        group_sync(group);
+      }
+#pragma unroll
+      for (int c = 0; c < RP; c += 8) {
+        uint32_t w[S::kTermsP][4];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const int r = c + e;
+          const float2 x = fma2(make_float2(s[r], s[r + 1]), sc, *reinterpret_cast<const float2*>(&s_nm[group][r]));
+          const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+          l[r / 2] = add2(l[r / 2], pp);
+          uint32_t term[S::kTermsP];
+          split(pp.x, pp.y, term);
+#pragma unroll
+          for (int t = 0; t < S::kTermsP; ++t) w[t][e / 2] = term[t];
+        }
+#pragma unroll
+        for (int t = 0; t < S::kTermsP; ++t) {
+          const int q = (t * RP + c) / 8;  // 8 columns: a 16-byte piece
+          *reinterpret_cast<uint4*>(prow + (q >> 3) * S::kBlock + (((q & 7) ^ (ln & 7)) * 16)) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tm_fence_before();
+      if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
+    }
+    if (pairs > group) take(group + (pairs - 1 - group) / 2 * 2);
+    ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
+    tm_fence_after();
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    // the sums, staged in the ring (every copy and MMA has finished by then)
+    float* st = reinterpret_cast<float*>(ring) + group * RP * D;
+    if (ok && ln < D) {
+#pragma unroll
+      for (int r = 0; r < RP; ++r) st[r * D + ln] = acc[r];
+    }
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      float x = r & 1 ? l[r / 2].y : l[r / 2].x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) s_w[group][quarter][r] = x;
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (warp == kTaScore)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
+  if (*fail) {
+    if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
+    return;
+  }
+  // join the groups; a split's sum goes to the workspace, a whole one to the output
+  const float* st = reinterpret_cast<const float*>(ring);
+  for (int e = i; e < a.R * (D / 4); e += kTaThreads) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4, b = node_of(r, a.inv_g);
+    const float M = -fminf(s_nm[0][r], s_nm[1][r]);
+    float L = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const float m = -s_nm[d][r], w = m == M ? 1.0f : ex2(m - M);
+      const float4 x = *reinterpret_cast<const float4*>(st + (d * RP + r) * D + c);
+      L = fmaf((s_w[d][0][r] + s_w[d][1][r]) + (s_w[d][2][r] + s_w[d][3][r]), w, L);
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
+    }
+    if (s_bad) {  // tree values that are not finite, for the nodes that see them
+      for (int k = 0; k < a.B; ++k) {
+        if (!(s_mask[r] >> k & 1u)) continue;
+        const uint2 v = *reinterpret_cast<const uint2*>(a.vtree + (int64_t)g * a.head_stride + (int64_t)k * D + c);
+        if (!isfinite(low_f(v.x))) o.x += low_f(v.x);
+        if (!isfinite(high_f(v.x))) o.y += high_f(v.x);
+        if (!isfinite(low_f(v.y))) o.z += low_f(v.y);
+        if (!isfinite(high_f(v.y))) o.w += high_f(v.y);
+      }
+    }
+    if (a.nsplit > 1) {
+      const int64_t at = (int64_t)unit * RP + r;
+      *reinterpret_cast<float4*>(a.part + at * D + c) = o;
+      if (c == 0) a.ml[at] = make_float2(M, L);
+    } else {
+      const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
+      const int64_t at = ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
+    }
+  }
+}
+
+// ---- host -----------------------------------------------------------------------------------
+template <typename T, int D, int RP>
+nt_status launch_few(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
+  static std::atomic<int> attr_set[64];  // per device: the ring's dynamic shared memory allowed
+  int dev = 0;
+  NT_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return set_error(NT_ERR_CUDA, "device index out of range");
+  constexpr int smem = TfShape<T, D, RP>::kSmem;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    NT_CUDA_TRY(cudaFuncSetAttribute(tree_few_kernel<T, D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    attr_set[dev].store(1, std::memory_order_release);
+  }
+  const unsigned units = (unsigned)(a.Hq / a.G * a.nsplit);
+  NT_CUDA_TRY(launch_kernel(tree_few_kernel<T, D, RP>, dim3(units), dim3(kTaThreads), smem, st, true, maps, a));
+  return check_launch("tree_few_kernel");
+}
+template <typename T, int D>
+nt_status launch_few_rows(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
+  return a.R <= 8 ? launch_few<T, D, 8>(maps, a, st) : a.R <= 16 ? launch_few<T, D, 16>(maps, a, st) : launch_few<T, D, 32>(maps, a, st);
+}
+
+}  // namespace
+
+nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st) {
+  if (dtype == NT_F32) return D == 64 ? launch_few_rows<float, 64>(maps, a, st) : launch_few_rows<float, 128>(maps, a, st);
+  return D == 64 ? launch_few_rows<uint16_t, 64>(maps, a, st) : launch_few_rows<uint16_t, 128>(maps, a, st);
+}
+
+}  // namespace nt
