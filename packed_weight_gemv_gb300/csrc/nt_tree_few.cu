@@ -57,34 +57,60 @@ __host__ __device__ constexpr uint32_t idesc_few(int n, bool rows) {  // both op
   return (1u << 4) | (1u << 7) | (1u << 10) | (rows ? 3u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void tm_ld8(uint32_t addr, float* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8]; tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-      : "r"(addr)
-      : "memory");
-}
-// The terms' columns of 8 rows, summed from the smallest on; the second term's sign is turned.
+// The terms' columns of 8 rows, summed from the smallest on; the second term's sign is turned. One wait for
+// all the loads, in one statement with them: registers of a load on its way must not be moved or spilled.
 template <int TERMS, int RP>
 __device__ __forceinline__ void tm_terms8(uint32_t addr, float (&x)[8]) {
-  float hi[8];
   if constexpr (TERMS == 1) {
-    tm_ld8(addr, x);
+    asm volatile(
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        " tcgen05.wait::ld.sync.aligned;"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+        : "r"(addr)
+        : "memory");
   } else {
     float mid[8];
-    tm_ld8(addr + RP, mid);
     if constexpr (TERMS == 3) {
-      tm_ld8(addr + 2 * RP, x);
+      float low[8];
+      asm volatile(
+          " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%24];\n"
+          " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n"
+          " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n"
+          " tcgen05.wait::ld.sync.aligned;"
+          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7]), "=f"(low[0]), "=f"(low[1]), "=f"(low[2]), "=f"(low[3]), "=f"(low[4]), "=f"(low[5]), "=f"(low[6]), "=f"(low[7])
+          : "r"(addr), "r"(addr + RP), "r"(addr + 2 * RP)
+          : "memory");
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] -= mid[e];
+      for (int e = 0; e < 8; ++e) mid[e] -= low[e];
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = -mid[e];
+      asm volatile(
+          " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+          " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
+          " tcgen05.wait::ld.sync.aligned;"
+          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7])
+          : "r"(addr), "r"(addr + RP)
+          : "memory");
     }
-    tm_ld8(addr, hi);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += hi[e];
+    for (int e = 0; e < 8; ++e) x[e] -= mid[e];
   }
+}
+// Sums of N values (8, 16 or 32 of them) over a warp: lane r gets value r's, and lanes N on repeat them. Half of the values go
+// to the other half of the lanes at every step.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int e = 0; e < o; ++e) {
+      const float send = up ? v[e] : v[e + o], keep = up ? v[e + o] : v[e];
+      v[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
 }
 __device__ __forceinline__ float warp_max(float x) {  // NaN left out
   float r;
@@ -117,6 +143,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   __shared__ uint32_t tmem_slot, s_mask[RP];
   __shared__ int s_fail, s_bad;
   __shared__ __align__(16) float s_nm[2][RP];  // minus a group's reference maxima (log2 units)
+  __shared__ __align__(16) float s_corr[2][RP];  // what a raise of them scales sums by
   __shared__ float s_w[2][4][RP];  // a warp's largest scores; at the end its sums
   const uint32_t keyfull = smem_u32(bars), keyempty = keyfull + 8 * S::kKeySlots;
   const uint32_t valfull = keyempty + 8 * S::kKeySlots, valempty = valfull + 8 * S::kValSlots;
@@ -169,7 +196,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (; j < pairs && !a.fault; ++j) {
         const int k = j % slots;
         if (j >= slots && !wait(empty + 8 * k, (j / slots - 1) & 1)) break;
-        if (j >= 1 && !wait(qfull, 0)) break;  // the queries before all but the first copies
         bar_expect_tx(full + 8 * k, S::kSlot);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -235,22 +261,26 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const int idx = i - 32 * kTaFirstSoftmax;
       if (idx < RP) s_mask[idx] = idx < a.R ? a.mask[(int64_t)node_of(idx, a.inv_g) * a.words] : 0u;
       uint8_t* qs = ring + S::kAtQ;
+      constexpr int kAll = RP * (D / 8), kPer = (kAll + kTaSoftmax - 1) / kTaSoftmax;  // pieces of 8 dimensions
+      uint4 v[kPer][sizeof(T) / 2];
 #pragma unroll
-      for (int e = idx; e < RP * (D / 8); e += kTaSoftmax) {
-        const int r = e / (D / 8), c = e % (D / 8), b = node_of(r, a.inv_g);
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c * 8;
+      for (int p = 0; p < kPer; ++p) {
+        const int e = idx + p * kTaSoftmax, r = e / (D / 8), b = node_of(r, a.inv_g);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + e % (D / 8) * 8;
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+          v[p][h] = r < a.R ? reinterpret_cast<const uint4*>(q)[h] : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        const int e = idx + p * kTaSoftmax, r = e / (D / 8), c = e % (D / 8);
         uint32_t w[S::kTermsQ][4];
         if constexpr (sizeof(T) == 4) {
-          float4 v[2] = {};
-          if (r < a.R) {
-            v[0] = reinterpret_cast<const float4*>(q)[0];
-            v[1] = reinterpret_cast<const float4*>(q)[1];
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t x[3], y[3];
-            split(v[h].x, v[h].y, x);
-            split(v[h].z, v[h].w, y);
+            split(__uint_as_float(v[p][h].x), __uint_as_float(v[p][h].y), x);
+            split(__uint_as_float(v[p][h].z), __uint_as_float(v[p][h].w), y);
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
               w[t][2 * h] = x[t];
@@ -258,14 +288,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
           }
         } else {
-          const uint4 v = r < a.R ? *reinterpret_cast<const uint4*>(q) : make_uint4(0u, 0u, 0u, 0u);
-          w[0][0] = v.x; w[0][1] = v.y; w[0][2] = v.z; w[0][3] = v.w;
+          w[0][0] = v[p][0].x; w[0][1] = v[p][0].y; w[0][2] = v[p][0].z; w[0][3] = v[p][0].w;
         }
+        if (e < kAll) {
 #pragma unroll
-        for (int t = 0; t < S::kTermsQ; ++t) {
-          const int nr = t * RP + r;
-          *reinterpret_cast<uint4*>(qs + (c >> 3) * (S::kNQ * 128) + nr * 128 + (((c & 7) ^ (nr & 7)) * 16)) =
-              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+          for (int t = 0; t < S::kTermsQ; ++t) {
+            const int nr = t * RP + r;
+            *reinterpret_cast<uint4*>(qs + (c >> 3) * (S::kNQ * 128) + nr * 128 + (((c & 7) ^ (nr & 7)) * 16)) =
+                make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -359,19 +390,21 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
         if (lane < RP) s_w[group][quarter][lane] = mine;
         group_sync(group);
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          const float top = fmaxf(fmaxf(s_w[group][0][r], s_w[group][1][r]), fmaxf(s_w[group][2][r], s_w[group][3][r]));
-          const float old = -s_nm[group][r], to = fmaxf(old, top * a.scale_log2);
-          const float corr = old == to ? 1.0f : ex2(old - to);
-          acc[r] *= corr;
-          if (r & 1) l[r / 2].y *= corr;
-          else l[r / 2].x *= corr;
-          if (ln == r) mine = to;
+        if (ln < RP) {
+          const float top = fmaxf(fmaxf(s_w[group][0][ln], s_w[group][1][ln]), fmaxf(s_w[group][2][ln], s_w[group][3][ln]));
+          const float old = -s_nm[group][ln], to = fmaxf(old, top * a.scale_log2);
+          s_corr[group][ln] = old == to ? 1.0f : ex2(old - to);
+          s_nm[group][ln] = -to;
         }
         group_sync(group);
-        if (ln < RP) s_nm[group][ln] = -mine;
-        group_sync(group);
+#pragma unroll
+        for (int r = 0; r < RP; r += 2) {
+          const float2 corr = *reinterpret_cast<const float2*>(&s_corr[group][r]);
+          acc[r] *= corr.x;
+          acc[r + 1] *= corr.y;
+          l[r / 2].x *= corr.x;
+          l[r / 2].y *= corr.y;
+        }
       }
 #pragma unroll
       for (int c = 0; c < RP; c += 8) {
@@ -407,13 +440,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
       for (int r = 0; r < RP; ++r) st[r * D + ln] = acc[r];
     }
+    float sums[RP];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      float x = r & 1 ? l[r / 2].y : l[r / 2].x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == 0) s_w[group][quarter][r] = x;
+    for (int r = 0; r < RP; r += 2) {
+      sums[r] = l[r / 2].x;
+      sums[r + 1] = l[r / 2].y;
     }
+    const float sum = warp_sums(sums, lane);
+    if (lane < RP) s_w[group][quarter][lane] = sum;
   }
   tm_fence_before();
   __syncthreads();
