@@ -657,17 +657,22 @@ TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
   p.tiles = p.pre_tiles + (B + kTaKeys - 1) / kTaKeys;
   const int64_t groups = (int64_t)Hkv * p.mtiles;
   // Splits as the GPU holds them, but few enough that what the join spends on one more is worth the tiles it
-  // takes off the others: about a seventh of a tile's time (one query head group over 12,000 keys, D 64: 152
-  // splits 17.7 us, 64 10.9, 32 9.9; over 32,000, D 128: 152 splits 24.2 us, 64 19.2, 32 23.3).
+  // takes off the others. In units of about a seventh of a tile's time (few rows: a quarter of a pair of tiles')
+  // the join takes one for a split and its launch 20 (12). Measured: one key-value head of 20 rows over 12,000 keys, D 64:
+  // 152 splits 17.7 us, 64 10.9, 32 9.9; one row group of 4 over 200 keys unsplit 5.3 us, in 5 parts 5.9; over 1,500
+  // keys in 7 parts 6.3, in 13 6.7, in 2 8.9.
+  const bool few = R <= kTaFewRows;
   const int most = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, kTaFill / groups));
+  const int at_once = few ? 2 : 1, step = few ? 4 : 7, launch = few ? 12 : 20;
   p.nsplit = most;
-  for (int per = (p.tiles + most - 1) / most, best = INT_MAX; per <= p.tiles; ++per) {
-    const int n = (p.tiles + per - 1) / per, cost = 20 * per + 3 * n;
+  for (int steps = ((p.tiles + most - 1) / most + at_once - 1) / at_once, best = INT_MAX; step * steps < best; ++steps) {
+    const int n = std::min(most, (p.tiles + at_once * steps - 1) / (at_once * steps));
+    const int cost = step * steps + n + (n > 1 ? launch : 0);
     if (cost < best) {
       best = cost;
       p.nsplit = n;
     }
-    if (20 * per >= best) break;
+    if (n == 1) break;
   }
   p.units = groups * p.nsplit;
   return p;
