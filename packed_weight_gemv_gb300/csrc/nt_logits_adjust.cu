@@ -27,6 +27,7 @@ constexpr int kAdjPer = 8;                  // tokens per thread
 constexpr int kAdjChunk = kAdjPer * kAdjThreads;
 constexpr int kAdjRows = 16;                // rows of a group at most
 constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
+constexpr int kAdjFew = 64;                 // used tokens of a warp's 256 that are adjusted one by one
 static_assert(kTreeMaxNodes <= kAdjThreads, "one thread per node");
 
 // Workspace: the 16-byte status header, then per row the best (value, index) key and, in the first row
@@ -106,6 +107,12 @@ __device__ __forceinline__ uint32_t choice_key(float y) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <int N>
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
@@ -122,6 +129,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   __shared__ int path_node[kTreeMaxNodes], path_tok[kTreeMaxNodes];  // the tree's tokens inside the chunk
   __shared__ uint32_t path_rows[kTreeMaxNodes];                      // bit r: on the path of the group's row r
   __shared__ int n_path, s_last;
+  __shared__ int2 used_list[kPenalties ? kAdjThreads / 32 : 1][kAdjFew];  // (place, bit 16: on a path; count)
   __shared__ unsigned long long row_best[kAdjRows][kAdjThreads / 32];
   dependent_launch_wait();
   const int i = threadIdx.x, lane = i & 31, v0 = blockIdx.x * kAdjChunk;
@@ -199,11 +207,26 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   const bool row_counts = a.counts && a.counts_stride != 0, row_bias = a.bias && a.bias_stride != 0;
   if (a.counts && !row_counts) load(a.counts + v0, c, 0);
   if (a.bias && !row_bias) load(a.bias + v0, bias, -0.0f);
-  bool on_path = false;  // a token is on some path of the group
+  uint32_t on_path = 0;  // bit e: token e is on some path of the group
   for (int p = 0; p < np; ++p)
 #pragma unroll
-    for (int e = 0; e < N; ++e) on_path |= path_tok[p] == place(e);
-  const bool warp_path = __any_sync(0xffffffffu, on_path);
+    for (int e = 0; e < N; ++e) on_path |= (uint32_t)(path_tok[p] == place(e)) << e;
+  const bool warp_path = __any_sync(0xffffffffu, on_path != 0);
+  // Most warps have a few used tokens, the same ones in every row: those are listed and adjusted in
+  // shared memory, a lane each, before the row is read.
+  int listed = -1;  // -1: too many, or other ones in every row
+  if (kPenalties && !row_counts) {
+    listed = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const bool mine = c[e] > 0 || (on_path >> e & 1u);
+      const uint32_t all = __ballot_sync(0xffffffffu, mine);
+      const int at = listed + __popc(all & ((1u << lane) - 1u));
+      if (mine && at < kAdjFew) used_list[i >> 5][at] = make_int2(place(e) | (int)(on_path >> e & 1u) << 16, c[e]);
+      listed += __popc(all);
+    }
+    if (listed > kAdjFew) listed = -1;
+  }
   float less[N];      // - frequency * count
   uint32_t used = 0;  // bit e: token e has been used
   auto count = [&](const int(&n)[N]) {
@@ -218,7 +241,24 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
 
   for (int r = 0; r < nb; ++r) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdjAhead - 1) : "memory");  // this row is here
-    const float* st = ring[r % kAdjAhead];
+    float* st = ring[r % kAdjAhead];
+    if (kPenalties && listed > 0) {
+      __syncwarp();  // the other lanes' copies (and the list)
+      for (int k = lane; k < listed; k += 32) {
+        const int2 t = used_list[i >> 5][k];
+        const int at = t.x & 0xffff;
+        int n = t.y;
+        if (t.x >> 16)
+          for (int p = 0; p < np; ++p) n += path_tok[p] == at ? (int)(path_rows[p] >> r & 1u) : 0;
+        if (n > 0) {
+          const float x = st[at];
+          float v = x > 0.0f ? __fdiv_rn(x, a.rep) : __fmul_rn(x, a.rep);
+          v = __fsub_rn(__fsub_rn(v, __fmul_rn(a.freq, __int2float_rn(n))), a.pres);
+          st[at] = v;
+        }
+      }
+      __syncwarp();
+    }
     float y[N];
 #pragma unroll
     for (int e = 0; e < N; e += VEC) {
@@ -239,7 +279,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
     load_allowed(r + 1);
     fetch(r + kAdjAhead);
     if (row_bias) load(a.bias + (b0 + r) * a.bias_stride + v0, bias, -0.0f);
-    if constexpr (kPenalties) {
+    if (kPenalties && listed < 0) {
       if (row_counts || warp_path) {
         int n[N];
         if (row_counts) load(a.counts + (b0 + r) * a.counts_stride + v0, n, 0);
@@ -286,9 +326,10 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
         for (int e = 0; e < N; ++e)
           if (!on(e)) y[e] = -INFINITY;
       }
-      float top = y[0];
+      float tops[2] = {y[0], y[1]};  // NaN is left out
 #pragma unroll
-      for (int e = 1; e < N; ++e) top = fmaxf(top, y[e]);  // NaN is left out
+      for (int e = 2; e < N; e += 2) tops[e >> 1 & 1] = max3(tops[e >> 1 & 1], y[e], y[e + 1]);
+      const float top = fmaxf(tops[0], tops[1]);
       const uint32_t key = choice_key(top), most = __reduce_max_sync(0xffffffffu, key);
       uint32_t at = ~0u;  // the lowest token with that value
       if (key == most) {
