@@ -25,6 +25,7 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kAdjPer = 8;                  // tokens per thread
 constexpr int kAdjChunk = kAdjPer * kAdjThreads;
+constexpr int kAdjPerSm = 4;                // CTAs that an SM holds (64 registers a thread; asking the compiler for 4 cost 2 us)
 constexpr int kAdjRows = 16;                // rows of a group at most
 constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
 constexpr int kAdjFew = 64;                 // used tokens of a warp's 256 that are adjusted one by one
@@ -169,25 +170,6 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   load_allowed(0);
   float* out = a.out ? a.out + (int64_t)b0 * a.V + v0 : nullptr;
 
-  int np = 0;
-  if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
-    if (i == 0) n_path = 0;
-    __syncthreads();
-    const int t = i < a.B ? a.tokens[i] : -1;
-    if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
-      const int at = atomicAdd(&n_path, 1);
-      path_node[at] = i;
-      path_tok[at] = t - v0;
-      path_rows[at] = 0u;
-    }
-    __syncthreads();
-    np = n_path;
-    for (int x = i; x < np * nb; x += kAdjThreads) {
-      const int p = x / nb, r = x - p * nb, node = path_node[p];
-      if (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (node >> 5)) >> (node & 31) & 1u) atomicOr(&path_rows[p], 1u << r);
-    }
-    __syncthreads();
-  }
   auto load = [&](const auto* row, auto(&x)[N], auto none) {  // this thread's part of a row of counts or biases
 #pragma unroll
     for (int e = 0; e < N; e += VEC) {
@@ -207,23 +189,51 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   const bool row_counts = a.counts && a.counts_stride != 0, row_bias = a.bias && a.bias_stride != 0;
   if (a.counts && !row_counts) load(a.counts + v0, c, 0);
   if (a.bias && !row_bias) load(a.bias + v0, bias, -0.0f);
+  int np = 0;
+  if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
+    if (i == 0) n_path = 0;
+    __syncthreads();
+    const int t = i < a.B ? a.tokens[i] : -1;
+    if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
+      const int at = atomicAdd(&n_path, 1);
+      path_node[at] = i;
+      path_tok[at] = t - v0;
+      path_rows[at] = 0u;
+    }
+    __syncthreads();
+    np = n_path;
+    for (int x = i; x < np * nb; x += kAdjThreads) {
+      const int p = x / nb, r = x - p * nb, node = path_node[p];
+      if (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (node >> 5)) >> (node & 31) & 1u) atomicOr(&path_rows[p], 1u << r);
+    }
+    __syncthreads();
+  }
   uint32_t on_path = 0;  // bit e: token e is on some path of the group
-  for (int p = 0; p < np; ++p)
-#pragma unroll
-    for (int e = 0; e < N; ++e) on_path |= (uint32_t)(path_tok[p] == place(e)) << e;
+  for (int p = 0; p < np; ++p) {
+    const int t = path_tok[p], own = VEC == 4 ? t / 4 % kAdjThreads : t % kAdjThreads;
+    const int e = VEC == 4 ? t / (4 * kAdjThreads) * 4 + t % 4 : t / kAdjThreads;
+    if (own == i) on_path |= 1u << e;
+  }
   const bool warp_path = __any_sync(0xffffffffu, on_path != 0);
   // Most warps have a few used tokens, the same ones in every row: those are listed and adjusted in
   // shared memory, a lane each, before the row is read.
   int listed = -1;  // -1: too many, or other ones in every row
   if (kPenalties && !row_counts) {
-    listed = 0;
+    uint32_t mine = on_path;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const bool mine = c[e] > 0 || (on_path >> e & 1u);
-      const uint32_t all = __ballot_sync(0xffffffffu, mine);
-      const int at = listed + __popc(all & ((1u << lane) - 1u));
-      if (mine && at < kAdjFew) used_list[i >> 5][at] = make_int2(place(e) | (int)(on_path >> e & 1u) << 16, c[e]);
-      listed += __popc(all);
+    for (int e = 0; e < N; ++e) mine |= (uint32_t)(c[e] > 0) << e;
+    int at = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int before = __shfl_up_sync(0xffffffffu, at, o);
+      at += lane >= o ? before : 0;
+    }
+    listed = __shfl_sync(0xffffffffu, at, 31);
+    at -= __popc(mine);
+    if (listed <= kAdjFew && mine) {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (mine >> e & 1u) used_list[i >> 5][at++] = make_int2(place(e) | (int)(on_path >> e & 1u) << 16, c[e]);
     }
     if (listed > kAdjFew) listed = -1;
   }
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
       used |= (uint32_t)(n[e] > 0) << e;
     }
   };
-  count(c);
+  if (listed < 0) count(c);
 
   for (int r = 0; r < nb; ++r) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdjAhead - 1) : "memory");  // this row is here
@@ -447,10 +457,11 @@ nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* cou
                          : (argmax_opt ? adjust_kernel<4, false, true> : adjust_kernel<4, false, false>))
                   : (pen ? (argmax_opt ? adjust_kernel<1, true, true> : adjust_kernel<1, true, false>)
                          : (argmax_opt ? adjust_kernel<1, false, true> : adjust_kernel<1, false, false>));
-  // Rows per CTA: as many as leave every SM its three CTAs, alike in all groups.
+  // Groups of rows: as many as one wave of CTAs holds, alike, or whole waves of them where a group would have
+  // too many rows (64 rows of 151,936, 75 chunks, 608 CTAs at a time, in a graph: 7 groups 18.5 us, 8 16.1, 10 18.6).
   const int chunks = (V + kAdjChunk - 1) / kAdjChunk;
-  const int64_t most = std::min<int64_t>(kAdjRows, std::max<int64_t>(1, (int64_t)chunks * B / (3 * device_sm_count())));
-  const int groups = (int)((B + most - 1) / most);
+  const int wave = std::max(1, kAdjPerSm * device_sm_count() / chunks), least = (B + kAdjRows - 1) / kAdjRows;
+  const int groups = std::min(B, (least + wave - 1) / wave * wave);
   a.group = (B + groups - 1) / groups;
   const dim3 grid(chunks, (B + a.group - 1) / a.group);
   NT_CUDA_TRY(launch_kernel(kern, grid, dim3(kAdjThreads), 0, reinterpret_cast<cudaStream_t>(stream), true, a));

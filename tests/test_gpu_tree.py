@@ -297,6 +297,28 @@ def test_adjust_ties_nans_and_infinities(V):
     assert np.array_equal(y[:6], x[:6], equal_nan=True) and y[6, 5] == -np.inf
 
 
+@pytest.mark.parametrize("V", [6144, 6145])
+@pytest.mark.parametrize("every", [1, 2, 3, 4, 5, 40])
+def test_adjust_however_many_tokens_are_used(V, every):
+    """From all tokens to a few: the kernel lists a few used tokens and works on all of them otherwise."""
+    rs = np.random.RandomState(every)
+    B = 9
+    x = (rs.randn(B, V) * 4).astype(np.float32)
+    counts = np.where(np.arange(V) % every == 0, 1 + rs.randint(0, 3, V), 0).astype(np.int32)
+    sees = _tree.ancestors(_tree.parents(rs, B))
+    tokens = rs.randint(0, V, B).astype(np.int32)
+    tokens[3:6] = tokens[0]  # the same token on several nodes, some of a path
+    full = np.stack([counts + np.bincount(tokens[s], minlength=V) for s in sees]).astype(np.int32)
+    want = _tree.adjust(x, full, 1.3, 0.25, -0.5, None, None, np.float32)
+    out = torch.empty(B, V, device=DEV)
+    arg = torch.empty(B, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(nt.nt_logits_adjust_workspace_size(V, B), dtype=torch.uint8, device=DEV)
+    nt.nt_logits_adjust(dev(x), counts=dev(counts), tree_mask=dev(_tree.pack(sees)), tokens=dev(tokens), repetition=1.3,
+                        frequency=0.25, presence=-0.5, out=out, argmax=arg, ws=ws)
+    assert np.array_equal(host(out), want)
+    assert np.array_equal(host(arg), _tree.choice(want))
+
+
 @pytest.mark.parametrize("rep", [1.1, 1.0, 1.25, 3.0, 0.7, 1.9999999, 1e-5, 7e4, 1e-30, 1e30])
 def test_adjust_quotients_are_rounded(rep):
     """Every significand of one binade, and values of any size, divided as IEEE division does."""
