@@ -9,9 +9,12 @@
 // their way and the instructions per value are few. A CTA holds a chunk of 2,048 tokens -- their
 // counts and biases, when the batch shares them, in registers -- and walks a group of rows over it;
 // the rows' values come through shared memory by asynchronous copies, up to four rows ahead.
-// The penalties are straight-line code for every value, two values to an instruction: with a branch
-// around them nearly every warp took it for each of a lane's tokens (a chunk has a few used tokens, a
-// text's first chunks hundreds), and a row cost 240 instructions per 128 values.
+// Of a warp's 256 tokens a few have been used, in a text's first chunks hundreds. A few are listed and
+// adjusted in shared memory, a lane each; for more the penalties are straight-line code for every
+// value, two values to an instruction (with a branch around them nearly every warp took it for each of
+// a lane's tokens). 64 rows of 151,936 with all adjustments (80 MB): 240 instructions per 128 values 32.5
+// us, straight-line for all 24.7, listed 21.6, groups of rows that fill one wave 19.4 = 4.1 TB/s, 61 % of
+// the measured copy rate; instruction issue and the start of the CTAs (counts, paths) bound it.
 #include <math.h>
 #include <string.h>
 
@@ -127,7 +130,7 @@ template <int VEC, bool kPenalties, bool kChoice>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   constexpr int N = kAdjPer;
   __shared__ __align__(16) float ring[kAdjAhead][kAdjChunk];         // rows on their way
-  __shared__ int path_node[kTreeMaxNodes], path_tok[kTreeMaxNodes];  // the tree's tokens inside the chunk
+  __shared__ int path_tok[kTreeMaxNodes];                            // the tree's tokens inside the chunk
   __shared__ uint32_t path_rows[kTreeMaxNodes];                      // bit r: on the path of the group's row r
   __shared__ int n_path, s_last;
   __shared__ int2 used_list[kPenalties ? kAdjThreads / 32 : 1][kAdjFew];  // (place, bit 16: on a path; count)
@@ -191,22 +194,22 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   if (a.bias && !row_bias) load(a.bias + v0, bias, -0.0f);
   int np = 0;
   if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
+    const int t = i < a.B ? __ldg(a.tokens + i) : -1;
+    uint32_t rows = 0;
+    if (i < a.B) {
+#pragma unroll
+      for (int r = 0; r < kAdjRows; ++r)
+        if (r < nb) rows |= (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (i >> 5)) >> (i & 31) & 1u) << r;
+    }
     if (i == 0) n_path = 0;
     __syncthreads();
-    const int t = i < a.B ? a.tokens[i] : -1;
     if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
       const int at = atomicAdd(&n_path, 1);
-      path_node[at] = i;
       path_tok[at] = t - v0;
-      path_rows[at] = 0u;
+      path_rows[at] = rows;
     }
     __syncthreads();
     np = n_path;
-    for (int x = i; x < np * nb; x += kAdjThreads) {
-      const int p = x / nb, r = x - p * nb, node = path_node[p];
-      if (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (node >> 5)) >> (node & 31) & 1u) atomicOr(&path_rows[p], 1u << r);
-    }
-    __syncthreads();
   }
   uint32_t on_path = 0;  // bit e: token e is on some path of the group
   for (int p = 0; p < np; ++p) {
