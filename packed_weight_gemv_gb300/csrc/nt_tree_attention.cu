@@ -93,7 +93,9 @@ struct TaShape {
 __device__ __forceinline__ int ring_key(int j) { return j < 2 ? j : 2 * j - 2; }
 __device__ __forceinline__ int ring_val(int j, int n) { return min(2 * j + 3, n + j); }
 
-template <typename T, int D, int DUP>
+// kShares: the CTA takes an equal share of all tiles, which may touch several tiles of rows; otherwise a
+// split of one of them. (One code for both, with the loop over pieces, took 39.1 us instead of 36.0 at 25 nodes over 26K.)
+template <typename T, int D, int DUP, bool kShares>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_attn_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
   using S = TaShape<T, D>;
@@ -102,39 +104,43 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   constexpr int kDims = D / 2;          // dimensions of a row that one thread looks after outside the tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t bars[2 * S::kStages + 13];
+  constexpr int kBars = 2 * S::kStages + 13;
+  constexpr int kPieces = kShares ? kTaPieces : 1;
+  __shared__ __align__(8) uint64_t bars[kPieces][kBars];
   __shared__ uint32_t tmem_slot;
   __shared__ int s_fail, s_bad;
   __shared__ float s_m[128], s_l[2][128];
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
-  const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16;
-  const uint32_t readmost0 = sfree0 + 16, qfull = readmost0 + 16, flushed = qfull + 8, drain = flushed + 8;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
-
-  const int unit = blockIdx.x;
-  const int mt = unit % a.mtiles, sp = unit / a.mtiles % a.nsplit, g = unit / a.mtiles / a.nsplit;
-  const int t0 = (int)((int64_t)a.tiles * sp / a.nsplit), n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
-  const int rows = min(kRows, a.R - mt * kRows);
-
+  int id = 0, g, mt, t0, n;  // tile of rows among those of all heads; its head, place, first tile of keys, tiles
+  bool last = true;
+  auto locate = [&](int piece) {
+    if constexpr (kShares) {
+      const int64_t work = (int64_t)a.groups * a.tiles, end = work * (blockIdx.x + 1) / gridDim.x, from = work * blockIdx.x / gridDim.x;
+      const int id0 = (int)(from / a.tiles);
+      id = id0 + piece;
+      g = id / a.mtiles;
+      mt = id % a.mtiles;
+      t0 = piece == 0 ? (int)(from - (int64_t)id0 * a.tiles) : 0;
+      n = (int)min(end - (int64_t)id * a.tiles, (int64_t)a.tiles) - t0;
+      last = (int64_t)(id + 1) * a.tiles >= end;
+    } else {
+      const int unit = blockIdx.x, sp = unit / a.mtiles % a.nsplit;
+      g = unit / a.mtiles / a.nsplit;
+      mt = unit % a.mtiles;
+      t0 = (int)((int64_t)a.tiles * sp / a.nsplit);
+      n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
+    }
+  };
+  locate(0);
+  for (int x = i; x < kPieces * kBars; x += kTaThreads) {
+    const int b = x % kBars - 2 * S::kStages;  // the groups' four warps arrive at pfull, sfree and flushed, all eight at qfull
+    bar_init(smem_u32(bars) + 8 * x, b == 2 || b == 3 || b == 6 || b == 7 || b == 11 ? 4 : b == 10 ? kTaSoftmax / 32 : b == 12 ? 2 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   if (i == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      bar_init(full0 + 8 * s, 1);
-      bar_init(empty0 + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      bar_init(sfull0 + 8 * b, 1);
-      bar_init(pfull0 + 8 * b, 4);  // the warps of the tile's group
-      bar_init(sfree0 + 8 * b, 4);
-      bar_init(readmost0 + 8 * b, 1);
-      bar_init(pvdone0 + 8 * b, 1);
-    }
-    bar_init(qfull, kTaSoftmax / 32);
-    bar_init(flushed, 4);
-    bar_init(drain, 2);
     s_fail = 0;
     s_bad = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (i < 128) s_m[i] = -INFINITY;
   if (warp == kTaScore) {
@@ -150,408 +156,425 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   // The set-up above overlaps the previous kernel; nothing below reads an input before its end.
   dependent_launch_wait();
 
-  auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
-  auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
-  auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
-  auto slot = [&](int k) { return smem_u32(ring + (k % S::kStages) * S::kSlot); };
-  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+  // Each piece of a share has barriers of its own.
+  for (int piece = 0;; ++piece) {
+    const uint32_t full0 = smem_u32(bars[piece]), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
+    const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16;
+    const uint32_t readmost0 = sfree0 + 16, qfull = readmost0 + 16, flushed = qfull + 8, drain = flushed + 8;
+    const int rows = min(kRows, a.R - mt * kRows);
 
-  if (warp == kTaKeyLoad || warp == kTaValueLoad) {
-    if (elect_one()) {
-      const bool val = warp == kTaValueLoad;
-      int j = 0;
-      for (; j < n && !a.fault; ++j) {
-        const int k = val ? ring_val(j, n) : ring_key(j);
-        if (k >= S::kStages && !wait(empty(k), turn(k) ^ 1u)) break;
-        // The first tiles' keys and values, then the queries (which pass through the ring's end), then
-        // the rest: with the whole ring asked for at once the queries arrived 4 us later.
-        if (k >= kTaFirst && !wait(qfull, 0)) break;
-        const int t = t0 + j;
-        const bool tree = t >= a.pre_tiles;
-        const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
-        const int y = (tree ? t - a.pre_tiles : t) * kTaKeys;
-        bar_expect_tx(full(k), S::kSlot);
+    auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
+    auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
+    auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
+    auto slot = [&](int k) { return smem_u32(ring + (k % S::kStages) * S::kSlot); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+
+    if (warp == kTaKeyLoad || warp == kTaValueLoad) {
+      if (elect_one()) {
+        const bool val = warp == kTaValueLoad;
+        int j = 0;
+        for (; j < n && !a.fault; ++j) {
+          const int k = val ? ring_val(j, n) : ring_key(j);
+          if (k >= S::kStages && !wait(empty(k), turn(k) ^ 1u)) break;
+          // The first tiles' keys and values, then the queries (which pass through the ring's end), then
+          // the rest: with the whole ring asked for at once the queries arrived 4 us later.
+          if (k >= kTaFirst && !wait(qfull, 0)) break;
+          const int t = t0 + j;
+          const bool tree = t >= a.pre_tiles;
+          const CUtensorMap* map = val ? (tree ? &maps.vt : &maps.vp) : (tree ? &maps.kt : &maps.kp);
+          const int y = (tree ? t - a.pre_tiles : t) * kTaKeys;
+          bar_expect_tx(full(k), S::kSlot);
 #pragma unroll
-        for (int x = 0; x < D; x += 64) tma_3d(slot(k) + x * kTaKeys * 2, map, x, y, g, full(k));
-      }
-      // every copy must land before the CTA may exit
-      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-      for (int d = max(0, j - S::kStages); d < j; ++d) {
-        const int k = val ? ring_val(d, n) : ring_key(d);
-        if (k + S::kStages < 2 * n && *fail == 0) continue;  // its slot has been filled again since
-        while (!bar_try(full(k), turn(k)))
-          if (globaltimer_ns() > deadline) break;
-      }
-    }
-    __syncwarp();
-  } else if (warp == kTaScore) {
-    if (elect_one()) {
-      bool ok = wait(qfull, 0);
-      tm_fence_after();
-      for (int j = 0; ok && j < n; ++j) {
-        const int k = ring_key(j);
-        ok = wait(full(k), turn(k));
-        if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
-        if (!ok) break;
-        tm_fence_after();
-        const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
-        const uint64_t bd = sdesc(slot(k), 16);
-        // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
-#pragma unroll
-        for (int t = S::kTermsQ - 1; t >= 0; --t)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t b = bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16;
-            const uint32_t more = t < S::kTermsQ - 1 || kk > 0;
-            if (t < S::kTermsQT)
-              mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, b, idesc_bf16(kTaKeys, false), more);
-            else
-              mma_smem_a(d, sdesc(smem_u32(ring + S::kStages * S::kSlot), 16) + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, b,
-                         idesc_bf16(kTaKeys, false), more);
-          }
-        mma_commit(sfull0 + 8 * (j & 1));
-        mma_commit(empty(k));
-      }
-      mma_commit(drain);
-    }
-    __syncwarp();
-  } else if (warp == kTaValue) {
-    if (elect_one()) {
-      for (int j = 0; j < n; ++j) {
-        const int k = ring_val(j, n);
-        constexpr int kF = S::kFlush ? S::kFlush : 1;
-        const bool fresh = S::kFlush ? j % kF == 0 : j == 0;
-        bool ok = wait(full(k), turn(k));
-        if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
-        if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
-        tm_fence_after();
-        const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
-#pragma unroll
-        for (int t = S::kTermsP - 1; t >= 0; --t) {
-          const uint32_t p = tmem + S::weights(j, t);
-#pragma unroll
-          for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-            mma_tmem_a(tmem + S::kColO, p + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true, t == 1),
-                       t < S::kTermsP - 1 || kk > 0 || !fresh);
-          if (S::kTight && t == 1) mma_commit(readmost0 + 8 * (j & 1));
+          for (int x = 0; x < D; x += 64) tma_3d(slot(k) + x * kTaKeys * 2, map, x, y, g, full(k));
         }
-        mma_commit(pvdone0 + 8 * (j & 1));
-        mma_commit(empty(k));
+        // every copy must land before the CTA may exit
+        const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+        for (int d = max(0, j - S::kStages); d < j; ++d) {
+          const int k = val ? ring_val(d, n) : ring_key(d);
+          if (k + S::kStages < 2 * n && *fail == 0) continue;  // its slot has been filled again since
+          while (!bar_try(full(k), turn(k)))
+            if (globaltimer_ns() > deadline) break;
+        }
       }
-      mma_commit(drain);
-    }
-    __syncwarp();
-  } else {
-    const int quarter = warp & 3, group = (warp - kTaFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
-    const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
-    const int b = node_of(mt * kRows + r, a.inv_g);
-    const bool live = r < rows;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    {  // the row's query terms into tensor memory, kDims dimensions each
-      constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a part of a row; parts per load
-      uint8_t* stage = ring + S::kQSlot * S::kSlot + (warp - kTaFirstSoftmax) * 32 * S::kQPitch;
-      uint4 v[kVecs];
-#pragma unroll
-      for (int e = 0; e < kVecs; ++e) {
-        const int ri = (quarter * 32 + e * kAtOnce + lane / kVecs) % kRows, ra = mt * kRows + ri;
-        const int rb = node_of(ra, a.inv_g);
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + group * kDims;
-        v[e] = ri < rows ? reinterpret_cast<const uint4*>(q)[lane % kVecs] : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int e = 0; e < kVecs; ++e)
-        *reinterpret_cast<uint4*>(stage + (e * kAtOnce + lane / kVecs) * S::kQPitch + lane % kVecs * 16) = v[e];
       __syncwarp();
-      const uint4* own = reinterpret_cast<const uint4*>(stage + lane * S::kQPitch);
+    } else if (warp == kTaScore) {
+      if (elect_one()) {
+        bool ok = wait(qfull, 0);
+        tm_fence_after();
+        for (int j = 0; ok && j < n; ++j) {
+          const int k = ring_key(j);
+          ok = wait(full(k), turn(k));
+          if (ok && j >= 2) ok = wait(sfree0 + 8 * (j & 1), ((j >> 1) - 1) & 1);  // the group's last scores have been taken
+          if (!ok) break;
+          tm_fence_after();
+          const uint32_t d = tmem + S::kColS + (j & 1) * kTaKeys;
+          const uint64_t bd = sdesc(slot(k), 16);
+          // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
+#pragma unroll
+          for (int t = S::kTermsQ - 1; t >= 0; --t)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t b = bd + ((kk >> 2) * (kTaKeys * 128) + (kk & 3) * 32) / 16;
+              const uint32_t more = t < S::kTermsQ - 1 || kk > 0;
+              if (t < S::kTermsQT)
+                mma_tmem_a(d, tmem + S::kColQ + t * (D / 2) + 8 * kk, b, idesc_bf16(kTaKeys, false), more);
+              else
+                mma_smem_a(d, sdesc(smem_u32(ring + S::kStages * S::kSlot), 16) + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, b,
+                           idesc_bf16(kTaKeys, false), more);
+            }
+          mma_commit(sfull0 + 8 * (j & 1));
+          mma_commit(empty(k));
+        }
+        mma_commit(drain);
+      }
+      __syncwarp();
+    } else if (warp == kTaValue) {
+      if (elect_one()) {
+        for (int j = 0; j < n; ++j) {
+          const int k = ring_val(j, n);
+          constexpr int kF = S::kFlush ? S::kFlush : 1;
+          const bool fresh = S::kFlush ? j % kF == 0 : j == 0;
+          bool ok = wait(full(k), turn(k));
+          if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
+          if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
+          tm_fence_after();
+          const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
+#pragma unroll
+          for (int t = S::kTermsP - 1; t >= 0; --t) {
+            const uint32_t p = tmem + S::weights(j, t);
+#pragma unroll
+            for (int kk = 0; kk < kTaKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
+              mma_tmem_a(tmem + S::kColO, p + 8 * kk, bd + kk * 2048 / 16, idesc_bf16(D, true, t == 1),
+                         t < S::kTermsP - 1 || kk > 0 || !fresh);
+            if (S::kTight && t == 1) mma_commit(readmost0 + 8 * (j & 1));
+          }
+          mma_commit(pvdone0 + 8 * (j & 1));
+          mma_commit(empty(k));
+        }
+        mma_commit(drain);
+      }
+      __syncwarp();
+    } else {
+      const int quarter = warp & 3, group = (warp - kTaFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // tensor-memory lane
+      const int r = ln % kRows, part = ln / kRows;  // row, and which keys of a tile its lane weighs (one for a warp)
+      const int b = node_of(mt * kRows + r, a.inv_g);
+      const bool live = r < rows;
+      const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+      {  // the row's query terms into tensor memory, kDims dimensions each
+        constexpr int kVecs = S::kQRow / 16, kAtOnce = 32 / kVecs;  // 16-byte pieces of a part of a row; parts per load
+        uint8_t* stage = ring + S::kQSlot * S::kSlot + (warp - kTaFirstSoftmax) * 32 * S::kQPitch;
+        uint4 v[kVecs];
+#pragma unroll
+        for (int e = 0; e < kVecs; ++e) {
+          const int ri = (quarter * 32 + e * kAtOnce + lane / kVecs) % kRows, ra = mt * kRows + ri;
+          const int rb = node_of(ra, a.inv_g);
+          const T* q = static_cast<const T*>(a.q) + ((int64_t)rb * a.Hq + g * a.G + (ra - rb * a.G)) * D + group * kDims;
+          v[e] = ri < rows ? reinterpret_cast<const uint4*>(q)[lane % kVecs] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int e = 0; e < kVecs; ++e)
+          *reinterpret_cast<uint4*>(stage + (e * kAtOnce + lane / kVecs) * S::kQPitch + lane % kVecs * 16) = v[e];
+        __syncwarp();
+        const uint4* own = reinterpret_cast<const uint4*>(stage + lane * S::kQPitch);
 #pragma unroll 2
-      for (int c = 0; c < kDims; c += 16) {
-        uint32_t w[S::kTermsQ][8];
-        if constexpr (sizeof(T) == 4) {
+        for (int c = 0; c < kDims; c += 16) {
+          uint32_t w[S::kTermsQ][8];
+          if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 u = own[c / 4 + e];
-            uint32_t x[3], y[3];
-            split(__uint_as_float(u.x), __uint_as_float(u.y), x);
-            split(__uint_as_float(u.z), __uint_as_float(u.w), y);
+            for (int e = 0; e < 4; ++e) {
+              const uint4 u = own[c / 4 + e];
+              uint32_t x[3], y[3];
+              split(__uint_as_float(u.x), __uint_as_float(u.y), x);
+              split(__uint_as_float(u.z), __uint_as_float(u.w), y);
 #pragma unroll
-            for (int t = 0; t < S::kTermsQ; ++t) {
-              const uint32_t sign = t == 1 ? 0x80008000u : 0u;
-              w[t][2 * e] = x[t] ^ sign;
-              w[t][2 * e + 1] = y[t] ^ sign;
+              for (int t = 0; t < S::kTermsQ; ++t) {
+                const uint32_t sign = t == 1 ? 0x80008000u : 0u;
+                w[t][2 * e] = x[t] ^ sign;
+                w[t][2 * e + 1] = y[t] ^ sign;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 u = own[c / 8 + e];
+              w[0][4 * e] = u.x; w[0][4 * e + 1] = u.y; w[0][4 * e + 2] = u.z; w[0][4 * e + 3] = u.w;
             }
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint4 u = own[c / 8 + e];
-            w[0][4 * e] = u.x; w[0][4 * e + 1] = u.y; w[0][4 * e + 2] = u.z; w[0][4 * e + 3] = u.w;
+          for (int t = 0; t < S::kTermsQT; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
+          if constexpr (S::kTight) {  // rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
+            uint8_t* low = ring + S::kStages * S::kSlot + group * (128 * 128) + ln * 128;
+            const uint32_t* x = w[S::kTermsQ - 1];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(low + (((c / 8 + e) ^ (ln & 7)) * 16)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           }
         }
-#pragma unroll
-        for (int t = 0; t < S::kTermsQT; ++t) tm_st8(tl + S::kColQ + t * (D / 2) + (group * kDims + c) / 2, w[t]);
-        if constexpr (S::kTight) {  // rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
-          uint8_t* low = ring + S::kStages * S::kSlot + group * (128 * 128) + ln * 128;
-          const uint32_t* x = w[S::kTermsQ - 1];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<uint4*>(low + (((c / 8 + e) ^ (ln & 7)) * 16)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-        }
+        tm_st_wait();
+        tm_fence_before();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before MMAs that read it, copies over the staging slots
+        bar_arrive_warp(qfull, lane);
       }
-      tm_st_wait();
-      tm_fence_before();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before MMAs that read it, copies over the staging slots
-      bar_arrive_warp(qfull, lane);
-    }
-    // warps of rows past the last one only keep the barriers going (their lanes' weights are
-    // whatever the columns hold, and reach no row that is read)
-    const bool idle = r - lane >= rows;
-    const int c0 = part * kCols;  // this thread's first key of a tile
-    const uint32_t ocol = tl + S::kColO + group * kDims;  // its half of the accumulator
-    const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units) as this group knows it, its weight sum
-    constexpr int kF = S::kFlush ? S::kFlush : 1;
-    float acc[S::kFlush ? kDims : 1];
-    if constexpr (S::kFlush > 0) {
-#pragma unroll
-      for (int e = 0; e < kDims; ++e) acc[e] = 0.0f;
-    }
-    // After a wait that ran out a warp keeps walking the tiles, as the other group's turns need it,
-    // and leaves the rest out.
-    bool ok = true;
-    // Tile j's products have been added. A parity tells a phase from the next one only, so a caller
-    // knows of tile j - 2 before it asks for j: room(j) leaves tile j - 2's known.
-    auto done = [&](int j) {
-      ok = ok && bar_wait_warp(pvdone0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
-      tm_fence_after();
-    };
-    auto rescale = [&](float to) {  // what this thread holds, to another reference
-      const float corr = m == to ? 1.0f : ex2(m - to);
-      l *= corr;
+      // warps of rows past the last one only keep the barriers going (their lanes' weights are
+      // whatever the columns hold, and reach no row that is read)
+      const bool idle = r - lane >= rows;
+      const int c0 = part * kCols;  // this thread's first key of a tile
+      const uint32_t ocol = tl + S::kColO + group * kDims;  // its half of the accumulator
+      const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units) as this group knows it, its weight sum
+      constexpr int kF = S::kFlush ? S::kFlush : 1;
+      float acc[S::kFlush ? kDims : 1];
       if constexpr (S::kFlush > 0) {
 #pragma unroll
-        for (int e = 0; e < kDims; ++e) acc[e] *= corr;
+        for (int e = 0; e < kDims; ++e) acc[e] = 0.0f;
       }
-      m = to;
-      return corr;
-    };
-    auto flush = [&](int j, float corr) {  // the accumulator before tile j, times corr, into registers
-      done(j - 1);
-      if (ok && !idle) {
+      // After a wait that ran out a warp keeps walking the tiles, as the other group's turns need it,
+      // and leaves the rest out.
+      bool ok = true;
+      // Tile j's products have been added. A parity tells a phase from the next one only, so a caller
+      // knows of tile j - 2 before it asks for j: room(j) leaves tile j - 2's known.
+      auto done = [&](int j) {
+        ok = ok && bar_wait_warp(pvdone0 + 8 * (j & 1), (j >> 1) & 1, fail, a.timeout_ns);
+        tm_fence_after();
+      };
+      auto rescale = [&](float to) {  // what this thread holds, to another reference
+        const float corr = m == to ? 1.0f : ex2(m - to);
+        l *= corr;
         if constexpr (S::kFlush > 0) {
 #pragma unroll
-          for (int c = 0; c < kDims; c += 16) {
-            float o[16];
-            tm_load(ocol + c, o);
+          for (int e = 0; e < kDims; ++e) acc[e] *= corr;
+        }
+        m = to;
+        return corr;
+      };
+      auto flush = [&](int j, float corr) {  // the accumulator before tile j, times corr, into registers
+        done(j - 1);
+        if (ok && !idle) {
+          if constexpr (S::kFlush > 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], corr, acc[c + e]);
+            for (int c = 0; c < kDims; c += 16) {
+              float o[16];
+              tm_load(ocol + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], corr, acc[c + e]);
+            }
           }
         }
-      }
-    };
-    auto room = [&](int j) {  // for tile j's weights: what stood in their places has been read
-      if (!S::kTight) {
-        if (j >= 2) done(j - 2);
-      } else if (j >= 1) {  // all but the largest term of the tile before, and so everything before that
-        ok = ok && bar_wait_warp(readmost0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns);
+      };
+      auto room = [&](int j) {  // for tile j's weights: what stood in their places has been read
+        if (!S::kTight) {
+          if (j >= 2) done(j - 2);
+        } else if (j >= 1) {  // all but the largest term of the tile before, and so everything before that
+          ok = ok && bar_wait_warp(readmost0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, fail, a.timeout_ns);
+          tm_fence_after();
+        }
+      };
+      for (int j = group; j < n; j += 2) {
+        const int t = t0 + j;
+        const bool tree = t >= a.pre_tiles;
+        ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
         tm_fence_after();
-      }
-    };
-    for (int j = group; j < n; j += 2) {
-      const int t = t0 + j;
-      const bool tree = t >= a.pre_tiles;
-      ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
-      tm_fence_after();
-      float s[kCols];
-      if (ok && !idle) {
-        tm_load(tl + S::kColS + group * kTaKeys + c0, s);
-      } else {
+        float s[kCols];
+        if (ok && !idle) {
+          tm_load(tl + S::kColS + group * kTaKeys + c0, s);
+        } else {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
-      }
-      tm_fence_before();
-      if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
-      if (tree) {  // take tree values that are not finite out of the product
-        const int k = ring_val(j, n);
-        ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
-        bool bad = false;
-        for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
-          uint4* p = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
-          const uint4 v = *p;
-          if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
-            uint16_t* h = reinterpret_cast<uint16_t*>(p);
-            for (int x = 0; x < 8; ++x)
-              if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
-            bad = true;
-          }
+          for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
         }
-        if (bad) s_bad = 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
-      if (tree || left < kTaKeys) {
-        uint64_t seen = ~0ull;
-        if (tree) {
-          const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
-          seen = w[0];
-          if (left > 32) seen |= (uint64_t)w[1] << 32;
-        }
-        if (left < kTaKeys) seen &= (1ull << left) - 1;
-        if (!live) seen = 0;
-        seen >>= c0;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (!(seen >> c & 1)) s[c] = -INFINITY;
-      }
-      float mx2[2] = {s[0], s[1]};
-#pragma unroll
-      for (int c = 2; c + 1 < kCols; c += 2) mx2[c >> 1 & 1] = max3(mx2[c >> 1 & 1], s[c], s[c + 1]);
-      const float mx = fmaxf(mx2[0], mx2[1]) * a.scale_log2;
-      if (S::kFlush > 0 && group == 1 && j > 1 && (j - 1) % kF == 0) {  // the other group's tile starts afresh
-        flush(j - 1, 1.0f);
         tm_fence_before();
-        if (ok) bar_arrive_warp(flushed, lane);
-      }
-      // this tile's reference, after the one of the tile before it
-      const bool restart = S::kFlush > 0 && group == 0 && j > 0 && j % kF == 0;
-      float pend = 1.0f;  // rescaling of what this group's flush adds
-      if (j > 0) turn_wait(quarter, group);
-      if (!idle) {
-        const float known = s_m[ln];
-        if (__any_sync(0xffffffffu, known != m || mx > m + kTaLazy)) {
-          rescale(known);
-          if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
-            const float corr = rescale(fmaxf(m, mx));
-            s_m[ln] = m;
-            if (restart) {
-              pend = corr;
-            } else if (j > 0) {
-              if (j > 1) done(j - 2);  // room(j - 2) told of j - 4
-              done(j - 1);
-#pragma unroll 1
-              for (int c = 0; ok && c < D; c += 16) {
-                float o[16];
-                tm_load(tl + S::kColO + c, o);
-                uint32_t w[16];
+        if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
+        if (tree) {  // take tree values that are not finite out of the product
+          const int k = ring_val(j, n);
+          ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
+          bool bad = false;
+          for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
+            uint4* p = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
+            const uint4 v = *p;
+            if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
+              uint16_t* h = reinterpret_cast<uint16_t*>(p);
+              for (int x = 0; x < 8; ++x)
+                if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
+              bad = true;
+            }
+          }
+          if (bad) s_bad = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
+        if (tree || left < kTaKeys) {
+          uint64_t seen = ~0ull;
+          if (tree) {
+            const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
+            seen = w[0];
+            if (left > 32) seen |= (uint64_t)w[1] << 32;
+          }
+          if (left < kTaKeys) seen &= (1ull << left) - 1;
+          if (!live) seen = 0;
+          seen >>= c0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
-                tm_store(tl + S::kColO + c, w);
+          for (int c = 0; c < kCols; ++c)
+            if (!(seen >> c & 1)) s[c] = -INFINITY;
+        }
+        float mx2[2] = {s[0], s[1]};
+#pragma unroll
+        for (int c = 2; c + 1 < kCols; c += 2) mx2[c >> 1 & 1] = max3(mx2[c >> 1 & 1], s[c], s[c + 1]);
+        const float mx = fmaxf(mx2[0], mx2[1]) * a.scale_log2;
+        if (S::kFlush > 0 && group == 1 && j > 1 && (j - 1) % kF == 0) {  // the other group's tile starts afresh
+          flush(j - 1, 1.0f);
+          tm_fence_before();
+          if (ok) bar_arrive_warp(flushed, lane);
+        }
+        // this tile's reference, after the one of the tile before it
+        const bool restart = S::kFlush > 0 && group == 0 && j > 0 && j % kF == 0;
+        float pend = 1.0f;  // rescaling of what this group's flush adds
+        if (j > 0) turn_wait(quarter, group);
+        if (!idle) {
+          const float known = s_m[ln];
+          if (__any_sync(0xffffffffu, known != m || mx > m + kTaLazy)) {
+            rescale(known);
+            if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+              const float corr = rescale(fmaxf(m, mx));
+              s_m[ln] = m;
+              if (restart) {
+                pend = corr;
+              } else if (j > 0) {
+                if (j > 1) done(j - 2);  // room(j - 2) told of j - 4
+                done(j - 1);
+#pragma unroll 1
+                for (int c = 0; ok && c < D; c += 16) {
+                  float o[16];
+                  tm_load(tl + S::kColO + c, o);
+                  uint32_t w[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
+                  tm_store(tl + S::kColO + c, w);
+                }
               }
             }
           }
         }
-      }
-      if (j + 1 < n) turn_pass(quarter, group);
-      if (!idle && ok) {
-        const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
-        float2 ls = make_float2(0.0f, 0.0f);
-        const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
+        if (j + 1 < n) turn_pass(quarter, group);
+        if (!idle && ok) {
+          const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+          float2 ls = make_float2(0.0f, 0.0f);
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
 #pragma unroll
-        for (int ch = 0; ch < kCols; ch += 16) {  // 16 keys at a time, for the registers' sake
-          uint32_t w[S::kTermsP][8];
+          for (int ch = 0; ch < kCols; ch += 16) {  // 16 keys at a time, for the registers' sake
+            uint32_t w[S::kTermsP][8];
 #pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float2 x = fma2(make_float2(s[ch + c], s[ch + c + 1]), sc, mm);
-            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-            ls = add2(ls, pp);
-            uint32_t term[S::kTermsP];
-            split(pp.x, pp.y, term);
+            for (int c = 0; c < 16; c += 2) {
+              const float2 x = fma2(make_float2(s[ch + c], s[ch + c + 1]), sc, mm);
+              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              ls = add2(ls, pp);
+              uint32_t term[S::kTermsP];
+              split(pp.x, pp.y, term);
 #pragma unroll
-            for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
+              for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
+            }
+            if (ch == 0) room(j);
+#pragma unroll
+            for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(tl + S::weights(j, tt) + (c0 + ch) / 2, w[tt]);
           }
-          if (ch == 0) room(j);
+          l += ls.x + ls.y;
+          if constexpr (DUP > 1) {  // the keys that other lanes weigh
 #pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(tl + S::weights(j, tt) + (c0 + ch) / 2, w[tt]);
+            for (int tt = 0; tt < S::kTermsP; ++tt)
+#pragma unroll
+              for (int c = 0; c < kTaKeys / 2; c += 8)
+                if (c / (kCols / 2) != part) tm_store(tl + S::weights(j, tt) + c, zero);
+          }
         }
-        l += ls.x + ls.y;
-        if constexpr (DUP > 1) {  // the keys that other lanes weigh
-#pragma unroll
-          for (int tt = 0; tt < S::kTermsP; ++tt)
-#pragma unroll
-            for (int c = 0; c < kTaKeys / 2; c += 8)
-              if (c / (kCols / 2) != part) tm_store(tl + S::weights(j, tt) + c, zero);
-        }
+        // An idle warp also waits for its group's last products: its arrival below must not count for them.
+        if (idle) room(j);
+        if (restart) flush(j, pend);
+        tm_st_wait();
+        tm_fence_before();
+        if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
       }
-      // An idle warp also waits for its group's last products: its arrival below must not count for them.
-      if (idle) room(j);
-      if (restart) flush(j, pend);
-      tm_st_wait();
-      tm_fence_before();
-      if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
+      if (S::kFlush > 0 && group == 1 && n > 1 && (n - 1) % kF == 0) {  // the last tile is the other group's, and starts afresh
+        flush(n - 1, 1.0f);
+        tm_fence_before();
+        if (ok) bar_arrive_warp(flushed, lane);
+      }
+      // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
+      ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
+      tm_fence_after();
+      asm volatile("bar.sync 9, 256;" ::: "memory");  // both groups' last word on the references
+      if (ok) {
+        rescale(s_m[ln]);
+        float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + group * kDims;
+#pragma unroll
+        for (int c = 0; c < kDims; c += 16) {
+          float o[16];
+          tm_load(ocol + c, o);
+          if constexpr (S::kFlush > 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += acc[c + e];
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        s_l[group][ln] = l;
+      }
     }
-    if (S::kFlush > 0 && group == 1 && n > 1 && (n - 1) % kF == 0) {  // the last tile is the other group's, and starts afresh
-      flush(n - 1, 1.0f);
-      tm_fence_before();
-      if (ok) bar_arrive_warp(flushed, lane);
-    }
-    // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
-    ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
+    tm_fence_before();
+    __syncthreads();
     tm_fence_after();
-    asm volatile("bar.sync 9, 256;" ::: "memory");  // both groups' last word on the references
-    if (ok) {
-      rescale(s_m[ln]);
-      float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + group * kDims;
+    if (warp == kTaScore && (last || *fail))
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
+    if (*fail) {
+      if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
+      return;
+    }
+    // join the lanes of each row; a split's sum goes to the workspace, a whole one to the output
+    const float* st = reinterpret_cast<const float*>(ring);
+    for (int e = i; e < rows * (D / 4); e += kTaThreads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float M = -INFINITY, L = 0.0f;
 #pragma unroll
-      for (int c = 0; c < kDims; c += 16) {
-        float o[16];
-        tm_load(ocol + c, o);
-        if constexpr (S::kFlush > 0) {
+      for (int d = 0; d < DUP; ++d) M = fmaxf(M, s_m[r + d * kRows]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] += acc[c + e];
+      for (int d = 0; d < DUP; ++d) {
+        const int ln = r + d * kRows;
+        const float4 x = *reinterpret_cast<const float4*>(st + ln * S::kPitch + c);
+        const float w = DUP == 1 || s_m[ln] == M ? 1.0f : ex2(s_m[ln] - M);
+        L = fmaf(s_l[0][ln] + s_l[1][ln], w, L);
+        o.x = fmaf(x.x, w, o.x);
+        o.y = fmaf(x.y, w, o.y);
+        o.z = fmaf(x.z, w, o.z);
+        o.w = fmaf(x.w, w, o.w);
+      }
+      const int rr = mt * kRows + r, b = node_of(rr, a.inv_g);
+      if (s_bad) {  // tree values that are not finite, for the nodes that see them
+        for (int k = max(t0 - a.pre_tiles, 0) * kTaKeys; k < min(a.B, (t0 + n - a.pre_tiles) * kTaKeys); ++k) {
+          if (!(a.mask[(int64_t)b * a.words + (k >> 5)] >> (k & 31) & 1u)) continue;
+          const uint2 v = *reinterpret_cast<const uint2*>(a.vtree + (int64_t)g * a.head_stride + (int64_t)k * D + c);
+          if (!isfinite(low_f(v.x))) o.x += low_f(v.x);
+          if (!isfinite(high_f(v.x))) o.y += high_f(v.x);
+          if (!isfinite(low_f(v.y))) o.z += low_f(v.y);
+          if (!isfinite(high_f(v.y))) o.w += high_f(v.y);
         }
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      s_l[group][ln] = l;
-    }
-  }
-  tm_fence_before();
-  __syncthreads();
-  if (warp == kTaScore)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
-  if (*fail) {
-    if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
-    return;
-  }
-  // join the lanes of each row; a split's sum goes to the workspace, a whole one to the output
-  const float* st = reinterpret_cast<const float*>(ring);
-  for (int e = i; e < rows * (D / 4); e += kTaThreads) {
-    const int r = e / (D / 4), c = e % (D / 4) * 4;
-    float M = -INFINITY, L = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DUP; ++d) M = fmaxf(M, s_m[r + d * kRows]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int d = 0; d < DUP; ++d) {
-      const int ln = r + d * kRows;
-      const float4 x = *reinterpret_cast<const float4*>(st + ln * S::kPitch + c);
-      const float w = DUP == 1 || s_m[ln] == M ? 1.0f : ex2(s_m[ln] - M);
-      L = fmaf(s_l[0][ln] + s_l[1][ln], w, L);
-      o.x = fmaf(x.x, w, o.x);
-      o.y = fmaf(x.y, w, o.y);
-      o.z = fmaf(x.z, w, o.z);
-      o.w = fmaf(x.w, w, o.w);
-    }
-    const int rr = mt * kRows + r, b = node_of(rr, a.inv_g);
-    if (s_bad) {  // tree values that are not finite, for the nodes that see them
-      for (int k = max(t0 - a.pre_tiles, 0) * kTaKeys; k < min(a.B, (t0 + n - a.pre_tiles) * kTaKeys); ++k) {
-        if (!(a.mask[(int64_t)b * a.words + (k >> 5)] >> (k & 31) & 1u)) continue;
-        const uint2 v = *reinterpret_cast<const uint2*>(a.vtree + (int64_t)g * a.head_stride + (int64_t)k * D + c);
-        if (!isfinite(low_f(v.x))) o.x += low_f(v.x);
-        if (!isfinite(high_f(v.x))) o.y += high_f(v.x);
-        if (!isfinite(low_f(v.y))) o.z += low_f(v.y);
-        if (!isfinite(high_f(v.y))) o.w += high_f(v.y);
+      if (kShares ? n < a.tiles : a.nsplit > 1) {
+        // a share's pieces each move on to another CTA or tile of rows
+        const int64_t to = (kShares ? (int64_t)blockIdx.x + id : (int64_t)blockIdx.x) * kRows + r;
+        *reinterpret_cast<float4*>(a.part + to * D + c) = o;
+        if (c == 0) a.ml[to] = make_float2(M, L);
+      } else {
+        const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
+        const int64_t to = ((int64_t)b * a.Hq + g * a.G + (rr - b * a.G)) * D + c;
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+        else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
       }
     }
-    if (a.nsplit > 1) {
-      const int64_t at = (int64_t)unit * kRows + r;
-      *reinterpret_cast<float4*>(a.part + at * D + c) = o;
-      if (c == 0) a.ml[at] = make_float2(M, L);
-    } else {
-      const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
-      const int64_t at = ((int64_t)b * a.Hq + g * a.G + (rr - b * a.G)) * D + c;
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
-      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
-    }
+    if (last) break;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next piece's copies over the staged rows
+    __syncthreads();
+    if (i < 128) s_m[i] = -INFINITY;
+    if (i == 0) s_bad = 0;
+    __syncthreads();
+    locate(piece + 1);
   }
 }
 
@@ -569,22 +592,31 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
   const int64_t row = min((int64_t)blockIdx.x * (4 / W) + warp / W, (int64_t)a.B * a.Hq - 1);  // b * Hq + h
   const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / a.G;
   const int rr = b * a.G + h % a.G, mt = rr / rows_per_tile, r = rr % rows_per_tile;
-  const int64_t first = ((int64_t)g * a.nsplit * a.mtiles + mt) * rows_per_tile + r;
-  const int64_t step = (int64_t)a.mtiles * rows_per_tile;
+  int64_t first = ((int64_t)g * a.nsplit * a.mtiles + mt) * rows_per_tile + r, step = (int64_t)a.mtiles * rows_per_tile;
+  int splits = a.nsplit;
+  if (splits == 0) {  // shares of all tiles: from the one with the first of this tile of rows to the one with the last
+    const int64_t id = (int64_t)g * a.mtiles + mt;
+    const int64_t work = (int64_t)a.groups * a.tiles;
+    const int64_t from = ((id * a.tiles + 1) * a.ctas - 1) / work;
+    splits = (int)(((id + 1) * a.tiles * a.ctas - 1) / work - from) + 1;
+    if (splits == 1) return;  // written already
+    first = (from + id) * rows_per_tile + r;
+    step = rows_per_tile;
+  }
   using V = typename std::conditional<E == 4, float4, float2>::type;
   float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int s0 = w; s0 < a.nsplit; s0 += kBatch * W) {
+  for (int s0 = w; s0 < splits; s0 += kBatch * W) {
     V x[kBatch];
     float2 ml[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int s = s0 + k * W;
-      const int64_t at = first + min(s, a.nsplit - 1) * step;
+      const int64_t at = first + min(s, splits - 1) * step;
       x[k] = __ldcg(reinterpret_cast<const V*>(a.part + at * D) + lane);
       ml[k] = __ldcg(a.ml + at);
-      if (s >= a.nsplit) ml[k] = make_float2(-INFINITY, 0.0f);
+      if (s >= splits) ml[k] = make_float2(-INFINITY, 0.0f);
     }
     float mn = M;
 #pragma unroll
@@ -595,7 +627,7 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
     for (int e = 0; e < E; ++e) acc[e] *= corr;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (s0 + k * W >= a.nsplit) break;
+      if (s0 + k * W >= splits) break;
       const float wt = ml[k].x == mn ? 1.0f : ex2(ml[k].x - mn);
       L = fmaf(ml[k].y, wt, L);
       const float* xe = reinterpret_cast<const float*>(&x[k]);
@@ -644,8 +676,11 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
 
 // ---- host -----------------------------------------------------------------------------------
 struct TaPlan {
-  int dup, rows, mtiles, nsplit, tiles, pre_tiles;
+  int dup, rows, mtiles, tiles, pre_tiles;
+  int nsplit;     // 0: every CTA an equal share of all tiles
+  int parts;      // splits of a row at most
   int64_t units;  // CTAs
+  int64_t slots;  // of splits' results
 };
 TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
   TaPlan p;
@@ -675,12 +710,27 @@ TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
     if (n == 1) break;
   }
   p.units = groups * p.nsplit;
+  p.parts = p.nsplit;
+  p.slots = p.units;
+  // Whole splits leave SMs idle where they do not fill the GPU (64 tiles of rows: 128 CTAs of two splits), or
+  // fill it with little more than once (160: two rounds). Equal shares then begin and end within a tile of rows, at
+  // the cost of a second start and end, about kTaPiece tiles.
+  const int64_t work = groups * p.tiles, share = (work + kTaFill - 1) / kTaFill;
+  const int64_t pieces = (share + p.tiles - 2) / p.tiles + 1;
+  const int64_t rounds = (p.units + kTaFill - 1) / kTaFill * ((p.tiles + p.nsplit - 1) / p.nsplit) + (p.nsplit > 1 ? 3 : 0);
+  if (!few && work >= kTaFill && pieces <= kTaPieces && share + 3 + kTaPiece * (pieces - 1) < rounds) {
+    p.nsplit = 0;
+    p.units = kTaFill;
+    p.parts = (int)std::min<int64_t>(p.units, (p.tiles + share - 2) / share + 1);
+    p.slots = p.units + groups;
+  }
   return p;
 }
-size_t ta_part_bytes(const TaPlan& p, int D) { return p.nsplit == 1 ? 0 : (size_t)p.units * p.rows * D * 4; }
+bool ta_joins(const TaPlan& p) { return p.nsplit != 1; }
+size_t ta_part_bytes(const TaPlan& p, int D) { return ta_joins(p) ? (size_t)p.slots * p.rows * D * 4 : 0; }
 size_t tree_attn_ws_bytes(int B, int Hq, int Hkv, int D, int prefix) {
   const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
-  return kWsHeaderBytes + ta_part_bytes(p, D) + (p.nsplit == 1 ? 0 : (size_t)p.units * p.rows * sizeof(float2));
+  return kWsHeaderBytes + ta_part_bytes(p, D) + (ta_joins(p) ? (size_t)p.slots * p.rows * sizeof(float2) : 0);
 }
 
 std::mutex g_ta_mu;
@@ -711,7 +761,7 @@ nt_status ta_map(CUtensorMap* map, const uint16_t* base, int D, int rows, int Hk
   return NT_OK;
 }
 
-template <typename T, int D, int DUP>
+template <typename T, int D, int DUP, bool kShares>
 nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p, cudaStream_t st) {
   static std::atomic<int> attr_set[64];  // per device: the ring's dynamic shared memory allowed
   int dev = 0;
@@ -719,23 +769,24 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
   if (dev < 0 || dev >= 64) return set_error(NT_ERR_CUDA, "device index out of range");
   constexpr int smem = TaShape<T, D>::kSmem;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    NT_CUDA_TRY(cudaFuncSetAttribute(tree_attn_kernel<T, D, DUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    NT_CUDA_TRY(cudaFuncSetAttribute(tree_attn_kernel<T, D, DUP, kShares>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     attr_set[dev].store(1, std::memory_order_release);
   }
-  NT_CUDA_TRY(launch_kernel(tree_attn_kernel<T, D, DUP>, dim3((unsigned)p.units), dim3(kTaThreads), smem, st, true, maps, a));
+  NT_CUDA_TRY(launch_kernel(tree_attn_kernel<T, D, DUP, kShares>, dim3((unsigned)p.units), dim3(kTaThreads), smem, st, true, maps, a));
   return check_launch("tree_attn_kernel");
 }
 template <typename T, int D>
 nt_status launch_tree_attn_all(const TaMaps& maps, const TaArgs& a, const TaPlan& p, int dtype, cudaStream_t st) {
   const nt_status s = a.R <= kTaFewRows ? launch_tree_few(maps, a, dtype, D, st)
-                      : p.dup == 2 ? launch_tree_attn<T, D, 2>(maps, a, p, st) : launch_tree_attn<T, D, 1>(maps, a, p, st);
+                      : p.nsplit == 0 ? (p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st))
+                      : p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
   NT_TRY(s);
-  if (p.nsplit > 1) {
+  if (ta_joins(p)) {
     const int64_t rows = (int64_t)a.B * a.Hq;
     // Warps per row and splits at a time: one round trip for up to 32 splits, and no load twice for few.
-    const int w = p.nsplit > 4 ? 4 : 1;
-    auto join = p.nsplit > 16 ? tree_attn_join_kernel<T, D, 4, 8> : p.nsplit > 8 ? tree_attn_join_kernel<T, D, 4, 4>
-                : p.nsplit > 4 ? tree_attn_join_kernel<T, D, 4, 2> : p.nsplit > 2 ? tree_attn_join_kernel<T, D, 1, 4>
+    const int w = p.parts > 4 ? 4 : 1;
+    auto join = p.parts > 16 ? tree_attn_join_kernel<T, D, 4, 8> : p.parts > 8 ? tree_attn_join_kernel<T, D, 4, 4>
+                : p.parts > 4 ? tree_attn_join_kernel<T, D, 4, 2> : p.parts > 2 ? tree_attn_join_kernel<T, D, 1, 4>
                 : tree_attn_join_kernel<T, D, 1, 2>;
     NT_CUDA_TRY(launch_kernel(join, dim3((unsigned)((rows * w + 3) / 4)), dim3(128), 0, st, true, a, p.rows));
     NT_TRY(check_launch("tree_attn_join_kernel"));
@@ -799,6 +850,8 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
   a.mtiles = p.mtiles;
+  a.groups = Hkv * p.mtiles;
+  a.ctas = (int)p.units;
   a.inv_g = 1.0f / (float)a.G;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
   TaMaps maps;

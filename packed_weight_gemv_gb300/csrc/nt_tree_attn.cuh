@@ -15,14 +15,15 @@ struct TaArgs {
   const uint32_t* mask;     // [B][words]
   const uint16_t* vtree;    // the tree's first value row of head 0
   int64_t head_stride;      // elements between heads of a cache
-  float* part;              // [units][rows][D] weighted sums of a split
-  float2* ml;               // [units][rows] (m, sum)
+  float* part;              // [slots][rows][D] weighted sums of a split
+  float2* ml;               // [slots][rows] (m, sum)
   unsigned int* err;        // the workspace's status header [code, CTA]
   uint64_t timeout_ns;
   int fault;
   int B, Hq, G, R, words;   // R = B * G rows per key-value head
   int prefix, pre_tiles, tiles;  // 64-key tiles of the sequence, and with the tree's
-  int nsplit, mtiles;
+  int nsplit, mtiles;       // splits of a tile of rows (0: every CTA an equal share of all tiles), tiles of rows per head
+  int groups, ctas;         // tiles of rows of all heads; CTAs of the first kernel
   float scale_log2;         // log2(e) / sqrt(D)
   float inv_g;              // 1 / G
 };
@@ -39,6 +40,8 @@ constexpr int kTaSoftmax = 256;         // two groups of 128 threads = tensor-me
 constexpr int kTaThreads = 32 * kTaFirstSoftmax + kTaSoftmax;
 constexpr int kTaTmemCols = 512;
 constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
+constexpr int kTaPieces = 4;            // tiles of rows that a CTA's share may touch
+constexpr int kTaPiece = 12;            // tiles that one more of them costs (with 6, 65 tiles of 64 row tiles took 48.4 us in shares, 46.4 in splits)
 constexpr int kTaFirst = 3;             // ring slots filled before the queries have arrived
 constexpr float kTaLazy = 8.0f;         // a maximum is raised once a score exceeds it by 2^8
 constexpr uint64_t kTaTimeoutNs = 2000000000ull;

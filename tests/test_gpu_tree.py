@@ -451,6 +451,30 @@ def test_attention_many_tiles_to_a_block(B, D, kind):
         within(f64(out), want, attn_bound(q, k, v, prefix, sees, "f32", want), (kind, tiles))
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,prefix,dtype,D", [
+    (40, 160, 160, 2000, "f32", 64), (40, 160, 160, 2100, "bf16", 128), (200, 64, 8, 4000, "f32", 128), (200, 64, 8, 4011, "bf16", 64),
+    (255, 32, 4, 12000, "f32", 64), (70, 300, 300, 1500, "f32", 128)])
+@pytest.mark.parametrize("kind", ["random", "rise", "non-finite"])
+def test_attention_equal_shares(B, Hq, Hkv, prefix, dtype, D, kind):
+    """Numbers of row tiles that do not fill the GPU evenly: blocks begin and end within a row tile."""
+    q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 1, dtype, seed=B)
+    if kind == "rise":
+        ramp = torch.linspace(0, 10, k.shape[1], device=DEV)
+        u = q.float().view(B, Hkv, -1, D).mean((0, 2))
+        k = (k * 0.1 + ramp[None, :, None] * (u / u.norm(dim=-1, keepdim=True))[:, None]).bfloat16()
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(B), B))
+    bad = B - 1  # seen by itself alone
+    if kind == "non-finite":
+        v[:, prefix + 1 + bad] = float("inf")
+        k[:, prefix] = v[:, prefix] = float("nan")  # between the sequence and the tree
+    out = f64(run_attend(q, k, v, prefix, prefix + 1, sees, runs=2))
+    want = attend_64(q, k, v.nan_to_num(0, 0, 0), prefix, prefix + 1, sees)
+    if kind == "non-finite":
+        assert np.isposinf(out[bad]).all()
+        out, want, sees = out[:bad], want[:bad], sees[:bad]
+    within(out, want, attn_bound(q, k, v, prefix, sees, dtype, want), kind)
+
+
 def test_attention_chain_matches_the_chain_call():
     q, k, v = attn_inputs(6, 32, 8, 128, 700, 0, "f32", tail=0)
     sees = np.tril(np.ones((6, 6), bool))
