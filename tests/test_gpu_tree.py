@@ -433,7 +433,7 @@ def attend_64(q, k, v, prefix, row0, sees):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("B", [2, 40, 70, 133])
+@pytest.mark.parametrize("B", [2, 12, 30, 40, 70, 133])
 @pytest.mark.parametrize("kind", ["random", "rise"])
 def test_attention_many_tiles_to_a_block(B, D, kind):
     """A head to a block (more heads than SMs), so that one block walks every tile count about the
@@ -580,6 +580,26 @@ def test_attention_timeout_is_reported_until_cleared():
     assert nt.nt_workspace_status(ws) == nt.NT_ERR_TIMEOUT
     ws.zero_()
     nt.nt_tree_attention(q, k, v, 400, 400, mask, out, ws)
+    torch.cuda.synchronize()
+    assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,prefix,D,dtype", [(3, 8, 2, 400, 128, "f32"), (8, 8, 2, 90, 64, "bf16"), (40, 160, 160, 2000, 64, "f32")])
+def test_attention_timeout_with_few_rows_and_in_shares(B, Hq, Hkv, prefix, D, dtype):
+    q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 0, dtype)
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(6), B))
+    want = run_attend(q, k, v, prefix, prefix, sees)
+    ws = torch.zeros(nt.nt_tree_attention_workspace_size(B, Hq, Hkv, D, prefix), dtype=torch.uint8, device=DEV)
+    mask, out = dev(_tree.pack(sees)), torch.empty_like(q)
+    try:
+        nt.nt_set_test_fault(5, 20.0)
+        nt.nt_tree_attention(q, k, v, prefix, prefix, mask, out, ws)
+        torch.cuda.synchronize()
+    finally:
+        nt.nt_set_test_fault(0)
+    assert nt.nt_workspace_status(ws) == nt.NT_ERR_TIMEOUT
+    ws.zero_()
+    nt.nt_tree_attention(q, k, v, prefix, prefix, mask, out, ws)
     torch.cuda.synchronize()
     assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
 
