@@ -47,8 +47,7 @@ class Decoder:
         caches = [torch.zeros(2, Hkv, rows, D, dtype=torch.bfloat16, device=dev) for _ in range(layers)]
         self.k, self.v = [c[0] for c in caches], [c[1] for c in caches]
         self.k_ptr, self.v_ptr = nt.pointer_array(self.k), nt.pointer_array(self.v)
-        self.ws_attn = torch.zeros(max(nt.nt_tree_attention_workspace_size(b, Hq, Hkv, D, p)
-                                       for b in range(1, MAX_NODES + 1) for p in (0, 63, rows // 2, rows - MAX_NODES)),
+        self.ws_attn = torch.zeros(max(nt.nt_tree_attention_workspace_size(b, Hq, Hkv, D, 0) for b in range(1, MAX_NODES + 1)),
                                    dtype=torch.uint8, device=dev)
         self.ws_head = torch.zeros(nt.nt_int8_logits_workspace_size(V, d, MAX_NODES), dtype=torch.uint8, device=dev)
         self.ws_adj = torch.zeros(nt.nt_logits_adjust_workspace_size(V, MAX_NODES), dtype=torch.uint8, device=dev)

@@ -412,8 +412,9 @@ nt_status nt_tree_layout(const int32_t* parent, int B, int pos0, uint32_t* mask,
  *   q, out [B][Hq][D] of type dtype (nt_dtype; out may be q); k_cache, v_cache [Hkv][t_stride][D]
  *   bf16; D 64 or 128; Hq a multiple of Hkv; B * Hq <= 1048576; 0 <= prefix <= tree_row0,
  *   tree_row0 + B <= t_stride. q, out and caches 16-byte aligned.
- *   ws: nt_tree_attention_workspace_size bytes (16-byte aligned, zero-filled before its first use;
- *   calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
+ *   ws: nt_tree_attention_workspace_size bytes (the same for every prefix; 16-byte aligned,
+ *   zero-filled before its first use; calls sharing it must not overlap). It starts with the status
+ *   header of nt_workspace_status. A score or value that is visible and not finite makes the result so.
  */
 nt_status nt_tree_attention_workspace_size(int B, int Hq, int Hkv, int D, int prefix, size_t* bytes);
 nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, const uint16_t* v_cache,

@@ -680,7 +680,6 @@ struct TaPlan {
   int nsplit;     // 0: every CTA an equal share of all tiles
   int parts;      // splits of a row at most
   int64_t units;  // CTAs
-  int64_t slots;  // of splits' results
 };
 TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
   TaPlan p;
@@ -711,7 +710,6 @@ TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
   }
   p.units = groups * p.nsplit;
   p.parts = p.nsplit;
-  p.slots = p.units;
   // Whole splits leave SMs idle where they do not fill the GPU (64 tiles of rows: 128 CTAs of two splits), or
   // fill it with little more than once (160: two rounds). Equal shares then begin and end within a tile of rows, at
   // the cost of a second start and end, about kTaPiece tiles.
@@ -722,15 +720,18 @@ TaPlan ta_plan(int B, int Hq, int Hkv, int prefix) {
     p.nsplit = 0;
     p.units = kTaFill;
     p.parts = (int)std::min<int64_t>(p.units, (p.tiles + share - 2) / share + 1);
-    p.slots = p.units + groups;
   }
   return p;
 }
 bool ta_joins(const TaPlan& p) { return p.nsplit != 1; }
-size_t ta_part_bytes(const TaPlan& p, int D) { return ta_joins(p) ? (size_t)p.slots * p.rows * D * 4 : 0; }
-size_t tree_attn_ws_bytes(int B, int Hq, int Hkv, int D, int prefix) {
-  const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
-  return kWsHeaderBytes + ta_part_bytes(p, D) + (ta_joins(p) ? (size_t)p.slots * p.rows * sizeof(float2) : 0);
+// Rows of results that the splits of any prefix take: kTaFill CTAs, and in shares one more for each tile of rows.
+int64_t ta_split_rows(const TaPlan& p, int64_t groups) {
+  if (groups > kTaPieces * kTaFill) return 0;  // never split
+  return (kTaFill + groups) * p.rows;
+}
+size_t tree_attn_ws_bytes(int B, int Hq, int Hkv, int D) {
+  const TaPlan p = ta_plan(B, Hq, Hkv, 0);
+  return kWsHeaderBytes + (size_t)ta_split_rows(p, (int64_t)Hkv * p.mtiles) * (D * 4 + sizeof(float2));
 }
 
 std::mutex g_ta_mu;
@@ -806,7 +807,7 @@ nt_status nt_tree_attention_workspace_size(int B, int Hq, int Hkv, int D, int pr
     return set_error(NT_ERR_INVALID_ARG, "need 1 <= B <= 256, Hq a multiple of Hkv >= 1, prefix >= 0 and a result pointer");
   if (D != 64 && D != 128) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
   if ((int64_t)B * Hq > kTreeMaxRows) return set_error(NT_ERR_INVALID_ARG, "B * Hq leaves the supported range (1048576)");
-  *bytes = tree_attn_ws_bytes(B, Hq, Hkv, D, prefix);
+  *bytes = tree_attn_ws_bytes(B, Hq, Hkv, D);
   return NT_OK;
 }
 
@@ -824,7 +825,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
     return set_error(NT_ERR_INVALID_ARG, "need 0 <= prefix <= tree_row0 and tree_row0 + B <= t_stride");
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(mask, 4))
     return set_error(NT_ERR_ALIGNMENT, "q, out and the caches must be 16-byte, the mask 4-byte aligned");
-  if (!ws || !aligned(ws, 16) || ws_bytes < tree_attn_ws_bytes(B, Hq, Hkv, D, prefix))
+  if (!ws || !aligned(ws, 16) || ws_bytes < tree_attn_ws_bytes(B, Hq, Hkv, D))
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_tree_attention_workspace_size");
   NT_TRY(check_device());
   NT_TRY(ta_setup());
@@ -836,7 +837,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.vtree = v_cache + (int64_t)tree_row0 * D;
   a.head_stride = (int64_t)t_stride * D;
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
-  a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes + ta_part_bytes(p, D));
+  a.ml = reinterpret_cast<float2*>(a.part + ta_split_rows(p, (int64_t)Hkv * p.mtiles) * D);
   a.err = static_cast<unsigned int*>(ws);
   a.timeout_ns = test_fault_timeout_ns(kTaTimeoutNs);
   a.fault = test_fault() == kFaultTree;

@@ -88,6 +88,11 @@ def test_attention_refusals(lib, bad, status):
     assert call(lib.nt_tree_attention, ATTEND, **bad) == status
 
 
+def test_attention_workspace_does_not_depend_on_the_prefix(lib):
+    for shape in ((1, 32, 8, 128), (40, 160, 160, 64), (255, 32, 4, 64), (256, 64, 64, 128)):
+        assert len({nt.nt_tree_attention_workspace_size(*shape, p) for p in (0, 1, 64, 1000, 2000, 30000, 1 << 20)}) == 1
+
+
 def test_attention_workspace_is_what_the_call_wants(lib):
     for B, Hq, Hkv, D, prefix in ((5, 8, 2, 128, 100), (1, 32, 8, 128, 30000), (256, 32, 4, 64, 16000), (1, 1, 1, 64, 0)):
         n = nt.nt_tree_attention_workspace_size(B, Hq, Hkv, D, prefix)
