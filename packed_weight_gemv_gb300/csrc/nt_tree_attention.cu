@@ -5,7 +5,8 @@
 //
 // The R = B * Hq / Hkv query rows that share a key-value head read the cache once: they are the
 // M side of tcgen05.mma (128 rows to a tile), 64 keys at a time the N side of the scores, and the
-// weights, written back to tensor memory, the A operand of the weighted values.
+// weights, written back to tensor memory, the A operand of the weighted values. (Up to 32 rows have a
+// kernel with the sides turned, nt_tree_few.cu.)
 //
 // Products are exact: queries enter as bf16 terms (three for fp32 queries, which hold every bit of
 // a value; one for bf16 queries), keys and values are bf16, and the weights are three bf16 terms
@@ -21,12 +22,18 @@
 //                     tile. The reference maximum m of a row is raised only when a score exceeds it
 //                     by 2^8, and the accumulator rescaled only then; both groups add to one
 //                     accumulator, so they decide on m tile after tile, in turns.
-// Few rows are spread over the lanes: with R <= 32 (64) each row stands in four (two) lanes, each
-// of which weighs a quarter (half) of every tile's keys with a maximum and sum of its own and
-// leaves zeros elsewhere; their accumulators are joined at the end. So the instructions of the
-// softmax, which would otherwise be one warp's, are shared by four.
+// Up to 64 rows are spread over the lanes: each row stands in two lanes, each of which weighs half of
+// every tile's keys with a maximum and sum of its own and leaves zeros elsewhere; their accumulators
+// are joined at the end. So the instructions of the softmax, which would otherwise be two warps',
+// are shared by four.
 // The keys of one head are split over CTAs so that the GPU is filled once; the parts' results
 // (weighted sum, m, sum) meet in the workspace and a second kernel joins them.
+//
+// fp32 queries at D 128 are bound by the tensor pipe and the softmax alike (six bf16 products: 1,690
+// cycles per tile, 0.88 us; a tile takes 1.05): 25 nodes over 26,000 keys, 32 / 8 heads, 36.3 us = 107
+// MB at 3.0 TB/s, of which 9.4 us are a call of one tile and 2.5 the join. bf16 queries: 768 cycles per
+// tile, 0.6 us taken: 64 nodes over 32,704 keys 43.7 us = 785 TFLOP/s of the one product that the formula
+// asks for. At D 64 the softmax's instructions bound it: 255 nodes over 16,001 keys, 32 / 4 heads, 86 us.
 //
 // What a node does not see has no part in its result: the rows past the sequence and past the
 // tree are beyond the extent of their tensor maps (zeros), masked scores are replaced, and a tree
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   __shared__ float s_m[128], s_l[2][128];
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
-  int id = 0, g, mt, t0, n;  // tile of rows among those of all heads; its head, place, first tile of keys, tiles
+  int id = 0, g, mt, rows, t0, n;  // tile of rows among those of all heads; its head, place, rows, first tile of keys, tiles
   bool last = true;
   auto locate = [&](int piece) {
     if constexpr (kShares) {
@@ -131,8 +138,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       t0 = (int)((int64_t)a.tiles * sp / a.nsplit);
       n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
     }
+    rows = min(kRows, a.R - mt * kRows);
   };
   locate(0);
+  // computed here, before the wait below (and with fewer registers spilled)
+  asm volatile("" : "+r"(g), "+r"(mt), "+r"(rows), "+r"(t0), "+r"(n));
   for (int x = i; x < kPieces * kBars; x += kTaThreads) {
     const int b = x % kBars - 2 * S::kStages;  // the groups' four warps arrive at pfull, sfree and flushed, all eight at qfull
     bar_init(smem_u32(bars) + 8 * x, b == 2 || b == 3 || b == 6 || b == 7 || b == 11 ? 4 : b == 10 ? kTaSoftmax / 32 : b == 12 ? 2 : 1);
@@ -161,8 +171,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t full0 = smem_u32(bars[piece]), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages;
     const uint32_t pfull0 = sfull0 + 16, pvdone0 = pfull0 + 16, sfree0 = pvdone0 + 16;
     const uint32_t readmost0 = sfree0 + 16, qfull = readmost0 + 16, flushed = qfull + 8, drain = flushed + 8;
-    const int rows = min(kRows, a.R - mt * kRows);
-
     auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
     auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
     auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
@@ -528,6 +536,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     // join the lanes of each row; a split's sum goes to the workspace, a whole one to the output
     const float* st = reinterpret_cast<const float*>(ring);
+#pragma unroll 4
     for (int e = i; e < rows * (D / 4); e += kTaThreads) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float M = -INFINITY, L = 0.0f;
@@ -836,8 +845,8 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.mask = mask;
   a.vtree = v_cache + (int64_t)tree_row0 * D;
   a.head_stride = (int64_t)t_stride * D;
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
-  a.ml = reinterpret_cast<float2*>(a.part + ta_split_rows(p, (int64_t)Hkv * p.mtiles) * D);
+  a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+  a.part = reinterpret_cast<float*>(a.ml + ta_split_rows(p, (int64_t)Hkv * p.mtiles));
   a.err = static_cast<unsigned int*>(ws);
   a.timeout_ns = test_fault_timeout_ns(kTaTimeoutNs);
   a.fault = test_fault() == kFaultTree;
