@@ -32,7 +32,7 @@ constexpr int kAdjPerSm = 4;                // CTAs that an SM holds (64 registe
 constexpr int kAdjRows = 16;                // rows of a group at most
 constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
 constexpr int kAdjFew = 64;                 // used tokens of a warp's 256 that are adjusted one by one
-static_assert(kTreeMaxNodes <= kAdjThreads, "one thread per node");
+static_assert(kTreeMaxNodes <= kAdjThreads && kAdjRows * kTreeMaxNodes / 32 <= kAdjThreads, "one thread per node, and per word");
 
 // Workspace: the 16-byte status header, then per row the best (value, index) key and, in the first row
 // of a group, the counter of CTAs done with the group; all zero between calls.
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   __shared__ __align__(16) float ring[kAdjAhead][kAdjChunk];         // rows on their way
   __shared__ int path_tok[kTreeMaxNodes];                            // the tree's tokens inside the chunk
   __shared__ uint32_t path_rows[kTreeMaxNodes];                      // bit r: on the path of the group's row r
+  __shared__ uint32_t group_mask[kAdjRows * kTreeMaxNodes / 32];     // the group's rows of ancestor bits
   __shared__ int n_path, s_last;
   __shared__ int2 used_list[kPenalties ? kAdjThreads / 32 : 1][kAdjFew];  // (place, bit 16: on a path; count)
   __shared__ unsigned long long row_best[kAdjRows][kAdjThreads / 32];
@@ -194,16 +195,15 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   if (a.bias && !row_bias) load(a.bias + v0, bias, -0.0f);
   int np = 0;
   if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
-    const int t = i < a.B ? __ldg(a.tokens + i) : -1;
-    uint32_t rows = 0;
-    if (i < a.B) {
-#pragma unroll
-      for (int r = 0; r < kAdjRows; ++r)
-        if (r < nb) rows |= (__ldg(a.tree_mask + (int64_t)(b0 + r) * a.mask_words + (i >> 5)) >> (i & 31) & 1u) << r;
-    }
+    // All CTAs read these few lines at once, so a warp asks for as much as it can (with a load per row and
+    // node they waited 3 us for one another's).
+    const int t = i < a.B ? __ldg(a.tokens + i) : -1, used_words = (a.B + 31) / 32;
+    if (i < nb * used_words) group_mask[i] = __ldg(a.tree_mask + (int64_t)(b0 + i / used_words) * a.mask_words + i % used_words);
     if (i == 0) n_path = 0;
     __syncthreads();
     if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
+      uint32_t rows = 0;
+      for (int r = 0; r < nb; ++r) rows |= (group_mask[r * used_words + (i >> 5)] >> (i & 31) & 1u) << r;
       const int at = atomicAdd(&n_path, 1);
       path_tok[at] = t - v0;
       path_rows[at] = rows;

@@ -21,6 +21,10 @@
 //   warps 4-7, 8-11 - two groups, each with every other pair of tiles, a maximum, sum and accumulator of
 //                     its own, so they meet only at the end. The maxima are raised when a score of any row
 //                     exceeds its maximum by 2^8.
+//
+// Bound by the memory for long sequences and by latency for short ones. 32 / 8 heads of 128, fp32, join
+// included: one node over 32,767 keys 26.3 us = 5.1 TB/s, 75 % of the measured copy rate (bf16 25.9; with rows on
+// the M side 35.5), 8 nodes (32 rows) 29.7; one node over 4,095 keys 8.1, over 400 5.7, over 50 (unsplit) 4.1.
 #include <cuda_bf16.h>
 
 #include <atomic>
