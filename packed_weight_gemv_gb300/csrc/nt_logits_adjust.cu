@@ -13,8 +13,9 @@
 // adjusted in shared memory, a lane each; for more the penalties are straight-line code for every
 // value, two values to an instruction (with a branch around them nearly every warp took it for each of
 // a lane's tokens). 64 rows of 151,936 with all adjustments (80 MB): 240 instructions per 128 values 32.5
-// us, straight-line for all 24.7, listed 21.6, groups of rows that fill one wave 19.4 = 4.1 TB/s, 61 % of
-// the measured copy rate; instruction issue and the start of the CTAs (counts, paths) bound it.
+// us, straight-line for all 24.7, listed 21.6, groups of rows that fill one wave 19.4, the ancestor bits in a
+// few loads and the listed tokens in registers 19.1 = 4.2 TB/s, 62 % of the measured copy rate (15.1 where
+// L2 holds the rows). Instruction issue, a row's dependent steps and the start of a CTA bound it.
 #include <math.h>
 #include <string.h>
 
@@ -31,7 +32,8 @@ constexpr int kAdjChunk = kAdjPer * kAdjThreads;
 constexpr int kAdjPerSm = 4;                // CTAs that an SM holds (64 registers a thread; asking the compiler for 4 cost 2 us)
 constexpr int kAdjRows = 16;                // rows of a group at most
 constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
-constexpr int kAdjFew = 64;                 // used tokens of a warp's 256 that are adjusted one by one
+constexpr int kAdjEach = 2;                 // used tokens per lane that are adjusted one by one
+constexpr int kAdjFew = 32 * kAdjEach;      // so many of a warp's 256
 static_assert(kTreeMaxNodes <= kAdjThreads && kAdjRows * kTreeMaxNodes / 32 <= kAdjThreads, "one thread per node, and per word");
 
 // Workspace: the 16-byte status header, then per row the best (value, index) key and, in the first row
@@ -240,6 +242,29 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
     }
     if (listed > kAdjFew) listed = -1;
   }
+  // The lane's listed tokens: place, count, on which rows' paths, and whether several nodes have it.
+  int own_at[kAdjEach], own_count[kAdjEach];
+  uint32_t own_rows[kAdjEach];
+  bool several = false;
+#pragma unroll
+  for (int k = 0; k < kAdjEach; ++k) own_at[k] = own_count[k] = 0, own_rows[k] = 0u;
+  if (listed > 0) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kAdjEach; ++k) {
+      if (lane + 32 * k >= listed) continue;
+      const int2 t = used_list[i >> 5][lane + 32 * k];
+      own_at[k] = t.x & 0xffff;
+      own_count[k] = t.y;
+      if (t.x >> 16) {
+        for (int p = 0; p < np; ++p) {
+          if (path_tok[p] != own_at[k]) continue;
+          several = several || own_rows[k] != 0;
+          own_rows[k] |= path_rows[p];
+        }
+      }
+    }
+  }
   float less[N];      // - frequency * count
   uint32_t used = 0;  // bit e: token e has been used
   auto count = [&](const int(&n)[N]) {
@@ -256,18 +281,21 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdjAhead - 1) : "memory");  // this row is here
     float* st = ring[r % kAdjAhead];
     if (kPenalties && listed > 0) {
-      __syncwarp();  // the other lanes' copies (and the list)
-      for (int k = lane; k < listed; k += 32) {
-        const int2 t = used_list[i >> 5][k];
-        const int at = t.x & 0xffff;
-        int n = t.y;
-        if (t.x >> 16)
-          for (int p = 0; p < np; ++p) n += path_tok[p] == at ? (int)(path_rows[p] >> r & 1u) : 0;
+      __syncwarp();  // the other lanes' copies
+#pragma unroll
+      for (int k = 0; k < kAdjEach; ++k) {
+        if (32 * k >= listed) break;
+        int n = own_count[k] + (int)(own_rows[k] >> r & 1u);
+        if (several && own_rows[k]) {
+          n = own_count[k];
+          for (int p = 0; p < np; ++p) n += path_tok[p] == own_at[k] ? (int)(path_rows[p] >> r & 1u) : 0;
+        }
         if (n > 0) {
-          const float x = st[at];
-          float v = x > 0.0f ? __fdiv_rn(x, a.rep) : __fmul_rn(x, a.rep);
-          v = __fsub_rn(__fsub_rn(v, __fmul_rn(a.freq, __int2float_rn(n))), a.pres);
-          st[at] = v;
+          const float x = st[own_at[k]];
+          float v = quotient(Pair{x, x}, both(-a.rep), both(a.rep_inv)).x;
+          if (size_code(x) > kAdjRange || a.rep_inv == 0.0f) v = divide_one(x, a.rep);
+          v = x > 0.0f ? v : __fmul_rn(x, a.rep);
+          st[own_at[k]] = __fsub_rn(__fsub_rn(v, __fmul_rn(a.freq, __int2float_rn(n))), a.pres);
         }
       }
       __syncwarp();
