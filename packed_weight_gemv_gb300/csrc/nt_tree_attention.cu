@@ -787,11 +787,12 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
 }
 template <typename T, int D>
 nt_status launch_tree_attn_all(const TaMaps& maps, const TaArgs& a, const TaPlan& p, int dtype, cudaStream_t st) {
-  const nt_status s = a.R <= kTaFewRows ? launch_tree_few(maps, a, dtype, D, st)
+  bool joined = !ta_joins(p);
+  const nt_status s = a.R <= kTaFewRows ? launch_tree_few(maps, a, dtype, D, st, &joined)
                       : p.nsplit == 0 ? (p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st))
                       : p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
   NT_TRY(s);
-  if (ta_joins(p)) {
+  if (!joined) {
     const int64_t rows = (int64_t)a.B * a.Hq;
     // Warps per row and splits at a time: one round trip for up to 32 splits, and no load twice for few.
     const int w = p.parts > 4 ? 4 : 1;

@@ -24,6 +24,7 @@ struct TaArgs {
   int prefix, pre_tiles, tiles;  // 64-key tiles of the sequence, and with the tree's
   int nsplit, mtiles;       // splits of a tile of rows (0: every CTA an equal share of all tiles), tiles of rows per head
   int groups, ctas;         // tiles of rows of all heads; CTAs of the first kernel
+  int cluster;              // few rows: whether a cluster holds the splits of a head
   float scale_log2;         // log2(e) / sqrt(D)
   float inv_g;              // 1 / G
 };
@@ -269,6 +270,7 @@ __device__ __forceinline__ int node_of(int row, float inv_g) { return (int)(((fl
 // Up to kTaFewRows query rows per key-value head; a split's results stand few_rows(R) rows apart.
 constexpr int kTaFewRows = 32;
 constexpr int few_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
-nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st);
+// *joined: whether the output is complete, without the join of splits.
+nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st, bool* joined);
 
 }  // namespace nt

@@ -23,8 +23,8 @@
 //                     exceeds its maximum by 2^8.
 //
 // Bound by the memory for long sequences and by latency for short ones. 32 / 8 heads of 128, fp32, join
-// included: one node over 32,767 keys 26.3 us = 5.1 TB/s, 75 % of the measured copy rate (bf16 25.9; with rows on
-// the M side 35.5), 8 nodes (32 rows) 29.7; one node over 4,095 keys 8.1, over 400 5.7, over 50 (unsplit) 4.1.
+// included: one node over 32,767 keys 26.0 us = 5.2 TB/s, 76 % of the measured copy rate (bf16 25.9; with rows on
+// the M side 35.5), 8 nodes (32 rows) 29.7; one node over 4,095 keys 7.7, over 800 5.5, over 50 (unsplit) 4.1.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -36,6 +36,8 @@ namespace nt {
 namespace {
 
 constexpr int kTfKeys = 2 * kTaKeys;    // keys of a pair of tiles
+constexpr int kTfCluster = 8;            // CTAs of a cluster at most
+constexpr int kTfClusterTiles = 96;      // tiles of keys up to which a cluster takes a head
 constexpr float kTfLowest = -3.0e38f;   // reference of a row that has seen nothing (its weights are 0)
 
 constexpr int up16(int n) { return (n + 15) / 16 * 16; }
@@ -54,7 +56,7 @@ struct TfShape {
   static constexpr int kSmem = kAtQ + kQ + 1024;                  // and alignment
   static constexpr int kColS = 0, kColO = 2 * kNQ;                // tensor-memory columns, one of each per group
   static_assert(kValSlots >= 2 && 2 * (kNQ + kNP) <= kTaTmemCols, "ring and tensor memory");
-  static_assert(2 * RP * D * 4 <= kSlots * kSlot, "the sums are staged in the ring");
+  static_assert(3 * RP * D * 4 <= kSlots * kSlot, "the sums are staged in the ring");
 };
 
 __host__ __device__ constexpr uint32_t idesc_few(int n, bool rows) {  // both operands K-major, or both with the reduction along rows
@@ -137,6 +139,28 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of the cluster's CTA `rank`, at the address that this CTA has it.
+__device__ __forceinline__ float2 peer_ld2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile("{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %2, %3;\n ld.shared::cluster.v2.f32 {%0,%1}, [p];\n}\n"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile("{\n .reg .b32 p;\n mapa.shared::cluster.u32 p, %4, %5;\n ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [p];\n}\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
+
 template <typename T, int D, int RP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_few_kernel(const __grid_constant__ TaMaps maps, const TaArgs a) {
@@ -148,6 +172,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   __shared__ int s_fail, s_bad;
   __shared__ __align__(16) float s_nm[2][RP];  // minus a group's reference maxima (log2 units)
   __shared__ __align__(16) float s_corr[2][RP];  // what a raise of them scales sums by
+  __shared__ float2 s_ml[RP];  // a row's (m, sum) for the other CTAs of a cluster
   __shared__ float s_w[2][4][RP];  // a warp's largest scores; at the end its sums
   const uint32_t keyfull = smem_u32(bars), keyempty = keyfull + 8 * S::kKeySlots;
   const uint32_t valfull = keyempty + 8 * S::kKeySlots, valempty = valfull + 8 * S::kValSlots;
@@ -459,12 +484,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTaTmemCols) : "memory");
   if (*fail) {
     if (i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
-    return;
+    if (!a.cluster) return;  // a cluster's other CTAs wait for this one below
   }
-  // join the groups; a split's sum goes to the workspace, a whole one to the output
+  auto emit = [&](int r, int c, float4 o, float L) {
+    const int b = node_of(r, a.inv_g);
+    const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
+    const int64_t at = ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+    else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
+  };
+  // join the groups; a split's sum goes to the workspace or stays for its cluster, a whole one to the output
   const float* st = reinterpret_cast<const float*>(ring);
+  float* sums = reinterpret_cast<float*>(ring) + 2 * RP * D;  // [RP][D], the groups' joined
   for (int e = i; e < a.R * (D / 4); e += kTaThreads) {
-    const int r = e / (D / 4), c = e % (D / 4) * 4, b = node_of(r, a.inv_g);
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
     const float M = -fminf(s_nm[0][r], s_nm[1][r]);
     float L = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -488,45 +521,110 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (!isfinite(high_f(v.y))) o.w += high_f(v.y);
       }
     }
-    if (a.nsplit > 1) {
+    if (a.cluster) {
+      *reinterpret_cast<float4*>(sums + r * D + c) = o;
+      if (c == 0) s_ml[r] = make_float2(M, L);
+    } else if (a.nsplit > 1) {
       const int64_t at = (int64_t)unit * RP + r;
       *reinterpret_cast<float4*>(a.part + at * D + c) = o;
       if (c == 0) a.ml[at] = make_float2(M, L);
     } else {
-      const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
-      const int64_t at = ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c;
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
-      else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
+      emit(r, c, o, L);
     }
   }
+  if (!a.cluster) return;
+  // Each CTA of the cluster joins its part of the rows' values over all of them.
+  cluster_sync();
+  const int items = a.R * (D / 4), per = (items + a.nsplit - 1) / a.nsplit;
+  for (int e = sp * per + i; e < min(items, (sp + 1) * per); e += kTaThreads) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    float2 ml[kTfCluster];
+    float4 x[kTfCluster];
+    float M = kTfLowest, L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kTfCluster; ++k) {
+      ml[k] = make_float2(kTfLowest, 0.0f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < a.nsplit) {
+        ml[k] = peer_ld2(smem_u32(s_ml + r), k);
+        x[k] = peer_ld4(smem_u32(sums + r * D + c), k);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTfCluster; ++k) M = fmaxf(M, ml[k].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kTfCluster; ++k) {
+      const float w = ml[k].x == M ? 1.0f : ex2(ml[k].x - M);
+      L = fmaf(ml[k].y, w, L);
+      o.x = fmaf(x[k].x, w, o.x);
+      o.y = fmaf(x[k].y, w, o.y);
+      o.z = fmaf(x[k].z, w, o.z);
+      o.w = fmaf(x[k].w, w, o.w);
+    }
+    emit(r, c, o, L);
+  }
+  cluster_sync();  // no CTA's shared memory goes while another may read it
 }
 
 // ---- host -----------------------------------------------------------------------------------
+cudaLaunchConfig_t few_config(cudaLaunchAttribute (&attr)[2], unsigned units, int smem, int cluster, cudaStream_t st) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units);
+  cfg.blockDim = dim3(kTaThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cfg;
+}
+
 template <typename T, int D, int RP>
-nt_status launch_few(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
+nt_status launch_few(const TaMaps& maps, TaArgs a, cudaStream_t st, bool* joined) {
   static std::atomic<int> attr_set[64];  // per device: the ring's dynamic shared memory allowed
+  static std::atomic<int> active[64];    // per device: clusters of kTfCluster CTAs that run at a time
   int dev = 0;
   NT_CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return set_error(NT_ERR_CUDA, "device index out of range");
   constexpr int smem = TfShape<T, D, RP>::kSmem;
+  cudaLaunchAttribute attr[2];
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     NT_CUDA_TRY(cudaFuncSetAttribute(tree_few_kernel<T, D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const cudaLaunchConfig_t cfg = few_config(attr, kTfCluster, smem, kTfCluster, st);
+    int n = 0;
+    NT_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, tree_few_kernel<T, D, RP>, &cfg));
+    active[dev].store(n, std::memory_order_relaxed);
     attr_set[dev].store(1, std::memory_order_release);
   }
-  const unsigned units = (unsigned)(a.Hq / a.G * a.nsplit);
-  NT_CUDA_TRY(launch_kernel(tree_few_kernel<T, D, RP>, dim3(units), dim3(kTaThreads), smem, st, true, maps, a));
+  const int heads = a.Hq / a.G;
+  // A cluster joins its splits over distributed shared memory instead of in a second kernel. From its 8 CTAs' own number of
+  // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128: over 400 keys 5.6 us, unsplit 5.8; 800 5.5,
+  // in splits 6.1; 4,000 7.1 and 8.0; 8 nodes over 6,000 12.0 and 12.3, over 8,191 14.4 and 13.8).
+  if (a.tiles >= kTfCluster && a.tiles <= kTfClusterTiles && heads <= active[dev].load(std::memory_order_relaxed)) {
+    a.cluster = 1;
+    a.nsplit = kTfCluster;
+  }
+  *joined = a.cluster || a.nsplit == 1;
+  const cudaLaunchConfig_t cfg = few_config(attr, (unsigned)(heads * a.nsplit), smem, a.cluster ? a.nsplit : 1, st);
+  NT_CUDA_TRY(cudaLaunchKernelEx(&cfg, tree_few_kernel<T, D, RP>, maps, a));
   return check_launch("tree_few_kernel");
 }
 template <typename T, int D>
-nt_status launch_few_rows(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
-  return a.R <= 8 ? launch_few<T, D, 8>(maps, a, st) : a.R <= 16 ? launch_few<T, D, 16>(maps, a, st) : launch_few<T, D, 32>(maps, a, st);
+nt_status launch_few_rows(const TaMaps& maps, const TaArgs& a, cudaStream_t st, bool* joined) {
+  return a.R <= 8 ? launch_few<T, D, 8>(maps, a, st, joined)
+         : a.R <= 16 ? launch_few<T, D, 16>(maps, a, st, joined) : launch_few<T, D, 32>(maps, a, st, joined);
 }
 
 }  // namespace
 
-nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st) {
-  if (dtype == NT_F32) return D == 64 ? launch_few_rows<float, 64>(maps, a, st) : launch_few_rows<float, 128>(maps, a, st);
-  return D == 64 ? launch_few_rows<uint16_t, 64>(maps, a, st) : launch_few_rows<uint16_t, 128>(maps, a, st);
+nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st, bool* joined) {
+  if (dtype == NT_F32) return D == 64 ? launch_few_rows<float, 64>(maps, a, st, joined) : launch_few_rows<float, 128>(maps, a, st, joined);
+  return D == 64 ? launch_few_rows<uint16_t, 64>(maps, a, st, joined) : launch_few_rows<uint16_t, 128>(maps, a, st, joined);
 }
 
 }  // namespace nt

@@ -421,6 +421,18 @@ def test_attention_many_heads():
     check_attend(3, 320, 2, 128, 70, 0, "f32")     # 160 query heads share one
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 8, 8), (2, 16, 4), (3, 20, 2), (7, 32, 8), (32, 3, 3)])
+def test_attention_few_rows_of_every_length(B, Hq, Hkv, dtype, D):
+    """Up to 32 rows per key-value head: unsplit, in clusters, in splits; odd numbers of tiles."""
+    for prefix in (0, 1, 62, 64, 65, 300, 383, 447, 448, 449, 511, 900, 1500, 2303, 5900, 6079, 6080, 6144, 6200, 9000):
+        q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 2, dtype, seed=prefix)
+        sees = _tree.ancestors(_tree.parents(np.random.RandomState(prefix), B))
+        out = f64(run_attend(q, k, v, prefix, prefix + 2, sees, runs=2))
+        want = attend_64(q, k, v, prefix, prefix + 2, sees)
+        within(out, want, attn_bound(q, k, v, prefix, sees, dtype, want), prefix)
+
+
 def attend_64(q, k, v, prefix, row0, sees):
     """_tree.attend for many heads at a time."""
     (B, Hq, D), Hkv = q.shape, k.shape[0]
@@ -584,7 +596,7 @@ def test_attention_timeout_is_reported_until_cleared():
     assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,prefix,D,dtype", [(3, 8, 2, 400, 128, "f32"), (8, 8, 2, 90, 64, "bf16"), (40, 160, 160, 2000, 64, "f32")])
+@pytest.mark.parametrize("B,Hq,Hkv,prefix,D,dtype", [(3, 8, 2, 400, 128, "f32"), (3, 8, 2, 900, 128, "f32"), (2, 8, 2, 9000, 64, "f32"), (8, 8, 2, 90, 64, "bf16"), (40, 160, 160, 2000, 64, "f32")])
 def test_attention_timeout_with_few_rows_and_in_shares(B, Hq, Hkv, prefix, D, dtype):
     q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 0, dtype)
     sees = _tree.ancestors(_tree.parents(np.random.RandomState(6), B))
