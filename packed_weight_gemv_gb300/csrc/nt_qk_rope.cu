@@ -7,8 +7,9 @@
 //
 // Every value is read once and written once (queries to q_out, keys and values rounded to bf16
 // into the cache), so the kernel is bound by memory for many tokens and by the launch for few:
-// 8,191 tokens of 32 + 8 heads of 128 (fp32, 369 MB) take 64.6 us = 5.7 TB/s, 84 % of the measured
-// copy rate; one such token 2.1 us and 64 of them in bf16 2.5 us in a replayed graph.
+// 8,191 tokens of 32 + 8 heads of 128 (fp32, 369 MB) take 60.5 us = 6.1 TB/s, 90 % of the measured
+// copy rate (64.6 without the elements asked for a pass ahead); one such token 2.1 us and 64 of them in
+// bf16 2.5 us in a replayed graph.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,13 +42,18 @@ struct RopeArgs {
   uint32_t* n_bad;
 };
 
+// Four neighbouring elements as they are in memory.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
+using Raw4 = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+template <typename T>
+__device__ __forceinline__ Raw4<T> raw4(const T* p) {
+  return *reinterpret_cast<const Raw4<T>*>(p);
+}
+template <typename V>
+__device__ __forceinline__ void unpack4(V v, float (&x)[4]) {
+  if constexpr (sizeof(V) == 16) {
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
   } else {  // bf16 is the upper half of an fp32
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
     x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
     x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
   }
@@ -86,6 +92,23 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a)
   const int b = blockIdx.x, i = threadIdx.x, u = i % LPH;
   const int pos = a.pos ? a.pos[b] : a.pos0 + b;
   const int row = a.rows ? a.rows[b] : a.row0 + b;
+  const bool rot = u < a.rd / 8, live = u < a.D / 8;
+  // the unit's two groups of four elements
+  const int e0 = rot && kHalf ? 4 * u : 8 * u, e1 = rot && kHalf ? a.rd / 2 + 4 * u : 8 * u + 4;
+  const int heads = a.Hq + 2 * a.Hkv;
+  // A pass's elements are asked for a pass ahead, the first one's before the angles are formed.
+  Raw4<T> next0{}, next1{};
+  auto fetch = [&](int h0) {
+    const int h = h0 + i / LPH;
+    if (!live || h >= heads) return;
+    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
+    const int g = isq ? h : isv ? h - a.Hq - a.Hkv : h - a.Hq;
+    const T* x = static_cast<const T*>(isq ? a.q : isv ? a.v : a.k) +
+                 (int64_t)b * (isq ? a.q_stride : isv ? a.v_stride : a.k_stride) + (int64_t)g * a.D;
+    next0 = raw4(x + e0);
+    next1 = raw4(x + e1);
+  };
+  fetch(blockIdx.y * kHeads);
   for (int p = i; p < a.rd / 2; p += kRopeThreads) {
     float s, c;
     turn_sincos(a.inv_freq[p], pos, &s, &c);
@@ -95,21 +118,16 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a)
   __syncthreads();
   const bool row_ok = row >= 0 && row < a.ts;
   if (!row_ok && a.n_bad && blockIdx.y == 0 && i == 0) atomicAdd(a.n_bad, 1u);
-  const bool rot = u < a.rd / 8, live = u < a.D / 8;
-  // the unit's two groups of four elements
-  const int e0 = rot && kHalf ? 4 * u : 8 * u, e1 = rot && kHalf ? a.rd / 2 + 4 * u : 8 * u + 4;
-  const int heads = a.Hq + 2 * a.Hkv;
   for (int h0 = blockIdx.y * kHeads; h0 < heads; h0 += gridDim.y * kHeads) {
     const int h = h0 + i / LPH;
     const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv, on = live && h < heads;
     const int g = isq ? h : isv ? h - a.Hq - a.Hkv : h - a.Hq;
-    const T* x = static_cast<const T*>(isq ? a.q : isv ? a.v : a.k) +
-                 (int64_t)b * (isq ? a.q_stride : isv ? a.v_stride : a.k_stride) + (int64_t)g * a.D;
     float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
     if (on) {
-      load4(x + e0, x0);
-      load4(x + e1, x1);
+      unpack4(next0, x0);
+      unpack4(next1, x1);
     }
+    fetch(h0 + gridDim.y * kHeads);
     const float* gamma = isq ? a.q_gamma : a.k_gamma;
     float ss = 0.0f;
 #pragma unroll
@@ -121,8 +139,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a)
       if (gamma) {
         const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
         float g0[4], g1[4];
-        load4(gamma + e0, g0);
-        load4(gamma + e1, g1);
+        unpack4(raw4(gamma + e0), g0);
+        unpack4(raw4(gamma + e1), g1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x0[e] = x0[e] * r * g0[e];
