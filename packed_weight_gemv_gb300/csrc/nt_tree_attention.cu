@@ -788,9 +788,10 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
 template <typename T, int D>
 nt_status launch_tree_attn_all(const TaMaps& maps, const TaArgs& a, const TaPlan& p, int dtype, cudaStream_t st) {
   bool joined = !ta_joins(p);
-  const nt_status s = a.R <= kTaFewRows ? launch_tree_few(maps, a, dtype, D, st, &joined)
-                      : p.nsplit == 0 ? (p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st))
-                      : p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
+  nt_status s;
+  if (a.R <= kTaFewRows) s = launch_tree_few(maps, a, dtype, D, st, &joined);
+  else if (p.nsplit == 0) s = p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st);
+  else s = p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
   NT_TRY(s);
   if (!joined) {
     const int64_t rows = (int64_t)a.B * a.Hq;

@@ -83,7 +83,9 @@ __device__ __forceinline__ void tm_terms8(uint32_t addr, float (&x)[8]) {
           " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%25];\n"
           " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%26];\n"
           " tcgen05.wait::ld.sync.aligned;"
-          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7]), "=f"(low[0]), "=f"(low[1]), "=f"(low[2]), "=f"(low[3]), "=f"(low[4]), "=f"(low[5]), "=f"(low[6]), "=f"(low[7])
+          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+            "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7]),
+            "=f"(low[0]), "=f"(low[1]), "=f"(low[2]), "=f"(low[3]), "=f"(low[4]), "=f"(low[5]), "=f"(low[6]), "=f"(low[7])
           : "r"(addr), "r"(addr + RP), "r"(addr + 2 * RP)
           : "memory");
 #pragma unroll
@@ -93,7 +95,8 @@ __device__ __forceinline__ void tm_terms8(uint32_t addr, float (&x)[8]) {
           " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
           " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
           " tcgen05.wait::ld.sync.aligned;"
-          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7])
+          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+            "=f"(mid[0]), "=f"(mid[1]), "=f"(mid[2]), "=f"(mid[3]), "=f"(mid[4]), "=f"(mid[5]), "=f"(mid[6]), "=f"(mid[7])
           : "r"(addr), "r"(addr + RP)
           : "memory");
     }
@@ -101,8 +104,8 @@ __device__ __forceinline__ void tm_terms8(uint32_t addr, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] -= mid[e];
   }
 }
-// Sums of N values (8, 16 or 32 of them) over a warp: lane r gets value r's, and lanes N on repeat them. Half of the values go
-// to the other half of the lanes at every step.
+// Sums of N values (8, 16 or 32 of them) over a warp: lane r gets value r's, and lanes N on repeat
+// them. Half of the values go to the other half of the lanes at every step.
 template <int N>
 __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 #pragma unroll

@@ -596,7 +596,9 @@ def test_attention_timeout_is_reported_until_cleared():
     assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
 
 
-@pytest.mark.parametrize("B,Hq,Hkv,prefix,D,dtype", [(3, 8, 2, 400, 128, "f32"), (3, 8, 2, 900, 128, "f32"), (2, 8, 2, 9000, 64, "f32"), (8, 8, 2, 90, 64, "bf16"), (40, 160, 160, 2000, 64, "f32")])
+@pytest.mark.parametrize("B,Hq,Hkv,prefix,D,dtype", [
+    (3, 8, 2, 400, 128, "f32"), (3, 8, 2, 900, 128, "f32"), (2, 8, 2, 9000, 64, "f32"), (8, 8, 2, 90, 64, "bf16"),
+    (40, 160, 160, 2000, 64, "f32")])
 def test_attention_timeout_with_few_rows_and_in_shares(B, Hq, Hkv, prefix, D, dtype):
     q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 0, dtype)
     sees = _tree.ancestors(_tree.parents(np.random.RandomState(6), B))
