@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "nt_tree.cuh"
+#include "nt_tree_plan.cuh"
 
 namespace nt {
 
@@ -34,15 +35,11 @@ struct TaMaps {
 
 namespace {
 
-constexpr int kTaKeys = 64;             // keys per tile
 // Warps: the issuers come first, as the scheduler prefers older warps and each of them holds up all others.
 constexpr int kTaKeyLoad = 0, kTaScore = 1, kTaValue = 2, kTaValueLoad = 3, kTaFirstSoftmax = 4;
 constexpr int kTaSoftmax = 256;         // two groups of 128 threads = tensor-memory lanes (rows)
 constexpr int kTaThreads = 32 * kTaFirstSoftmax + kTaSoftmax;
 constexpr int kTaTmemCols = 512;
-constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
-constexpr int kTaPieces = 4;            // tiles of rows that a CTA's share may touch
-constexpr int kTaPiece = 12;            // tiles that one more of them costs (with 6, 65 tiles of 64 row tiles took 48.4 us in shares, 46.4 in splits)
 constexpr int kTaFirst = 3;             // ring slots filled before the queries have arrived
 constexpr float kTaLazy = 8.0f;         // a maximum is raised once a score exceeds it by 2^8
 constexpr uint64_t kTaTimeoutNs = 2000000000ull;
@@ -267,9 +264,6 @@ __device__ __forceinline__ int node_of(int row, float inv_g) { return (int)(((fl
 
 }  // namespace
 
-// Up to kTaFewRows query rows per key-value head; a split's results stand few_rows(R) rows apart.
-constexpr int kTaFewRows = 32;
-constexpr int few_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 // *joined: whether the output is complete, without the join of splits.
 nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st, bool* joined);
 

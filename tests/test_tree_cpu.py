@@ -2,6 +2,9 @@
 launch (no GPU needed), with the status the header states; well-formed ones get as far as the
 device check."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -213,3 +216,18 @@ def test_plain_forms_against_closed_forms():
     y = _tree.adjust(np.array([[2.0, -2.0, 1.0]]), np.array([[1, 2, 0]]), 2.0, 0.5, 0.25, None, None)
     assert np.allclose(y, [[0.25, -5.25, 1.0]])
     assert _tree.accept([-1, 0, 0, 1], [9, 5, 5, 7], [5, 7, 3, 8]) == ([0, 1, 3], [5, 7, 8])
+
+
+def test_attention_plan_covers_every_tile(tmp_path):
+    """tests/host/tree_plan_check.cu: the split of the attention's work over CTAs, host functions only."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "tree_plan_check")
+    r = subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-std=c++17", "-O2", "-I",
+                        os.path.join(root, "packed_weight_gemv_gb300", "csrc"), os.path.join(root, "tests", "host", "tree_plan_check.cu"),
+                        "-o", exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
