@@ -619,6 +619,57 @@ def test_attention_timeout_with_few_rows_and_in_shares(B, Hq, Hkv, prefix, D, dt
 
 
 # ---- streams and graphs --------------------------------------------------------------------------
+def test_attention_forms_in_one_graph_and_on_two_streams():
+    """Unsplit, in a cluster, in splits, many rows and equal shares: one after the other in a replayed graph, and at once."""
+    calls = []
+    for B, Hq, Hkv, prefix, D, dtype in [(1, 32, 8, 60, 128, "f32"), (2, 32, 8, 1500, 128, "f32"), (1, 8, 2, 20000, 64, "bf16"),
+                                         (25, 32, 8, 2000, 128, "f32"), (40, 160, 160, 2000, 64, "f32"), (7, 32, 8, 900, 64, "bf16")]:
+        q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 0, dtype, seed=prefix)
+        sees = _tree.ancestors(_tree.parents(np.random.RandomState(B), B))
+        want = run_attend(q, k, v, prefix, prefix, sees)
+        ws = torch.zeros(nt.nt_tree_attention_workspace_size(B, Hq, Hkv, D, prefix), dtype=torch.uint8, device=DEV)
+        calls.append(((q, k, v, prefix, prefix, dev(_tree.pack(sees))), torch.zeros_like(q), ws, want))
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        for args, out, ws, _ in calls:
+            nt.nt_tree_attention(*args, out, ws)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for _, out, ws, want in calls:
+            assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
+            out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(4):
+        for at, (args, out, ws, _) in enumerate(calls):
+            nt.nt_tree_attention(*args, out, ws, stream=streams[at % 3])
+    torch.cuda.synchronize()
+    for _, out, ws, want in calls:
+        assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
+    for args, _, ws, want in calls:  # the queries' own place
+        q = args[0].clone()
+        nt.nt_tree_attention(q, *args[1:], q, ws)
+        assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("V", [5000, 5001])
+def test_adjust_in_place(V):
+    rs = np.random.RandomState(V)
+    B = 37
+    x = (rs.randn(B, V) * 4).astype(np.float32)
+    counts = (rs.rand(V) < 0.1).astype(np.int32) * 2
+    bias = rs.randn(V).astype(np.float32)
+    full = np.tile(counts, (B, 1))
+    want = _tree.adjust(x, full, 1.2, 0.5, 0.25, bias, None, np.float32)
+    y = dev(x)
+    arg = torch.empty(B, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(nt.nt_logits_adjust_workspace_size(V, B), dtype=torch.uint8, device=DEV)
+    nt.nt_logits_adjust(y, counts=dev(counts), repetition=1.2, frequency=0.5, presence=0.25, bias=dev(bias), out=y, argmax=arg, ws=ws)
+    assert np.array_equal(host(y), want) and np.array_equal(host(arg), _tree.choice(want))
+
+
 def test_a_whole_pass_on_another_stream_and_in_a_graph():
     rs = np.random.RandomState(5)
     B, Hq, Hkv, D, P, V = 12, 8, 2, 128, 300, 3001
