@@ -6,7 +6,7 @@
 // The R = B * Hq / Hkv query rows that share a key-value head read the cache once: they are the
 // M side of tcgen05.mma (128 rows to a tile), 64 keys at a time the N side of the scores, and the
 // weights, written back to tensor memory, the A operand of the weighted values. (Up to 32 rows have a
-// kernel with the sides turned, nt_tree_few.cu.)
+// kernel with the sides turned, nt_tree_few.cu, which also takes more of them over shorter sequences.)
 //
 // Products are exact: queries enter as bf16 terms (three for fp32 queries, which hold every bit of
 // a value; one for bf16 queries), keys and values are bf16, and the weights are three bf16 terms
@@ -685,8 +685,7 @@ __global__ void __launch_bounds__(128) tree_attn_join_kernel(const TaArgs a, int
 
 // ---- host -----------------------------------------------------------------------------------
 size_t tree_attn_ws_bytes(int B, int Hq, int Hkv, int D) {
-  const TaPlan p = ta_plan(B, Hq, Hkv, 0);
-  return kWsHeaderBytes + (size_t)ta_split_rows(p, (int64_t)Hkv * p.mtiles) * (D * 4 + sizeof(float2));
+  return kWsHeaderBytes + (size_t)ta_split_rows(B, Hq, Hkv) * (D * 4 + sizeof(float2));
 }
 
 std::mutex g_ta_mu;
@@ -735,7 +734,7 @@ template <typename T, int D>
 nt_status launch_tree_attn_all(const TaMaps& maps, const TaArgs& a, const TaPlan& p, int dtype, cudaStream_t st) {
   bool joined = !ta_joins(p);
   nt_status s;
-  if (a.R <= kTaFewRows) s = launch_tree_few(maps, a, dtype, D, st, &joined);
+  if (p.few) s = launch_tree_few(maps, a, dtype, D, st, &joined);
   else if (p.nsplit == 0) s = p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st);
   else s = p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
   NT_TRY(s);
@@ -786,7 +785,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_tree_attention_workspace_size");
   NT_TRY(check_device());
   NT_TRY(ta_setup());
-  const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
+  const TaPlan p = ta_plan(B, Hq, Hkv, prefix, dtype == NT_F32, D);
   TaArgs a{};
   a.q = q;
   a.out = out;
@@ -794,7 +793,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.vtree = v_cache + (int64_t)tree_row0 * D;
   a.head_stride = (int64_t)t_stride * D;
   a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
-  a.part = reinterpret_cast<float*>(a.ml + ta_split_rows(p, (int64_t)Hkv * p.mtiles));
+  a.part = reinterpret_cast<float*>(a.ml + ta_split_rows(B, Hq, Hkv));
   a.err = static_cast<unsigned int*>(ws);
   a.timeout_ns = test_fault_timeout_ns(kTaTimeoutNs);
   a.fault = test_fault() == kFaultTree;

@@ -1,6 +1,6 @@
 // nt_tree_few.cu -- attention of a drafted token tree with few query rows: single tokens and small
 // trees, up to 32 rows B * Hq / Hkv per key-value head (the formula and the rules on what a node sees
-// are the same as for more rows).
+// are the same as for more rows). Over shorter sequences also more rows, 32 to a CTA.
 //
 // With the query rows on the M side of tcgen05.mma, 128 of them to a tile, few rows cost the tensor
 // pipe as much as 128 do: 0.88 us per 64 keys for fp32 queries, above the 0.7 us that a CTA's share of
@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
 
-  const int unit = blockIdx.x, g = unit / a.nsplit, sp = unit % a.nsplit;
+  // A cluster's CTAs are neighbours; otherwise the tiles of rows that read the same keys are.
+  const int unit = blockIdx.x, g = unit / (a.nsplit * a.mtiles), in_head = unit - g * (a.nsplit * a.mtiles);
+  const int mt = a.cluster ? in_head / a.nsplit : in_head % a.mtiles, sp = a.cluster ? in_head % a.nsplit : in_head / a.mtiles;
+  const int r0 = mt * RP, rows = min(RP, a.R - r0);
   const int t0 = (int)((int64_t)a.tiles * sp / a.nsplit), n = (int)((int64_t)a.tiles * (sp + 1) / a.nsplit) - t0;
   const int pairs = (n + 1) / 2;
 
@@ -291,17 +294,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     {  // the query terms: rows of 64 dimensions, 16-byte pieces in the order of the 128-byte swizzle
       const int idx = i - 32 * kTaFirstSoftmax;
-      if (idx < RP) s_mask[idx] = idx < a.R ? a.mask[(int64_t)node_of(idx, a.inv_g) * a.words] : 0u;
+      if (idx < RP) s_mask[idx] = idx < rows ? a.mask[(int64_t)node_of(r0 + idx, a.inv_g) * a.words] : 0u;
       uint8_t* qs = ring + S::kAtQ;
       constexpr int kAll = RP * (D / 8), kPer = (kAll + kTaSoftmax - 1) / kTaSoftmax;  // pieces of 8 dimensions
       uint4 v[kPer][sizeof(T) / 2];
 #pragma unroll
       for (int p = 0; p < kPer; ++p) {
-        const int e = idx + p * kTaSoftmax, r = e / (D / 8), b = node_of(r, a.inv_g);
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + e % (D / 8) * 8;
+        const int e = idx + p * kTaSoftmax, r = e / (D / 8), b = node_of(r0 + r, a.inv_g);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Hq + g * a.G + (r0 + r - b * a.G)) * D + e % (D / 8) * 8;
 #pragma unroll
         for (int h = 0; h < (int)sizeof(T) / 2; ++h)
-          v[p][h] = r < a.R ? reinterpret_cast<const uint4*>(q)[h] : make_uint4(0u, 0u, 0u, 0u);
+          v[p][h] = r < rows ? reinterpret_cast<const uint4*>(q)[h] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int p = 0; p < kPer; ++p) {
@@ -490,16 +493,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (!a.cluster) return;  // a cluster's other CTAs wait for this one below
   }
   auto emit = [&](int r, int c, float4 o, float L) {
-    const int b = node_of(r, a.inv_g);
+    const int b = node_of(r0 + r, a.inv_g);
     const float s = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the node sees nothing
-    const int64_t at = ((int64_t)b * a.Hq + g * a.G + (r - b * a.G)) * D + c;
+    const int64_t at = ((int64_t)b * a.Hq + g * a.G + (r0 + r - b * a.G)) * D + c;
     if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
     else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_rn(o.x * s, o.y * s), pack_rn(o.z * s, o.w * s));
   };
   // join the groups; a split's sum goes to the workspace or stays for its cluster, a whole one to the output
   const float* st = reinterpret_cast<const float*>(ring);
   float* sums = reinterpret_cast<float*>(ring) + 2 * RP * D;  // [RP][D], the groups' joined
-  for (int e = i; e < a.R * (D / 4); e += kTaThreads) {
+  for (int e = i; e < rows * (D / 4); e += kTaThreads) {
     const int r = e / (D / 4), c = e % (D / 4) * 4;
     const float M = -fminf(s_nm[0][r], s_nm[1][r]);
     float L = 0.0f;
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   if (!a.cluster) return;
   // Each CTA of the cluster joins its part of the rows' values over all of them.
   cluster_sync();
-  const int items = a.R * (D / 4), per = (items + a.nsplit - 1) / a.nsplit;
+  const int items = rows * (D / 4), per = (items + a.nsplit - 1) / a.nsplit;
   for (int e = sp * per + i; e < min(items, (sp + 1) * per); e += kTaThreads) {
     const int r = e / (D / 4), c = e % (D / 4) * 4;
     float2 ml[kTfCluster];
@@ -604,16 +607,15 @@ nt_status launch_few(const TaMaps& maps, TaArgs a, cudaStream_t st, bool* joined
     active[dev].store(n, std::memory_order_relaxed);
     attr_set[dev].store(1, std::memory_order_release);
   }
-  const int heads = a.Hq / a.G;
   // A cluster joins its splits over distributed shared memory instead of in a second kernel. From its 8 CTAs' own number of
   // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128: over 400 keys 5.6 us, unsplit 5.8; 800 5.5,
   // in splits 6.1; 4,000 7.1 and 8.0; 8 nodes over 6,000 12.0 and 12.3, over 8,191 14.4 and 13.8).
-  if (a.tiles >= kTfCluster && a.tiles <= kTfClusterTiles && heads <= active[dev].load(std::memory_order_relaxed)) {
+  if (a.tiles >= kTfCluster && a.tiles <= kTfClusterTiles && a.groups <= active[dev].load(std::memory_order_relaxed)) {
     a.cluster = 1;
     a.nsplit = kTfCluster;
   }
   *joined = a.cluster || a.nsplit == 1;
-  const cudaLaunchConfig_t cfg = few_config(attr, (unsigned)(heads * a.nsplit), smem, a.cluster ? a.nsplit : 1, st);
+  const cudaLaunchConfig_t cfg = few_config(attr, (unsigned)(a.groups * a.nsplit), smem, a.cluster ? a.nsplit : 1, st);
   NT_CUDA_TRY(cudaLaunchKernelEx(&cfg, tree_few_kernel<T, D, RP>, maps, a));
   return check_launch("tree_few_kernel");
 }

@@ -13,14 +13,15 @@ static int fail(const char* what, int B, int Hq, int Hkv, int prefix) {
   return 1;
 }
 
-static int check(int B, int Hq, int Hkv, int prefix, int* shares) {
-  const TaPlan p = ta_plan(B, Hq, Hkv, prefix);
+static int check(int B, int Hq, int Hkv, int prefix, bool f32, int* shares, int* several) {
+  const TaPlan p = ta_plan(B, Hq, Hkv, prefix, f32, prefix % 2 ? 64 : 128);
   const int R = B * (Hq / Hkv);
   const int64_t groups = (int64_t)Hkv * p.mtiles, work = groups * p.tiles;
   if (p.pre_tiles * (int64_t)kTaKeys < prefix || p.tiles - p.pre_tiles != (B + kTaKeys - 1) / kTaKeys)
     return fail("tiles", B, Hq, Hkv, prefix);
-  if ((int64_t)p.mtiles * p.rows < R || (R <= kTaFewRows && p.mtiles != 1)) return fail("rows", B, Hq, Hkv, prefix);
-  const int64_t room = ta_split_rows(p, groups) / p.rows;
+  if ((int64_t)p.mtiles * p.rows < R || (p.few && (p.rows > kTaFewRows || B > kTaFewNodes)) || (R <= kTaFewRows && !p.few)) return fail("rows", B, Hq, Hkv, prefix);
+  const int64_t room = ta_split_rows(B, Hq, Hkv) / p.rows;
+  *several += p.few && p.mtiles > 1;
   if (p.nsplit > 0) {
     if (p.nsplit > p.tiles || p.units != groups * p.nsplit) return fail("splits", B, Hq, Hkv, prefix);
     if (p.nsplit > 1 && (p.units > room || p.units > kTaFill)) return fail("workspace of splits", B, Hq, Hkv, prefix);
@@ -28,7 +29,7 @@ static int check(int B, int Hq, int Hkv, int prefix, int* shares) {
   }
   ++*shares;
   const int ctas = (int)p.units;
-  if (R <= kTaFewRows || ctas > work) return fail("shares", B, Hq, Hkv, prefix);
+  if (p.few || ctas > work) return fail("shares", B, Hq, Hkv, prefix);
   std::vector<char> used(room, 0);
   int64_t next = 0;
   for (int c = 0; c < ctas; ++c) {
@@ -61,19 +62,19 @@ static int check(int B, int Hq, int Hkv, int prefix, int* shares) {
 int main() {
   std::mt19937 rng(1);
   auto pick = [&](int lo, int hi) { return lo + (int)(rng() % (unsigned)(hi - lo + 1)); };
-  int cases = 0, shares = 0;
+  int cases = 0, shares = 0, several = 0;
   for (; cases < 30000; ++cases) {
     const int Hkv = cases % 3 == 0 ? pick(1, 700) : pick(1, 40), Hq = Hkv * pick(1, cases % 5 == 0 ? 64 : 8);
     const int B = pick(1, 256), prefix = (int)((double)(1 << pick(0, 20)) * (rng() % 1000) / 1000.0);
-    if (check(B, Hq, Hkv, prefix, &shares)) return 1;
+    if (check(B, Hq, Hkv, prefix, cases & 1, &shares, &several)) return 1;
   }
   for (int prefix : {0, 1, 2147483391})
     for (int B : {1, 256})
       for (int Hkv : {1, 8, 152, 153, 608, 609, 4096}) {
         ++cases;
-        if (prefix < 100 ? check(B, Hkv, Hkv, prefix, &shares) : ta_plan(B, Hkv, Hkv, prefix).nsplit < 0) return 1;
+        if (prefix < 100 ? check(B, Hkv, Hkv, prefix, true, &shares, &several) : ta_plan(B, Hkv, Hkv, prefix, true, 128).nsplit < 0) return 1;
       }
-  if (shares < 1000) return fail("too few shares", shares, 0, 0, 0);
-  std::printf("ok %d (%d in shares)\n", cases, shares);
+  if (shares < 1000 || several < 100) return fail("too few shares, or row tiles of few rows", shares, several, 0, 0);
+  std::printf("ok %d (%d in shares, %d in tiles of few rows)\n", cases, shares, several);
   return 0;
 }

@@ -422,9 +422,9 @@ def test_attention_many_heads():
 
 
 @pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 128), ("bf16", 64), ("bf16", 128)])
-@pytest.mark.parametrize("B,Hq,Hkv", [(1, 8, 8), (2, 16, 4), (3, 20, 2), (7, 32, 8), (32, 3, 3)])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 8, 8), (2, 16, 4), (3, 20, 2), (7, 32, 8), (32, 3, 3), (9, 32, 8), (32, 14, 2), (25, 32, 8)])
 def test_attention_few_rows_of_every_length(B, Hq, Hkv, dtype, D):
-    """Up to 32 rows per key-value head: unsplit, in clusters, in splits; odd numbers of tiles."""
+    """Up to 32 rows per key-value head, and more of up to 32 nodes: unsplit, in clusters, in splits; odd numbers of tiles."""
     for prefix in (0, 1, 62, 64, 65, 300, 383, 447, 448, 449, 511, 900, 1500, 2303, 5900, 6079, 6080, 6144, 6200, 9000):
         q, k, v = attn_inputs(B, Hq, Hkv, D, prefix, 2, dtype, seed=prefix)
         sees = _tree.ancestors(_tree.parents(np.random.RandomState(prefix), B))
