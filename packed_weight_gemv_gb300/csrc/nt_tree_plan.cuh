@@ -59,7 +59,7 @@ inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few) {
   p.units = groups * p.nsplit;
   p.parts = p.nsplit;
   // Whole splits leave SMs idle where they do not fill the GPU (64 tiles of rows: 128 CTAs of two splits), or
-  // fill it with little more than once (160: two rounds). Equal shares then begin and end within a tile of rows, at
+  // fill it with little more than once (160: two waves). Equal shares then begin and end within a tile of rows, at
   // the cost of a second start and end, about kTaPiece tiles.
   const int64_t work = groups * p.tiles, share = (work + kTaFill - 1) / kTaFill;
   const int64_t pieces = (share + p.tiles - 2) / p.tiles + 1;
