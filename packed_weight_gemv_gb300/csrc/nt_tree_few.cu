@@ -394,6 +394,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const int tree = a.pre_tiles - t0 - 2 * j;  // which half is the tree's
       if (tree < 2 && tree >= 0 && a.pre_tiles < t0 + n) {  // take its values that are not finite out of the product
         const int k = j % S::kValSlots;
+        // Pair j - 2's products tell that the values before pair j's have left the slot: a parity alone could answer for them.
+        if (j >= 2) ok = ok && bar_wait_warp(pvdone0 + 8 * group, ((j >> 1) - 1) & 1, fail, a.timeout_ns);
         ok = ok && bar_wait_warp(valfull + 8 * k, (j / S::kValSlots) & 1, fail, a.timeout_ns);
         bool bad = false;
         for (int e = ln; ok && e < a.B * (D / 8); e += 128) {
