@@ -414,7 +414,11 @@ nt_status nt_tree_layout(const int32_t* parent, int B, int pos0, uint32_t* mask,
  *   tree_row0 + B <= t_stride. q, out and caches 16-byte aligned.
  *   ws: nt_tree_attention_workspace_size bytes (the same for every prefix; 16-byte aligned,
  *   zero-filled before its first use; calls sharing it must not overlap). It starts with the status
- *   header of nt_workspace_status. A score or value that is visible and not finite makes the result so.
+ *   header of nt_workspace_status. A score or value that is visible and not finite makes the result so
+ *   (a score of -infinity may also weigh nothing).
+ * fp32 queries: products are exact; scores, weights and sums are fp32. bf16 queries: the same, with each
+ * weight as two bf16 terms (within 2^-18 of it). Sums lose at most 2^-16 of the sum of
+ * their terms' magnitudes, however long the sequence (fp32 queries: 2^-16.4), before the output is rounded.
  */
 nt_status nt_tree_attention_workspace_size(int B, int Hq, int Hkv, int D, int prefix, size_t* bytes);
 nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, const uint16_t* v_cache,

@@ -10,8 +10,9 @@
 //
 // Products are exact: queries enter as bf16 terms (three for fp32 queries, which hold every bit of
 // a value; one for bf16 queries), keys and values are bf16, and the weights are three bf16 terms
-// cut from the fp32 weight without loss (fp32 queries) or two rounded ones (bf16 queries: 2^-17,
-// small next to the output's 2^-9). Scores, weights, sums and the output accumulate in fp32.
+// cut from the fp32 weight without loss (fp32 queries) or two rounded ones (bf16 queries: 2^-18 of
+// a weight at most, either way, next to 2^-8 of the output; a third term made 64 nodes over 32K 10 % slower).
+// Scores, weights, sums and the output accumulate in fp32.
 //
 // CTA (384 threads): one tile of rows, one key-value head, a range of 64-key tiles.
 //   warps 0, 3     -- (one lane each) 64-row TMA boxes of keys, of values (128-byte swizzle) into a ring;
@@ -32,7 +33,7 @@
 // fp32 queries at D 128 are bound by the tensor pipe and the softmax alike (six bf16 products: 1,690
 // cycles per tile, 0.88 us; a tile takes 1.05): 25 nodes over 26,000 keys, 32 / 8 heads, 36.3 us = 107
 // MB at 3.0 TB/s, of which 9.4 us are a call of one tile and 2.5 the join. bf16 queries: 768 cycles per
-// tile, 0.6 us taken: 64 nodes over 32,704 keys 43.7 us = 785 TFLOP/s of the one product that the formula
+// tile, 0.6 us taken: 64 nodes over 32,704 keys 46.1 us = 744 TFLOP/s of the one product that the formula
 // asks for. At D 64 the softmax's instructions bound it: 255 nodes over 16,001 keys, 32 / 4 heads, 86 us.
 //
 // What a node does not see has no part in its result: the rows past the sequence and past the
@@ -69,6 +70,18 @@ struct TaShape {
   static constexpr int kTermsQT = kTermsQ - (kTight ? 1 : 0);  // query terms in tensor memory
   static constexpr int kPlaces = kTight ? 4 : 2 * kTermsP;     // of weight terms
   static constexpr int kColO = 0, kColQ = D, kColS = D + kTermsQT * D / 2, kColP = kColS + 2 * kTaKeys;
+  // The tensor core cuts its fp32 sums off instead of rounding them: 64 keys cost about 4.4e-7 of the final sum,
+  // always toward zero (measured: values of one sign, 1,001 tiles in one accumulator, 4.4e-4). So the accumulator is
+  // added to sums that round to nearest, and started afresh, every kFlush tiles: 8 with fp32 queries; 16
+  // with bf16 queries, 7e-6, no more than their weights' own rounding.
+  static constexpr int kFlush = sizeof(T) == 4 ? 8 : 16;
+  // Of the D / 2 dimensions that a thread looks after kSumsT are summed in tensor memory, where it has room, and
+  // the others in registers. Once for 16 tiles the softmax stops for it between two tiles (64 bf16 nodes over 32K
+  // 46.1 us; inside the loop over tiles, whose code it makes slower, 48.6; without these sums 43.7); more often it is
+  // better woven in (fp32, 64 nodes 70.8 us, between tiles 74.9).
+  static constexpr bool kBetween = sizeof(T) == 2;
+  static constexpr int kSumsT = kBetween ? 32 : 0;
+  static constexpr int kColSums = kColP + kPlaces * kTermCols;
   static_assert(!kTight || kTermsP == 3, "the turns of the places");
   // Columns of term t (0 the largest) of tile j's weights.
   __device__ static __forceinline__ int weights(int j, int t) {
@@ -84,14 +97,10 @@ struct TaShape {
   // bank conflicts.
   static constexpr int kQRow = D / 2 * (int)sizeof(T), kQPitch = kQRow + 16;
   static constexpr int kQSlot = kStages - (kTaSoftmax * kQPitch + kSlot - 1) / kSlot;  // first ring slot they use
-  // The tensor core cuts its fp32 sums off instead of rounding them, about 2^-25 of the sum lost
-  // per 16 keys and term. With fp32 queries the accumulator is therefore added to registers and
-  // started afresh every kFlush tiles; next to a bf16 output the loss does not count.
-  static constexpr int kFlush = sizeof(T) == 4 ? 8 : 0;
   static constexpr int kPitch = D + 4;                     // floats: staged output rows
   static constexpr int kSmem = kStages * kSlot + kLowBytes + 1024;  // and alignment
   static_assert(kQSlot >= kTaFirst, "the queries' staging slots are filled after them");
-  static_assert(kColP + kPlaces * kTermCols <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kColSums + 2 * kSumsT <= kTaTmemCols, "tensor-memory columns");
   static_assert(128 * kPitch * 4 <= kStages * kSlot, "the output is staged in the ring");
 };
 
@@ -144,8 +153,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   // computed here, before the wait below (and with fewer registers spilled)
   asm volatile("" : "+r"(g), "+r"(mt), "+r"(rows), "+r"(t0), "+r"(n));
   for (int x = i; x < kPieces * kBars; x += kTaThreads) {
-    const int b = x % kBars - 2 * S::kStages;  // the groups' four warps arrive at pfull, sfree and flushed, all eight at qfull
-    bar_init(smem_u32(bars) + 8 * x, b == 2 || b == 3 || b == 6 || b == 7 || b == 11 ? 4 : b == 10 ? kTaSoftmax / 32 : b == 12 ? 2 : 1);
+    const int b = x % kBars - 2 * S::kStages;  // the groups' four warps arrive at pfull and sfree, all eight at qfull and flushed
+    bar_init(smem_u32(bars) + 8 * x, b == 2 || b == 3 || b == 6 || b == 7 ? 4 : b == 10 || b == 11 ? kTaSoftmax / 32 : b == 12 ? 2 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (i == 0) {
@@ -240,10 +249,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if (elect_one()) {
         for (int j = 0; j < n; ++j) {
           const int k = ring_val(j, n);
-          constexpr int kF = S::kFlush ? S::kFlush : 1;
-          const bool fresh = S::kFlush ? j % kF == 0 : j == 0;
+          const bool fresh = j % S::kFlush == 0;
           bool ok = wait(full(k), turn(k));
-          if (S::kFlush && fresh && j > 0) ok = ok && wait(flushed, (j / kF - 1) & 1);  // the other group has taken its part
+          if (fresh && j > 0) ok = ok && wait(flushed, (j / S::kFlush - 1) & 1);  // the other group has taken its part
           if (!ok || !wait(pfull0 + 8 * (j & 1), (j >> 1) & 1)) break;
           tm_fence_after();
           const uint64_t bd = sdesc(slot(k), kTaKeys * 128);
@@ -330,12 +338,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const uint32_t ocol = tl + S::kColO + group * kDims;  // its half of the accumulator
       const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
       float m = -INFINITY, l = 0.0f;  // the lane's reference maximum (log2 units) as this group knows it, its weight sum
-      constexpr int kF = S::kFlush ? S::kFlush : 1;
-      float acc[S::kFlush ? kDims : 1];
-      if constexpr (S::kFlush > 0) {
+      // What the accumulator has been added to, in units of a reference of its own.
+      constexpr int kRegs = kDims - S::kSumsT;
+      float acc[kRegs > 0 ? kRegs : 1], sums_m = -INFINITY;
+      bool summed = false;
+      if constexpr (kRegs > 0) {
 #pragma unroll
-        for (int e = 0; e < kDims; ++e) acc[e] = 0.0f;
+        for (int e = 0; e < kRegs; ++e) acc[e] = 0.0f;
       }
+      const uint32_t tsums = tl + S::kColSums + group * S::kSumsT;
       // After a wait that ran out a warp keeps walking the tiles, as the other group's turns need it,
       // and leaves the rest out.
       bool ok = true;
@@ -348,26 +359,49 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       auto rescale = [&](float to) {  // what this thread holds, to another reference
         const float corr = m == to ? 1.0f : ex2(m - to);
         l *= corr;
-        if constexpr (S::kFlush > 0) {
-#pragma unroll
-          for (int e = 0; e < kDims; ++e) acc[e] *= corr;
-        }
         m = to;
         return corr;
       };
-      auto flush = [&](int j, float corr) {  // the accumulator before tile j, times corr, into registers
+      // o, dimensions c .. c + 15 in units of reference `unit`, plus what has been summed of them.
+      auto with_sums = [&](int c, float (&o)[16], float scale) {
+        if (c < S::kSumsT) {
+          if (summed) {
+            float old[16];
+            tm_load(tsums + c, old);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(old[e], scale, o[e]);
+          }
+        } else if constexpr (kRegs > 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(acc[c - S::kSumsT + e], scale, o[e]);
+        }
+      };
+      // The accumulator before tile j, in units of reference `unit`, to the sums.
+      auto flush = [&](int j, float unit) {
         done(j - 1);
         if (ok && !idle) {
-          if constexpr (S::kFlush > 0) {
+          const float scale = sums_m == unit ? 1.0f : ex2(sums_m - unit);
 #pragma unroll
-            for (int c = 0; c < kDims; c += 16) {
-              float o[16];
-              tm_load(ocol + c, o);
+          for (int c = 0; c < kDims; c += 16) {
+            float o[16];
+            tm_load(ocol + c, o);
+            with_sums(c, o, scale);
+            if (c < S::kSumsT) {
+              uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[c + e] = fmaf(o[e], corr, acc[c + e]);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e]);
+              tm_store(tsums + c, w);
+            } else if constexpr (kRegs > 0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[c - S::kSumsT + e] = o[e];
             }
           }
+          if constexpr (S::kSumsT > 0) tm_st_wait();
+          sums_m = unit;
+          summed = true;
         }
+        tm_fence_before();
+        if (ok) bar_arrive_warp(flushed, lane);
       };
       auto room = [&](int j) {  // for tile j's weights: what stood in their places has been read
         if (!S::kTight) {
@@ -377,148 +411,150 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           tm_fence_after();
         }
       };
-      for (int j = group; j < n; j += 2) {
-        const int t = t0 + j;
-        const bool tree = t >= a.pre_tiles;
-        ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
-        tm_fence_after();
-        float s[kCols];
-        if (ok && !idle) {
-          tm_load(tl + S::kColS + group * kTaKeys + c0, s);
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
-        }
+      auto commit = [&]() {
+        tm_st_wait();
         tm_fence_before();
-        if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
-        if (tree) {  // take tree values that are not finite out of the product
-          const int k = ring_val(j, n);
-          ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
-          bool bad = false;
-          for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
-            uint4* p = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
-            const uint4 v = *p;
-            if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
-              uint16_t* h = reinterpret_cast<uint16_t*>(p);
-              for (int x = 0; x < 8; ++x)
-                if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
-              bad = true;
-            }
-          }
-          if (bad) s_bad = 1;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
-        if (tree || left < kTaKeys) {
-          uint64_t seen = ~0ull;
-          if (tree) {
-            const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
-            seen = w[0];
-            if (left > 32) seen |= (uint64_t)w[1] << 32;
-          }
-          if (left < kTaKeys) seen &= (1ull << left) - 1;
-          if (!live) seen = 0;
-          seen >>= c0;
+        if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
+      };
+      float unit = -INFINITY;  // the row's reference before this group's tile
+      // The accumulator starts afresh at tiles j0 = kFlush, 2 kFlush, ...: group 1 adds it to the sums after its
+      // tile j0 - 1, group 0 with its weights of tile j0 ready.
+      for (int j = group, j0 = S::kFlush;; j += 2, j0 += S::kFlush) {
+        const int stop = S::kBetween && j0 < n ? j0 - group : n;
+        for (; j < n; j += 2) {
+          const int t = t0 + j;
+          const bool tree = t >= a.pre_tiles;
+          ok = ok && bar_wait_warp(sfull0 + 8 * group, (j >> 1) & 1, fail, a.timeout_ns);
+          tm_fence_after();
+          float s[kCols];
+          if (ok && !idle) {
+            tm_load(tl + S::kColS + group * kTaKeys + c0, s);
+          } else {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (!(seen >> c & 1)) s[c] = -INFINITY;
-        }
-        float mx2[2] = {s[0], s[1]};
-#pragma unroll
-        for (int c = 2; c + 1 < kCols; c += 2) mx2[c >> 1 & 1] = max3(mx2[c >> 1 & 1], s[c], s[c + 1]);
-        const float mx = fmaxf(mx2[0], mx2[1]) * a.scale_log2;
-        if (S::kFlush > 0 && group == 1 && j > 1 && (j - 1) % kF == 0) {  // the other group's tile starts afresh
-          flush(j - 1, 1.0f);
+            for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
+          }
           tm_fence_before();
-          if (ok) bar_arrive_warp(flushed, lane);
-        }
-        // this tile's reference, after the one of the tile before it
-        const bool restart = S::kFlush > 0 && group == 0 && j > 0 && j % kF == 0;
-        float pend = 1.0f;  // rescaling of what this group's flush adds
-        if (j > 0) turn_wait(quarter, group);
-        if (!idle) {
-          const float known = s_m[ln];
-          if (__any_sync(0xffffffffu, known != m || mx > m + kTaLazy)) {
-            rescale(known);
-            if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
-              const float corr = rescale(fmaxf(m, mx));
-              s_m[ln] = m;
-              if (restart) {
-                pend = corr;
-              } else if (j > 0) {
-                if (j > 1) done(j - 2);  // room(j - 2) told of j - 4
-                done(j - 1);
-#pragma unroll 1
-                for (int c = 0; ok && c < D; c += 16) {
-                  float o[16];
-                  tm_load(tl + S::kColO + c, o);
-                  uint32_t w[16];
+          if (ok) bar_arrive_warp(sfree0 + 8 * group, lane);
+          if (tree) {  // take tree values that are not finite out of the product
+            const int k = ring_val(j, n);
+            ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
+            bool bad = false;
+            for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
+              uint4* p = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
+              const uint4 v = *p;
+              if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
+                uint16_t* h = reinterpret_cast<uint16_t*>(p);
+                for (int x = 0; x < 8; ++x)
+                  if ((h[x] & 0x7f80u) == 0x7f80u) h[x] = 0;
+                bad = true;
+              }
+            }
+            if (bad) s_bad = 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          const int left = tree ? a.B - (t - a.pre_tiles) * kTaKeys : a.prefix - t * kTaKeys;  // keys of the tile
+          if (tree || left < kTaKeys) {
+            uint64_t seen = ~0ull;
+            if (tree) {
+              const uint32_t* w = a.mask + (int64_t)(live ? b : 0) * a.words + (t - a.pre_tiles) * 2;
+              seen = w[0];
+              if (left > 32) seen |= (uint64_t)w[1] << 32;
+            }
+            if (left < kTaKeys) seen &= (1ull << left) - 1;
+            if (!live) seen = 0;
+            seen >>= c0;
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
-                  tm_store(tl + S::kColO + c, w);
+            for (int c = 0; c < kCols; ++c)
+              if (!(seen >> c & 1)) s[c] = -INFINITY;
+          }
+          float mx2[2] = {s[0], s[1]};
+#pragma unroll
+          for (int c = 2; c + 1 < kCols; c += 2) mx2[c >> 1 & 1] = max3(mx2[c >> 1 & 1], s[c], s[c + 1]);
+          const float mx = fmaxf(mx2[0], mx2[1]) * a.scale_log2;
+          if (!S::kBetween && group == 1 && j > 1 && (j - 1) % S::kFlush == 0) flush(j - 1, m);
+          // this tile's reference, after the one of the tile before it
+          if (j > 0) turn_wait(quarter, group);
+          if (!idle) {
+            const float known = s_m[ln];
+            unit = known;
+            if (__any_sync(0xffffffffu, known != m || mx > m + kTaLazy)) {
+              rescale(known);
+              if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+                const float corr = rescale(fmaxf(m, mx));
+                s_m[ln] = m;
+                if (j % S::kFlush != 0) {  // the accumulator starts afresh otherwise
+                  if (j > 1) done(j - 2);  // room(j - 2) told of j - 4
+                  done(j - 1);
+#pragma unroll 1
+                  for (int c = 0; ok && c < D; c += 16) {
+                    float o[16];
+                    tm_load(tl + S::kColO + c, o);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
+                    tm_store(tl + S::kColO + c, w);
+                  }
                 }
               }
             }
           }
-        }
-        if (j + 1 < n) turn_pass(quarter, group);
-        if (!idle && ok) {
-          const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
-          float2 ls = make_float2(0.0f, 0.0f);
-          const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
+          if (j + 1 < n) turn_pass(quarter, group);
+          if (!idle && ok) {
+            const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+            float2 ls = make_float2(0.0f, 0.0f);
+            const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-mu, -mu);
 #pragma unroll
-          for (int ch = 0; ch < kCols; ch += 16) {  // 16 keys at a time, for the registers' sake
-            uint32_t w[S::kTermsP][8];
+            for (int ch = 0; ch < kCols; ch += 16) {  // 16 keys at a time, for the registers' sake
+              uint32_t w[S::kTermsP][8];
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              const float2 x = fma2(make_float2(s[ch + c], s[ch + c + 1]), sc, mm);
-              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
-              ls = add2(ls, pp);
-              uint32_t term[S::kTermsP];
-              split(pp.x, pp.y, term);
+              for (int c = 0; c < 16; c += 2) {
+                const float2 x = fma2(make_float2(s[ch + c], s[ch + c + 1]), sc, mm);
+                const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+                ls = add2(ls, pp);
+                uint32_t term[S::kTermsP];
+                split(pp.x, pp.y, term);
 #pragma unroll
-              for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
+                for (int tt = 0; tt < S::kTermsP; ++tt) w[tt][c / 2] = term[tt];
+              }
+              if (ch == 0) room(j);
+#pragma unroll
+              for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(tl + S::weights(j, tt) + (c0 + ch) / 2, w[tt]);
             }
-            if (ch == 0) room(j);
+            l += ls.x + ls.y;
+            if constexpr (DUP > 1) {  // the keys that other lanes weigh
 #pragma unroll
-            for (int tt = 0; tt < S::kTermsP; ++tt) tm_store(tl + S::weights(j, tt) + (c0 + ch) / 2, w[tt]);
+              for (int tt = 0; tt < S::kTermsP; ++tt)
+#pragma unroll
+                for (int c = 0; c < kTaKeys / 2; c += 8)
+                  if (c / (kCols / 2) != part) tm_store(tl + S::weights(j, tt) + c, zero);
+            }
           }
-          l += ls.x + ls.y;
-          if constexpr (DUP > 1) {  // the keys that other lanes weigh
-#pragma unroll
-            for (int tt = 0; tt < S::kTermsP; ++tt)
-#pragma unroll
-              for (int c = 0; c < kTaKeys / 2; c += 8)
-                if (c / (kCols / 2) != part) tm_store(tl + S::weights(j, tt) + c, zero);
-          }
+          // An idle warp also waits for its group's last products: its arrival below must not count for them.
+          if (idle) room(j);
+          if (j == stop) break;
+          if (!S::kBetween && group == 0 && j > 0 && j % S::kFlush == 0) flush(j, unit);
+          commit();
         }
-        // An idle warp also waits for its group's last products: its arrival below must not count for them.
-        if (idle) room(j);
-        if (restart) flush(j, pend);
-        tm_st_wait();
-        tm_fence_before();
-        if (ok) bar_arrive_warp(pfull0 + 8 * group, lane);
+        if (j >= n) break;
+        if (group == 1) commit();
+        flush(j0, group == 1 ? m : unit);
+        if (group == 0) commit();
       }
-      if (S::kFlush > 0 && group == 1 && n > 1 && (n - 1) % kF == 0) {  // the last tile is the other group's, and starts afresh
-        flush(n - 1, 1.0f);
-        tm_fence_before();
-        if (ok) bar_arrive_warp(flushed, lane);
-      }
+      // the last tile is the other group's, and starts afresh
+      if (!S::kBetween && group == 1 && n > 1 && (n - 1) % S::kFlush == 0) flush(n - 1, m);
       // the row's accumulator, staged in the ring (every copy and MMA has finished by then)
       ok = bar_wait_warp(drain, 0, fail, a.timeout_ns) && ok;
       tm_fence_after();
       asm volatile("bar.sync 9, 256;" ::: "memory");  // both groups' last word on the references
       if (ok) {
         rescale(s_m[ln]);
+        const float scale = sums_m == m ? 1.0f : ex2(sums_m - m);
         float* st = reinterpret_cast<float*>(ring) + ln * S::kPitch + group * kDims;
 #pragma unroll
         for (int c = 0; c < kDims; c += 16) {
           float o[16];
           tm_load(ocol + c, o);
-          if constexpr (S::kFlush > 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += acc[c + e];
-          }
+          with_sums(c, o, scale);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(st + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }

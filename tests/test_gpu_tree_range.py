@@ -1,0 +1,63 @@
+"""The tree-verify operators over the whole range that their calls accept: long sums, groups of rows, a whole pass in the
+order in which a program makes it. References are in 64 bits; tolerances count roundings (fp32 2^-24, bf16 2^-8)."""
+import numpy as np
+import pytest
+import torch
+
+from packed_weight_gemv_gb300 import nt
+from tests import _tree
+from tests._gpu import DEV, dev, host
+
+pytestmark = pytest.mark.gpu
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ---- attention -------------------------------------------------------------------------------
+@pytest.mark.parametrize("B,D,tiles,dtype", [(36, 128, 1600, "bf16"), (70, 128, 1001, "bf16"), (36, 64, 1600, "bf16"),
+                                             (70, 64, 1601, "bf16"), (36, 64, 1600, "f32"), (70, 128, 1001, "f32")])
+def test_attention_sums_of_one_sign_keep_their_bits(B, D, tiles, dtype):
+    """A head to a block and values of one sign: a thousand tiles and more go to one accumulator, and what the tensor core cuts
+    off its sums cannot cancel. A sum loses at most one step, 2^-23, per 16 keys and weight term while it stays in tensor
+    memory: 12 per tile over 8 tiles with fp32 queries, 8 over 16 with bf16 ones. What it is added to rounds to nearest.
+    A bf16 output has rounded, so the loss shows in the mean over many outputs, whose values spread over a binade (a scale to
+    every head and dimension): the bf16 rounding and the weights' own (2^-18 each) have no side and are allowed five standard
+    deviations of that mean."""
+    Hkv, prefix = 152, 64 * (tiles - (B + 63) // 64)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(B + D)
+    ts = prefix + B
+    q = torch.randn(B, Hkv, D, generator=g, device=DEV).mul_(0.5).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    k, v = (torch.empty(Hkv, ts, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for h in range(Hkv):
+        k[h] = torch.randn(ts, D, generator=g, device=DEV).mul_(0.25).bfloat16()
+        v[h] = ((1 + torch.rand(ts, D, generator=g, device=DEV) * 0.5) * torch.rand(D, generator=g, device=DEV).exp2()).bfloat16()
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(B), B))
+    ws = torch.zeros(nt.nt_tree_attention_workspace_size(B, Hkv, Hkv, D, prefix), dtype=torch.uint8, device=DEV)
+    outs = []
+    for _ in range(3):
+        out = torch.empty_like(q)
+        nt.nt_tree_attention(q, k, v, prefix, prefix, dev(_tree.pack(sees)), out, ws)
+        torch.cuda.synchronize()
+        assert nt.nt_workspace_status(ws) == nt.NT_OK
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    off = np.empty((Hkv, B, D))
+    for h in range(Hkv):
+        s = q[:, h].double() @ k[h].double().T / D ** 0.5
+        s[:, prefix:] = s[:, prefix:].masked_fill(~dev(sees), float("-inf"))
+        want = s.softmax(-1) @ v[h].double()
+        off[h] = host(outs[0][:, h].double() / want - 1)
+    loss = (8 * 16 if dtype == "bf16" else 12 * 8) * 2 * U32
+    # scores (sqrt(D) roundings of |q| |k| / sqrt(D), twice: in a weight and in the weights' sum), sums, exponentials and quotient
+    rest = 2 * U32 * (2 * 0.5 * 0.25 * D ** 0.5 * 1.5 + tiles ** 0.5 + 16)
+    mean, worst = float(off.mean()), float(np.abs(off).max())
+    if dtype == "f32":
+        assert worst <= loss + rest, (worst, loss, rest)
+    else:
+        spread = off.mean(1).std() / (Hkv * D) ** 0.5  # a head's nodes have much the same sums: one sample for all of them
+        assert abs(mean) <= loss + 5 * spread, (mean, loss, spread, worst)
+        assert worst <= U16 + loss + rest + 2.0 ** -18, worst
