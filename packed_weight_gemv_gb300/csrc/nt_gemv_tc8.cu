@@ -175,7 +175,7 @@ __device__ __forceinline__ void tc8_cta(const CUtensorMap* tmW_, const CUtensorM
   const int kb0 = part * p.kb_per_part;
   const int nkb = (p.kblocks - kb0 < p.kb_per_part) ? p.kblocks - kb0 : p.kb_per_part;
 
-  dependent_launch_wait();
+  dependent_launch_join();
   if (t == 0) {
     for (int s = 0; s < kTc8Stages; ++s) {
       bar_init(full0 + 8 * s, 1);
@@ -198,6 +198,7 @@ __device__ __forceinline__ void tc8_cta(const CUtensorMap* tmW_, const CUtensorM
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  dependent_launch_begin();  // not before every CTA has its tensor memory
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 4) {
