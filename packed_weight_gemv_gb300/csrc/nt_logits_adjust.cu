@@ -55,7 +55,7 @@ struct AdjArgs {
   int mask_words;
   const int32_t* tokens;  // [B] the nodes' tokens
   float rep, freq, pres;
-  float rep_inv;  // 1 / rep rounded, 0 where quotient() does not apply
+  float rep_inv;  // 1 / rep rounded, 0 where quotient() does not hold
   const float* bias;
   int64_t bias_stride;
   const uint32_t* allowed;  // rows allowed_stride words apart
@@ -68,7 +68,9 @@ struct AdjArgs {
 
 // x / rep rounded to nearest, by Markstein's method (IBM J. Res. Dev. 34, 1990): with y = 1 / rep
 // rounded, one step q + (x - rep q) y brings q = x y within an ulp, and a second one, whose remainder
-// is exact, to the rounded quotient. It holds while nothing leaves the normal range: `plain`.
+// is exact, to the rounded quotient. It holds while the quotient is normal and the remainder's last bit is
+// no less than 2^-149: for 2^-24 <= rep <= 2^24 and 2^-100 <= |x| < 2^100 the quotient is within 2^-124 and
+// 2^124, and the last bits of rep and q multiply to 2^-148 at least.
 struct Pair {  // two fp32 values that one instruction works on
   float x, y;
 };
@@ -479,7 +481,7 @@ nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* cou
   AdjArgs a{logits, B, V, counts_opt, counts_stride, tree_mask_opt, mask_words, tokens_opt, repetition, frequency,
             presence, 0.0f, bias_opt, bias_stride, allowed_opt, allowed_stride, out_opt, argmax_opt, static_cast<AdjWs*>(ws),
             1};
-  if (repetition > 1e-9f && repetition < 1e9f) a.rep_inv = 1.0f / repetition;
+  if (repetition >= 0x1p-24f && repetition <= 0x1p24f) a.rep_inv = 1.0f / repetition;
   const bool vec = V % 4 == 0 && aligned(logits, 16) && (!out_opt || aligned(out_opt, 16)) &&
                    (!counts_opt || (aligned(counts_opt, 16) && counts_stride % 4 == 0)) &&
                    (!bias_opt || (aligned(bias_opt, 16) && bias_stride % 4 == 0));

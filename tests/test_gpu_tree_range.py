@@ -61,3 +61,24 @@ def test_attention_sums_of_one_sign_keep_their_bits(B, D, tiles, dtype):
         spread = off.mean(1).std() / (Hkv * D) ** 0.5  # a head's nodes have much the same sums: one sample for all of them
         assert abs(mean) <= loss + 5 * spread, (mean, loss, spread, worst)
         assert worst <= U16 + loss + rest + 2.0 ** -18, worst
+
+
+# ---- logits ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("rep", [2e-9, 5.9e-8, 2.0 ** -24, 6.1e-8, 1.6e7, 2.0 ** 24, 1.7e7, 9e8, 1.5e-9, 9.99e8])
+def test_adjust_quotients_where_they_leave_the_range(rep):
+    """Values whose quotients overflow, are subnormal or lie next to either, one by one (listed tokens) and all together."""
+    rs = np.random.RandomState(3)
+    sig = np.concatenate([1 + rs.rand(4000), [1.0, 2 - 2.0 ** -23, 1.5, 1.4142135]]).astype(np.float32)
+    x = np.concatenate([np.ldexp(sig, e) for e in (-149, -126, -125, -101, -100, -99, 0, 98, 99, 100, 126, 127)]).astype(np.float32)
+    x = np.concatenate([x, -x, np.float32([0.0, -0.0, np.inf, -np.inf])])
+    with np.errstate(over="ignore", under="ignore"):
+        r = np.float32(rep)
+        want = np.where(x > 0, x / r, x * r)
+    for every in (1, 37):
+        counts = (np.arange(x.size) % every == 0).astype(np.int32)
+        out, arg = torch.empty(1, x.size, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+        ws = torch.zeros(nt.nt_logits_adjust_workspace_size(x.size, 1), dtype=torch.uint8, device=DEV)
+        nt.nt_logits_adjust(dev(x[None]), counts=dev(counts), repetition=rep, out=out, argmax=arg, ws=ws)
+        full = np.where(counts > 0, want, x)[None]
+        assert np.array_equal(host(out), full)
+        assert np.array_equal(host(arg), _tree.choice(full))
