@@ -21,16 +21,12 @@
 
 #include <algorithm>
 
+#include "nt_adjust_plan.cuh"
 #include "nt_tree.cuh"
 
 namespace nt {
 namespace {
 
-constexpr int kAdjThreads = 256;
-constexpr int kAdjPer = 8;                  // tokens per thread
-constexpr int kAdjChunk = kAdjPer * kAdjThreads;
-constexpr int kAdjPerSm = 4;                // CTAs that an SM holds (64 registers a thread; asking the compiler for 4 cost 2 us)
-constexpr int kAdjRows = 16;                // rows of a group at most
 constexpr int kAdjAhead = 4;                // rows of the ring in shared memory
 constexpr int kAdjEach = 2;                 // used tokens per lane that are adjusted one by one
 constexpr int kAdjFew = 32 * kAdjEach;      // so many of a warp's 256
@@ -490,13 +486,8 @@ nt_status nt_logits_adjust(const float* logits, int B, int V, const int32_t* cou
                          : (argmax_opt ? adjust_kernel<4, false, true> : adjust_kernel<4, false, false>))
                   : (pen ? (argmax_opt ? adjust_kernel<1, true, true> : adjust_kernel<1, true, false>)
                          : (argmax_opt ? adjust_kernel<1, false, true> : adjust_kernel<1, false, false>));
-  // Groups of rows: as many as one wave of CTAs holds, alike, or whole waves of them where a group would have
-  // too many rows (64 rows of 151,936, 75 chunks, 608 CTAs at a time, in a graph: 7 groups 18.5 us, 8 16.1, 10 18.6).
-  const int chunks = (V + kAdjChunk - 1) / kAdjChunk;
-  const int wave = std::max(1, kAdjPerSm * device_sm_count() / chunks), least = (B + kAdjRows - 1) / kAdjRows;
-  const int groups = std::min(B, (least + wave - 1) / wave * wave);
-  a.group = (B + groups - 1) / groups;
-  const dim3 grid(chunks, (B + a.group - 1) / a.group);
+  a.group = adjust_group(B, V, device_sm_count());
+  const dim3 grid((V + kAdjChunk - 1) / kAdjChunk, (B + a.group - 1) / a.group);
   NT_CUDA_TRY(launch_kernel(kern, grid, dim3(kAdjThreads), 0, reinterpret_cast<cudaStream_t>(stream), true, a));
   return check_launch("adjust_kernel");
 }

@@ -7,6 +7,8 @@ import torch
 from packed_weight_gemv_gb300 import nt
 from tests import _tree
 from tests._gpu import DEV, dev, host
+from tests.test_gpu_tree import run_adjust
+from tests.test_tree_plans_cpu import GROUPED_ROWS
 
 pytestmark = pytest.mark.gpu
 U32, U16 = 2.0 ** -24, 2.0 ** -8
@@ -82,3 +84,33 @@ def test_adjust_quotients_where_they_leave_the_range(rep):
         full = np.where(counts > 0, want, x)[None]
         assert np.array_equal(host(out), full)
         assert np.array_equal(host(arg), _tree.choice(full))
+
+
+@pytest.mark.parametrize("group,B,V", GROUPED_ROWS)
+@pytest.mark.parametrize("kind", ["paths", "rows", "in place"])
+def test_adjust_rows_in_groups(group, B, V, kind):
+    """Several rows to a block: the ring of rows goes round, every row has its own path, allowed words and (rows) counts and
+    biases, the last group is ragged; against the fp32 evaluation step by step, twice on one workspace."""
+    assert group > 1 and torch.cuda.get_device_properties(DEV).multi_processor_count == 152
+    run_adjust(B, V, True, "row", True, seed=B, strided=kind == "rows", inplace=kind == "in place", want_out=V != 40004)
+
+
+@pytest.mark.parametrize("V", [151936, 151935])
+def test_adjust_groups_with_the_same_tokens_on_many_nodes(V):
+    """A token on several nodes of a path counts once for each, in every row of a group, listed (few used tokens) or not."""
+    rs = np.random.RandomState(V)
+    B = 64
+    x = (rs.randn(B, V) * 4).astype(np.float32)
+    sees = _tree.ancestors(_tree.parents(rs, B))
+    for every in (3000, 3):
+        counts = np.where(np.arange(V) % every == 0, 1 + rs.randint(0, 3, V), 0).astype(np.int32)
+        tokens = rs.choice([7, 8, 2000, 2047, 2048, V - 1, V // 2], B).astype(np.int32)
+        full = np.stack([counts + np.bincount(tokens[s], minlength=V) for s in sees]).astype(np.int32)
+        want = _tree.adjust(x, full, 1.3, 0.25, -0.5, None, None, np.float32)
+        out, arg = torch.empty(B, V, device=DEV), torch.empty(B, dtype=torch.int32, device=DEV)
+        ws = torch.zeros(nt.nt_logits_adjust_workspace_size(V, B), dtype=torch.uint8, device=DEV)
+        for _ in range(2):
+            nt.nt_logits_adjust(dev(x), counts=dev(counts), tree_mask=dev(_tree.pack(sees)), tokens=dev(tokens), repetition=1.3,
+                                frequency=0.25, presence=-0.5, out=out, argmax=arg, ws=ws)
+            assert np.array_equal(host(out), want) and np.array_equal(host(arg), _tree.choice(want))
+            assert not ws.any()
