@@ -8,6 +8,7 @@ rebuilt when it or any header is newer than its object.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libnt.so")
 BIND = os.path.join(OUT_DIR, "_ntbind.so")
+BIND_STAMP = BIND + ".for"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,12 +40,26 @@ def _flags(extra=()):
             "-I", CSRC, "--expt-relaxed-constexpr", *extra]
 
 
-def build_binding() -> str:
-    """csrc/nt_binding.cpp against this machine's torch and Python headers."""
+def binding_stamp() -> str:
+    """What the native binding is compiled against besides its sources."""
+    return "\n".join((sys.version, sysconfig.get_paths()["include"], importlib.metadata.version("torch"),
+                      importlib.util.find_spec("torch").origin))
+
+
+def binding_is_current() -> bool:
     src = os.path.join(CSRC, "nt_binding.cpp")
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "nt.h")))
-    if os.path.exists(BIND) and os.path.getmtime(BIND) >= newest:
+    if not os.path.exists(BIND) or os.path.getmtime(BIND) < newest or not os.path.exists(BIND_STAMP):
+        return False
+    with open(BIND_STAMP) as f:
+        return f.read() == binding_stamp()
+
+
+def build_binding() -> str:
+    """csrc/nt_binding.cpp against this machine's torch and Python headers; again when either is another one."""
+    if binding_is_current():
         return BIND
+    src = os.path.join(CSRC, "nt_binding.cpp")
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = BIND + f".{os.getpid()}.tmp"
@@ -55,6 +71,8 @@ def build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on nt_binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(BIND_STAMP, "w") as f:
+        f.write(binding_stamp())
     return BIND
 
 

@@ -20,6 +20,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libnt.so")
 BIND_PATH = os.path.join(_HERE, "_lib", "_ntbind.so")
+_BUILD = "build it with `python -c 'import __graft_entry__ as g; g.build()'`"
 
 NT_OK = 0
 NT_ERR_INVALID_ARG = 1
@@ -109,15 +110,13 @@ _BOUND = ("nt_last_error_string", "nt_qk_norm_rope_append", "nt_tree_layout", "n
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Loads libnt.so and its native binding (once). Raises if one is missing: there is no other implementation."""
-    global _lib, _bind
+    """Loads libnt.so (once). Raises if it is missing: there is no other implementation."""
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
-        for p in (path, BIND_PATH):
-            if not os.path.exists(p):
-                raise RuntimeError(f"{p} is missing: build it with "
-                                   "`python -c 'import __graft_entry__ as g; g.build()'`")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: {_BUILD}")
         lib = ctypes.CDLL(path)
         i, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
         i64, f, d = ctypes.c_int64, ctypes.c_float, ctypes.c_double
@@ -173,11 +172,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        loader = importlib.machinery.ExtensionFileLoader("_ntbind", BIND_PATH)
-        bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ntbind", loader))
-        loader.exec_module(bind)
-        bind.init(NtError, *[ctypes.cast(getattr(lib, name), vp).value for name in _BOUND])
-        _bind = bind
         _lib = lib
         return lib
 
@@ -366,8 +360,23 @@ def nt_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, B: int, D: int, eps: float,
 # the tensors and refuses what the C ABI cannot see (another type, other shapes, elements that are
 # not contiguous) with the same exception.
 def _native():
-    if _bind is None:
-        load_library()
+    """The native binding, loaded by the first call that needs it. It is compiled against one torch and one Python."""
+    global _bind
+    if _bind is not None:
+        return _bind
+    lib = load_library()
+    with _lock:
+        if _bind is None:
+            if not os.path.exists(BIND_PATH):
+                raise RuntimeError(f"{BIND_PATH} is missing: {_BUILD}")
+            loader = importlib.machinery.ExtensionFileLoader("_ntbind", BIND_PATH)
+            try:
+                bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ntbind", loader))
+                loader.exec_module(bind)
+            except ImportError as e:
+                raise RuntimeError(f"{BIND_PATH} does not load (built for another torch or Python?): {_BUILD}") from e
+            bind.init(NtError, *[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND])
+            _bind = bind
     return _bind
 
 
