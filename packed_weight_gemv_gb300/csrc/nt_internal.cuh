@@ -166,6 +166,8 @@ __device__ __forceinline__ int verify_accept_device(const int32_t* draft, const 
 // First statement of a kernel that may be launched as a programmatic dependent: waits until the
 // previous kernel in the stream has completed and its writes are visible (returns at once when
 // the launch had no such dependency), then lets the next kernel's launch begin.
+// What the previous kernel may still write while this one is resident is not read-only for this one's lifetime:
+// such inputs are neither const __restrict__ nor loaded with __ldg.
 // A kernel that allocates tensor memory does so before it lets the next launch begin, and the CTA's
 // threads meet in between: a CTA of the next kernel holds its own columns while it waits for this grid's end,
 // and a CTA of this grid that then asked for columns on the same SM would wait for it, without end.

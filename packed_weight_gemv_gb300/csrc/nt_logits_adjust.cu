@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   uint32_t next_allowed[2] = {~0u, ~0u};
   auto load_allowed = [&](int r) {
     if (next_word && r < nb) {
-      if (w0 < words) next_allowed[0] = __ldg(next_word + w0);
-      if (VEC == 4 && w1 < words) next_allowed[1] = __ldg(next_word + w1);
+      if (w0 < words) next_allowed[0] = next_word[w0];
+      if (VEC == 4 && w1 < words) next_allowed[1] = next_word[w1];
       next_word += a.allowed_stride;
     }
   };
@@ -178,11 +178,11 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
 #pragma unroll
     for (int e = 0; e < N; e += VEC) {
       if constexpr (VEC == 4) {
-        const uint4 t = on(e) ? __ldg(reinterpret_cast<const uint4*>(row + place(e))) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 t = on(e) ? *reinterpret_cast<const uint4*>(row + place(e)) : make_uint4(0u, 0u, 0u, 0u);
         memcpy(&x[e], &t, 16);
         if (!on(e)) x[e] = x[e + 1] = x[e + 2] = x[e + 3] = none;
       } else {
-        x[e] = on(e) ? __ldg(row + place(e)) : none;
+        x[e] = on(e) ? row[place(e)] : none;
       }
     }
   };
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   if (a.tree_mask) {  // thread = node: a tree has at most kAdjThreads
     // All CTAs read these few lines at once, so a warp asks for as much as it can (with a load per row and
     // node they waited 3 us for one another's).
-    const int t = i < a.B ? __ldg(a.tokens + i) : -1, used_words = (a.B + 31) / 32;
-    if (i < nb * used_words) group_mask[i] = __ldg(a.tree_mask + (int64_t)(b0 + i / used_words) * a.mask_words + i % used_words);
+    const int t = i < a.B ? a.tokens[i] : -1, used_words = (a.B + 31) / 32;
+    if (i < nb * used_words) group_mask[i] = a.tree_mask[(int64_t)(b0 + i / used_words) * a.mask_words + i % used_words];
     if (i == 0) n_path = 0;
     __syncthreads();
     if (t >= v0 && t - v0 < min(kAdjChunk, inside)) {
@@ -404,10 +404,8 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjArgs a) {
   if (i < nb) a.argmax[b0 + i] = best ? (int32_t)~(uint32_t)best : -1;
 }
 
-__global__ void __launch_bounds__(kAdjThreads) count_kernel(const int32_t* __restrict__ tokens,
-                                                            const int32_t* __restrict__ index, int n,
-                                                            const int32_t* __restrict__ n_dev, int V,
-                                                            int32_t* __restrict__ counts, uint32_t* n_bad) {
+__global__ void __launch_bounds__(kAdjThreads) count_kernel(const int32_t* tokens, const int32_t* index, int n,
+                                                            const int32_t* n_dev, int V, int32_t* counts, uint32_t* n_bad) {
   dependent_launch_wait();
   const int m = n_dev ? min(n, *n_dev) : n;
   for (int64_t i = blockIdx.x * kAdjThreads + threadIdx.x; i < m; i += gridDim.x * kAdjThreads) {

@@ -17,9 +17,8 @@ constexpr int kCommitLayers = 128;
 
 // One CTA, thread = node. Pointer jumping: after k rounds a node's bits cover its 2^k nearest
 // ancestors (itself among them) and `up` is the one after those, so 8 rounds do for 256 nodes.
-__global__ void __launch_bounds__(kTreeMaxNodes) tree_layout_kernel(const int32_t* __restrict__ parent, int B,
-                                                                    int pos0, uint32_t* __restrict__ mask, int words,
-                                                                    int32_t* __restrict__ pos, uint32_t* n_bad) {
+__global__ void __launch_bounds__(kTreeMaxNodes) tree_layout_kernel(const int32_t* parent, int B, int pos0, uint32_t* mask,
+                                                                    int words, int32_t* pos, uint32_t* n_bad) {
   __shared__ uint32_t bits[kTreeMaxNodes][kTreeWords + 1];  // one word of padding against bank conflicts
   __shared__ int up[kTreeMaxNodes];
   dependent_launch_wait();
@@ -61,11 +60,9 @@ __global__ void __launch_bounds__(kTreeMaxNodes) tree_layout_kernel(const int32_
 
 // One CTA, thread = node. A node follows its parent when its token is the model's choice there
 // (the lowest such child); the accepted path is the chain of those links from the root.
-__global__ void __launch_bounds__(kTreeMaxNodes) tree_accept_kernel(const int32_t* __restrict__ parent,
-                                                                    const int32_t* __restrict__ token,
-                                                                    const int32_t* __restrict__ choice, int B,
-                                                                    int32_t* __restrict__ emit,
-                                                                    int32_t* __restrict__ path, int32_t* n_emit) {
+__global__ void __launch_bounds__(kTreeMaxNodes) tree_accept_kernel(const int32_t* parent, const int32_t* token,
+                                                                    const int32_t* choice, int B, int32_t* emit,
+                                                                    int32_t* path, int32_t* n_emit) {
   __shared__ int next[kTreeMaxNodes], way[kTreeMaxNodes];
   __shared__ int n_way;
   dependent_launch_wait();

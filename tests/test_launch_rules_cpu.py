@@ -37,3 +37,13 @@ def test_tensor_memory_is_allocated_before_the_next_launch_begins(name, text):
     assert not BEGINS.search(text[:at]), f"{name} lets the next launch begin before it has its tensor memory"
     begin = BEGINS.search(text, at)
     assert begin is None or "__syncthreads();" in text[at:begin.start()], f"{name}: other threads may let the next launch begin earlier"
+
+
+@pytest.mark.parametrize("name", ["nt_tree.cu", "nt_tree.cuh", "nt_tree_attention.cu", "nt_tree_attn.cuh", "nt_tree_few.cu",
+                                  "nt_logits_adjust.cu", "nt_qk_rope.cu"])
+def test_inputs_that_the_kernel_before_writes_are_not_promised_constant(name):
+    """These kernels become resident while the one before still writes their inputs: a load that the language lets the compiler
+    move, or cache for the kernel's lifetime, could return the old data."""
+    text = code(os.path.join(CSRC, name))
+    assert "__ldg(" not in text and "ld.global.nc" not in text
+    assert not re.search(r"const\s+[\w:]+\s*\*\s*__restrict__", text)
