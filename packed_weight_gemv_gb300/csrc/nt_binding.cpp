@@ -2,12 +2,15 @@
 // (nt_qk_norm_rope_append, nt_tree_*, nt_logits_adjust, nt_token_counts): reads torch tensors' types,
 // shapes and strides, refuses what the C ABI cannot see, and calls libnt.so. Their Python forms
 // are in nt.py. Through ctypes a call took 15 to 27 us on the host, most of a small call's time.
+// Among what is refused are tensors of the host or of another GPU than the current one: their addresses would
+// go to the kernel.
 //
 // The module links to no library of its own: init() gets the addresses of the loaded libnt.so's
 // functions and the exception class.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -45,9 +48,38 @@ std::string shape_text(Shape s) {
   return t + "]";
 }
 
+// The tensors of the call at hand; where they are is looked at once types and shapes are in order.
+struct Given {
+  const char* name;
+  bool cuda;
+  c10::DeviceIndex index;
+};
+struct Call {
+  Given given[24];
+  int n = 0;
+  void add(const char* name, c10::Device device) {
+    if (n == (int)(sizeof(given) / sizeof(given[0]))) refuse("too many tensors");
+    given[n++] = Given{name, device.is_cuda(), device.index()};
+  }
+  void check() const {
+    for (int i = 0; i < n; ++i)
+      if (!given[i].cuda) refuse(std::string(given[i].name) + " must be a CUDA tensor");
+    const c10::DeviceIndex current = c10::cuda::current_device();
+    for (int i = 0; i < n; ++i)
+      if (given[i].index != current)
+        refuse(std::string(given[i].name) + " is on cuda:" + std::to_string(given[i].index) + ", not on the current device, cuda:" +
+               std::to_string(current));
+  }
+};
+thread_local Call* t_call = nullptr;  // of guarded() below
+
 const at::Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
   return THPVariable_Unpack(o);
+}
+void* address(const at::Tensor& t, const char* name) {
+  t_call->add(name, t.device());
+  return t.data_ptr();
 }
 
 // Address of a contiguous tensor of this type (and shape, if one is given); None gives NULL.
@@ -58,7 +90,7 @@ T* flat(PyObject* o, const char* name, at::ScalarType dtype, const Shape* shape 
   if (t.scalar_type() != dtype || !t.is_contiguous() || (shape && !t.sizes().equals(*shape)))
     refuse(std::string(name) + " must be a contiguous " + c10::toString(dtype) + " tensor" +
            (shape ? " of shape " + shape_text(*shape) : ""));
-  return static_cast<T*>(t.data_ptr());
+  return static_cast<T*>(address(t, name));
 }
 template <typename T = void>
 T* flat(PyObject* o, const char* name, at::ScalarType dtype, const Shape& shape) {
@@ -72,7 +104,7 @@ const void* rows(PyObject* o, const char* name, at::ScalarType dtype, Shape shap
   if (t.scalar_type() != dtype || !t.sizes().equals(shape) || t.stride(2) != 1 || (n[1] > 1 && t.stride(1) != n[2]))
     refuse(std::string(name) + " must be " + c10::toString(dtype) + " " + shape_text(shape) + " with contiguous heads");
   *stride = n[0] > 1 ? t.stride(0) : n[1] * n[2];
-  return t.data_ptr();
+  return address(t, name);
 }
 
 // Address and row stride of a [n] tensor for all rows or a [B, n] tensor (stride 0: one row for all).
@@ -87,7 +119,7 @@ T* shared(PyObject* o, const char* name, at::ScalarType dtype, int64_t B, int64_
     refuse(std::string(name) + " must be " + c10::toString(dtype) + " " + shape_text({n}) + " or " + shape_text({B, n}) +
            " with contiguous rows");
   if (d == 2 && t.size(0) > 1) *stride = t.stride(0);
-  return static_cast<T*>(t.data_ptr());
+  return static_cast<T*>(address(t, name));
 }
 
 int integer(PyObject* o) {
@@ -106,14 +138,15 @@ int activation(const at::Tensor& t, const char* name) {
   if (t.scalar_type() == kBf16) return NT_BF16;
   refuse(std::string(name) + " must be fp32 or bf16");
 }
-// None: torch's current stream; an object with cuda_stream, or the stream's address.
+// None: torch's current stream; an object with cuda_stream, or the stream's address. The last argument to be read.
 void* stream_of(PyObject* o) {
+  t_call->check();
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-  PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
+  PyObject* a = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
   if (!a) throw PythonError{};
   void* s = PyLong_AsVoidPtr(a);
   Py_DECREF(a);
+  if (PyErr_Occurred()) throw PythonError{};
   return s;
 }
 void* workspace(PyObject* o, size_t* bytes) {
@@ -122,9 +155,16 @@ void* workspace(PyObject* o, size_t* bytes) {
   const at::Tensor& t = tensor(o, "ws");
   if (!t.is_contiguous()) refuse("ws must be contiguous");
   *bytes = t.nbytes();
-  return t.data_ptr();
+  return address(t, "ws");
 }
-uint32_t* counter(PyObject* o) { return flat<uint32_t>(o, "n_bad", kI32); }
+// One number on the device, or None. (A tensor without elements has no address: it would pass for None.)
+template <typename T>
+T* single(PyObject* o, const char* name) {
+  T* p = flat<T>(o, name, kI32);
+  if (o != Py_None && tensor(o, name).numel() < 1) refuse(std::string(name) + " must have an element");
+  return p;
+}
+uint32_t* counter(PyObject* o) { return single<uint32_t>(o, "n_bad"); }
 
 template <typename F>
 nt_status released(F&& f) {
@@ -135,17 +175,19 @@ nt_status released(F&& f) {
 
 // Runs a call; a refusal, here or in the library, becomes an NtError.
 template <typename F>
-PyObject* guarded(const char* call, Py_ssize_t got, Py_ssize_t want, F&& f) {
+PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, F&& f) {
   if (!g_error) {
     PyErr_SetString(PyExc_RuntimeError, "init() first");
     return nullptr;
   }
   if (got != want) {
-    PyErr_Format(PyExc_TypeError, "%s: %zd arguments, not %zd", call, want, got);
+    PyErr_Format(PyExc_TypeError, "%s: %zd arguments, not %zd", name, want, got);
     return nullptr;
   }
   int status = NT_OK;
   std::string what;
+  Call call;
+  t_call = &call;
   try {
     status = f();
     if (status != NT_OK) what = p_last_error();
@@ -159,7 +201,7 @@ PyObject* guarded(const char* call, Py_ssize_t got, Py_ssize_t want, F&& f) {
     return nullptr;
   }
   if (status == NT_OK) Py_RETURN_NONE;
-  if (PyObject* e = PyObject_CallFunction(g_error, "iss", status, call, what.c_str())) {
+  if (PyObject* e = PyObject_CallFunction(g_error, "iss", status, name, what.c_str())) {
     PyErr_SetObject(g_error, e);
     Py_DECREF(e);
   }
@@ -245,7 +287,7 @@ PyObject* counts(PyObject*, PyObject* const* x, Py_ssize_t n) {
     if (m > INT32_MAX || V > INT32_MAX) refuse("a size leaves the int range");
     const auto *tp = flat<int32_t>(x[0], "tokens", kI32), *ip = flat<int32_t>(x[1], "index", kI32);
     if (ip && tensor(x[1], "index").numel() != m) refuse("index must have as many entries as tokens");
-    const auto* np = flat<int32_t>(x[2], "n", kI32);
+    const auto* np = single<const int32_t>(x[2], "n");
     auto* cp = flat<int32_t>(x[3], "counts", kI32);
     uint32_t* bad = counter(x[4]);
     void* st = stream_of(x[5]);
@@ -291,22 +333,23 @@ PyObject* accept(PyObject*, PyObject* const* x, Py_ssize_t n) {
     const auto *p = flat<int32_t>(x[0], "parent", kI32, {B}), *t = flat<int32_t>(x[1], "token", kI32, {B}),
                *a = flat<int32_t>(x[2], "argmax", kI32, {B});
     auto *e = flat<int32_t>(x[3], "emit", kI32, {B}), *w = flat<int32_t>(x[4], "path", kI32, {B}),
-         *m = flat<int32_t>(x[5], "n_emit", kI32);
+         *m = single<int32_t>(x[5], "n_emit");
     void* st = stream_of(x[6]);
     return released([&] { return p_accept(p, t, a, (int)std::min<int64_t>(B, INT32_MAX), e, w, m, st); });
   });
 }
 
-// (k_caches, v_caches: addresses of arrays of n_layers pointers, n_layers, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream)
+// (k_caches, v_caches: addresses of arrays of n_layers pointers, n_layers, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream, the caches' CUDA device or -1)
 PyObject* commit(PyObject*, PyObject* const* x, Py_ssize_t n) {
-  return guarded("nt_tree_commit", n, 11, [&]() -> nt_status {
+  return guarded("nt_tree_commit", n, 12, [&]() -> nt_status {
     auto* kp = static_cast<uint16_t* const*>(PyLong_AsVoidPtr(x[0]));
     auto* vp = static_cast<uint16_t* const*>(PyLong_AsVoidPtr(x[1]));
     if (PyErr_Occurred()) throw PythonError{};
     const int L = integer(x[2]), Hkv = integer(x[3]), D = integer(x[4]), ts = integer(x[5]);
     const int64_t B = tensor(x[6], "path").numel();
-    const auto *p = flat<int32_t>(x[6], "path", kI32), *m = flat<int32_t>(x[7], "n_emit", kI32);
-    const int src = integer(x[8]), dst = integer(x[9]);
+    const auto *p = flat<int32_t>(x[6], "path", kI32), *m = single<int32_t>(x[7], "n_emit");
+    const int src = integer(x[8]), dst = integer(x[9]), at = integer(x[11]);
+    t_call->add("the caches", at < 0 ? c10::Device(c10::kCPU) : c10::Device(c10::kCUDA, (c10::DeviceIndex)at));
     void* st = stream_of(x[10]);
     return released([&] { return p_commit(kp, vp, L, Hkv, D, ts, p, m, (int)std::min<int64_t>(B, INT32_MAX), src, dst, st); });
   });

@@ -358,7 +358,7 @@ def nt_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, B: int, D: int, eps: float,
 # ---- verifying a drafted token tree --------------------------------------------------------
 # These calls go through the native binding (csrc/nt_binding.cpp), which reads shapes and strides from
 # the tensors and refuses what the C ABI cannot see (another type, other shapes, elements that are
-# not contiguous) with the same exception.
+# not contiguous, tensors of the host or of another GPU than the current one) with the same exception.
 def _native():
     """The native binding, loaded by the first call that needs it. It is compiled against one torch and one Python."""
     global _bind
@@ -385,6 +385,8 @@ def nt_rope_frequencies(rotary_dim: int, base: float, inv_freq: torch.Tensor, sc
     """Angles per position of each rotated pair into inv_freq [rotary_dim / 2] float64."""
     if inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous() or 2 * inv_freq.numel() != rotary_dim:
         raise NtError(NT_ERR_INVALID_ARG, "nt_rope_frequencies", "inv_freq must be contiguous float64 [rotary_dim / 2]")
+    if not inv_freq.is_cuda:
+        raise NtError(NT_ERR_INVALID_ARG, "nt_rope_frequencies", "inv_freq must be a CUDA tensor")
     _check(load_library().nt_rope_frequencies(rotary_dim, base, scaling, factor, trained_len, slow, fast,
                                               inv_freq.data_ptr(), _stream(stream)), "nt_rope_frequencies")
 
@@ -454,9 +456,12 @@ class pointer_array:
     def __init__(self, tensors: Sequence[torch.Tensor]):
         self._keep = list(tensors)
         self.shape = tuple(self._keep[0].shape) if self._keep else ()
+        where = self._keep[0].device if self._keep else torch.device("cpu")
         for t in self._keep:
-            if t.dtype is not torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != self.shape or t.dim() != 3:
+            if (t.dtype is not torch.bfloat16 or not t.is_contiguous() or tuple(t.shape) != self.shape or t.dim() != 3
+                    or t.device != where):
                 raise NtError(NT_ERR_INVALID_ARG, "pointer_array", "caches must be contiguous bf16 [Hkv, t_stride, D], all alike")
+        self.cuda_device = where.index if where.type == "cuda" else -1
         self.array = (ctypes.c_void_p * len(self._keep))(*[t.data_ptr() for t in self._keep])
         self.address = ctypes.addressof(self.array)
 
@@ -468,9 +473,11 @@ def nt_tree_commit(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D
                    n_emit: torch.Tensor, src_row0: int, dst_row0: int, stream=None):
     """Moves the accepted nodes' rows in every layer's caches (pointer_array); path [B], n_emit [1] int32."""
     n = len(k_caches)
-    if n == 0 or len(v_caches) != n or k_caches.shape != (Hkv, t_stride, D) or v_caches.shape != k_caches.shape:
+    if (n == 0 or len(v_caches) != n or k_caches.shape != (Hkv, t_stride, D) or v_caches.shape != k_caches.shape
+            or v_caches.cuda_device != k_caches.cuda_device):
         raise NtError(NT_ERR_INVALID_ARG, "nt_tree_commit", "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
-    _native().commit(k_caches.address, v_caches.address, n, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream)
+    _native().commit(k_caches.address, v_caches.address, n, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream,
+                     k_caches.cuda_device)
 
 
 class DecodePlan:
