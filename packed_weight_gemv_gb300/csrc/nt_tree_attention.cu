@@ -768,13 +768,12 @@ nt_status launch_tree_attn(const TaMaps& maps, const TaArgs& a, const TaPlan& p,
 }
 template <typename T, int D>
 nt_status launch_tree_attn_all(const TaMaps& maps, const TaArgs& a, const TaPlan& p, int dtype, cudaStream_t st) {
-  bool joined = !ta_joins(p);
   nt_status s;
-  if (p.few) s = launch_tree_few(maps, a, dtype, D, st, &joined);
+  if (p.few) s = launch_tree_few(maps, a, dtype, D, st);
   else if (p.nsplit == 0) s = p.dup == 2 ? launch_tree_attn<T, D, 2, true>(maps, a, p, st) : launch_tree_attn<T, D, 1, true>(maps, a, p, st);
   else s = p.dup == 2 ? launch_tree_attn<T, D, 2, false>(maps, a, p, st) : launch_tree_attn<T, D, 1, false>(maps, a, p, st);
   NT_TRY(s);
-  if (!joined) {
+  if (ta_joins(p)) {
     const int64_t rows = (int64_t)a.B * a.Hq;
     // Warps per row and splits at a time: one round trip for up to 32 splits, and no load twice for few.
     const int w = p.parts > 4 ? 4 : 1;
@@ -821,7 +820,9 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_tree_attention_workspace_size");
   NT_TRY(check_device());
   NT_TRY(ta_setup());
-  const TaPlan p = ta_plan(B, Hq, Hkv, prefix, dtype == NT_F32, D);
+  int clusters = 0;
+  if (B <= kTaFewNodes) NT_TRY(set_up_tree_few(B * (Hq / Hkv), dtype, D, &clusters));  // up to kTaFewRows rows are no more nodes
+  const TaPlan p = ta_plan(B, Hq, Hkv, prefix, dtype == NT_F32, D, clusters);
   TaArgs a{};
   a.q = q;
   a.out = out;
@@ -842,6 +843,7 @@ nt_status nt_tree_attention(const void* q, int dtype, const uint16_t* k_cache, c
   a.pre_tiles = p.pre_tiles;
   a.tiles = p.tiles;
   a.nsplit = p.nsplit;
+  a.cluster = p.cluster;
   a.mtiles = p.mtiles;
   a.groups = Hkv * p.mtiles;
   a.ctas = (int)p.units;

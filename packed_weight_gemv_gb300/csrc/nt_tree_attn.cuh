@@ -264,7 +264,8 @@ __device__ __forceinline__ int node_of(int row, float inv_g) { return (int)(((fl
 
 }  // namespace
 
-// *joined: whether the output is complete, without the join of splits.
-nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st, bool* joined);
+// Before a call with up to kTaFewNodes nodes or kTaFewRows rows is planned. *clusters: how many run at a time.
+nt_status set_up_tree_few(int R, int dtype, int D, int* clusters);
+nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st);
 
 }  // namespace nt

@@ -36,8 +36,6 @@ namespace nt {
 namespace {
 
 constexpr int kTfKeys = 2 * kTaKeys;    // keys of a pair of tiles
-constexpr int kTfCluster = 8;            // CTAs of a cluster at most
-constexpr int kTfClusterTiles = 96;      // tiles of keys up to which a cluster takes a head
 constexpr float kTfLowest = -3.0e38f;   // reference of a row that has seen nothing (its weights are 0)
 
 constexpr int up16(int n) { return (n + 15) / 16 * 16; }
@@ -592,46 +590,56 @@ cudaLaunchConfig_t few_config(cudaLaunchAttribute (&attr)[2], unsigned units, in
   return cfg;
 }
 
+// The kernel's dynamic shared memory allowed on this device; how many of its clusters run at a time.
 template <typename T, int D, int RP>
-nt_status launch_few(const TaMaps& maps, TaArgs a, cudaStream_t st, bool* joined) {
-  static std::atomic<int> attr_set[64];  // per device: the ring's dynamic shared memory allowed
-  static std::atomic<int> active[64];    // per device: clusters of kTfCluster CTAs that run at a time
+nt_status set_up_few(int* clusters) {
+  static std::atomic<int> set[64];     // per device
+  static std::atomic<int> active[64];
   int dev = 0;
   NT_CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return set_error(NT_ERR_CUDA, "device index out of range");
-  constexpr int smem = TfShape<T, D, RP>::kSmem;
-  cudaLaunchAttribute attr[2];
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
+  if (!set[dev].load(std::memory_order_acquire)) {
+    constexpr int smem = TfShape<T, D, RP>::kSmem;
     NT_CUDA_TRY(cudaFuncSetAttribute(tree_few_kernel<T, D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const cudaLaunchConfig_t cfg = few_config(attr, kTfCluster, smem, kTfCluster, st);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = few_config(attr, kTfCluster, smem, kTfCluster, nullptr);
     int n = 0;
     NT_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, tree_few_kernel<T, D, RP>, &cfg));
     active[dev].store(n, std::memory_order_relaxed);
-    attr_set[dev].store(1, std::memory_order_release);
+    set[dev].store(1, std::memory_order_release);
   }
-  // A cluster joins its splits over distributed shared memory instead of in a second kernel. From its 8 CTAs' own number of
-  // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128: over 400 keys 5.6 us, unsplit 5.8; 800 5.5,
-  // in splits 6.1; 4,000 7.1 and 8.0; 8 nodes over 6,000 12.0 and 12.3, over 8,191 14.4 and 13.8).
-  if (a.tiles >= kTfCluster && a.tiles <= kTfClusterTiles && a.groups <= active[dev].load(std::memory_order_relaxed)) {
-    a.cluster = 1;
-    a.nsplit = kTfCluster;
-  }
-  *joined = a.cluster || a.nsplit == 1;
+  *clusters = active[dev].load(std::memory_order_relaxed);
+  return NT_OK;
+}
+template <typename T, int D>
+nt_status set_up_few_rows(int R, int* clusters) {
+  return few_rows(R) == 8 ? set_up_few<T, D, 8>(clusters) : few_rows(R) == 16 ? set_up_few<T, D, 16>(clusters) : set_up_few<T, D, 32>(clusters);
+}
+
+template <typename T, int D, int RP>
+nt_status launch_few(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
+  constexpr int smem = TfShape<T, D, RP>::kSmem;
+  cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = few_config(attr, (unsigned)(a.groups * a.nsplit), smem, a.cluster ? a.nsplit : 1, st);
   NT_CUDA_TRY(cudaLaunchKernelEx(&cfg, tree_few_kernel<T, D, RP>, maps, a));
   return check_launch("tree_few_kernel");
 }
 template <typename T, int D>
-nt_status launch_few_rows(const TaMaps& maps, const TaArgs& a, cudaStream_t st, bool* joined) {
-  return a.R <= 8 ? launch_few<T, D, 8>(maps, a, st, joined)
-         : a.R <= 16 ? launch_few<T, D, 16>(maps, a, st, joined) : launch_few<T, D, 32>(maps, a, st, joined);
+nt_status launch_few_rows(const TaMaps& maps, const TaArgs& a, cudaStream_t st) {
+  return few_rows(a.R) == 8 ? launch_few<T, D, 8>(maps, a, st)
+         : few_rows(a.R) == 16 ? launch_few<T, D, 16>(maps, a, st) : launch_few<T, D, 32>(maps, a, st);
 }
 
 }  // namespace
 
-nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st, bool* joined) {
-  if (dtype == NT_F32) return D == 64 ? launch_few_rows<float, 64>(maps, a, st, joined) : launch_few_rows<float, 128>(maps, a, st, joined);
-  return D == 64 ? launch_few_rows<uint16_t, 64>(maps, a, st, joined) : launch_few_rows<uint16_t, 128>(maps, a, st, joined);
+nt_status set_up_tree_few(int R, int dtype, int D, int* clusters) {
+  if (dtype == NT_F32) return D == 64 ? set_up_few_rows<float, 64>(R, clusters) : set_up_few_rows<float, 128>(R, clusters);
+  return D == 64 ? set_up_few_rows<uint16_t, 64>(R, clusters) : set_up_few_rows<uint16_t, 128>(R, clusters);
+}
+
+nt_status launch_tree_few(const TaMaps& maps, const TaArgs& a, int dtype, int D, cudaStream_t st) {
+  if (dtype == NT_F32) return D == 64 ? launch_few_rows<float, 64>(maps, a, st) : launch_few_rows<float, 128>(maps, a, st);
+  return D == 64 ? launch_few_rows<uint16_t, 64>(maps, a, st) : launch_few_rows<uint16_t, 128>(maps, a, st);
 }
 
 }  // namespace nt

@@ -17,6 +17,8 @@ constexpr int kTaPiece = 12;            // tiles that one more of them costs (wi
 constexpr int kTaFewRows = 32;
 constexpr int kTaFewNodes = 32;         // nodes whose mask is one word
 constexpr int few_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
+constexpr int kTfCluster = 8;           // CTAs of a cluster
+constexpr int kTfClusterTiles = 96;     // tiles of keys up to which a cluster takes a head
 
 // Equal shares of `work` tiles: the first tile of CTA c, and the CTA whose share holds tile x.
 __host__ __device__ inline int64_t share_from(int64_t work, int c, int ctas) { return work * c / ctas; }
@@ -26,10 +28,12 @@ struct TaPlan {
   int few;        // the form for few rows
   int dup, rows, mtiles, tiles, pre_tiles;
   int nsplit;     // 0: every CTA an equal share of all tiles
+  int cluster;    // few rows: a cluster holds the splits of a tile of rows and joins them
   int parts;      // splits of a row at most
   int64_t units;  // CTAs
 };
-inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few) {
+// clusters: so many clusters of the form for few rows run at a time.
+inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few, int clusters = 0) {
   TaPlan p;
   const int R = B * (Hq / Hkv);
   p.few = few;
@@ -38,7 +42,17 @@ inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few) {
   p.mtiles = (R + p.rows - 1) / p.rows;
   p.pre_tiles = (int)(((int64_t)prefix + kTaKeys - 1) / kTaKeys);
   p.tiles = p.pre_tiles + (B + kTaKeys - 1) / kTaKeys;
+  p.cluster = 0;
   const int64_t groups = (int64_t)Hkv * p.mtiles;
+  // A cluster joins its splits over distributed shared memory instead of in a second kernel. From its 8 CTAs' own number of
+  // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128: over 400 keys 5.6 us, unsplit 5.8; 800 5.5,
+  // in splits 6.1; 4,000 7.1 and 8.0; 8 nodes over 6,000 12.0 and 12.3, over 8,191 14.4 and 13.8).
+  if (few && p.tiles >= kTfCluster && p.tiles <= kTfClusterTiles && groups <= clusters) {
+    p.cluster = 1;
+    p.nsplit = p.parts = kTfCluster;
+    p.units = groups * kTfCluster;
+    return p;
+  }
   // Splits as the GPU holds them, but few enough that what the join spends on one more is worth the tiles it
   // takes off the others. In units of about a seventh of a tile's time (few rows: a quarter of a pair of tiles')
   // the join takes one for a split and its launch 20 (12). Measured: one key-value head of 20 rows over 12,000 keys, D 64:
@@ -73,27 +87,29 @@ inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few) {
 }
 // What a form of the plan takes, in hundredths of a microsecond as measured: a call's start and end, each step
 // of a CTA (a pair of tiles with few rows, one tile with many), the join. At 32 / 8 heads of 128, fp32, the form for
-// few rows and the one for many: 16 nodes over 400 keys 9.0 and 10.7 us, 4,000 13.0 and 15.6, 32,000 36.1 and
-// 37.6; 25 nodes 9.2 and 11.7, 16.3 and 16.5, 58.8 and 41.4; bf16, 25 nodes 8.5 and 9.7, 15.0 and 12.8.
+// few rows (in splits) and the one for many: 16 nodes over 400 keys 9.0 and 10.7 us, 4,000 13.0 and 15.6, 32,000 36.1 and
+// 37.6; 25 nodes 9.2 and 11.7, 16.3 and 16.5, 58.8 and 41.4; bf16, 25 nodes 8.5 and 9.7, 15.0 and 12.8. In a cluster, 12 to
+// 32 nodes of 1 and 4 key-value heads over 450 to 6,000 keys, a join of 190 chose the slower form by 0.01 us on average and
+// 0.33 at most (the splits' cost in its place: 0.05 and 0.94).
 inline int64_t ta_cost(const TaPlan& p, bool f32, int D) {
   const int at_once = p.few ? 2 : 1;
   const int64_t steps = ((p.tiles + p.nsplit - 1) / p.nsplit + at_once - 1) / at_once * ((p.units + kTaFill - 1) / kTaFill);
-  const int64_t join = p.nsplit > 1 ? 200 + 8 * p.nsplit : 0;
+  const int64_t join = p.cluster ? 190 : p.nsplit > 1 ? 200 + 8 * p.nsplit : 0;
   if (p.few) return (D == 128 ? 500 : 450) + 100 * steps + join;
   if (D == 128) return (f32 ? 750 : 600) + (p.dup == 2 ? 0 : f32 ? 80 : 100) + (f32 ? 105 : 60) * steps + join;
   return (f32 ? 560 : 460) + (p.dup == 2 ? 0 : f32 ? 40 : 100) + (f32 ? 60 : 50) * steps + join;
 }
 // Up to kTaFewRows rows the form for few rows; up to kTaFewNodes nodes also in several tiles of rows, where that costs
 // less than the form for many: short sequences.
-inline TaPlan ta_plan(int B, int Hq, int Hkv, int prefix, bool f32, int D) {
+inline TaPlan ta_plan(int B, int Hq, int Hkv, int prefix, bool f32, int D, int clusters = 0) {
   const int R = B * (Hq / Hkv);
-  if (R <= kTaFewRows) return ta_form(B, Hq, Hkv, prefix, true);
+  if (R <= kTaFewRows) return ta_form(B, Hq, Hkv, prefix, true, clusters);
   const TaPlan many = ta_form(B, Hq, Hkv, prefix, false);
   if (B > kTaFewNodes || many.nsplit == 0) return many;
-  const TaPlan few = ta_form(B, Hq, Hkv, prefix, true);
+  const TaPlan few = ta_form(B, Hq, Hkv, prefix, true, clusters);
   return ta_cost(few, f32, D) < ta_cost(many, f32, D) ? few : many;
 }
-inline bool ta_joins(const TaPlan& p) { return p.nsplit != 1; }
+inline bool ta_joins(const TaPlan& p) { return p.nsplit != 1 && !p.cluster; }  // in a second kernel
 // Rows of results that the splits of any prefix take: kTaFill CTAs, and in shares one more for each tile of rows
 // (several tiles of few rows take less).
 inline int64_t ta_split_rows(int B, int Hq, int Hkv) {

@@ -32,3 +32,8 @@ def test_adjustments_cover_every_row(tmp_path):
     assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
     got = [int(x) for x in run(*[n for _, B, V in GROUPED_ROWS for n in (B, V)]).stdout.split()]
     assert got == [g for g, _, _ in GROUPED_ROWS]
+
+
+def test_attention_plans_with_clusters(tmp_path):
+    r = compiled("tree_cluster_check", tmp_path)()
+    assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
