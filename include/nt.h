@@ -352,6 +352,7 @@ nt_status nt_rmsnorm(const float* x, const float* gamma, int B, int D, float eps
  * nt_logits_adjust, nt_tree_accept, nt_tree_commit and nt_token_counts. B = 1 with a mask of
  * one set bit is plain decoding. The kernels of these calls are programmatic dependent launches:
  * they start while the previous kernel of the stream finishes and touch memory after it.
+ * Lengths and cache rows are host numbers: a recorded graph of a pass is good for one length.
  */
 typedef enum nt_dtype { NT_F32 = 0, NT_BF16 = 1 } nt_dtype; /* fp32; bf16 bit patterns */
 enum nt_rope_layout { NT_ROPE_HALF = 0,          /* pair i of the rotated r dimensions: (i, i + r / 2) */

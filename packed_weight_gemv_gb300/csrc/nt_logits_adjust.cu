@@ -14,7 +14,7 @@
 // value, two values to an instruction (with a branch around them nearly every warp took it for each of
 // a lane's tokens). 64 rows of 151,936 with all adjustments (80 MB): 240 instructions per 128 values 32.5
 // us, straight-line for all 24.7, listed 21.6, groups of rows that fill one wave 19.4, the ancestor bits in a
-// few loads and the listed tokens in registers 19.1 = 4.2 TB/s, 62 % of the measured copy rate (15.1 where
+// few loads and the listed tokens in registers 19.1 = 4.2 TB/s, 62 % of the measured copy rate (15.5 where
 // L2 holds the rows). Instruction issue, a row's dependent steps and the start of a CTA bound it.
 #include <math.h>
 #include <string.h>

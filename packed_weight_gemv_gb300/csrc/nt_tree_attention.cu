@@ -31,9 +31,9 @@
 // (weighted sum, m, sum) meet in the workspace and a second kernel joins them.
 //
 // fp32 queries at D 128 are bound by the tensor pipe and the softmax alike (six bf16 products: 1,690
-// cycles per tile, 0.88 us; a tile takes 1.05): 25 nodes over 26,000 keys, 32 / 8 heads, 36.3 us = 107
+// cycles per tile, 0.88 us; a tile takes 1.05): 25 nodes over 26,000 keys, 32 / 8 heads, in a replayed graph 35.7 us = 107
 // MB at 3.0 TB/s, of which 9.4 us are a call of one tile and 2.5 the join. bf16 queries: 768 cycles per
-// tile, 0.6 us taken: 64 nodes over 32,704 keys 46.1 us = 744 TFLOP/s of the one product that the formula
+// tile, 0.6 us taken, and 0.8 us more every 16 tiles: 64 nodes over 32,704 keys 45.4 us = 755 TFLOP/s of the one product that the formula
 // asks for. At D 64 the softmax's instructions bound it: 255 nodes over 16,001 keys, 32 / 4 heads, 86 us.
 //
 // What a node does not see has no part in its result: the rows past the sequence and past the

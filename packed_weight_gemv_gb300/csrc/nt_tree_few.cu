@@ -23,8 +23,10 @@
 //                     exceeds its maximum by 2^8.
 //
 // Bound by the memory for long sequences and by latency for short ones. 32 / 8 heads of 128, fp32, join
-// included: one node over 32,767 keys 26.0 us = 5.2 TB/s, 76 % of the measured copy rate (bf16 25.9; with rows on
-// the M side 35.5), 8 nodes (32 rows) 29.7; one node over 4,095 keys 7.7, over 800 5.5, over 50 (unsplit) 4.1.
+// included, in a replayed graph: one node over 32,767 keys 26.1 us = 5.1 TB/s, 76 % of the measured copy rate (bf16 26.3;
+// with rows on the M side 35.5); one node over 4,095 keys 7.9, over 800 5.7, over 50 (unsplit) 4.2. 8 nodes (32 rows)
+// over 32,700 take 29.9: a group's steps for 32 rows, one behind the other, bound them (13 or 14 pairs of tiles to a
+// CTA, 1.9 us each; 25 % of the issue slots, 19 % of the tensor pipe).
 #include <cuda_bf16.h>
 
 #include <atomic>

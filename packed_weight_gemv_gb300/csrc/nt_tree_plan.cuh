@@ -10,7 +10,7 @@
 namespace nt {
 
 constexpr int kTaKeys = 64;             // keys per tile
-constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM)
+constexpr int kTaFill = 152;            // CTAs that fill the GPU once (one per SM of a GB300; the workspace's size, which is asked for without a device, goes by it)
 constexpr int kTaPieces = 4;            // tiles of rows that a CTA's share may touch
 constexpr int kTaPiece = 12;            // tiles that one more of them costs (with 6, 65 tiles of 64 row tiles took 48.4 us in shares, 46.4 in splits)
 // Up to kTaFewRows query rows per key-value head; a split's results stand few_rows(R) rows apart.
@@ -45,8 +45,9 @@ inline TaPlan ta_form(int B, int Hq, int Hkv, int prefix, bool few, int clusters
   p.cluster = 0;
   const int64_t groups = (int64_t)Hkv * p.mtiles;
   // A cluster joins its splits over distributed shared memory instead of in a second kernel. From its 8 CTAs' own number of
-  // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128: over 400 keys 5.6 us, unsplit 5.8; 800 5.5,
-  // in splits 6.1; 4,000 7.1 and 8.0; 8 nodes over 6,000 12.0 and 12.3, over 8,191 14.4 and 13.8).
+  // tiles up to 12 tiles each that is the faster way (one node, 8 heads of D 128, in a replayed graph: over 800 keys 5.7 us,
+  // in splits 6.2; 4,000 7.3 and 7.8; 8 nodes over 6,000 12.0 and 12.5, over 8,191 14.4 and 13.7). With 8 heads 64 of the
+  // SMs have work then.
   if (few && p.tiles >= kTfCluster && p.tiles <= kTfClusterTiles && groups <= clusters) {
     p.cluster = 1;
     p.nsplit = p.parts = kTfCluster;
