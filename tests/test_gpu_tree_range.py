@@ -7,7 +7,7 @@ import torch
 from packed_weight_gemv_gb300 import nt
 from tests import _tree
 from tests._gpu import DEV, dev, host
-from tests.test_gpu_tree import run_adjust
+from tests.test_gpu_tree import attend_64, attn_bound, attn_inputs, run_adjust, run_attend, within
 from tests.test_tree_plans_cpu import GROUPED_ROWS
 
 pytestmark = pytest.mark.gpu
@@ -63,6 +63,64 @@ def test_attention_sums_of_one_sign_keep_their_bits(B, D, tiles, dtype):
         spread = off.mean(1).std() / (Hkv * D) ** 0.5  # a head's nodes have much the same sums: one sample for all of them
         assert abs(mean) <= loss + 5 * spread, (mean, loss, spread, worst)
         assert worst <= U16 + loss + rest + 2.0 ** -18, worst
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B", [36, 70, 133])
+@pytest.mark.parametrize("kind", ["random", "rise", "fall", "steps"])
+def test_attention_bf16_about_the_points_where_sums_are_taken(B, D, kind):
+    """A head to a block, every tile count about the multiples of 16; the reference stays, rises with every tile, falls, or jumps at
+    the tiles about those points."""
+    Hkv = 160
+    for tiles in (15, 16, 17, 18, 31, 32, 33, 34, 47, 48, 49, 50, 64, 65):
+        prefix = max(0, 64 * tiles - 64 * ((B + 63) // 64) - (tiles % 3) * 9)
+        q, k, v = attn_inputs(B, Hkv, Hkv, D, prefix, 0, "bf16", seed=tiles)
+        if kind != "random":
+            at = torch.arange(k.shape[1], device=DEV)
+            ramp = {"rise": at / k.shape[1] * 40, "fall": 40 - at / k.shape[1] * 40, "steps": (at // 64 + 1) // 16 * 12.0}[kind]
+            u = q.float().mean(0)
+            k = (k * 0.1 + ramp[None, :, None] * (u / u.norm(dim=-1, keepdim=True))[:, None]).bfloat16()
+        sees = _tree.ancestors(_tree.parents(np.random.RandomState(tiles), B))
+        out = run_attend(q, k, v, prefix, prefix, sees, runs=2)
+        want = attend_64(q, k, v, prefix, prefix, sees)
+        within(f64(out), want, attn_bound(q, k, v, prefix, sees, "bf16", want), (kind, tiles))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hkv,prefix", [(70, 200, 2500), (40, 170, 3100), (255, 8, 9000)])
+def test_attention_bf16_sums_in_shares(B, Hkv, prefix, D):
+    """Blocks that begin and end within a tile of rows, each piece with sums of its own; a node's infinity reaches it alone."""
+    q, k, v = attn_inputs(B, Hkv * (1 if Hkv > 8 else 4), Hkv, D, prefix, 1, "bf16", seed=B)
+    ramp = torch.linspace(0, 30, k.shape[1], device=DEV)
+    u = q.float().view(B, Hkv, -1, D).mean((0, 2))
+    k = (k * 0.1 + ramp[None, :, None] * (u / u.norm(dim=-1, keepdim=True))[:, None]).bfloat16()
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(B), B))
+    sees[:, B - 1] = False
+    sees[B - 1, B - 1] = True
+    v[:, prefix + B] = float("inf")
+    out = f64(run_attend(q, k, v, prefix, prefix + 1, sees, runs=2))
+    want = attend_64(q, k, v.nan_to_num(0, 0, 0), prefix, prefix + 1, sees)
+    assert np.isposinf(out[B - 1]).all()
+    within(out[:-1], want[:-1], attn_bound(q, k, v, prefix, sees, "bf16", want)[:-1])
+
+
+def test_attention_bf16_timeout_is_reported_with_sums_aside():
+    q, k, v = attn_inputs(70, 160, 160, 128, 3000, 0, "bf16")
+    sees = _tree.ancestors(_tree.parents(np.random.RandomState(6), 70))
+    want = run_attend(q, k, v, 3000, 3000, sees)
+    ws = torch.zeros(nt.nt_tree_attention_workspace_size(70, 160, 160, 128, 3000), dtype=torch.uint8, device=DEV)
+    mask, out = dev(_tree.pack(sees)), torch.empty_like(q)
+    try:
+        nt.nt_set_test_fault(5, 20.0)
+        nt.nt_tree_attention(q, k, v, 3000, 3000, mask, out, ws)
+        torch.cuda.synchronize()
+    finally:
+        nt.nt_set_test_fault(0)
+    assert nt.nt_workspace_status(ws) == nt.NT_ERR_TIMEOUT
+    ws.zero_()
+    nt.nt_tree_attention(q, k, v, 3000, 3000, mask, out, ws)
+    torch.cuda.synchronize()
+    assert nt.nt_workspace_status(ws) == nt.NT_OK and torch.equal(out, want)
 
 
 # ---- logits ----------------------------------------------------------------------------------
