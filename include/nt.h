@@ -477,6 +477,102 @@ nt_status nt_tree_commit(uint16_t* const* k_caches, uint16_t* const* v_caches, i
                          int dst_row0, void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Several sequences over one paged cache, and beams of them. The pages describe neither; formulas and
+ * readings are stated per call. A pool is an ordinary cache [Hkv][t_stride][D] whose rows are taken in pages: page p is
+ * rows p * page .. (p + 1) * page - 1 of every head, page = 16, 32, 64, 128 or 256, and the pool has n_pages pages (t_stride / page,
+ * rounded down). Row r of a table [S][width] (int32, device) names the pages of sequence r in order; length[r] rows of them are in
+ * use, and entries behind ceil(length[r] / page) mean nothing. refs [n_pages] counts the sequences that hold each page; a
+ * page with refs 0 is free. A caller that keeps pages of its own (a shared prompt) adds 1 to their refs.
+ * One step of S sequences with T new tokens, sequence s having those from q_start[s] to q_start[s + 1] - 1:
+ * nt_page_fork where sequences branch or end; nt_page_extend and nt_page_copy; per layer the projections,
+ * nt_qk_norm_rope_append with the rows and positions of nt_page_extend, and nt_paged_attention; at the end nt_beam_select, whose
+ * parents the next nt_page_fork takes. Lengths stand on the device, so a recorded graph of a step is good for any length.
+ * 1 <= S <= 4096, 1 <= T <= 2^20. The kernels of these calls are programmatic dependent launches.
+ */
+
+/* Tables that follow their parents: sequence i of S_out goes on as sequence parent[i] of S_in, or is empty where parent[i] is
+ * -1 (any other value outside [0, S_in) is taken for -1 and counted in n_bad). table_out [S_out][width] (entries behind the used
+ * ones -1) and length_out [S_out] must not overlap the inputs. refs: every page loses the old sequences that hold it and gains
+ * the new ones, so pages of sequences without a child become free. An entry outside [0, n_pages) among the used ones is copied,
+ * and counted in n_bad_opt (device uint32 or NULL; the call ADDS). Lengths are taken as at most width * page. */
+nt_status nt_page_fork(const int32_t* table, const int32_t* length, int S_in, int width, const int32_t* parent, int S_out, int page,
+                       int32_t* refs, int n_pages, int32_t* table_out, int32_t* length_out, uint32_t* n_bad_opt, void* stream);
+
+/* Room for new tokens. Sequence s gets n = q_start[s + 1] - q_start[s] more rows: length[s] += n, and free pages, lowest first,
+ * into its table (their refs become 1). Where its last page is partly filled and held by others too, it is given a page of its own
+ * instead: pairs[s] = (old page, new page), which nt_page_copy copies before anything is appended, and refs of the old page less 1.
+ * Of the sequences of a call that share such a page each gives it up, in order, until one is alone with it. pairs[s] = (-1, -1)
+ * elsewhere.
+ *   rows, pos [T]: cache row and position of every token, for nt_qk_norm_rope_append (pos_opt, rows_opt) of this layer and every
+ *   other; row -1 and position 0 for tokens outside every sequence (a padded batch).
+ * A sequence that cannot be extended is left as it was, its tokens get row -1, and 1 is added to n_bad_opt: one whose table is
+ * full, whose length is negative, whose last page is outside [0, n_pages); and where the free pages do not suffice, the first sequence that
+ * they do not suffice for and every one behind it.
+ *   q_start [S + 1], rising (values are taken as within [0, T]); pairs [S][2] */
+nt_status nt_page_extend(int32_t* table, int32_t* length, int S, int width, const int32_t* q_start, int T, int page, int32_t* refs,
+                         int n_pages, int32_t* rows, int32_t* pos, int32_t* pairs, uint32_t* n_bad_opt, void* stream);
+
+/* Copies of whole pages in every layer: for i < n, page pairs[i][1] <- page pairs[i][0] of every head of every cache; a pair with a
+ * page outside [0, t_stride / page) is passed over. No page may be written twice, nor read and written. k_caches, v_caches: host arrays
+ * of n_layers device pointers to [Hkv][t_stride][D] bf16 (16-byte aligned); D a multiple of 8 up to 256; Hkv <= 65535. pairs [n][2]
+ * device int32, from nt_page_extend or nt_page_compact. */
+nt_status nt_page_copy(uint16_t* const* k_caches, uint16_t* const* v_caches, int n_layers, int Hkv, int D, int t_stride, int page,
+                       const int32_t* pairs, int n, void* stream);
+
+/* Moves the pages in use to the front of the pool. With U pages in use (*n_used, device), the i-th page in use at U or behind goes to the
+ * i-th free page below U: pairs[i] = (from, to), for nt_page_copy, and (-1, -1) behind the last one (n >= n_pages / 2 pairs). The
+ * tables' used entries and refs follow; pages that no table names but refs counts move too, and the caller finds them by pairs.
+ * Entries outside [0, n_pages) stay and are counted in n_bad_opt.
+ *   ws: nt_page_compact_workspace_size bytes (16-byte aligned; scratch; calls sharing it must not overlap) */
+nt_status nt_page_compact_workspace_size(int n_pages, size_t* bytes);
+nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int32_t* length, int S, int width, int page, int32_t* pairs,
+                          int n, int32_t* n_used, uint32_t* n_bad_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of ragged chunks of new tokens over the pool. Token t = q_start[s] + i of sequence s, which has length[s] rows with
+ * its n new ones (nt_page_extend), stands at position p = length[s] - n + i and sees rows max(0, p - window + 1) .. p of its
+ * sequence (window 0: all up to p). With x = q[t][h] . k[j] / sqrt(D):
+ *   cap > 0:  x <- cap * tanh(x / cap);   slopes: x <- x - slopes[h] * (p - j)
+ *   out[t][h] = sum_j softmax_j(x) v[j]
+ * keys and values of head h / (Hq / Hkv). Tokens at q_start[S] and behind are left as they were; a token that sees nothing gets
+ * 0. What a token does not see has no part in its result, whatever it holds: rows behind the sequence's in its last page, and later
+ * tokens', may be NaN or infinite.
+ *   q, out [T][Hq][D] of type dtype (nt_dtype; out may be q), q's tokens q_stride elements apart (a multiple of 8); k_pool, v_pool [Hkv][t_stride][D] bf16;
+ *     D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64, T * Hq <= 2^24; all 16-byte aligned
+ *   table [S][width], q_start [S + 1] (rising; values taken as within [0, T]), length [S] (taken as within [0, width * page])
+ *   max_new: the caller's bound on the new tokens of a sequence (0: none known). It only chooses the kernel: results are right
+ *     for more, if slower
+ *   window >= 0; cap >= 0 and finite; slopes_opt [Hq] fp32 or NULL
+ *   n_bad_opt: device uint32 counter or NULL; a nonzero number is ADDED where entries outside [0, t_stride / page) were met among
+ *     those of rows that are seen (such rows read as zeros)
+ *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes (16-byte aligned, zero-filled before its first use, its counters
+ *     left zero; calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
+ * fp32 queries: products are exact, scores, weights and sums are fp32 (on the tensor cores weights are two bf16 terms, within 2^-17 of
+ * them). bf16 queries: on the tensor cores each weight is rounded to bf16, for the sums of the weights too. Either way sums lose at
+ * most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the output is rounded. */
+nt_status nt_paged_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, size_t* bytes);
+nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const uint16_t* k_pool, const uint16_t* v_pool, int T, int S,
+                             int Hq, int Hkv, int D, int page, int t_stride, const int32_t* table, int width, const int32_t* q_start,
+                             const int32_t* length, int max_new, int window, float cap, const float* slopes_opt, void* out,
+                             uint32_t* n_bad_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* The next beams: logits [N][V] fp32 and scores [N] (sums of log probabilities so far) of N / W groups of W beams. Beam b continues
+ * with token v at
+ *   total = scores[b] + (logits[b][v] - log sum_u e^logits[b][u]),   ranked by total / (lengths[b] + 1)^alpha
+ * A finished beam (done[b] != 0) has one continuation, token eos, with total = scores[b] ranked by total / max(lengths[b], 1)^alpha. Of
+ * each group the K best in order, ties by the lower beam, then the lower token: parent (the beam's row, for nt_page_fork),
+ * token, score (total) and done_out (1: finished before or by eos), [N / W][K] each; -1, -1, -inf and 0 where there are fewer.
+ * Sums run in fp32 and are joined in 64 bits, ranks are compared in pairs of fp32 (48 bits): score is within 2^-22 of the exact one, relative
+ * to the larger of it and the logits. A logit of NaN or -inf is never chosen and adds nothing; a beam whose score is not finite, or with
+ * a logit of +inf, has no continuation.
+ *   1 <= W, K <= 64; N a multiple of W, N <= 65536; V <= 2^24; eos -1 (none) or below V; 0 <= alpha <= 16 (0: lengths not
+ *   needed); done_opt, lengths_opt [N] int32
+ *   ws: nt_beam_select_workspace_size(V, N) bytes (16-byte aligned; scratch; calls sharing it must not overlap) */
+nt_status nt_beam_select_workspace_size(int V, int N, size_t* bytes);
+nt_status nt_beam_select(const float* logits, const float* scores, int N, int W, int V, int K, const int32_t* done_opt, int eos,
+                         const int32_t* lengths_opt, double alpha, int32_t* parent, int32_t* token, float* score,
+                         int32_t* done_out_opt, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Decode step: every projection of every layer, then optionally the output projection, in
  * one submission ("A 104 microsecond floor ...": on the instrumented A100 step, roughly
  * 590 of 694 microseconds were spent across about 120 kernel boundaries rather than in

@@ -1,5 +1,5 @@
 // nt_binding.cpp -- native marshalling for the calls that are made many times per token
-// (nt_qk_norm_rope_append, nt_tree_*, nt_logits_adjust, nt_token_counts): reads torch tensors' types,
+// (nt_qk_norm_rope_append, nt_tree_*, nt_logits_adjust, nt_token_counts, nt_page*, nt_beam_select): reads torch tensors' types,
 // shapes and strides, refuses what the C ABI cannot see, and calls libnt.so. Their Python forms
 // are in nt.py. Through ctypes a call took 15 to 27 us on the host, most of a small call's time.
 // Among what is refused are tensors of the host or of another GPU than the current one: their addresses would
@@ -30,6 +30,12 @@ decltype(&nt_token_counts) p_counts = nullptr;
 decltype(&nt_logits_adjust) p_adjust = nullptr;
 decltype(&nt_tree_accept) p_accept = nullptr;
 decltype(&nt_tree_commit) p_commit = nullptr;
+decltype(&nt_page_fork) p_fork = nullptr;
+decltype(&nt_page_extend) p_extend = nullptr;
+decltype(&nt_page_copy) p_copy = nullptr;
+decltype(&nt_page_compact) p_compact = nullptr;
+decltype(&nt_paged_attention) p_paged = nullptr;
+decltype(&nt_beam_select) p_beam = nullptr;
 
 struct Refusal {
   int status;
@@ -355,33 +361,173 @@ PyObject* commit(PyObject*, PyObject* const* x, Py_ssize_t n) {
   });
 }
 
-// (NtError, last_error, append, layout, attention, counts, adjust, accept, commit): addresses of the library's functions
+int64_t fit(int64_t n) {
+  if (n > INT32_MAX) refuse("a size leaves the int range");
+  return n;
+}
+// A table [S][width] of pages.
+const at::Tensor& pages(PyObject* o, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() != 2) refuse(std::string(name) + " must be [S, width]");
+  fit(t.size(0));
+  fit(t.size(1));
+  return t;
+}
+
+// (table, length, parent, refs, page, table_out, length_out, n_bad, stream)
+PyObject* fork(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_page_fork", n, 9, [&]() -> nt_status {
+    const int64_t S = pages(x[0], "table").size(0), W = tensor(x[0], "table").size(1), So = fit(tensor(x[2], "parent").numel()),
+                  P = fit(tensor(x[3], "refs").numel());
+    const auto *t = flat<int32_t>(x[0], "table", kI32), *l = flat<int32_t>(x[1], "length", kI32, {S}), *p = flat<int32_t>(x[2], "parent", kI32, {So});
+    auto *r = flat<int32_t>(x[3], "refs", kI32, {P}), *to = flat<int32_t>(x[5], "table_out", kI32, {So, W}),
+         *lo = flat<int32_t>(x[6], "length_out", kI32, {So});
+    const int page = integer(x[4]);
+    uint32_t* bad = counter(x[7]);
+    void* st = stream_of(x[8]);
+    return released([&] { return p_fork(t, l, (int)S, (int)W, p, (int)So, page, r, (int)P, to, lo, bad, st); });
+  });
+}
+
+// (table, length, refs, q_start, page, rows, pos, pairs, n_bad, stream)
+PyObject* extend(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_page_extend", n, 10, [&]() -> nt_status {
+    const int64_t S = pages(x[0], "table").size(0), W = tensor(x[0], "table").size(1), P = fit(tensor(x[2], "refs").numel()),
+                  T = fit(tensor(x[5], "rows").numel());
+    auto *t = flat<int32_t>(x[0], "table", kI32), *l = flat<int32_t>(x[1], "length", kI32, {S}), *r = flat<int32_t>(x[2], "refs", kI32, {P}),
+         *q = flat<int32_t>(x[3], "q_start", kI32, {S + 1}), *rw = flat<int32_t>(x[5], "rows", kI32, {T}), *ps = flat<int32_t>(x[6], "pos", kI32, {T}),
+         *pr = flat<int32_t>(x[7], "pairs", kI32, {S, 2});
+    const int page = integer(x[4]);
+    uint32_t* bad = counter(x[8]);
+    void* st = stream_of(x[9]);
+    return released([&] { return p_extend(t, l, (int)S, (int)W, q, (int)T, page, r, (int)P, rw, ps, pr, bad, st); });
+  });
+}
+
+// (k_caches, v_caches: addresses of arrays of n_layers pointers, n_layers, Hkv, D, t_stride, page, pairs, stream, the caches' CUDA device or -1)
+PyObject* copy(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_page_copy", n, 10, [&]() -> nt_status {
+    auto* kp = static_cast<uint16_t* const*>(PyLong_AsVoidPtr(x[0]));
+    auto* vp = static_cast<uint16_t* const*>(PyLong_AsVoidPtr(x[1]));
+    if (PyErr_Occurred()) throw PythonError{};
+    const int L = integer(x[2]), Hkv = integer(x[3]), D = integer(x[4]), ts = integer(x[5]), page = integer(x[6]), at = integer(x[9]);
+    const int64_t m = pages(x[7], "pairs").size(0);
+    const auto* p = flat<int32_t>(x[7], "pairs", kI32, {m, 2});
+    t_call->add("the caches", at < 0 ? c10::Device(c10::kCPU) : c10::Device(c10::kCUDA, (c10::DeviceIndex)at));
+    void* st = stream_of(x[8]);
+    return released([&] { return p_copy(kp, vp, L, Hkv, D, ts, page, p, (int)m, st); });
+  });
+}
+
+// (refs, table, length, page, pairs, n_used, n_bad, ws, stream)
+PyObject* compact(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_page_compact", n, 9, [&]() -> nt_status {
+    const int64_t P = fit(tensor(x[0], "refs").numel()), S = pages(x[1], "table").size(0), W = tensor(x[1], "table").size(1),
+                  m = pages(x[4], "pairs").size(0);
+    auto *r = flat<int32_t>(x[0], "refs", kI32, {P}), *t = flat<int32_t>(x[1], "table", kI32), *l = flat<int32_t>(x[2], "length", kI32, {S}),
+         *pr = flat<int32_t>(x[4], "pairs", kI32, {m, 2});
+    const int page = integer(x[3]);
+    auto* used = single<int32_t>(x[5], "n_used");
+    uint32_t* bad = counter(x[6]);
+    size_t bytes;
+    void *ws = workspace(x[7], &bytes), *st = stream_of(x[8]);
+    return released([&] { return p_compact(r, (int)P, t, l, (int)S, (int)W, page, pr, (int)m, used, bad, ws, bytes, st); });
+  });
+}
+
+// (q, k_pool, v_pool, page, table, q_start, length, out, ws, max_new, window, cap, slopes, n_bad, stream)
+PyObject* paged(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_paged_attention", n, 15, [&]() -> nt_status {
+    const at::Tensor &q = tensor(x[0], "q"), &kc = tensor(x[1], "k_pool");
+    if (q.dim() != 3 || kc.dim() != 3) refuse("q [T, Hq, D] and pools [Hkv, t_stride, D] are needed");
+    const int dtype = activation(q, "q");
+    const int64_t T = fit(q.size(0)), Hq = fit(q.size(1)), D = fit(q.size(2)), Hkv = fit(kc.size(0)), ts = fit(kc.size(1));
+    const int64_t S = pages(x[4], "table").size(0), W = tensor(x[4], "table").size(1);
+    int64_t qs;
+    const void* qp = rows(x[0], "q", q.scalar_type(), {T, Hq, D}, &qs);
+    const auto *kp = flat<uint16_t>(x[1], "k_pool", kBf16, {Hkv, ts, D}), *vp = flat<uint16_t>(x[2], "v_pool", kBf16, {Hkv, ts, D});
+    const auto *t = flat<int32_t>(x[4], "table", kI32), *qst = flat<int32_t>(x[5], "q_start", kI32, {S + 1}),
+               *l = flat<int32_t>(x[6], "length", kI32, {S});
+    void* out = flat(x[7], "out", q.scalar_type(), {T, Hq, D});
+    size_t bytes;
+    void* ws = workspace(x[8], &bytes);
+    const int page = integer(x[3]), most = integer(x[9]), window = integer(x[10]);
+    const float cap = number(x[11]);
+    const auto* sl = flat<float>(x[12], "slopes", kF32, {Hq});
+    uint32_t* bad = counter(x[13]);
+    void* st = stream_of(x[14]);
+    return released([&] {
+      return p_paged(qp, dtype, qs, kp, vp, (int)T, (int)S, (int)Hq, (int)Hkv, (int)D, page, (int)ts, t, (int)W, qst, l, most, window, cap,
+                     sl, out, bad, ws, bytes, st);
+    });
+  });
+}
+
+// (logits, scores, beams, parent, token, score, done, done_out, eos, lengths, alpha, ws, stream)
+PyObject* beam(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded("nt_beam_select", n, 13, [&]() -> nt_status {
+    const at::Tensor& lg = tensor(x[0], "logits");
+    if (lg.dim() != 2) refuse("logits must be [N, V]");
+    const int64_t N = fit(lg.size(0)), V = fit(lg.size(1)), M = fit(tensor(x[3], "parent").numel());
+    const int W = integer(x[2]);
+    if (W < 1 || N % W != 0 || N < W || M % (N / W) != 0) refuse("need rows of logits a multiple of beams, and as many results for each group");
+    const auto *lp = flat<float>(x[0], "logits", kF32), *sp = flat<float>(x[1], "scores", kF32, {N});
+    auto *p = flat<int32_t>(x[3], "parent", kI32), *t = flat<int32_t>(x[4], "token", kI32);
+    auto* sc = flat<float>(x[5], "score", kF32);
+    if (tensor(x[4], "token").numel() != M || tensor(x[5], "score").numel() != M) refuse("parent, token and score must be alike");
+    const auto* d = flat<int32_t>(x[6], "done", kI32, {N});
+    auto* dn = flat<int32_t>(x[7], "done_out", kI32);
+    if (dn && tensor(x[7], "done_out").numel() != M) refuse("done_out must be like parent");
+    const int eos = integer(x[8]);
+    const auto* l = flat<int32_t>(x[9], "lengths", kI32, {N});
+    const double alpha = PyFloat_AsDouble(x[10]);
+    if (alpha == -1.0 && PyErr_Occurred()) throw PythonError{};
+    size_t bytes;
+    void *ws = workspace(x[11], &bytes), *st = stream_of(x[12]);
+    return released([&] {
+      return p_beam(lp, sp, (int)N, W, (int)V, (int)(M / (N / W)), d, eos, l, alpha, p, t, sc, dn, ws, bytes, st);
+    });
+  });
+}
+
+// (NtError, last_error, append, layout, attention, counts, adjust, accept, commit, fork, extend, copy, compact, paged, beam): addresses of
+// the library's functions
 PyObject* init(PyObject*, PyObject* const* x, Py_ssize_t n) {
-  if (n != 9) {
-    PyErr_SetString(PyExc_TypeError, "init: 9 arguments");
+  constexpr int kArgs = 15;
+  if (n != kArgs) {
+    PyErr_Format(PyExc_TypeError, "init: %d arguments", kArgs);
     return nullptr;
   }
-  void* p[9] = {};
-  for (int i = 1; i < 9; ++i) p[i] = PyLong_AsVoidPtr(x[i]);
+  void* p[kArgs] = {};
+  for (int i = 1; i < kArgs; ++i) p[i] = PyLong_AsVoidPtr(x[i]);
   if (PyErr_Occurred()) return nullptr;
   Py_INCREF(x[0]);
   Py_XDECREF(g_error);
   g_error = x[0];
-  p_last_error = reinterpret_cast<decltype(p_last_error)>(p[1]);
-  p_append = reinterpret_cast<decltype(p_append)>(p[2]);
-  p_layout = reinterpret_cast<decltype(p_layout)>(p[3]);
-  p_attention = reinterpret_cast<decltype(p_attention)>(p[4]);
-  p_counts = reinterpret_cast<decltype(p_counts)>(p[5]);
-  p_adjust = reinterpret_cast<decltype(p_adjust)>(p[6]);
-  p_accept = reinterpret_cast<decltype(p_accept)>(p[7]);
-  p_commit = reinterpret_cast<decltype(p_commit)>(p[8]);
+  int i = 0;
+  auto next = [&](auto& f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(p[++i]); };
+  next(p_last_error);
+  next(p_append);
+  next(p_layout);
+  next(p_attention);
+  next(p_counts);
+  next(p_adjust);
+  next(p_accept);
+  next(p_commit);
+  next(p_fork);
+  next(p_extend);
+  next(p_copy);
+  next(p_compact);
+  next(p_paged);
+  next(p_beam);
   Py_RETURN_NONE;
 }
 
 #define NT_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr }
 PyMethodDef g_methods[] = {NT_METHOD(init),   NT_METHOD(append), NT_METHOD(layout), NT_METHOD(attention), NT_METHOD(counts),
-                           NT_METHOD(adjust), NT_METHOD(accept), NT_METHOD(commit), {nullptr, nullptr, 0, nullptr}};
+                           NT_METHOD(adjust), NT_METHOD(accept), NT_METHOD(commit), NT_METHOD(fork),   NT_METHOD(extend),
+                           NT_METHOD(copy),   NT_METHOD(compact), NT_METHOD(paged), NT_METHOD(beam), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ntbind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,97 @@
+// nt_paged_attention.cu -- attention of ragged chunks of new tokens over a paged bf16 cache: the call.
+#include <cmath>
+
+#include <algorithm>
+
+#include "nt_paged.cuh"
+
+namespace nt {
+namespace {
+
+// Parts of a launch take a slot each, two per CTA.
+size_t part_floats(int D) { return (size_t)2 * kPaFewCtas * kPaFewRows * (D + 2); }
+size_t paged_counts(int T, int S, int Hq, int Hkv) { return ((size_t)T * Hq + (size_t)S * Hkv + 63) / 64 * 64; }
+size_t paged_ws_bytes(int T, int S, int Hq, int Hkv, int D) {
+  return kWsHeaderBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + part_floats(D) * sizeof(float);
+}
+nt_status check_paged(int T, int S, int Hq, int Hkv, int D) {
+  if (D != 64 && D != 128) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
+  if (T < 1 || T > kPagedMaxTokens || S < 1 || S > kPageMaxSeqs) return set_error(NT_ERR_INVALID_ARG, "need 1 <= T <= 1048576 and 1 <= S <= 4096");
+  if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kPaMaxGroup || (int64_t)T * Hq > 1 << 24)
+    return set_error(NT_ERR_INVALID_ARG, "need Hq a multiple of Hkv >= 1, Hq / Hkv <= 64 and T * Hq <= 2^24");
+  return NT_OK;
+}
+
+}  // namespace
+}  // namespace nt
+
+using namespace nt;
+
+extern "C" {
+
+nt_status nt_paged_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, size_t* bytes) {
+  clear_error();
+  if (!bytes) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
+  NT_TRY(check_paged(T, S, Hq, Hkv, D));
+  *bytes = paged_ws_bytes(T, S, Hq, Hkv, D);
+  return NT_OK;
+}
+
+nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const uint16_t* k_pool, const uint16_t* v_pool, int T, int S,
+                             int Hq, int Hkv, int D, int page, int t_stride, const int32_t* table, int width, const int32_t* q_start,
+                             const int32_t* length, int max_new, int window, float cap, const float* slopes_opt, void* out,
+                             uint32_t* n_bad_opt, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  if (!q || !k_pool || !v_pool || !table || !q_start || !length || !out) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
+  if (dtype != NT_F32 && dtype != NT_BF16) return set_error(NT_ERR_INVALID_ARG, "dtype must be NT_F32 or NT_BF16");
+  NT_TRY(check_paged(T, S, Hq, Hkv, D));
+  if (!page_ok(page)) return set_error(NT_ERR_INVALID_ARG, "page must be 16, 32, 64, 128 or 256 rows");
+  if (t_stride < page || width < 1) return set_error(NT_ERR_INVALID_ARG, "need t_stride >= page and width >= 1");
+  if (max_new < 0 || window < 0 || !(cap >= 0.0f) || !std::isfinite(cap))
+    return set_error(NT_ERR_INVALID_ARG, "need max_new, window >= 0 and a finite cap >= 0");
+  if (q_stride % 8 != 0) return set_error(NT_ERR_ALIGNMENT, "q_stride must be a multiple of 8");
+  if (T > 1 && q_stride < (int64_t)Hq * D) return set_error(NT_ERR_INVALID_ARG, "need q_stride >= Hq * D");
+  if (out == q && T > 1 && q_stride != (int64_t)Hq * D) return set_error(NT_ERR_INVALID_ARG, "out may be q where q is contiguous");
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+    return set_error(NT_ERR_ALIGNMENT, "q, out and the pools must be 16-byte aligned");
+  if (!aligned(table, 4) || !aligned(q_start, 4) || !aligned(length, 4) || (slopes_opt && !aligned(slopes_opt, 4)) ||
+      (n_bad_opt && !aligned(n_bad_opt, 4)))
+    return set_error(NT_ERR_ALIGNMENT, "int32 and fp32 arrays must be 4-byte aligned");
+  if (!ws || !aligned(ws, 16) || ws_bytes < paged_ws_bytes(T, S, Hq, Hkv, D))
+    return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_paged_attention_workspace_size");
+  NT_TRY(check_device());
+  PaArgs a{};
+  a.q = q;
+  a.out = out;
+  a.k = k_pool;
+  a.v = v_pool;
+  a.table = table;
+  a.q_start = q_start;
+  a.length = length;
+  a.slopes = slopes_opt;
+  a.n_bad = n_bad_opt;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.err = reinterpret_cast<unsigned int*>(w);
+  a.count = reinterpret_cast<unsigned int*>(w + kWsHeaderBytes);
+  a.part = reinterpret_cast<float*>(a.count + paged_counts(T, S, Hq, Hkv));
+  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * kPaFewCtas * kPaFewRows * D);
+  a.q_stride = q_stride;
+  a.which = kPaAll;
+  a.T = T;
+  a.S = S;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.width = width;
+  a.page = page;
+  a.shift = page_shift(page);
+  a.n_pages = t_stride / page;
+  a.ts = t_stride;
+  a.window = window > 0 ? window : INT32_MAX;
+  a.cap = cap;
+  a.scale = (float)(1.0 / std::sqrt((double)D));
+  const int64_t most = (int64_t)(max_new > 0 ? std::min(max_new, T) : T) * a.G;
+  return launch_paged_few(a, dtype, D, most, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

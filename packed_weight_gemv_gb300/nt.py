@@ -59,6 +59,8 @@ EXPORTS = (
     "nt_rope_frequencies", "nt_qk_norm_rope_append", "nt_tree_layout", "nt_tree_attention_workspace_size",
     "nt_tree_attention", "nt_token_counts", "nt_logits_adjust_workspace_size", "nt_logits_adjust",
     "nt_tree_accept", "nt_tree_commit",
+    "nt_page_fork", "nt_page_extend", "nt_page_copy", "nt_page_compact_workspace_size", "nt_page_compact",
+    "nt_paged_attention_workspace_size", "nt_paged_attention", "nt_beam_select_workspace_size", "nt_beam_select",
     "nt_decode_plan_create", "nt_decode_step", "nt_decode_step_status", "nt_decode_plan_reset",
     "nt_decode_plan_set_position",
     "nt_decode_plan_trace_layout", "nt_decode_plan_set_trace", "nt_decode_plan_capture_size",
@@ -106,7 +108,8 @@ _bind = None  # the native binding of the tree-verify calls
 
 # What the native binding calls, in the order of its init().
 _BOUND = ("nt_last_error_string", "nt_qk_norm_rope_append", "nt_tree_layout", "nt_tree_attention", "nt_token_counts",
-          "nt_logits_adjust", "nt_tree_accept", "nt_tree_commit")
+          "nt_logits_adjust", "nt_tree_accept", "nt_tree_commit", "nt_page_fork", "nt_page_extend", "nt_page_copy",
+          "nt_page_compact", "nt_paged_attention", "nt_beam_select")
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -157,6 +160,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "nt_logits_adjust": ([vp, i, i, vp, i64, vp, i, vp, f, f, f, vp, i64, vp, i64, vp, vp, vp, sz, vp], i),
             "nt_tree_accept": ([vp, vp, vp, i, vp, vp, vp, vp], i),
             "nt_tree_commit": ([vp, vp, i, i, i, i, vp, vp, i, i, i, vp], i),
+            "nt_page_fork": ([vp, vp, i, i, vp, i, i, vp, i, vp, vp, vp, vp], i),
+            "nt_page_extend": ([vp, vp, i, i, vp, i, i, vp, i, vp, vp, vp, vp, vp], i),
+            "nt_page_copy": ([vp, vp, i, i, i, i, i, vp, i, vp], i),
+            "nt_page_compact_workspace_size": ([i, ctypes.POINTER(sz)], i),
+            "nt_page_compact": ([vp, i, vp, vp, i, i, i, vp, i, vp, vp, vp, sz, vp], i),
+            "nt_paged_attention_workspace_size": ([i, i, i, i, i, ctypes.POINTER(sz)], i),
+            "nt_paged_attention": ([vp, i, i64, vp, vp, i, i, i, i, i, i, i, vp, i, vp, vp, i, i, f, vp, vp, vp, vp, sz, vp], i),
+            "nt_beam_select_workspace_size": ([i, i, ctypes.POINTER(sz)], i),
+            "nt_beam_select": ([vp, vp, i, i, i, i, vp, i, vp, d, vp, vp, vp, vp, vp, sz, vp], i),
             "nt_decode_plan_create": ([ctypes.POINTER(nt_decode_desc), ctypes.POINTER(vp)], i),
             "nt_decode_step": ([vp, vp], i),
             "nt_decode_step_status": ([vp, ctypes.POINTER(i)], i),
@@ -469,15 +481,82 @@ class pointer_array:
         return len(self._keep)
 
 
-def nt_tree_commit(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, path: torch.Tensor,
-                   n_emit: torch.Tensor, src_row0: int, dst_row0: int, stream=None):
-    """Moves the accepted nodes' rows in every layer's caches (pointer_array); path [B], n_emit [1] int32."""
+def _layers(call: str, k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int) -> int:
     n = len(k_caches)
     if (n == 0 or len(v_caches) != n or k_caches.shape != (Hkv, t_stride, D) or v_caches.shape != k_caches.shape
             or v_caches.cuda_device != k_caches.cuda_device):
-        raise NtError(NT_ERR_INVALID_ARG, "nt_tree_commit", "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
+        raise NtError(NT_ERR_INVALID_ARG, call, "k_caches and v_caches must hold one [Hkv, t_stride, D] cache per layer each")
+    return n
+
+
+def nt_tree_commit(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, path: torch.Tensor,
+                   n_emit: torch.Tensor, src_row0: int, dst_row0: int, stream=None):
+    """Moves the accepted nodes' rows in every layer's caches (pointer_array); path [B], n_emit [1] int32."""
+    n = _layers("nt_tree_commit", k_caches, v_caches, Hkv, D, t_stride)
     _native().commit(k_caches.address, v_caches.address, n, Hkv, D, t_stride, path, n_emit, src_row0, dst_row0, stream,
                      k_caches.cuda_device)
+
+
+# ---- several sequences over a paged cache --------------------------------------------------
+# Through the native binding as well. Tables are int32 [S, width], lengths and parents int32 [S], refs int32 [n_pages].
+def nt_page_fork(table: torch.Tensor, length: torch.Tensor, parent: torch.Tensor, refs: torch.Tensor, page: int,
+                 table_out: torch.Tensor, length_out: torch.Tensor, n_bad: Optional[torch.Tensor] = None, stream=None):
+    """Sequence i of table_out goes on as sequence parent[i] of table (-1: empty); refs follow."""
+    _native().fork(table, length, parent, refs, page, table_out, length_out, n_bad, stream)
+
+
+def nt_page_extend(table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor, q_start: torch.Tensor, page: int,
+                   rows: torch.Tensor, pos: torch.Tensor, pairs: torch.Tensor, n_bad: Optional[torch.Tensor] = None, stream=None):
+    """Pages for the new tokens q_start [S + 1]; rows and pos [T] of every token, pairs [S, 2] of pages to copy first."""
+    _native().extend(table, length, refs, q_start, page, rows, pos, pairs, n_bad, stream)
+
+
+def nt_page_copy(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, page: int,
+                 pairs: torch.Tensor, stream=None):
+    """Copies page pairs[i, 0] to page pairs[i, 1] in every layer's caches (pointer_array)."""
+    n = _layers("nt_page_copy", k_caches, v_caches, Hkv, D, t_stride)
+    _native().copy(k_caches.address, v_caches.address, n, Hkv, D, t_stride, page, pairs, stream, k_caches.cuda_device)
+
+
+def nt_page_compact_workspace_size(n_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().nt_page_compact_workspace_size(n_pages, ctypes.byref(n)), "nt_page_compact_workspace_size")
+    return n.value
+
+
+def nt_page_compact(refs: torch.Tensor, table: torch.Tensor, length: torch.Tensor, page: int, pairs: torch.Tensor,
+                    n_used: torch.Tensor, ws: torch.Tensor, n_bad: Optional[torch.Tensor] = None, stream=None):
+    """Pages in use to the front: table and refs follow, pairs [n_pages // 2 or more, 2] are the moves for nt_page_copy."""
+    _native().compact(refs, table, length, page, pairs, n_used, n_bad, ws, stream)
+
+
+def nt_paged_attention_workspace_size(T: int, S: int, Hq: int, Hkv: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().nt_paged_attention_workspace_size(T, S, Hq, Hkv, D, ctypes.byref(n)),
+           "nt_paged_attention_workspace_size")
+    return n.value
+
+
+def nt_paged_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, page: int, table: torch.Tensor,
+                       q_start: torch.Tensor, length: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, max_new: int = 0,
+                       window: int = 0, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                       n_bad: Optional[torch.Tensor] = None, stream=None):
+    """q [T, Hq, D] fp32 or bf16 (tokens any stride apart), out the same contiguous, pools [Hkv, t_stride, D] bf16."""
+    _native().paged(q, k_pool, v_pool, page, table, q_start, length, out, ws, max_new, window, cap, slopes, n_bad, stream)
+
+
+def nt_beam_select_workspace_size(V: int, N: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().nt_beam_select_workspace_size(V, N, ctypes.byref(n)), "nt_beam_select_workspace_size")
+    return n.value
+
+
+def nt_beam_select(logits: torch.Tensor, scores: torch.Tensor, beams: int, parent: torch.Tensor, token: torch.Tensor,
+                   score: torch.Tensor, ws: torch.Tensor, done: Optional[torch.Tensor] = None,
+                   done_out: Optional[torch.Tensor] = None, eos: int = -1, lengths: Optional[torch.Tensor] = None,
+                   alpha: float = 0.0, stream=None):
+    """logits [N, V] fp32 and scores [N] of N / beams groups -> the best of each: parent, token (int32), score [groups * K]."""
+    _native().beam(logits, scores, beams, parent, token, score, done, done_out, eos, lengths, alpha, ws, stream)
 
 
 class DecodePlan:
