@@ -103,8 +103,8 @@ const char* nt_last_error_string(void);
 /* Status of a workspace after the calls that used it ("A 104 microsecond floor ...": the
  * kernels that stream the weights wait on copies in flight, and every such wait here has a time
  * limit). Every workspace the library takes (nt_ternary_gemm, nt_ternary_gemm_multi,
- * nt_int8_logits_argmax, nt_tree_attention, nt_logits_adjust) begins with a 16-byte status header. When a bounded device-side wait
- * of a call runs out (the streaming output projection: 250 ms; the tensor-core GEMMs and nt_tree_attention: 2 s), the
+ * nt_int8_logits_argmax, nt_tree_attention, nt_logits_adjust and those of the paged cache) begins with a 16-byte status header. When a bounded device-side wait
+ * of a call runs out (the streaming output projection: 250 ms; the tensor-core GEMMs, nt_tree_attention and nt_paged_attention: 2 s), the
  * kernel records an error code and its CTA there instead of hanging; that call's outputs are
  * invalid (the output projection writes -1 as every vector's arg-max). The code stays until the
  * caller zero-fills the whole workspace again, and until then the results of every call that
@@ -120,8 +120,8 @@ nt_status nt_workspace_status(const void* ws, nt_status* device_status);
  * timeout_ms (<= 0 keeps the normal limits) and the call's workspace reports NT_ERR_TIMEOUT.
  *   fault 1: the streaming output projection (nt_int8_logits_argmax and its allocation-free
  *            variant at B = 1); 2: the tcgen05 path of nt_ternary_gemm (2..16 vectors with a
- *            workspace, N >= 128); 3: the prefill GEMM (64 or more vectors); 5: nt_tree_attention; 0: none
- *   (4 is not assigned).
+ *            workspace, N >= 128); 3: the prefill GEMM (64 or more vectors); 5: nt_tree_attention; 6: nt_paged_attention
+ *   on the tensor cores; 0: none (4 is not assigned).
  * Process-wide; set it only while no other thread launches library calls. No GPU fault is
  * involved: every wait gives up cleanly and the context stays usable. */
 nt_status nt_set_test_fault(int fault, double timeout_ms);
@@ -535,7 +535,7 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *   out[t][h] = sum_j softmax_j(x) v[j]
  * keys and values of head h / (Hq / Hkv). Tokens at q_start[S] and behind are left as they were; a token that sees nothing gets
  * 0. What a token does not see has no part in its result, whatever it holds: rows behind the sequence's in its last page, and later
- * tokens', may be NaN or infinite.
+ * tokens', may be NaN or infinite. A score or value that is seen and not finite makes the result NaN or infinite.
  *   q, out [T][Hq][D] of type dtype (nt_dtype; out may be q), q's tokens q_stride elements apart (a multiple of 8); k_pool, v_pool [Hkv][t_stride][D] bf16;
  *     D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64, T * Hq <= 2^24; all 16-byte aligned
  *   table [S][width], q_start [S + 1] (rising; values taken as within [0, T]), length [S] (taken as within [0, width * page])

@@ -5,6 +5,7 @@
 #include <mutex>
 #include <string>
 
+#include "nt_pages.cuh"
 #include "nt_tree.cuh"
 
 namespace nt {
@@ -118,8 +119,8 @@ const char* nt_last_error_string(void) { return g_last_error.c_str(); }
 
 nt_status nt_set_test_fault(int fault, double timeout_ms) {
   clear_error();
-  if (fault < kFaultNone || (fault > kFaultPrefill && fault != kFaultTree))
-    return set_error(NT_ERR_INVALID_ARG, "fault must be 0..3 or 5");
+  if (fault < kFaultNone || (fault > kFaultPrefill && fault != kFaultTree && fault != kFaultPaged))
+    return set_error(NT_ERR_INVALID_ARG, "fault must be 0..3, 5 or 6");
   g_fault_timeout_ns.store(timeout_ms > 0 ? (uint64_t)(timeout_ms * 1e6) : 0, std::memory_order_relaxed);
   g_fault.store(fault, std::memory_order_relaxed);
   return NT_OK;

@@ -15,6 +15,7 @@ namespace nt {
 constexpr int kPaFewRows = 8;     // rows up to which a sequence's tokens take the kernel without tensor cores
 constexpr int kPaFewCtas = 320, kPaManyCtas = 160;  // of a launch at most (the workspace's size, asked for without a device, goes by them)
 constexpr int kPaMaxGroup = 64;
+constexpr uint64_t kPaTimeoutNs = 2000000000ull;
 
 enum : int { kPaAll = 0, kPaFew = 1, kPaMany = 2 };  // which sequences a launch takes: any; up to kPaFewRows rows; more
 
@@ -32,6 +33,7 @@ struct PaArgs {
   float* scratch;           // [CTAs][2][D][128] sums taken off the tensor cores
   uint64_t timeout_ns;
   int64_t q_stride;
+  int64_t jobs;             // places of `count`
   int fault, which;
   int T, S, Hq, Hkv, G, width, page, shift, n_pages, ts;
   int window;               // INT32_MAX: none
@@ -116,7 +118,7 @@ struct PaShare {
 __device__ __forceinline__ int64_t pa_from(int64_t work, int c, int ctas) { return work * c / ctas; }
 __device__ __forceinline__ int pa_with(int64_t work, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / work); }
 
-// starts: S + 1 places of shared memory (scratch); all threads of the CTA, every one gets the share.
+// starts: S places of shared memory (scratch); all threads of the CTA, every one gets the share.
 template <int kThreads, int kKeys>
 __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
   __shared__ int64_t s_warps[32];
@@ -131,7 +133,8 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
     if (s < a.S) starts[s] = (int)(units + at);
     units += total;
   }
-  if (i == 0) starts[a.S] = (int)units;
+  PaShare r{};
+  if (units * a.Hkv > a.jobs) return r;  // starts that do not rise name more tokens than there are: no work
   __syncthreads();
   auto tiles = [&](int64_t u, int* s_out, int* mt_out) -> int64_t {
     if (u >= units) return 0;
@@ -145,7 +148,6 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
     *mt_out = (int)u - starts[s];
     return (int64_t)pa_unit<kKeys>(a, s, *mt_out, rows).tiles * a.Hkv;
   };
-  PaShare r{};
   int s = 0, mt = 0;
   int64_t mine = 0, at = 0;
   for (int64_t u0 = 0; u0 < units; u0 += kThreads) {
@@ -239,5 +241,7 @@ struct PaWalk {
 
 // Up to 8 rows of a sequence to a CTA (max_rows: the most that a sequence is expected to have).
 nt_status launch_paged_few(const PaArgs& a, int dtype, int D, int64_t max_rows, cudaStream_t st);
+// Any number of rows, on the tensor cores.
+nt_status launch_paged_many(const PaArgs& a, int dtype, int D, int64_t max_rows, cudaStream_t st);
 
 }  // namespace nt

@@ -8,11 +8,19 @@
 namespace nt {
 namespace {
 
-// Parts of a launch take a slot each, two per CTA.
-size_t part_floats(int D) { return (size_t)2 * kPaFewCtas * kPaFewRows * (D + 2); }
+// Parts of a launch take a slot each, two per CTA; on the tensor cores each has up to 256 rows (fewer where the call has), and a
+// CTA's sums beside.
+int64_t part_rows(int T, int Hq, int Hkv) {
+  const int64_t rows = (int64_t)T * (Hq / Hkv);
+  const int64_t many = rows <= kPaFewRows ? 0 : (int64_t)2 * kPaManyCtas * (rows <= 128 ? 128 : 256);
+  return std::max<int64_t>(many, 2 * kPaFewCtas * kPaFewRows);
+}
+size_t scratch_floats(int T, int Hq, int Hkv, int D) {
+  return (int64_t)T * (Hq / Hkv) <= kPaFewRows ? 0 : (size_t)kPaManyCtas * 2 * 128 * D;
+}
 size_t paged_counts(int T, int S, int Hq, int Hkv) { return ((size_t)T * Hq + (size_t)S * Hkv + 63) / 64 * 64; }
 size_t paged_ws_bytes(int T, int S, int Hq, int Hkv, int D) {
-  return kWsHeaderBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + part_floats(D) * sizeof(float);
+  return kWsHeaderBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + (part_rows(T, Hq, Hkv) * (D + 2) + scratch_floats(T, Hq, Hkv, D)) * sizeof(float);
 }
 nt_status check_paged(int T, int S, int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
@@ -74,8 +82,12 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   a.err = reinterpret_cast<unsigned int*>(w);
   a.count = reinterpret_cast<unsigned int*>(w + kWsHeaderBytes);
   a.part = reinterpret_cast<float*>(a.count + paged_counts(T, S, Hq, Hkv));
-  a.ml = reinterpret_cast<float2*>(a.part + (size_t)2 * kPaFewCtas * kPaFewRows * D);
+  a.scratch = a.part + part_rows(T, Hq, Hkv) * D;
+  a.ml = reinterpret_cast<float2*>(a.scratch + scratch_floats(T, Hq, Hkv, D));
+  a.timeout_ns = test_fault_timeout_ns(kPaTimeoutNs);
+  a.fault = test_fault() == kFaultPaged;
   a.q_stride = q_stride;
+  a.jobs = (int64_t)T * Hq + (int64_t)S * Hkv;
   a.which = kPaAll;
   a.T = T;
   a.S = S;
@@ -91,7 +103,16 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   a.cap = cap;
   a.scale = (float)(1.0 / std::sqrt((double)D));
   const int64_t most = (int64_t)(max_new > 0 ? std::min(max_new, T) : T) * a.G;
-  return launch_paged_few(a, dtype, D, most, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (most <= kPaFewRows) return launch_paged_few(a, dtype, D, most, st);
+  if (S == 1) return launch_paged_many(a, dtype, D, most, st);
+  // Sequences of few rows are bound by memory, and on the tensor cores each would take a tile for itself.
+  if (a.G <= kPaFewRows) {
+    a.which = kPaFew;
+    NT_TRY(launch_paged_few(a, dtype, D, a.G, st));  // a token's rows to a tile
+    a.which = kPaMany;
+  }
+  return launch_paged_many(a, dtype, D, most, st);
 }
 
 }  // extern "C"

@@ -352,9 +352,9 @@ template <typename T, int D, int R, bool kExtra>
 nt_status launch_few(const PaArgs& a, cudaStream_t st) {
   const int per = R <= 2 ? 2 : 1;
   const int ctas = std::min(per * device_sm_count(), kPaFewCtas);
-  const size_t smem = ((size_t)a.S + 1) * sizeof(int);
+  const size_t smem = (size_t)a.S * sizeof(int);
   static std::atomic<int> allowed[64];
-  NT_TRY(allow_smem(paged_few_kernel<T, D, R, kExtra>, (kPageMaxSeqs + 1) * (int)sizeof(int), allowed));
+  NT_TRY(allow_smem(paged_few_kernel<T, D, R, kExtra>, kPageMaxSeqs * (int)sizeof(int), allowed));
   NT_CUDA_TRY(launch_kernel(paged_few_kernel<T, D, R, kExtra>, dim3((unsigned)ctas), dim3(kFewThreads), smem, st, true, a));
   return check_launch("paged_few_kernel");
 }

@@ -1,0 +1,634 @@
+// nt_paged_many.cu -- paged attention of chunks of new tokens on the tensor cores.
+//
+//   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(x_j log2(e) - m)
+//
+// The query rows of a tile (128 rows: tokens x the G heads of a key-value head) are the M side of tcgen05.mma. 128 keys at a time
+// are the N side of the scores S = Q K^T; the softmax turns S into weights P in the place of S in tensor memory, and P is the A operand of
+// O += P V. Two groups of 128 threads (thread = row = tensor-memory lane) take turns, so that one's exponentials run under
+// the other's products: each has a tile of rows of its own over the same keys (bf16 queries, more than 128 rows: 256 rows to a CTA), or both have
+// the same rows and every other tile of keys, with sums of their own that are joined at the end (fp32 queries, whose three bf16 terms
+// take the shared memory of three tiles; and up to 128 rows).
+//
+// CTA (384 threads): warp 0 asks for the pages (TMA boxes of one page each, 128-byte swizzle) into a ring of tiles; one lane of
+// warp 1 issues all MMAs, in the order S(1st), S(2nd), { O, next S } of the groups in turn, so the tensor pipe has one group's products
+// while the other group's weights are formed, and a commit behind an S also tells that the O before it is done; warps 4-7 and 8-11 are
+// the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
+//
+// fp32 queries enter as three bf16 terms without loss and their weights as two rounded ones (2^-17); bf16 queries' weights are rounded to
+// bf16, and the sum of the weights is that of the rounded ones, so a row that one key decides is exact. The tensor core
+// cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
+// that round to nearest.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+#include <string>
+#include <type_traits>
+
+#include "nt_tree_attn.cuh"
+#include "nt_paged.cuh"
+
+namespace nt {
+namespace {
+
+constexpr int kPmKeys = 128;
+constexpr int kPmLoad = 0, kPmMma = 1, kPmFirstSoftmax = 4;
+constexpr int kPmThreads = 32 * kPmFirstSoftmax + 256;
+constexpr int kPmSmem = 224 * 1024;
+
+struct PmMaps {
+  CUtensorMap k, v;  // boxes of 64 dimensions x a page (at most 128 rows)
+};
+
+template <typename T, int D, bool kPair>
+struct PmShape {
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr int kTermsQ = kF32 ? 3 : 1, kTermsP = kF32 ? 2 : 1;
+  static constexpr int kRows = kPair ? 256 : 128;
+  static constexpr int kSlot = kPmKeys * D * 2;
+  static constexpr int kQTile = 128 * D * 2;  // one term of 128 rows
+  static constexpr int kQBytes = kQTile * kTermsQ * (kPair ? 2 : 1);
+  static constexpr int kStages = std::min(8, (kPmSmem - kQBytes) / kSlot);
+  static constexpr int kAhead = kPair ? 1 : 2;  // tiles whose scores are formed before the first weights
+  static constexpr int kColO = 0, kColS = 2 * D;
+  // A tile costs a sum at most 16 (fp32) or 8 cuts of 2^-23: 2^-16 over 8 tiles, 2^-14 over 64.
+  static constexpr int kFlush = kF32 ? 8 : 64;
+  static constexpr int kSmem = kQBytes + kStages * kSlot + 1024;
+  static_assert(kStages >= 4, "ring");
+  static_assert(kColS + 2 * kPmKeys <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kPageMaxSeqs * 4 <= kStages * kSlot, "the division's scratch stands in the ring");
+};
+
+__device__ __forceinline__ void store_row(float* p, const float (&o)[16], float f) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f);
+}
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&o)[16], float f) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 8)
+    *reinterpret_cast<uint4*>(p + e) = make_uint4(pack_rn(o[e] * f, o[e + 1] * f), pack_rn(o[e + 2] * f, o[e + 3] * f),
+                                                  pack_rn(o[e + 4] * f, o[e + 5] * f), pack_rn(o[e + 6] * f, o[e + 7] * f));
+}
+
+template <typename T, int D, bool kPair, bool kExtra>
+__global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_constant__ PmMaps maps, const __grid_constant__ PaArgs a) {
+  using S = PmShape<T, D, kPair>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* q_smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = q_smem + S::kQBytes;
+  constexpr int kBars = 2 * S::kStages + 6;
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_fail, s_bad, s_last;
+  volatile int* fail = &s_fail;
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages, pfull0 = sfull0 + 16,
+                 qfull = pfull0 + 16, drain = qfull + 8;
+  if (i < kBars) {
+    const int b = i - 2 * S::kStages;  // a group's four warps arrive at pfull, all eight at qfull
+    bar_init(full0 + 8 * i, b == 2 || b == 3 ? 4 : b == 4 ? 8 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (i == 0) s_fail = s_bad = 0;
+  if (warp == kPmMma) tm_alloc(smem_u32(&tmem_slot), kTaTmemCols);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = tmem_slot;
+  dependent_launch_wait();
+  PaWalk<kPmKeys> walk(a, pa_share<kPmThreads, kPmKeys>(a, S::kRows, reinterpret_cast<int*>(ring)), S::kRows);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before copies over the division's scratch
+  __syncthreads();
+  auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
+  auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
+  auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
+  auto slot = [&](int k) { return smem_u32(ring) + (k % S::kStages) * S::kSlot; };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+  // Ring order of a piece of n tiles: the keys of the first kAhead, then values j and keys j + kAhead in turn.
+  auto ring_val = [&](int j, int n) { return min(S::kAhead, n) + j + min(j, max(n - S::kAhead, 0)); };
+  auto ring_key = [&](int j) { return j < S::kAhead ? j : 2 * j - S::kAhead + 1; };
+  int k0 = 0;  // tiles of the pieces before
+
+  if (warp == kPmLoad) {
+    const int per = min(a.page, kPmKeys), boxes = kPmKeys / per;  // rows of a box; boxes of 64 dimensions of a tile
+    const int box = lane % boxes, half = lane / boxes;
+    const bool mine = half < D / 64;
+    bool ok = true;
+    int bad = 0, issued = 0;
+    for (; walk.more() && ok;) {
+      const PaPiece p = walk.piece(a);
+      const int hi = p.u.p1 + 1;  // no row sees this key
+      const int32_t* ids = a.table + (int64_t)p.u.s * a.width;
+      auto row_of = [&](int j) {  // the cache row of this lane's box of tile j; behind the pool (zeros) where nothing is seen
+        const int key = (p.u.tile0 + p.t0 + j) * kPmKeys + box * per;
+        if (j >= p.n || key >= hi) return a.ts;
+        const int id = ids[key >> a.shift];
+        if ((unsigned)id >= (unsigned)a.n_pages) {
+          bad = 1;
+          return a.ts;
+        }
+        return (id << a.shift) + (key & (a.page - 1));
+      };
+      int row[S::kAhead + 1];  // of the tiles whose values are to come
+#pragma unroll
+      for (int j = 0; j <= S::kAhead; ++j) row[j] = row_of(j);
+      auto load = [&](int k, const CUtensorMap* map, int y) {
+        if (k >= S::kStages && !bar_wait_warp(empty(k), turn(k) ^ 1u, fail, a.timeout_ns)) return false;
+        if (lane == 0) bar_expect_tx(full(k), S::kSlot);
+        __syncwarp();
+        if (mine) tma_3d(slot(k) + half * (kPmKeys * 128) + box * per * 128, map, half * 64, y, p.g, full(k));
+        issued = k + 1;
+        return true;
+      };
+      if (a.fault) ok = false;
+#pragma unroll
+      for (int j = 0; j < S::kAhead; ++j)
+        if (j < p.n) ok = ok && load(k0 + j, &maps.k, row[j]);
+      for (int j = 0; ok && j < p.n; ++j) {
+        const int next = row_of(j + S::kAhead + 1);
+        ok = load(k0 + ring_val(j, p.n), &maps.v, row[0]);
+        if (ok && j + S::kAhead < p.n) ok = load(k0 + ring_key(j + S::kAhead), &maps.k, row[S::kAhead]);
+#pragma unroll
+        for (int e = 0; e < S::kAhead; ++e) row[e] = row[e + 1];
+        row[S::kAhead] = next;
+      }
+      k0 += 2 * p.n;
+      walk.next(a, p);
+    }
+    if (!ok) {  // every copy must land before the CTA may exit
+      const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+      for (int k = max(0, issued - S::kStages); k < issued; ++k)
+        while (!bar_try(full(k), turn(k)))
+          if (globaltimer_ns() > deadline) break;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0 && bad && a.n_bad) atomicAdd(a.n_bad, 1u);
+  } else if (warp == kPmMma) {
+    if (elect_one()) {
+      bool ok = true;
+      int piece = 0, steps[2] = {0, 0};  // steps of the groups so far
+      for (; walk.more() && ok; ++piece) {
+        const PaPiece p = walk.piece(a);
+        const int n = p.n;
+        auto scores = [&](int x, int k) {
+          const uint32_t d = tmem + S::kColS + x * kPmKeys;
+          const uint64_t bd = sdesc(slot(k), 16);
+          // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
+#pragma unroll
+          for (int t = S::kTermsQ - 1; t >= 0; --t) {
+            const uint64_t ad = sdesc(smem_u32(q_smem) + ((kPair ? x : 0) * S::kTermsQ + t) * S::kQTile, 16);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16;
+              mma_smem_a(d, ad + at, bd + at, idesc_bf16(kPmKeys, false), t < S::kTermsQ - 1 || kk > 0);
+            }
+          }
+        };
+        ok = wait(qfull, piece & 1);
+        tm_fence_after();
+        int c[2] = {0, 0};  // steps of the groups in this piece
+        if constexpr (kPair) {
+          ok = ok && wait(full(k0), turn(k0));
+          tm_fence_after();
+          if (ok) {
+            scores(0, k0);
+            mma_commit(sfull0);
+            scores(1, k0);
+            mma_commit(sfull0 + 8);
+            mma_commit(empty(k0));
+          }
+        } else {
+          for (int x = 0; x < 2 && x < n && ok; ++x) {
+            ok = wait(full(k0 + x), turn(k0 + x));
+            tm_fence_after();
+            if (!ok) break;
+            scores(x, k0 + x);
+            mma_commit(sfull0 + 8 * x);
+            mma_commit(empty(k0 + x));
+          }
+        }
+        for (int s = 0; ok && s < (kPair ? 2 * n : n); ++s) {
+          const int x = s & 1, j = kPair ? s >> 1 : s, kv = k0 + ring_val(j, n), next = j + S::kAhead, kk0 = k0 + ring_key(next);
+          const bool first = !kPair || x == 0, last = !kPair || x == 1;
+          if (first) ok = wait(full(kv), turn(kv));
+          ok = ok && wait(pfull0 + 8 * x, steps[x] & 1);
+          if (!ok) break;
+          tm_fence_after();
+          const uint64_t bd = sdesc(slot(kv), kPmKeys * 128);
+          const bool fresh = c[x] % S::kFlush == 0;
+#pragma unroll
+          for (int t = S::kTermsP - 1; t >= 0; --t)
+#pragma unroll
+            for (int kk = 0; kk < kPmKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
+              mma_tmem_a(tmem + S::kColO + x * D, tmem + S::kColS + x * kPmKeys + t * (kPmKeys / 2) + 8 * kk, bd + kk * 2048 / 16,
+                         idesc_bf16(D, true, t == 1), t < S::kTermsP - 1 || kk > 0 || !fresh);
+          if (next < n) {
+            if (first) ok = wait(full(kk0), turn(kk0));
+            if (!ok) break;
+            tm_fence_after();
+            scores(x, kk0);
+          }
+          if (last) {
+            mma_commit(empty(kv));
+            if (next < n) mma_commit(empty(kk0));
+          }
+          mma_commit(sfull0 + 8 * x);  // the last word of a piece: nothing is under way behind it
+          ++steps[x];
+          ++c[x];
+        }
+        k0 += 2 * n;
+        walk.next(a, p);
+      }
+      if (!ok) {
+        mma_commit(drain);
+        const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+        while (!bar_try(drain, 0))
+          if (globaltimer_ns() > deadline) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kPmFirstSoftmax) {
+    const int quarter = warp & 3, x = (warp - kPmFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // group; tensor-memory lane
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    float* scratch = a.scratch + ((int64_t)blockIdx.x * 2) * D * 128 + ln;  // [2][D][128]
+    float4* s_stat = reinterpret_cast<float4*>(q_smem);  // [2][128], when the queries have been read
+    bool ok = true;
+    uint32_t phase = 0;  // of sfull
+    auto meet = [&] { asm volatile("bar.sync 9, 256;" ::: "memory"); };
+    for (; walk.more();) {
+      const PaPiece p = walk.piece(a);
+      const PaUnit& u = p.u;
+      const int n = p.n;
+      const int row0 = u.mt * S::kRows;
+      {  // the queries' terms into shared memory, rows of 64 dimensions with the 128-byte swizzle
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kMine = kPair ? 32 : 16;
+        const int c = lane % kLanes;
+        uint8_t* to = q_smem + (kPair ? x * S::kTermsQ * S::kQTile : 0) + (c >> 3) * (128 * 128);
+#pragma unroll 4
+        for (int e = 0; e < kMine; e += kAt) {
+          const int r = quarter * 32 + (kPair ? 0 : x * 16) + e + lane / kLanes;  // row of the tile
+          const int ru = (kPair ? x * 128 : 0) + r, ra = row0 + ru, tok = ra / a.G;
+          const bool live = ru < u.rows;
+          const T* q = static_cast<const T*>(a.q) + (int64_t)(u.t0 + tok) * a.q_stride + (int64_t)(p.g * a.G + ra - tok * a.G) * D + c * 8;
+          uint4 w[S::kTermsQ];
+          if constexpr (S::kF32) {
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 f0 = live ? reinterpret_cast<const uint4*>(q)[0] : z, f1 = live ? reinterpret_cast<const uint4*>(q)[1] : z;
+            uint32_t t0[3], t1[3], t2[3], t3[3];
+            split(__uint_as_float(f0.x), __uint_as_float(f0.y), t0);
+            split(__uint_as_float(f0.z), __uint_as_float(f0.w), t1);
+            split(__uint_as_float(f1.x), __uint_as_float(f1.y), t2);
+            split(__uint_as_float(f1.z), __uint_as_float(f1.w), t3);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              const uint32_t sign = t == 1 ? 0x80008000u : 0u;
+              w[t] = make_uint4(t0[t] ^ sign, t1[t] ^ sign, t2[t] ^ sign, t3[t] ^ sign);
+            }
+          } else {
+            w[0] = live ? *reinterpret_cast<const uint4*>(q) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int t = 0; t < S::kTermsQ; ++t) *reinterpret_cast<uint4*>(to + t * S::kQTile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[t];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bar_arrive_warp(qfull, lane);
+      }
+      const int ru = (kPair ? x * 128 : 0) + ln;           // row of the unit
+      const bool live = ru < u.rows, idle = ru - lane >= u.rows;  // warps of rows past the last one only keep the barriers going
+      const int ra = row0 + min(ru, u.rows - 1), tok = ra / a.G, h = p.g * a.G + ra - tok * a.G;
+      const int pos = u.len - u.n + tok;
+      const int lo = (int)max((int64_t)0, (int64_t)pos - a.window + 1);
+      const int sure_lo = (int)max((int64_t)0, (int64_t)u.p1 - a.window + 1);  // every row sees from here to u.p0
+      const float slope = kExtra && a.slopes ? a.slopes[h] : 0.0f;
+      const int cnt = kPair ? n : (n + 1 - x) / 2;
+      const int key_first = (u.tile0 + p.t0) * kPmKeys;
+      auto partial = [&](int key) { return key + kPmKeys - 1 > u.p0 || key < sure_lo; };
+      float m = -INFINITY, l = 0.0f, sums_m = -INFINITY;
+      bool summed = false;
+      for (int c = 0; c < cnt; ++c) {
+        const int j = kPair ? c : 2 * c + x, key0 = key_first + j * kPmKeys;
+        ok = ok && bar_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
+        ++phase;
+        tm_fence_after();
+        float s[kPmKeys];
+        if (ok && !idle) {
+          tm_load(tl + S::kColS + x * kPmKeys, s);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPmKeys; ++e) s[e] = 0.0f;
+        }
+        const bool part = partial(key0);
+        if (part) {  // values that are not finite are taken out: some row may not see them
+          const int k = k0 + ring_val(j, n);
+          ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
+          bool bad = false;
+          for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
+            uint4* at = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
+            const uint4 v = *at;
+            if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
+              uint16_t* w = reinterpret_cast<uint16_t*>(at);
+              for (int y = 0; y < 8; ++y)
+                if ((w[y] & 0x7f80u) == 0x7f80u) w[y] = 0;
+              bad = true;
+            }
+          }
+          if (bad) s_bad = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        if constexpr (kExtra) {
+          if (a.cap > 0.0f) {
+            // cap tanh(y / cap) = cap - 2 cap / (1 + e^(2 y / cap)): within 2^-22 of cap
+            const float f = a.scale / a.cap * 2.885390081777927f, c2 = -2.0f * a.cap;
+#pragma unroll
+            for (int e = 0; e < kPmKeys; ++e) s[e] = fmaf(c2, __frcp_rn(1.0f + ex2(s[e] * f)), a.cap);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPmKeys; ++e) s[e] *= a.scale;
+          }
+          if (a.slopes) {
+            const float away = (float)(pos - key0);
+#pragma unroll
+            for (int e = 0; e < kPmKeys; ++e) s[e] = fmaf(slope, (float)e - away, s[e]);
+          }
+        }
+        if (part) {
+          const int to = pos - key0, from = lo - key0;
+#pragma unroll
+          for (int e = 0; e < kPmKeys; ++e)
+            if (e > to || e < from) s[e] = -INFINITY;
+        }
+        const float f = kExtra ? 1.4426950408889634f : a.scale * 1.4426950408889634f;
+        float mx2[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < kPmKeys; e += 8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (e + 2 * y + 1 < kPmKeys) mx2[y] = max3(mx2[y], s[e + 2 * y], s[e + 2 * y + 1]);
+        }
+        const float mx = fmaxf(fmaxf(mx2[0], mx2[1]), fmaxf(mx2[2], mx2[3])) * f;
+        const bool fresh = c % S::kFlush == 0;
+        if (fresh && c > 0 && ok && !idle) {  // O to the sums, which are in units of a reference of their own
+          const float scale = sums_m == m ? 1.0f : ex2(sums_m - m);
+          float* to = scratch + (int64_t)x * D * 128;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+            tm_load(tl + S::kColO + x * D + d, o);
+            if (summed) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(to[(d + e) * 128], scale, o[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) to[(d + e) * 128] = o[e];
+          }
+          sums_m = m;
+          summed = true;
+        }
+        if (!idle && ok) {
+          if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
+            const float to = fmaxf(m, mx), corr = to == m ? 1.0f : ex2(m - to);
+            l *= corr;
+            m = to;
+            if (!fresh) {
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tm_load(tl + S::kColO + x * D + d, o);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
+                tm_store(tl + S::kColO + x * D + d, w);
+              }
+            }
+          }
+          const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
+          const float2 sc = make_float2(f, f), mm = make_float2(-mu, -mu);
+          float2 ls = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int ch = 0; ch < kPmKeys; ch += 16) {
+            uint32_t w[S::kTermsP][8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 y = fma2(make_float2(s[ch + e], s[ch + e + 1]), sc, mm);
+              const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+              if constexpr (S::kF32) {
+                ls = add2(ls, pp);
+                uint32_t term[2];
+                split(pp.x, pp.y, term);
+                w[0][e / 2] = term[0];
+                w[1][e / 2] = term[1];
+              } else {
+                w[0][e / 2] = pack_rn(pp.x, pp.y);
+                ls = add2(ls, make_float2(low_f(w[0][e / 2]), high_f(w[0][e / 2])));
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < S::kTermsP; ++t) tm_store(tl + S::kColS + x * kPmKeys + t * (kPmKeys / 2) + ch / 2, w[t]);
+          }
+          l += ls.x + ls.y;
+        }
+        tm_st_wait();
+        tm_fence_before();
+        if (ok) bar_arrive_warp(pfull0 + 8 * x, lane);
+      }
+      if (cnt > 0) {  // the last products
+        ok = ok && bar_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
+        ++phase;
+      }
+      tm_fence_after();
+      // The row's sums: its own, or those of both groups, half of the dimensions each.
+      float M = m, L = l, f_own[2] = {1.0f, 1.0f}, f_sum[2];
+      bool use[2] = {cnt > 0, false}, more[2] = {summed, false};
+      f_sum[0] = summed ? ex2(sums_m - m) : 0.0f;
+      if (summed && sums_m == m) f_sum[0] = 1.0f;
+      // (A group without a tile leaves the place of its statistics alone: the other one's scores may still read the queries there.)
+      if (!kPair && cnt > 0) s_stat[x * 128 + ln] = make_float4(m, l, sums_m, summed ? 1.0f : 0.0f);
+      tm_fence_before();
+      meet();
+      tm_fence_after();
+      if constexpr (!kPair) {
+        const float4 t0 = s_stat[ln], t1 = n > 1 ? s_stat[128 + ln] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        M = fmaxf(t0.x, t1.x);
+        auto rel = [&](float r) { return r == M ? 1.0f : ex2(r - M); };
+        f_own[0] = rel(t0.x);
+        f_own[1] = rel(t1.x);
+        L = fmaf(t0.y, f_own[0], t1.y * f_own[1]);
+        f_sum[0] = rel(t0.z);
+        f_sum[1] = rel(t1.z);
+        use[0] = true;
+        use[1] = n > 1;
+        more[0] = t0.w != 0.0f;
+        more[1] = t1.w != 0.0f;
+      }
+      if (ok && !idle) {
+        const bool split_up = n < u.tiles;
+        const float f = split_up ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
+        const int64_t to = split_up ? ((int64_t)walk.slot(p.off, blockIdx.x) * S::kRows + ru) * D : ((int64_t)(u.t0 + tok) * a.Hq + h) * D;
+        const bool fix = s_bad;
+#pragma unroll 1
+        for (int d = kPair ? 0 : x * (D / 2); d < (kPair ? D : (x + 1) * (D / 2)); d += 16) {
+          __syncwarp();
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+#pragma unroll
+          for (int y = 0; y < (kPair ? 1 : 2); ++y) {
+            const int gr = kPair ? x : y;
+            float t[16];
+            if (use[y]) {
+              tm_load(tl + S::kColO + gr * D + d, t);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(t[e], f_own[y], o[e]);
+            }
+            if (more[y]) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(scratch[((int64_t)gr * D + d + e) * 128], f_sum[y], o[e]);
+            }
+          }
+          if (fix && live) {  // values that are not finite, for the rows that see them
+            for (int j = 0; j < n; ++j) {
+              const int key0 = key_first + j * kPmKeys;
+              if (!partial(key0)) continue;
+              for (int key = max(key0, lo); key < min(key0 + kPmKeys, pos + 1); ++key) {
+                const int id = a.table[(int64_t)u.s * a.width + (key >> a.shift)];
+                if ((unsigned)id >= (unsigned)a.n_pages) continue;
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                    a.v + ((int64_t)p.g * a.ts + ((int64_t)id << a.shift) + (key & (a.page - 1))) * D + d);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const uint32_t w = v[e / 2];
+                  if (!isfinite(low_f(w))) o[e] += low_f(w);
+                  if (!isfinite(high_f(w))) o[e + 1] += high_f(w);
+                }
+              }
+            }
+          }
+          if (live) {
+            if (split_up) store_row(a.part + to + d, o, 1.0f);
+            else store_row(static_cast<T*>(a.out) + to + d, o, f);
+          }
+        }
+        if (split_up && live && (kPair || x == 0)) a.ml[to / D] = make_float2(M, L);
+      }
+      tm_fence_before();
+      const bool split_up = n < u.tiles;
+      if (split_up) __threadfence();
+      meet();  // all has been read: tensor memory, the statistics, s_bad
+      if (split_up) {
+        const int c0 = pa_with(walk.sh.work, p.off, walk.sh.ctas), c1 = pa_with(walk.sh.work, p.off + u.tiles - 1, walk.sh.ctas);
+        if (i == 32 * kPmFirstSoftmax) {
+          s_last = 0;
+          if (*fail == 0) {
+            const unsigned before = atomicAdd(a.count + p.job, 1u);
+            s_last = before == (unsigned)(c1 - c0);
+            if (s_last) a.count[p.job] = 0;
+          }
+        }
+        meet();
+        if (s_last) {
+          __threadfence();
+          constexpr int kCols = D / 4;  // threads of a row, four dimensions each
+          for (int e = i - 32 * kPmFirstSoftmax; e < u.rows * kCols; e += 256) {
+            const int r = e / kCols, d = e % kCols * 4;
+            float mj = -INFINITY, lj = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int b0 = c0; b0 <= c1; b0 += 4) {
+              float4 y[4];
+              float2 ml[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const int64_t from = (int64_t)walk.slot(p.off, min(b0 + b, c1)) * S::kRows + r;
+                y[b] = __ldcg(reinterpret_cast<const float4*>(a.part + from * D + d));
+                ml[b] = __ldcg(a.ml + from);
+                if (b0 + b > c1) ml[b] = make_float2(-INFINITY, 0.0f);
+              }
+              const float to = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), mj);
+              const float corr = mj == to ? 1.0f : ex2(mj - to);
+              lj *= corr;
+              o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
+              mj = to;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                if (b0 + b > c1) break;
+                const float g = ml[b].x == mj ? 1.0f : ex2(ml[b].x - mj);
+                lj = fmaf(ml[b].y, g, lj);
+                o = make_float4(fmaf(y[b].x, g, o.x), fmaf(y[b].y, g, o.y), fmaf(y[b].z, g, o.z), fmaf(y[b].w, g, o.w));
+              }
+            }
+            const float g = lj == 0.0f ? 0.0f : 1.0f / lj;
+            const int rj = row0 + r, tj = rj / a.G;
+            T* out = static_cast<T*>(a.out) + ((int64_t)(u.t0 + tj) * a.Hq + p.g * a.G + rj - tj * a.G) * D + d;
+            if constexpr (S::kF32) *reinterpret_cast<float4*>(out) = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
+            else *reinterpret_cast<uint2*>(out) = make_uint2(pack_rn(o.x * g, o.y * g), pack_rn(o.z * g, o.w * g));
+          }
+        }
+      }
+      if (i == 32 * kPmFirstSoftmax) s_bad = 0;
+      meet();
+      k0 += 2 * n;
+      walk.next(a, p);
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == kPmMma) tm_free(tmem, kTaTmemCols);
+  if (*fail && i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
+}
+
+// ---- host -----------------------------------------------------------------------------------
+std::mutex g_pm_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_pm_encode = nullptr;
+
+nt_status pm_map(CUtensorMap* map, const uint16_t* base, int D, const PaArgs& a) {
+  {
+    std::lock_guard<std::mutex> lock(g_pm_mu);
+    if (!g_pm_encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      NT_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q));
+      if (q != cudaDriverEntryPointSuccess || !fn) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled not available");
+      g_pm_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.ts, (cuuint64_t)a.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.ts * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)std::min(a.page, kPmKeys), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_pm_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
+  return NT_OK;
+}
+
+template <typename T, int D, bool kPair, bool kExtra>
+nt_status launch_many(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
+  constexpr int smem = PmShape<T, D, kPair>::kSmem;
+  static std::atomic<int> allowed[64];
+  NT_TRY(allow_smem(paged_many_kernel<T, D, kPair, kExtra>, smem, allowed));
+  const int ctas = std::min(device_sm_count(), kPaManyCtas);
+  NT_CUDA_TRY(launch_kernel(paged_many_kernel<T, D, kPair, kExtra>, dim3((unsigned)ctas), dim3(kPmThreads), smem, st, true, maps, a));
+  return check_launch("paged_many_kernel");
+}
+template <typename T, int D, bool kPair>
+nt_status launch_many_extra(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
+  return a.cap > 0.0f || a.slopes ? launch_many<T, D, kPair, true>(maps, a, st) : launch_many<T, D, kPair, false>(maps, a, st);
+}
+
+}  // namespace
+
+nt_status launch_paged_many(const PaArgs& a, int dtype, int D, int64_t max_rows, cudaStream_t st) {
+  PmMaps maps;
+  NT_TRY(pm_map(&maps.k, a.k, D, a));
+  NT_TRY(pm_map(&maps.v, a.v, D, a));
+  if (dtype == NT_F32) return D == 64 ? launch_many_extra<float, 64, false>(maps, a, st) : launch_many_extra<float, 128, false>(maps, a, st);
+  if (max_rows <= 128)
+    return D == 64 ? launch_many_extra<uint16_t, 64, false>(maps, a, st) : launch_many_extra<uint16_t, 128, false>(maps, a, st);
+  return D == 64 ? launch_many_extra<uint16_t, 64, true>(maps, a, st) : launch_many_extra<uint16_t, 128, true>(maps, a, st);
+}
+
+}  // namespace nt
