@@ -67,8 +67,7 @@ struct PaUnit {
   int tile0, tiles;   // tiles of keys
 };
 template <int kKeys>
-__device__ __forceinline__ PaUnit pa_unit(const PaArgs& a, int s, int mt, int rows) {
-  const PaSeq q = pa_seq(a, s);
+__device__ __forceinline__ PaUnit pa_unit(const PaArgs& a, const PaSeq& q, int s, int mt, int rows) {
   PaUnit u;
   u.s = s;
   u.mt = mt;
@@ -118,8 +117,9 @@ struct PaShare {
 __device__ __forceinline__ int64_t pa_from(int64_t work, int c, int ctas) { return work * c / ctas; }
 __device__ __forceinline__ int pa_with(int64_t work, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / work); }
 
+// A unit's work for a head is its tiles and kStart, what beginning and ending a piece costs in tiles.
 // starts: S places of shared memory (scratch); all threads of the CTA, every one gets the share.
-template <int kThreads, int kKeys>
+template <int kThreads, int kKeys, int kStart>
 __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
   __shared__ int64_t s_warps[32];
   __shared__ int s_first[3];
@@ -146,7 +146,7 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
     }
     *s_out = s;
     *mt_out = (int)u - starts[s];
-    return (int64_t)pa_unit<kKeys>(a, s, *mt_out, rows).tiles * a.Hkv;
+    return (int64_t)(pa_unit<kKeys>(a, pa_seq(a, s), s, *mt_out, rows).tiles + kStart) * a.Hkv;
   };
   int s = 0, mt = 0;
   int64_t mine = 0, at = 0;
@@ -190,50 +190,61 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
   return r;
 }
 
-// A piece of a share: tiles [t0, t0 + n) of one unit and head.
+// A piece of a share: tiles [t0, t0 + n) of one unit and head. The kStart at the front of its work have no tile.
 struct PaPiece {
   PaUnit u;
   int g, t0, n;
-  int64_t off;     // work before the unit's first tile for this head
-  int64_t x;       // work before the piece
+  int c0, c1;      // CTAs with the unit's first and last tile for this head
+  int slot;        // where this CTA leaves its part
   int job;         // unit and head: the place of the counter
 };
-template <int kKeys>
+template <int kKeys, int kStart>
 struct PaWalk {
   PaShare sh;
   int rows;
-  int64_t x;
+  int g = 0;
+  PaSeq q;
   PaUnit u;
-  __device__ __forceinline__ PaWalk(const PaArgs& a, const PaShare& share, int rows_) : sh(share), rows(rows_), x(share.from) {
-    if (x < sh.end) u = pa_unit<kKeys>(a, sh.s, sh.mt, rows);
+  __device__ __forceinline__ PaWalk(const PaArgs& a, const PaShare& share, int rows_) : sh(share), rows(rows_) {
+    if (sh.from >= sh.end) return;
+    q = pa_seq(a, sh.s);
+    u = pa_unit<kKeys>(a, q, sh.s, sh.mt, rows);
+    g = (int)((sh.from - sh.off) / (u.tiles + kStart));
+    sh.off += (int64_t)g * (u.tiles + kStart);
   }
-  __device__ __forceinline__ bool more() const { return x < sh.end; }
+  // sh.off: the work before this unit and head. A share that ends among the first kStart has no tile of it.
+  __device__ __forceinline__ bool more() const { return sh.off + kStart < sh.end; }
   __device__ __forceinline__ PaPiece piece(const PaArgs& a) const {
     PaPiece p;
     p.u = u;
-    p.g = (int)((x - sh.off) / u.tiles);
-    p.off = sh.off + (int64_t)p.g * u.tiles;
-    p.t0 = (int)(x - p.off);
-    p.n = (int)min((int64_t)u.tiles - p.t0, sh.end - x);
-    p.x = x;
-    p.job = sh.unit * a.Hkv + p.g;
+    p.g = g;
+    const int64_t tile = sh.off + kStart;  // the first one
+    p.t0 = (int)max((int64_t)0, sh.from - tile);
+    p.n = (int)min((int64_t)u.tiles, sh.end - tile) - p.t0;
+    p.c0 = p.c1 = blockIdx.x;
+    p.slot = slot(blockIdx.x);
+    p.job = sh.unit * a.Hkv + g;
     return p;
   }
-  __device__ __forceinline__ void next(const PaArgs& a, const PaPiece& p) {
-    x += p.n;
-    if (x >= sh.end || x < sh.off + (int64_t)u.tiles * a.Hkv) return;
-    sh.off = x;
+  __device__ __forceinline__ void parts(PaPiece& p) const {  // of a piece that is not all of its unit
+    p.c0 = pa_with(sh.work, sh.off + kStart, sh.ctas);
+    p.c1 = pa_with(sh.work, sh.off + kStart + u.tiles - 1, sh.ctas);
+  }
+  // Where CTA c leaves its part of this unit and head: in its first place if its share begins among the unit's tiles.
+  __device__ __forceinline__ int slot(int c) const { return 2 * c + (pa_from(sh.work, c, sh.ctas) <= sh.off + kStart); }
+  __device__ __forceinline__ void next(const PaArgs& a) {
+    sh.off += u.tiles + kStart;
+    if (!more()) return;
+    if (++g < a.Hkv) return;
+    g = 0;
     ++sh.unit;
     ++sh.mt;
-    int n = u.n;
-    while (sh.mt >= pa_row_tiles(a, n, rows)) {  // there is one: work is left
+    while (sh.mt >= pa_row_tiles(a, q.n, rows)) {  // there is one: work is left
       sh.mt = 0;
-      n = pa_seq(a, ++sh.s).n;
+      q = pa_seq(a, ++sh.s);
     }
-    u = pa_unit<kKeys>(a, sh.s, sh.mt, rows);
+    u = pa_unit<kKeys>(a, q, sh.s, sh.mt, rows);
   }
-  // Where CTA c leaves its part of the unit and head whose work starts at `off`.
-  __device__ __forceinline__ int slot(int64_t off, int c) const { return 2 * c + (pa_from(sh.work, c, sh.ctas) < off); }
 };
 
 }  // namespace

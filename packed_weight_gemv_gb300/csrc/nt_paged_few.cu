@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kFewKeys = 64;  // keys per tile of the division
+constexpr int kFewStart = 1;
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p) {
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
   __shared__ int s_last;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31, dl = lane % kLanes, kg = lane / kLanes;
   dependent_launch_wait();
-  PaWalk<kFewKeys> walk(a, pa_share<kFewThreads, kFewKeys>(a, R, s_starts), R);
+  PaWalk<kFewKeys, kFewStart> walk(a, pa_share<kFewThreads, kFewKeys, kFewStart>(a, R, s_starts), R);
   // The scores that this lane ends with: row `row`, loads j0 .. j0 + kSums - 1; `own`: the lane counts them.
   int at = 0;
   bool own = true;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
   const int row = at / 8, j0 = at % 8;
   int bad = 0;
   for (; walk.more();) {
-    const PaPiece p = walk.piece(a);
+    PaPiece p = walk.piece(a);
     const PaUnit& u = p.u;
     auto token = [&](int r) { return (u.mt * R + min(r, u.rows - 1)) / a.G; };  // rows behind the last one repeat it
     auto head = [&](int r) { return p.g * a.G + (u.mt * R + min(r, u.rows - 1)) % a.G; };
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
     }
     __syncthreads();
     const bool split = p.n < u.tiles;
-    const int64_t slot = walk.slot(p.off, blockIdx.x);
+    const int64_t slot = p.slot;
     auto write = [&](int r, int c, float4 x, float L) {
       if (r >= u.rows) return;
       const float f = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
@@ -296,7 +297,8 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
       }
     }
     if (split) {
-      const int c0 = pa_with(walk.sh.work, p.off, walk.sh.ctas), c1 = pa_with(walk.sh.work, p.off + u.tiles - 1, walk.sh.ctas);
+      walk.parts(p);
+      const int c0 = p.c0, c1 = p.c1;
       __threadfence();
       __syncthreads();
       if (i == 0) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
             float2 ml[8];
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-              const int64_t from = (int64_t)walk.slot(p.off, min(b0 + b, c1)) * R + r;
+              const int64_t from = (int64_t)walk.slot(min(b0 + b, c1)) * R + r;
               y[b] = __ldcg(reinterpret_cast<const float4*>(a.part + from * D + c));
               ml[b] = __ldcg(a.ml + from);
               if (b0 + b > c1) ml[b] = make_float2(-INFINITY, 0.0f);
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kFewThreads, R <= 2 ? 2 : 1) paged_few_kernel(
         }
       }
     }
-    walk.next(a, p);
+    walk.next(a);
   }
   if (bad && a.n_bad) atomicAdd(a.n_bad, 1u);
 }

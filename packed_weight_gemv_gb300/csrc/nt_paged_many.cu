@@ -36,7 +36,10 @@ namespace {
 constexpr int kPmKeys = 128;
 constexpr int kPmLoad = 0, kPmMma = 1, kPmFirstSoftmax = 4;
 constexpr int kPmThreads = 32 * kPmFirstSoftmax + 256;
+constexpr int kPmStart = 4;
 constexpr int kPmSmem = 224 * 1024;
+// Registers of a thread: launched with 168; the first four warps give theirs to the softmax (128 x 88 + 256 x 208 = 384 x 168).
+constexpr int kPmRegsIssue = 88, kPmRegsSoftmax = 208;
 
 struct PmMaps {
   CUtensorMap k, v;  // boxes of 64 dimensions x a page (at most 128 rows)
@@ -72,6 +75,54 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&o)[16], flo
                                                   pack_rn(o[e + 4] * f, o[e + 5] * f), pack_rn(o[e + 6] * f, o[e + 7] * f));
 }
 
+// bar_wait in one piece: a call would fix the registers that setmaxnreg moves.
+__device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
+  if (bar_try(bar, parity)) return true;
+  uint64_t deadline = 0;
+#pragma unroll 1
+  for (uint32_t it = 1; !bar_try(bar, parity); ++it) {
+    if ((it & 255u) != 0u) continue;
+    const uint64_t now = globaltimer_ns();
+    if (deadline == 0) deadline = now + timeout_ns;
+    if (*fail || now > deadline) {
+      *fail = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool pm_wait_warp(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, pm_wait(bar, parity, fail, timeout_ns));
+}
+
+// 128 columns of this lane: four loads under way together, and the wait.
+__device__ __forceinline__ void tm_ld128(uint32_t addr, float (&r)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]),
+        "=f"(r[32]), "=f"(r[33]), "=f"(r[34]), "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]),
+        "=f"(r[40]), "=f"(r[41]), "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]),
+        "=f"(r[48]), "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]),
+        "=f"(r[56]), "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]), "=f"(r[63]),
+        "=f"(r[64]), "=f"(r[65]), "=f"(r[66]), "=f"(r[67]), "=f"(r[68]), "=f"(r[69]), "=f"(r[70]), "=f"(r[71]),
+        "=f"(r[72]), "=f"(r[73]), "=f"(r[74]), "=f"(r[75]), "=f"(r[76]), "=f"(r[77]), "=f"(r[78]), "=f"(r[79]),
+        "=f"(r[80]), "=f"(r[81]), "=f"(r[82]), "=f"(r[83]), "=f"(r[84]), "=f"(r[85]), "=f"(r[86]), "=f"(r[87]),
+        "=f"(r[88]), "=f"(r[89]), "=f"(r[90]), "=f"(r[91]), "=f"(r[92]), "=f"(r[93]), "=f"(r[94]), "=f"(r[95]),
+        "=f"(r[96]), "=f"(r[97]), "=f"(r[98]), "=f"(r[99]), "=f"(r[100]), "=f"(r[101]), "=f"(r[102]), "=f"(r[103]),
+        "=f"(r[104]), "=f"(r[105]), "=f"(r[106]), "=f"(r[107]), "=f"(r[108]), "=f"(r[109]), "=f"(r[110]), "=f"(r[111]),
+        "=f"(r[112]), "=f"(r[113]), "=f"(r[114]), "=f"(r[115]), "=f"(r[116]), "=f"(r[117]), "=f"(r[118]), "=f"(r[119]),
+        "=f"(r[120]), "=f"(r[121]), "=f"(r[122]), "=f"(r[123]), "=f"(r[124]), "=f"(r[125]), "=f"(r[126]), "=f"(r[127])
+      : "r"(addr), "r"(addr + 32), "r"(addr + 64), "r"(addr + 96)
+      : "memory");
+}
+
 template <typename T, int D, bool kPair, bool kExtra>
 __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_constant__ PmMaps maps, const __grid_constant__ PaArgs a) {
   using S = PmShape<T, D, kPair>;
@@ -98,27 +149,30 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
   tm_fence_after();
   const uint32_t tmem = tmem_slot;
   dependent_launch_wait();
-  PaWalk<kPmKeys> walk(a, pa_share<kPmThreads, kPmKeys>(a, S::kRows, reinterpret_cast<int*>(ring)), S::kRows);
+  PaWalk<kPmKeys, kPmStart> walk(a, pa_share<kPmThreads, kPmKeys, kPmStart>(a, S::kRows, reinterpret_cast<int*>(ring)), S::kRows);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before copies over the division's scratch
   __syncthreads();
   auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
   auto empty = [&](int k) { return empty0 + 8 * (k % S::kStages); };
   auto turn = [&](int k) { return (uint32_t)(k / S::kStages) & 1u; };
   auto slot = [&](int k) { return smem_u32(ring) + (k % S::kStages) * S::kSlot; };
-  auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, fail, a.timeout_ns); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return pm_wait(bar, parity, fail, a.timeout_ns); };
   // Ring order of a piece of n tiles: the keys of the first kAhead, then values j and keys j + kAhead in turn.
   auto ring_val = [&](int j, int n) { return min(S::kAhead, n) + j + min(j, max(n - S::kAhead, 0)); };
   auto ring_key = [&](int j) { return j < S::kAhead ? j : 2 * j - S::kAhead + 1; };
   int k0 = 0;  // tiles of the pieces before
 
+  // (in every branch: code behind a join of the two would be held to the smaller number)
+  auto give = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPmRegsIssue)); };
   if (warp == kPmLoad) {
+    give();
     const int per = min(a.page, kPmKeys), boxes = kPmKeys / per;  // rows of a box; boxes of 64 dimensions of a tile
     const int box = lane % boxes, half = lane / boxes;
     const bool mine = half < D / 64;
     bool ok = true;
     int bad = 0, issued = 0;
     for (; walk.more() && ok;) {
-      const PaPiece p = walk.piece(a);
+      PaPiece p = walk.piece(a);
       const int hi = p.u.p1 + 1;  // no row sees this key
       const int32_t* ids = a.table + (int64_t)p.u.s * a.width;
       auto row_of = [&](int j) {  // the cache row of this lane's box of tile j; behind the pool (zeros) where nothing is seen
@@ -135,7 +189,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j <= S::kAhead; ++j) row[j] = row_of(j);
       auto load = [&](int k, const CUtensorMap* map, int y) {
-        if (k >= S::kStages && !bar_wait_warp(empty(k), turn(k) ^ 1u, fail, a.timeout_ns)) return false;
+        if (k >= S::kStages && !pm_wait_warp(empty(k), turn(k) ^ 1u, fail, a.timeout_ns)) return false;
         if (lane == 0) bar_expect_tx(full(k), S::kSlot);
         __syncwarp();
         if (mine) tma_3d(slot(k) + half * (kPmKeys * 128) + box * per * 128, map, half * 64, y, p.g, full(k));
@@ -155,7 +209,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         row[S::kAhead] = next;
       }
       k0 += 2 * p.n;
-      walk.next(a, p);
+      walk.next(a);
     }
     if (!ok) {  // every copy must land before the CTA may exit
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
@@ -166,11 +220,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0 && bad && a.n_bad) atomicAdd(a.n_bad, 1u);
   } else if (warp == kPmMma) {
+    give();
     if (elect_one()) {
       bool ok = true;
       int piece = 0, steps[2] = {0, 0};  // steps of the groups so far
       for (; walk.more() && ok; ++piece) {
-        const PaPiece p = walk.piece(a);
+        PaPiece p = walk.piece(a);
         const int n = p.n;
         auto scores = [&](int x, int k) {
           const uint32_t d = tmem + S::kColS + x * kPmKeys;
@@ -239,7 +294,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           ++c[x];
         }
         k0 += 2 * n;
-        walk.next(a, p);
+        walk.next(a);
       }
       if (!ok) {
         mma_commit(drain);
@@ -249,45 +304,55 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (warp >= kPmFirstSoftmax) {
+  } else if (warp < kPmFirstSoftmax) {
+    give();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPmRegsSoftmax));
     const int quarter = warp & 3, x = (warp - kPmFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // group; tensor-memory lane
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     float* scratch = a.scratch + ((int64_t)blockIdx.x * 2) * D * 128 + ln;  // [2][D][128]
+    const float inv_g = 1.0f / (float)a.G;
     float4* s_stat = reinterpret_cast<float4*>(q_smem);  // [2][128], when the queries have been read
     bool ok = true;
     uint32_t phase = 0;  // of sfull
     auto meet = [&] { asm volatile("bar.sync 9, 256;" ::: "memory"); };
     for (; walk.more();) {
-      const PaPiece p = walk.piece(a);
+      PaPiece p = walk.piece(a);
       const PaUnit& u = p.u;
       const int n = p.n;
-      const int row0 = u.mt * S::kRows;
+      // Row r of the tile is token tok0 + token_of(r), head head0 + r - G token_of(r).
+      const int row0 = u.mt * S::kRows, first = row0 / a.G, rest = row0 - first * a.G;
+      const int tok0 = u.t0 + first, head0 = p.g * a.G + rest;
+      auto token_of = [&](int r) { return node_of(rest + r, inv_g); };
       {  // the queries' terms into shared memory, rows of 64 dimensions with the 128-byte swizzle
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kMine = kPair ? 32 : 16;
-        const int c = lane % kLanes;
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kMine = kPair ? 32 : 16, kLoads = kMine / kAt, kVecs = S::kF32 ? 2 : 1;
+        const int c = lane % kLanes, r0 = quarter * 32 + (kPair ? 0 : x * 16) + lane / kLanes;
+        uint4 f[kLoads][kVecs];  // all asked for at once
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int ru = (kPair ? x * 128 : 0) + r0 + e * kAt, away = token_of(ru);
+          const T* q = static_cast<const T*>(a.q) + (int64_t)(tok0 + away) * a.q_stride + (int64_t)(head0 + ru - away * a.G) * D + c * 8;
+#pragma unroll
+          for (int y = 0; y < kVecs; ++y) f[e][y] = ru < u.rows ? reinterpret_cast<const uint4*>(q)[y] : make_uint4(0u, 0u, 0u, 0u);
+        }
         uint8_t* to = q_smem + (kPair ? x * S::kTermsQ * S::kQTile : 0) + (c >> 3) * (128 * 128);
-#pragma unroll 4
-        for (int e = 0; e < kMine; e += kAt) {
-          const int r = quarter * 32 + (kPair ? 0 : x * 16) + e + lane / kLanes;  // row of the tile
-          const int ru = (kPair ? x * 128 : 0) + r, ra = row0 + ru, tok = ra / a.G;
-          const bool live = ru < u.rows;
-          const T* q = static_cast<const T*>(a.q) + (int64_t)(u.t0 + tok) * a.q_stride + (int64_t)(p.g * a.G + ra - tok * a.G) * D + c * 8;
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int r = r0 + e * kAt;
           uint4 w[S::kTermsQ];
           if constexpr (S::kF32) {
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            const uint4 f0 = live ? reinterpret_cast<const uint4*>(q)[0] : z, f1 = live ? reinterpret_cast<const uint4*>(q)[1] : z;
             uint32_t t0[3], t1[3], t2[3], t3[3];
-            split(__uint_as_float(f0.x), __uint_as_float(f0.y), t0);
-            split(__uint_as_float(f0.z), __uint_as_float(f0.w), t1);
-            split(__uint_as_float(f1.x), __uint_as_float(f1.y), t2);
-            split(__uint_as_float(f1.z), __uint_as_float(f1.w), t3);
+            split(__uint_as_float(f[e][0].x), __uint_as_float(f[e][0].y), t0);
+            split(__uint_as_float(f[e][0].z), __uint_as_float(f[e][0].w), t1);
+            split(__uint_as_float(f[e][1].x), __uint_as_float(f[e][1].y), t2);
+            split(__uint_as_float(f[e][1].z), __uint_as_float(f[e][1].w), t3);
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
               const uint32_t sign = t == 1 ? 0x80008000u : 0u;
               w[t] = make_uint4(t0[t] ^ sign, t1[t] ^ sign, t2[t] ^ sign, t3[t] ^ sign);
             }
           } else {
-            w[0] = live ? *reinterpret_cast<const uint4*>(q) : make_uint4(0u, 0u, 0u, 0u);
+            w[0] = f[e][0];
           }
 #pragma unroll
           for (int t = 0; t < S::kTermsQ; ++t) *reinterpret_cast<uint4*>(to + t * S::kQTile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[t];
@@ -297,8 +362,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       }
       const int ru = (kPair ? x * 128 : 0) + ln;           // row of the unit
       const bool live = ru < u.rows, idle = ru - lane >= u.rows;  // warps of rows past the last one only keep the barriers going
-      const int ra = row0 + min(ru, u.rows - 1), tok = ra / a.G, h = p.g * a.G + ra - tok * a.G;
-      const int pos = u.len - u.n + tok;
+      const int rl = min(ru, u.rows - 1), tok = token_of(rl), h = head0 + rl - tok * a.G;
+      const int pos = u.len - u.n + first + tok;
       const int lo = (int)max((int64_t)0, (int64_t)pos - a.window + 1);
       const int sure_lo = (int)max((int64_t)0, (int64_t)u.p1 - a.window + 1);  // every row sees from here to u.p0
       const float slope = kExtra && a.slopes ? a.slopes[h] : 0.0f;
@@ -309,12 +374,12 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       bool summed = false;
       for (int c = 0; c < cnt; ++c) {
         const int j = kPair ? c : 2 * c + x, key0 = key_first + j * kPmKeys;
-        ok = ok && bar_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
+        ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
         ++phase;
         tm_fence_after();
         float s[kPmKeys];
         if (ok && !idle) {
-          tm_load(tl + S::kColS + x * kPmKeys, s);
+          tm_ld128(tl + S::kColS + x * kPmKeys, s);
         } else {
 #pragma unroll
           for (int e = 0; e < kPmKeys; ++e) s[e] = 0.0f;
@@ -322,19 +387,23 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         const bool part = partial(key0);
         if (part) {  // values that are not finite are taken out: some row may not see them
           const int k = k0 + ring_val(j, n);
-          ok = ok && bar_wait_warp(full(k), turn(k), fail, a.timeout_ns);
+          ok = ok && pm_wait_warp(full(k), turn(k), fail, a.timeout_ns);
+          uint4* at = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + ln;
           bool bad = false;
-          for (int e = ln; ok && e < S::kSlot / 16; e += 128) {
-            uint4* at = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + e;
-            const uint4 v = *at;
-            if (word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w)) {
-              uint16_t* w = reinterpret_cast<uint16_t*>(at);
+#pragma unroll
+          for (int e = 0; e < S::kSlot / 16; e += 128) {
+            const uint4 v = at[e];
+            bad |= word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w);
+          }
+          if (bad && ok) {
+#pragma unroll 1
+            for (int e = 0; e < S::kSlot / 16; e += 128) {
+              uint16_t* w = reinterpret_cast<uint16_t*>(at + e);
               for (int y = 0; y < 8; ++y)
                 if ((w[y] & 0x7f80u) == 0x7f80u) w[y] = 0;
-              bad = true;
             }
+            s_bad = 1;
           }
-          if (bad) s_bad = 1;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
@@ -435,7 +504,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         if (ok) bar_arrive_warp(pfull0 + 8 * x, lane);
       }
       if (cnt > 0) {  // the last products
-        ok = ok && bar_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
+        ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
         ++phase;
       }
       tm_fence_after();
@@ -466,7 +535,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       if (ok && !idle) {
         const bool split_up = n < u.tiles;
         const float f = split_up ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
-        const int64_t to = split_up ? ((int64_t)walk.slot(p.off, blockIdx.x) * S::kRows + ru) * D : ((int64_t)(u.t0 + tok) * a.Hq + h) * D;
+        const int64_t to = split_up ? ((int64_t)p.slot * S::kRows + ru) * D : ((int64_t)(tok0 + tok) * a.Hq + h) * D;
         const bool fix = s_bad;
 #pragma unroll 1
         for (int d = kPair ? 0 : x * (D / 2); d < (kPair ? D : (x + 1) * (D / 2)); d += 16) {
@@ -518,7 +587,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       if (split_up) __threadfence();
       meet();  // all has been read: tensor memory, the statistics, s_bad
       if (split_up) {
-        const int c0 = pa_with(walk.sh.work, p.off, walk.sh.ctas), c1 = pa_with(walk.sh.work, p.off + u.tiles - 1, walk.sh.ctas);
+        walk.parts(p);
+        const int c0 = p.c0, c1 = p.c1;
         if (i == 32 * kPmFirstSoftmax) {
           s_last = 0;
           if (*fail == 0) {
@@ -540,7 +610,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
               float2 ml[4];
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
-                const int64_t from = (int64_t)walk.slot(p.off, min(b0 + b, c1)) * S::kRows + r;
+                const int64_t from = (int64_t)walk.slot(min(b0 + b, c1)) * S::kRows + r;
                 y[b] = __ldcg(reinterpret_cast<const float4*>(a.part + from * D + d));
                 ml[b] = __ldcg(a.ml + from);
                 if (b0 + b > c1) ml[b] = make_float2(-INFINITY, 0.0f);
@@ -559,8 +629,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
               }
             }
             const float g = lj == 0.0f ? 0.0f : 1.0f / lj;
-            const int rj = row0 + r, tj = rj / a.G;
-            T* out = static_cast<T*>(a.out) + ((int64_t)(u.t0 + tj) * a.Hq + p.g * a.G + rj - tj * a.G) * D + d;
+            const int tj = token_of(r);
+            T* out = static_cast<T*>(a.out) + ((int64_t)(tok0 + tj) * a.Hq + head0 + r - tj * a.G) * D + d;
             if constexpr (S::kF32) *reinterpret_cast<float4*>(out) = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
             else *reinterpret_cast<uint2*>(out) = make_uint2(pack_rn(o.x * g, o.y * g), pack_rn(o.z * g, o.w * g));
           }
@@ -569,7 +639,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       if (i == 32 * kPmFirstSoftmax) s_bad = 0;
       meet();
       k0 += 2 * n;
-      walk.next(a, p);
+      walk.next(a);
     }
   }
   tm_fence_before();
