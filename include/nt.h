@@ -547,7 +547,7 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes (16-byte aligned, zero-filled before its first use, its counters
  *     left zero; calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
  * fp32 queries: products are exact, scores, weights and sums are fp32 (on the tensor cores weights are two bf16 terms, within 2^-17 of
- * them). bf16 queries: on the tensor cores each weight is rounded to bf16, for the sums of the weights too. Either way sums lose at
+ * them). bf16 queries: on the tensor cores each weight is rounded to bf16 before it meets its value. Either way sums lose at
  * most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the output is rounded. */
 nt_status nt_paged_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, size_t* bytes);
 nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const uint16_t* k_pool, const uint16_t* v_pool, int T, int S,

@@ -19,6 +19,10 @@ constexpr uint64_t kPaTimeoutNs = 2000000000ull;
 
 enum : int { kPaAll = 0, kPaFew = 1, kPaMany = 2 };  // which sequences a launch takes: any; up to kPaFewRows rows; more
 
+// A unit that several CTAs of the tensor-core kernel share, left by the one with its first tile: row r is token tok0 + (rest + r) / G.
+struct PaJoin {
+  int tok0, head0, rest, rows, last;  // last: the CTA with its last tile; rows 0: nothing to join
+};
 struct PaArgs {
   const void* q;            // [T][Hq][D], tokens q_stride elements apart
   void* out;                // [T][Hq][D]
@@ -30,6 +34,7 @@ struct PaArgs {
   unsigned int* count;      // [units x heads] parts that have arrived, all 0 between calls
   float* part;              // [2 x CTAs][rows][D] weighted sums
   float2* ml;               // [2 x CTAs][rows] (maximum, sum of weights)
+  PaJoin* join;             // [CTAs]
   float* scratch;           // [CTAs][2][D][128] sums taken off the tensor cores
   uint64_t timeout_ns;
   int64_t q_stride;

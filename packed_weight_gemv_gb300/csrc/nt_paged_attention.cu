@@ -19,8 +19,9 @@ size_t scratch_floats(int T, int Hq, int Hkv, int D) {
   return (int64_t)T * (Hq / Hkv) <= kPaFewRows ? 0 : (size_t)kPaManyCtas * 2 * 128 * D;
 }
 size_t paged_counts(int T, int S, int Hq, int Hkv) { return ((size_t)T * Hq + (size_t)S * Hkv + 63) / 64 * 64; }
+constexpr size_t kJoinBytes = (kPaManyCtas * sizeof(PaJoin) + 255) / 256 * 256;
 size_t paged_ws_bytes(int T, int S, int Hq, int Hkv, int D) {
-  return kWsHeaderBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + (part_rows(T, Hq, Hkv) * (D + 2) + scratch_floats(T, Hq, Hkv, D)) * sizeof(float);
+  return kWsHeaderBytes + kJoinBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + (part_rows(T, Hq, Hkv) * (D + 2) + scratch_floats(T, Hq, Hkv, D)) * sizeof(float);
 }
 nt_status check_paged(int T, int S, int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
@@ -80,7 +81,8 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   a.n_bad = n_bad_opt;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<unsigned int*>(w);
-  a.count = reinterpret_cast<unsigned int*>(w + kWsHeaderBytes);
+  a.join = reinterpret_cast<PaJoin*>(w + kWsHeaderBytes);
+  a.count = reinterpret_cast<unsigned int*>(w + kWsHeaderBytes + kJoinBytes);
   a.part = reinterpret_cast<float*>(a.count + paged_counts(T, S, Hq, Hkv));
   a.scratch = a.part + part_rows(T, Hq, Hkv) * D;
   a.ml = reinterpret_cast<float2*>(a.scratch + scratch_floats(T, Hq, Hkv, D));

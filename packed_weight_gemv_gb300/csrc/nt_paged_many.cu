@@ -9,13 +9,14 @@
 // the same rows and every other tile of keys, with sums of their own that are joined at the end (fp32 queries, whose three bf16 terms
 // take the shared memory of three tiles; and up to 128 rows).
 //
-// CTA (384 threads): warp 0 asks for the pages (TMA boxes of one page each, 128-byte swizzle) into a ring of tiles; one lane of
+// CTA (384 threads): warps 0 and 2 ask for the pages of keys and values (TMA boxes of one page each, 128-byte swizzle) into a ring of tiles; one lane of
 // warp 1 issues all MMAs, in the order S(1st), S(2nd), { O, next S } of the groups in turn, so the tensor pipe has one group's products
 // while the other group's weights are formed, and a commit behind an S also tells that the O before it is done; warps 4-7 and 8-11 are
 // the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
 //
 // fp32 queries enter as three bf16 terms without loss and their weights as two rounded ones (2^-17); bf16 queries' weights are rounded to
-// bf16, and the sum of the weights is that of the rounded ones, so a row that one key decides is exact. The tensor core
+// bf16 (2^-8, next to the output's own 2^-8; the sum of the weights is that of the unrounded ones: taking the rounded ones' cost two half-rate
+// instructions a pair). The tensor core
 // cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
 // that round to nearest.
 #include <cudaTypedefs.h>
@@ -34,11 +35,13 @@ namespace nt {
 namespace {
 
 constexpr int kPmKeys = 128;
-constexpr int kPmLoad = 0, kPmMma = 1, kPmFirstSoftmax = 4;
-constexpr int kPmThreads = 32 * kPmFirstSoftmax + 256;
+constexpr int kPmKeyLoad = 0, kPmMma = 1, kPmValueLoad = 2, kPmFirstSoftmax = 4;
+constexpr int kPmSoftmax = 256;  // two groups of 128 threads
+constexpr int kPmThreads = 32 * kPmFirstSoftmax + kPmSoftmax;
 constexpr int kPmStart = 4;
+constexpr float kPmLazy = 32.0f;  // a reference is raised once a score exceeds it by 2^32: weights that large lose nothing in fp32 or bf16
 constexpr int kPmSmem = 224 * 1024;
-// Registers of a thread: launched with 168; the first four warps give theirs to the softmax (128 x 88 + 256 x 208 = 384 x 168).
+// Registers of a thread: launched with 168; the first four warps give some of theirs to the softmax (128 x 88 + 256 x 208 = 384 x 168).
 constexpr int kPmRegsIssue = 88, kPmRegsSoftmax = 208;
 
 struct PmMaps {
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
   constexpr int kBars = 2 * S::kStages + 6;
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_fail, s_bad, s_last;
+  __shared__ int s_fail, s_bad;
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages, sfull0 = empty0 + 8 * S::kStages, pfull0 = sfull0 + 16,
@@ -164,61 +167,59 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
 
   // (in every branch: code behind a join of the two would be held to the smaller number)
   auto give = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPmRegsIssue)); };
-  if (warp == kPmLoad) {
+  if (warp == kPmKeyLoad || warp == kPmValueLoad) {
     give();
+    const bool val = warp == kPmValueLoad;
+    const CUtensorMap* map = val ? &maps.v : &maps.k;
     const int per = min(a.page, kPmKeys), boxes = kPmKeys / per;  // rows of a box; boxes of 64 dimensions of a tile
     const int box = lane % boxes, half = lane / boxes;
     const bool mine = half < D / 64;
-    bool ok = true;
-    int bad = 0, issued = 0;
-    for (; walk.more() && ok;) {
-      PaPiece p = walk.piece(a);
+    bool ok = a.fault == 0;
+    int bad = 0, issued = -1;
+    for (; walk.more() && ok; walk.next(a)) {
+      const PaPiece p = walk.piece(a);
       const int hi = p.u.p1 + 1;  // no row sees this key
       const int32_t* ids = a.table + (int64_t)p.u.s * a.width;
-      auto row_of = [&](int j) {  // the cache row of this lane's box of tile j; behind the pool (zeros) where nothing is seen
-        const int key = (p.u.tile0 + p.t0 + j) * kPmKeys + box * per;
-        if (j >= p.n || key >= hi) return a.ts;
-        const int id = ids[key >> a.shift];
-        if ((unsigned)id >= (unsigned)a.n_pages) {
-          bad = 1;
-          return a.ts;
-        }
-        return (id << a.shift) + (key & (a.page - 1));
+      const int first = (p.u.tile0 + p.t0) * kPmKeys + box * per;
+      // The page of this lane's box of tile j. Asked for three tiles before it is looked at: the loads would otherwise wait for it, a
+      // round trip to L2 for every tile.
+      auto ask = [&](int j) {
+        const int key = first + j * kPmKeys;
+        return j < p.n && key < hi ? ids[key >> a.shift] : -1;
       };
-      int row[S::kAhead + 1];  // of the tiles whose values are to come
+      constexpr int kAsk = 3;
+      int id[kAsk];
 #pragma unroll
-      for (int j = 0; j <= S::kAhead; ++j) row[j] = row_of(j);
-      auto load = [&](int k, const CUtensorMap* map, int y) {
-        if (k >= S::kStages && !pm_wait_warp(empty(k), turn(k) ^ 1u, fail, a.timeout_ns)) return false;
+      for (int j = 0; j < kAsk; ++j) id[j] = ask(j);
+      for (int j = 0; ok && j < p.n; ++j) {
+        const int key = first + j * kPmKeys, page = id[0];
+        int y = a.ts;  // behind the pool (zeros) where nothing is seen, or nothing is there
+        if (key < hi) {
+          if ((unsigned)page < (unsigned)a.n_pages) y = (page << a.shift) + (key & (a.page - 1));
+          else bad = 1;
+        }
+#pragma unroll
+        for (int e = 0; e + 1 < kAsk; ++e) id[e] = id[e + 1];
+        id[kAsk - 1] = ask(j + kAsk);
+        const int k = k0 + (val ? ring_val(j, p.n) : ring_key(j));
+        if (k >= S::kStages) ok = pm_wait_warp(empty(k), turn(k) ^ 1u, fail, a.timeout_ns);
+        if (!ok) break;
         if (lane == 0) bar_expect_tx(full(k), S::kSlot);
         __syncwarp();
         if (mine) tma_3d(slot(k) + half * (kPmKeys * 128) + box * per * 128, map, half * 64, y, p.g, full(k));
-        issued = k + 1;
-        return true;
-      };
-      if (a.fault) ok = false;
-#pragma unroll
-      for (int j = 0; j < S::kAhead; ++j)
-        if (j < p.n) ok = ok && load(k0 + j, &maps.k, row[j]);
-      for (int j = 0; ok && j < p.n; ++j) {
-        const int next = row_of(j + S::kAhead + 1);
-        ok = load(k0 + ring_val(j, p.n), &maps.v, row[0]);
-        if (ok && j + S::kAhead < p.n) ok = load(k0 + ring_key(j + S::kAhead), &maps.k, row[S::kAhead]);
-#pragma unroll
-        for (int e = 0; e < S::kAhead; ++e) row[e] = row[e + 1];
-        row[S::kAhead] = next;
+        issued = k;
       }
       k0 += 2 * p.n;
-      walk.next(a);
     }
     if (!ok) {  // every copy must land before the CTA may exit
       const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-      for (int k = max(0, issued - S::kStages); k < issued; ++k)
+      // (the places of the last kStages that this warp has filled are among these; a wait for the other warp's ends as well)
+      for (int k = max(0, issued - S::kStages + 1); k <= issued; ++k)
         while (!bar_try(full(k), turn(k)))
           if (globaltimer_ns() > deadline) break;
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0 && bad && a.n_bad) atomicAdd(a.n_bad, 1u);
+    if (lane == 0 && bad && !val && a.n_bad) atomicAdd(a.n_bad, 1u);
   } else if (warp == kPmMma) {
     give();
     if (elect_one()) {
@@ -279,16 +280,14 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
             for (int kk = 0; kk < kPmKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
               mma_tmem_a(tmem + S::kColO + x * D, tmem + S::kColS + x * kPmKeys + t * (kPmKeys / 2) + 8 * kk, bd + kk * 2048 / 16,
                          idesc_bf16(D, true, t == 1), t < S::kTermsP - 1 || kk > 0 || !fresh);
+          if (last) mma_commit(empty(kv));
           if (next < n) {
             if (first) ok = wait(full(kk0), turn(kk0));
             if (!ok) break;
             tm_fence_after();
             scores(x, kk0);
           }
-          if (last) {
-            mma_commit(empty(kv));
-            if (next < n) mma_commit(empty(kk0));
-          }
+          if (last && next < n) mma_commit(empty(kk0));
           mma_commit(sfull0 + 8 * x);  // the last word of a piece: nothing is under way behind it
           ++steps[x];
           ++c[x];
@@ -308,16 +307,17 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
     give();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPmRegsSoftmax));
-    const int quarter = warp & 3, x = (warp - kPmFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // group; tensor-memory lane
+    const int quarter = warp & 3, x = (warp - kPmFirstSoftmax) >> 2, ln = quarter * 32 + lane;  // group, tensor-memory lane
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     float* scratch = a.scratch + ((int64_t)blockIdx.x * 2) * D * 128 + ln;  // [2][D][128]
-    const float inv_g = 1.0f / (float)a.G;
     float4* s_stat = reinterpret_cast<float4*>(q_smem);  // [2][128], when the queries have been read
-    bool ok = true;
+    const float inv_g = 1.0f / (float)a.G;
+    constexpr int kChunk = 16;  // keys whose weights are formed together
+    bool ok = true, left_part = false;
     uint32_t phase = 0;  // of sfull
-    auto meet = [&] { asm volatile("bar.sync 9, 256;" ::: "memory"); };
-    for (; walk.more();) {
-      PaPiece p = walk.piece(a);
+    auto meet = [&] { asm volatile("bar.sync 9, %0;" ::"n"(kPmSoftmax) : "memory"); };
+    for (; walk.more(); walk.next(a)) {
+      const PaPiece p = walk.piece(a);
       const PaUnit& u = p.u;
       const int n = p.n;
       // Row r of the tile is token tok0 + token_of(r), head head0 + r - G token_of(r).
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       const int tok0 = u.t0 + first, head0 = p.g * a.G + rest;
       auto token_of = [&](int r) { return node_of(rest + r, inv_g); };
       {  // the queries' terms into shared memory, rows of 64 dimensions with the 128-byte swizzle
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kMine = kPair ? 32 : 16, kLoads = kMine / kAt, kVecs = S::kF32 ? 2 : 1;
-        const int c = lane % kLanes, r0 = quarter * 32 + (kPair ? 0 : x * 16) + lane / kLanes;
+        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kRowsMine = kPair ? 32 : 16, kLoads = kRowsMine / kAt, kVecs = S::kF32 ? 2 : 1;
+        const int c = lane % kLanes, r0 = quarter * 32 + (kPair ? 0 : x * kRowsMine) + lane / kLanes;
         uint4 f[kLoads][kVecs];  // all asked for at once
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
@@ -370,27 +370,47 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       const int cnt = kPair ? n : (n + 1 - x) / 2;
       const int key_first = (u.tile0 + p.t0) * kPmKeys;
       auto partial = [&](int key) { return key + kPmKeys - 1 > u.p0 || key < sure_lo; };
+      const uint32_t scol = tl + S::kColS + x * kPmKeys, ocol = tl + S::kColO + x * D;
       float m = -INFINITY, l = 0.0f, sums_m = -INFINITY;
       bool summed = false;
       for (int c = 0; c < cnt; ++c) {
         const int j = kPair ? c : 2 * c + x, key0 = key_first + j * kPmKeys;
+        const bool fresh = c % S::kFlush == 0;
+        if (fresh && c > 0) {  // O to the sums, which are in units of a reference of their own and asked for before the wait
+          float* to = scratch + (int64_t)x * D * 128;
+          float old[D];
+          if (summed) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) old[d] = to[d * 128];
+          } else {
+#pragma unroll
+            for (int d = 0; d < D; ++d) old[d] = 0.0f;
+          }
+          ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
+          tm_fence_after();
+          if (ok && !idle) {
+            const float scale = sums_m == m ? 1.0f : ex2(sums_m - m);
+#pragma unroll
+            for (int d = 0; d < D; d += 16) {
+              float o[16];
+              tm_load(ocol + d, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) to[(d + e) * 128] = summed ? fmaf(old[d + e], scale, o[e]) : o[e];
+            }
+            sums_m = m;
+            summed = true;
+          }
+        }
         ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
         ++phase;
         tm_fence_after();
-        float s[kPmKeys];
-        if (ok && !idle) {
-          tm_ld128(tl + S::kColS + x * kPmKeys, s);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kPmKeys; ++e) s[e] = 0.0f;
-        }
         const bool part = partial(key0);
         if (part) {  // values that are not finite are taken out: some row may not see them
           const int k = k0 + ring_val(j, n);
           ok = ok && pm_wait_warp(full(k), turn(k), fail, a.timeout_ns);
           uint4* at = reinterpret_cast<uint4*>(ring + (k % S::kStages) * S::kSlot) + ln;
           bool bad = false;
-#pragma unroll
+#pragma unroll 4
           for (int e = 0; e < S::kSlot / 16; e += 128) {
             const uint4 v = at[e];
             bad |= word_bad(v.x) || word_bad(v.y) || word_bad(v.z) || word_bad(v.w);
@@ -406,6 +426,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
+        }
+        float s[kPmKeys];
+        if (ok && !idle) {
+          tm_ld128(scol, s);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPmKeys; ++e) s[e] = 0.0f;
         }
         if constexpr (kExtra) {
           if (a.cap > 0.0f) {
@@ -430,72 +457,49 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
             if (e > to || e < from) s[e] = -INFINITY;
         }
         const float f = kExtra ? 1.4426950408889634f : a.scale * 1.4426950408889634f;
-        float mx2[4] = {s[0], s[1], s[2], s[3]};
+        float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 4; e < kPmKeys; e += 8) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (e + 2 * y + 1 < kPmKeys) mx2[y] = max3(mx2[y], s[e + 2 * y], s[e + 2 * y + 1]);
-        }
-        const float mx = fmaxf(fmaxf(mx2[0], mx2[1]), fmaxf(mx2[2], mx2[3])) * f;
-        const bool fresh = c % S::kFlush == 0;
-        if (fresh && c > 0 && ok && !idle) {  // O to the sums, which are in units of a reference of their own
-          const float scale = sums_m == m ? 1.0f : ex2(sums_m - m);
-          float* to = scratch + (int64_t)x * D * 128;
+        for (int e = 4; e + 1 < kPmKeys; e += 2) mx4[e >> 1 & 3] = max3(mx4[e >> 1 & 3], s[e], s[e + 1]);
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f;
+        if (__any_sync(0xffffffffu, ok && !idle && mx > m + kPmLazy)) {
+          const float to = fmaxf(m, mx), corr = to == m ? 1.0f : ex2(m - to);
+          l *= corr;
+          m = to;
+          if (!fresh && ok && !idle) {
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            float o[16];
-            tm_load(tl + S::kColO + x * D + d, o);
-            if (summed) {
+            for (int d = 0; d < D; d += 16) {
+              float o[16];
+              tm_load(ocol + d, o);
+              uint32_t v[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fmaf(to[(d + e) * 128], scale, o[e]);
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * corr);
+              tm_store(ocol + d, v);
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) to[(d + e) * 128] = o[e];
           }
-          sums_m = m;
-          summed = true;
         }
         if (!idle && ok) {
-          if (__any_sync(0xffffffffu, mx > m + kTaLazy)) {
-            const float to = fmaxf(m, mx), corr = to == m ? 1.0f : ex2(m - to);
-            l *= corr;
-            m = to;
-            if (!fresh) {
-#pragma unroll 1
-              for (int d = 0; d < D; d += 16) {
-                float o[16];
-                tm_load(tl + S::kColO + x * D + d, o);
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * corr);
-                tm_store(tl + S::kColO + x * D + d, w);
-              }
-            }
-          }
           const float mu = m == -INFINITY ? 0.0f : m;  // nothing seen so far: every weight is 2^-inf
           const float2 sc = make_float2(f, f), mm = make_float2(-mu, -mu);
           float2 ls = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int ch = 0; ch < kPmKeys; ch += 16) {
-            uint32_t w[S::kTermsP][8];
+          for (int ch = 0; ch < kPmKeys; ch += kChunk) {
+            uint32_t w[S::kTermsP][kChunk / 2];
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
+            for (int e = 0; e < kChunk; e += 2) {
               const float2 y = fma2(make_float2(s[ch + e], s[ch + e + 1]), sc, mm);
               const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+              ls = add2(ls, pp);
               if constexpr (S::kF32) {
-                ls = add2(ls, pp);
                 uint32_t term[2];
                 split(pp.x, pp.y, term);
                 w[0][e / 2] = term[0];
                 w[1][e / 2] = term[1];
               } else {
                 w[0][e / 2] = pack_rn(pp.x, pp.y);
-                ls = add2(ls, make_float2(low_f(w[0][e / 2]), high_f(w[0][e / 2])));
               }
             }
 #pragma unroll
-            for (int t = 0; t < S::kTermsP; ++t) tm_store(tl + S::kColS + x * kPmKeys + t * (kPmKeys / 2) + ch / 2, w[t]);
+            for (int t = 0; t < S::kTermsP; ++t) tm_store(scol + t * (kPmKeys / 2) + ch / 2, w[t]);
           }
           l += ls.x + ls.y;
         }
@@ -507,38 +511,41 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
         ++phase;
       }
-      tm_fence_after();
-      // The row's sums: its own, or those of both groups, half of the dimensions each.
-      float M = m, L = l, f_own[2] = {1.0f, 1.0f}, f_sum[2];
-      bool use[2] = {cnt > 0, false}, more[2] = {summed, false};
-      f_sum[0] = summed ? ex2(sums_m - m) : 0.0f;
-      if (summed && sums_m == m) f_sum[0] = 1.0f;
-      // (A group without a tile leaves the place of its statistics alone: the other one's scores may still read the queries there.)
-      if (!kPair && cnt > 0) s_stat[x * 128 + ln] = make_float4(m, l, sums_m, summed ? 1.0f : 0.0f);
+      // The row's sums: the halves' of its group, or of both groups. (A group without a tile leaves the place of its statistics
+      // alone: the other one's scores may still read the queries there.)
+      if (cnt > 0) s_stat[x * 128 + ln] = make_float4(m, l, sums_m, summed ? 1.0f : 0.0f);
       tm_fence_before();
       meet();
       tm_fence_after();
-      if constexpr (!kPair) {
-        const float4 t0 = s_stat[ln], t1 = n > 1 ? s_stat[128 + ln] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+      float M, L, f_own[2] = {1.0f, 0.0f}, f_sum[2] = {0.0f, 0.0f};
+      bool use[2] = {true, false}, more[2] = {false, false};
+      {
+        const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+        const int g0 = kPair ? x : 0;
+        const float4 t0 = s_stat[g0 * 128 + ln], t1 = !kPair && n > 1 ? s_stat[128 + ln] : none;
         M = fmaxf(t0.x, t1.x);
         auto rel = [&](float r) { return r == M ? 1.0f : ex2(r - M); };
         f_own[0] = rel(t0.x);
-        f_own[1] = rel(t1.x);
-        L = fmaf(t0.y, f_own[0], t1.y * f_own[1]);
         f_sum[0] = rel(t0.z);
-        f_sum[1] = rel(t1.z);
-        use[0] = true;
-        use[1] = n > 1;
         more[0] = t0.w != 0.0f;
-        more[1] = t1.w != 0.0f;
+        L = t0.y * f_own[0];
+        if (!kPair && n > 1) {
+          f_own[1] = rel(t1.x);
+          f_sum[1] = rel(t1.z);
+          use[1] = true;
+          more[1] = t1.w != 0.0f;
+          L = fmaf(t1.y, f_own[1], L);
+        }
       }
+      const bool split_up = n < u.tiles;
       if (ok && !idle) {
-        const bool split_up = n < u.tiles;
-        const float f = split_up ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
+        constexpr int kOut = kPair ? D : D / 2;  // dimensions of a thread
+        const float f = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
         const int64_t to = split_up ? ((int64_t)p.slot * S::kRows + ru) * D : ((int64_t)(tok0 + tok) * a.Hq + h) * D;
         const bool fix = s_bad;
+        const int d0 = kPair ? 0 : x * kOut;
 #pragma unroll 1
-        for (int d = kPair ? 0 : x * (D / 2); d < (kPair ? D : (x + 1) * (D / 2)); d += 16) {
+        for (int d = d0; d < d0 + kOut; d += 16) {
           __syncwarp();
           float o[16];
 #pragma unroll
@@ -580,73 +587,93 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
             else store_row(static_cast<T*>(a.out) + to + d, o, f);
           }
         }
-        if (split_up && live && (kPair || x == 0)) a.ml[to / D] = make_float2(M, L);
+        if (split_up && live && d0 == 0) a.ml[to / D] = make_float2(M, L);
+      }
+      if (i == 32 * kPmFirstSoftmax && split_up && p.t0 == 0) {  // the first part of a unit: what the join has to know
+        PaPiece part = p;
+        walk.parts(part);
+        PaJoin* to = a.join + blockIdx.x;
+        to->tok0 = tok0;
+        to->head0 = head0;
+        to->rest = rest;
+        to->rows = ok ? u.rows : 0;
+        to->last = part.c1;
+        left_part = true;
       }
       tm_fence_before();
-      const bool split_up = n < u.tiles;
-      if (split_up) __threadfence();
       meet();  // all has been read: tensor memory, the statistics, s_bad
-      if (split_up) {
-        walk.parts(p);
-        const int c0 = p.c0, c1 = p.c1;
-        if (i == 32 * kPmFirstSoftmax) {
-          s_last = 0;
-          if (*fail == 0) {
-            const unsigned before = atomicAdd(a.count + p.job, 1u);
-            s_last = before == (unsigned)(c1 - c0);
-            if (s_last) a.count[p.job] = 0;
-          }
-        }
-        meet();
-        if (s_last) {
-          __threadfence();
-          constexpr int kCols = D / 4;  // threads of a row, four dimensions each
-          for (int e = i - 32 * kPmFirstSoftmax; e < u.rows * kCols; e += 256) {
-            const int r = e / kCols, d = e % kCols * 4;
-            float mj = -INFINITY, lj = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int b0 = c0; b0 <= c1; b0 += 4) {
-              float4 y[4];
-              float2 ml[4];
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const int64_t from = (int64_t)walk.slot(min(b0 + b, c1)) * S::kRows + r;
-                y[b] = __ldcg(reinterpret_cast<const float4*>(a.part + from * D + d));
-                ml[b] = __ldcg(a.ml + from);
-                if (b0 + b > c1) ml[b] = make_float2(-INFINITY, 0.0f);
-              }
-              const float to = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), mj);
-              const float corr = mj == to ? 1.0f : ex2(mj - to);
-              lj *= corr;
-              o = make_float4(o.x * corr, o.y * corr, o.z * corr, o.w * corr);
-              mj = to;
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                if (b0 + b > c1) break;
-                const float g = ml[b].x == mj ? 1.0f : ex2(ml[b].x - mj);
-                lj = fmaf(ml[b].y, g, lj);
-                o = make_float4(fmaf(y[b].x, g, o.x), fmaf(y[b].y, g, o.y), fmaf(y[b].z, g, o.z), fmaf(y[b].w, g, o.w));
-              }
-            }
-            const float g = lj == 0.0f ? 0.0f : 1.0f / lj;
-            const int tj = token_of(r);
-            T* out = static_cast<T*>(a.out) + ((int64_t)(tok0 + tj) * a.Hq + head0 + r - tj * a.G) * D + d;
-            if constexpr (S::kF32) *reinterpret_cast<float4*>(out) = make_float4(o.x * g, o.y * g, o.z * g, o.w * g);
-            else *reinterpret_cast<uint2*>(out) = make_uint2(pack_rn(o.x * g, o.y * g), pack_rn(o.z * g, o.w * g));
-          }
-        }
-      }
       if (i == 32 * kPmFirstSoftmax) s_bad = 0;
-      meet();
       k0 += 2 * n;
-      walk.next(a);
     }
+    if (i == 32 * kPmFirstSoftmax && !left_part) a.join[blockIdx.x].rows = 0;
   }
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
   if (warp == kPmMma) tm_free(tmem, kTaTmemCols);
   if (*fail && i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
+}
+
+// Joins the parts of the units that were split: CTA b takes a sixteenth of the rows of the unit whose first part is CTA b / 16's; a
+// warp per row, four (D 64: two) dimensions a lane, eight parts asked for at a time.
+constexpr int kPmJoin = 16;
+template <typename T, int D, int kRows>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PaArgs a) {
+  constexpr int E = D / 32;
+  using V = typename std::conditional<E == 4, float4, float2>::type;
+  dependent_launch_wait();
+  const int c0 = blockIdx.x / kPmJoin, lane = threadIdx.x & 31;
+  const PaJoin job = a.join[c0];
+  const float inv_g = 1.0f / (float)a.G;
+  constexpr int kPmKeys = kRows / kPmJoin;
+  const int first = (blockIdx.x % kPmJoin) * kPmKeys;
+  for (int r = first + (threadIdx.x >> 5); r < min(first + kPmKeys, job.rows); r += 4) {
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int b0 = c0; b0 <= job.last; b0 += 8) {
+      V y[8];
+      float2 ml[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const int c = min(b0 + b, job.last);
+        const int64_t from = (int64_t)(2 * c + (c == c0)) * kRows + r;
+        y[b] = __ldcg(reinterpret_cast<const V*>(a.part + from * D) + lane);
+        ml[b] = __ldcg(a.ml + from);
+        if (b0 + b > job.last) ml[b] = make_float2(-INFINITY, 0.0f);
+      }
+      float to = m;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) to = fmaxf(to, ml[b].x);
+      const float corr = m == to ? 1.0f : ex2(m - to);
+      l *= corr;
+      m = to;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= corr;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b0 + b > job.last) break;
+        const float g = ml[b].x == m ? 1.0f : ex2(ml[b].x - m);
+        const float* ye = reinterpret_cast<const float*>(&y[b]);
+        l = fmaf(ml[b].y, g, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(ye[e], g, o[e]);
+      }
+    }
+    const float g = l == 0.0f ? 0.0f : 1.0f / l;
+    const int away = node_of(job.rest + r, inv_g);
+    T* out = static_cast<T*>(a.out) + ((int64_t)(job.tok0 + away) * a.Hq + job.head0 + r - away * a.G) * D + lane * E;
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (E == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * g, o[1] * g, o[2] * g, o[3] * g);
+      else *reinterpret_cast<float2*>(out) = make_float2(o[0] * g, o[1] * g);
+    } else {
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) w[e / 2] = pack_rn(o[e] * g, o[e + 1] * g);
+      if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(out) = w[0];
+    }
+  }
 }
 
 // ---- host -----------------------------------------------------------------------------------
@@ -682,7 +709,9 @@ nt_status launch_many(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
   NT_TRY(allow_smem(paged_many_kernel<T, D, kPair, kExtra>, smem, allowed));
   const int ctas = std::min(device_sm_count(), kPaManyCtas);
   NT_CUDA_TRY(launch_kernel(paged_many_kernel<T, D, kPair, kExtra>, dim3((unsigned)ctas), dim3(kPmThreads), smem, st, true, maps, a));
-  return check_launch("paged_many_kernel");
+  NT_TRY(check_launch("paged_many_kernel"));
+  NT_CUDA_TRY(launch_kernel(paged_join_kernel<T, D, PmShape<T, D, kPair>::kRows>, dim3((unsigned)(ctas * kPmJoin)), dim3(128), 0, st, true, a));
+  return check_launch("paged_join_kernel");
 }
 template <typename T, int D, bool kPair>
 nt_status launch_many_extra(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
