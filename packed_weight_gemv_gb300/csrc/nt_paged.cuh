@@ -3,10 +3,12 @@
 //
 // A unit is a tile of query rows (a row = one token and one of the G query heads of a key-value head) of one sequence; with every
 // key-value head it stands for, it has to pass over the tiles of keys that any of its rows sees. Lengths are known on the device
-// only, so every CTA works out the division itself: all (unit, head, tile) in a row, cut into equal shares, one per CTA. A share
-// begins and ends anywhere, so a unit's keys may be split over CTAs; then each leaves its part (weighted sum, maximum, sum of weights)
-// in the workspace and the one that comes last joins them, in the order of the keys.
+// only, so every CTA works out the division itself: all (unit, head, tile) in a row, cut into shares that are as good as equal, one per
+// CTA. A unit's keys may so be split over CTAs; then each leaves its part (weighted sum, maximum, sum of weights) in the workspace,
+// and they are joined in the order of the keys: on the fp32 units by the CTA that comes last, on the tensor cores by a kernel behind.
 #pragma once
+
+#include <cuda.h>
 
 #include "nt_pages.cuh"
 
@@ -113,22 +115,109 @@ __device__ __forceinline__ int64_t pa_scan(int64_t x, int64_t* warps, int64_t* t
   return before + y - x;
 }
 
-// A CTA's share: [from, end) of all work; the unit that `from` falls into, its number, and the work before it.
-struct PaShare {
-  int64_t work, from, end, off;
-  int s, mt, unit;
-  int ctas;  // with a share: no more than there are tiles
-};
-__device__ __forceinline__ int64_t pa_from(int64_t work, int c, int ctas) { return work * c / ctas; }
-__device__ __forceinline__ int pa_with(int64_t work, int64_t x, int ctas) { return (int)(((x + 1) * ctas - 1) / work); }
+__device__ __forceinline__ int64_t pa_div(int64_t x, int64_t y) {  // x >= 0, y > 0
+  return (x | y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
-// A unit's work for a head is its tiles and kStart, what beginning and ending a piece costs in tiles.
-// starts: S places of shared memory (scratch); all threads of the CTA, every one gets the share.
+// How the work of a call is cut. A unit's work for a head is its tiles and kStart, what beginning and ending a piece costs in tiles.
+// Equal shares, whose ends move to that of a unit and head where that is nearer than `near` tiles: a CTA would otherwise begin
+// and end a piece for next to nothing.
+template <int kStart>
+struct PaCut {
+  int64_t work, base, near;
+  int ctas, rem;
+  __device__ __forceinline__ void set(int64_t all, int grid, int most) {
+    work = all;
+    ctas = (int)min((int64_t)grid, all);
+    base = ctas ? pa_div(all, ctas) : 0;
+    rem = (int)(all - base * ctas);
+    near = max((int64_t)1, min((int64_t)most, base / 2));
+  }
+  __device__ __forceinline__ int64_t from(int c) const { return base * c + min(c, rem); }
+  // The first CTA whose share begins at y or behind.
+  __device__ __forceinline__ int first_from(int64_t y) const {
+    const int64_t big = (base + 1) * rem;
+    return (int)(y <= big ? pa_div(y + base, base + 1) : rem + pa_div(y - big + base - 1, base));
+  }
+  // The end x of a share among the work [off, off + w) of a unit and head.
+  __device__ __forceinline__ int64_t snap(int64_t x, int64_t off, int64_t w) const {
+    const int64_t lo = off + kStart + near, hi = off + w - near;
+    if (lo > hi) return x - off < off + w - x ? off : off + w;
+    return x < lo ? off : x > hi ? off + w : x;
+  }
+};
+
+// A CTA's share: [from, end) of all work; the unit and head that `from` falls into, and the work before it.
+template <int kStart>
+struct PaShare {
+  PaCut<kStart> cut;
+  int64_t from, end, off;
+  int s, mt, unit, g;
+};
+
+// starts: S places of shared memory (scratch); all threads of the CTA, every one gets the share. near: see PaCut.
 template <int kThreads, int kKeys, int kStart>
-__device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
+__device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* starts) {
+  const int lane = threadIdx.x & 31;
+  PaShare<kStart> r{};
+  // A few sequences and units: every warp works it out for itself.
+  if (a.S <= 32) {
+    PaSeq q{};
+    int n = 0;
+    if (lane < a.S) {
+      q = pa_seq(a, lane);
+      n = pa_row_tiles(a, q.n, rows);
+    }
+    int upto = n;
+    bool many = n > 32;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int z = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += z;
+      many |= upto > 32;  // (before it could overflow)
+    }
+    if (!__any_sync(0xffffffffu, many)) {
+      const int units = __shfl_sync(0xffffffffu, upto, 31);
+      if ((int64_t)units * a.Hkv > a.jobs) return r;  // starts that do not rise name more tokens than there are: no work
+      int s = 0;  // of unit `lane`: the sequences that end at or before it
+#pragma unroll
+      for (int d = 16; d; d /= 2)
+        if (__shfl_sync(0xffffffffu, upto, s + d - 1) <= lane) s += d;
+      s = min(s, 31);
+      const int mt = lane - (__shfl_sync(0xffffffffu, upto, s) - __shfl_sync(0xffffffffu, n, s));
+      PaSeq mine;
+      mine.t0 = __shfl_sync(0xffffffffu, q.t0, s);
+      mine.n = __shfl_sync(0xffffffffu, q.n, s);
+      mine.len = __shfl_sync(0xffffffffu, q.len, s);
+      int64_t w = 0;
+      if (lane < units) w = (int64_t)(pa_unit<kKeys>(a, mine, s, mt, rows).tiles + kStart);
+      const int64_t w_all = w * a.Hkv;
+      int64_t end = w_all;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int64_t z = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += z;
+      }
+      r.cut.set(__shfl_sync(0xffffffffu, end, 31), gridDim.x, near);
+      if ((int)blockIdx.x >= r.cut.ctas) return r;
+      const int64_t x0 = r.cut.from(blockIdx.x), x1 = r.cut.from(blockIdx.x + 1);
+      const unsigned h0 = __ballot_sync(0xffffffffu, end - w_all <= x0 && x0 < end), h1 = __ballot_sync(0xffffffffu, end - w_all <= x1 && x1 < end);
+      const int u0 = __ffs(h0) - 1, u1 = h1 ? __ffs(h1) - 1 : 0;
+      const int64_t off0 = __shfl_sync(0xffffffffu, end - w_all, u0), off1 = __shfl_sync(0xffffffffu, end - w_all, u1);
+      const int64_t w0 = __shfl_sync(0xffffffffu, w, u0), w1 = __shfl_sync(0xffffffffu, w, u1);
+      r.s = __shfl_sync(0xffffffffu, s, u0);
+      r.mt = __shfl_sync(0xffffffffu, mt, u0);
+      r.unit = u0;
+      r.g = (int)pa_div(x0 - off0, w0);
+      r.off = off0 + r.g * w0;
+      r.from = r.cut.snap(x0, r.off, w0);
+      r.end = h1 ? r.cut.snap(x1, off1 + pa_div(x1 - off1, w1) * w1, w1) : r.cut.work;
+      return r;
+    }
+  }
   __shared__ int64_t s_warps[32];
   __shared__ int s_first[3];
-  __shared__ int64_t s_off;
+  __shared__ int64_t s_at[4];  // work before the units of both ends, and a head's
   const int i = threadIdx.x;
   int64_t units = 0;
   for (int s0 = 0; s0 < a.S; s0 += kThreads) {
@@ -138,8 +227,7 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
     if (s < a.S) starts[s] = (int)(units + at);
     units += total;
   }
-  PaShare r{};
-  if (units * a.Hkv > a.jobs) return r;  // starts that do not rise name more tokens than there are: no work
+  if (units * a.Hkv > a.jobs) return r;  // as above
   __syncthreads();
   auto tiles = [&](int64_t u, int* s_out, int* mt_out) -> int64_t {
     if (u >= units) return 0;
@@ -154,36 +242,38 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
     return (int64_t)(pa_unit<kKeys>(a, pa_seq(a, s), s, *mt_out, rows).tiles + kStart) * a.Hkv;
   };
   int s = 0, mt = 0;
-  int64_t mine = 0, at = 0;
+  int64_t mine = 0, at = 0, work = 0;
   for (int64_t u0 = 0; u0 < units; u0 += kThreads) {
     int64_t total;
     mine = tiles(u0 + i, &s, &mt);
-    at = r.work + pa_scan<kThreads>(mine, s_warps, &total);
-    r.work += total;
+    at = work + pa_scan<kThreads>(mine, s_warps, &total);
+    work += total;
   }
-  r.ctas = (int)min((int64_t)gridDim.x, r.work);
-  if ((int)blockIdx.x >= r.ctas) return r;  // nothing left for this CTA
-  r.from = pa_from(r.work, blockIdx.x, r.ctas);
-  r.end = pa_from(r.work, blockIdx.x + 1, r.ctas);
-  if (units <= kThreads) {
-    if (at <= r.from && r.from < at + mine) {
+  r.cut.set(work, gridDim.x, near);
+  if ((int)blockIdx.x >= r.cut.ctas) return r;  // nothing left for this CTA
+  const int64_t x0 = r.cut.from(blockIdx.x), x1 = r.cut.from(blockIdx.x + 1);
+  auto found = [&](int64_t u) {
+    if (at <= x0 && x0 < at + mine) {
       s_first[0] = s;
       s_first[1] = mt;
-      s_first[2] = i;
-      s_off = at;
+      s_first[2] = (int)u;
+      s_at[0] = at;
+      s_at[1] = mine / a.Hkv;
     }
+    if (at <= x1 && x1 < at + mine) {
+      s_at[2] = at;
+      s_at[3] = mine / a.Hkv;
+    }
+  };
+  if (units <= kThreads) {
+    found(i);
   } else {
     int64_t sum = 0;
-    for (int64_t u0 = 0; u0 < units && sum <= r.from; u0 += kThreads) {
+    for (int64_t u0 = 0; u0 < units && sum <= x1; u0 += kThreads) {
       int64_t total;
       mine = tiles(u0 + i, &s, &mt);
       at = sum + pa_scan<kThreads>(mine, s_warps, &total);
-      if (at <= r.from && r.from < at + mine) {
-        s_first[0] = s;
-        s_first[1] = mt;
-        s_first[2] = (int)(u0 + i);
-        s_off = at;
-      }
+      found(u0 + i);
       sum += total;
     }
   }
@@ -191,7 +281,10 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
   r.s = s_first[0];
   r.mt = s_first[1];
   r.unit = s_first[2];
-  r.off = s_off;
+  r.g = (int)pa_div(x0 - s_at[0], s_at[1]);
+  r.off = s_at[0] + r.g * s_at[1];
+  r.from = r.cut.snap(x0, r.off, s_at[1]);
+  r.end = x1 < work ? r.cut.snap(x1, s_at[2] + pa_div(x1 - s_at[2], s_at[3]) * s_at[3], s_at[3]) : work;
   return r;
 }
 
@@ -199,49 +292,47 @@ __device__ PaShare pa_share(const PaArgs& a, int rows, int* starts) {
 struct PaPiece {
   PaUnit u;
   int g, t0, n;
-  int c0, c1;      // CTAs with the unit's first and last tile for this head
+  int c0, c1;      // CTAs with the unit's first and last tile for this head (PaWalk::parts)
   int slot;        // where this CTA leaves its part
   int job;         // unit and head: the place of the counter
 };
 template <int kKeys, int kStart>
 struct PaWalk {
-  PaShare sh;
+  PaShare<kStart> sh;
   int rows;
-  int g = 0;
   PaSeq q;
   PaUnit u;
-  __device__ __forceinline__ PaWalk(const PaArgs& a, const PaShare& share, int rows_) : sh(share), rows(rows_) {
+  __device__ __forceinline__ PaWalk(const PaArgs& a, const PaShare<kStart>& share, int rows_) : sh(share), rows(rows_) {
     if (sh.from >= sh.end) return;
     q = pa_seq(a, sh.s);
     u = pa_unit<kKeys>(a, q, sh.s, sh.mt, rows);
-    g = (int)((sh.from - sh.off) / (u.tiles + kStart));
-    sh.off += (int64_t)g * (u.tiles + kStart);
+    if (sh.from >= sh.off + u.tiles + kStart) next(a);  // the share begins where this unit and head end
   }
-  // sh.off: the work before this unit and head. A share that ends among the first kStart has no tile of it.
-  __device__ __forceinline__ bool more() const { return sh.off + kStart < sh.end; }
+  // sh.off: the work before this unit and head. A share begins and ends with one, or among its tiles.
+  __device__ __forceinline__ bool more() const { return sh.off + kStart < sh.end && sh.from < sh.end; }
   __device__ __forceinline__ PaPiece piece(const PaArgs& a) const {
     PaPiece p;
     p.u = u;
-    p.g = g;
+    p.g = sh.g;
     const int64_t tile = sh.off + kStart;  // the first one
     p.t0 = (int)max((int64_t)0, sh.from - tile);
     p.n = (int)min((int64_t)u.tiles, sh.end - tile) - p.t0;
     p.c0 = p.c1 = blockIdx.x;
-    p.slot = slot(blockIdx.x);
-    p.job = sh.unit * a.Hkv + g;
+    p.slot = 2 * blockIdx.x + (p.t0 == 0);
+    p.job = sh.unit * a.Hkv + sh.g;
     return p;
   }
-  __device__ __forceinline__ void parts(PaPiece& p) const {  // of a piece that is not all of its unit
-    p.c0 = pa_with(sh.work, sh.off + kStart, sh.ctas);
-    p.c1 = pa_with(sh.work, sh.off + kStart + u.tiles - 1, sh.ctas);
+  // Of a piece that is not all of its unit and head. CTA c leaves its part in place 2 c, c0 in 2 c0 + 1 (its share may have begun with
+  // a part of another).
+  __device__ __forceinline__ void parts(PaPiece& p) const {
+    p.c0 = sh.cut.first_from(sh.off + kStart + sh.cut.near) - 1;
+    p.c1 = sh.cut.first_from(sh.off + kStart + u.tiles - sh.cut.near + 1) - 1;
   }
-  // Where CTA c leaves its part of this unit and head: in its first place if its share begins among the unit's tiles.
-  __device__ __forceinline__ int slot(int c) const { return 2 * c + (pa_from(sh.work, c, sh.ctas) <= sh.off + kStart); }
   __device__ __forceinline__ void next(const PaArgs& a) {
     sh.off += u.tiles + kStart;
     if (!more()) return;
-    if (++g < a.Hkv) return;
-    g = 0;
+    if (++sh.g < a.Hkv) return;
+    sh.g = 0;
     ++sh.unit;
     ++sh.mt;
     while (sh.mt >= pa_row_tiles(a, q.n, rows)) {  // there is one: work is left
@@ -255,6 +346,8 @@ struct PaWalk {
 }  // namespace
 #endif  // __CUDACC__
 
+// Boxes of 64 dimensions x box_rows rows of the pool, 128-byte swizzle; rows behind it read as zeros.
+nt_status paged_map(CUtensorMap* map, const uint16_t* base, int D, int box_rows, const PaArgs& a);
 // Up to 8 rows of a sequence to a CTA (max_rows: the most that a sequence is expected to have).
 nt_status launch_paged_few(const PaArgs& a, int dtype, int D, int64_t max_rows, cudaStream_t st);
 // Any number of rows, on the tensor cores.

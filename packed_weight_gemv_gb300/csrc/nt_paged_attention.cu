@@ -1,7 +1,10 @@
 // nt_paged_attention.cu -- attention of ragged chunks of new tokens over a paged bf16 cache: the call.
-#include <cmath>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <string>
 
 #include "nt_paged.cuh"
 
@@ -31,7 +34,33 @@ nt_status check_paged(int T, int S, int Hq, int Hkv, int D) {
   return NT_OK;
 }
 
+std::mutex g_paged_mu;
+PFN_cuTensorMapEncodeTiled_v12000 g_paged_encode = nullptr;
+
 }  // namespace
+
+nt_status paged_map(CUtensorMap* map, const uint16_t* base, int D, int box_rows, const PaArgs& a) {
+  {
+    std::lock_guard<std::mutex> lock(g_paged_mu);
+    if (!g_paged_encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      NT_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q));
+      if (q != cudaDriverEntryPointSuccess || !fn) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled not available");
+      g_paged_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.ts, (cuuint64_t)a.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.ts * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_paged_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
+                                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
+  return NT_OK;
+}
+
 }  // namespace nt
 
 using namespace nt;

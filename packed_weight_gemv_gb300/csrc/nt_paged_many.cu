@@ -19,13 +19,10 @@
 // instructions a pair). The tensor core
 // cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
 // that round to nearest.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
-#include <string>
 #include <type_traits>
 
 #include "nt_tree_attn.cuh"
@@ -38,7 +35,7 @@ constexpr int kPmKeys = 128;
 constexpr int kPmKeyLoad = 0, kPmMma = 1, kPmValueLoad = 2, kPmFirstSoftmax = 4;
 constexpr int kPmSoftmax = 256;  // two groups of 128 threads
 constexpr int kPmThreads = 32 * kPmFirstSoftmax + kPmSoftmax;
-constexpr int kPmStart = 4;
+constexpr int kPmStart = 4, kPmNear = 3;
 constexpr float kPmLazy = 32.0f;  // a reference is raised once a score exceeds it by 2^32: weights that large lose nothing in fp32 or bf16
 constexpr int kPmSmem = 224 * 1024;
 // Registers of a thread: launched with 168; the first four warps give some of theirs to the softmax (128 x 88 + 256 x 208 = 384 x 168).
@@ -152,7 +149,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
   tm_fence_after();
   const uint32_t tmem = tmem_slot;
   dependent_launch_wait();
-  PaWalk<kPmKeys, kPmStart> walk(a, pa_share<kPmThreads, kPmKeys, kPmStart>(a, S::kRows, reinterpret_cast<int*>(ring)), S::kRows);
+  PaWalk<kPmKeys, kPmStart> walk(a, pa_share<kPmThreads, kPmKeys, kPmStart>(a, S::kRows, kPmNear, reinterpret_cast<int*>(ring)), S::kRows);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before copies over the division's scratch
   __syncthreads();
   auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
@@ -677,31 +674,6 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 }
 
 // ---- host -----------------------------------------------------------------------------------
-std::mutex g_pm_mu;
-PFN_cuTensorMapEncodeTiled_v12000 g_pm_encode = nullptr;
-
-nt_status pm_map(CUtensorMap* map, const uint16_t* base, int D, const PaArgs& a) {
-  {
-    std::lock_guard<std::mutex> lock(g_pm_mu);
-    if (!g_pm_encode) {
-      void* fn = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      NT_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q));
-      if (q != cudaDriverEntryPointSuccess || !fn) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled not available");
-      g_pm_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
-  }
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.ts, (cuuint64_t)a.Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.ts * D * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)std::min(a.page, kPmKeys), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_pm_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, box, estr,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return set_error(NT_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string((int)r) + ")");
-  return NT_OK;
-}
-
 template <typename T, int D, bool kPair, bool kExtra>
 nt_status launch_many(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
   constexpr int smem = PmShape<T, D, kPair>::kSmem;
@@ -722,8 +694,8 @@ nt_status launch_many_extra(const PmMaps& maps, const PaArgs& a, cudaStream_t st
 
 nt_status launch_paged_many(const PaArgs& a, int dtype, int D, int64_t max_rows, cudaStream_t st) {
   PmMaps maps;
-  NT_TRY(pm_map(&maps.k, a.k, D, a));
-  NT_TRY(pm_map(&maps.v, a.v, D, a));
+  NT_TRY(paged_map(&maps.k, a.k, D, std::min(a.page, kPmKeys), a));
+  NT_TRY(paged_map(&maps.v, a.v, D, std::min(a.page, kPmKeys), a));
   if (dtype == NT_F32) return D == 64 ? launch_many_extra<float, 64, false>(maps, a, st) : launch_many_extra<float, 128, false>(maps, a, st);
   if (max_rows <= 128)
     return D == 64 ? launch_many_extra<uint16_t, 64, false>(maps, a, st) : launch_many_extra<uint16_t, 128, false>(maps, a, st);
