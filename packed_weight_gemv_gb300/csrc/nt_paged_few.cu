@@ -27,7 +27,7 @@ namespace nt {
 namespace {
 
 constexpr int kFewKeys = 64;  // keys per tile of the division
-constexpr int kFewStart = 1, kFewNear = 6;
+constexpr int kFewStart = 5, kFewNear = 6;
 
 __device__ __forceinline__ void load_matrices(uint32_t at, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
   __shared__ float s_m[kFewWarps][R], s_l[kFewWarps][R];
   __shared__ __align__(8) uint64_t bars[kFewWarps * S::kPlaces + 1];
   __shared__ FewPart s_part[2];
-  __shared__ int s_fail, s_arrived, s_last;
+  __shared__ int s_fail, s_arrived, s_last[2];
   volatile int* fail = &s_fail;
   const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
   const int g = lane >> 2, t2 = 2 * (lane & 3);  // an MMA's row (and g + 8) and first column of this lane
@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     const PaUnit& u = p.u;
     auto token = [&](int r) { return (u.mt * R + min(r, u.rows - 1)) / a.G; };  // rows behind the last one repeat it
     auto head = [&](int r) { return p.g * a.G + (u.mt * R + min(r, u.rows - 1)) % a.G; };
-    if (pieces > 0) queries(p);
     uint32_t q[S::kTiles][D / 16][4];
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
@@ -254,6 +253,11 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
           q[S::kTiles - 1][k][2 * y + 1] = 0u;
         }
       }
+    {  // the next piece's are asked for while this one is weighed
+      PaWalk<kFewKeys, kFewStart> after = walk;
+      after.next(a);
+      if (after.more()) queries(after.piece(a));
+    }
     const int pos = u.len - u.n + token(row);
     const float slope = kExtra && a.slopes ? a.slopes[head(row)] : 0.0f;
     const int hi = min(u.p1 + 1, (p.t0 + u.tile0 + p.n) * kFewKeys);            // no row sees this key or one behind it
@@ -296,13 +300,13 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
       const uint32_t kp = arrived();
       if (!ok) break;
       const bool whole = base >= sure_lo && base + S::kBlock - 1 <= sure_hi;  // every row sees every key
-      float s4[S::kTiles][kCols][4];
+      float s4[S::kTiles][kCols][4], other[S::kTiles][kCols][4];  // even and odd steps: two chains of MMAs, not one
 #pragma unroll
       for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s4[t][n][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) s4[t][n][e] = other[t][n][e] = 0.0f;
 #pragma unroll
       for (int h = 0; h < kSubs; ++h)
 #pragma unroll
@@ -311,11 +315,17 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
           load_matrices(kp + chunk(h * 16 + (lane >> 4) * 8 + (lane & 7), 2 * k + (lane >> 3 & 1)), b);
 #pragma unroll
           for (int t = 0; t < S::kTiles; ++t) {
-            mma_16816(s4[t][2 * h], q[t][k], b[0], b[1]);
-            mma_16816(s4[t][2 * h + 1], q[t][k], b[2], b[3]);
+            mma_16816(k & 1 ? other[t][2 * h] : s4[t][2 * h], q[t][k], b[0], b[1]);
+            mma_16816(k & 1 ? other[t][2 * h + 1] : s4[t][2 * h + 1], q[t][k], b[2], b[3]);
           }
         }
       read();
+#pragma unroll
+      for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s4[t][n][e] += other[t][n][e];
       // The terms' rows together: keys base + 8 n + t2 + e of row g.
       float s[kCols][2];
 #pragma unroll
@@ -474,88 +484,79 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     return;
   }
   // The parts that this CTA has left: whoever comes last joins all of a unit and head.
-  for (int k = 0; k < 2; ++k) {
-    const FewPart part = s_part[k];
-    if (!part.there) continue;
-    if (i == 0) {
+  if (i < 2) {
+    s_last[i] = 0;
+    if (s_part[i].there) {
+      __threadfence();  // (of this thread for all, which have met it)
+      const unsigned before = atomicAdd(a.count + s_part[i].job, 1u);
+      s_last[i] = before == (unsigned)(s_part[i].c1 - s_part[i].c0);
+      if (s_last[i]) a.count[s_part[i].job] = 0;
       __threadfence();
-      const unsigned before = atomicAdd(a.count + part.job, 1u);  // (fences: of this thread for all, which have met it)
-      s_last = before == (unsigned)(part.c1 - part.c0);
-      if (s_last) a.count[part.job] = 0;
     }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      constexpr int kBatch = 16;  // parts asked for at a time
-      // kSets threads to four dimensions of a row, every kSets-th part each
-      constexpr int kItems = R * D / 4, kSets = std::min(kFewWarps, std::max(1, kFewThreads / kItems));
-      float(*s_set)[R][D] = s_o;  // [kSets]
-      for (int e0 = 0; e0 < kItems * kSets; e0 += kFewThreads) {
-        const int e = min(e0 + i, kItems * kSets - 1), set = e / kItems, r = e % kItems / (D / 4), c = e % (D / 4) * 4;
-        float M = -INFINITY, L = 0.0f;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b0 = part.c0 + set; b0 <= part.c1; b0 += kBatch * kSets) {
-          float4 y[kBatch];
-          float2 ml[kBatch];
+  }
+  __syncthreads();
+  // A warp takes every eighth part, three asked for at a time; then the warps' sums are joined as those of a piece are. (Unrolled over 16
+  // parts this took 4 us: code that an SM has not run yet comes from L2.)
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (!s_last[k]) continue;
+    const FewPart part = s_part[k];
+    constexpr int kItems = R * D / 128, kBatch = 3;  // four dimensions each of a lane's rows
+    float4 x[kItems];
+    float M[kItems], L[kItems];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const int cta = min(b0 + b * kSets, part.c1);
-            const int64_t from = (int64_t)(2 * cta + (cta == part.c0)) * R + r;
-            y[b] = __ldcg(reinterpret_cast<const float4*>(a.part + from * D + c));
-            ml[b] = __ldcg(a.ml + from);
-            if (b0 + b * kSets > part.c1) ml[b] = make_float2(-INFINITY, 0.0f);
-          }
-          float to = M;
+    for (int e = 0; e < kItems; ++e) {
+      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      M[e] = -INFINITY;
+      L[e] = 0.0f;
+    }
+    auto row_of = [&](int e) { return D == 128 ? e : 2 * e + (lane >> 4); };
+    const int col = lane * 4 % D;
+#pragma unroll 1
+    for (int b0 = part.c0 + warp; b0 <= part.c1; b0 += kBatch * kFewWarps) {
+      float4 y[kBatch][kItems];
+      float2 ml[kBatch][kItems];
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) to = fmaxf(to, ml[b].x);
-          const float corr = M == to ? 1.0f : ex2(M - to);
-          L *= corr;
-          x = make_float4(x.x * corr, x.y * corr, x.z * corr, x.w * corr);
-          M = to;
+      for (int b = 0; b < kBatch; ++b) {
+        const int cta = b0 + b * kFewWarps;
+        const int64_t from = (int64_t)(2 * min(cta, part.c1) + (cta == part.c0)) * R;
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            if (b0 + b * kSets > part.c1) break;
-            const float f = ml[b].x == M ? 1.0f : ex2(ml[b].x - M);
-            L = fmaf(ml[b].y, f, L);
-            x.x = fmaf(y[b].x, f, x.x);
-            x.y = fmaf(y[b].y, f, x.y);
-            x.z = fmaf(y[b].z, f, x.z);
-            x.w = fmaf(y[b].w, f, x.w);
-          }
+        for (int e = 0; e < kItems; ++e) {
+          y[b][e] = __ldcg(reinterpret_cast<const float4*>(a.part + (from + row_of(e)) * D + col));
+          ml[b][e] = __ldcg(a.ml + from + row_of(e));
+          if (cta > part.c1) ml[b][e] = make_float2(-INFINITY, 0.0f);
         }
-        if constexpr (kSets > 1) {
-          *reinterpret_cast<float4*>(&s_set[set][r][c]) = x;
-          if (c == 0) {
-            s_m[set][r] = M;
-            s_l[set][r] = L;
-          }
-          __syncthreads();
-          if (set == 0) {
-            M = -INFINITY;
+      }
 #pragma unroll
-            for (int w = 0; w < kSets; ++w) M = fmaxf(M, s_m[w][r]);
-            L = 0.0f;
-            x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int b = 0; b < kBatch; ++b) {
+        if (b0 + b * kFewWarps > part.c1) break;
 #pragma unroll
-            for (int w = 0; w < kSets; ++w) {
-              const float f = s_m[w][r] == M ? 1.0f : ex2(s_m[w][r] - M);
-              const float4 y = *reinterpret_cast<const float4*>(&s_set[w][r][c]);
-              L = fmaf(s_l[w][r], f, L);
-              x.x = fmaf(y.x, f, x.x);
-              x.y = fmaf(y.y, f, x.y);
-              x.z = fmaf(y.z, f, x.z);
-              x.w = fmaf(y.w, f, x.w);
-            }
-          }
-        }
-        if (set == 0 && r < part.rows && e == e0 + i) {
-          const float f = L == 0.0f ? 0.0f : 1.0f / L;
-          const int ra = part.mt * R + r, tok = ra / a.G;
-          T* to = static_cast<T*>(a.out) + ((int64_t)(part.t0 + tok) * a.Hq + part.g * a.G + ra - tok * a.G) * D + c;
-          store4(to, make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+        for (int e = 0; e < kItems; ++e) {
+          const float to = fmaxf(M[e], ml[b][e].x);
+          const float f0 = M[e] == to ? 1.0f : ex2(M[e] - to), f1 = ml[b][e].x == to ? 1.0f : ex2(ml[b][e].x - to);
+          M[e] = to;
+          L[e] = fmaf(L[e], f0, ml[b][e].y * f1);
+          x[e] = make_float4(fmaf(x[e].x, f0, y[b][e].x * f1), fmaf(x[e].y, f0, y[b][e].y * f1), fmaf(x[e].z, f0, y[b][e].z * f1),
+                             fmaf(x[e].w, f0, y[b][e].w * f1));
         }
       }
     }
+#pragma unroll
+    for (int e = 0; e < kItems; ++e) {
+      *reinterpret_cast<float4*>(&s_o[warp][row_of(e)][col]) = x[e];
+      if (col == 0) {
+        s_m[warp][row_of(e)] = M[e];
+        s_l[warp][row_of(e)] = L[e];
+      }
+    }
+    __syncthreads();
+    PaPiece whole{};
+    whole.u.mt = part.mt;
+    whole.u.t0 = part.t0;
+    whole.u.rows = part.rows;
+    whole.u.tiles = whole.n = 1;
+    whole.g = part.g;
+    join(whole, i, kFewThreads);
     __syncthreads();
   }
 }
