@@ -35,7 +35,7 @@ constexpr int kPmKeys = 128;
 constexpr int kPmKeyLoad = 0, kPmMma = 1, kPmValueLoad = 2, kPmFirstSoftmax = 4;
 constexpr int kPmSoftmax = 256;  // two groups of 128 threads
 constexpr int kPmThreads = 32 * kPmFirstSoftmax + kPmSoftmax;
-constexpr int kPmStart = 4, kPmNear = 3;
+constexpr int kPmNear = 1;
 constexpr float kPmLazy = 32.0f;  // a reference is raised once a score exceeds it by 2^32: weights that large lose nothing in fp32 or bf16
 constexpr int kPmSmem = 224 * 1024;
 // Registers of a thread: launched with 168; the first four warps give some of theirs to the softmax (128 x 88 + 256 x 208 = 384 x 168).
@@ -55,6 +55,9 @@ struct PmShape {
   static constexpr int kQBytes = kQTile * kTermsQ * (kPair ? 2 : 1);
   static constexpr int kStages = std::min(8, (kPmSmem - kQBytes) / kSlot);
   static constexpr int kAhead = kPair ? 1 : 2;  // tiles whose scores are formed before the first weights
+  // What a piece's start and end cost in tiles. Measured, bf16 in pairs: ragged prompts 1,026 us with 2, 897 with 3, 651 with 6 and 10;
+  // fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
+  static constexpr int kStart = kPair ? 8 : 3;
   static constexpr int kColO = 0, kColS = 2 * D;
   // A tile costs a sum at most 16 (fp32) or 8 cuts of 2^-23: 2^-16 over 8 tiles, 2^-14 over 64.
   static constexpr int kFlush = kF32 ? 8 : 64;
@@ -63,17 +66,6 @@ struct PmShape {
   static_assert(kColS + 2 * kPmKeys <= kTaTmemCols, "tensor-memory columns");
   static_assert(kPageMaxSeqs * 4 <= kStages * kSlot, "the division's scratch stands in the ring");
 };
-
-__device__ __forceinline__ void store_row(float* p, const float (&o)[16], float f) {
-#pragma unroll
-  for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(o[e] * f, o[e + 1] * f, o[e + 2] * f, o[e + 3] * f);
-}
-__device__ __forceinline__ void store_row(uint16_t* p, const float (&o)[16], float f) {
-#pragma unroll
-  for (int e = 0; e < 16; e += 8)
-    *reinterpret_cast<uint4*>(p + e) = make_uint4(pack_rn(o[e] * f, o[e + 1] * f), pack_rn(o[e + 2] * f, o[e + 3] * f),
-                                                  pack_rn(o[e + 4] * f, o[e + 5] * f), pack_rn(o[e + 6] * f, o[e + 7] * f));
-}
 
 // bar_wait in one piece: a call would fix the registers that setmaxnreg moves.
 __device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
@@ -149,7 +141,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
   tm_fence_after();
   const uint32_t tmem = tmem_slot;
   dependent_launch_wait();
-  PaWalk<kPmKeys, kPmStart> walk(a, pa_share<kPmThreads, kPmKeys, kPmStart>(a, S::kRows, kPmNear, reinterpret_cast<int*>(ring)), S::kRows);
+  PaWalk<kPmKeys, S::kStart> walk(a, pa_share<kPmThreads, kPmKeys, S::kStart>(a, S::kRows, kPmNear, reinterpret_cast<int*>(ring)), S::kRows);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before copies over the division's scratch
   __syncthreads();
   auto full = [&](int k) { return full0 + 8 * (k % S::kStages); };
@@ -313,6 +305,26 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
     bool ok = true, left_part = false;
     uint32_t phase = 0;  // of sfull
     auto meet = [&] { asm volatile("bar.sync 9, %0;" ::"n"(kPmSoftmax) : "memory"); };
+    // This thread's part of a piece's queries, asked for before the end of the piece before: 8 dimensions each of kLoads rows.
+    constexpr int kLanes = D / 8, kAt = 32 / kLanes, kRowsMine = kPair ? 32 : 16, kLoads = kRowsMine / kAt, kVecs = S::kF32 ? 2 : 1;
+    uint4 f[kLoads][kVecs];
+    auto queries = [&](const PaPiece& p) {
+      const int row0 = p.u.mt * S::kRows, first = row0 / a.G, rest = row0 - first * a.G;
+      const int r0 = (kPair ? x * 128 : x * kRowsMine) + quarter * 32 + lane / kLanes;
+      const T* q0 = static_cast<const T*>(a.q) + (int64_t)(p.u.t0 + first) * a.q_stride + (int64_t)(p.g * a.G + rest) * D + lane % kLanes * 8;
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int ru = r0 + e * kAt, away = node_of(rest + ru, inv_g);
+        const T* q = q0 + (int64_t)away * a.q_stride + (ru - away * a.G) * D;
+#pragma unroll
+        for (int y = 0; y < kVecs; ++y) f[e][y] = ru < p.u.rows ? reinterpret_cast<const uint4*>(q)[y] : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    {
+      PaPiece ahead{};
+      if (walk.more()) ahead = walk.piece(a);
+      queries(ahead);
+    }
     for (; walk.more(); walk.next(a)) {
       const PaPiece p = walk.piece(a);
       const PaUnit& u = p.u;
@@ -322,16 +334,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       const int tok0 = u.t0 + first, head0 = p.g * a.G + rest;
       auto token_of = [&](int r) { return node_of(rest + r, inv_g); };
       {  // the queries' terms into shared memory, rows of 64 dimensions with the 128-byte swizzle
-        constexpr int kLanes = D / 8, kAt = 32 / kLanes, kRowsMine = kPair ? 32 : 16, kLoads = kRowsMine / kAt, kVecs = S::kF32 ? 2 : 1;
         const int c = lane % kLanes, r0 = quarter * 32 + (kPair ? 0 : x * kRowsMine) + lane / kLanes;
-        uint4 f[kLoads][kVecs];  // all asked for at once
-#pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-          const int ru = (kPair ? x * 128 : 0) + r0 + e * kAt, away = token_of(ru);
-          const T* q = static_cast<const T*>(a.q) + (int64_t)(tok0 + away) * a.q_stride + (int64_t)(head0 + ru - away * a.G) * D + c * 8;
-#pragma unroll
-          for (int y = 0; y < kVecs; ++y) f[e][y] = ru < u.rows ? reinterpret_cast<const uint4*>(q)[y] : make_uint4(0u, 0u, 0u, 0u);
-        }
         uint8_t* to = q_smem + (kPair ? x * S::kTermsQ * S::kQTile : 0) + (c >> 3) * (128 * 128);
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
@@ -504,13 +507,20 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         tm_fence_before();
         if (ok) bar_arrive_warp(pfull0 + 8 * x, lane);
       }
+      {
+        PaWalk<kPmKeys, S::kStart> after = walk;
+        after.next(a);
+        PaPiece ahead{};
+        if (after.more()) ahead = after.piece(a);
+        queries(ahead);  // (of none, zeros: what is only set at times would take registers all along)
+      }
       if (cnt > 0) {  // the last products
         ok = ok && pm_wait_warp(sfull0 + 8 * x, phase & 1, fail, a.timeout_ns);
         ++phase;
       }
-      // The row's sums: the halves' of its group, or of both groups. (A group without a tile leaves the place of its statistics
+      // The row's sums: its own, or those of both groups. (A group without a tile leaves the place of its statistics
       // alone: the other one's scores may still read the queries there.)
-      if (cnt > 0) s_stat[x * 128 + ln] = make_float4(m, l, sums_m, summed ? 1.0f : 0.0f);
+      if (!kPair && cnt > 0) s_stat[x * 128 + ln] = make_float4(m, l, sums_m, summed ? 1.0f : 0.0f);
       tm_fence_before();
       meet();
       tm_fence_after();
@@ -518,8 +528,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       bool use[2] = {true, false}, more[2] = {false, false};
       {
         const float4 none = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-        const int g0 = kPair ? x : 0;
-        const float4 t0 = s_stat[g0 * 128 + ln], t1 = !kPair && n > 1 ? s_stat[128 + ln] : none;
+        const float4 t0 = kPair ? make_float4(m, l, sums_m, summed ? 1.0f : 0.0f) : s_stat[ln], t1 = !kPair && n > 1 ? s_stat[128 + ln] : none;
         M = fmaxf(t0.x, t1.x);
         auto rel = [&](float r) { return r == M ? 1.0f : ex2(r - M); };
         f_own[0] = rel(t0.x);
@@ -534,57 +543,90 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           L = fmaf(t1.y, f_own[1], L);
         }
       }
+      if (!kPair) meet();  // the statistics have been read: rows are staged there
       const bool split_up = n < u.tiles;
       if (ok && !idle) {
+        // Rows pass through the queries' place, 32 of a warp at a time, so that they are written in pieces of up to 128 bytes: a thread
+        // that wrote its own row took 4 us for what now takes one.
         constexpr int kOut = kPair ? D : D / 2;  // dimensions of a thread
-        const float f = L == 0.0f ? 0.0f : 1.0f / L;  // L = 0: the row sees nothing
-        const int64_t to = split_up ? ((int64_t)p.slot * S::kRows + ru) * D : ((int64_t)(tok0 + tok) * a.Hq + h) * D;
+        const float f = split_up || L == 0.0f ? (split_up ? 1.0f : 0.0f) : 1.0f / L;  // L = 0: the row sees nothing
         const bool fix = s_bad;
         const int d0 = kPair ? 0 : x * kOut;
+        const bool wide = sizeof(T) == 4 || split_up;  // fp32 rows
+        constexpr int kStage = std::min(S::kQBytes / 8, 4096);  // of a warp
+        const int size = wide ? 4 : 2, seg = min(kStage / 32, kOut * size), per = seg / size, chunks = seg / 16;
+        uint8_t* stage = q_smem + (warp - kPmFirstSoftmax) * kStage;
 #pragma unroll 1
-        for (int d = d0; d < d0 + kOut; d += 16) {
-          __syncwarp();
-          float o[16];
+        for (int ds = d0; ds < d0 + kOut; ds += per) {
+#pragma unroll 1
+          for (int d = ds; d < ds + per; d += 16) {
+            __syncwarp();
+            float o[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+            for (int e = 0; e < 16; ++e) o[e] = 0.0f;
 #pragma unroll
-          for (int y = 0; y < (kPair ? 1 : 2); ++y) {
-            const int gr = kPair ? x : y;
-            float t[16];
-            if (use[y]) {
-              tm_load(tl + S::kColO + gr * D + d, t);
+            for (int y = 0; y < (kPair ? 1 : 2); ++y) {
+              const int gr = kPair ? x : y;
+              float t[16];
+              if (use[y]) {
+                tm_load(tl + S::kColO + gr * D + d, t);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fmaf(t[e], f_own[y], o[e]);
+                for (int e = 0; e < 16; ++e) o[e] = fmaf(t[e], f_own[y], o[e]);
+              }
+              if (more[y]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = fmaf(scratch[((int64_t)gr * D + d + e) * 128], f_sum[y], o[e]);
+              }
             }
-            if (more[y]) {
+            if (fix && live) {  // values that are not finite, for the rows that see them
+              for (int j = 0; j < n; ++j) {
+                const int key0 = key_first + j * kPmKeys;
+                if (!partial(key0)) continue;
+                for (int key = max(key0, lo); key < min(key0 + kPmKeys, pos + 1); ++key) {
+                  const int id = a.table[(int64_t)u.s * a.width + (key >> a.shift)];
+                  if ((unsigned)id >= (unsigned)a.n_pages) continue;
+                  const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                      a.v + ((int64_t)p.g * a.ts + ((int64_t)id << a.shift) + (key & (a.page - 1))) * D + d);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fmaf(scratch[((int64_t)gr * D + d + e) * 128], f_sum[y], o[e]);
-            }
-          }
-          if (fix && live) {  // values that are not finite, for the rows that see them
-            for (int j = 0; j < n; ++j) {
-              const int key0 = key_first + j * kPmKeys;
-              if (!partial(key0)) continue;
-              for (int key = max(key0, lo); key < min(key0 + kPmKeys, pos + 1); ++key) {
-                const int id = a.table[(int64_t)u.s * a.width + (key >> a.shift)];
-                if ((unsigned)id >= (unsigned)a.n_pages) continue;
-                const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                    a.v + ((int64_t)p.g * a.ts + ((int64_t)id << a.shift) + (key & (a.page - 1))) * D + d);
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const uint32_t w = v[e / 2];
-                  if (!isfinite(low_f(w))) o[e] += low_f(w);
-                  if (!isfinite(high_f(w))) o[e + 1] += high_f(w);
+                  for (int e = 0; e < 16; e += 2) {
+                    const uint32_t w = v[e / 2];
+                    if (!isfinite(low_f(w))) o[e] += low_f(w);
+                    if (!isfinite(high_f(w))) o[e + 1] += high_f(w);
+                  }
                 }
               }
             }
+            const int c0 = (d - ds) * size / 16;  // 16-byte pieces, in an order that keeps a column of rows off one bank
+            auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * seg + ((c ^ (lane & (chunks - 1))) << 4)) = v; };
+            if (wide) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                put(c0 + e / 4, make_uint4(__float_as_uint(o[e] * f), __float_as_uint(o[e + 1] * f), __float_as_uint(o[e + 2] * f),
+                                           __float_as_uint(o[e + 3] * f)));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
+                put(c0 + e / 8, make_uint4(pack_rn(o[e] * f, o[e + 1] * f), pack_rn(o[e + 2] * f, o[e + 3] * f),
+                                           pack_rn(o[e + 4] * f, o[e + 5] * f), pack_rn(o[e + 6] * f, o[e + 7] * f)));
+            }
           }
-          if (live) {
-            if (split_up) store_row(a.part + to + d, o, 1.0f);
-            else store_row(static_cast<T*>(a.out) + to + d, o, f);
+          __syncwarp();
+          const int c = lane & (chunks - 1), step = 32 / chunks;
+#pragma unroll 2
+          for (int r = lane / chunks; r < 32; r += step) {
+            const int rr = ru - lane + r;
+            if (rr >= u.rows) break;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * seg + ((c ^ (r & (chunks - 1))) << 4));
+            if (split_up) {
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.part + ((int64_t)p.slot * S::kRows + rr) * D + ds) + c * 16) = v;
+            } else {
+              const int away = token_of(rr);
+              T* out = static_cast<T*>(a.out) + ((int64_t)(tok0 + away) * a.Hq + head0 + rr - away * a.G) * D + ds;
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(out) + c * 16) = v;
+            }
           }
         }
-        if (split_up && live && d0 == 0) a.ml[to / D] = make_float2(M, L);
+        if (split_up && live && d0 == 0) a.ml[(int64_t)p.slot * S::kRows + ru] = make_float2(M, L);
       }
       if (i == 32 * kPmFirstSoftmax && split_up && p.t0 == 0) {  // the first part of a unit: what the join has to know
         PaPiece part = p;
