@@ -150,13 +150,97 @@ struct PickShared {
   int wat[kPickThreads / 32];
 };
 
-// The K best of n items (key, place), in order, into out_key and out_at (shared; places -1 where there are fewer).
-// fetch(i) is item i's key; 0 is none. Items are dealt to the threads in turn.
+// An item that reaches the bound, into the list.
+__device__ __forceinline__ void collect(PickShared& s, bool in, uint64_t key, int at) {
+  const int lane = threadIdx.x & 31;
+  const unsigned who = __ballot_sync(0xffffffffu, in);
+  if (who == 0) return;
+  int to = 0;
+  if (lane == __ffs(who) - 1) to = atomicAdd(&s.n, __popc(who));
+  to = __shfl_sync(0xffffffffu, to, __ffs(who) - 1) + __popc(who & ((1u << lane) - 1));
+  if (in && to < kList) {
+    s.key[to] = key;
+    s.at[to] = at;
+  }
+}
+
+// The K best of the list, or, where it has overflowed, of all n items one after the other: (key, place), in order, into out_key and
+// out_at (shared; places -1 where there are fewer). fetch(i) is item i's key; 0 is none.
+template <typename F>
+__device__ void best(int n, int K, F fetch, PickShared& s, uint64_t* out_key, int* out_at) {
+  const int i = threadIdx.x, lane = i & 31;
+  if (i < K) {
+    out_key[i] = 0;
+    out_at[i] = -1;
+  }
+  __syncthreads();
+  const int m = s.n;
+  if (m <= kList) {  // every item's rank among those that reach the bound
+    for (int e = i; e < m; e += kPickThreads) {
+      const uint64_t k = s.key[e];
+      const int at = s.at[e];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < m; ++j) rank += before(s.key[j], s.at[j], k, at);
+      if (rank < K) {
+        out_key[rank] = k;
+        out_at[rank] = at;
+      }
+    }
+    __syncthreads();
+    return;
+  }
+  // Too many alike (a row of equal logits).
+  uint64_t last = ~0ull;
+  int last_at = -1;
+  for (int r = 0; r < K; ++r) {
+    uint64_t top = 0;
+    int at = INT32_MAX;
+    for (int e = i; e < n; e += kPickThreads) {
+      const uint64_t k = fetch(e);
+      if (k != 0 && before(last, last_at, k, e) && before(k, e, top, at)) {
+        top = k;
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+      const uint64_t k = __shfl_xor_sync(0xffffffffu, top, d);
+      const int o = __shfl_xor_sync(0xffffffffu, at, d);
+      if (before(k, o, top, at)) {
+        top = k;
+        at = o;
+      }
+    }
+    __syncthreads();
+    if (lane == 0) {
+      s.wkey[i >> 5] = top;
+      s.wat[i >> 5] = at;
+    }
+    __syncthreads();
+    for (int w = 0; w < kPickThreads / 32; ++w)
+      if (w == 0 || before(s.wkey[w], s.wat[w], top, at)) {
+        top = s.wkey[w];
+        at = s.wat[w];
+      }
+    if (top == 0) break;
+    if (i == 0) {
+      out_key[r] = top;
+      out_at[r] = at;
+    }
+    last = top;
+    last_at = at;
+  }
+  __syncthreads();
+}
+
+// The K best of n items, dealt to the threads in turn.
 template <typename F>
 __device__ void pick(int n, int K, F fetch, PickShared& s, uint64_t* out_key, int* out_at) {
-  const int i = threadIdx.x, lane = i & 31;
+  const int i = threadIdx.x;
   // The K-th best of the sets' maxima is a bound that K items reach.
   uint64_t mine = 0;
+#pragma unroll 4
   for (int e = i; e < n; e += kPickThreads) mine = max(mine, fetch(e));
 #pragma unroll
   for (int d = 1; d < kPickThreads / kGroups; d *= 2) mine = shfl_max(mine, d);
@@ -164,10 +248,6 @@ __device__ void pick(int n, int K, F fetch, PickShared& s, uint64_t* out_key, in
   if (i == 0) {
     s.bound = 0;
     s.n = 0;
-  }
-  if (i < K) {
-    out_key[i] = 0;
-    out_at[i] = -1;
   }
   __syncthreads();
   if (i < kGroups) {
@@ -179,78 +259,13 @@ __device__ void pick(int n, int K, F fetch, PickShared& s, uint64_t* out_key, in
   }
   __syncthreads();
   const uint64_t bound = s.bound > 0 ? s.bound : 1;
+#pragma unroll 4
   for (int e0 = 0; e0 < n; e0 += kPickThreads) {
     const int e = e0 + i;
     const uint64_t k = e < n ? fetch(e) : 0;
-    const bool in = k >= bound;
-    const unsigned who = __ballot_sync(0xffffffffu, in);
-    if (who == 0) continue;
-    int at = 0;
-    if (lane == __ffs(who) - 1) at = atomicAdd(&s.n, __popc(who));
-    at = __shfl_sync(0xffffffffu, at, __ffs(who) - 1) + __popc(who & ((1u << lane) - 1));
-    if (in && at < kList) {
-      s.key[at] = k;
-      s.at[at] = e;
-    }
+    collect(s, k >= bound, k, e);
   }
-  __syncthreads();
-  const int m = s.n;
-  if (m <= kList) {  // every item's rank among those that reach the bound
-    for (int e = i; e < m; e += kPickThreads) {
-      const uint64_t k = s.key[e];
-      const int at = s.at[e];
-      int rank = 0;
-      for (int j = 0; j < m; ++j) rank += before(s.key[j], s.at[j], k, at);
-      if (rank < K) {
-        out_key[rank] = k;
-        out_at[rank] = at;
-      }
-    }
-    __syncthreads();
-    return;
-  }
-  // Too many alike (a row of equal logits): one after the other.
-  uint64_t last = ~0ull;
-  int last_at = -1;
-  for (int r = 0; r < K; ++r) {
-    uint64_t best = 0;
-    int at = INT32_MAX;
-    for (int e = i; e < n; e += kPickThreads) {
-      const uint64_t k = fetch(e);
-      if (k != 0 && before(last, last_at, k, e) && before(k, e, best, at)) {
-        best = k;
-        at = e;
-      }
-    }
-#pragma unroll
-    for (int d = 16; d; d /= 2) {
-      const uint64_t k = __shfl_xor_sync(0xffffffffu, best, d);
-      const int o = __shfl_xor_sync(0xffffffffu, at, d);
-      if (before(k, o, best, at)) {
-        best = k;
-        at = o;
-      }
-    }
-    __syncthreads();
-    if (lane == 0) {
-      s.wkey[i >> 5] = best;
-      s.wat[i >> 5] = at;
-    }
-    __syncthreads();
-    for (int w = 0; w < kPickThreads / 32; ++w)
-      if (w == 0 || before(s.wkey[w], s.wat[w], best, at)) {
-        best = s.wkey[w];
-        at = s.wat[w];
-      }
-    if (best == 0) break;
-    if (i == 0) {
-      out_key[r] = best;
-      out_at[r] = at;
-    }
-    last = best;
-    last_at = at;
-  }
-  __syncthreads();
+  best(n, K, fetch, s, out_key, out_at);
 }
 
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs a) {
@@ -273,17 +288,24 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
       M = 0.0f;
       S = 1.0f;
     } else {
-      for (int j = lane; j < a.nchunks; j += 32) {
-        const float m = __ldcg(c + j).x;
-        s_max[w * a.nchunks + j] = m;
-        M = fmaxf(M, m);
+      constexpr int kMost = kChunksMax / 32;
+      float2 y[kMost];  // all asked for at once
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        const int j = k * 32 + lane;
+        y[k] = j < a.nchunks ? __ldcg(c + j) : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < kMost; ++k) {
+        const int j = k * 32 + lane;
+        if (j < a.nchunks) s_max[w * a.nchunks + j] = y[k].x;
+        M = fmaxf(M, y[k].x);
       }
 #pragma unroll
       for (int d = 16; d; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      for (int j = lane; j < a.nchunks; j += 32) {
-        const float2 y = __ldcg(c + j);
-        if (y.x > -INFINITY) S += y.y * expf(y.x - M);
-      }
+#pragma unroll
+      for (int k = 0; k < kMost; ++k)
+        if (y[k].x > -INFINITY) S += y[k].y * expf(y[k].x - M);
 #pragma unroll
       for (int d = 16; d; d /= 2) S += __shfl_xor_sync(0xffffffffu, S, d);
     }
@@ -304,7 +326,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
   __syncthreads();
   const int nch = a.nchunks;
   pick(a.W * nch, a.K, [&](int e) { return key_of(s_row[e / nch], s_max[e]); }, s, s_key[0], s_at[0]);
-  // The elements of the chosen chunks, in the order of the chunks' places so that ties keep theirs.
+  // The elements of the chosen chunks, in the order of the chunks' places so that ties keep theirs. The K-th chunk's maximum is a bound
+  // that K elements reach.
+  const uint64_t bound = s_key[0][a.K - 1] > 0 ? s_key[0][a.K - 1] : 1;
+  if (i == 0) s.n = 0;
   if (i < a.K) {
     const int at = s_at[0][i];
     int rank = 0;
@@ -321,7 +346,29 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
     if (s_done[w]) return v == a.eos ? key_of(s_row[w], 0.0f) : 0;
     return key_of(s_row[w], __ldcg(a.logits + (int64_t)(row0 + w) * a.V + v));
   };
-  pick(a.K * chunk, a.K, element, s, s_key[0], s_at[0]);
+  // a warp per 512 elements, all of them asked for at once
+  for (int e0 = warp * kChunkMin; e0 < a.K * chunk; e0 += kPickThreads / 32 * kChunkMin) {
+    const int place = s_at[1][e0 / chunk];
+    if (place < 0) continue;
+    const int w = place / nch, v0 = (place - w * nch) * chunk + e0 % chunk;
+    const RowKey row = s_row[w];
+    if (s_done[w]) {
+      const int e = a.eos - v0;  // its one continuation
+      collect(s, lane == 0 && e >= 0 && e < kChunkMin && key_of(row, 0.0f) >= bound, key_of(row, 0.0f), e0 + e);
+      continue;
+    }
+    const float* x = a.logits + (int64_t)(row0 + w) * a.V + v0;
+    float y[kChunkMin / 32];
+#pragma unroll
+    for (int k = 0; k < kChunkMin / 32; ++k) y[k] = v0 + k * 32 + lane < a.V ? __ldcg(x + k * 32 + lane) : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kChunkMin / 32; ++k) {
+      const uint64_t key = key_of(row, y[k]);
+      collect(s, key >= bound, key, e0 + k * 32 + lane);
+    }
+  }
+  __syncthreads();
+  best(a.K * chunk, a.K, element, s, s_key[0], s_at[0]);
   if (i < a.K) {
     const int e = s_at[0][i];
     const int64_t to = (int64_t)blockIdx.x * a.K + i;

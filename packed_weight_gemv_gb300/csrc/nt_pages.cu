@@ -87,7 +87,26 @@ __global__ void __launch_bounds__(kPageThreads) page_extend_kernel(const ExtendA
   __shared__ int s_bad;
   dependent_launch_wait();
   const int i = threadIdx.x;
+  // free pages among eight
+  auto look = [&](int p0, int (&c)[kPerThread]) {
+    int n = 0;
+    if (p0 + kPerThread <= a.n_pages && a.wide) {
+#pragma unroll
+      for (int k = 0; k < kPerThread; k += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(a.refs + p0 + k);
+        c[k] = v.x; c[k + 1] = v.y; c[k + 2] = v.z; c[k + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPerThread; ++k) c[k] = p0 + k < a.n_pages ? a.refs[p0 + k] : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) n += c[k] == 0;
+    return n;
+  };
   if (i == 0) s_bad = 0;
+  int c[kPerThread];
+  const int early = look(i * kPerThread, c);  // asked for before anything is known of the demand
   for (int s = i; s <= a.S; s += kPageThreads) first[s] = min(max(a.q_start[s], 0), a.T);
   __syncthreads();
   const int most = (int)min((int64_t)a.width * a.page, (int64_t)INT32_MAX);
@@ -114,7 +133,8 @@ __global__ void __launch_bounds__(kPageThreads) page_extend_kernel(const ExtendA
       if (page >= 0) {
         int left = a.refs[page];
         if (left > 1) {
-          for (int t = 0; t < s && left > 1; ++t) left -= hold[t] == page;
+#pragma unroll 8
+          for (int t = 0; t < s; ++t) left -= hold[t] == page;
           if (left > 1) d |= 1 << 30;
         }
       }
@@ -129,28 +149,11 @@ __global__ void __launch_bounds__(kPageThreads) page_extend_kernel(const ExtendA
   __syncthreads();
   const int demand = carry;
   auto sum = [&](int s) { return s < 0 ? 0 : upto[s] & INT32_MAX; };
-  // free pages, as many as are wanted
-  auto look = [&](int p0, int (&c)[kPerThread]) {
-    int n = 0;
-    if (p0 + kPerThread <= a.n_pages && a.wide) {
-#pragma unroll
-      for (int k = 0; k < kPerThread; k += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(a.refs + p0 + k);
-        c[k] = v.x; c[k + 1] = v.y; c[k + 2] = v.z; c[k + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kPerThread; ++k) c[k] = p0 + k < a.n_pages ? a.refs[p0 + k] : 1;
-    }
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) n += c[k] == 0;
-    return n;
-  };
   const int step = kPageThreads * kPerThread;
-  int have = 0;
+  int have = 0, before = 0;
   for (int p0 = 0; p0 < a.n_pages && have < demand; p0 += step) {
-    int c[kPerThread], total;
-    block_scan(look(p0 + i * kPerThread, c), s_warps, &total);
+    int total;
+    before = block_scan(p0 == 0 ? early : look(p0 + i * kPerThread, c), s_warps, &total);
     have += total;
   }
   // sequences whose demand, with those before, is not met are left as they were
@@ -163,9 +166,10 @@ __global__ void __launch_bounds__(kPageThreads) page_extend_kernel(const ExtendA
   const int give = sum(served - 1);
   int given = 0;
   for (int p0 = 0; p0 < a.n_pages && given < give; p0 += step) {
-    int c[kPerThread], total;
-    const int at = p0 + i * kPerThread, n = look(at, c);
-    int f = given + block_scan(n, s_warps, &total);
+    int total = have;
+    const int at = p0 + i * kPerThread;
+    int f = before;  // as found above, where one round holds all
+    if (a.n_pages > step) f = given + block_scan(look(at, c), s_warps, &total);
     for (int k = 0; k < kPerThread && f < give; ++k) {
       if (c[k] != 0) continue;
       int s = 0;  // the sequence whose share holds number f
@@ -213,18 +217,18 @@ __global__ void __launch_bounds__(kPageThreads) page_extend_kernel(const ExtendA
   if (i == 0 && s_bad) atomicAdd(a.n_bad, (uint32_t)s_bad);
 }
 
-// Copies of pages: the pairs that are there, then every CTA a share of their pieces of up to 4 KB (256 threads x 16 bytes): a
-// page of one head stands in one piece of memory. Four of them are loaded before any is stored.
+// Copies of pages: the pairs that are there, then every CTA some of them for one job (layer, keys or values, head) after another, in
+// rounds of 256 threads x 16 bytes, eight pages' loaded before any is stored: a page of one head stands in one piece of memory.
 __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ CopyArgs a) {
   __shared__ int2 s_pair[kCopyPairs];
   __shared__ int s_count[8];
   dependent_launch_wait();
   const int i = threadIdx.x;
-  const unsigned vecs = a.page * a.D / 8, subs = (vecs + 255) / 256;  // 16-byte pieces of a page of one head; rounds of the threads
-  for (int p0 = 0; p0 < a.n; p0 += a.batch) {
+  const int vecs = a.page * a.D / 8;  // 16-byte pieces of a page of one head
+  for (int p0 = 0; p0 < a.n; p0 += kCopyPairs) {
     // in their order: every CTA has the same list
     int n = 0;
-    const int end = min(a.n, p0 + a.batch);
+    const int end = min(a.n, p0 + kCopyPairs);
     for (int p1 = p0; p1 < end; p1 += 256) {
       const int p = p1 + i;
       const int from = p < end ? a.pairs[2 * p] : -1, to = p < end ? a.pairs[2 * p + 1] : -1;
@@ -242,25 +246,21 @@ __global__ void __launch_bounds__(256) page_copy_kernel(const __grid_constant__ 
       if (there) s_pair[at] = make_int2(from, to);
     }
     __syncthreads();
-    const unsigned all = (unsigned)n * a.jobs * subs;
-    constexpr unsigned kAtOnce = 4;
-    for (unsigned u0 = blockIdx.x * kAtOnce; u0 < all; u0 += gridDim.x * kAtOnce) {
-      uint4 v[kAtOnce];
-      uint4* to[kAtOnce];
+    constexpr int kAtOnce = 8;
+    for (int job = blockIdx.x % a.jobs; job < a.jobs; job += gridDim.x) {  // (one, unless there are more jobs than CTAs)
+      const int lv = job / a.Hkv, h = job - lv * a.Hkv;
+      uint4* base = reinterpret_cast<uint4*>(((lv & 1) ? a.vc[lv >> 1] : a.kc[lv >> 1]) + (int64_t)h * a.ts * a.D);
+      for (int p = blockIdx.x / a.jobs; p < n; p += a.shares * kAtOnce) {
+        for (int e = i; e < vecs; e += 256) {
+          uint4 v[kAtOnce];
 #pragma unroll
-      for (unsigned k = 0; k < kAtOnce; ++k) {
-        const unsigned u = u0 + k, piece = u / subs, e = (u - piece * subs) * 256 + i;
-        to[k] = nullptr;
-        if (u >= all || e >= vecs) continue;
-        const unsigned at = piece / a.jobs, job = piece - at * a.jobs, lv = job / a.Hkv, h = job - lv * a.Hkv;
-        const int2 pair = s_pair[at];
-        uint4* base = reinterpret_cast<uint4*>(((lv & 1) ? a.vc[lv >> 1] : a.kc[lv >> 1]) + (int64_t)h * a.ts * a.D);
-        v[k] = base[(int64_t)pair.x * vecs + e];
-        to[k] = base + (int64_t)pair.y * vecs + e;
+          for (int k = 0; k < kAtOnce; ++k)
+            if (p + k * a.shares < n) v[k] = base[(int64_t)s_pair[p + k * a.shares].x * vecs + e];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k)
+            if (p + k * a.shares < n) base[(int64_t)s_pair[p + k * a.shares].y * vecs + e] = v[k];
+        }
       }
-#pragma unroll
-      for (unsigned k = 0; k < kAtOnce; ++k)
-        if (to[k]) *to[k] = v[k];
     }
   }
 }
@@ -398,11 +398,10 @@ nt_status nt_page_copy(uint16_t* const* k_caches, uint16_t* const* v_caches, int
     a.ts = t_stride;
     a.page = page;
     a.n_pages = t_stride / page;
-    const int64_t per = (int64_t)a.jobs * ((page * D / 8 + 255) / 256);  // pieces of a pair: at most 2^29
-    a.batch = (int)std::min<int64_t>(kCopyPairs, INT32_MAX / per);
-    const int64_t most = ((int64_t)n * per + 3) / 4;
-    NT_CUDA_TRY(launch_kernel(page_copy_kernel, dim3((unsigned)std::min<int64_t>(most, 4 * device_sm_count())), dim3(256), 0,
-                              reinterpret_cast<cudaStream_t>(stream), true, a));
+    // CTAs that fill the GPU, but no more shares of the pairs than there are
+    a.shares = std::max(1, std::min(n, (6 * device_sm_count() + a.jobs - 1) / a.jobs));
+    const int64_t ctas = std::min<int64_t>((int64_t)a.jobs * a.shares, 1 << 20);
+    NT_CUDA_TRY(launch_kernel(page_copy_kernel, dim3((unsigned)ctas), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, a));
   }
   return check_launch("page_copy_kernel");
 }

@@ -40,7 +40,7 @@ struct CopyArgs {
   uint16_t* kc[128];
   uint16_t* vc[128];
   const int32_t* pairs;
-  int n, batch, jobs, Hkv, D, ts, page, n_pages;  // batch: pairs at a time
+  int n, shares, jobs, Hkv, D, ts, page, n_pages;  // shares: CTAs of a job
 };
 struct CompactArgs {
   int32_t *refs, *table;
