@@ -37,24 +37,33 @@ struct BeamArgs {
   int32_t* done_out;     // or null
   float2* chunks;        // [N][nchunks] (maximum, sum)
   double* scale;         // [N] 1 / len^alpha
-  int V, W, K, chunk, nchunks, eos, wide;
+  int N, V, W, K, chunk, nchunks, eos, wide;
   double alpha;
 };
 
 __device__ __forceinline__ bool row_done(const BeamArgs& a, int row) { return a.done && a.done[row] != 0; }
 
+// e^x for x <= 0 (e^-inf = 0): log2(e) in two parts, as one part's error would be that of every term alike.
+__device__ __forceinline__ float weight(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, 1.44269502e+0f, x * 1.92596299e-8f)));
+  return y;
+}
+
 // A warp per chunk.
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamArgs a, int64_t jobs) {
   dependent_launch_wait();
+  // 1 / len^alpha of 32 rows by the first warp of each of the first CTAs: 64-bit operations take an SM 16 cycles a warp, however few
+  // of its lanes want them.
+  const int own = blockIdx.x * 32 + threadIdx.x;
+  if (a.alpha != 0.0 && threadIdx.x < 32 && own < a.N) {
+    const bool ended = row_done(a, own);
+    a.scale[own] = 1.0 / pow((double)max(a.lens[own], ended ? 1 : 0) + (ended ? 0.0 : 1.0), a.alpha);
+  }
   const int64_t job = (int64_t)blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);
   if (job >= jobs) return;
   const int lane = threadIdx.x & 31, row = (int)(job / a.nchunks), c = (int)(job - (int64_t)row * a.nchunks);
   const bool done = row_done(a, row);
-  if (c == 0 && lane == 0) {
-    double s = 1.0;
-    if (a.alpha != 0.0 && a.lens) s = 1.0 / pow((double)max(a.lens[row], done ? 1 : 0) + (done ? 0.0 : 1.0), a.alpha);
-    a.scale[row] = s;
-  }
   if (done) return;  // it has one continuation, which is known
   const float* x = a.logits + (int64_t)row * a.V;
   const int v0 = c * a.chunk, v1 = min(a.V, v0 + a.chunk);
@@ -69,25 +78,27 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamArgs 
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {  // the same elements to a lane as above
-        const int e = v + (k / 4) * 128 + lane * 4 + (k & 3);
-        y[k] = e < v1 ? x[e] : -INFINITY;
-      }
+      for (int k = 0; k < 16; ++k) y[k] = v + k * 32 + lane < v1 ? __ldcs(x + v + k * 32 + lane) : -INFINITY;
     }
     float mx = m;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) mx = fmaxf(mx, y[k]);  // NaN is left out
+    for (int k = 0; k < 16; ++k) {
+      y[k] = fmaxf(y[k], -INFINITY);  // NaN counts as -inf
+      mx = fmaxf(mx, y[k]);
+    }
     if (mx > -INFINITY) {
-      sum = m > -INFINITY ? sum * expf(m - mx) : 0.0f;
+      sum *= weight(m - mx);
+      float more[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < 16; ++k) sum += y[k] > -INFINITY ? expf(y[k] - mx) : 0.0f;
+      for (int k = 0; k < 16; ++k) more[k & 3] += weight(y[k] - mx);
+      sum += (more[0] + more[1]) + (more[2] + more[3]);
     }
     m = mx;
   }
   float M = m;
 #pragma unroll
   for (int d = 16; d; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  sum = m > -INFINITY ? sum * expf(m - M) : 0.0f;
+  sum = m > -INFINITY ? sum * weight(m - M) : 0.0f;
 #pragma unroll
   for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) a.chunks[job] = make_float2(M, sum);
@@ -98,6 +109,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 // What a row adds to its logits, and the factor that ranks it: pairs of fp32.
 struct RowKey {
   float add_hi, add_lo, mul_hi, mul_lo;  // add_hi NaN: the row has no continuation
@@ -240,7 +252,7 @@ __device__ void pick(int n, int K, F fetch, PickShared& s, uint64_t* out_key, in
   const int i = threadIdx.x;
   // The K-th best of the sets' maxima is a bound that K items reach.
   uint64_t mine = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int e = i; e < n; e += kPickThreads) mine = max(mine, fetch(e));
 #pragma unroll
   for (int d = 1; d < kPickThreads / kGroups; d *= 2) mine = shfl_max(mine, d);
@@ -259,7 +271,7 @@ __device__ void pick(int n, int K, F fetch, PickShared& s, uint64_t* out_key, in
   }
   __syncthreads();
   const uint64_t bound = s.bound > 0 ? s.bound : 1;
-#pragma unroll 4
+#pragma unroll 1
   for (int e0 = 0; e0 < n; e0 += kPickThreads) {
     const int e = e0 + i;
     const uint64_t k = e < n ? fetch(e) : 0;
@@ -310,18 +322,28 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
       for (int d = 16; d; d /= 2) S += __shfl_xor_sync(0xffffffffu, S, d);
     }
     if (lane == 0) {
-      const float sc = a.scores[row];
-      const double add = done ? (double)sc : ((double)sc - (double)M) - log((double)S), mul = a.scale[row];
-      RowKey r;
-      r.add_hi = (float)add;
-      r.add_lo = (float)(add - (double)r.add_hi);
-      r.mul_hi = (float)mul;
-      r.mul_lo = (float)(mul - (double)r.mul_hi);
-      // no finite score, nothing above -inf, or a logit of +inf: no continuation
-      if (!isfinite(sc) || !isfinite(M) || !isfinite(r.add_hi) || !(isfinite(r.mul_hi) && r.mul_hi > 0.0f)) r.add_hi = NAN;
-      s_row[w] = r;
+      s_row[w].add_hi = M;
+      s_row[w].add_lo = S;
       s_done[w] = done;
     }
+  }
+  __syncthreads();
+  if (i < a.W) {  // a lane per row: see above
+    const float sc = a.scores[row0 + i], M = s_row[i].add_hi, S = s_row[i].add_lo;
+    const double add = s_done[i] ? (double)sc : ((double)sc - (double)M) - log((double)S);
+    RowKey r;
+    r.add_hi = (float)add;
+    r.add_lo = (float)(add - (double)r.add_hi);
+    r.mul_hi = 1.0f;
+    r.mul_lo = 0.0f;
+    if (a.alpha != 0.0) {
+      const double mul = a.scale[row0 + i];
+      r.mul_hi = (float)mul;
+      r.mul_lo = (float)(mul - (double)r.mul_hi);
+    }
+    // no finite score, nothing above -inf, or a logit of +inf: no continuation
+    if (!isfinite(sc) || !isfinite(M) || !isfinite(r.add_hi) || !(isfinite(r.mul_hi) && r.mul_hi > 0.0f)) r.add_hi = NAN;
+    s_row[i] = r;
   }
   __syncthreads();
   const int nch = a.nchunks;
@@ -361,10 +383,21 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
     float y[kChunkMin / 32];
 #pragma unroll
     for (int k = 0; k < kChunkMin / 32; ++k) y[k] = v0 + k * 32 + lane < a.V ? __ldcg(x + k * 32 + lane) : -INFINITY;
+    // What is below the bound by more than fp32 can err is left out (few stay), the others' keys are formed.
+    const float level = unordered((uint32_t)(bound >> 32)) / row.mul_hi, least = level - row.add_hi - 1e-5f * (fabsf(level) + fabsf(row.add_hi));
+    unsigned may = 0;
 #pragma unroll
-    for (int k = 0; k < kChunkMin / 32; ++k) {
-      const uint64_t key = key_of(row, y[k]);
+    for (int k = 0; k < kChunkMin / 32; ++k) may |= (y[k] > -INFINITY && !(y[k] < least) ? 1u : 0u) << k;
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, may != 0)) {
+      const int k = __ffs(may) - 1;
+      float z = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kChunkMin / 32; ++j)
+        if (j == k) z = y[j];
+      const uint64_t key = key_of(row, z);
       collect(s, key >= bound, key, e0 + k * 32 + lane);
+      may &= may - 1;
     }
   }
   __syncthreads();
@@ -438,6 +471,7 @@ nt_status nt_beam_select(const float* logits, const float* scores, int N, int W,
   a.token = token;
   a.score = score;
   a.done_out = done_out_opt;
+  a.N = N;
   a.V = V;
   a.W = W;
   a.K = K;
@@ -450,8 +484,8 @@ nt_status nt_beam_select(const float* logits, const float* scores, int N, int W,
   a.wide = V % 4 == 0 && aligned(logits, 16);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t jobs = (int64_t)N * a.nchunks;
-  NT_CUDA_TRY(launch_kernel(beam_scan_kernel, dim3((unsigned)((jobs + kScanThreads / 32 - 1) / (kScanThreads / 32))), dim3(kScanThreads),
-                            0, st, true, a, jobs));
+  const int64_t ctas = std::max<int64_t>((jobs + kScanThreads / 32 - 1) / (kScanThreads / 32), (N + 31) / 32);
+  NT_CUDA_TRY(launch_kernel(beam_scan_kernel, dim3((unsigned)ctas), dim3(kScanThreads), 0, st, true, a, jobs));
   NT_TRY(check_launch("beam_scan_kernel"));
   static std::atomic<int> allowed[64];
   const int smem = W * a.nchunks * (int)sizeof(float);
