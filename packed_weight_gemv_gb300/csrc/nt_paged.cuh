@@ -115,7 +115,7 @@ __device__ __forceinline__ int64_t pa_scan(int64_t x, int64_t* warps, int64_t* t
   return before + y - x;
 }
 
-__device__ __forceinline__ int64_t pa_div(int64_t x, int64_t y) {  // x >= 0, y > 0
+__host__ __device__ inline int64_t pa_div(int64_t x, int64_t y) {  // x >= 0, y > 0
   return (x | y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
@@ -126,21 +126,22 @@ template <int kStart>
 struct PaCut {
   int64_t work, base, near;
   int ctas, rem;
-  __device__ __forceinline__ void set(int64_t all, int grid, int most) {
+  __host__ __device__ inline void set(int64_t all, int grid, int most) {
     work = all;
-    ctas = (int)min((int64_t)grid, all);
+    ctas = (int)(all < grid ? all : (int64_t)grid);
     base = ctas ? pa_div(all, ctas) : 0;
     rem = (int)(all - base * ctas);
-    near = max((int64_t)1, min((int64_t)most, base / 2));
+    near = base / 2 < most ? base / 2 : most;
+    if (near < 1) near = 1;
   }
-  __device__ __forceinline__ int64_t from(int c) const { return base * c + min(c, rem); }
+  __host__ __device__ inline int64_t from(int c) const { return base * c + (c < rem ? c : rem); }
   // The first CTA whose share begins at y or behind.
-  __device__ __forceinline__ int first_from(int64_t y) const {
+  __host__ __device__ inline int first_from(int64_t y) const {
     const int64_t big = (base + 1) * rem;
     return (int)(y <= big ? pa_div(y + base, base + 1) : rem + pa_div(y - big + base - 1, base));
   }
   // The end x of a share among the work [off, off + w) of a unit and head.
-  __device__ __forceinline__ int64_t snap(int64_t x, int64_t off, int64_t w) const {
+  __host__ __device__ inline int64_t snap(int64_t x, int64_t off, int64_t w) const {
     const int64_t lo = off + kStart + near, hi = off + w - near;
     if (lo > hi) return x - off < off + w - x ? off : off + w;
     return x < lo ? off : x > hi ? off + w : x;
