@@ -570,6 +570,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         constexpr int kStage = std::min(S::kQBytes / 8, 4096);  // of a warp
         const int size = wide ? 4 : 2, seg = min(kStage / 32, kOut * size), per = seg / size, chunks = seg / 16;
         uint8_t* stage = q_smem + (warp - kPmFirstSoftmax) * kStage;
+        // where this thread's row goes; the lanes that write it ask for it
+        uint8_t* own = split_up ? reinterpret_cast<uint8_t*>(a.part + ((int64_t)p.slot * S::kRows + ru) * D)
+                                : reinterpret_cast<uint8_t*>(static_cast<T*>(a.out) + ((int64_t)(tok0 + tok) * a.Hq + h) * D);
+        const int left = u.rows - (ru - lane);  // live rows of the warp
 #pragma unroll 1
         for (int ds = d0; ds < d0 + kOut; ds += per) {
 #pragma unroll 1
@@ -593,9 +597,11 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
               }
             }
             if (fix && live) {  // values that are not finite, for the rows that see them
+#pragma unroll 1
               for (int j = 0; j < n; ++j) {
                 const int key0 = key_first + j * kPmKeys;
                 if (!partial(key0)) continue;
+#pragma unroll 1
                 for (int key = max(key0, lo); key < min(key0 + kPmKeys, pos + 1); ++key) {
                   const int id = a.table[(int64_t)u.s * a.width + (key >> a.shift)];
                   if ((unsigned)id >= (unsigned)a.n_pages) continue;
@@ -626,18 +632,13 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           }
           __syncwarp();
           const int c = lane & (chunks - 1), step = 32 / chunks;
-#pragma unroll 2
-          for (int r = lane / chunks; r < 32; r += step) {
-            const int rr = ru - lane + r;
-            if (rr >= u.rows) break;
+          uint8_t* at = own + ds * size;
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += step) {
+            const int r = r0 + lane / chunks;
             const uint4 v = *reinterpret_cast<const uint4*>(stage + r * seg + ((c ^ (r & (chunks - 1))) << 4));
-            if (split_up) {
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.part + ((int64_t)p.slot * S::kRows + rr) * D + ds) + c * 16) = v;
-            } else {
-              const int away = token_of(rr);
-              T* out = static_cast<T*>(a.out) + ((int64_t)(tok0 + away) * a.Hq + head0 + rr - away * a.G) * D + ds;
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(out) + c * 16) = v;
-            }
+            uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), r));
+            if (r < left) *reinterpret_cast<uint4*>(to + c * 16) = v;
           }
         }
         if (split_up && live && d0 == 0) a.ml[(int64_t)p.slot * S::kRows + ru] = make_float2(M, L);
@@ -667,65 +668,59 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
   if (*fail && i == 0 && atomicCAS(a.err, 0u, kTaErrWait) == 0u) a.err[1] = blockIdx.x;
 }
 
-// Joins the parts of the units that were split: CTA b takes a sixteenth of the rows of the unit whose first part is CTA b / 16's; a
-// warp per row, four (D 64: two) dimensions a lane, eight parts asked for at a time.
-constexpr int kPmJoin = 16;
+// Joins the parts of the units that were split: a warp per row, four (D 64: two) dimensions a lane. Statistics come first, a part to a
+// lane, so that nothing waits between the parts themselves (a warp with two rows and running statistics took 15 us for 128 rows of
+// 19 parts).
 template <typename T, int D, int kRows>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PaArgs a) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kBlocks = kRows / 4;
   using V = typename std::conditional<E == 4, float4, float2>::type;
   dependent_launch_wait();
-  const int c0 = blockIdx.x / kPmJoin, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x / kBlocks, lane = threadIdx.x & 31, r = blockIdx.x % kBlocks * 4 + (threadIdx.x >> 5);
   const PaJoin job = a.join[c0];
-  const float inv_g = 1.0f / (float)a.G;
-  constexpr int kPmKeys = kRows / kPmJoin;
-  const int first = (blockIdx.x % kPmJoin) * kPmKeys;
-  for (int r = first + (threadIdx.x >> 5); r < min(first + kPmKeys, job.rows); r += 4) {
-    float m = -INFINITY, l = 0.0f, o[E];
+  if (r >= job.rows) return;
+  const V* part = reinterpret_cast<const V*>(a.part + (int64_t)r * D) + lane;
+  auto place = [&](int c) { return (int64_t)(2 * c + (c == c0)) * kRows; };
+  float M = -INFINITY, L = 0.0f, o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int b0 = c0; b0 <= job.last; b0 += 8) {
-      V y[8];
-      float2 ml[8];
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 1
+  for (int b0 = c0; b0 <= job.last; b0 += 32) {  // 32 parts at a time
+    const float2 ml = b0 + lane <= job.last ? __ldcg(a.ml + place(b0 + lane) + r) : make_float2(-INFINITY, 0.0f);
+    float to = ml.x;
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const int c = min(b0 + b, job.last);
-        const int64_t from = (int64_t)(2 * c + (c == c0)) * kRows + r;
-        y[b] = __ldcg(reinterpret_cast<const V*>(a.part + from * D) + lane);
-        ml[b] = __ldcg(a.ml + from);
-        if (b0 + b > job.last) ml[b] = make_float2(-INFINITY, 0.0f);
-      }
-      float to = m;
+    for (int d = 16; d; d /= 2) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+    to = fmaxf(to, M);
+    const float corr = M == to ? 1.0f : ex2(M - to), mine = ml.x == to ? 1.0f : ex2(ml.x - to);
+    float sum = ml.y * mine;
 #pragma unroll
-      for (int b = 0; b < 8; ++b) to = fmaxf(to, ml[b].x);
-      const float corr = m == to ? 1.0f : ex2(m - to);
-      l *= corr;
-      m = to;
+    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    L = fmaf(L, corr, sum);
+    M = to;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= corr;
+    for (int e = 0; e < E; ++e) o[e] *= corr;
+    const int n = min(32, job.last - b0 + 1);
+#pragma unroll 8
+    for (int b = 0; b < n; ++b) {
+      const V y = __ldcg(part + place(b0 + b) * (D / E));
+      const float g = __shfl_sync(0xffffffffu, mine, b);
+      const float* ye = reinterpret_cast<const float*>(&y);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (b0 + b > job.last) break;
-        const float g = ml[b].x == m ? 1.0f : ex2(ml[b].x - m);
-        const float* ye = reinterpret_cast<const float*>(&y[b]);
-        l = fmaf(ml[b].y, g, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(ye[e], g, o[e]);
-      }
+      for (int e = 0; e < E; ++e) o[e] = fmaf(ye[e], g, o[e]);
     }
-    const float g = l == 0.0f ? 0.0f : 1.0f / l;
-    const int away = node_of(job.rest + r, inv_g);
-    T* out = static_cast<T*>(a.out) + ((int64_t)(job.tok0 + away) * a.Hq + job.head0 + r - away * a.G) * D + lane * E;
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (E == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * g, o[1] * g, o[2] * g, o[3] * g);
-      else *reinterpret_cast<float2*>(out) = make_float2(o[0] * g, o[1] * g);
-    } else {
-      uint32_t w[E / 2];
+  }
+  const float g = L == 0.0f ? 0.0f : 1.0f / L;
+  const int away = node_of(job.rest + r, 1.0f / (float)a.G);
+  T* out = static_cast<T*>(a.out) + ((int64_t)(job.tok0 + away) * a.Hq + job.head0 + r - away * a.G) * D + lane * E;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (E == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * g, o[1] * g, o[2] * g, o[3] * g);
+    else *reinterpret_cast<float2*>(out) = make_float2(o[0] * g, o[1] * g);
+  } else {
+    uint32_t w[E / 2];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) w[e / 2] = pack_rn(o[e] * g, o[e + 1] * g);
-      if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(out) = w[0];
-    }
+    for (int e = 0; e < E; e += 2) w[e / 2] = pack_rn(o[e] * g, o[e + 1] * g);
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(out) = w[0];
   }
 }
 
@@ -738,7 +733,8 @@ nt_status launch_many(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
   const int ctas = std::min(device_sm_count(), kPaManyCtas);
   NT_CUDA_TRY(launch_kernel(paged_many_kernel<T, D, kPair, kExtra>, dim3((unsigned)ctas), dim3(kPmThreads), smem, st, true, maps, a));
   NT_TRY(check_launch("paged_many_kernel"));
-  NT_CUDA_TRY(launch_kernel(paged_join_kernel<T, D, PmShape<T, D, kPair>::kRows>, dim3((unsigned)(ctas * kPmJoin)), dim3(128), 0, st, true, a));
+  constexpr int kRows = PmShape<T, D, kPair>::kRows;
+  NT_CUDA_TRY(launch_kernel(paged_join_kernel<T, D, kRows>, dim3((unsigned)(ctas * (kRows / 4))), dim3(128), 0, st, true, a));
   return check_launch("paged_join_kernel");
 }
 template <typename T, int D, bool kPair>
