@@ -5,7 +5,8 @@
 //
 // Such a call is bound by reading keys and values once. Its products are few, so they run on mma.sync (m16n8k16, bf16, fp32 sums): it
 // takes 16 rows at least, which the terms of the values share: an fp32 query is three bf16 terms (nothing is lost) in rows of their own,
-// a weight two rounded ones (2^-17) in rows of their own, and the rows are summed behind. (On the fp32 units a block of 16
+// its weights three as well, or two rounded ones (2^-17) where eight rows leave no more room, and the rows are summed behind; weights of
+// bf16 queries are two terms. (On the fp32 units a block of 16
 // keys took 770 instructions, on eight warps of an SM 141 us for 64 sequences of 158,000 rows together.)
 //
 // A warp takes a block of 16 keys (D 64: 32) at a time: the scores come out of the MMAs in the places where the weights go in. The
@@ -65,6 +66,8 @@ struct FewShape {
   // Rows of an MMA: up to four query rows' three terms in rows 0-3, 4-7 and 8-11 of one; eight rows' in 0-7 and 8-15 of one and 0-7 of
   // another.
   static constexpr int kTiles = kF32 && R > 4 ? 2 : 1;
+  // Weights: rows 0-3, 8-11 and 4-7 hold the terms of up to four fp32 rows' weights without loss; eight rows' have room for two terms.
+  static constexpr int kTermsP = kF32 && R <= 4 ? 3 : 2;
   // 2^-23 of a sum is cut at most for each k-step: 2^-17 over 64 steps.
   static constexpr int kFlush = 64 / (kBlock / 16);
 };
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     }
-    auto flush = [&] {  // rows g and g + 8 hold the products of a weight's two terms
+    auto flush = [&] {  // rows g and g + 8 hold the products of a weight's two terms, rows g + 4 those of a third
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
           if constexpr (S::kF32) {
             if constexpr (R > 4) {
               x += s4[0][n][e + 2] + s4[S::kTiles - 1][n][e];
-            } else {
-              const float mid = __shfl_xor_sync(0xffffffffu, x, 16);
-              x += s4[0][n][e + 2] + mid;
+            } else {  // (rows 12-15 are zero: lanes g and g + 4 get the same sum)
+              x += s4[0][n][e + 2];
+              x += __shfl_xor_sync(0xffffffffu, x, 16);
             }
           }
           s[n][e] = x;
@@ -383,9 +386,9 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
       for (int n = 0; n < kCols; ++n) {
         const float x = ex2(s[n][0] - mu), y = ex2(s[n][1] - mu);
         l += x + y;
-        uint32_t term[2];
+        uint32_t term[S::kTermsP];
         split(x, y, term);
-        w[n >> 1][2 * (n & 1)] = mine ? term[0] : 0u;
+        w[n >> 1][2 * (n & 1)] = mine ? term[0] : S::kTermsP > 2 ? term[S::kTermsP - 1] : 0u;
         w[n >> 1][2 * (n & 1) + 1] = mine ? term[1] ^ 0x80008000u : 0u;
       }
       const uint32_t vp = arrived();
@@ -436,6 +439,12 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
       }
     }
     flush();
+    if constexpr (S::kTermsP > 2) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sums[n][e] += __shfl_xor_sync(0xffffffffu, sums[n][e], 16);
+    }
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     // the piece before has been joined (the warps do not wait for one another otherwise)

@@ -670,57 +670,90 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
 
 // Joins the parts of the units that were split: a warp per row, four (D 64: two) dimensions a lane. Statistics come first, a part to a
 // lane, so that nothing waits between the parts themselves (a warp with two rows and running statistics took 15 us for 128 rows of
-// 19 parts).
+// 19 parts). The live rows of all units, in order, are dealt to warps: most CTAs of the first kernel leave no rows to join, and a grid of
+// a CTA for every four rows there could be took 10 us to start and end.
+constexpr int kJoinWarps = 8, kJoinCtas = 4;  // CTAs per CTA of the first kernel
 template <typename T, int D, int kRows>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PaArgs a) {
-  constexpr int E = D / 32, kBlocks = kRows / 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PaArgs a, int jobs) {
+  constexpr int E = D / 32;
   using V = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ int s_rows[kPaManyCtas + 1];  // rows of the units before
   dependent_launch_wait();
-  const int c0 = blockIdx.x / kBlocks, lane = threadIdx.x & 31, r = blockIdx.x % kBlocks * 4 + (threadIdx.x >> 5);
-  const PaJoin job = a.join[c0];
-  if (r >= job.rows) return;
-  const V* part = reinterpret_cast<const V*>(a.part + (int64_t)r * D) + lane;
-  auto place = [&](int c) { return (int64_t)(2 * c + (c == c0)) * kRows; };
-  float M = -INFINITY, L = 0.0f, o[E];
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    constexpr int kEach = (kPaManyCtas + 31) / 32;
+    int n[kEach], sum = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 1
-  for (int b0 = c0; b0 <= job.last; b0 += 32) {  // 32 parts at a time
-    const float2 ml = b0 + lane <= job.last ? __ldcg(a.ml + place(b0 + lane) + r) : make_float2(-INFINITY, 0.0f);
-    float to = ml.x;
+    for (int e = 0; e < kEach; ++e) n[e] = lane * kEach + e < jobs ? a.join[lane * kEach + e].rows : 0;
 #pragma unroll
-    for (int d = 16; d; d /= 2) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
-    to = fmaxf(to, M);
-    const float corr = M == to ? 1.0f : ex2(M - to), mine = ml.x == to ? 1.0f : ex2(ml.x - to);
-    float sum = ml.y * mine;
+    for (int e = 0; e < kEach; ++e) sum += n[e];
+    int before = sum;
 #pragma unroll
-    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    L = fmaf(L, corr, sum);
-    M = to;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= corr;
-    const int n = min(32, job.last - b0 + 1);
-#pragma unroll 8
-    for (int b = 0; b < n; ++b) {
-      const V y = __ldcg(part + place(b0 + b) * (D / E));
-      const float g = __shfl_sync(0xffffffffu, mine, b);
-      const float* ye = reinterpret_cast<const float*>(&y);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(ye[e], g, o[e]);
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, before, d);
+      before += lane < d ? 0 : x;
     }
-  }
-  const float g = L == 0.0f ? 0.0f : 1.0f / L;
-  const int away = node_of(job.rest + r, 1.0f / (float)a.G);
-  T* out = static_cast<T*>(a.out) + ((int64_t)(job.tok0 + away) * a.Hq + job.head0 + r - away * a.G) * D + lane * E;
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (E == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * g, o[1] * g, o[2] * g, o[3] * g);
-    else *reinterpret_cast<float2*>(out) = make_float2(o[0] * g, o[1] * g);
-  } else {
-    uint32_t w[E / 2];
+    before -= sum;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) w[e / 2] = pack_rn(o[e] * g, o[e + 1] * g);
-    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(out) = w[0];
+    for (int e = 0; e < kEach; ++e) {
+      if (lane * kEach + e <= kPaManyCtas) s_rows[lane * kEach + e] = before;
+      before += n[e];
+    }
+    if (lane == 31) s_rows[kPaManyCtas] = before;
+  }
+  __syncthreads();
+  const int total = s_rows[kPaManyCtas];
+#pragma unroll 1
+  for (int item = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); item < total; item += gridDim.x * kJoinWarps) {
+    int c0 = 0;  // the last unit that begins at or before this row
+#pragma unroll
+    for (int d = 128; d; d /= 2)
+      if (c0 + d < kPaManyCtas && s_rows[c0 + d] <= item) c0 += d;
+    const PaJoin job = a.join[c0];
+    const int r = item - s_rows[c0];
+    const V* part = reinterpret_cast<const V*>(a.part + (int64_t)r * D) + lane;
+    auto place = [&](int c) { return (int64_t)(2 * c + (c == c0)) * kRows; };
+    float M = -INFINITY, L = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 1
+    for (int b0 = c0; b0 <= job.last; b0 += 32) {  // 32 parts at a time
+      const float2 ml = b0 + lane <= job.last ? __ldcg(a.ml + place(b0 + lane) + r) : make_float2(-INFINITY, 0.0f);
+      float to = ml.x;
+#pragma unroll
+      for (int d = 16; d; d /= 2) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+      to = fmaxf(to, M);
+      const float corr = M == to ? 1.0f : ex2(M - to), mine = ml.x == to ? 1.0f : ex2(ml.x - to);
+      float sum = ml.y * mine;
+#pragma unroll
+      for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      L = fmaf(L, corr, sum);
+      M = to;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= corr;
+      const int n = min(32, job.last - b0 + 1);
+#pragma unroll 8
+      for (int b = 0; b < n; ++b) {
+        const V y = __ldcg(part + place(b0 + b) * (D / E));
+        const float g = __shfl_sync(0xffffffffu, mine, b);
+        const float* ye = reinterpret_cast<const float*>(&y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(ye[e], g, o[e]);
+      }
+    }
+    const float g = L == 0.0f ? 0.0f : 1.0f / L;
+    const int away = node_of(job.rest + r, 1.0f / (float)a.G);
+    T* out = static_cast<T*>(a.out) + ((int64_t)(job.tok0 + away) * a.Hq + job.head0 + r - away * a.G) * D + lane * E;
+    if constexpr (sizeof(T) == 4) {
+      if constexpr (E == 4) *reinterpret_cast<float4*>(out) = make_float4(o[0] * g, o[1] * g, o[2] * g, o[3] * g);
+      else *reinterpret_cast<float2*>(out) = make_float2(o[0] * g, o[1] * g);
+    } else {
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) w[e / 2] = pack_rn(o[e] * g, o[e + 1] * g);
+      if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(out) = w[0];
+    }
   }
 }
 
@@ -733,8 +766,7 @@ nt_status launch_many(const PmMaps& maps, const PaArgs& a, cudaStream_t st) {
   const int ctas = std::min(device_sm_count(), kPaManyCtas);
   NT_CUDA_TRY(launch_kernel(paged_many_kernel<T, D, kPair, kExtra>, dim3((unsigned)ctas), dim3(kPmThreads), smem, st, true, maps, a));
   NT_TRY(check_launch("paged_many_kernel"));
-  constexpr int kRows = PmShape<T, D, kPair>::kRows;
-  NT_CUDA_TRY(launch_kernel(paged_join_kernel<T, D, kRows>, dim3((unsigned)(ctas * (kRows / 4))), dim3(128), 0, st, true, a));
+  NT_CUDA_TRY(launch_kernel(paged_join_kernel<T, D, PmShape<T, D, kPair>::kRows>, dim3((unsigned)(ctas * kJoinCtas)), dim3(32 * kJoinWarps), 0, st, true, a, ctas));
   return check_launch("paged_join_kernel");
 }
 template <typename T, int D, bool kPair>
