@@ -5,7 +5,7 @@
 // key-value head it stands for, it has to pass over the tiles of keys that any of its rows sees. Lengths are known on the device
 // only, so every CTA works out the division itself: all (unit, head, tile) in a row, cut into shares that are as good as equal, one per
 // CTA. A unit's keys may so be split over CTAs; then each leaves its part (weighted sum, maximum, sum of weights) in the workspace,
-// and they are joined in the order of the keys: on the fp32 units by the CTA that comes last, on the tensor cores by a kernel behind.
+// and they are joined in the order of the keys: those of few rows by the CTA that comes last, the others by a kernel behind.
 #pragma once
 
 #include <cuda.h>
@@ -14,7 +14,7 @@
 
 namespace nt {
 
-constexpr int kPaFewRows = 8;     // rows up to which a sequence's tokens take the kernel without tensor cores
+constexpr int kPaFewRows = 8;     // rows up to which a sequence's tokens take the kernel for few rows
 constexpr int kPaFewCtas = 320, kPaManyCtas = 160;  // of a launch at most (the workspace's size, asked for without a device, goes by them)
 constexpr int kPaMaxGroup = 64;
 constexpr uint64_t kPaTimeoutNs = 2000000000ull;
@@ -49,6 +49,25 @@ struct PaArgs {
 
 #ifdef __CUDACC__
 namespace {
+
+// cap tanh(y). By tanh(y) = 1 - 2 / (1 + e^2y), within 2^-21 of the cap (with a rounded quotient a tile of 128 keys took three times as
+// long); and, for small y, by its series y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835 - 1382 y^11/155925, the next term of which is
+// 2^-32 of the cap at a quarter: up to there it is taken where the first form's loss of what is small next to 1 would show.
+constexpr float kCapSmall = 0.25f;
+__device__ __forceinline__ float cap_whole(float y, float cap) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * 2.885390081777927f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));  // within 2^-23 (1 / inf = 0)
+  return fmaf(-2.0f * cap, r, cap);
+}
+__device__ __forceinline__ float cap_series(float y, float cap) {
+  const float z = y * y;
+  float p = fmaf(z, -0.0088632355f, 0.0218694885f);
+  p = fmaf(z, p, -0.0539682540f);
+  p = fmaf(z, p, 0.1333333333f);
+  p = fmaf(z, p, -0.3333333333f);
+  return cap * y * fmaf(z, p, 1.0f);
+}
 
 // Sequence s as the call sees it.
 struct PaSeq {

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     const int sure_hi = u.p0;                                                   // to here
     constexpr int kCols = S::kBlock / 8;
     const float f = kExtra ? 1.4426950408889634f : a.scale * 1.4426950408889634f;
+    const float to_cap = kExtra && a.cap > 0.0f ? a.scale / a.cap : 0.0f;
     const bool mine = R > 4 || g < 4;  // lanes whose row g is a query's
     float o[D / 8][4], sums[D / 8][2], m = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -354,8 +355,8 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           const int key = base + 8 * n + t2 + e;
           if constexpr (kExtra) {
-            float x = s[n][e] * a.scale;
-            if (a.cap > 0.0f) x = a.cap * tanhf(x / a.cap);
+            float x = s[n][e] * (a.cap > 0.0f ? to_cap : a.scale);
+            if (a.cap > 0.0f) x = fabsf(x) < kCapSmall ? cap_series(x, a.cap) : cap_whole(x, a.cap);
             if (a.slopes) x -= slope * (float)(pos - key);
             s[n][e] = x;
           }

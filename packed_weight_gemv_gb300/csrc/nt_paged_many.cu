@@ -59,7 +59,9 @@ struct PmShape {
   // fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
   static constexpr int kStart = kPair ? 8 : 3;
   static constexpr int kColO = 0, kColS = 2 * D;
-  // A tile costs a sum at most 16 (fp32) or 8 cuts of 2^-23: 2^-16 over 8 tiles, 2^-14 over 64.
+  // A tile costs a sum at most 16 (fp32) or 8 cuts of 2^-23: 2^-16 over 8 tiles, 2^-14 over 64. (fp32, 511 tokens over 7,489: 3.4e-6 off
+  // in 124 us; every 4 tiles 2.7e-6 in 135, every 2 2.5e-6 in 154, as the weights' two terms are left. A third term has no place: 192
+  // columns for P next to S and O of two groups.)
   static constexpr int kFlush = kF32 ? 8 : 64;
   static constexpr int kSmem = kQBytes + kStages * kSlot + 1024;
   static_assert(kStages >= 4, "ring");
@@ -67,11 +69,6 @@ struct PmShape {
   static_assert(kPageMaxSeqs * 4 <= kStages * kSlot, "the division's scratch stands in the ring");
 };
 
-__device__ __forceinline__ float rcp(float x) {  // 1 / x within 2^-23 (1 / inf = 0)
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // bar_wait in one piece: a call would fix the registers that setmaxnreg moves.
 __device__ __forceinline__ bool pm_wait(uint32_t bar, uint32_t parity, volatile int* fail, uint64_t timeout_ns) {
   if (bar_try(bar, parity)) return true;
@@ -432,37 +429,51 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
+        if constexpr (kExtra) {
+          // Cap and bias, from tensor memory and back: 32 keys at a time in a loop, as code for 128 in a row is fetched more slowly than
+          // it runs (300 fp32 tokens over 4,000, capped: 71 us instead of 93; bf16, 257 among decoding sequences: 87 instead of 89).
+          const float f = a.cap > 0.0f ? a.scale / a.cap : a.scale;
+          if (ok && !idle) {
+#pragma unroll 1
+            for (int c = 0; c < kPmKeys; c += 32) {
+              float r[32];
+              tm_load(scol + c, r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] *= f;
+              if (a.cap > 0.0f) {
+                bool big = !S::kF32;  // of bf16 queries, the first form always: the other one takes as long
+#pragma unroll
+                for (int e = 0; S::kF32 && e < 32; ++e) big |= !(fabsf(r[e]) < kCapSmall);
+                if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const float t = cap_whole(r[e], a.cap);
+                    r[e] = S::kF32 && fabsf(r[e]) < kCapSmall ? cap_series(r[e], a.cap) : t;
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) r[e] = cap_series(r[e], a.cap);
+                }
+              }
+              if (a.slopes) {
+                const float away = (float)(pos - key0 - c);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = fmaf(slope, (float)e - away, r[e]);
+              }
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(r[e]);
+              tm_store(scol + c, w);
+            }
+            tm_st_wait();
+          }
+        }
         float s[kPmKeys];
         if (ok && !idle) {
           tm_ld128(scol, s);
         } else {
 #pragma unroll
           for (int e = 0; e < kPmKeys; ++e) s[e] = 0.0f;
-        }
-        if constexpr (kExtra) {
-          if (a.cap > 0.0f) {
-            // tanh(y) = 1 - 2 / (1 + e^2y), within 2^-21 (with a rounded quotient a chunk took three times as long, 110 us of 37); of fp32
-            // queries, for small y, its series y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315 + 62 y^9 / 2835, within 2^-23 of it up to a quarter.
-            const float f = a.scale / a.cap, c2 = -2.0f * a.cap;
-#pragma unroll
-            for (int e = 0; e < kPmKeys; ++e) {
-              const float y = s[e] * f;
-              float t = fmaf(c2, rcp(1.0f + ex2(y * 2.885390081777927f)), a.cap);
-              if constexpr (S::kF32) {
-                const float z = y * y, p = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.0218694885f, -0.0539682540f), 0.1333333333f), -0.3333333333f), 1.0f);
-                if (fabsf(y) < 0.25f) t = a.cap * (y * p);
-              }
-              s[e] = t;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < kPmKeys; ++e) s[e] *= a.scale;
-          }
-          if (a.slopes) {
-            const float away = (float)(pos - key0);
-#pragma unroll
-            for (int e = 0; e < kPmKeys; ++e) s[e] = fmaf(slope, (float)e - away, s[e]);
-          }
         }
         if (part) {
           const int to = pos - key0, from = lo - key0;
