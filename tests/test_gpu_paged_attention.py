@@ -104,6 +104,25 @@ def test_caps_windows_and_slopes(seqs, Hq, Hkv, window, cap, slopes, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cap", [2.0 ** -100, 1e-20, 1e-3, 255.0, 257.0])
+def test_small_and_large_caps(cap, dtype):
+    c = Call("70+200 1+3 1+900", 4, 1, 64, 16, dtype, seed=5, cap=cap)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cap", [1e5, 1e12, 2.0 ** 100])
+def test_a_cap_far_above_the_scores_loses_nothing_of_them(cap, dtype):
+    """cap tanh(x / cap) is off x by at most |x|^3 / (3 cap^2), which is less than a rounding of x here: the tolerance of no cap holds."""
+    c = Call("70+200 1+3 1+900", 4, 1, 64, 16, dtype, seed=5, cap=cap)
+    score = float(c.q.float().norm(dim=-1).max() * c.k.float().nan_to_num(0).norm(dim=-1).max()) / c.D ** 0.5
+    assert score ** 2 / (3 * cap ** 2) < U32
+    out = c.run()
+    c.cap = 0.0
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("seqs,Hq,Hkv,D", [("1+20000", 8, 2, 128), ("1+9000 1+12 1+4000", 32, 8, 64), ("200+9000", 8, 2, 128), ("700+3000 400+0", 4, 1, 64),
                                            ("17+33000", 2, 1, 128), ("1+0 " * 40 + "1+700 " * 40, 8, 2, 128)])
 def test_long_sequences_and_many(seqs, Hq, Hkv, D, dtype):

@@ -72,6 +72,7 @@ def test_compact_refusals(lib, bad, status):
     (dict(out=None), INV), (dict(dtype=2), INV), (dict(D=96), UNSUP), (dict(T=0), INV), (dict(T=(1 << 20) + 1), INV), (dict(S=0), INV), (dict(S=4097), INV),
     (dict(Hkv=0), INV), (dict(Hq=9), INV), (dict(Hq=130, Hkv=2), INV), (dict(T=1 << 20, Hq=32, qs=4096), INV), (dict(page=20), INV), (dict(ts=15), INV),
     (dict(W=0), INV), (dict(most=-1), INV), (dict(window=-1), INV), (dict(cap=-1.0), INV), (dict(cap=float("inf")), INV), (dict(cap=float("nan")), INV),
+    (dict(cap=2.0 ** -101), INV), (dict(cap=2.0 ** 101), INV),
     (dict(qs=1028), ALIGN), (dict(qs=1016), INV), (dict(out=P[0], qs=2048), INV), (dict(q=P[0] + 8), ALIGN), (dict(k=P[1] + 2), ALIGN),
     (dict(v=P[2] + 8), ALIGN), (dict(out=P[6] + 4), ALIGN), (dict(table=P[3] + 1), ALIGN), (dict(slopes=P[8] + 2), ALIGN), (dict(bad=P[8] + 2), ALIGN),
     (dict(ws=None), WS), (dict(ws=P[7] + 8), WS), (dict(bytes=100), WS)])
