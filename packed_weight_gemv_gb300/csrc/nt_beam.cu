@@ -56,7 +56,7 @@ __device__ __forceinline__ float weight(float x) {
 // A warp per chunk.
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const BeamArgs a, int64_t jobs) {
   dependent_launch_wait();
-  // 1 / len^alpha of 32 rows by the first warp of each of the first CTAs: 64-bit operations take an SM 16 cycles a warp, however few
+  // 1 / len^alpha (at least 2^-124) of 32 rows by the first warp of each of the first CTAs: 64-bit operations take an SM 16 cycles a warp, however few
   // of its lanes want them.
   const int own = blockIdx.x * 32 + threadIdx.x;
   if (a.alpha != 0.0 && threadIdx.x < 32 && own < a.N) {
@@ -457,13 +457,18 @@ nt_status nt_beam_select(const float* logits, const float* scores, int N, int W,
   if (W < 1 || W > kBeamMax || N % W != 0 || K < 1 || K > kBeamMax)
     return set_error(NT_ERR_INVALID_ARG, "need 1 <= W, K <= 64 and N a multiple of W");
   if (eos < -1 || eos >= V || (done_opt && eos < 0)) return set_error(NT_ERR_INVALID_ARG, "need -1 <= eos < V, and a token with done");
-  if (!std::isfinite(alpha) || alpha < 0.0 || alpha > 16.0 || (alpha != 0.0 && !lengths_opt))
-    return set_error(NT_ERR_INVALID_ARG, "need 0 <= alpha <= 16, and lengths where it is not 0");
+  if (!std::isfinite(alpha) || alpha < 0.0 || alpha > 4.0 || (alpha != 0.0 && !lengths_opt))
+    return set_error(NT_ERR_INVALID_ARG, "need 0 <= alpha <= 4, and lengths where it is not 0");
   if (!aligned(logits, 4) || !aligned(scores, 4) || (done_opt && !aligned(done_opt, 4)) || (lengths_opt && !aligned(lengths_opt, 4)) ||
       !aligned(parent, 4) || !aligned(token, 4) || !aligned(score, 4) || (done_out_opt && !aligned(done_out_opt, 4)))
     return set_error(NT_ERR_ALIGNMENT, "arrays must be 4-byte aligned");
   if (!ws || !aligned(ws, 16) || ws_bytes < beam_ws_bytes(V, N))
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_beam_select_workspace_size");
+  const size_t in = (size_t)N * 4, chosen = (size_t)(N / W) * K * 4;
+  for (const void* o : {(const void*)parent, (const void*)token, (const void*)score, (const void*)done_out_opt})
+    if (o && (overlap(o, chosen, scores, in) || (done_opt && overlap(o, chosen, done_opt, in)) || (lengths_opt && overlap(o, chosen, lengths_opt, in)) ||
+              overlap(o, chosen, logits, in * V)))
+      return set_error(NT_ERR_INVALID_ARG, "outputs must not overlap inputs");
   NT_TRY(check_device());
   BeamArgs a{};
   a.logits = logits;

@@ -317,10 +317,6 @@ __global__ void __launch_bounds__(256) page_remap_kernel(const CompactArgs a) {
 }
 
 // ---- host -----------------------------------------------------------------------------------
-bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  return a < b + ny && b < a + nx;
-}
 nt_status check_pages(int page, int n_pages, int width) {
   if (!page_ok(page)) return set_error(NT_ERR_INVALID_ARG, "page must be 16, 32, 64, 128 or 256 rows");
   if (n_pages < 1 || (int64_t)n_pages * page > INT32_MAX) return set_error(NT_ERR_INVALID_ARG, "need n_pages >= 1 and n_pages * page in the int range");

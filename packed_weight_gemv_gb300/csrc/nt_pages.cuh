@@ -20,6 +20,10 @@ inline int page_shift(int page) {
   while (1 << s < page) ++s;
   return s;
 }
+inline bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + ny && b < a + nx;
+}
 // Pages that `rows` rows take.
 __host__ __device__ inline int pages_of(int rows, int shift) { return (int)(((int64_t)rows + (1 << shift) - 1) >> shift); }
 

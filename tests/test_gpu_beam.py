@@ -63,6 +63,15 @@ def test_finished_beams_and_lengths(W, K, V, alpha):
     assert (got[3][K:K + min(W, K)] == 1).all()
 
 
+@pytest.mark.parametrize("alpha", [1.0, 4.0])
+@pytest.mark.parametrize("most", [300, 1 << 20, (1 << 31) - 1])
+def test_steep_penalties_of_long_beams(alpha, most):
+    """1 / length^alpha is 2^-124 at the smallest, so it ranks every beam; scores are not touched by it."""
+    rs = np.random.RandomState(most & 0xffff)
+    x, s = random(rs, 8, 900)
+    check(x, s, 4, 6, np.array([0, 1, 0, 0] * 2), 7, rs.randint(most // 2, most, 8), alpha)
+
+
 def test_ties_go_to_the_lower_beam_and_token():
     V = 3001
     for fill in (0.0, -3.25, 1e-30):

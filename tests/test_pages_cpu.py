@@ -95,7 +95,8 @@ def test_attention_workspace_is_what_the_call_wants(lib):
 @pytest.mark.parametrize("bad,status", [
     (dict(x=None), INV), (dict(s=None), INV), (dict(parent=None), INV), (dict(token=None), INV), (dict(score=None), INV), (dict(N=0), INV),
     (dict(N=9), INV), (dict(N=65540), INV), (dict(W=0), INV), (dict(W=65, N=65), INV), (dict(V=0), INV), (dict(V=(1 << 24) + 1), INV), (dict(K=0), INV),
-    (dict(K=65), INV), (dict(eos=100), INV), (dict(eos=-2), INV), (dict(eos=-1), INV), (dict(alpha=-0.1), INV), (dict(alpha=17.0), INV),
+    (dict(K=65), INV), (dict(eos=100), INV), (dict(eos=-2), INV), (dict(eos=-1), INV), (dict(alpha=-0.1), INV), (dict(alpha=17.0), INV), (dict(alpha=4.01), INV),
+    (dict(score=P[1]), INV), (dict(dout=P[2]), INV), (dict(parent=P[3]), INV), (dict(token=P[0] + 64), INV),
     (dict(alpha=float("nan")), INV), (dict(lens=None), INV), (dict(x=P[0] + 2), ALIGN), (dict(done=P[2] + 1), ALIGN), (dict(dout=P[7] + 2), ALIGN),
     (dict(ws=None), WS), (dict(ws=P[8] + 8), WS), (dict(bytes=300), WS)])
 def test_beam_refusals(lib, bad, status):
