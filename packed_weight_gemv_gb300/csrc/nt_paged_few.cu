@@ -7,8 +7,8 @@
 // takes 16 rows at least, which the terms of the values share: an fp32 query is three bf16 terms (nothing is lost) in rows of their own,
 // its weights three as well, or two rounded ones (2^-17) where eight rows leave no more room, and the rows are summed behind; weights of
 // bf16 queries are two terms. (On the fp32 units a block of 16
-// keys took 770 instructions, on eight warps of an SM 141 us for 64 sequences of 158,000 rows together; now 122, 5.4 TB/s, with the issue slots
-// next to memory as the bound. A single token over 4,094 rows is latency: 12 us.)
+// keys took 770 instructions, on eight warps of an SM 141 us for 64 sequences of 158,000 rows together; now 122, 5.4 TB/s, with a warp's chain of
+// dependent steps next to memory as the bound. A single token over 4,094 rows is latency: 12 us.)
 //
 // A warp takes a block of 16 keys (D 64: 32) at a time: the scores come out of the MMAs in the places where the weights go in. The
 // reference m of a row is raised only when a score exceeds it by 2^8. Accumulators go to sums that round to nearest every kFlush
