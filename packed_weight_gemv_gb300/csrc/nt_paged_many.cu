@@ -23,7 +23,7 @@
 // Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 430 us (1,320 TFLOP/s),
 // ragged prompts of 8,000 tokens together 624 us (1,190), 511 fp32 tokens over 7,489 123 us (five products for one, 1,320 of
 // them). Keys and values from L2 alone would take half of that, the exponentials three quarters. What a call pays
-// besides is about 25 us: 13 to the end of a first tile, 8 for the join of parts.
+// besides is about 25 us: 13 to the end of a first tile, 6 for the join of parts.
 #include <math.h>
 
 #include <algorithm>
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] *= corr;
       const int n = min(32, job.last - b0 + 1);
-#pragma unroll 8
+#pragma unroll 16
       for (int b = 0; b < n; ++b) {
         const V y = __ldcg(part + place(b0 + b) * (D / E));
         const float g = __shfl_sync(0xffffffffu, mine, b);
