@@ -546,8 +546,8 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *     those of rows that are seen (such rows read as zeros)
  *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes (16-byte aligned, zero-filled before its first use, its counters
  *     left zero; calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
- * Products of queries and keys are exact, scores and statistics fp32. fp32 queries' weights are fp32 or two bf16 terms, within 2^-17 of
- * them; bf16 queries' are two terms where a sequence has up to 8 rows (tokens x Hq / Hkv) and one rounded bf16 value where it has more.
+ * Products of queries and keys are exact, scores and statistics fp32. Where a sequence has up to 8 rows (tokens x Hq / Hkv), fp32
+ * queries' weights are fp32 and bf16 queries' two bf16 terms (within 2^-17); where it has more, they are two terms and one rounded bf16 value.
  * The capped score is within 2^-21 of the cap, and within some roundings of itself where |x| < cap / 4 (bf16 queries: and the
  * cap is above 256). Sums lose at most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the
  * output is rounded. */

@@ -5,8 +5,7 @@
 //
 // Such a call is bound by reading keys and values once. Its products are few, so they run on mma.sync (m16n8k16, bf16, fp32 sums): it
 // takes 16 rows at least, which the terms of the values share: an fp32 query is three bf16 terms (nothing is lost) in rows of their own,
-// its weights three as well, or two rounded ones (2^-17) where eight rows leave no more room, and the rows are summed behind; weights of
-// bf16 queries are two terms. (On the fp32 units a block of 16
+// its weights three as well, and the rows are summed behind; weights of bf16 queries are two rounded terms (2^-17). (On the fp32 units a block of 16
 // keys took 770 instructions, on eight warps of an SM 141 us for 64 sequences of 158,000 rows together; now 122, 5.4 TB/s, with a warp's chain of
 // dependent steps next to memory as the bound. A single token over 4,094 rows is latency: 12 us.)
 //
@@ -67,8 +66,9 @@ struct FewShape {
   // Rows of an MMA: up to four query rows' three terms in rows 0-3, 4-7 and 8-11 of one; eight rows' in 0-7 and 8-15 of one and 0-7 of
   // another.
   static constexpr int kTiles = kF32 && R > 4 ? 2 : 1;
-  // Weights: rows 0-3, 8-11 and 4-7 hold the terms of up to four fp32 rows' weights without loss; eight rows' have room for two terms.
-  static constexpr int kTermsP = kF32 && R <= 4 ? 3 : 2;
+  // Weights: rows 0-3, 8-11 and 4-7 hold the terms of up to four fp32 rows' weights without loss; of eight rows', rows 0-7 and 8-15 two
+  // terms and a second MMA the third (1 % longer over memory).
+  static constexpr int kTermsP = kF32 ? 3 : 2;
   // 2^-23 of a sum is cut at most for each k-step: 2^-17 over 64 steps.
   static constexpr int kFlush = 64 / (kBlock / 16);
 };
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     }
-    auto flush = [&] {  // rows g and g + 8 hold the products of a weight's two terms, rows g + 4 those of a third
+    auto flush = [&] {  // rows g and g + 8 hold the products of a weight's first two terms
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
         }
       }
       const float mu = m == -INFINITY ? 0.0f : m;
-      uint32_t w[kSubs][4];
+      uint32_t w[kSubs][4], third[kSubs][2];  // eight rows' third terms: an MMA of their own onto the rows of the first ones
 #pragma unroll
       for (int n = 0; n < kCols; ++n) {
         const float x = ex2(s[n][0] - mu), y = ex2(s[n][1] - mu);
@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
         uint32_t term[S::kTermsP];
         split(x, y, term);
         w[n >> 1][2 * (n & 1)] = mine ? term[0] : S::kTermsP > 2 ? term[S::kTermsP - 1] : 0u;
+        third[n >> 1][n & 1] = term[S::kTermsP - 1];
         w[n >> 1][2 * (n & 1) + 1] = mine ? term[1] ^ 0x80008000u : 0u;
       }
       const uint32_t vp = arrived();
@@ -431,6 +432,11 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
         for (int n = 0; n < D / 16; ++n) {
           uint32_t b[4];  // keys 0-7 and 8-15 of two chunks of dimensions
           load_matrices_turned(vp + chunk(h * 16 + (lane >> 3 & 1) * 8 + (lane & 7), 2 * n + (lane >> 4)), b);
+          if constexpr (S::kF32 && R > 4) {
+            const uint32_t low[4] = {third[h][0], 0u, third[h][1], 0u};
+            mma_16816(o[2 * n], low, b[0], b[1]);
+            mma_16816(o[2 * n + 1], low, b[2], b[3]);
+          }
           mma_16816(o[2 * n], w[h], b[0], b[1]);
           mma_16816(o[2 * n + 1], w[h], b[2], b[3]);
         }
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
       }
     }
     flush();
-    if constexpr (S::kTermsP > 2) {
+    if constexpr (S::kTermsP > 2 && R <= 4) {
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
