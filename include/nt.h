@@ -544,8 +544,9 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *   window >= 0; cap 0 or 2^-100 .. 2^100; slopes_opt [Hq] fp32 or NULL
  *   n_bad_opt: device uint32 counter or NULL; a nonzero number is ADDED where entries outside [0, t_stride / page) were met among
  *     those of rows that are seen (such rows read as zeros)
- *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes (16-byte aligned, zero-filled before its first use, its counters
- *     left zero; calls sharing it must not overlap). It starts with the status header of nt_workspace_status.
+ *   ws: nt_paged_attention_workspace_size(T, S, Hq, Hkv, D) bytes or more (16-byte aligned, zero-filled before its first use; calls
+ *     sharing it must not overlap). Calls of any sizes may follow one another on it: its counters stand at one place and are left zero.
+ *     It starts with the status header of nt_workspace_status.
  * Products of queries and keys are exact, scores and statistics fp32. Where a sequence has up to 8 rows (tokens x Hq / Hkv), fp32
  * queries' weights are fp32 and bf16 queries' two bf16 terms (within 2^-17); where it has more, they are two terms and one rounded bf16 value.
  * The capped score is within 2^-21 of the cap, and within some roundings of itself where |x| < cap / 4 (bf16 queries: and the

@@ -33,19 +33,41 @@ struct PaArgs {
   const float* slopes;      // [Hq] or null
   uint32_t* n_bad;
   unsigned int* err;        // the workspace's status header [code, CTA]
-  unsigned int* count;      // [units x heads] parts that have arrived, all 0 between calls
+  unsigned int* count;      // [kPaFewCtas] parts that have arrived of the unit that a CTA has the first tile of, all 0 between calls
   float* part;              // [2 x CTAs][rows][D] weighted sums
   float2* ml;               // [2 x CTAs][rows] (maximum, sum of weights)
   PaJoin* join;             // [CTAs]
   float* scratch;           // [CTAs][2][D][128] sums taken off the tensor cores
   uint64_t timeout_ns;
   int64_t q_stride;
-  int64_t jobs;             // places of `count`
+  int64_t most;             // units x heads that a call can have
   int fault, which;
   int T, S, Hq, Hkv, G, width, page, shift, n_pages, ts;
   int window;               // INT32_MAX: none
   float cap, scale;         // scale = 1 / sqrt(D)
 };
+
+// The workspace of a call. What has to be 0 when a call begins stands at places that do not depend on its sizes: a server hands one
+// workspace to steps of any sizes, and what one of them leaves behind must not be another's counters. A CTA has the first tile of one
+// unit at most that goes on in other CTAs, so the CTA names the counter.
+struct PaLayout {
+  size_t join, count, part, scratch, ml, bytes;
+};
+inline PaLayout paged_layout(int T, int Hq, int Hkv, int D) {
+  // Parts of a launch take a slot each, two per CTA; on the tensor cores each has up to 256 rows (fewer where the call has), and a
+  // CTA's sums beside.
+  const int64_t rows = (int64_t)T * (Hq / Hkv), few = 2 * kPaFewCtas * kPaFewRows;
+  const int64_t many = rows <= kPaFewRows ? 0 : (int64_t)2 * kPaManyCtas * (rows <= 128 ? 128 : 256);
+  const size_t parts = (size_t)(many > few ? many : few), sums = rows <= kPaFewRows ? 0 : (size_t)kPaManyCtas * 2 * 128 * D;
+  PaLayout l;
+  l.join = kWsHeaderBytes;
+  l.count = l.join + (kPaManyCtas * sizeof(PaJoin) + 255) / 256 * 256;
+  l.part = l.count + (kPaFewCtas * sizeof(unsigned int) + 255) / 256 * 256;
+  l.scratch = l.part + parts * D * sizeof(float);
+  l.ml = l.scratch + sums * sizeof(float);
+  l.bytes = l.ml + parts * sizeof(float2);
+  return l;
+}
 
 #ifdef __CUDACC__
 namespace {
@@ -172,7 +194,7 @@ template <int kStart>
 struct PaShare {
   PaCut<kStart> cut;
   int64_t from, end, off;
-  int s, mt, unit, g;
+  int s, mt, g;
 };
 
 // starts: S places of shared memory (scratch); all threads of the CTA, every one gets the share. near: see PaCut.
@@ -198,7 +220,7 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
     }
     if (!__any_sync(0xffffffffu, many)) {
       const int units = __shfl_sync(0xffffffffu, upto, 31);
-      if ((int64_t)units * a.Hkv > a.jobs) return r;  // starts that do not rise name more tokens than there are: no work
+      if ((int64_t)units * a.Hkv > a.most) return r;  // starts that do not rise name more tokens than there are: no work
       int s = 0;  // of unit `lane`: the sequences that end at or before it
 #pragma unroll
       for (int d = 16; d; d /= 2)
@@ -227,7 +249,6 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
       const int64_t w0 = __shfl_sync(0xffffffffu, w, u0), w1 = __shfl_sync(0xffffffffu, w, u1);
       r.s = __shfl_sync(0xffffffffu, s, u0);
       r.mt = __shfl_sync(0xffffffffu, mt, u0);
-      r.unit = u0;
       r.g = (int)pa_div(x0 - off0, w0);
       r.off = off0 + r.g * w0;
       r.from = r.cut.snap(x0, r.off, w0);
@@ -236,7 +257,7 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
     }
   }
   __shared__ int64_t s_warps[32];
-  __shared__ int s_first[3];
+  __shared__ int s_first[2];
   __shared__ int64_t s_at[4];  // work before the units of both ends, and a head's
   const int i = threadIdx.x;
   int64_t units = 0;
@@ -247,7 +268,7 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
     if (s < a.S) starts[s] = (int)(units + at);
     units += total;
   }
-  if (units * a.Hkv > a.jobs) return r;  // as above
+  if (units * a.Hkv > a.most) return r;  // as above
   __syncthreads();
   auto tiles = [&](int64_t u, int* s_out, int* mt_out) -> int64_t {
     if (u >= units) return 0;
@@ -272,11 +293,10 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
   r.cut.set(work, gridDim.x, near);
   if ((int)blockIdx.x >= r.cut.ctas) return r;  // nothing left for this CTA
   const int64_t x0 = r.cut.from(blockIdx.x), x1 = r.cut.from(blockIdx.x + 1);
-  auto found = [&](int64_t u) {
+  auto found = [&] {
     if (at <= x0 && x0 < at + mine) {
       s_first[0] = s;
       s_first[1] = mt;
-      s_first[2] = (int)u;
       s_at[0] = at;
       s_at[1] = mine / a.Hkv;
     }
@@ -286,21 +306,20 @@ __device__ PaShare<kStart> pa_share(const PaArgs& a, int rows, int near, int* st
     }
   };
   if (units <= kThreads) {
-    found(i);
+    found();
   } else {
     int64_t sum = 0;
     for (int64_t u0 = 0; u0 < units && sum <= x1; u0 += kThreads) {
       int64_t total;
       mine = tiles(u0 + i, &s, &mt);
       at = sum + pa_scan<kThreads>(mine, s_warps, &total);
-      found(u0 + i);
+      found();
       sum += total;
     }
   }
   __syncthreads();
   r.s = s_first[0];
   r.mt = s_first[1];
-  r.unit = s_first[2];
   r.g = (int)pa_div(x0 - s_at[0], s_at[1]);
   r.off = s_at[0] + r.g * s_at[1];
   r.from = r.cut.snap(x0, r.off, s_at[1]);
@@ -314,7 +333,6 @@ struct PaPiece {
   int g, t0, n;
   int c0, c1;      // CTAs with the unit's first and last tile for this head (PaWalk::parts)
   int slot;        // where this CTA leaves its part
-  int job;         // unit and head: the place of the counter
 };
 template <int kKeys, int kStart>
 struct PaWalk {
@@ -339,7 +357,6 @@ struct PaWalk {
     p.n = (int)min((int64_t)u.tiles, sh.end - tile) - p.t0;
     p.c0 = p.c1 = blockIdx.x;
     p.slot = 2 * blockIdx.x + (p.t0 == 0);
-    p.job = sh.unit * a.Hkv + sh.g;
     return p;
   }
   // Of a piece that is not all of its unit and head. CTA c leaves its part in place 2 c, c0 in 2 c0 + 1 (its share may have begun with
@@ -353,7 +370,6 @@ struct PaWalk {
     if (!more()) return;
     if (++sh.g < a.Hkv) return;
     sh.g = 0;
-    ++sh.unit;
     ++sh.mt;
     while (sh.mt >= pa_row_tiles(a, q.n, rows)) {  // there is one: work is left
       sh.mt = 0;

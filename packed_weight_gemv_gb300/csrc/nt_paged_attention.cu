@@ -11,21 +11,6 @@
 namespace nt {
 namespace {
 
-// Parts of a launch take a slot each, two per CTA; on the tensor cores each has up to 256 rows (fewer where the call has), and a
-// CTA's sums beside.
-int64_t part_rows(int T, int Hq, int Hkv) {
-  const int64_t rows = (int64_t)T * (Hq / Hkv);
-  const int64_t many = rows <= kPaFewRows ? 0 : (int64_t)2 * kPaManyCtas * (rows <= 128 ? 128 : 256);
-  return std::max<int64_t>(many, 2 * kPaFewCtas * kPaFewRows);
-}
-size_t scratch_floats(int T, int Hq, int Hkv, int D) {
-  return (int64_t)T * (Hq / Hkv) <= kPaFewRows ? 0 : (size_t)kPaManyCtas * 2 * 128 * D;
-}
-size_t paged_counts(int T, int S, int Hq, int Hkv) { return ((size_t)T * Hq + (size_t)S * Hkv + 63) / 64 * 64; }
-constexpr size_t kJoinBytes = (kPaManyCtas * sizeof(PaJoin) + 255) / 256 * 256;
-size_t paged_ws_bytes(int T, int S, int Hq, int Hkv, int D) {
-  return kWsHeaderBytes + kJoinBytes + paged_counts(T, S, Hq, Hkv) * sizeof(unsigned int) + (part_rows(T, Hq, Hkv) * (D + 2) + scratch_floats(T, Hq, Hkv, D)) * sizeof(float);
-}
 nt_status check_paged(int T, int S, int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
   if (T < 1 || T > kPagedMaxTokens || S < 1 || S > kPageMaxSeqs) return set_error(NT_ERR_INVALID_ARG, "need 1 <= T <= 1048576 and 1 <= S <= 4096");
@@ -71,7 +56,7 @@ nt_status nt_paged_attention_workspace_size(int T, int S, int Hq, int Hkv, int D
   clear_error();
   if (!bytes) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
   NT_TRY(check_paged(T, S, Hq, Hkv, D));
-  *bytes = paged_ws_bytes(T, S, Hq, Hkv, D);
+  *bytes = paged_layout(T, Hq, Hkv, D).bytes;
   return NT_OK;
 }
 
@@ -96,7 +81,8 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   if (!aligned(table, 4) || !aligned(q_start, 4) || !aligned(length, 4) || (slopes_opt && !aligned(slopes_opt, 4)) ||
       (n_bad_opt && !aligned(n_bad_opt, 4)))
     return set_error(NT_ERR_ALIGNMENT, "int32 and fp32 arrays must be 4-byte aligned");
-  if (!ws || !aligned(ws, 16) || ws_bytes < paged_ws_bytes(T, S, Hq, Hkv, D))
+  const PaLayout at = paged_layout(T, Hq, Hkv, D);
+  if (!ws || !aligned(ws, 16) || ws_bytes < at.bytes)
     return set_error(NT_ERR_WORKSPACE, "workspace NULL, misaligned or smaller than nt_paged_attention_workspace_size");
   NT_TRY(check_device());
   PaArgs a{};
@@ -111,15 +97,15 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
   a.n_bad = n_bad_opt;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<unsigned int*>(w);
-  a.join = reinterpret_cast<PaJoin*>(w + kWsHeaderBytes);
-  a.count = reinterpret_cast<unsigned int*>(w + kWsHeaderBytes + kJoinBytes);
-  a.part = reinterpret_cast<float*>(a.count + paged_counts(T, S, Hq, Hkv));
-  a.scratch = a.part + part_rows(T, Hq, Hkv) * D;
-  a.ml = reinterpret_cast<float2*>(a.scratch + scratch_floats(T, Hq, Hkv, D));
+  a.join = reinterpret_cast<PaJoin*>(w + at.join);
+  a.count = reinterpret_cast<unsigned int*>(w + at.count);
+  a.part = reinterpret_cast<float*>(w + at.part);
+  a.scratch = reinterpret_cast<float*>(w + at.scratch);
+  a.ml = reinterpret_cast<float2*>(w + at.ml);
   a.timeout_ns = test_fault_timeout_ns(kPaTimeoutNs);
   a.fault = test_fault() == kFaultPaged;
   a.q_stride = q_stride;
-  a.jobs = (int64_t)T * Hq + (int64_t)S * Hkv;
+  a.most = (int64_t)T * Hq + (int64_t)S * Hkv;
   a.which = kPaAll;
   a.T = T;
   a.S = S;

@@ -74,7 +74,7 @@ struct FewShape {
 };
 // A unit and head that several CTAs share, for the join behind the pieces.
 struct FewPart {
-  int there, job, c0, c1, mt, t0, rows, g;
+  int there, c0, c1, mt, t0, rows, g;
 };
 
 template <typename T, int D, int R, bool kExtra>
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     }
     if (split_up && from == 0) {
       walk.parts(p);
-      s_part[p.t0 == 0] = FewPart{1, p.job, p.c0, p.c1, u.mt, u.t0, u.rows, p.g};
+      s_part[p.t0 == 0] = FewPart{1, p.c0, p.c1, u.mt, u.t0, u.rows, p.g};
     }
   };
   auto later = [](PaWalk<kFewKeys, kFewStart> w) {  // whether a piece follows this one, which ends with its unit and head
@@ -505,9 +505,9 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     s_last[i] = 0;
     if (s_part[i].there) {
       __threadfence();  // (of this thread for all, which have met it)
-      const unsigned before = atomicAdd(a.count + s_part[i].job, 1u);
+      const unsigned before = atomicAdd(a.count + s_part[i].c0, 1u);
       s_last[i] = before == (unsigned)(s_part[i].c1 - s_part[i].c0);
-      if (s_last[i]) a.count[s_part[i].job] = 0;
+      if (s_last[i]) a.count[s_part[i].c0] = 0;
       __threadfence();
     }
   }
