@@ -112,6 +112,7 @@ struct PaUnit {
   int t0, n, len;     // as in PaSeq
   int rows;           // live rows
   int p0, p1;         // positions of its first and last token
+  int lo;             // the first key that any of them sees
   int tile0, tiles;   // tiles of keys
 };
 template <int kKeys>
@@ -126,8 +127,9 @@ __device__ __forceinline__ PaUnit pa_unit(const PaArgs& a, const PaSeq& q, int s
   u.rows = min(rows, all - r0);
   u.p0 = q.len - q.n + r0 / a.G;
   u.p1 = q.len - q.n + (r0 + u.rows - 1) / a.G;
-  const int lo = (int)max((int64_t)0, (int64_t)u.p0 - a.window + 1), hi = max(u.p1 + 1, 0);
-  u.tile0 = lo / kKeys;
+  const int hi = max(u.p1 + 1, 0);
+  u.lo = (int)max((int64_t)0, (int64_t)u.p0 - a.window + 1);
+  u.tile0 = u.lo / kKeys;
   u.tiles = max(1, (hi + kKeys - 1) / kKeys - u.tile0);  // one, all of it masked, where nothing is seen
   return u;
 }

@@ -174,14 +174,16 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
     int bad = 0, issued = -1;
     for (; walk.more() && ok; walk.next(a)) {
       const PaPiece p = walk.piece(a);
-      const int hi = p.u.p1 + 1;  // no row sees this key
+      // Whether any row sees a key of a box. (The first tile begins before the first key that is seen: pages that a window has left behind
+      // may be gone.)
+      auto there = [&](int key) { return key <= p.u.p1 && key + per - 1 >= p.u.lo; };
       const int32_t* ids = a.table + (int64_t)p.u.s * a.width;
       const int first = (p.u.tile0 + p.t0) * kPmKeys + box * per;
       // The page of this lane's box of tile j. Asked for three tiles before it is looked at: the loads would otherwise wait for it, a
       // round trip to L2 for every tile.
       auto ask = [&](int j) {
         const int key = first + j * kPmKeys;
-        return j < p.n && key < hi ? ids[key >> a.shift] : -1;
+        return j < p.n && there(key) ? ids[key >> a.shift] : -1;
       };
       constexpr int kAsk = 3;
       int id[kAsk];
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       for (int j = 0; ok && j < p.n; ++j) {
         const int key = first + j * kPmKeys, page = id[0];
         int y = a.ts;  // behind the pool (zeros) where nothing is seen, or nothing is there
-        if (key < hi) {
+        if (there(key)) {
           if ((unsigned)page < (unsigned)a.n_pages) y = (page << a.shift) + (key & (a.page - 1));
           else bad = 1;
         }
