@@ -565,8 +565,8 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
  * each group the K best in order, ties by the lower beam, then the lower token: parent (the beam's row, for nt_page_fork),
  * token, score (total) and done_out (1: finished before or by eos), [N / W][K] each; -1, -1, -inf and 0 where there are fewer.
  * Sums run in fp32 and are joined in 64 bits, ranks are compared in pairs of fp32 (48 bits): score is within 2^-22 of the exact one, relative
- * to the larger of it and the logits. A logit of NaN or -inf is never chosen and adds nothing; a beam whose score is not finite, or with
- * a logit of +inf, has no continuation.
+ * to the larger of it and the logits. A logit of NaN or -inf is never chosen and adds nothing, nor is a total below the range of fp32 chosen; a
+ * beam whose score is not finite, or with a logit of +inf, has no continuation.
  *   1 <= W, K <= 64; N a multiple of W, N <= 65536; V <= 2^24; eos -1 (none) or below V; 0 <= alpha <= 4 (0: lengths not
  *   needed); done_opt, lengths_opt [N] int32; outputs must not overlap inputs
  *   ws: nt_beam_select_workspace_size(V, N) bytes (16-byte aligned; scratch; calls sharing it must not overlap) */

@@ -1,6 +1,9 @@
 // nt_beam.cu -- the next beams of beam search: per group of W beams the K best of their W * V continuations.
 //
-//   key(w, v) = (score[w] + (x[w][v] - lse[w])) / (len[w] + 1)^alpha,   lse[w] = log sum_v e^x[w][v]
+//   key(w, v) = ((score[w] - log S[w]) + (x[w][v] - M[w])) / (len[w] + 1)^alpha,   M[w] = max_v x[w][v],   S[w] = sum_v e^(x[w][v] - M[w])
+//
+// The largest logit comes off first: where a mask has put a whole row at the type's lowest value, score and log S would be lost in it (such
+// a beam's keys came out as 0, above every other).
 //
 // Keys are compared in pairs of fp32 (a sum of two, 48 bits), ties by the lower beam and then the lower token: beams of a
 // group often have continuations closer than fp32 tells apart at their scores' size.
@@ -113,9 +116,9 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
-// What a row adds to its logits, and the factor that ranks it: pairs of fp32.
+// A row's largest logit, what is added to the logits less that, and the factor that ranks it: pairs of fp32.
 struct RowKey {
-  float add_hi, add_lo, mul_hi, mul_lo;  // add_hi NaN: the row has no continuation
+  float top, add_hi, add_lo, mul_hi, mul_lo;  // add_hi NaN: the row has no continuation
 };
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = __fadd_rn(a, b);
@@ -126,16 +129,18 @@ __device__ __forceinline__ void fast_two_sum(float a, float b, float& s, float& 
   s = __fadd_rn(a, b);
   e = __fsub_rn(b, __fsub_rn(s, a));
 }
-// x plus what the row adds.
+// (x - top) plus what the row adds; not finite where that is below the range.
 __device__ __forceinline__ float2 total_of(const RowKey& r, float x) {
-  float s, e;
-  two_sum(r.add_hi, x, s, e);
-  fast_two_sum(s, __fadd_rn(e, r.add_lo), s, e);
+  float d, f, s, e;
+  two_sum(x, -r.top, d, f);
+  two_sum(r.add_hi, d, s, e);
+  two_sum(s, __fadd_rn(e, __fadd_rn(f, r.add_lo)), s, e);
   return make_float2(s, e);
 }
 __device__ __forceinline__ uint64_t key_of(const RowKey& r, float x) {
   if (!(x > -INFINITY) || isnan(r.add_hi)) return 0;
   const float2 t = total_of(r, x);
+  if (!isfinite(t.x)) return 0;
   float p = __fmul_rn(t.x, r.mul_hi);
   float q = __fmaf_rn(t.x, r.mul_hi, -p);
   q = __fmaf_rn(t.x, r.mul_lo, __fmaf_rn(t.y, r.mul_hi, q));
@@ -325,16 +330,17 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
       for (int d = 16; d; d /= 2) S += __shfl_xor_sync(0xffffffffu, S, d);
     }
     if (lane == 0) {
-      s_row[w].add_hi = M;
+      s_row[w].top = M;
       s_row[w].add_lo = S;
       s_done[w] = done;
     }
   }
   __syncthreads();
   if (i < a.W) {  // a lane per row: see above
-    const float sc = a.scores[row0 + i], M = s_row[i].add_hi, S = s_row[i].add_lo;
-    const double add = s_done[i] ? (double)sc : ((double)sc - (double)M) - log((double)S);
+    const float sc = a.scores[row0 + i], M = s_row[i].top, S = s_row[i].add_lo;
+    const double add = s_done[i] ? (double)sc : (double)sc - log((double)S);
     RowKey r;
+    r.top = M;
     r.add_hi = (float)add;
     r.add_lo = (float)(add - (double)r.add_hi);
     r.mul_hi = 1.0f;
@@ -387,7 +393,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
 #pragma unroll
     for (int k = 0; k < kChunkMin / 32; ++k) y[k] = v0 + k * 32 + lane < a.V ? __ldcg(x + k * 32 + lane) : -INFINITY;
     // What is below the bound by more than fp32 can err is left out (few stay), the others' keys are formed.
-    const float level = unordered((uint32_t)(bound >> 32)) / row.mul_hi, least = level - row.add_hi - 1e-5f * (fabsf(level) + fabsf(row.add_hi));
+    const float level = unordered((uint32_t)(bound >> 32)) / row.mul_hi,
+                least = level - row.add_hi + row.top - 1e-5f * (fabsf(level) + fabsf(row.add_hi) + fabsf(row.top));
     unsigned may = 0;
 #pragma unroll
     for (int k = 0; k < kChunkMin / 32; ++k) may |= (y[k] > -INFINITY && !(y[k] < least) ? 1u : 0u) << k;
