@@ -564,8 +564,9 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
  * A finished beam (done[b] != 0) has one continuation, token eos, with total = scores[b] ranked by total / max(lengths[b], 1)^alpha. Of
  * each group the K best in order, ties by the lower beam, then the lower token: parent (the beam's row, for nt_page_fork),
  * token, score (total) and done_out (1: finished before or by eos), [N / W][K] each; -1, -1, -inf and 0 where there are fewer.
- * Sums run in fp32 and are joined in 64 bits, ranks are compared in pairs of fp32 (48 bits): score is within 2^-22 of the exact one, relative
- * to the larger of it and the logits. A logit of NaN or -inf is never chosen and adds nothing, nor is a total below the range of fp32 chosen; a
+ * Sums of exponentials run in fp32: score is within 2^-22 of the exact one, relative to the larger of it and the logits. Ranks are compared
+ * in pairs of fp32 (48 bits), so a beam's own continuations come in the order of their logits. All of them carry the error of their row's
+ * log-sum alike (some 2^-23, 2^-17 at the very most), so continuations of different beams are told apart where they differ by more. A logit of NaN or -inf is never chosen and adds nothing, nor is a total below the range of fp32 chosen; a
  * beam whose score is not finite, or with a logit of +inf, has no continuation.
  *   1 <= W, K <= 64; N a multiple of W, N <= 65536; V <= 2^24; eos -1 (none) or below V; 0 <= alpha <= 4 (0: lengths not
  *   needed); done_opt, lengths_opt [N] int32; outputs must not overlap inputs

@@ -5,8 +5,12 @@
 // The largest logit comes off first: where a mask has put a whole row at the type's lowest value, score and log S would be lost in it (such
 // a beam's keys came out as 0, above every other).
 //
-// Keys are compared in pairs of fp32 (a sum of two, 48 bits), ties by the lower beam and then the lower token: beams of a
-// group often have continuations closer than fp32 tells apart at their scores' size.
+// Keys are compared in pairs of fp32 (a sum of two, 48 bits), ties by the lower beam and then the lower token: continuations of a beam are
+// often closer than fp32 tells apart at its score's size. Between beams the order is as good as log S, which all continuations
+// of a beam share: S is summed in fp32. At the very most log S is off by 2^-18 for up to 262,144 tokens and 2^-17 for more (a term that matters
+// is D = log V below the largest at most; subtractions and exponents cost 2 D steps of 2^-24, three exponentials 4 each, sums 31 and
+// one for every further 512 elements of a chunk), and as a rule by 2^-23 (2^-21.5 where all but one of 151,936 are alike). Weights in more than fp32 would take as long as reading the
+// logits does, or longer.
 //
 // The first kernel reads the logits once: for every chunk of a row its maximum and the sum of e^(x - maximum), and the row's
 // 1 / len^alpha beside. The second one, a CTA per group, joins the sums and then reads again only the K chunks that can hold
