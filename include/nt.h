@@ -120,8 +120,8 @@ nt_status nt_workspace_status(const void* ws, nt_status* device_status);
  * timeout_ms (<= 0 keeps the normal limits) and the call's workspace reports NT_ERR_TIMEOUT.
  *   fault 1: the streaming output projection (nt_int8_logits_argmax and its allocation-free
  *            variant at B = 1); 2: the tcgen05 path of nt_ternary_gemm (2..16 vectors with a
- *            workspace, N >= 128); 3: the prefill GEMM (64 or more vectors); 5: nt_tree_attention; 6: nt_paged_attention
- *   on the tensor cores; 0: none (4 is not assigned).
+ *            workspace, N >= 128); 3: the prefill GEMM (64 or more vectors); 5: nt_tree_attention; 6: nt_paged_attention;
+ *   0: none (4 is not assigned).
  * Process-wide; set it only while no other thread launches library calls. No GPU fault is
  * involved: every wait gives up cleanly and the context stays usable. */
 nt_status nt_set_test_fault(int fault, double timeout_ms);

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(FewShape<T, D, R>::kThreads, 1)
     for (int h = 0; h < kSubs; ++h) id[h] = next + 16 * h < next_hi && !(notes >> h & 1) ? ids[(next + 16 * h) >> a.shift] : -1;
   };
   auto enter = [&] {  // the next piece of which this warp has a block
-    for (; ahead.more(); ahead.next(a)) {
+    for (; ahead.more() && a.fault == 0; ahead.next(a)) {
       ap = ahead.piece(a);
       next = (ap.u.tile0 + ap.t0) * kFewKeys + warp * S::kBlock;
       next_hi = min(ap.u.p1 + 1, (ap.t0 + ap.u.tile0 + ap.n) * kFewKeys);

@@ -12,7 +12,7 @@ constexpr int kPagedMaxTokens = 1 << 20;    // new tokens of a call
 constexpr int kCopyPairs = 1024;            // pairs that a CTA of the copy holds at a time
 constexpr int kBeamMaxRows = 65536;         // rows of logits of a beam selection
 constexpr int kBeamMaxVocab = 1 << 24;
-constexpr int kFaultPaged = 6;              // nt_set_test_fault: nt_paged_attention on the tensor cores issues no copies
+constexpr int kFaultPaged = 6;              // nt_set_test_fault: nt_paged_attention issues no copies
 
 inline bool page_ok(int page) { return page >= 16 && page <= 256 && (page & (page - 1)) == 0; }
 inline int page_shift(int page) {
