@@ -415,6 +415,7 @@ PyObject* copy(PyObject*, PyObject* const* x, Py_ssize_t n) {
     const auto* p = flat<int32_t>(x[7], "pairs", kI32, {m, 2});
     t_call->add("the caches", at < 0 ? c10::Device(c10::kCPU) : c10::Device(c10::kCUDA, (c10::DeviceIndex)at));
     void* st = stream_of(x[8]);
+    if (m == 0) return NT_OK;  // of a pool of one page
     return released([&] { return p_copy(kp, vp, L, Hkv, D, ts, page, p, (int)m, st); });
   });
 }

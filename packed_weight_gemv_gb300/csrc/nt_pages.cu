@@ -415,7 +415,7 @@ nt_status nt_page_compact_workspace_size(int n_pages, size_t* bytes) {
 nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int32_t* length, int S, int width, int page, int32_t* pairs,
                           int n, int32_t* n_used, uint32_t* n_bad_opt, void* ws, size_t ws_bytes, void* stream) {
   clear_error();
-  if (!refs || !table || !length || !pairs || !n_used) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
+  if (!refs || !table || !length || (!pairs && n != 0) || !n_used) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
   NT_TRY(check_pages(page, n_pages, width));
   if (S < 1 || S > kPageMaxSeqs || n < n_pages / 2) return set_error(NT_ERR_INVALID_ARG, "need 1 <= S <= 4096 and n >= n_pages / 2");
   if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(length, 4) || !aligned(pairs, 4) || !aligned(n_used, 4) ||

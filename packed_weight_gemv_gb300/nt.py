@@ -513,7 +513,7 @@ def nt_page_extend(table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor
 
 def nt_page_copy(k_caches: pointer_array, v_caches: pointer_array, Hkv: int, D: int, t_stride: int, page: int,
                  pairs: torch.Tensor, stream=None):
-    """Copies page pairs[i, 0] to page pairs[i, 1] in every layer's caches (pointer_array)."""
+    """Copies page pairs[i, 0] to page pairs[i, 1] in every layer's caches (pointer_array); none where pairs is empty."""
     n = _layers("nt_page_copy", k_caches, v_caches, Hkv, D, t_stride)
     _native().copy(k_caches.address, v_caches.address, n, Hkv, D, t_stride, page, pairs, stream, k_caches.cuda_device)
 
