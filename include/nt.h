@@ -515,12 +515,12 @@ nt_status nt_page_extend(int32_t* table, int32_t* length, int S, int width, cons
 /* Copies of whole pages in every layer: for i < n, page pairs[i][1] <- page pairs[i][0] of every head of every cache; a pair with a
  * page outside [0, t_stride / page) is passed over. No page may be written twice, nor read and written. k_caches, v_caches: host arrays
  * of n_layers device pointers to [Hkv][t_stride][D] bf16 (16-byte aligned); D a multiple of 8 up to 256; Hkv <= 65535. pairs [n][2]
- * device int32, n >= 1, from nt_page_extend or nt_page_compact. */
+ * device int32, 1 <= n <= 2^30, from nt_page_extend or nt_page_compact. */
 nt_status nt_page_copy(uint16_t* const* k_caches, uint16_t* const* v_caches, int n_layers, int Hkv, int D, int t_stride, int page,
                        const int32_t* pairs, int n, void* stream);
 
 /* Moves the pages in use to the front of the pool. With U pages in use (*n_used, device), the i-th page in use at U or behind goes to the
- * i-th free page below U: pairs[i] = (from, to), for nt_page_copy, and (-1, -1) behind the last one (n >= n_pages / 2 pairs; n 0 and pairs
+ * i-th free page below U: pairs[i] = (from, to), for nt_page_copy, and (-1, -1) behind the last one (n_pages / 2 <= n <= 2^30 pairs; n 0 and pairs
  * NULL will do for a pool of one page, which leaves nothing to copy). The
  * tables' used entries and refs follow; pages that no table names but refs counts move too, and the caller finds them by pairs.
  * Entries outside [0, n_pages) stay and are counted in n_bad_opt.

@@ -375,8 +375,8 @@ nt_status nt_page_copy(uint16_t* const* k_caches, uint16_t* const* v_caches, int
   clear_error();
   if (!k_caches || !v_caches || !pairs) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
   if (!page_ok(page)) return set_error(NT_ERR_INVALID_ARG, "page must be 16, 32, 64, 128 or 256 rows");
-  if (n_layers < 1 || Hkv < 1 || Hkv > 65535 || t_stride < page || n < 1)
-    return set_error(NT_ERR_INVALID_ARG, "need n_layers >= 1, 1 <= Hkv <= 65535, t_stride >= page and n >= 1");
+  if (n_layers < 1 || Hkv < 1 || Hkv > 65535 || t_stride < page || n < 1 || n > kPageMaxPairs)
+    return set_error(NT_ERR_INVALID_ARG, "need n_layers >= 1, 1 <= Hkv <= 65535, t_stride >= page and 1 <= n <= 2^30");
   if (D < 8 || D > 256 || D % 8 != 0) return set_error(NT_ERR_UNSUPPORTED, "head dimension must be a multiple of 8 up to 256");
   if (!aligned(pairs, 4)) return set_error(NT_ERR_ALIGNMENT, "int32 arrays must be 4-byte aligned");
   for (int i = 0; i < n_layers; ++i) {
@@ -417,7 +417,8 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
   clear_error();
   if (!refs || !table || !length || (!pairs && n != 0) || !n_used) return set_error(NT_ERR_INVALID_ARG, "NULL pointer");
   NT_TRY(check_pages(page, n_pages, width));
-  if (S < 1 || S > kPageMaxSeqs || n < n_pages / 2) return set_error(NT_ERR_INVALID_ARG, "need 1 <= S <= 4096 and n >= n_pages / 2");
+  if (S < 1 || S > kPageMaxSeqs || n < n_pages / 2 || n > kPageMaxPairs)
+    return set_error(NT_ERR_INVALID_ARG, "need 1 <= S <= 4096 and n_pages / 2 <= n <= 2^30");
   if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(length, 4) || !aligned(pairs, 4) || !aligned(n_used, 4) ||
       (n_bad_opt && !aligned(n_bad_opt, 4)))
     return set_error(NT_ERR_ALIGNMENT, "int32 arrays must be 4-byte aligned");

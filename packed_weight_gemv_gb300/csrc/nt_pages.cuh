@@ -10,6 +10,7 @@ namespace nt {
 constexpr int kPageMaxSeqs = 4096;          // sequences of a call
 constexpr int kPagedMaxTokens = 1 << 20;    // new tokens of a call
 constexpr int kCopyPairs = 1024;            // pairs that a CTA of the copy holds at a time
+constexpr int kPageMaxPairs = 1 << 30;      // of a copy or a compaction: 2 n stays an int
 constexpr int kBeamMaxRows = 65536;         // rows of logits of a beam selection
 constexpr int kBeamMaxVocab = 1 << 24;
 constexpr int kFaultPaged = 6;              // nt_set_test_fault: nt_paged_attention issues no copies
