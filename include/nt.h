@@ -536,7 +536,9 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *   out[t][h] = sum_j softmax_j(x) v[j]
  * keys and values of head h / (Hq / Hkv). Tokens at q_start[S] and behind are left as they were; a token that sees nothing gets
  * 0. What a token does not see has no part in its result, whatever it holds: rows behind the sequence's in its last page, and later
- * tokens', may be NaN or infinite. A score or value that is seen and not finite makes the result NaN or infinite.
+ * tokens', may be NaN or infinite. A value that is seen and not finite, or a score of NaN or +inf, makes the result NaN or infinite; a score of
+ * -inf has weight 0 (with fp32 queries it may come out as NaN), and a token that sees no other gets 0. Weights go up to 2^32 before
+ * they are divided by their sum, so finite values are to stay below 2^64.
  *   q, out [T][Hq][D] of type dtype (nt_dtype; out may be q), q's tokens q_stride elements apart (a multiple of 8); k_pool, v_pool [Hkv][t_stride][D] bf16;
  *     D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 64, T * Hq <= 2^24; all 16-byte aligned
  *   table [S][width], q_start [S + 1] (rising; values taken as within [0, T]), length [S] (taken as within [0, width * page])
@@ -567,8 +569,9 @@ nt_status nt_paged_attention(const void* q, int dtype, int64_t q_stride, const u
  * token, score (total) and done_out (1: finished before or by eos), [N / W][K] each; -1, -1, -inf and 0 where there are fewer.
  * Sums of exponentials run in fp32: score is within 2^-22 of the exact one, relative to the larger of it and the logits. Ranks are compared
  * in pairs of fp32 (48 bits), so a beam's own continuations come in the order of their logits. All of them carry the error of their row's
- * log-sum alike (some 2^-23, 2^-17 at the very most), so continuations of different beams are told apart where they differ by more. A logit of NaN or -inf is never chosen and adds nothing, nor is a total below the range of fp32 chosen; a
- * beam whose score is not finite, or with a logit of +inf, has no continuation.
+ * log-sum alike (some 2^-23, 2^-17 at the very most), so continuations of different beams are told apart where they differ by more. A
+ * logit of NaN or -inf is never chosen and adds nothing, nor is a total below the range of fp32 chosen; a beam whose score is not finite, or with
+ * a logit of +inf, has no continuation.
  *   1 <= W, K <= 64; N a multiple of W, N <= 65536; V <= 2^24; eos -1 (none) or below V; 0 <= alpha <= 4 (0: lengths not
  *   needed); done_opt, lengths_opt [N] int32; outputs must not overlap inputs
  *   ws: nt_beam_select_workspace_size(V, N) bytes (16-byte aligned; scratch; calls sharing it must not overlap) */
