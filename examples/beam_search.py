@@ -20,7 +20,7 @@ if ROOT not in sys.path:
 from examples.tree_verify import Decoder  # noqa: E402
 from packed_weight_gemv_gb300 import nt  # noqa: E402
 
-CHUNK = 48  # new tokens of a pass over prompts
+CHUNK = 48  # new tokens of a pass over prompts, and rows of a projection at a time (from 64 on it wants a workspace)
 
 
 class PagedDecoder(Decoder):
@@ -30,7 +30,7 @@ class PagedDecoder(Decoder):
         super().__init__(rows=n_pages * page, seed=seed, **shape)
         self.page, self.n_pages, self.most = page, n_pages, most
         i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=self.dev)  # noqa: E731
-        self.width = n_pages // 4
+        self.width = n_pages  # of a sequence at most
         self.pages, self.length = i32(0, self.width), i32(0)
         self.refs = i32(n_pages)
         self.ws_paged = torch.zeros(nt.nt_paged_attention_workspace_size(max(most, CHUNK), most, self.Hq, self.Hkv, self.D),
@@ -41,6 +41,9 @@ class PagedDecoder(Decoder):
 
     def ints(self, a):
         return torch.tensor(a, dtype=torch.int32, device=self.dev)
+
+    def project(self, i, x):
+        return torch.cat([super(PagedDecoder, self).project(i, part.contiguous()) for part in x.split(CHUNK)])
 
     def fork(self, parent):
         """Sequence i goes on as sequence parent[i] (-1: empty)."""
@@ -112,6 +115,8 @@ class PagedDecoder(Decoder):
 
 def search(model, prompts, beams, tokens, eos, alpha=0.6, compact_every=0):
     """The best continuation of every prompt as (tokens, score), its beams' in order."""
+    if not all(prompts) or len(prompts) * beams > model.most:
+        raise ValueError(f"prompts must have tokens, and prompts times beams be at most {model.most}")
     G, dev = len(prompts), model.dev
     model.refs.zero_()
     model.pages, model.length = model.pages[:0], model.length[:0]
@@ -140,15 +145,18 @@ def search(model, prompts, beams, tokens, eos, alpha=0.6, compact_every=0):
     return [[(lines[g * beams + b], float(scores[g * beams + b])) for b in range(beams)] for g in range(G)]
 
 
-def main():
+def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("--beams", type=int, default=4)
+    ap.add_argument("--beams", type=int, default=4, help="1 to 64")
     ap.add_argument("--tokens", type=int, default=40)
     ap.add_argument("--seed", type=int, default=0)
-    args = ap.parse_args()
-    model = PagedDecoder(seed=args.seed)
+    args = ap.parse_args(argv)
+    page, sizes = 16, (70, 5, 33)
+    # a pool that no search can exhaust: the prompts' pages, and per beam those of its own tokens with the two it shares in part
+    n_pages = sum(n // page + 1 for n in sizes) + len(sizes) * args.beams * (args.tokens // page + 3)
+    model = PagedDecoder(most=len(sizes) * args.beams, page=page, n_pages=max(64, n_pages), seed=args.seed)
     rs = np.random.RandomState(args.seed)
-    prompts = [rs.randint(0, model.V, n).tolist() for n in (70, 5, 33)]
+    prompts = [rs.randint(0, model.V, n).tolist() for n in sizes]
     for prompt, found in zip(prompts, search(model, prompts, args.beams, args.tokens, eos=model.V - 1)):
         line, score = found[0]
         print(f"prompt of {len(prompt)}: {len(line)} tokens, log probability {score:.3f}, begins {line[:6]}; the beams' {[round(s, 2) for _, s in found]}")
