@@ -198,7 +198,8 @@ nt_status nt_ternary_gemv(const void* w, int layout, const float* s_w, int N, in
  * calls sharing it must not overlap) the call runs on the tensor cores: from N >= 128 on
  * tcgen05 with the decoded trits in tensor memory (e4m3) and the activations split exactly
  * into two e4m3 digits kept in the workspace, below that f16 mma.sync; int32 partial sums of
- * K parts meet in the workspace, which every call leaves zero apart from the digit rows.
+ * K parts meet in the workspace, which every call leaves zero apart from the digit rows (so a workspace serves calls
+ * of one N, K and B: it must be zero-filled again before a call of others).
  * With ws NULL or short it runs the dp4a kernel. Otherwise the size is 0 and ws may be NULL.
  */
 /* Every workspace of this call starts with the 16-byte status header nt_workspace_status
@@ -317,7 +318,8 @@ nt_status nt_verify_accept(const int32_t* draft, const int32_t* argmax, int B, i
  *   q [B][Hq][D] fp32; k_cache, v_cache [Hkv][t_stride][D] bf16 bit patterns (16-byte
  *   aligned); out [B][Hq][D] fp32; Hq / Hkv in {1, 2, 4, 8}; 1 <= B <= 64; B <= T <= t_stride.
  *   ws: device workspace of nt_attention_workspace_size(B, Hq, Hkv, T) bytes (16-byte
- *   aligned), all zero before its first use (every call leaves its counters zero again);
+ *   aligned), all zero before its first use (every call leaves its counters zero again); calls of any B and T may follow one
+ *   another on one that is large enough for each (the size does not rise with T throughout), as long as Hkv is the same;
  *   calls sharing a workspace must not overlap.
  */
 nt_status nt_attention_workspace_size(int B, int Hq, int Hkv, int T, size_t* bytes);

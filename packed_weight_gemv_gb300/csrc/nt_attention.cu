@@ -19,6 +19,7 @@ constexpr int kAttnStep = 16;      // cache positions per warp step (two 8-posit
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnMaxSplit = 512;
+constexpr int kAttnMaxB = 64;      // new positions of a call
 constexpr int kPartRow = kAttnD + 4;  // floats per partial result: weighted sum, max, sum, padding
 constexpr float kAttnLazy = 8.0f;     // a running maximum is raised only once a score exceeds it by 2^8
 
@@ -591,14 +592,15 @@ size_t attn_part_bytes(int B, int Hq, int Hkv, int T) {
 
 }  // namespace
 
-size_t attention_ws_bytes(int B, int Hq, int Hkv, int T) {
-  return attn_part_bytes(B, Hq, Hkv, T) + sizeof(unsigned int) * (size_t)B * Hkv;
-}
+// The counters come first, as many as any call with these key-value heads has: where the parts of calls of other lengths or numbers of
+// positions end must not be where a call's counters stand.
+static size_t attn_count_bytes(int Hkv) { return ((size_t)kAttnMaxB * Hkv * sizeof(unsigned int) + 255) / 256 * 256; }
+size_t attention_ws_bytes(int B, int Hq, int Hkv, int T) { return attn_count_bytes(Hkv) + attn_part_bytes(B, Hq, Hkv, T); }
 
 nt_status launch_attention(const float* q, const uint16_t* kc, const uint16_t* vc, int B, int Hq, int Hkv, int T,
                            int ts, float* out, void* ws, cudaStream_t st, const int* T_dev, bool pdl) {
-  float* part = static_cast<float*>(ws);
-  unsigned int* done = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + attn_part_bytes(B, Hq, Hkv, T));
+  unsigned int* done = static_cast<unsigned int*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn_count_bytes(Hkv));
   const int G = Hq / Hkv;
   AttnArgs a{q, kc, vc, part, done, out, B, Hq, Hkv, T, ts, attn_units(T, Hkv, G), attn_span(T, Hkv, G),
              (float)(1.4426950408889634 / sqrt((double)kAttnD)), T_dev};
@@ -646,7 +648,7 @@ nt_status nt_attention_decode(const float* q, const uint16_t* k_cache, const uin
   if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return set_error(NT_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
   const int G = Hq / Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8) return set_error(NT_ERR_UNSUPPORTED, "Hq / Hkv must be 1, 2, 4 or 8");
-  if (B < 1 || B > 64 || T < B || t_stride < T) return set_error(NT_ERR_INVALID_ARG, "need 1 <= B <= 64, B <= T <= t_stride");
+  if (B < 1 || B > kAttnMaxB || T < B || t_stride < T) return set_error(NT_ERR_INVALID_ARG, "need 1 <= B <= 64, B <= T <= t_stride");
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 4) || !aligned(ws, 16))
     return set_error(NT_ERR_ALIGNMENT, "q, caches and workspace must be 16-byte aligned");
   if (ws_bytes < attention_ws_bytes(B, Hq, Hkv, T)) return set_error(NT_ERR_WORKSPACE, "workspace too small");
