@@ -635,6 +635,8 @@ nt_status nt_attention_workspace_size(int B, int Hq, int Hkv, int T, size_t* byt
   clear_error();
   if (!bytes || B < 1 || Hq < 1 || Hkv < 1 || T < 1)
     return set_error(NT_ERR_INVALID_ARG, "need B, Hq, Hkv, T >= 1 and a result pointer");
+  check_device();  // the parts go by the number of SMs (without a device: of one)
+  clear_error();
   *bytes = attention_ws_bytes(B, Hq, Hkv, T);
   return NT_OK;
 }
