@@ -14,15 +14,16 @@
 // while the other group's weights are formed, and a commit behind an S also tells that the O before it is done; warps 4-7 and 8-11 are
 // the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
 //
-// fp32 queries enter as three bf16 terms without loss and their weights as two rounded ones (2^-17); bf16 queries' weights are rounded to
-// bf16 (2^-8, next to the output's own 2^-8; the sum of the weights is that of the unrounded ones: taking the rounded ones' cost two half-rate
-// instructions a pair). The tensor core
+// fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17). For bf16 queries one term would do
+// with two products for three (ragged prompts of 8,000 tokens 626 us for 795, 257 among decoding sequences 93 for 96, 32 over 8,000 25.3 for 26.5), but its 2^-8
+// stands beside the output's own: 1.28 to 1.41 times the error of rounding the output alone, which is all that two terms leave, and
+// a token would be less exact in a chunk than by itself. The tensor core
 // cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
 // that round to nearest.
 //
-// Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 430 us (1,320 TFLOP/s),
-// ragged prompts of 8,000 tokens together 624 us (1,190), 511 fp32 tokens over 7,489 123 us (five products for one, 1,320 of
-// them). Keys and values from L2 alone would take half of that, the exponentials three quarters. What a call pays
+// Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 552 us (three products for
+// two, 1,560 TFLOP/s of them), ragged prompts of 8,000 tokens together 794 us (1,400; 839 with cold caches), 511 fp32 tokens over 7,489 124
+// us (127 cold; five products for two, 1,310 of them). Keys and values from L2 alone would take half of that, the exponentials three quarters. What a call pays
 // besides is about 25 us: 13 to the end of a first tile, 6 for the join of parts.
 #include <math.h>
 
@@ -53,7 +54,7 @@ struct PmMaps {
 template <typename T, int D, bool kPair>
 struct PmShape {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kTermsQ = kF32 ? 3 : 1, kTermsP = kF32 ? 2 : 1;
+  static constexpr int kTermsQ = kF32 ? 3 : 1, kTermsP = 2;
   static constexpr int kRows = kPair ? 256 : 128;
   static constexpr int kSlot = kPmKeys * D * 2;
   static constexpr int kQTile = 128 * D * 2;  // one term of 128 rows
@@ -64,7 +65,7 @@ struct PmShape {
   // fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
   static constexpr int kStart = kPair ? 8 : 3;
   static constexpr int kColO = 0, kColS = 2 * D;
-  // A tile costs a sum at most 16 (fp32) or 8 cuts of 2^-23: 2^-16 over 8 tiles, 2^-14 over 64. (fp32, 511 tokens over 7,489: 3.4e-6 off
+  // A tile costs a sum at most 16 cuts of 2^-23: 2^-16 over 8 tiles, 2^-13 over 64. (fp32, 511 tokens over 7,489: 3.4e-6 off
   // in 124 us; every 4 tiles 2.7e-6 in 135, every 2 2.5e-6 in 154, as the weights' two terms are left. A third term has no place: 192
   // columns for P next to S and O of two groups.)
   static constexpr int kFlush = kF32 ? 8 : 64;
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] *= f;
               if (a.cap > 0.0f) {
-                bool big = !S::kF32 && a.cap <= 256.0f;  // 2^-21 of it is nothing next to bf16 weights, and the series takes as long
+                bool big = !S::kF32 && a.cap <= 256.0f;  // 2^-21 of it is nothing next to a bf16 output, and the series takes as long
 #pragma unroll
                 for (int e = 0; e < 32; ++e) big |= !(fabsf(r[e]) < kCapSmall);
                 if (__any_sync(0xffffffffu, big)) {
@@ -521,14 +522,10 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
               const float2 y = fma2(make_float2(s[ch + e], s[ch + e + 1]), sc, mm);
               const float2 pp = make_float2(ex2(y.x), ex2(y.y));
               ls = add2(ls, pp);
-              if constexpr (S::kF32) {
-                uint32_t term[2];
-                split(pp.x, pp.y, term);
-                w[0][e / 2] = term[0];
-                w[1][e / 2] = term[1];
-              } else {
-                w[0][e / 2] = pack_rn(pp.x, pp.y);
-              }
+              uint32_t term[S::kTermsP];
+              split(pp.x, pp.y, term);
+#pragma unroll
+              for (int t = 0; t < S::kTermsP; ++t) w[t][e / 2] = term[t];
             }
 #pragma unroll
             for (int t = 0; t < S::kTermsP; ++t) tm_store(scol + t * (kPmKeys / 2) + ch / 2, w[t]);
