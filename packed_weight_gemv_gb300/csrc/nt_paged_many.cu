@@ -15,14 +15,14 @@
 // the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
 //
 // fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17). For bf16 queries one term would do
-// with two products for three (ragged prompts of 8,000 tokens 626 us for 795, 257 among decoding sequences 93 for 96, 32 over 8,000 25.3 for 26.5), but its 2^-8
+// with two products for three (ragged prompts of 8,000 tokens 626 us for 776, 257 among decoding sequences 93 for 94, 32 over 8,000 25.3 for 26.9), but its 2^-8
 // stands beside the output's own: 1.28 to 1.41 times the error of rounding the output alone, which is all that two terms leave, and
 // a token would be less exact in a chunk than by itself. The tensor core
 // cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
 // that round to nearest.
 //
-// Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 552 us (three products for
-// two, 1,560 TFLOP/s of them), ragged prompts of 8,000 tokens together 794 us (1,400; 839 with cold caches), 511 fp32 tokens over 7,489 124
+// Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 549 us (three products for
+// two, 1,560 TFLOP/s of them), ragged prompts of 8,000 tokens together 776 us (1,430), 511 fp32 tokens over 7,489 124
 // us (127 cold; five products for two, 1,310 of them). Keys and values from L2 alone would take half of that, the exponentials three quarters. What a call pays
 // besides is about 25 us: 13 to the end of a first tile, 6 for the join of parts.
 #include <math.h>
@@ -61,9 +61,9 @@ struct PmShape {
   static constexpr int kQBytes = kQTile * kTermsQ * (kPair ? 2 : 1);
   static constexpr int kStages = std::min(8, (kPmSmem - kQBytes) / kSlot);
   static constexpr int kAhead = kPair ? 1 : 2;  // tiles whose scores are formed before the first weights
-  // What a piece's start and end cost in tiles. Measured, bf16 in pairs: ragged prompts 1,026 us with 2, 897 with 3, 651 with 6 and 10;
-  // fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
-  static constexpr int kStart = kPair ? 8 : 3;
+  // What a piece's start and end cost in tiles. Measured, bf16 in pairs: ragged prompts 817 us with 4, 776 with 5, 780 with 6, 794 with 8, 808
+  // with 10; a chunk among decoding sequences 91, 94, 95, 96, 99. fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
+  static constexpr int kStart = kPair ? 5 : 3;
   static constexpr int kColO = 0, kColS = 2 * D;
   // A tile costs a sum at most 16 cuts of 2^-23: 2^-16 over 8 tiles, 2^-13 over 64. (fp32, 511 tokens over 7,489: 3.4e-6 off
   // in 124 us; every 4 tiles 2.7e-6 in 135, every 2 2.5e-6 in 154, as the weights' two terms are left. A third term has no place: 192
