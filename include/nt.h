@@ -553,7 +553,7 @@ nt_status nt_page_compact(int32_t* refs, int n_pages, int32_t* table, const int3
  *     sharing it must not overlap). Calls of any sizes may follow one another on it: its counters stand at one place and are left zero.
  *     It starts with the status header of nt_workspace_status.
  * Products of queries and keys are exact, scores and statistics fp32. Weights are two bf16 terms (within 2^-17), and fp32 with fp32 queries
- * where a sequence has up to 8 rows (tokens x Hq / Hkv).
+ * where D is 64 or a sequence has up to 8 rows (tokens x Hq / Hkv).
  * The capped score is within 2^-21 of the cap, and within some roundings of itself where |x| < cap / 4 (bf16 queries: and the
  * cap is above 256). Sums lose at most 2^-12 of the sum of their terms' magnitudes with bf16 queries and 2^-16 with fp32 ones, before the
  * output is rounded. */

@@ -14,7 +14,8 @@
 // while the other group's weights are formed, and a commit behind an S also tells that the O before it is done; warps 4-7 and 8-11 are
 // the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
 //
-// fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17). For bf16 queries one term would do
+// fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17), those of fp32 queries with D 64 as three
+// without loss. For bf16 queries one term would do
 // with two products for three (ragged prompts of 8,000 tokens 626 us for 776, 257 among decoding sequences 93 for 94, 32 over 8,000 25.3 for 26.9), but its 2^-8
 // stands beside the output's own: 1.28 to 1.41 times the error of rounding the output alone, which is all that two terms leave, and
 // a token would be less exact in a chunk than by itself. The tensor core
@@ -54,7 +55,8 @@ struct PmMaps {
 template <typename T, int D, bool kPair>
 struct PmShape {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int kTermsQ = kF32 ? 3 : 1, kTermsP = 2;
+  static constexpr int kTermsQ = kF32 ? 3 : 1, kTermsP = kF32 && D == 64 ? 3 : 2;
+  static constexpr int kScoreCols = std::max(kPmKeys, kTermsP * kPmKeys / 2);  // of a group: its weights' terms stand in the place of its scores
   static constexpr int kRows = kPair ? 256 : 128;
   static constexpr int kSlot = kPmKeys * D * 2;
   static constexpr int kQTile = 128 * D * 2;  // one term of 128 rows
@@ -65,13 +67,14 @@ struct PmShape {
   // with 10; a chunk among decoding sequences 91, 94, 95, 96, 99. fp32: 511 tokens over 7,489 123 us with 3, 127 with 6.
   static constexpr int kStart = kPair ? 5 : 3;
   static constexpr int kColO = 0, kColS = 2 * D;
-  // A tile costs a sum at most 16 cuts of 2^-23: 2^-16 over 8 tiles, 2^-13 over 64. (fp32, 511 tokens over 7,489: 3.4e-6 off
-  // in 124 us; every 4 tiles 2.7e-6 in 135, every 2 2.5e-6 in 154, as the weights' two terms are left. A third term has no place: 192
-  // columns for P next to S and O of two groups.)
-  static constexpr int kFlush = kF32 ? 8 : 64;
+  // A tile costs a sum at most 8 cuts of 2^-23 for every term of the weights: 2^-16 over 8 tiles (three terms: 4), 2^-13 over 64. (fp32, 511
+  // tokens over 7,489. D 64: 81 us and 3.3e-6 off with two terms, 98 us and 1.7e-6 with three, as torch's own products in fp32. D 128: 124
+  // us and 3.3e-6; every 4 tiles 135 and 2.7e-6, every 2 155 and 2.5e-6, as the two terms are left; a third has no place, 192 columns for P next
+  // to S and O of two groups, but with tiles of 64 keys, whose scores read the queries' terms twice as often: 172 us and 1.9e-6.)
+  static constexpr int kFlush = kF32 ? (kTermsP == 3 ? 4 : 8) : 64;
   static constexpr int kSmem = kQBytes + kStages * kSlot + 1024;
   static_assert(kStages >= 4, "ring");
-  static_assert(kColS + 2 * kPmKeys <= kTaTmemCols, "tensor-memory columns");
+  static_assert(kColS + 2 * kScoreCols <= kTaTmemCols, "tensor-memory columns");
   static_assert(kPageMaxSeqs * 4 <= kStages * kSlot, "the division's scratch stands in the ring");
 };
 
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         PaPiece p = walk.piece(a);
         const int n = p.n;
         auto scores = [&](int x, int k) {
-          const uint32_t d = tmem + S::kColS + x * kPmKeys;
+          const uint32_t d = tmem + S::kColS + x * S::kScoreCols;
           const uint64_t bd = sdesc(slot(k), 16);
           // the smallest terms first: the tensor core cuts its sums off, so a sum loses least while it is small
 #pragma unroll
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
           for (int t = S::kTermsP - 1; t >= 0; --t)
 #pragma unroll
             for (int kk = 0; kk < kPmKeys / 16; ++kk)  // 16 keys: 2,048 bytes of each 64 dimensions
-              mma_tmem_a(tmem + S::kColO + x * D, tmem + S::kColS + x * kPmKeys + t * (kPmKeys / 2) + 8 * kk, bd + kk * 2048 / 16,
+              mma_tmem_a(tmem + S::kColO + x * D, tmem + S::kColS + x * S::kScoreCols + t * (kPmKeys / 2) + 8 * kk, bd + kk * 2048 / 16,
                          idesc_bf16(D, true, t == 1), t < S::kTermsP - 1 || kk > 0 || !fresh);
           if (last) mma_commit(empty(kv));
           if (next < n) {
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
       const int cnt = kPair ? n : (n + 1 - x) / 2;
       const int key_first = (u.tile0 + p.t0) * kPmKeys;
       auto partial = [&](int key) { return key + kPmKeys - 1 > u.p0 || key < sure_lo; };
-      const uint32_t scol = tl + S::kColS + x * kPmKeys, ocol = tl + S::kColO + x * D;
+      const uint32_t scol = tl + S::kColS + x * S::kScoreCols, ocol = tl + S::kColO + x * D;
       float m = -INFINITY, l = 0.0f, sums_m = -INFINITY;
       bool summed = false;
       for (int c = 0; c < cnt; ++c) {
