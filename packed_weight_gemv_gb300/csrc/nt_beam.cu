@@ -17,8 +17,8 @@
 // the best: the K best elements stand in the K chunks that come first by maximum (ties by order), for an element of another
 // chunk has the K maxima before it. So the logits cross the memory once and a group's K chunks from L2.
 //
-// 128 rows of 151,936 take 23 us, 12 of them the scan (a fifth of the rows is finished and not read: 62 MB, 5.2 TB/s); 4 rows 12 us and 48 of 32,003
-// with 32 best 15 us, the latency of two launches and four dependent round trips of the choice.
+// 128 rows of 151,936 take 24 us (a fifth of the rows is finished and not read; as single cold launches the scan takes 15.0, 61 MB at 4.1 TB/s,
+// and the choice 16.7); 4 rows 12 us and 48 of 32,003 with 32 best 15 us, the latency of two launches and four dependent round trips of the choice.
 #include <cmath>
 
 #include <algorithm>

@@ -14,18 +14,17 @@
 // while the other group's weights are formed, and a commit behind an S also tells that the O before it is done; warps 4-7 and 8-11 are
 // the groups. S of the next tile goes where P of the last one stood: MMAs of one thread run in the order they are issued in.
 //
-// fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17), those of fp32 queries with D 64 as three
-// without loss. For bf16 queries one term would do
-// with two products for three (ragged prompts of 8,000 tokens 626 us for 776, 257 among decoding sequences 93 for 94, 32 over 8,000 25.3 for 26.9), but its 2^-8
-// stands beside the output's own: 1.28 to 1.41 times the error of rounding the output alone, which is all that two terms leave, and
-// a token would be less exact in a chunk than by itself. The tensor core
-// cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush tiles of a group, into sums in the workspace
-// that round to nearest.
+// fp32 queries enter as three bf16 terms without loss. Weights enter as two rounded bf16 terms (2^-17), those of fp32 queries with D 64
+// as three without loss. For bf16 queries one term would do with two products in place of three (ragged prompts of 8,000 tokens 626 us
+// instead of 776, 257 among decoding sequences 93 instead of 94, 32 over 8,000 25.3 instead of 26.9), but its 2^-8 stands beside the
+// output's own: 1.28 to 1.41 times the error of rounding the output alone, which is all that two terms leave, and a token would be less
+// exact in a chunk than by itself. The tensor core cuts its fp32 sums off instead of rounding them, so O is taken off it every kFlush
+// tiles of a group, into sums in the workspace that round to nearest.
 //
 // Bound by the tensor pipe, the more so the longer the keys: 2,049 bf16 tokens over 16,000, 32 / 8 heads of 128, take 549 us (three products for
 // two, 1,560 TFLOP/s of them), ragged prompts of 8,000 tokens together 776 us (1,430), 511 fp32 tokens over 7,489 124
-// us (127 cold; five products for two, 1,310 of them). Keys and values from L2 alone would take half of that, the exponentials three quarters. What a call pays
-// besides is about 25 us: 13 to the end of a first tile, 6 for the join of parts.
+// us (127 cold; five products for two, 1,310 of them). Of the bf16 times keys and values from L2 alone would take four
+// tenths, the exponentials six. What a call pays besides is about 25 us: 13 to the end of a first tile, 6 for the join of parts.
 #include <math.h>
 
 #include <algorithm>
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kPmThreads, 1) paged_many_kernel(const __grid_
         }
         if constexpr (kExtra) {
           // Cap and bias, from tensor memory and back: 32 keys at a time in a loop, as code for 128 in a row is fetched more slowly than
-          // it runs (300 fp32 tokens over 4,000, capped: 71 us instead of 93; bf16, 257 among decoding sequences: 87 instead of 89).
+          // it runs (300 fp32 tokens over 4,000, capped: 73 us, 22 more in a row; bf16, 257 among decoding sequences: 2 us more).
           const float f = a.cap > 0.0f ? a.scale / a.cap : a.scale;
           if (ok && !idle) {
 #pragma unroll 1
